@@ -324,7 +324,9 @@ def _write_one(x, pages, descale, slots, s):
         amax = rows.abs().amax(-1)
         scaled = amax.clamp(min=TINY_AMAX)
         one = torch.where(amax > 0, scaled / E4M3_MAX, torch.ones_like(amax))
-        rows = rows * torch.where(amax > 0, E4M3_MAX / scaled, torch.ones_like(amax))[..., None]
+        # (a number over a tensor would be a reciprocal and a product: two roundings)
+        scale = torch.full_like(scaled, E4M3_MAX) / scaled
+        rows = rows * torch.where(amax > 0, scale, torch.ones_like(amax))[..., None]
         rows = rows.clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn).view(torch.uint8)
         descale[at // s["page"], :, at % s["page"]] = one
     pages.view(-1, s["Hkv"], s["d"])[at] = rows
