@@ -1,5 +1,7 @@
 """GB300 (sm_103a) exact attention: fused forward (dense and packed
-variable-length), backward, and split-KV decode (contiguous or paged cache).
+variable-length), backward, and split-KV decode (contiguous or paged cache); and
+around it rotary positions, writing and reading the paged cache (bf16 or E4M3),
+and attention of a tree of drafted tokens over that cache.
 
 Thin ctypes binding over the C ABI in ``include/attn.h`` (library
 ``libgb300_attn.so`` built in-tree by ``_build.build()``).  The functions here
@@ -26,6 +28,9 @@ __all__ = [
     "attn_fwd_num_units", "attn_fwd_schedule", "attn_fwd_split_plan", "attn_decode_kernel_launches",
     "attn_bwd", "attn_bwd_workspace_size", "backward", "attn_bwd_varlen",
     "attn_bwd_varlen_workspace_size", "backward_varlen", "attn_decode_paged", "decode_paged", "forward", "decode", "library_path", "load",
+    "attn_rope", "rope", "rope_backward", "attn_rope_frequencies", "rope_frequencies",
+    "attn_cache_write", "attn_cache_read", "cache_read", "attn_decode_tree",
+    "attn_decode_tree_workspace_size", "decode_tree", "tree_mask_words",
 ]
 
 ATTN_OK = 0
@@ -36,6 +41,9 @@ ATTN_ERR_TIMEOUT = 4
 ATTN_ERR_WORKSPACE = 5
 ATTN_OUT_BF16 = 0
 ATTN_OUT_F32 = 1
+ATTN_CACHE_BF16 = 0
+ATTN_CACHE_E4M3 = 1
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgb300_attn.so")
 _lib = None
@@ -81,6 +89,15 @@ SIGNATURES = {
     "attn_bwd": (_c_int, [ctypes.c_void_p] * 9 + [_c_int] * 7 + [ctypes.c_float, _c_int, _c_int,
                                                                  ctypes.c_void_p, ctypes.c_size_t,
                                                                  ctypes.c_void_p]),
+    "attn_rope_frequencies": (_c_int, [_c_int, ctypes.c_double, _c_int, ctypes.c_double, _c_int,
+                                       ctypes.c_double, ctypes.c_double,
+                                       ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_c_f)]),
+    "attn_rope": (_c_int, [_vp] * 9 + [_c_ll, _vp] + [_c_int] * 8 + [_c_f, _c_int, _c_int, _vp]),
+    "attn_cache_write": (_c_int, [_vp] * 9 + [_c_int] * 4 + [_c_ll, _c_int, _c_int, _vp]),
+    "attn_cache_read": (_c_int, [_vp] * 8 + [_c_int] * 3 + [_c_ll] + [_c_int] * 5 + [_vp]),
+    "attn_decode_tree_workspace_size": (_c_sz, [_c_int] * 8),
+    "attn_decode_tree": (_c_int, [_vp] * 11 + [_c_int] * 4 + [_c_ll] + [_c_int] * 3 +
+                         [_c_f, _c_int, _vp, _c_sz, _c_int, _vp]),
     "attn_fwd_split_plan": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
                                      _c_int, ctypes.POINTER(ctypes.c_int),
                                      ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]),
@@ -761,3 +778,333 @@ def decode_paged(q, k_pages, v_pages, block_table, seqlens, *, scale: float | No
     lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=q.device)
     return attn_decode_paged(q, k_pages, v_pages, block_table, seqlens, o, lse, scale=scale,
                              num_splits=num_splits, stream=stream)
+
+
+# ------------------- positions, the paged cache, drafted tokens -------------------
+def _tensor(t, dtypes, name):
+    """A CUDA tensor of one of the given dtypes (any layout)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _rows(t, name):
+    """(B, H, N, d) and the host strides {batch, head, token} of a [B,H,N,d]
+    view or a packed [total,H,d] one (B = 1), whose rows are contiguous and
+    16-byte aligned."""
+    if t.ndim == 4:
+        B, H, N, d = t.shape
+        sb, sh, sn, sd = t.stride()
+    elif t.ndim == 3:
+        (N, H, d), B = t.shape, 1
+        sn, sh, sd = t.stride()
+        sb = 0
+    else:
+        raise ValueError(f"{name} must be [B, H, N, d] or packed [total, H, d]")
+    if min(B, H, N, d) < 1:
+        raise ValueError(f"{name} is empty")
+    if sd != 1 and d > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    strides = (ctypes.c_longlong * 3)(sb if B > 1 else 0, sh if H > 1 else 0, sn if N > 1 else 0)
+    per16 = 16 // t.element_size()
+    if any(s % per16 for s in strides) or t.data_ptr() % 16:
+        raise ValueError(f"{name}: rows must be 16-byte aligned")
+    return (B, H, N, d), strides
+
+
+def _used_on(stream, *tensors):
+    """Tensors allocated here and used on a stream of the caller's: freed only
+    after that stream's use."""
+    import torch
+    if isinstance(stream, torch.cuda.Stream):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def attn_rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "none",
+                          factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0,
+                          beta_slow: float = 1.0):
+    """([inv_freq, ...] in radians per position, magnitude) as Python floats.
+    scaling: "none", "linear", "ntk" or "by_parts" (the last needs
+    original_len, the trained context)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    out = (ctypes.c_double * max(int(rotary_dim) // 2, 1))()
+    mag = _c_f()
+    _check(load().attn_rope_frequencies(int(rotary_dim), float(base), ROPE_SCALINGS[scaling],
+                                        float(factor), int(original_len), float(beta_fast),
+                                        float(beta_slow), out, ctypes.byref(mag)),
+           "attn_rope_frequencies")
+    return list(out), mag.value
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "none",
+                     factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, device="cuda"):
+    """(inv_freq float64 tensor [rotary_dim / 2] on ``device``, magnitude) for
+    rope() and rope_backward(); see attn_rope_frequencies."""
+    import torch
+    f, mag = attn_rope_frequencies(rotary_dim, base, scaling=scaling, factor=factor,
+                                   original_len=original_len, beta_fast=beta_fast,
+                                   beta_slow=beta_slow)
+    return torch.tensor(f, dtype=torch.float64, device=device), mag
+
+
+def attn_rope(q, k, q_out, k_out, positions, inv_freq, *, interleaved: bool = False,
+              inverse: bool = False, magnitude: float = 1.0, stream=None):
+    """Rotary positions on q and k (k and k_out may be None) into caller-provided
+    outputs, one launch.
+
+    q, q_out [B,Hq,N,d] and k, k_out [B,Hkv,N,d], or packed [total,H,d]; bf16 or
+    fp32 (q and k alike, the outputs alike); any strides with contiguous,
+    16-byte-aligned rows, so a slice of a projection's [B,N,H,d] output works as
+    q.transpose(1, 2).  positions int32 [B,N] or [N] ([total] for packed
+    tensors); inv_freq float64 [rotary_dim / 2] (rope_frequencies); the columns
+    past rotary_dim are copied.  inverse: the gradient.  In place when an output
+    is its input.  Asynchronous on ``stream``."""
+    import torch
+    kinds = (torch.bfloat16, torch.float32)
+    for t, n in ((q, "q"), (q_out, "q_out")):
+        _tensor(t, kinds, n)
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    _tensor(positions, (torch.int32,), "positions")
+    _need(inv_freq, torch.float64, "inv_freq")
+    (B, Hq, N, d), qs = _rows(q, "q")
+    shape, qos = _rows(q_out, "q_out")
+    if shape != (B, Hq, N, d) or q_out.ndim != q.ndim:
+        raise ValueError("q_out shape mismatch")
+    Hkv, ks, kos = 0, None, None
+    if k is not None:
+        _tensor(k, (q.dtype,), "k")
+        _tensor(k_out, (q_out.dtype,), "k_out")
+        (Bk, Hkv, Nk, dk), ks = _rows(k, "k")
+        shape, kos = _rows(k_out, "k_out")
+        if (Bk, Nk, dk) != (B, N, d) or k.ndim != q.ndim:
+            raise ValueError("q / k shape mismatch")
+        if shape != (B, Hkv, N, d) or k_out.ndim != k.ndim:
+            raise ValueError("k_out shape mismatch")
+    if tuple(positions.shape) not in ((N,), (B, N)):
+        raise ValueError("positions must be [B, N] or [N]")
+    if N > 1 and positions.stride(-1) != 1:
+        raise ValueError("positions: the last dimension must be contiguous")
+    pos_stride = positions.stride(0) if positions.ndim == 2 and B > 1 else 0
+    if inv_freq.ndim != 1 or not 1 <= inv_freq.numel() <= d // 2:
+        raise ValueError("inv_freq must hold rotary_dim / 2 <= d / 2 frequencies")
+    idt = ATTN_OUT_F32 if q.dtype == torch.float32 else ATTN_OUT_BF16
+    odt = ATTN_OUT_F32 if q_out.dtype == torch.float32 else ATTN_OUT_BF16
+    with _on(_one_device(q, k, q_out, k_out, positions, inv_freq)):
+        rc = load().attn_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), qs, ks, qos, kos,
+                              _ptr(positions), pos_stride, _ptr(inv_freq), B, Hq, Hkv, N, d,
+                              2 * inv_freq.numel(), int(bool(interleaved)), int(bool(inverse)),
+                              float(magnitude), idt, odt, _stream_ptr(stream))
+    _check(rc, "attn_rope")
+    return q_out, k_out
+
+
+def rope(q, k, positions, inv_freq, *, interleaved: bool = False, magnitude: float = 1.0,
+         out_dtype=None, stream=None, inverse: bool = False):
+    """Allocate the outputs (contiguous, of q's and k's shapes) with torch and
+    run attn_rope.  Returns (q_out, k_out); k may be None."""
+    import torch
+    out_dtype = out_dtype or q.dtype
+    q_out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    k_out = None if k is None else torch.empty(k.shape, dtype=out_dtype, device=q.device)
+    _used_on(stream, q_out, k_out)
+    return attn_rope(q, k, q_out, k_out, positions, inv_freq, interleaved=interleaved,
+                     inverse=inverse, magnitude=magnitude, stream=stream)
+
+
+def rope_backward(dq_out, dk_out, positions, inv_freq, *, interleaved: bool = False,
+                  magnitude: float = 1.0, grad_dtype=None, stream=None):
+    """The gradients of rope()'s q and k from those of its outputs (attn_bwd's
+    dQ and dK): (dq, dk), dk None when dk_out is."""
+    return rope(dq_out, dk_out, positions, inv_freq, interleaved=interleaved, magnitude=magnitude,
+                out_dtype=grad_dtype, stream=stream, inverse=True)
+
+
+def _check_pages(k_pages, v_pages, k_descale, v_descale):
+    """Types, shapes and placement of a paged cache; returns (num_blocks,
+    page_size, Hkv, d, cache dtype)."""
+    import torch
+    _tensor(k_pages, (torch.bfloat16, torch.uint8), "k_pages")
+    _need(k_pages, k_pages.dtype, "k_pages")
+    _need(v_pages, k_pages.dtype, "v_pages")
+    if k_pages.ndim != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must both be [num_blocks, page_size, Hkv, d]")
+    num_blocks, page_size, Hkv, d = k_pages.shape
+    if k_pages.dtype == torch.bfloat16:
+        if k_descale is not None or v_descale is not None:
+            raise ValueError("a bf16 cache has no descales")
+        return num_blocks, page_size, Hkv, d, ATTN_CACHE_BF16
+    for t, n in ((k_descale, "k_descale"), (v_descale, "v_descale")):
+        _need(t, torch.float32, n)
+        if tuple(t.shape) != (num_blocks, Hkv, page_size):
+            raise ValueError(f"{n} must be [num_blocks, Hkv, page_size]")
+    return num_blocks, page_size, Hkv, d, ATTN_CACHE_E4M3
+
+
+def attn_cache_write(k, v, k_pages, v_pages, slots, k_descale=None, v_descale=None, *, stream=None):
+    """Write keys and values into a paged cache (in place).
+
+    k, v bf16 [B,Hkv,N,d] or packed [total,Hkv,d], any strides with contiguous,
+    16-byte-aligned rows; k_pages, v_pages [num_blocks,page_size,Hkv,d] bf16, or
+    uint8 E4M3 codes with k_descale, v_descale fp32 [num_blocks,Hkv,page_size];
+    slots int64 [B,N] (or [total]): page * page_size + key in the page, distinct,
+    -1 for tokens to leave out.  Asynchronous."""
+    import torch
+    _tensor(k, (torch.bfloat16,), "k")
+    _tensor(v, (torch.bfloat16,), "v")
+    num_blocks, page_size, Hkv, d, kind = _check_pages(k_pages, v_pages, k_descale, v_descale)
+    (B, H, N, dk), ks = _rows(k, "k")
+    if v.shape != k.shape or (H, dk) != (Hkv, d):
+        raise ValueError("k / v / page shapes mismatch")
+    _, vs = _rows(v, "v")
+    _need(slots, torch.int64, "slots")
+    if tuple(slots.shape) != (k.shape[:1] if k.ndim == 3 else (B, N)):
+        raise ValueError("slots must be [B, N] ([total] for packed keys)")
+    with _on(_one_device(k, v, k_pages, v_pages, slots, k_descale, v_descale)):
+        rc = load().attn_cache_write(_ptr(k), _ptr(v), ks, vs, _ptr(k_pages), _ptr(v_pages),
+                                     _ptr(k_descale), _ptr(v_descale), _ptr(slots), B, N, Hkv, d,
+                                     num_blocks, page_size, kind, _stream_ptr(stream))
+    _check(rc, "attn_cache_write")
+
+
+def attn_cache_read(k_pages, v_pages, block_table, cu_seqlens, k_out, v_out, k_descale=None,
+                    v_descale=None, *, stream=None):
+    """Read a paged cache back into packed k_out, v_out [total,Hkv,d] (bf16 or
+    fp32), which attn_fwd_varlen takes: keys 0.. of sequence b to rows
+    cu_seqlens[b]..cu_seqlens[b+1].  block_table int32 [B,max_blocks],
+    cu_seqlens int32 [B+1], both on the device.  Rows outside every sequence
+    stay as they were.  Asynchronous."""
+    import torch
+    num_blocks, page_size, Hkv, d, kind = _check_pages(k_pages, v_pages, k_descale, v_descale)
+    _need(block_table, torch.int32, "block_table")
+    _need(cu_seqlens, torch.int32, "cu_seqlens")
+    _tensor(k_out, (torch.bfloat16, torch.float32), "k_out")
+    _need(k_out, k_out.dtype, "k_out")
+    _need(v_out, k_out.dtype, "v_out")
+    if block_table.ndim != 2 or tuple(cu_seqlens.shape) != (block_table.shape[0] + 1,):
+        raise ValueError("block_table must be [B, max_blocks] and cu_seqlens [B + 1]")
+    B, max_blocks = block_table.shape
+    if k_out.ndim != 3 or tuple(k_out.shape[1:]) != (Hkv, d) or v_out.shape != k_out.shape:
+        raise ValueError("k_out and v_out must both be [total, Hkv, d]")
+    odt = ATTN_OUT_F32 if k_out.dtype == torch.float32 else ATTN_OUT_BF16
+    with _on(_one_device(k_pages, v_pages, block_table, cu_seqlens, k_out, v_out, k_descale, v_descale)):
+        rc = load().attn_cache_read(_ptr(k_pages), _ptr(v_pages), _ptr(k_descale), _ptr(v_descale),
+                                    _ptr(block_table), _ptr(cu_seqlens), _ptr(k_out), _ptr(v_out),
+                                    B, Hkv, k_out.shape[0], num_blocks, page_size, max_blocks, d,
+                                    kind, odt, _stream_ptr(stream))
+    _check(rc, "attn_cache_read")
+    return k_out, v_out
+
+
+def cache_read(k_pages, v_pages, block_table, cu_seqlens, total: int, k_descale=None,
+               v_descale=None, *, out_dtype=None, stream=None):
+    """Allocate k and v [total,Hkv,d] with torch and run attn_cache_read (total
+    = cu_seqlens[-1], known to the host)."""
+    import torch
+    out_dtype = out_dtype or torch.bfloat16
+    shape = (int(total),) + tuple(k_pages.shape[2:])
+    k = torch.empty(shape, dtype=out_dtype, device=k_pages.device)
+    v = torch.empty(shape, dtype=out_dtype, device=k_pages.device)
+    _used_on(stream, k, v)
+    return attn_cache_read(k_pages, v_pages, block_table, cu_seqlens, k, v, k_descale, v_descale,
+                           stream=stream)
+
+
+def tree_mask_words(mask):
+    """bool [B,T,T] (mask[b, t, u]: drafted token t sees drafted token u) ->
+    the int64 words [B,T,ceil(T/64)] that attn_decode_tree takes."""
+    import torch
+    if mask.ndim != 3 or mask.shape[1] != mask.shape[2] or mask.dtype != torch.bool:
+        raise ValueError("mask must be bool [B, T, T]")
+    B, T, _ = mask.shape
+    W = (T + 63) // 64
+    bits = torch.zeros((B, T, W * 64), dtype=torch.int64, device=mask.device)
+    bits[..., :T] = mask
+    return (bits.view(B, T, W, 64) << torch.arange(64, device=mask.device)).sum(-1)
+
+
+def attn_decode_tree_workspace_size(B: int, Hq: int, Hkv: int, T: int, max_blocks: int,
+                                    page_size: int, d: int, e4m3: bool = False) -> int:
+    return int(load().attn_decode_tree_workspace_size(B, Hq, Hkv, T, max_blocks, page_size, d,
+                                                      int(bool(e4m3))))
+
+
+def attn_decode_tree(q, k_pages, v_pages, block_table, seqlens, o, lse=None, tree_mask=None,
+                     q_lens=None, k_descale=None, v_descale=None, *, scale: float | None = None,
+                     workspace=None, stream=None):
+    """Attention of up to T drafted tokens per sequence over a paged cache that
+    holds their keys and values already, into caller-provided outputs.
+
+    q [B,Hq,T,d] bf16; the cache as for attn_cache_write; block_table int32
+    [B,max_blocks]; seqlens int32 [B], drafted tokens included; o [B,Hq,T,d]
+    bf16 or fp32; lse [B,Hq,T] fp32 or None; tree_mask int64 [B,T,ceil(T/64)]
+    (tree_mask_words) or None for a chain; q_lens int32 [B] drafted tokens of
+    each sequence, or None for T; workspace: a CUDA tensor of at least
+    attn_decode_tree_workspace_size(...) bytes, or None (then one is allocated
+    with torch).  T = 1 is plain decode.  Asynchronous."""
+    import torch
+    _need(q, torch.bfloat16, "q")
+    num_blocks, page_size, Hkv, d, kind = _check_pages(k_pages, v_pages, k_descale, v_descale)
+    _need(block_table, torch.int32, "block_table")
+    _need(seqlens, torch.int32, "seqlens")
+    _tensor(o, (torch.bfloat16, torch.float32), "o")
+    _need(o, o.dtype, "o")
+    if q.ndim != 4 or q.shape[3] != d:
+        raise ValueError("q / page shapes mismatch")
+    B, Hq, T, _ = q.shape
+    if block_table.ndim != 2 or block_table.shape[0] != B or tuple(seqlens.shape) != (B,):
+        raise ValueError("block_table must be [B, max_blocks] and seqlens [B]")
+    if o.shape != q.shape:
+        raise ValueError("o shape mismatch")
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        if tuple(lse.shape) != (B, Hq, T):
+            raise ValueError("lse shape mismatch")
+    if tree_mask is not None:
+        _need(tree_mask, torch.int64, "tree_mask")
+        if tuple(tree_mask.shape) != (B, T, (T + 63) // 64):
+            raise ValueError("tree_mask must be [B, T, ceil(T / 64)]")
+    if q_lens is not None:
+        _need(q_lens, torch.int32, "q_lens")
+        if tuple(q_lens.shape) != (B,):
+            raise ValueError("q_lens must be [B]")
+    if scale is None:
+        scale = d ** -0.5
+    max_blocks = block_table.shape[1]
+    odt = ATTN_OUT_F32 if o.dtype == torch.float32 else ATTN_OUT_BF16
+    dev = _one_device(q, k_pages, v_pages, block_table, seqlens, o, lse, tree_mask, q_lens,
+                      k_descale, v_descale, workspace)
+    with _on(dev):
+        if workspace is None:
+            need = load().attn_decode_tree_workspace_size(B, Hq, Hkv, T, max_blocks, page_size, d, kind)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            _used_on(stream, workspace)
+        ws_ptr, ws_bytes = _workspace(workspace)
+        rc = load().attn_decode_tree(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_descale),
+                                     _ptr(v_descale), _ptr(block_table), _ptr(seqlens),
+                                     _ptr(q_lens), _ptr(tree_mask), _ptr(o), _ptr(lse), B, Hq, Hkv,
+                                     T, num_blocks, page_size, max_blocks, d, float(scale), kind,
+                                     ws_ptr, ws_bytes, odt, _stream_ptr(stream))
+    _check(rc, "attn_decode_tree")
+    return o, lse
+
+
+def decode_tree(q, k_pages, v_pages, block_table, seqlens, tree_mask=None, q_lens=None,
+                k_descale=None, v_descale=None, *, scale: float | None = None, out_dtype=None,
+                return_lse: bool = True, stream=None):
+    """Allocate O (and LSE) with torch and run attn_decode_tree."""
+    import torch
+    out_dtype = out_dtype or torch.bfloat16
+    o = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
+    _used_on(stream, o, lse)
+    return attn_decode_tree(q, k_pages, v_pages, block_table, seqlens, o, lse, tree_mask, q_lens,
+                            k_descale, v_descale, scale=scale, stream=stream)

@@ -112,6 +112,22 @@ attn_status_t encode_tmap_paged_kv(CUtensorMap* map, const void* base, int d, in
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+attn_status_t encode_tmap_pages(CUtensorMap* map, const void* base, bool e4m3, int d, int Hkv,
+                                int page_size, long long num_blocks, int box_keys) {
+    if (!load_encoder()) return ATTN_ERR_CUDA;
+    const cuuint64_t es = e4m3 ? 1 : 2;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)Hkv, (cuuint64_t)page_size, (cuuint64_t)num_blocks};
+    cuuint64_t strides[3] = {(cuuint64_t)d * es, (cuuint64_t)Hkv * d * es,
+                             (cuuint64_t)page_size * Hkv * d * es};
+    cuuint32_t box[4] = {(cuuint32_t)(128 / es), 1u, (cuuint32_t)box_keys, 1u};
+    cuuint32_t elem[4] = {1u, 1u, 1u, 1u};
+    CUresult r = g_encode(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                          const_cast<void*>(base), dims, strides, box, elem,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 attn_status_t encode_tmap_f32_sw128_3d(CUtensorMap* map, void* base, int d, int rows,
                                        long long heads, int box_rows) {
     if (!load_encoder()) return ATTN_ERR_CUDA;
@@ -272,6 +288,56 @@ attn_status_t gb300::check_decode_call(const void* q, const void* k_cache, const
 }
 
 namespace {
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// Strides {batch, head, token} (elements) of a [B, H, N, d] view whose rows are
+// 16-byte aligned; `written`: no two elements may share a place.
+bool strides_ok(const long long* s, int B, int H, int N, int d, int element_bytes, bool written) {
+    if (!s) return false;
+    const int sizes[3] = {B, H, N};
+    for (int i = 0; i < 3; ++i)
+        if (s[i] < 0 || s[i] % (16 / element_bytes) != 0) return false;
+    if (!written) return true;
+    // from the smallest stride up, each has to clear what the ones below span
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int x, int y) { return s[x] < s[y]; });
+    long long span = d;
+    for (int i : order) {
+        if (sizes[i] == 1) continue;
+        if (s[i] < span) return false;
+        span += s[i] * (sizes[i] - 1);
+    }
+    return true;
+}
+
+// Shape checks shared by the paged-cache entry points.
+attn_status_t check_pages(int Hkv, int d, long long num_blocks, int page_size,
+                          attn_cache_dtype_t cache_dtype, const void* k_pages, const void* v_pages,
+                          const float* k_descale, const float* v_descale) {
+    if (cache_dtype != ATTN_CACHE_BF16 && cache_dtype != ATTN_CACHE_E4M3) return ATTN_ERR_INVALID_ARG;
+    if (!k_pages || !v_pages || !aligned16(k_pages) || !aligned16(v_pages)) return ATTN_ERR_INVALID_ARG;
+    const bool e4m3 = cache_dtype == ATTN_CACHE_E4M3;
+    if (e4m3 && (!k_descale || !v_descale || !aligned16(k_descale) || !aligned16(v_descale)))
+        return ATTN_ERR_INVALID_ARG;
+    if (Hkv < 1 || d < 1 || num_blocks < 1 || page_size < 1) return ATTN_ERR_INVALID_ARG;
+    if (num_blocks > (1ll << 31) - 1 || page_size > kMaxLen || Hkv > kMaxHeads) return ATTN_ERR_INVALID_ARG;
+    if (!fwd_head_dim_supported(d) || (e4m3 && d % 16 != 0)) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+attn_status_t check_tree_shape(int B, int Hq, int Hkv, int T, int max_blocks, int page_size, int d,
+                               attn_cache_dtype_t cache_dtype) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || max_blocks < 1 || page_size < 1 || d < 1)
+        return ATTN_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0 || (long long)B * Hq > kMaxHeads) return ATTN_ERR_INVALID_ARG;
+    if (cache_dtype != ATTN_CACHE_BF16 && cache_dtype != ATTN_CACHE_E4M3) return ATTN_ERR_INVALID_ARG;
+    if ((long long)max_blocks * page_size > kMaxLen) return ATTN_ERR_INVALID_ARG;
+    if (T > 1024 || page_size % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    if (!fwd_head_dim_supported(d) || (cache_dtype == ATTN_CACHE_E4M3 && d % 16 != 0))
+        return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
 
 // SM count of the current device, for the size queries (the launches read the
 // same per-device value).  -1 when no device can be queried.
@@ -512,6 +578,161 @@ attn_status_t attn_decode_paged(const void* q, const void* k_pages, const void* 
     return launch_decode_paged(q, k_pages, v_pages, block_table, seqlens, o, lse, B, Hq, Hkv,
                                num_blocks, page_size, max_blocks, d, scale, chunk, workspace,
                                o_dtype, static_cast<cudaStream_t>(stream), dev);
+}
+
+attn_status_t attn_rope_frequencies(int rotary_dim, double base, attn_rope_scaling_t scaling,
+                                    double factor, int original_len, double beta_fast,
+                                    double beta_slow, double* inv_freq, float* magnitude) {
+    if (!inv_freq || rotary_dim < 2 || rotary_dim % 2 != 0 || rotary_dim > 256) return ATTN_ERR_INVALID_ARG;
+    if (!(base > 1.0) || !std::isfinite(base)) return ATTN_ERR_INVALID_ARG;
+    if (scaling < ATTN_ROPE_PLAIN || scaling > ATTN_ROPE_BY_PARTS) return ATTN_ERR_INVALID_ARG;
+    if (scaling != ATTN_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return ATTN_ERR_INVALID_ARG;
+    if (scaling == ATTN_ROPE_BY_PARTS &&
+        (original_len < 1 || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) || !std::isfinite(beta_fast)))
+        return ATTN_ERR_INVALID_ARG;
+    const int n = rotary_dim / 2;
+    if (scaling == ATTN_ROPE_NTK && rotary_dim > 2)
+        base *= std::pow(factor, (double)rotary_dim / (rotary_dim - 2));
+    double lo = 0.0, hi = 0.0;
+    if (scaling == ATTN_ROPE_BY_PARTS) {
+        // the (fractional) pair that turns `turns` times over original_len positions
+        auto pair_of = [&](double turns) {
+            return rotary_dim * std::log(original_len / (turns * 6.283185307179586)) / (2.0 * std::log(base));
+        };
+        lo = std::max(std::floor(pair_of(beta_fast)), 0.0);
+        hi = std::min(std::ceil(pair_of(beta_slow)), (double)(n - 1));
+    }
+    for (int i = 0; i < n; ++i) {
+        double f = std::pow(base, -2.0 * i / rotary_dim);
+        if (scaling == ATTN_ROPE_LINEAR) f /= factor;
+        if (scaling == ATTN_ROPE_BY_PARTS) {
+            const double ramp = std::min(std::max((i - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
+            f = f / factor * ramp + f * (1.0 - ramp);
+        }
+        inv_freq[i] = f;
+    }
+    if (magnitude)
+        *magnitude = scaling == ATTN_ROPE_BY_PARTS ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return ATTN_OK;
+}
+
+attn_status_t attn_rope(const void* q, const void* k, void* q_out, void* k_out,
+                        const long long* q_strides, const long long* k_strides,
+                        const long long* q_out_strides, const long long* k_out_strides,
+                        const int* positions, long long positions_stride, const double* inv_freq,
+                        int B, int Hq, int Hkv, int N, int d, int rotary_dim, int interleaved,
+                        int inverse, float magnitude, attn_out_dtype_t in_dtype,
+                        attn_out_dtype_t out_dtype, void* stream) {
+    if (!q || !q_out || !positions || !inv_freq) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(q_out) || !aligned4(positions) || !aligned8(inv_freq))
+        return ATTN_ERR_INVALID_ARG;
+    if (!k != !k_out || (k && (!aligned16(k) || !aligned16(k_out)))) return ATTN_ERR_INVALID_ARG;
+    if (in_dtype != ATTN_OUT_BF16 && in_dtype != ATTN_OUT_F32) return ATTN_ERR_INVALID_ARG;
+    if (out_dtype != ATTN_OUT_BF16 && out_dtype != ATTN_OUT_F32) return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || Hq < 1 || N < 1 || d < 1 || (k ? Hkv < 1 : Hkv != 0)) return ATTN_ERR_INVALID_ARG;
+    if (Hq > kMaxHeads || Hkv > kMaxHeads || (long long)B * N > kMaxPackedRows) return ATTN_ERR_INVALID_ARG;
+    if (rotary_dim < 2 || rotary_dim % 2 != 0 || rotary_dim > d) return ATTN_ERR_INVALID_ARG;
+    if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1)) return ATTN_ERR_INVALID_ARG;
+    if (!std::isfinite(magnitude) || positions_stride < 0) return ATTN_ERR_INVALID_ARG;
+    if (!fwd_head_dim_supported(d)) return ATTN_ERR_UNSUPPORTED;
+    const int bi = in_dtype == ATTN_OUT_F32 ? 4 : 2, bo = out_dtype == ATTN_OUT_F32 ? 4 : 2;
+    if (!strides_ok(q_strides, B, Hq, N, d, bi, false) || !strides_ok(q_out_strides, B, Hq, N, d, bo, true))
+        return ATTN_ERR_INVALID_ARG;
+    if (k && (!strides_ok(k_strides, B, Hkv, N, d, bi, false) ||
+              !strides_ok(k_out_strides, B, Hkv, N, d, bo, true)))
+        return ATTN_ERR_INVALID_ARG;
+    // in place: every element has to be read and written at the same address
+    auto in_place_ok = [&](const void* x, const void* out, const long long* xs, const long long* os) {
+        return x != out || (bi == bo && std::equal(xs, xs + 3, os));
+    };
+    if (!in_place_ok(q, q_out, q_strides, q_out_strides) ||
+        (k && !in_place_ok(k, k_out, k_strides, k_out_strides)))
+        return ATTN_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    attn_status_t st = current_device_info(&dev);
+    if (st != ATTN_OK) return st;
+    return launch_rope(q, k, q_out, k_out, q_strides, k_strides, q_out_strides, k_out_strides,
+                       positions, positions_stride, inv_freq, B, Hq, Hkv, N, d, rotary_dim,
+                       interleaved, inverse, magnitude, in_dtype, out_dtype,
+                       static_cast<cudaStream_t>(stream), dev);
+}
+
+attn_status_t attn_cache_write(const void* k, const void* v, const long long* k_strides,
+                               const long long* v_strides, void* k_pages, void* v_pages,
+                               float* k_descale, float* v_descale, const long long* slots, int B,
+                               int N, int Hkv, int d, long long num_blocks, int page_size,
+                               attn_cache_dtype_t cache_dtype, void* stream) {
+    if (!k || !v || !slots || !aligned16(k) || !aligned16(v) || !aligned8(slots)) return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || N < 1 || (long long)B * N > kMaxPackedRows) return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_pages(Hkv, d, num_blocks, page_size, cache_dtype, k_pages, v_pages,
+                                   k_descale, v_descale);
+    if (st != ATTN_OK) return st;
+    if (!strides_ok(k_strides, B, Hkv, N, d, 2, false) || !strides_ok(v_strides, B, Hkv, N, d, 2, false))
+        return ATTN_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != ATTN_OK) return st;
+    return launch_cache_write(k, v, k_strides, v_strides, k_pages, v_pages, k_descale, v_descale,
+                              slots, B, N, Hkv, d, num_blocks, page_size, cache_dtype,
+                              static_cast<cudaStream_t>(stream), dev);
+}
+
+attn_status_t attn_cache_read(const void* k_pages, const void* v_pages, const float* k_descale,
+                              const float* v_descale, const int* block_table,
+                              const int* cu_seqlens, void* k_out, void* v_out, int B, int Hkv,
+                              int total, long long num_blocks, int page_size, int max_blocks,
+                              int d, attn_cache_dtype_t cache_dtype, attn_out_dtype_t out_dtype,
+                              void* stream) {
+    if (!block_table || !cu_seqlens || !k_out || !v_out || !aligned4(block_table) ||
+        !aligned4(cu_seqlens) || !aligned16(k_out) || !aligned16(v_out))
+        return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || total < 1 || total > kMaxPackedRows || max_blocks < 1) return ATTN_ERR_INVALID_ARG;
+    if (out_dtype != ATTN_OUT_BF16 && out_dtype != ATTN_OUT_F32) return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_pages(Hkv, d, num_blocks, page_size, cache_dtype, k_pages, v_pages,
+                                   k_descale, v_descale);
+    if (st != ATTN_OK) return st;
+    if ((long long)Hkv * d > (1ll << 24)) return ATTN_ERR_UNSUPPORTED;  // (32-bit indexes within a token)
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != ATTN_OK) return st;
+    return launch_cache_read(k_pages, v_pages, k_descale, v_descale, block_table, cu_seqlens, k_out,
+                             v_out, B, Hkv, total, num_blocks, page_size, max_blocks, d,
+                             cache_dtype, out_dtype, static_cast<cudaStream_t>(stream), dev);
+}
+
+size_t attn_decode_tree_workspace_size(int B, int Hq, int Hkv, int T, int max_blocks, int page_size,
+                                       int d, attn_cache_dtype_t cache_dtype) {
+    if (check_tree_shape(B, Hq, Hkv, T, max_blocks, page_size, d, cache_dtype) != ATTN_OK) return 0;
+    int sms = 0;
+    if (current_num_sms(&sms) != 0) return 0;
+    return tree_workspace_bytes(Hq, Hkv, T, d, cache_dtype, sms);
+}
+
+attn_status_t attn_decode_tree(const void* q, const void* k_pages, const void* v_pages,
+                               const float* k_descale, const float* v_descale,
+                               const int* block_table, const int* seqlens, const int* q_lens,
+                               const uint64_t* tree_mask, void* o, float* lse, int B, int Hq,
+                               int Hkv, int T, long long num_blocks, int page_size, int max_blocks,
+                               int d, float scale, attn_cache_dtype_t cache_dtype, void* workspace,
+                               size_t workspace_bytes, attn_out_dtype_t o_dtype, void* stream) {
+    if (!q || !block_table || !seqlens || !o) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o) || !aligned4(block_table) || !aligned4(seqlens))
+        return ATTN_ERR_INVALID_ARG;
+    if ((q_lens && !aligned4(q_lens)) || (tree_mask && !aligned8(tree_mask)) || (lse && !aligned4(lse)))
+        return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_common(B, Hq, Hkv, d, scale, o_dtype);
+    if (st != ATTN_OK) return st;
+    if ((st = check_tree_shape(B, Hq, Hkv, T, max_blocks, page_size, d, cache_dtype)) != ATTN_OK) return st;
+    if ((st = check_pages(Hkv, d, num_blocks, page_size, cache_dtype, k_pages, v_pages, k_descale,
+                          v_descale)) != ATTN_OK)
+        return st;
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != ATTN_OK) return st;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < tree_workspace_bytes(Hq, Hkv, T, d, cache_dtype, dev.num_sms))
+        return ATTN_ERR_WORKSPACE;
+    return launch_decode_tree(q, k_pages, v_pages, k_descale, v_descale, block_table, seqlens,
+                              q_lens, tree_mask, o, lse, B, Hq, Hkv, T, num_blocks, page_size,
+                              max_blocks, d, scale, cache_dtype, workspace, o_dtype,
+                              static_cast<cudaStream_t>(stream), dev);
 }
 
 const char* attn_status_string(attn_status_t s) {

@@ -50,6 +50,11 @@ attn_status_t encode_tmap_f32_sw128_3d(CUtensorMap* map, void* base, int d, int 
 attn_status_t encode_tmap_paged_kv(CUtensorMap* map, const void* base, int d, int Hkv,
                                    int page_size, long long num_blocks);
 
+// The same for a cache of bf16 or (e4m3) 8-bit codes, box of 128 bytes of d x
+// 1 (head) x box_keys x 1 (block).
+attn_status_t encode_tmap_pages(CUtensorMap* map, const void* base, bool e4m3, int d, int Hkv,
+                                int page_size, long long num_blocks, int box_keys);
+
 // 5-D tensor map over a packed [total, heads, d] array (bf16, or fp32 for
 // outputs) addressed per sequence: see the ragged layout in fwd_sched.h.  Box of
 // box_cols x 1 head x box_rows rows; 128-byte swizzle for the operand loads,
@@ -142,5 +147,42 @@ attn_status_t launch_decode_paged(const void* q, const void* k_pages, const void
                                   int B, int Hq, int Hkv, long long num_blocks, int page_size,
                                   int max_blocks, int d, float scale, int chunk, void* workspace,
                                   attn_out_dtype_t o_dtype, cudaStream_t stream, const DeviceInfo& dev);
+
+// Rotary positions of q [B, Hq, N, d] and k [B, Hkv, N, d] (k may be NULL);
+// strides are {batch, head, token} in elements.
+attn_status_t launch_rope(const void* q, const void* k, void* q_out, void* k_out,
+                          const long long* q_strides, const long long* k_strides,
+                          const long long* q_out_strides, const long long* k_out_strides,
+                          const int* positions, long long positions_stride, const double* inv_freq,
+                          int B, int Hq, int Hkv, int N, int d, int rotary_dim, int interleaved,
+                          int inverse, float magnitude, attn_out_dtype_t in_dtype,
+                          attn_out_dtype_t out_dtype, cudaStream_t stream, const DeviceInfo& dev);
+
+// Paged cache: keys and values [B, Hkv, N, d] (strides as above) to the rows
+// `slots` names, and back into packed [total, Hkv, d] arrays.
+attn_status_t launch_cache_write(const void* k, const void* v, const long long* k_strides,
+                                 const long long* v_strides, void* k_pages, void* v_pages,
+                                 float* k_descale, float* v_descale, const long long* slots, int B,
+                                 int N, int Hkv, int d, long long num_blocks, int page_size,
+                                 attn_cache_dtype_t cache_dtype, cudaStream_t stream,
+                                 const DeviceInfo& dev);
+attn_status_t launch_cache_read(const void* k_pages, const void* v_pages, const float* k_descale,
+                                const float* v_descale, const int* block_table,
+                                const int* cu_seqlens, void* k_out, void* v_out, int B, int Hkv,
+                                int total, long long num_blocks, int page_size, int max_blocks,
+                                int d, attn_cache_dtype_t cache_dtype, attn_out_dtype_t out_dtype,
+                                cudaStream_t stream, const DeviceInfo& dev);
+
+// Attention of T drafted tokens a sequence over a paged cache.
+size_t tree_workspace_bytes(int Hq, int Hkv, int T, int d, attn_cache_dtype_t cache_dtype, int num_sms);
+attn_status_t launch_decode_tree(const void* q, const void* k_pages, const void* v_pages,
+                                 const float* k_descale, const float* v_descale,
+                                 const int* block_table, const int* seqlens, const int* q_lens,
+                                 const uint64_t* tree_mask, void* o, float* lse, int B, int Hq,
+                                 int Hkv, int T, long long num_blocks, int page_size,
+                                 int max_blocks, int d, float scale,
+                                 attn_cache_dtype_t cache_dtype, void* workspace,
+                                 attn_out_dtype_t o_dtype, cudaStream_t stream,
+                                 const DeviceInfo& dev);
 
 }  // namespace gb300

@@ -1,0 +1,205 @@
+// tree_plan.h -- how the tree-attention kernels share out their work.
+//
+// An item is (sequence b, KV head h, tile of query rows rt); the rows of a
+// (sequence, KV head) are its drafted tokens times the group's heads, row
+// t * G + g.  An item's units are its key tiles.  Items lie one after another
+// (b, then h, then rt) and CTA c of n takes the units [c * total / n,
+// (c + 1) * total / n): every CTA has the same number of key tiles to read,
+// whatever the lengths are, and an item is cut only where a CTA's range ends.
+// The lengths live on the device, so each CTA works the ranges out itself.
+// A piece that is not a whole item leaves a partial result in the workspace:
+// a CTA has at most two such pieces, its first (place 2c) and its last
+// (2c + 1), so the workspace does not grow with the batch.  The merge kernel
+// redoes the same arithmetic to find an item's pieces.
+#pragma once
+
+#include <cstdint>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace gb300 {
+
+struct TreeParams {
+    int B, Hq, Hkv, G, T, W;   // W: mask words of a row
+    int max_blocks, page_size;
+    int box_keys;              // keys of one copy: the largest of 16, 32, 64, 128 that divides the page and the tile
+    long long num_blocks;
+    int dh;                    // head dim of the tensors
+    int ctas;                  // grid size of the attention kernel
+    int min_units;             // key tiles of a CTA, at least
+    int tile_keys, tile_rows;
+    float c;                   // scale * log2(e)
+    const int* block_table;
+    const int* seqlens;
+    const int* q_lens;         // NULL: T everywhere
+    const unsigned long long* mask;  // NULL: drafted token t sees tokens 0..t
+    const float* k_descale;
+    const float* v_descale;
+    const __nv_bfloat16* q;
+    void* o;
+    float* lse;
+    float* ws_o;               // [2 * ctas][tile_rows][dw]
+    float* ws_lse;             // [2 * ctas][tile_rows], base 2
+    int dw;                    // columns of a partial row
+    int out_f32;
+    unsigned int* err;
+};
+
+// A sequence of the batch: keys, drafted tokens, row tiles and key tiles of
+// its items.  Lengths out of range count as no drafted tokens at all.
+struct TreeSeq {
+    int keys, drafted, row_tiles, key_tiles;
+    bool bad;
+};
+
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
+    TreeSeq s;
+    s.keys = __ldg(p.seqlens + b);
+    s.drafted = p.q_lens ? __ldg(p.q_lens + b) : p.T;
+    s.bad = s.keys < 0 || (long long)s.keys > (long long)p.max_blocks * p.page_size || s.drafted < 0 ||
+            s.drafted > p.T || s.drafted > s.keys;
+    if (s.bad) s.keys = s.drafted = 0;
+    s.row_tiles = (s.drafted * p.G + p.tile_rows - 1) / p.tile_rows;
+    s.key_tiles = (s.keys + p.tile_keys - 1) / p.tile_keys;
+    return s;
+}
+__device__ __forceinline__ long long tree_units(const TreeParams& p, const TreeSeq& s) {
+    return (long long)p.Hkv * s.row_tiles * s.key_tiles;
+}
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+    return v;
+}
+
+// Units of the whole batch (a full warp calls).  `report`: record lengths out
+// of range in the error word.
+__device__ __forceinline__ long long tree_total(const TreeParams& p, bool report) {
+    const int lane = threadIdx.x & 31;
+    long long n = 0;
+    for (int b = lane; b < p.B; b += 32) {
+        const TreeSeq s = tree_seq(p, b);
+        if (s.bad && report) atomicOr(p.err, kErrBadSeqlen);
+        n += tree_units(p, s);
+    }
+    return warp_sum(n);
+}
+
+// Units of the sequences before b (a full warp calls).
+__device__ __forceinline__ long long tree_base(const TreeParams& p, int b) {
+    const int lane = threadIdx.x & 31;
+    long long n = 0;
+    for (int i = lane; i < b; i += 32) n += tree_units(p, tree_seq(p, i));
+    return warp_sum(n);
+}
+
+// CTAs that take part, and the first unit of CTA c of them.
+__device__ __forceinline__ int tree_ctas(const TreeParams& p, long long total) {
+    const long long want = (total + p.min_units - 1) / p.min_units;
+    return (int)(want < p.ctas ? (want < 1 ? 1 : want) : p.ctas);
+}
+__device__ __forceinline__ long long tree_first(long long total, int n, int c) { return total * c / n; }
+
+// A CTA's place in the list of units: its range, and the sequence that holds
+// its first unit (`base`: units before that sequence).
+struct TreeRange {
+    long long u0, u1, base;
+    int b;
+};
+
+// Found by a full warp; the same in every lane.
+__device__ __forceinline__ TreeRange tree_range(const TreeParams& p, int cta) {
+    const int lane = threadIdx.x & 31;
+    TreeRange r;
+    const long long total = tree_total(p, cta == 0);
+    const int n = tree_ctas(p, total);
+    r.u0 = r.u1 = r.base = 0;
+    r.b = 0;
+    if (cta >= n || total == 0) return r;
+    r.u0 = tree_first(total, n, cta);
+    r.u1 = tree_first(total, n, cta + 1);
+    long long base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        const long long mine = b < p.B ? tree_units(p, tree_seq(p, b)) : 0;
+        long long upto = mine;  // inclusive prefix sum over the lanes
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long v = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+            if (lane >= off) upto += v;
+        }
+        const unsigned hit = __ballot_sync(0xFFFFFFFFu, base + upto > r.u0);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            r.b = b0 + l;
+            r.base = base + __shfl_sync(0xFFFFFFFFu, upto - mine, l);
+            break;
+        }
+        base += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    }
+    return r;
+}
+
+// A piece of work: key tiles [k0, k1) of item (b, h, rt).
+struct TreePiece {
+    int b, h, rt, k0, k1;
+    int keys, drafted;   // of the sequence
+    bool whole;          // all of the item's key tiles
+};
+
+// Walks a range piece by piece; every role of a CTA walks its own copy.
+struct TreeWalk {
+    long long u, u1, base;
+    int b;
+    __device__ __forceinline__ void start(const TreeRange& r) {
+        u = r.u0; u1 = r.u1; base = r.base; b = r.b;
+    }
+    __device__ __forceinline__ bool next(const TreeParams& p, TreePiece& w) {
+        if (u >= u1) return false;
+        TreeSeq s = tree_seq(p, b);
+        long long n = tree_units(p, s);
+        while (u >= base + n) {  // ends: the units sum up to the total
+            base += n;
+            s = tree_seq(p, ++b);
+            n = tree_units(p, s);
+        }
+        const long long at = u - base;
+        const long long item = at / s.key_tiles;
+        w.k0 = (int)(at - item * s.key_tiles);
+        w.h = (int)(item / s.row_tiles);
+        w.rt = (int)(item - (long long)w.h * s.row_tiles);
+        const long long left = u1 - u;
+        w.k1 = (int)(left < s.key_tiles - w.k0 ? w.k0 + left : s.key_tiles);
+        w.b = b;
+        w.keys = s.keys;
+        w.drafted = s.drafted;
+        w.whole = w.k0 == 0 && w.k1 == s.key_tiles;
+        u += w.k1 - w.k0;
+        return true;
+    }
+};
+
+// The page of the cache that holds key `key` of sequence b, -1 (reads as
+// zeros) for keys past the sequence and for entries that name no page.
+__device__ __forceinline__ int tree_page(const TreeParams& p, int b, int key, int keys, int& off) {
+    const int blk = key / p.page_size;
+    off = key - blk * p.page_size;
+    if (key >= keys) return -1;
+    const int page = __ldg(p.block_table + (size_t)b * p.max_blocks + blk);
+    return page >= 0 && (long long)page < p.num_blocks ? page : -1;
+}
+
+// Whether row (drafted token t of sequence b) sees drafted token u.
+__device__ __forceinline__ bool tree_sees(const TreeParams& p, int b, int t, int u) {
+    if (!p.mask) return u <= t;
+    const unsigned long long w = __ldg(p.mask + ((size_t)b * p.T + t) * p.W + (u >> 6));
+    return (w >> (u & 63)) & 1ull;
+}
+
+// Merges the pieces of the items that were cut, and writes the rows past each
+// sequence's drafted tokens (O = 0, LSE = -inf).
+attn_status_t launch_tree_merge(const TreeParams& p, cudaStream_t stream);
+
+}  // namespace gb300

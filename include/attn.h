@@ -24,7 +24,12 @@
  *                notes section 6.1 and exercise 3; "FlashAttention tiling &
  *                online softmax" section 7.1), with query heads that share a
  *                KV head packed as rows of one tile (lecture notes 6.2);
- *                attn_decode_paged reads the cache through a block table.
+ *                attn_decode_paged reads the cache through a block table;
+ *   attn_rope    rotary positions on Q and K, and their gradient;
+ *   attn_cache_write, attn_cache_read  keys and values into a paged cache (bf16
+ *                or E4M3 with a descale per row) and back;
+ *   attn_decode_tree  several drafted tokens per sequence (a tree, a chain, one
+ *                token) over that cache.
  *
  * Conventions shared by every entry point
  *   - Pointers named q/k/v/o/lse/k_cache/v_cache/seqlens/workspace are DEVICE
@@ -401,6 +406,169 @@ attn_status_t attn_decode_noalloc(const void* q, const void* k_cache, const void
                                   int Hkv, int Nmax, int d, float scale, int num_splits,
                                   attn_out_dtype_t o_dtype, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the attention: positions, the paged cache, drafted tokens.
+ *
+ * Strides of these entry points are HOST arrays {batch, head, token} in
+ * elements of a [B, H, N, d] view whose last dimension is contiguous; rows are
+ * 16-byte aligned (strides multiples of 8 bf16 or 4 fp32 elements).  A packed
+ * [total, H, d] array is B = 1, N = total with strides {0, d, H * d}.
+ * ------------------------------------------------------------------------- */
+
+typedef enum {
+    ATTN_CACHE_BF16 = 0,       /* pages of bf16 values                           */
+    ATTN_CACHE_E4M3 = 1        /* pages of E4M3 codes, one descale per row       */
+} attn_cache_dtype_t;
+
+typedef enum {
+    ATTN_ROPE_PLAIN = 0,       /* f_i = base^(-2i / rotary_dim)                  */
+    ATTN_ROPE_LINEAR = 1,      /* f_i / factor (positions interpolated)          */
+    ATTN_ROPE_NTK = 2,         /* base * factor^(rotary_dim / (rotary_dim - 2))  */
+    ATTN_ROPE_BY_PARTS = 3     /* a ramp between f_i and f_i / factor            */
+} attn_rope_scaling_t;
+
+/*
+ * attn_rope_frequencies -- the frequencies of rotary positions, in radians per
+ * position (host only; touches no GPU).  Fills inv_freq[rotary_dim / 2] and, if
+ * magnitude is not NULL, the factor to pass to attn_rope.
+ *
+ *   rotary_dim  even, 2..256;  base > 1 (commonly 10000)
+ *   factor      >= 1: how much longer the context is than the trained one
+ *               (ignored by ATTN_ROPE_PLAIN)
+ *   ATTN_ROPE_BY_PARTS: pairs that turn at least beta_fast times over
+ *               original_len positions keep f_i, those that turn at most
+ *               beta_slow times get f_i / factor, linear in the pair's index in
+ *               between (the ends rounded outwards to whole pairs); magnitude =
+ *               0.1 ln(factor) + 1 (1 for the others)
+ */
+attn_status_t attn_rope_frequencies(int rotary_dim, double base, attn_rope_scaling_t scaling,
+                                    double factor, int original_len, double beta_fast,
+                                    double beta_slow, double* inv_freq, float* magnitude);
+
+/*
+ * attn_rope -- rotary positions on Q and K in one launch, or their gradient.
+ *
+ *   q, q_out  [B, Hq, N, d];  k, k_out  [B, Hkv, N, d], or both NULL with
+ *             Hkv = 0; element types in_dtype and out_dtype (bf16 or fp32)
+ *   positions  int32 (device): token n of batch b is at position
+ *             positions[b * positions_stride + n] (stride 0: shared); any
+ *             32-bit value
+ *   inv_freq  fp64 (device) [rotary_dim / 2]: finite radians per position
+ *   rotary_dim  even, 2..d: the first rotary_dim columns turn, the rest are
+ *             copied.  Pairs are columns (i, i + rotary_dim / 2), or
+ *             (2i, 2i + 1) when interleaved = 1.
+ *   inverse   0: (a, b) -> magnitude * (a cos - b sin, a sin + b cos);
+ *             1: the transpose of that (the gradient of q from that of q_out)
+ *
+ * The angle position * inv_freq is reduced exactly (64-bit fixed point), cos,
+ * sin and the products are fp32.  In place (q_out = q, k_out = k) needs the
+ * same strides and types; inputs and outputs may not overlap otherwise.
+ * Supported: 8 <= d <= 256, d % 8 == 0; B * N <= 2^30.
+ */
+attn_status_t attn_rope(const void* q, const void* k, void* q_out, void* k_out,
+                        const long long* q_strides, const long long* k_strides,
+                        const long long* q_out_strides, const long long* k_out_strides,
+                        const int* positions, long long positions_stride, const double* inv_freq,
+                        int B, int Hq, int Hkv, int N, int d, int rotary_dim, int interleaved,
+                        int inverse, float magnitude, attn_out_dtype_t in_dtype,
+                        attn_out_dtype_t out_dtype, void* stream);
+
+/*
+ * attn_cache_write -- keys and values into a paged cache.
+ *
+ *   k, v      bf16 [B, Hkv, N, d] (strided)
+ *   k_pages, v_pages  [num_blocks, page_size, Hkv, d], bf16 or E4M3 codes
+ *   k_descale, v_descale  E4M3: fp32 [num_blocks, Hkv, page_size] (16-byte
+ *             aligned); ignored for bf16
+ *   slots     int64 (device) [B, N]: token (b, n) goes to key slots % page_size
+ *             of page slots / page_size; -1 skips the token (padding).  Any
+ *             other slot outside [0, num_blocks * page_size) is skipped and
+ *             attn_last_device_error() reports ATTN_ERR_INVALID_ARG.  The slots
+ *             of a call must differ from one another (of two tokens on one slot
+ *             either may stay, its descale and codes from different ones).
+ *
+ * E4M3, per (token, head) row: a = max(max |x|, 2^-100), code = E4M3(x * (448 /
+ * a)) rounded to nearest even in fp32 arithmetic, descale = a / 448; an
+ * all-zero row gets descale 1.  NaN elements stay NaN; an infinity makes its row NaN.
+ * Supported: 8 <= d <= 256, d % 8 == 0 (E4M3: d % 16 == 0); B * N <= 2^30.
+ */
+attn_status_t attn_cache_write(const void* k, const void* v, const long long* k_strides,
+                               const long long* v_strides, void* k_pages, void* v_pages,
+                               float* k_descale, float* v_descale, const long long* slots, int B,
+                               int N, int Hkv, int d, long long num_blocks, int page_size,
+                               attn_cache_dtype_t cache_dtype, void* stream);
+
+/*
+ * attn_cache_read -- a paged cache back into packed keys and values (what
+ * attn_fwd_varlen takes: a chunk of a prompt over its cached prefix).
+ *
+ *   block_table  int32 [B, max_blocks] (device), as for attn_decode_paged
+ *   cu_seqlens   int32 [B + 1] (device), non-decreasing: keys [0, cu[b + 1] -
+ *             cu[b]) of sequence b go to rows cu[b].. of the outputs
+ *   k_out, v_out  [total, Hkv, d] in out_dtype: code * descale (one fp32
+ *             product) rounded to it, or the bf16 value
+ *
+ * Rows outside every sequence are left as they were.  A sequence whose offsets
+ * leave [0, total], decrease or exceed max_blocks * page_size keys is not read
+ * (ATTN_ERR_INVALID_ARG from attn_last_device_error() where it has rows below
+ * total); keys of a block-table entry outside [0, num_blocks) read as zeros.
+ */
+attn_status_t attn_cache_read(const void* k_pages, const void* v_pages, const float* k_descale,
+                              const float* v_descale, const int* block_table,
+                              const int* cu_seqlens, void* k_out, void* v_out, int B, int Hkv,
+                              int total, long long num_blocks, int page_size, int max_blocks,
+                              int d, attn_cache_dtype_t cache_dtype, attn_out_dtype_t out_dtype,
+                              void* stream);
+
+/*
+ * attn_decode_tree_workspace_size -- bytes of device workspace attn_decode_tree
+ * needs for this shape on the current device (it depends on the SM count, not
+ * on B or the lengths).  Returns 0 for arguments attn_decode_tree would reject,
+ * or when no device answers.
+ */
+size_t attn_decode_tree_workspace_size(int B, int Hq, int Hkv, int T, int max_blocks, int page_size,
+                                       int d, attn_cache_dtype_t cache_dtype);
+
+/*
+ * attn_decode_tree -- attention of up to T drafted tokens per sequence over a
+ * paged cache that already holds their keys and values: a tree of drafts, a
+ * chain (a chunk of new tokens), or one token (T = 1: plain decode).
+ *
+ *   q         bf16 [B, Hq, T, d]
+ *   k_pages, v_pages, k_descale, v_descale, cache_dtype  as attn_cache_write
+ *   block_table  int32 [B, max_blocks] (device), as for attn_decode_paged
+ *   seqlens   int32 [B] (device): keys of sequence b, its drafted tokens' included
+ *   q_lens    int32 [B] (device): drafted tokens n_b of sequence b, 0 <= n_b <=
+ *             min(T, seqlens[b]); NULL: T everywhere
+ *   tree_mask  uint64 [B, T, ceil(T / 64)] (device): bit u % 64 of word u / 64
+ *             of row (b, t): drafted token t sees drafted token u (its own bit
+ *             included); NULL: a chain, t sees 0..t
+ *   o         [B, Hq, T, d] per o_dtype;  lse  fp32 [B, Hq, T] or NULL
+ *   workspace  at least attn_decode_tree_workspace_size bytes, 16-byte aligned;
+ *             no initialisation needed, garbage afterwards.  Launches (and
+ *             replays of captured ones) that may overlap need separate ones.
+ *
+ * Drafted token u of sequence b is key seqlens[b] - n_b + u; drafted token t
+ * attends every key before the drafted ones and those its mask names.  Rows t >=
+ * n_b, and rows that attend no key, get O = 0, LSE = -inf.  A sequence whose
+ * lengths are out of range counts as n_b = 0 and attn_last_device_error()
+ * reports ATTN_ERR_INVALID_ARG.  Keys past a sequence's length, and drafted
+ * tokens a row does not see, never reach it (NaN included); a block-table entry
+ * outside [0, num_blocks) reads as zeros.
+ * Numerics: fp32 scores, softmax statistics and O; P is rounded to bf16 for a
+ * bf16 cache, and for E4M3 (whose codes are exact in fp16) to fp16 after V's
+ * descale.  Results do not change from run to run.
+ * Supported: 8 <= d <= 256, d % 8 == 0 (E4M3: d % 16 == 0); page_size % 16 ==
+ * 0; Hq % Hkv == 0; 1 <= T <= 1024; max_blocks * page_size <= 2^24.
+ */
+attn_status_t attn_decode_tree(const void* q, const void* k_pages, const void* v_pages,
+                               const float* k_descale, const float* v_descale,
+                               const int* block_table, const int* seqlens, const int* q_lens,
+                               const uint64_t* tree_mask, void* o, float* lse, int B, int Hq,
+                               int Hkv, int T, long long num_blocks, int page_size, int max_blocks,
+                               int d, float scale, attn_cache_dtype_t cache_dtype, void* workspace,
+                               size_t workspace_bytes, attn_out_dtype_t o_dtype, void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* attn_status_string(attn_status_t status);
 
@@ -408,7 +576,7 @@ const char* attn_status_string(attn_status_t status);
  * attn_last_device_error -- synchronises `stream`, then reads and clears the
  * current device's error word.  Returns ATTN_OK, ATTN_ERR_TIMEOUT (a kernel's
  * bounded wait ran out; its outputs are undefined), ATTN_ERR_INVALID_ARG (a
- * decode sequence length was out of range) or ATTN_ERR_CUDA.
+ * sequence length, offset or cache slot was out of range) or ATTN_ERR_CUDA.
  */
 attn_status_t attn_last_device_error(void* stream);
 
