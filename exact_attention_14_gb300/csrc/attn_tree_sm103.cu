@@ -8,8 +8,8 @@
 // E4M3 rows stand for code * descale: s_j = scale * kd_j (q . kc_j) and
 // O = sum_j p_j vd_j vc_j / sum_j p_j, the codes exact in fp16.
 //
-// This file: the kernel for 16 query rows at a time on mma.sync (m16n8k16),
-// and the merge of cut items (tree_plan.h has the work list).  A producer warp
+// This file: the kernel for 16 query rows at a time on mma.sync (m16n8k16;
+// more rows of head dims up to 128 go to attn_tree_tc_sm103.cu), and the merge of cut items (tree_plan.h has the work list).  A producer warp
 // streams 64-key tiles of K and V (and their descales) by TMA into a ring; each
 // of four consumer warps takes 16 keys of every tile with its own online
 // softmax (base 2), and the four are merged through shared memory at the end of
@@ -67,6 +67,17 @@ static_assert(sizeof(TreeBars) <= 1024, "barrier block");
 
 __device__ __forceinline__ void tree_consumers_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
+}
+// Whether any consumer says so (every consumer warp gets here: all leave together).
+__device__ __forceinline__ bool tree_consumers_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "n"(kConsumers * 32)
+        : "memory");
+    return r != 0;
 }
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -534,7 +545,10 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars->empty[slot]));
         }
-        if (!ok) break;
+        if (tree_consumers_any(!ok)) {
+            ok = false;
+            break;
+        }
         // ---- merge the four warps: sums over the quad, then the warps' maxima
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -731,11 +745,27 @@ attn_status_t launch_tree_merge(const TreeParams& p, cudaStream_t stream) {
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+// Whether a call runs on the tensor-core kernel of attn_tree_tc_sm103.cu.
+static bool tree_on_tc(int d, int rows) { return d <= 128 && rows > kRows; }
+
+static void tree_shape(TreeParams& p, int rows, bool f8, int num_sms) {
+    if (tree_on_tc(p.dh, rows)) {
+        tree_tc_shape(p, f8, num_sms);
+        return;
+    }
+    p.tile_rows = kRows;
+    p.tile_keys = kTileKeys;
+    p.dw = tree_width(p.dh, f8);
+    p.ctas = tree_grid(p.dh, f8, num_sms);
+    p.min_units = 2;
+}
+
 size_t tree_workspace_bytes(int Hq, int Hkv, int T, int d, attn_cache_dtype_t cache_dtype, int num_sms) {
-    (void)Hq; (void)Hkv; (void)T;
-    const bool f8 = cache_dtype == ATTN_CACHE_E4M3;
-    const size_t rows = (size_t)2 * tree_grid(d, f8, num_sms) * kRows;
-    return align16(rows * tree_width(d, f8) * 4) + align16(rows * 4);
+    TreeParams p;
+    p.dh = d;
+    tree_shape(p, T * (Hq / Hkv), cache_dtype == ATTN_CACHE_E4M3, num_sms);
+    const size_t rows = (size_t)2 * p.ctas * p.tile_rows;
+    return align16(rows * p.dw * 4) + align16(rows * 4);
 }
 
 attn_status_t launch_decode_tree(const void* q, const void* k_pages, const void* v_pages,
@@ -759,25 +789,24 @@ attn_status_t launch_decode_tree(const void* q, const void* k_pages, const void*
     p.page_size = page_size;
     p.num_blocks = num_blocks;
     p.dh = d;
-    p.dw = tree_width(d, f8);
-    p.ctas = tree_grid(d, f8, dev.num_sms);
-    p.min_units = 2;
-    p.tile_keys = kTileKeys;
-    p.tile_rows = kRows;
-    p.box_keys = 64;
+    const int rows_kv = T * p.G;
+    tree_shape(p, rows_kv, f8, dev.num_sms);
+    p.box_keys = p.tile_keys;
     while (page_size % p.box_keys) p.box_keys /= 2;
     p.c = scale * kLog2et;
     p.block_table = block_table;
     p.seqlens = seqlens;
     p.q_lens = q_lens;
     p.mask = reinterpret_cast<const unsigned long long*>(tree_mask);
+    p.k_pages = static_cast<const uint8_t*>(k_pages);
+    p.v_pages = static_cast<const uint8_t*>(v_pages);
     p.k_descale = k_descale;
     p.v_descale = v_descale;
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.o = o;
     p.lse = lse;
     p.ws_o = static_cast<float*>(workspace);
-    const size_t rows = (size_t)2 * p.ctas * kRows;
+    const size_t rows = (size_t)2 * p.ctas * p.tile_rows;
     p.ws_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align16(rows * p.dw * 4));
     p.out_f32 = o_dtype == ATTN_OUT_F32;
     p.err = dev.err_word;
@@ -785,7 +814,8 @@ attn_status_t launch_decode_tree(const void* q, const void* k_pages, const void*
     attn_status_t st;
     if ((st = encode_tmap_pages(&tk, k_pages, f8, d, Hkv, page_size, num_blocks, p.box_keys)) != ATTN_OK) return st;
     if ((st = encode_tmap_pages(&tv, v_pages, f8, d, Hkv, page_size, num_blocks, p.box_keys)) != ATTN_OK) return st;
-    if (f8) st = p.dw == 128 ? launch_tree_t<128, true>(tk, tv, p, stream, dev) : launch_tree_t<256, true>(tk, tv, p, stream, dev);
+    if (tree_on_tc(d, rows_kv)) st = launch_tree_tc(tk, tv, p, f8, stream, dev);
+    else if (f8) st = p.dw == 128 ? launch_tree_t<128, true>(tk, tv, p, stream, dev) : launch_tree_t<256, true>(tk, tv, p, stream, dev);
     else if (p.dw == 64) st = launch_tree_t<64, false>(tk, tv, p, stream, dev);
     else if (p.dw == 128) st = launch_tree_t<128, false>(tk, tv, p, stream, dev);
     else st = launch_tree_t<256, false>(tk, tv, p, stream, dev);

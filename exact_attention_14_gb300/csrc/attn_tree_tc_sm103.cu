@@ -1,0 +1,1048 @@
+// attn_tree_tc_sm103.cu -- tree attention (attn_tree_sm103.cu has the problem)
+// for many query rows: up to 256 rows of one (sequence, KV head) at a time on
+// the 5th-generation tensor cores.
+//
+// A persistent CTA per SM takes its range of the work list (tree_plan.h, items
+// of 256 rows, 128-key tiles).  Two streams t = 0, 1 run side by side, each a
+// 128-row tile with its own S, P and O in tensor memory and its own softmax
+// warpgroup, so that one's exponentials overlap the other's products:
+//   rows > 128 ("pair"):   the streams are the two row tiles and share every
+//                          K and V tile;
+//   rows <= 128 ("split"): both hold the same rows, stream t takes every second
+//                          key tile, and the two are merged at the end.
+// Roles: warp 0 TMA producer (K and V tiles in the order the products want
+// them), warp 1 MMA issuer, warps 4-7 and 8-11 softmax of stream 0 and 1 (a
+// thread per row; they also lay Q out in shared memory, whose rows are not
+// evenly spaced in a [B, Hq, T, d] tensor).  bf16 caches: warps 2-3 prepare V
+// in the tiles that hold drafted tokens or the end of the sequence.  E4M3
+// caches: warps 12-15 convert every tile from codes to fp16 and prepare V and
+// the descales as they go; Q (scaled by a power of two per row), K, P and V
+// are fp16 operands, exact but for P.
+//
+// Masked places: see attn_tree_sm103.cu.  Here V rows past the sequence, and
+// drafted tokens' V rows with a NaN or an infinity, are zeroed before the
+// product; the latter are added again at the end of a piece to the rows that
+// see them, with scores computed anew (a slow path that ordinary data never
+// takes).
+//
+// Bound: HBM up to about 128 rows (2 * 128 rows * 128 keys * 128 columns * 2
+// products take 1075 cycles of an SM's tensor cores, reading the 64 KiB tile
+// 2785 cycles of its share of HBM), the tensor cores and the exponentials above.
+#include <cmath>
+#include <cstdint>
+
+#include "tree_plan.h"
+
+namespace gb300 {
+namespace {
+
+constexpr int kTcKeys = 128;
+constexpr int kTcRows = 256;
+constexpr float kTcTau = 8.0f;        // rescale threshold (log2 units)
+constexpr float kTcFrame = 128.0f;    // E4M3: P is held times 2^7 / F (P <= 2^8, fp16 < 2^16)
+constexpr float kTcLn2 = 0.69314718055994530942f;
+
+template <int D, bool F8>
+struct TcCfg {
+    static constexpr int kThreads = F8 ? 512 : 384;
+    // registers of the control, softmax and converter warpgroups: their sum is
+    // the launch's (168 or 128 per thread)
+    static constexpr int kRegsControl = F8 ? 80 : 104;
+    static constexpr int kRegsSoftmax = F8 ? 176 : 200;
+    static constexpr int kRegsConvert = 80;
+    static constexpr int kTile = 128 * D * 2;                  // 16-bit operand tile
+    static constexpr int kStages = F8 ? 3 : (D == 128 ? 4 : 8);
+    static constexpr int kRawTile = 128 * 128;                 // E4M3 codes
+    static constexpr int kRawStages = F8 ? 3 : 0;
+    static constexpr int kRing = 2 * kTile;                    // after Q0, Q1
+    static constexpr int kRaw = kRing + kStages * kTile;
+    static constexpr int kBar = kRaw + kRawStages * kRawTile;
+    static constexpr int kSmem = kBar + 12 * 1024;
+    static_assert(kSmem <= 232448, "shared memory budget");
+};
+static_assert(128 * (104 + 2 * 200) <= 384 * 168 && 128 * (80 + 2 * 176 + 80) <= 512 * 128, "register split");
+
+constexpr int kFix = 8;        // special tiles between the fixer and its readers
+// Marks of the V rows that were taken out: for each of the last pieces, for
+// each of its special tiles (1024 drafted tokens reach over 10 at most), a bit
+// per key.  A writer is at most 4 pieces ahead of the readers (a piece takes two
+// of at most 8 ring slots), so 8 buffers need no hand-shake.
+constexpr int kBadBufs = 8;
+constexpr int kBadTiles = 10;
+constexpr int kDs = 4;
+
+struct TcBars {
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t full[8], empty[8];       // operand tiles
+    uint64_t raw_full[4], raw_empty[4];
+    uint64_t ds_full[kDs], ds_empty[kDs];
+    uint64_t fix_full[kFix];
+    uint64_t stat, done, drain;
+    TreeRange range;
+    uint32_t tmem_base;
+    int abort;
+    uint32_t bad[kBadBufs][kBadTiles][4];
+    float qs[2][128];                   // E4M3: what a row's products are multiplied with
+    float m[2][128], l[2][128], lx[2][128];
+    float fin[2];                       // E4M3: F / frame of a stream at the end
+    alignas(16) float kf[kDs][128];     // E4M3: K's descales of a tile
+    alignas(16) float wv[kDs][128];     // E4M3: V's descales times frame / F
+    int fexp[kDs];
+};
+static_assert(sizeof(TcBars) <= 12 * 1024, "barrier block");
+
+__device__ __forceinline__ void tc_abort(TcBars* bars, unsigned int* err) {
+    atomicOr(err, kErrTimeout);
+    *((volatile int*)&bars->abort) = 1;
+}
+__device__ __forceinline__ float tc_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ uint32_t tc_pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void tc_e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+__device__ __forceinline__ uint4 tc_lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void tc_lds_2x64(uint32_t a, uint64_t& x, uint64_t& y) {
+    asm volatile("ld.shared.v2.b64 {%0,%1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort_flag,
+                                          int polls = 0) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(bar), parity & 1u, abort_flag, polls));
+}
+
+// A piece's streams.  Tile s of stream t is key tile k0 + (pair ? s : 2 s + t).
+struct TcPiece {
+    TreePiece w;
+    int rows, n, prefix;
+    bool pair;
+    __device__ __forceinline__ void set(const TreeParams& p) {
+        rows = min(kTcRows, w.drafted * p.G - w.rt * kTcRows);
+        n = w.k1 - w.k0;
+        prefix = w.keys - w.drafted;
+        pair = rows > 128;
+    }
+    __device__ __forceinline__ int tile(int s, int t) const { return pair ? s : 2 * s + t; }
+    __device__ __forceinline__ bool has(int s, int t) const { return tile(s, t) < n; }
+    // a tile with drafted tokens or past the sequence's end
+    __device__ __forceinline__ bool special(int j) const { return (w.k0 + j + 1) * kTcKeys > prefix; }
+    __device__ __forceinline__ int first_special() const { return max(0, prefix / kTcKeys - w.k0); }
+};
+
+// ------------------------------------------------------------------ producer
+// One lane.  The loads of a piece come in the order the products take them:
+// K of the first tile of each stream, then per tile its V and the K of the
+// stream's next tile.
+template <int D, bool F8>
+__device__ void tc_produce(const CUtensorMap* tk, const CUtensorMap* tv, uint8_t* smem, TcBars* bars,
+                           const TreeParams& p) {
+    using C = TcCfg<D, F8>;
+    constexpr int kSlots = F8 ? C::kRawStages : C::kStages;
+    constexpr int kBytes = F8 ? C::kRawTile : C::kTile;
+    uint64_t* full = F8 ? bars->raw_full : bars->full;
+    uint64_t* empty = F8 ? bars->raw_empty : bars->empty;
+    uint8_t* ring = smem + (F8 ? C::kRaw : C::kRing);
+    const volatile int* abort_flag = &bars->abort;
+    const int boxes = kTcKeys / p.box_keys;
+    long long issued = 0;
+    bool ok = true;
+    TreeWalk walk;
+    walk.start(bars->range);
+    TcPiece x;
+    auto load = [&](const CUtensorMap* map, int j) {
+        const int slot = (int)(issued % kSlots);
+        const long long round = issued / kSlots;
+        if (round > 0) ok = mbar_wait(smem_u32(&empty[slot]), (uint32_t)((round - 1) & 1), abort_flag);
+        if (!ok) return;
+        const uint32_t bar = smem_u32(&full[slot]);
+        mbar_arrive_expect_tx(bar, kBytes);
+        const uint32_t dst = smem_u32(ring + slot * kBytes);
+        for (int i = 0; i < boxes; ++i) {
+            int off;
+            const int page = tree_page(p, x.w.b, (x.w.k0 + j) * kTcKeys + i * p.box_keys, x.w.keys, off);
+            const uint32_t to = dst + i * p.box_keys * 128;
+            if constexpr (F8) {
+                tma_load_4d(to, map, bar, 0, x.w.h, off, page);
+            } else {
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) tma_load_4d(to + c * 16384, map, bar, 64 * c, x.w.h, off, page);
+            }
+        }
+        ++issued;
+    };
+    while (ok && walk.next(p, x.w)) {
+        x.set(p);
+        const int ahead = x.pair ? 1 : 2;
+        for (int j = 0; j < ahead && j < x.n && ok; ++j) load(tk, j);
+        for (int j = 0; j < x.n && ok; ++j) {
+            load(tv, j);
+            if (ok && j + ahead < x.n) load(tk, j + ahead);
+        }
+    }
+    if (!ok) tc_abort(bars, p.err);
+    for (int slot = 0; slot < kSlots && slot < issued; ++slot) {  // every copy lands
+        const long long n = (issued - slot + kSlots - 1) / kSlots;
+        mbar_wait(smem_u32(&full[slot]), (uint32_t)((n - 1) & 1), nullptr);
+    }
+}
+
+// ----------------------------------------------------------------- MMA issuer
+constexpr uint32_t kTcDescHi = sdesc_hi_sw128(1024);
+
+template <int D, bool F8>
+__device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreeParams& p) {
+    using C = TcCfg<D, F8>;
+    const volatile int* abort_flag = &bars->abort;
+    // (both operands bf16, or both fp16: format code 0)
+    const int ncols = (p.dh + 15) / 16 * 16;  // columns past the head dim are skipped
+    const int ksteps = ncols / 16;
+    const uint32_t drop = F8 ? (1u << 7) | (1u << 10) : 0u;
+    const uint32_t idS = make_idesc_bf16(128, kTcKeys, 0, 0) & ~drop;
+    const uint32_t idO = make_idesc_bf16(128, ncols, 0, 1) & ~drop;
+    const uint32_t q_lo[2] = {sdesc_lo(smem_u32(smem), 16), sdesc_lo(smem_u32(smem + C::kTile), 16)};
+    const uint32_t ring = smem_u32(smem + C::kRing);
+    long long used = 0;  // operand tiles taken
+    uint32_t cnt_q[2] = {0u, 0u}, cnt_p[2] = {0u, 0u}, cnt_fix = 0;
+    bool ok = true;
+    auto take = [&](int& slot) {
+        slot = (int)(used % C::kStages);
+        ok = warp_wait(&bars->full[slot], (uint32_t)(used / C::kStages), abort_flag);
+        ++used;
+        tc_fence_after();
+    };
+    TreeWalk walk;
+    walk.start(bars->range);
+    TcPiece x;
+    while (ok && walk.next(p, x.w)) {
+        x.set(p);
+        int slot_k = 0, slot_v = 0;
+        auto scores = [&](int t) {
+            const uint32_t k_lo = sdesc_lo(ring + slot_k * C::kTile, 16);
+            const uint32_t a_lo = q_lo[x.pair ? t : 0];
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                if (kk >= ksteps) break;
+                const uint32_t step = (kk >> 2) * (16384 >> 4) + (kk & 3) * (32 >> 4);
+                mma_ss_warp(tmem + t * 128, sdesc_join(a_lo + step, kTcDescHi), sdesc_join(k_lo + step, kTcDescHi),
+                            idS, kk > 0 ? 1u : 0u);
+            }
+            mma_commit_warp(smem_u32(&bars->s_full[t]));
+            if (!x.pair || t == 1) mma_commit_warp(smem_u32(&bars->empty[slot_k]));
+        };
+        for (int t = 0; t < 2 && ok; ++t) {
+            if (!x.has(0, t)) continue;
+            if (x.pair || t == 0) {
+                ok = warp_wait(&bars->q_full[t], cnt_q[t]++, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            if (!x.pair || t == 0) take(slot_k);
+            if (ok) scores(t);
+        }
+        for (int s = 0; ok && x.has(s, 0); ++s) {
+            for (int t = 0; t < 2 && ok; ++t) {
+                if (!x.has(s, t)) continue;
+                if (!x.pair || t == 0) {
+                    take(slot_v);
+                    if (!F8 && ok && x.special(x.tile(s, t))) {
+                        ok = warp_wait(&bars->fix_full[cnt_fix % kFix], cnt_fix / kFix, abort_flag);
+                        ++cnt_fix;
+                    }
+                    if (!ok) break;
+                }
+                ok = warp_wait(&bars->p_full[t], cnt_p[t]++, abort_flag, 32);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t v_lo = sdesc_lo(ring + slot_v * C::kTile, 16384);
+#pragma unroll
+                for (int kk = 0; kk < kTcKeys / 16; ++kk)
+                    mma_ts_warp(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
+                                sdesc_join(v_lo + kk * (2048 >> 4), kTcDescHi), idO, (s > 0 || kk > 0) ? 1u : 0u);
+                if (!x.pair || t == 1) mma_commit_warp(smem_u32(&bars->empty[slot_v]));
+                if (x.has(s + 1, t)) {
+                    if (!x.pair || t == 0) take(slot_k);
+                    if (ok) scores(t);  // in order after the product that reads P over it
+                } else {
+                    mma_commit_warp(smem_u32(&bars->o_full[t]));
+                }
+            }
+        }
+    }
+    if (!ok && elect_one()) tc_abort(bars, p.err);
+    mma_commit_warp(smem_u32(&bars->drain));  // every product is done before TMEM goes
+    mbar_wait(smem_u32(&bars->drain), 0, nullptr);
+    __syncwarp();
+}
+
+// --------------------------------------------------- V of special tiles, bf16
+// Two warps, two keys a thread: rows past the sequence are zeroed, drafted
+// tokens' rows with a NaN or an infinity are noted and zeroed.
+template <int D>
+__device__ void tc_fix(int wf, uint8_t* smem, TcBars* bars, const TreeParams& p) {
+    using C = TcCfg<D, false>;
+    const int lane = threadIdx.x & 31;
+    const volatile int* abort_flag = &bars->abort;
+    long long seen = 0;
+    uint32_t fixed = 0;
+    bool ok = true;
+    TreeWalk walk;
+    walk.start(bars->range);
+    TcPiece x;
+    // the next load of the ring (every one is waited for: a barrier's parity
+    // tells only the last phase from the one before)
+    auto next_load = [&]() {
+        const int slot = (int)(seen % C::kStages);
+        ok = warp_wait(&bars->full[slot], (uint32_t)(seen / C::kStages), abort_flag);
+        ++seen;
+        return slot;
+    };
+    for (int piece = 0; ok && walk.next(p, x.w); ++piece) {
+        x.set(p);
+        const int ahead = x.pair ? 1 : 2;
+        for (int j = 0; j < ahead && j < x.n && ok; ++j) next_load();
+        for (int j = 0; j < x.n && ok; ++j) {
+            const int slot = next_load();
+            if (ok && x.special(j)) {
+                const uint32_t tile = smem_u32(smem + C::kRing + slot * C::kTile);
+                uint32_t* marks = bars->bad[piece % kBadBufs][j - x.first_special()];
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    const int row = wf * 64 + i * 32 + lane;
+                    const int key = (x.w.k0 + j) * kTcKeys + row;
+                    const uint32_t at = tile + row * 128;
+                    bool bad = false;
+                    if (key >= x.prefix && key < x.w.keys) {
+                        for (int c = 0; c < p.dh / 8; ++c) {
+                            const uint4 v = tc_lds128(at + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4));
+                            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                bad |= (u[e] & 0x7F80u) == 0x7F80u || (u[e] & 0x7F800000u) == 0x7F800000u;
+                        }
+                    }
+                    const uint32_t votes = __ballot_sync(0xFFFFFFFFu, bad);
+                    if (lane == 0) marks[2 * wf + i] = votes;
+                    if (bad || key >= x.w.keys)
+                        for (int c = 0; c < D / 8; ++c)
+                            sts128(at + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4), 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->fix_full[fixed % kFix]));
+                ++fixed;
+            }
+            if (ok && j + ahead < x.n) next_load();
+        }
+    }
+    if (!ok && lane == 0) tc_abort(bars, p.err);
+}
+
+// ------------------------------------------------------- codes to fp16, E4M3
+// Four warps.  Eight lanes take a row's 128 codes, 16 each; the two 16-byte
+// results go out in an order that keeps a quarter-warp's stores on different
+// banks.  With K of a tile its descales are laid out for the softmax: K's as
+// they are, V's times frame / F, F = 2^fexp above every one so far.
+template <int D>
+__device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams& p) {
+    using C = TcCfg<D, true>;
+    const int lane = threadIdx.x & 31;
+    const volatile int* abort_flag = &bars->abort;
+    long long taken = 0;
+    uint32_t tiles = 0;
+    bool ok = true;
+    TreeWalk walk;
+    walk.start(bars->range);
+    TcPiece x;
+    float kd = 0.f, vd[4] = {0.f, 0.f, 0.f, 0.f};
+    // descales of tile j: K's of key 32 wc + lane, V's of keys lane + 32 i
+    auto fetch = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            int off;
+            const int page = tree_page(p, x.w.b, (x.w.k0 + j) * kTcKeys + 32 * i + lane, x.w.keys, off);
+            const long long at = ((long long)(page < 0 ? 0 : page) * p.Hkv + x.w.h) * p.page_size + off;
+            vd[i] = page < 0 ? 0.f : __ldg(p.v_descale + at);
+            if (i == wc) kd = page < 0 ? 0.f : __ldg(p.k_descale + at);
+        }
+    };
+    for (int piece = 0; ok && walk.next(p, x.w); ++piece) {
+        x.set(p);
+        int fexp = -100;
+        const int ahead = x.pair ? 1 : 2;
+        // one tile of codes; is_v: rows that must not enter the product are zeroed
+        auto convert = [&](int j, bool is_v) {
+            const int rs = (int)(taken % C::kRawStages), os = (int)(taken % C::kStages);
+            ok = warp_wait(&bars->raw_full[rs], (uint32_t)(taken / C::kRawStages), abort_flag);
+            if (ok && taken >= C::kStages)
+                ok = warp_wait(&bars->empty[os], (uint32_t)(taken / C::kStages) - 1u, abort_flag);
+            if (!ok) return;
+            const uint32_t raw = smem_u32(smem + C::kRaw + rs * C::kRawTile);
+            const uint32_t out = smem_u32(smem + C::kRing + os * C::kTile);
+            const int c = lane & 7;
+            const bool check = is_v && x.special(j);
+            uint4 w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int row = 32 * wc + 4 * i + (lane >> 3);
+                w[i] = tc_lds128(raw + row * 128 + ((c ^ (row & 7)) << 4));
+            }
+            if (check) {
+                uint32_t marks = 0u;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = 32 * wc + 4 * i + (lane >> 3);
+                    const int key = (x.w.k0 + j) * kTcKeys + row;
+                    const bool drafted = key >= x.prefix && key < x.w.keys;
+                    bool hit = false;
+                    if (drafted) {
+                        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) hit |= ((u[e >> 2] >> (8 * (e & 3))) & 0x7Fu) == 0x7Fu;
+                        if (c == 0) {
+                            int off;
+                            const int page = tree_page(p, x.w.b, key, x.w.keys, off);
+                            if (page >= 0)
+                                hit |= !isfinite(__ldg(p.v_descale + ((long long)page * p.Hkv + x.w.h) * p.page_size + off));
+                        }
+                    }
+                    const unsigned votes = __ballot_sync(0xFFFFFFFFu, hit);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        if ((votes >> (8 * g)) & 0xFFu) marks |= 1u << (4 * i + g);
+                    if (key >= x.w.keys || ((votes >> (lane & 24)) & 0xFFu)) w[i] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                if (lane == 0) bars->bad[piece % kBadBufs][j - x.first_special()][wc] = marks;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int row = 32 * wc + 4 * i + (lane >> 3);
+                uint32_t h[8];
+                tc_e4m3x4(w[i].x, h[0], h[1]);
+                tc_e4m3x4(w[i].y, h[2], h[3]);
+                tc_e4m3x4(w[i].z, h[4], h[5]);
+                tc_e4m3x4(w[i].w, h[6], h[7]);
+                const uint32_t dst = out + (c >> 2) * 16384 + row * 128;
+                const int ch = 2 * (c & 3);
+                const bool swap = c & 4;  // the upper half's lanes write their odd chunk first
+                const uint32_t d0 = dst + (((ch + (swap ? 1 : 0)) ^ (row & 7)) << 4);
+                const uint32_t d1 = dst + (((ch + (swap ? 0 : 1)) ^ (row & 7)) << 4);
+                sts128(d0, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
+                sts128(d1, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&bars->raw_empty[rs]));
+                mbar_arrive(smem_u32(&bars->full[os]));
+            }
+            ++taken;
+        };
+        auto descales = [&](int j) {
+            const int slot = (int)(tiles % kDs);
+            if (tiles >= kDs) {
+                ok = warp_wait(&bars->ds_empty[slot], tiles / kDs - 1u, abort_flag);
+                if (!ok) return;
+            }
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool drop = !isfinite(vd[i]) && (x.w.k0 + j) * kTcKeys + 32 * i + lane >= x.prefix;
+                if (drop) vd[i] = 0.f;  // its row is added apart
+                top = fmaxf(top, fabsf(vd[i]));
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+            fexp = max(fexp, min((int)(__float_as_uint(top) >> 23) - 126, 111));
+            const float fr = kTcFrame * tc_pow2(-fexp);
+            float mine = vd[0];
+#pragma unroll
+            for (int i = 1; i < 4; ++i) mine = wc == i ? vd[i] : mine;
+            bars->kf[slot][32 * wc + lane] = kd;
+            bars->wv[slot][32 * wc + lane] = mine * fr;
+            if (wc == 0 && lane == 0) bars->fexp[slot] = fexp;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full[slot]));
+            ++tiles;
+        };
+        fetch(0);
+        for (int j = 0; j < ahead && j < x.n && ok; ++j) {
+            descales(j);
+            if (j + 1 < x.n) fetch(j + 1);
+            if (ok) convert(j, false);
+        }
+        for (int j = 0; j < x.n && ok; ++j) {
+            convert(j, true);
+            if (ok && j + ahead < x.n) {
+                descales(j + ahead);
+                if (j + ahead + 1 < x.n) fetch(j + ahead + 1);
+                if (ok) convert(j + ahead, false);
+            }
+        }
+    }
+    if (!ok && lane == 0) tc_abort(bars, p.err);
+}
+
+// -------------------------------------------------------------------- softmax
+// 32 keys' worth of a row's mask, key u0 + i (counted from the first drafted
+// token; negative: before it) at bit i.
+__device__ __forceinline__ uint32_t tc_allow32(const TreeParams& p, int b, int t, int drafted, int u0) {
+    if (u0 <= -32) return 0xFFFFFFFFu;
+    const int seen = p.mask ? drafted : min(t + 1, drafted);
+    const int n = seen - u0;  // keys below `seen`
+    const uint32_t range = n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
+    if (!p.mask) return range;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(p.mask + ((size_t)b * p.T + t) * p.W);
+    uint32_t m;
+    if (u0 < 0) {
+        m = (__ldg(w) << -u0) | ((1u << -u0) - 1u);
+    } else {
+        const int i = u0 >> 5;
+        const uint32_t lo = i < 2 * p.W ? __ldg(w + i) : 0u;
+        const uint32_t hi = i + 1 < 2 * p.W ? __ldg(w + i + 1) : 0u;
+        m = __funnelshift_r(lo, hi, u0 & 31);
+    }
+    return m & range;
+}
+
+struct TcRow {
+    float m, l, lx;  // running maximum (log2 units), sums of rounded and of unrounded P
+    int fexp;        // E4M3: F of what O holds
+};
+
+// Half a tile of this row's scores, columns [64 H, 64 H + 64).
+template <bool F8, bool MASKED, int H>
+__device__ __forceinline__ void tc_half(uint32_t tS, uint32_t kf, const uint32_t (&allow)[4], uint32_t (&sr)[64]) {
+    tmem_ld32(tS + 64 * H, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+    tmem_ld32(tS + 64 * H + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+    tmem_wait_ld();
+    if constexpr (F8) {
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+            uint64_t a, b;
+            float u, v;
+            tc_lds_2x64(kf + (64 * H + i) * 4, a, b);
+            f2_split(f2_mul(f2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), a), u, v);
+            sr[i] = __float_as_uint(u);
+            sr[i + 1] = __float_as_uint(v);
+            f2_split(f2_mul(f2(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])), b), u, v);
+            sr[i + 2] = __float_as_uint(u);
+            sr[i + 3] = __float_as_uint(v);
+        }
+    }
+    if constexpr (MASKED) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+            if (!(allow[2 * H + (i >> 5)] >> (i & 31) & 1u)) sr[i] = 0xFF800000u;
+    }
+}
+__device__ __forceinline__ float tc_max64(const uint32_t (&sr)[64], float from) {
+    float a = from, b = -INFINITY, c = -INFINITY, d = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 64; i += 8) {
+        a = fmax3(a, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+        b = fmax3(b, __uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3]));
+        c = fmax3(c, __uint_as_float(sr[i + 4]), __uint_as_float(sr[i + 5]));
+        d = fmax3(d, __uint_as_float(sr[i + 6]), __uint_as_float(sr[i + 7]));
+    }
+    return fmax3(fmaxf(a, b), c, d);
+}
+// P of half a tile to TMEM (over S's first 64 columns), and its sum.
+template <bool F8, bool MASKED, int H>
+__device__ __forceinline__ float tc_probs(uint32_t tS, uint32_t wv, const uint32_t (&allow)[4],
+                                          const uint32_t (&sr)[64], float c, float m) {
+    const uint64_t c2 = f2(c, c), nm2 = f2(-m, -m);
+    uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int col = 32 * g + 2 * i;
+            float a, b;
+            f2_split(f2_fma(f2(__uint_as_float(sr[col]), __uint_as_float(sr[col + 1])), c2, nm2), a, b);
+            float p0 = ex2(a), p1 = ex2(b);
+            if constexpr (MASKED) {
+                const uint32_t w = allow[2 * H + g];
+                p0 = w >> (2 * i) & 1u ? p0 : 0.f;
+                p1 = w >> (2 * i + 1) & 1u ? p1 : 0.f;
+            }
+            const uint64_t pp = f2(p0, p1);
+            if (i & 1) s1 = f2_add(s1, pp);
+            else s0 = f2_add(s0, pp);
+            if constexpr (F8) {
+                uint64_t x, y;
+                tc_lds_2x64(wv + (64 * H + (col & ~3)) * 4, x, y);  // (once for two pairs)
+                float u, v;
+                f2_split(f2_mul(pp, i & 1 ? y : x), u, v);
+                pk[i] = tc_pack_f16(u, v);
+            } else {
+                pk[i] = pack_bf16x2(p0, p1);
+            }
+        }
+        tmem_st16(tS + 32 * H + 16 * g, pk);
+    }
+    float u, v;
+    f2_split(f2_add(s0, s1), u, v);
+    return u + v;
+}
+
+template <int D, bool F8, bool MASKED>
+__device__ __forceinline__ void tc_softmax_tile(uint32_t tS, uint32_t tO, uint32_t kf, uint32_t wv, int fexp,
+                                                const uint32_t (&allow)[4], bool first, float c, int ncols,
+                                                TcRow& r) {
+    uint32_t sr[64];
+    tc_half<F8, MASKED, 1>(tS, kf, allow, sr);
+    float mx = tc_max64(sr, -INFINITY);
+    tc_half<F8, MASKED, 0>(tS, kf, allow, sr);
+    mx = tc_max64(sr, mx);
+    const float mt = MASKED && mx == -INFINITY ? -INFINITY : mx * c;
+    const bool need = mt > r.m + kTcTau;
+    bool grow = false;
+    if constexpr (F8) grow = !first && fexp != r.fexp;
+    if (__any_sync(0xFFFFFFFFu, need) || grow) {
+        const float m_new = need ? mt : r.m;
+        float alpha = need ? ex2(r.m - m_new) : 1.f;
+        r.l *= alpha;
+        r.lx *= alpha;
+        r.m = m_new;
+        if constexpr (F8)
+            if (grow) alpha = r.fexp - fexp < -126 ? 0.f : alpha * tc_pow2(r.fexp - fexp);
+        if (!first) {
+            // O is stable: this S was issued after the product before it
+            const uint64_t a2 = f2(alpha, alpha);
+#pragma unroll 1
+            for (int cc = 0; cc < ncols; cc += 16) {
+                uint32_t o[16];
+                asm volatile(
+                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                    "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                    : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
+                      "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
+                      "=r"(o[14]), "=r"(o[15])
+                    : "r"(tO + cc)
+                    : "memory");
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    float u, v;
+                    f2_split(f2_mul(f2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), a2), u, v);
+                    o[i] = __float_as_uint(u);
+                    o[i + 1] = __float_as_uint(v);
+                }
+                tmem_st16(tO + cc, o);
+            }
+        }
+    }
+    if constexpr (F8) r.fexp = fexp;
+    const float m = MASKED && r.m == -INFINITY ? 0.f : r.m;
+    if constexpr (!F8) {
+        // the tile's largest weight is its rounded P: its error enters l too
+        const float pm = MASKED && mx == -INFINITY ? 0.f : ex2(fmaf(mx, c, -m));
+        r.l += bf16lo_to_f32(pack_bf16x2(pm, 0.f)) - pm;
+    }
+    float sum = tc_probs<F8, MASKED, 0>(tS, wv, allow, sr, c, m);
+    tc_half<F8, MASKED, 1>(tS, kf, allow, sr);
+    sum += tc_probs<F8, MASKED, 1>(tS, wv, allow, sr, c, m);
+    r.l += sum;
+    r.lx += sum;
+}
+
+// Adds the drafted tokens whose V rows were taken out of the product to 16
+// columns of a finished row (rare; scores computed anew in fp32).
+template <bool F8>
+__device__ __noinline__ void tc_add_bad(const TreeParams& p, const TcPiece& x, const uint32_t* bad, int t,
+                                        const __nv_bfloat16* q, float m, float inv, int col, float (&v)[16]) {
+    const int key0 = (x.w.k0 + x.first_special()) * kTcKeys;
+    const int end = min(x.w.k1 * kTcKeys, x.w.keys);
+    for (int key = max(key0, x.prefix); key < end; ++key) {
+        const int i = key - key0;
+        if (!(*((const volatile uint32_t*)bad + (i >> 5)) >> (i & 31) & 1u)) continue;
+        if (!tree_sees(p, x.w.b, t, key - x.prefix)) continue;
+        int off;
+        const int page = tree_page(p, x.w.b, key, x.w.keys, off);
+        if (page < 0) continue;
+        const long long row = (((long long)page * p.page_size + off) * p.Hkv + x.w.h) * p.dh;
+        const long long ds = ((long long)page * p.Hkv + x.w.h) * p.page_size + off;
+        auto value = [&](const uint8_t* pages, const float* descale, int i) {
+            if constexpr (F8) {
+                uint32_t lo, hi;
+                tc_e4m3x4(pages[row + i], lo, hi);
+                float f;
+                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(f) : "r"(lo));
+                return f * descale[ds];
+            } else {
+                return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(pages)[row + i]);
+            }
+        };
+        float s = 0.f;
+        for (int i = 0; i < p.dh; ++i) s = fmaf(__bfloat162float(q[i]), value(p.k_pages, p.k_descale, i), s);
+        const float w = ex2(s * p.c - m) * inv;
+        for (int i = 0; i < 16; ++i)
+            if (col + i < p.dh) v[i] = fmaf(w, value(p.v_pages, p.v_descale, col + i), v[i]);
+    }
+}
+
+// Q rows of a stream's tile into shared memory: this warp's 32 rows, 16 lanes
+// a row (rows past the last repeat it), 128-byte swizzled 64-column halves.
+template <int D, bool F8>
+__device__ __forceinline__ void tc_load_q(const TreeParams& p, const TcPiece& x, int row0, int rows, int wq, int lane,
+                                          uint32_t tile, float* qs) {
+    constexpr int kLanes = D / 8;          // lanes of a row
+    constexpr int kPer = 32 / kLanes;      // rows of an instruction
+    const int c = lane % kLanes;
+    uint4 v[32 / kPer];
+#pragma unroll
+    for (int i = 0; i < 32 / kPer; ++i) {
+        const int r = x.w.rt * kTcRows + row0 + min(wq * 32 + i * kPer + lane / kLanes, rows - 1);
+        const int t = r / p.G;
+        const size_t at = ((size_t)x.w.b * p.Hq + (size_t)x.w.h * p.G + (r - t * p.G)) * p.T + t;
+        v[i] = 8 * c < p.dh ? __ldg(reinterpret_cast<const uint4*>(p.q + at * p.dh + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < 32 / kPer; ++i) {
+        const int row = wq * 32 + i * kPer + lane / kLanes;
+        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        if constexpr (F8) {
+            float mx = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16lo_to_f32(w[e])), fabsf(bf16hi_to_f32(w[e]))));
+#pragma unroll
+            for (int off = kLanes / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
+            // a power of two that puts the row's largest value in [2^14, 2^15)
+            int e = (int)(__float_as_uint(mx) >> 23) - 127;
+            e = e < -100 ? -100 : (e > 126 ? 126 : e);
+            const float up = tc_pow2(14 - e);
+            if (c == 0) qs[row] = p.c * tc_pow2(e - 14);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = tc_pack_f16(bf16lo_to_f32(w[k]) * up, bf16hi_to_f32(w[k]) * up);
+        }
+        sts128(tile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+template <int D, bool F8>
+__device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars, uint32_t tmem, const TreeParams& p) {
+    using C = TcCfg<D, F8>;
+    const volatile int* abort_flag = &bars->abort;
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    const uint32_t tS = tmem + t * 128 + lanes;
+    const uint32_t tO = tmem + 256 + lanes;  // of stream 0; stream 1: + 128
+    const int ncols = (p.dh + 15) / 16 * 16;
+    const int me = wq * 32 + lane;
+    uint32_t cnt_s = 0, cnt_o = 0, cnt_x = 0, tiles = 0;
+    bool ok = true, first_piece = true;
+    TreeWalk walk;
+    walk.start(bars->range);
+    TcPiece x;
+    for (int piece = 0; ok && walk.next(p, x.w); ++piece) {
+        x.set(p);
+        // this warpgroup's row tile, and this thread's row of it
+        const int row0 = x.pair ? 128 * t : 0;
+        const int rows = min(128, x.rows - row0);
+        const bool active = wq * 32 < rows;  // (warp-uniform)
+        const int row = row0 + min(me, rows - 1);
+        const int r = x.w.rt * kTcRows + row;
+        const int tok = r / p.G;
+        const size_t bht = ((size_t)x.w.b * p.Hq + (size_t)x.w.h * p.G + (r - tok * p.G)) * p.T + tok;
+        if (x.pair || t == 0) {
+            const int tile = x.pair ? t : 0;
+            if (active) tc_load_q<D, F8>(p, x, row0, rows, wq, lane, smem_u32(smem + tile * C::kTile), bars->qs[tile]);
+            if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[tile]));
+        }
+        if constexpr (F8) {
+            // in split mode stream 1 reads the factors that stream 0's warps wrote
+            if (!x.pair && t == 1) {
+                ok = warp_wait(&bars->q_full[0], (uint32_t)piece, abort_flag);
+                if (!ok) break;
+            }
+        }
+        const float c = F8 ? *((volatile float*)&bars->qs[x.pair ? t : 0][me]) : p.c;
+        TcRow st;
+        st.m = -INFINITY;
+        st.l = st.lx = 0.f;
+        st.fexp = -100;
+        int s = 0;
+        for (; x.has(s, t) && ok; ++s) {
+            const int j = x.tile(s, t);
+            ok = warp_wait(&bars->s_full[t], cnt_s++, abort_flag, 32);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t kf = 0, wv = 0;
+            int fexp = 0;
+            if constexpr (F8) {
+                const uint32_t g = tiles + (uint32_t)j;
+                const int slot = (int)(g % kDs);
+                ok = warp_wait(&bars->ds_full[slot], g / kDs, abort_flag);
+                if (!ok) break;
+                kf = smem_u32(bars->kf[slot]);
+                wv = smem_u32(bars->wv[slot]);
+                fexp = *((volatile int*)&bars->fexp[slot]);
+            }
+            if (active) {
+                uint32_t allow[4];
+                if (x.special(j)) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        allow[i] = tc_allow32(p, x.w.b, tok, x.w.drafted, (x.w.k0 + j) * kTcKeys + 32 * i - x.prefix);
+                    tc_softmax_tile<D, F8, true>(tS, tO + 128 * t, kf, wv, fexp, allow, s == 0, c, ncols, st);
+                } else {
+                    tc_softmax_tile<D, F8, false>(tS, tO + 128 * t, kf, wv, fexp, allow, s == 0, c, ncols, st);
+                }
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&bars->p_full[t]));
+                if constexpr (F8) {
+                    const uint32_t e = smem_u32(&bars->ds_empty[(tiles + (uint32_t)j) % kDs]);
+                    mbar_arrive(e);
+                    if (!x.pair) mbar_arrive(e);  // (the barrier counts both streams' warps)
+                }
+            }
+        }
+        if (!ok) break;
+        tiles += (uint32_t)x.n;
+        if (s > 0) {
+            ok = warp_wait(&bars->o_full[t], cnt_o++, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+        }
+        // ---- epilogue
+        float inv0, inv1 = 0.f, m = st.m, lx = st.lx;  // factors of stream 0's and 1's O
+        int col0 = 0, col1 = ncols;
+        uint32_t tA = tO + 128 * t;
+        if (x.pair) {
+            inv0 = st.l == 0.f ? 0.f : 1.0f / st.l;
+            if constexpr (F8) inv0 *= tc_pow2(st.fexp) / kTcFrame;
+        } else {
+            // the streams' statistics meet in shared memory; each warpgroup
+            // then merges half of the columns, both O's being in its lanes
+            bars->m[t][me] = st.m;
+            bars->l[t][me] = st.l;
+            bars->lx[t][me] = st.lx;
+            if (wq == 0 && lane == 0) bars->fin[t] = F8 ? tc_pow2(st.fexp) / kTcFrame : 1.f;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->stat));
+            ok = warp_wait(&bars->stat, cnt_x, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const float m0 = bars->m[0][me], m1 = bars->m[1][me];
+            m = fmaxf(m0, m1);
+            const float ms = m == -INFINITY ? 0.f : m;
+            const float a0 = ex2(m0 - ms), a1 = ex2(m1 - ms);
+            const float l = a0 * bars->l[0][me] + a1 * bars->l[1][me];
+            lx = a0 * bars->lx[0][me] + a1 * bars->lx[1][me];
+            const float inv = l == 0.f ? 0.f : 1.0f / l;
+            inv0 = a0 * inv * bars->fin[0];
+            inv1 = a1 * inv * bars->fin[1];
+            const int half = (ncols / 2 + 15) / 16 * 16;
+            col0 = t == 0 ? 0 : half;
+            col1 = t == 0 ? half : ncols;
+            tA = tO;
+        }
+        const bool two = !x.pair && x.n > 1;
+        const uint32_t* bad = &bars->bad[piece % kBadBufs][0][0];
+        uint32_t any_bad = 0u;
+        for (int i = 0; i < 4 * (x.n - x.first_special()); ++i) any_bad |= *((const volatile uint32_t*)bad + i);
+        const size_t place = ((size_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * kTcRows + row;
+        if (active) {
+#pragma unroll 1
+            for (int cc = col0; cc < col1; cc += 16) {
+                uint32_t a[16], b[16];
+                asm volatile(
+                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                    "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                    : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]),
+                      "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]),
+                      "=r"(a[14]), "=r"(a[15])
+                    : "r"(tA + cc)
+                    : "memory");
+                if (two)
+                    asm volatile(
+                        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                        : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]),
+                          "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]),
+                          "=r"(b[14]), "=r"(b[15])
+                        : "r"(tA + 128 + cc)
+                        : "memory");
+                tmem_wait_ld();
+                float v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    v[i] = __uint_as_float(a[i]) * inv0;
+                    if (two) v[i] = fmaf(__uint_as_float(b[i]), inv1, v[i]);
+                }
+                if (any_bad) {
+                    const float lsum = x.pair ? st.l : 0.f;
+                    float inv = lsum == 0.f ? 0.f : 1.0f / lsum;
+                    if (!x.pair) {
+                        const float ms = m == -INFINITY ? 0.f : m;
+                        const float l = ex2(bars->m[0][me] - ms) * bars->l[0][me] + ex2(bars->m[1][me] - ms) * bars->l[1][me];
+                        inv = l == 0.f ? 0.f : 1.0f / l;
+                    }
+                    tc_add_bad<F8>(p, x, bad, tok, p.q + bht * p.dh, m, inv, cc, v);
+                }
+                if (me < rows) {
+                    if (!x.w.whole) {
+                        float4* o = reinterpret_cast<float4*>(p.ws_o + place * p.dw + cc);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    } else if (p.out_f32) {
+                        float* o = static_cast<float*>(p.o) + bht * p.dh + cc;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (cc + 4 * i < p.dh)
+                                reinterpret_cast<float4*>(o)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    } else {
+                        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + bht * p.dh + cc;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (cc + 8 * i < p.dh)
+                                reinterpret_cast<uint4*>(o)[i] =
+                                    make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                               pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+                    }
+                }
+            }
+            if (me < rows && (x.pair || t == 0)) {
+                const float lse2 = lx == 0.f ? -INFINITY : m + log2f(lx);
+                if (!x.w.whole) p.ws_lse[place] = lse2;
+                else if (p.lse) p.lse[bht] = lse2 * kTcLn2;
+            }
+        }
+        // O, the statistics and the marks are read: the next piece may write them
+        tc_fence_before();
+        __syncwarp();
+        if (!x.pair) {
+            if (lane == 0) mbar_arrive(smem_u32(&bars->done));
+            ok = warp_wait(&bars->done, cnt_x, abort_flag);
+            ++cnt_x;
+            tc_fence_after();
+        }
+        first_piece = false;
+    }
+    if (!ok && lane == 0) tc_abort(bars, p.err);
+}
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
+attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                    const __grid_constant__ TreeParams p) {
+    using C = TcCfg<D, F8>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    TcBars* bars = reinterpret_cast<TcBars*>(smem + C::kBar);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (smem_u32(smem) & 1023u) {  // the swizzled boxes need 1024-byte bases
+        if (threadIdx.x == 0) atomicOr(p.err, kErrLayout);
+        return;
+    }
+    if (threadIdx.x == 64) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&bars->q_full[t]), 4);
+            mbar_init(smem_u32(&bars->s_full[t]), 1);
+            mbar_init(smem_u32(&bars->p_full[t]), 4);
+            mbar_init(smem_u32(&bars->o_full[t]), 1);
+        }
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(smem_u32(&bars->full[i]), F8 ? 4 : 1);
+            mbar_init(smem_u32(&bars->empty[i]), 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(smem_u32(&bars->raw_full[i]), 1);
+            mbar_init(smem_u32(&bars->raw_empty[i]), 4);
+        }
+        for (int i = 0; i < kDs; ++i) {
+            mbar_init(smem_u32(&bars->ds_full[i]), 4);
+            mbar_init(smem_u32(&bars->ds_empty[i]), 8);
+        }
+        for (int i = 0; i < kFix; ++i) mbar_init(smem_u32(&bars->fix_full[i]), 2);
+        mbar_init(smem_u32(&bars->stat), 8);
+        mbar_init(smem_u32(&bars->done), 8);
+        mbar_init(smem_u32(&bars->drain), 1);
+        bars->abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0) {
+        const TreeRange r = tree_range(p, blockIdx.x);
+        if (lane == 0) bars->range = r;
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&bars->tmem_base), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    if (warp < 4) {
+        reg_dealloc<C::kRegsControl>();
+        if (warp == 0) {
+            if (lane == 0) tc_produce<D, F8>(&tk, &tv, smem, bars, p);
+            __syncwarp();
+        } else if (warp == 1) {
+            tc_mma<D, F8>(smem, bars, tmem, p);
+        } else if constexpr (!F8) {
+            tc_fix<D>(warp - 2, smem, bars, p);
+        }
+    } else if (warp < 12) {
+        reg_alloc<C::kRegsSoftmax>();
+        tc_softmax<D, F8>((warp - 4) >> 2, warp & 3, lane, smem, bars, tmem, p);
+    } else if constexpr (F8) {
+        reg_dealloc<C::kRegsConvert>();
+        tc_convert<D>(warp - 12, smem, bars, p);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, bool F8>
+attn_status_t launch_tc_t(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream,
+                          const DeviceInfo& dev) {
+    using C = TcCfg<D, F8>;
+    static int attr_set[64] = {0};
+    if (dev.device >= 64 || !attr_set[dev.device]) {
+        if (cudaFuncSetAttribute(attn_tree_tc_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::kSmem) != cudaSuccess)
+            return ATTN_ERR_CUDA;
+        if (dev.device < 64) attr_set[dev.device] = 1;
+    }
+    attn_tree_tc_kernel<D, F8><<<p.ctas, C::kThreads, C::kSmem, stream>>>(tk, tv, p);
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+void tree_tc_shape(TreeParams& p, bool f8, int num_sms) {
+    p.tile_rows = kTcRows;
+    p.tile_keys = kTcKeys;
+    p.dw = p.dh <= 64 && !f8 ? 64 : 128;
+    p.ctas = num_sms;
+    p.min_units = 2;
+}
+
+attn_status_t launch_tree_tc(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, bool f8,
+                             cudaStream_t stream, const DeviceInfo& dev) {
+    if (f8) return launch_tc_t<128, true>(tk, tv, p, stream, dev);
+    return p.dw == 64 ? launch_tc_t<64, false>(tk, tv, p, stream, dev) : launch_tc_t<128, false>(tk, tv, p, stream, dev);
+}
+
+}  // namespace gb300

@@ -36,6 +36,8 @@ struct TreeParams {
     const unsigned long long* mask;  // NULL: drafted token t sees tokens 0..t
     const float* k_descale;
     const float* v_descale;
+    const uint8_t* k_pages;
+    const uint8_t* v_pages;
     const __nv_bfloat16* q;
     void* o;
     float* lse;
@@ -197,6 +199,12 @@ __device__ __forceinline__ bool tree_sees(const TreeParams& p, int b, int t, int
     const unsigned long long w = __ldg(p.mask + ((size_t)b * p.T + t) * p.W + (u >> 6));
     return (w >> (u & 63)) & 1ull;
 }
+
+// The kernel for many rows (attn_tree_tc_sm103.cu): its part of the
+// parameters, and its launch.
+void tree_tc_shape(TreeParams& p, bool f8, int num_sms);
+attn_status_t launch_tree_tc(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, bool f8,
+                             cudaStream_t stream, const DeviceInfo& dev);
 
 // Merges the pieces of the items that were cut, and writes the rows past each
 // sequence's drafted tokens (O = 0, LSE = -inf).
