@@ -143,8 +143,10 @@ def _check(code: int, where: str):
 
 def _stream_ptr(stream):
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # the current stream of the current device, without a Stream object
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return ctypes.c_void_p(int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -187,8 +189,22 @@ def _one_device(*tensors):
     return dev
 
 
+class _Here:
+    """No change of device."""
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
 def _on(dev):
     import torch
+    if dev.index == torch._C._cuda_getDevice():   # (a switch and back costs more than a launch)
+        return _HERE
     return torch.cuda.device(dev)
 
 
@@ -781,6 +797,9 @@ def decode_paged(q, k_pages, v_pages, block_table, seqlens, *, scale: float | No
 
 
 # ------------------- positions, the paged cache, drafted tokens -------------------
+_Strides = ctypes.c_longlong * 3
+
+
 def _tensor(t, dtypes, name):
     """A CUDA tensor of one of the given dtypes (any layout)."""
     import torch
@@ -792,28 +811,38 @@ def _tensor(t, dtypes, name):
         raise ValueError(f"{name} must be a CUDA tensor")
 
 
+def _at(t):
+    """Address of an optional tensor."""
+    return None if t is None else t.data_ptr()
+
+
 def _rows(t, name):
     """(B, H, N, d) and the host strides {batch, head, token} of a [B,H,N,d]
     view or a packed [total,H,d] one (B = 1), whose rows are contiguous and
     16-byte aligned."""
-    if t.ndim == 4:
+    nd = t.ndim
+    if nd == 4:
         B, H, N, d = t.shape
         sb, sh, sn, sd = t.stride()
-    elif t.ndim == 3:
-        (N, H, d), B = t.shape, 1
+        if B == 1:
+            sb = 0
+    elif nd == 3:
+        N, H, d = t.shape
         sn, sh, sd = t.stride()
-        sb = 0
+        B, sb = 1, 0
     else:
         raise ValueError(f"{name} must be [B, H, N, d] or packed [total, H, d]")
-    if min(B, H, N, d) < 1:
+    if not (B and H and N and d):
         raise ValueError(f"{name} is empty")
     if sd != 1 and d > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    strides = (ctypes.c_longlong * 3)(sb if B > 1 else 0, sh if H > 1 else 0, sn if N > 1 else 0)
-    per16 = 16 // t.element_size()
-    if any(s % per16 for s in strides) or t.data_ptr() % 16:
+    if H == 1:
+        sh = 0
+    if N == 1:
+        sn = 0
+    if (sb | sh | sn) % (16 // t.element_size()) or t.data_ptr() % 16:
         raise ValueError(f"{name}: rows must be 16-byte aligned")
-    return (B, H, N, d), strides
+    return (B, H, N, d), _Strides(sb, sh, sn)
 
 
 def _used_on(stream, *tensors):
@@ -855,6 +884,49 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "
     return torch.tensor(f, dtype=torch.float64, device=device), mag
 
 
+def _rope_inputs(q, k):
+    """Checks q and k; returns (B, Hq, Hkv, N, d) and their strides."""
+    import torch
+    _tensor(q, (torch.bfloat16, torch.float32), "q")
+    (B, Hq, N, d), qs = _rows(q, "q")
+    if k is None:
+        return B, Hq, 0, N, d, qs, None
+    _tensor(k, (q.dtype,), "k")
+    (Bk, Hkv, Nk, dk), ks = _rows(k, "k")
+    if Bk != B or Nk != N or dk != d or k.ndim != q.ndim:
+        raise ValueError("q / k shape mismatch")
+    return B, Hq, Hkv, N, d, qs, ks
+
+
+def _rope_call(q, k, q_out, k_out, positions, inv_freq, shape, qos, kos, interleaved, inverse,
+               magnitude, stream):
+    """attn_rope once q, k and the outputs are known to be good."""
+    import torch
+    B, Hq, Hkv, N, d, qs, ks = shape
+    _tensor(positions, (torch.int32,), "positions")
+    _need(inv_freq, torch.float64, "inv_freq")
+    if positions.shape == (N,):
+        pos_stride = 0
+    elif positions.shape == (B, N):
+        pos_stride = positions.stride(0) if B > 1 else 0
+    else:
+        raise ValueError("positions must be [B, N] or [N]")
+    if N > 1 and positions.stride(-1) != 1:
+        raise ValueError("positions: the last dimension must be contiguous")
+    pairs = inv_freq.shape[0] if inv_freq.ndim == 1 else 0
+    if not 1 <= pairs <= d // 2:
+        raise ValueError("inv_freq must hold rotary_dim / 2 <= d / 2 frequencies")
+    idt = ATTN_OUT_F32 if q.dtype == torch.float32 else ATTN_OUT_BF16
+    odt = ATTN_OUT_F32 if q_out.dtype == torch.float32 else ATTN_OUT_BF16
+    with _on(_one_device(q, k, q_out, k_out, positions, inv_freq)):
+        rc = load().attn_rope(q.data_ptr(), _at(k), q_out.data_ptr(), _at(k_out), qs, ks, qos, kos,
+                              positions.data_ptr(), pos_stride, inv_freq.data_ptr(), B, Hq, Hkv, N, d,
+                              2 * pairs, 1 if interleaved else 0, 1 if inverse else 0, magnitude, idt,
+                              odt, _stream_ptr(stream))
+    _check(rc, "attn_rope")
+    return q_out, k_out
+
+
 def attn_rope(q, k, q_out, k_out, positions, inv_freq, *, interleaved: bool = False,
               inverse: bool = False, magnitude: float = 1.0, stream=None):
     """Rotary positions on q and k (k and k_out may be None) into caller-provided
@@ -868,43 +940,31 @@ def attn_rope(q, k, q_out, k_out, positions, inv_freq, *, interleaved: bool = Fa
     past rotary_dim are copied.  inverse: the gradient.  In place when an output
     is its input.  Asynchronous on ``stream``."""
     import torch
-    kinds = (torch.bfloat16, torch.float32)
-    for t, n in ((q, "q"), (q_out, "q_out")):
-        _tensor(t, kinds, n)
+    shape = _rope_inputs(q, k)
+    B, Hq, Hkv, N, d = shape[:5]
+    _tensor(q_out, (torch.bfloat16, torch.float32), "q_out")
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
-    _tensor(positions, (torch.int32,), "positions")
-    _need(inv_freq, torch.float64, "inv_freq")
-    (B, Hq, N, d), qs = _rows(q, "q")
-    shape, qos = _rows(q_out, "q_out")
-    if shape != (B, Hq, N, d) or q_out.ndim != q.ndim:
+    if q_out.shape != q.shape:
         raise ValueError("q_out shape mismatch")
-    Hkv, ks, kos = 0, None, None
+    _, qos = _rows(q_out, "q_out")
+    kos = None
     if k is not None:
-        _tensor(k, (q.dtype,), "k")
         _tensor(k_out, (q_out.dtype,), "k_out")
-        (Bk, Hkv, Nk, dk), ks = _rows(k, "k")
-        shape, kos = _rows(k_out, "k_out")
-        if (Bk, Nk, dk) != (B, N, d) or k.ndim != q.ndim:
-            raise ValueError("q / k shape mismatch")
-        if shape != (B, Hkv, N, d) or k_out.ndim != k.ndim:
+        if k_out.shape != k.shape:
             raise ValueError("k_out shape mismatch")
-    if tuple(positions.shape) not in ((N,), (B, N)):
-        raise ValueError("positions must be [B, N] or [N]")
-    if N > 1 and positions.stride(-1) != 1:
-        raise ValueError("positions: the last dimension must be contiguous")
-    pos_stride = positions.stride(0) if positions.ndim == 2 and B > 1 else 0
-    if inv_freq.ndim != 1 or not 1 <= inv_freq.numel() <= d // 2:
-        raise ValueError("inv_freq must hold rotary_dim / 2 <= d / 2 frequencies")
-    idt = ATTN_OUT_F32 if q.dtype == torch.float32 else ATTN_OUT_BF16
-    odt = ATTN_OUT_F32 if q_out.dtype == torch.float32 else ATTN_OUT_BF16
-    with _on(_one_device(q, k, q_out, k_out, positions, inv_freq)):
-        rc = load().attn_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), qs, ks, qos, kos,
-                              _ptr(positions), pos_stride, _ptr(inv_freq), B, Hq, Hkv, N, d,
-                              2 * inv_freq.numel(), int(bool(interleaved)), int(bool(inverse)),
-                              float(magnitude), idt, odt, _stream_ptr(stream))
-    _check(rc, "attn_rope")
-    return q_out, k_out
+        _, kos = _rows(k_out, "k_out")
+    return _rope_call(q, k, q_out, k_out, positions, inv_freq, shape, qos, kos, interleaved,
+                      inverse, magnitude, stream)
+
+
+def _new_rows(x, dtype, H, N, d):
+    """A contiguous output of x's shape and its strides."""
+    import torch
+    out = torch.empty(x.shape, dtype=dtype, device=x.device)
+    if x.ndim == 4:
+        return out, _Strides(H * N * d if x.shape[0] > 1 else 0, N * d if H > 1 else 0, d if N > 1 else 0)
+    return out, _Strides(0, d if H > 1 else 0, H * d if N > 1 else 0)
 
 
 def rope(q, k, positions, inv_freq, *, interleaved: bool = False, magnitude: float = 1.0,
@@ -912,12 +972,17 @@ def rope(q, k, positions, inv_freq, *, interleaved: bool = False, magnitude: flo
     """Allocate the outputs (contiguous, of q's and k's shapes) with torch and
     run attn_rope.  Returns (q_out, k_out); k may be None."""
     import torch
+    shape = _rope_inputs(q, k)
+    _, Hq, Hkv, N, d = shape[:5]
     out_dtype = out_dtype or q.dtype
-    q_out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
-    k_out = None if k is None else torch.empty(k.shape, dtype=out_dtype, device=q.device)
-    _used_on(stream, q_out, k_out)
-    return attn_rope(q, k, q_out, k_out, positions, inv_freq, interleaved=interleaved,
-                     inverse=inverse, magnitude=magnitude, stream=stream)
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be bfloat16 or float32")
+    q_out, qos = _new_rows(q, out_dtype, Hq, N, d)
+    k_out, kos = (None, None) if k is None else _new_rows(k, out_dtype, Hkv, N, d)
+    if stream is not None:
+        _used_on(stream, q_out, k_out)
+    return _rope_call(q, k, q_out, k_out, positions, inv_freq, shape, qos, kos, interleaved,
+                      inverse, magnitude, stream)
 
 
 def rope_backward(dq_out, dk_out, positions, inv_freq, *, interleaved: bool = False,
@@ -944,7 +1009,7 @@ def _check_pages(k_pages, v_pages, k_descale, v_descale):
         return num_blocks, page_size, Hkv, d, ATTN_CACHE_BF16
     for t, n in ((k_descale, "k_descale"), (v_descale, "v_descale")):
         _need(t, torch.float32, n)
-        if tuple(t.shape) != (num_blocks, Hkv, page_size):
+        if t.shape != (num_blocks, Hkv, page_size):
             raise ValueError(f"{n} must be [num_blocks, Hkv, page_size]")
     return num_blocks, page_size, Hkv, d, ATTN_CACHE_E4M3
 
@@ -966,13 +1031,34 @@ def attn_cache_write(k, v, k_pages, v_pages, slots, k_descale=None, v_descale=No
         raise ValueError("k / v / page shapes mismatch")
     _, vs = _rows(v, "v")
     _need(slots, torch.int64, "slots")
-    if tuple(slots.shape) != (k.shape[:1] if k.ndim == 3 else (B, N)):
+    if slots.shape != (k.shape[:1] if k.ndim == 3 else (B, N)):
         raise ValueError("slots must be [B, N] ([total] for packed keys)")
     with _on(_one_device(k, v, k_pages, v_pages, slots, k_descale, v_descale)):
-        rc = load().attn_cache_write(_ptr(k), _ptr(v), ks, vs, _ptr(k_pages), _ptr(v_pages),
-                                     _ptr(k_descale), _ptr(v_descale), _ptr(slots), B, N, Hkv, d,
+        rc = load().attn_cache_write(_at(k), _at(v), ks, vs, _at(k_pages), _at(v_pages),
+                                     _at(k_descale), _at(v_descale), _at(slots), B, N, Hkv, d,
                                      num_blocks, page_size, kind, _stream_ptr(stream))
     _check(rc, "attn_cache_write")
+
+
+def _read_call(k_pages, v_pages, block_table, cu_seqlens, k_out, v_out, k_descale, v_descale,
+               cache, stream):
+    """attn_cache_read once the cache and the outputs are known to be good."""
+    import torch
+    num_blocks, page_size, Hkv, d, kind = cache
+    _need(block_table, torch.int32, "block_table")
+    _need(cu_seqlens, torch.int32, "cu_seqlens")
+    if block_table.ndim != 2 or cu_seqlens.shape != (block_table.shape[0] + 1,):
+        raise ValueError("block_table must be [B, max_blocks] and cu_seqlens [B + 1]")
+    B, max_blocks = block_table.shape
+    odt = ATTN_OUT_F32 if k_out.dtype == torch.float32 else ATTN_OUT_BF16
+    with _on(_one_device(k_pages, v_pages, block_table, cu_seqlens, k_out, v_out, k_descale, v_descale)):
+        rc = load().attn_cache_read(k_pages.data_ptr(), v_pages.data_ptr(), _at(k_descale),
+                                    _at(v_descale), block_table.data_ptr(), cu_seqlens.data_ptr(),
+                                    k_out.data_ptr(), v_out.data_ptr(), B, Hkv, k_out.shape[0],
+                                    num_blocks, page_size, max_blocks, d, kind, odt,
+                                    _stream_ptr(stream))
+    _check(rc, "attn_cache_read")
+    return k_out, v_out
 
 
 def attn_cache_read(k_pages, v_pages, block_table, cu_seqlens, k_out, v_out, k_descale=None,
@@ -983,25 +1069,14 @@ def attn_cache_read(k_pages, v_pages, block_table, cu_seqlens, k_out, v_out, k_d
     cu_seqlens int32 [B+1], both on the device.  Rows outside every sequence
     stay as they were.  Asynchronous."""
     import torch
-    num_blocks, page_size, Hkv, d, kind = _check_pages(k_pages, v_pages, k_descale, v_descale)
-    _need(block_table, torch.int32, "block_table")
-    _need(cu_seqlens, torch.int32, "cu_seqlens")
+    cache = _check_pages(k_pages, v_pages, k_descale, v_descale)
     _tensor(k_out, (torch.bfloat16, torch.float32), "k_out")
     _need(k_out, k_out.dtype, "k_out")
     _need(v_out, k_out.dtype, "v_out")
-    if block_table.ndim != 2 or tuple(cu_seqlens.shape) != (block_table.shape[0] + 1,):
-        raise ValueError("block_table must be [B, max_blocks] and cu_seqlens [B + 1]")
-    B, max_blocks = block_table.shape
-    if k_out.ndim != 3 or tuple(k_out.shape[1:]) != (Hkv, d) or v_out.shape != k_out.shape:
+    if k_out.ndim != 3 or k_out.shape[1:] != cache[2:4] or v_out.shape != k_out.shape:
         raise ValueError("k_out and v_out must both be [total, Hkv, d]")
-    odt = ATTN_OUT_F32 if k_out.dtype == torch.float32 else ATTN_OUT_BF16
-    with _on(_one_device(k_pages, v_pages, block_table, cu_seqlens, k_out, v_out, k_descale, v_descale)):
-        rc = load().attn_cache_read(_ptr(k_pages), _ptr(v_pages), _ptr(k_descale), _ptr(v_descale),
-                                    _ptr(block_table), _ptr(cu_seqlens), _ptr(k_out), _ptr(v_out),
-                                    B, Hkv, k_out.shape[0], num_blocks, page_size, max_blocks, d,
-                                    kind, odt, _stream_ptr(stream))
-    _check(rc, "attn_cache_read")
-    return k_out, v_out
+    return _read_call(k_pages, v_pages, block_table, cu_seqlens, k_out, v_out, k_descale, v_descale,
+                      cache, stream)
 
 
 def cache_read(k_pages, v_pages, block_table, cu_seqlens, total: int, k_descale=None,
@@ -1009,13 +1084,17 @@ def cache_read(k_pages, v_pages, block_table, cu_seqlens, total: int, k_descale=
     """Allocate k and v [total,Hkv,d] with torch and run attn_cache_read (total
     = cu_seqlens[-1], known to the host)."""
     import torch
+    cache = _check_pages(k_pages, v_pages, k_descale, v_descale)
     out_dtype = out_dtype or torch.bfloat16
-    shape = (int(total),) + tuple(k_pages.shape[2:])
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be bfloat16 or float32")
+    shape = (total, cache[2], cache[3])
     k = torch.empty(shape, dtype=out_dtype, device=k_pages.device)
     v = torch.empty(shape, dtype=out_dtype, device=k_pages.device)
-    _used_on(stream, k, v)
-    return attn_cache_read(k_pages, v_pages, block_table, cu_seqlens, k, v, k_descale, v_descale,
-                           stream=stream)
+    if stream is not None:
+        _used_on(stream, k, v)
+    return _read_call(k_pages, v_pages, block_table, cu_seqlens, k, v, k_descale, v_descale, cache,
+                      stream)
 
 
 def tree_mask_words(mask):
@@ -1037,6 +1116,52 @@ def attn_decode_tree_workspace_size(B: int, Hq: int, Hkv: int, T: int, max_block
                                                       int(bool(e4m3))))
 
 
+def _tree_call(q, k_pages, v_pages, block_table, seqlens, o, lse, tree_mask, q_lens, k_descale,
+               v_descale, scale, workspace, stream):
+    """attn_decode_tree once o and lse are known to be good."""
+    import torch
+    _need(q, torch.bfloat16, "q")
+    num_blocks, page_size, Hkv, d, kind = _check_pages(k_pages, v_pages, k_descale, v_descale)
+    _need(block_table, torch.int32, "block_table")
+    _need(seqlens, torch.int32, "seqlens")
+    if q.ndim != 4 or q.shape[3] != d:
+        raise ValueError("q / page shapes mismatch")
+    B, Hq, T, _ = q.shape
+    if block_table.ndim != 2 or block_table.shape[0] != B or seqlens.shape != (B,):
+        raise ValueError("block_table must be [B, max_blocks] and seqlens [B]")
+    if tree_mask is not None:
+        _need(tree_mask, torch.int64, "tree_mask")
+        if tree_mask.shape != (B, T, (T + 63) // 64):
+            raise ValueError("tree_mask must be [B, T, ceil(T / 64)]")
+    if q_lens is not None:
+        _need(q_lens, torch.int32, "q_lens")
+        if q_lens.shape != (B,):
+            raise ValueError("q_lens must be [B]")
+    if scale is None:
+        scale = d ** -0.5
+    max_blocks = block_table.shape[1]
+    odt = ATTN_OUT_F32 if o.dtype == torch.float32 else ATTN_OUT_BF16
+    dev = _one_device(q, k_pages, v_pages, block_table, seqlens, o, lse, tree_mask, q_lens,
+                      k_descale, v_descale, workspace)
+    lib = load()
+    with _on(dev):
+        if workspace is None:
+            need = lib.attn_decode_tree_workspace_size(B, Hq, Hkv, T, max_blocks, page_size, d, kind)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            if stream is not None:
+                _used_on(stream, workspace)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        rc = lib.attn_decode_tree(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                  _at(k_descale), _at(v_descale), block_table.data_ptr(),
+                                  seqlens.data_ptr(), _at(q_lens), _at(tree_mask), o.data_ptr(),
+                                  _at(lse), B, Hq, Hkv, T, num_blocks, page_size, max_blocks, d,
+                                  scale, kind, workspace.data_ptr(), workspace.nbytes, odt,
+                                  _stream_ptr(stream))
+    _check(rc, "attn_decode_tree")
+    return o, lse
+
+
 def attn_decode_tree(q, k_pages, v_pages, block_table, seqlens, o, lse=None, tree_mask=None,
                      q_lens=None, k_descale=None, v_descale=None, *, scale: float | None = None,
                      workspace=None, stream=None):
@@ -1051,50 +1176,16 @@ def attn_decode_tree(q, k_pages, v_pages, block_table, seqlens, o, lse=None, tre
     attn_decode_tree_workspace_size(...) bytes, or None (then one is allocated
     with torch).  T = 1 is plain decode.  Asynchronous."""
     import torch
-    _need(q, torch.bfloat16, "q")
-    num_blocks, page_size, Hkv, d, kind = _check_pages(k_pages, v_pages, k_descale, v_descale)
-    _need(block_table, torch.int32, "block_table")
-    _need(seqlens, torch.int32, "seqlens")
     _tensor(o, (torch.bfloat16, torch.float32), "o")
     _need(o, o.dtype, "o")
-    if q.ndim != 4 or q.shape[3] != d:
-        raise ValueError("q / page shapes mismatch")
-    B, Hq, T, _ = q.shape
-    if block_table.ndim != 2 or block_table.shape[0] != B or tuple(seqlens.shape) != (B,):
-        raise ValueError("block_table must be [B, max_blocks] and seqlens [B]")
     if o.shape != q.shape:
         raise ValueError("o shape mismatch")
     if lse is not None:
         _need(lse, torch.float32, "lse")
-        if tuple(lse.shape) != (B, Hq, T):
+        if lse.shape != q.shape[:3]:
             raise ValueError("lse shape mismatch")
-    if tree_mask is not None:
-        _need(tree_mask, torch.int64, "tree_mask")
-        if tuple(tree_mask.shape) != (B, T, (T + 63) // 64):
-            raise ValueError("tree_mask must be [B, T, ceil(T / 64)]")
-    if q_lens is not None:
-        _need(q_lens, torch.int32, "q_lens")
-        if tuple(q_lens.shape) != (B,):
-            raise ValueError("q_lens must be [B]")
-    if scale is None:
-        scale = d ** -0.5
-    max_blocks = block_table.shape[1]
-    odt = ATTN_OUT_F32 if o.dtype == torch.float32 else ATTN_OUT_BF16
-    dev = _one_device(q, k_pages, v_pages, block_table, seqlens, o, lse, tree_mask, q_lens,
-                      k_descale, v_descale, workspace)
-    with _on(dev):
-        if workspace is None:
-            need = load().attn_decode_tree_workspace_size(B, Hq, Hkv, T, max_blocks, page_size, d, kind)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            _used_on(stream, workspace)
-        ws_ptr, ws_bytes = _workspace(workspace)
-        rc = load().attn_decode_tree(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_descale),
-                                     _ptr(v_descale), _ptr(block_table), _ptr(seqlens),
-                                     _ptr(q_lens), _ptr(tree_mask), _ptr(o), _ptr(lse), B, Hq, Hkv,
-                                     T, num_blocks, page_size, max_blocks, d, float(scale), kind,
-                                     ws_ptr, ws_bytes, odt, _stream_ptr(stream))
-    _check(rc, "attn_decode_tree")
-    return o, lse
+    return _tree_call(q, k_pages, v_pages, block_table, seqlens, o, lse, tree_mask, q_lens, k_descale,
+                      v_descale, scale, workspace, stream)
 
 
 def decode_tree(q, k_pages, v_pages, block_table, seqlens, tree_mask=None, q_lens=None,
@@ -1103,8 +1194,11 @@ def decode_tree(q, k_pages, v_pages, block_table, seqlens, tree_mask=None, q_len
     """Allocate O (and LSE) with torch and run attn_decode_tree."""
     import torch
     out_dtype = out_dtype or torch.bfloat16
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be bfloat16 or float32")
     o = torch.empty(q.shape, dtype=out_dtype, device=q.device)
     lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
-    _used_on(stream, o, lse)
-    return attn_decode_tree(q, k_pages, v_pages, block_table, seqlens, o, lse, tree_mask, q_lens,
-                            k_descale, v_descale, scale=scale, stream=stream)
+    if stream is not None:
+        _used_on(stream, o, lse)
+    return _tree_call(q, k_pages, v_pages, block_table, seqlens, o, lse, tree_mask, q_lens, k_descale,
+                      v_descale, scale, None, stream)
