@@ -8,12 +8,19 @@
 // E4M3 rows stand for code * descale: s_j = scale * kd_j (q . kc_j) and
 // O = sum_j p_j vd_j vc_j / sum_j p_j, the codes exact in fp16.
 //
-// This file: the kernel for 16 query rows at a time on mma.sync (m16n8k16;
-// more rows of head dims up to 128 go to attn_tree_tc_sm103.cu), and the merge of cut items (tree_plan.h has the work list).  A producer warp
+// This file: the kernel for up to 16 query rows at a time on mma.sync
+// (m16n8k16; more rows of head dims up to 128 go to attn_tree_tc_sm103.cu), and
+// the merge of cut items (tree_plan.h has the work list).  A producer warp
 // streams 64-key tiles of K and V (and their descales) by TMA into a ring; each
 // of four consumer warps takes 16 keys of every tile with its own online
 // softmax (base 2), and the four are merged through shared memory at the end of
 // a piece.  Bound: HBM (each cached byte is read once per row tile).
+//
+// The products are transposed, S^T = K Q^T and O^T = V^T P^T: keys and columns
+// are the 16 rows of an MMA and the query rows its 8 columns, so up to 8 query
+// rows (a single token's heads) cost half the MMAs and registers that a 16-row
+// query operand would, which leaves room for three CTAs on an SM.  P^T becomes
+// the second product's operand by an 8x8 transposition across the warp.
 //
 // E4M3 fragments: a lane takes 16 consecutive code bytes of a key with one
 // shared load and spreads them over four k-steps (Q is laid out to match), so
@@ -29,6 +36,7 @@
 // that do not see it) and added to the rows that do see it by itself.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "tree_plan.h"
 
@@ -38,30 +46,37 @@ namespace {
 constexpr int kConsumers = 4;
 constexpr int kTreeThreads = (kConsumers + 1) * 32;
 constexpr int kTileKeys = 64;
-constexpr int kRows = 16;
+constexpr int kMaxRows = 16;
 constexpr float kLn2t = 0.69314718055994530942f;
 constexpr float kLog2et = 1.44269504088896340736f;
 constexpr float kPFrame = 32768.0f;  // E4M3: P is held times 2^15 / F
 
-template <int D, bool F8>
+// D columns, NT tiles of 8 query rows.
+template <int D, bool F8, int NT>
 struct TreeCfg {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kCtas = D == 256 ? (F8 && NT == 1 ? 2 : 1) : (NT == 1 ? 3 : 2);  // per SM
     // bytes of a 64-key K (or V) tile: 128-byte-wide swizzled boxes
     static constexpr int kBoxes = F8 ? D / 128 : D / 64;
     static constexpr int kHalf = kBoxes * kTileKeys * 128;
     static constexpr int kDescale = F8 ? 2 * kTileKeys * 4 : 0;  // kd, vd of a tile
     static constexpr int kStage = 2 * kHalf + (F8 ? 1024 : 0);   // (tiles stay 1024-byte aligned)
-    static constexpr int kStages = D <= 128 ? (F8 ? 5 : 3) : (F8 ? 5 : 3);
-    static constexpr int kScratch = kStages * kStage;            // O of two warps
-    static constexpr int kScratchBytes = 2 * kRows * D * 4;
+    static constexpr int kScratchBytes = 2 * kRows * D * 4;      // O of two warps
+    // 228 KiB to an SM, 1 KiB of it the system's for each CTA
+    static constexpr int kBudget = (228 / kCtas - 1) * 1024;
+    static constexpr int kFit = (kBudget - kScratchBytes - 1024) / kStage;
+    static constexpr int kStages = kFit < 6 ? kFit : 6;
+    static_assert(kStages >= 2, "ring");
+    static constexpr int kScratch = kStages * kStage;
     static constexpr int kBar = kScratch + kScratchBytes;
     static constexpr int kSmem = kBar + 1024;
 };
 
 struct TreeBars {
-    uint64_t full[5], empty[5];
+    uint64_t full[6], empty[6];
     TreeRange range;
     int abort;
-    float m[kConsumers][kRows], l[kConsumers][kRows], x[kConsumers][kRows], f[kConsumers];
+    float m[kConsumers][kMaxRows], l[kConsumers][kMaxRows], x[kConsumers][kMaxRows], f[kConsumers];
 };
 static_assert(sizeof(TreeBars) <= 1024, "barrier block");
 
@@ -130,6 +145,12 @@ __device__ __forceinline__ float e4m3_f32(uint32_t code) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(f) : "r"(r));
     return f;
 }
+// 8x8 transposition of 16-bit elements across the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
 // Power of two 2^e (e in [-126, 127]).
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
@@ -156,10 +177,13 @@ __device__ __forceinline__ bool not_finite(uint4 v) {
     return hit;
 }
 
-template <int D, bool F8>
+// The producer warp: lane 0 runs the ring, and each of the first lanes copies
+// the tile's box of its own number (with its page looked up one tile ahead).
+template <int D, bool F8, int NT>
 __device__ __forceinline__ void produce(const CUtensorMap* tk, const CUtensorMap* tv, uint8_t* smem,
                                         TreeBars* bars, const TreeParams& p) {
-    using C = TreeCfg<D, F8>;
+    using C = TreeCfg<D, F8, NT>;
+    const int lane = threadIdx.x & 31;
     const volatile int* abort_flag = &bars->abort;
     TreeWalk walk;
     walk.start(bars->range);
@@ -168,37 +192,42 @@ __device__ __forceinline__ void produce(const CUtensorMap* tk, const CUtensorMap
     bool ok = true;
     const int boxes = kTileKeys / p.box_keys;
     while (ok && walk.next(p, w)) {
+        int off = 0, page = lane < boxes ? tree_page(p, w.b, w.k0 * kTileKeys + lane * p.box_keys, w.keys, off) : -1;
         for (int kt = w.k0; kt < w.k1; ++kt, ++issued) {
             const int slot = (int)(issued % C::kStages);
             const long long round = issued / C::kStages;
+            const int my_page = page, my_off = off;
+            if (kt + 1 < w.k1 && lane < boxes)
+                page = tree_page(p, w.b, (kt + 1) * kTileKeys + lane * p.box_keys, w.keys, off);
             if (round > 0) {
-                ok = mbar_wait(smem_u32(&bars->empty[slot]), (uint32_t)((round - 1) & 1), abort_flag);
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->empty[slot]), (uint32_t)((round - 1) & 1),
+                                                       abort_flag));
                 if (!ok) break;
             }
             const uint32_t bar = smem_u32(&bars->full[slot]);
-            mbar_arrive_expect_tx(bar, 2 * C::kHalf + C::kDescale);
-            const uint32_t dk = smem_u32(smem + slot * C::kStage);
-            const uint32_t dv = dk + C::kHalf;
-            for (int x = 0; x < boxes; ++x) {
-                int off;
-                const int page = tree_page(p, w.b, kt * kTileKeys + x * p.box_keys, w.keys, off);
+            if (lane == 0) mbar_arrive_expect_tx(bar, 2 * C::kHalf + C::kDescale);
+            __syncwarp();
+            if (lane < boxes) {
+                const uint32_t dk = smem_u32(smem + slot * C::kStage);
+                const uint32_t dv = dk + C::kHalf;
 #pragma unroll
                 for (int c = 0; c < C::kBoxes; ++c) {
-                    const uint32_t to = c * (kTileKeys * 128) + x * p.box_keys * 128;
-                    tma_load_4d(dk + to, tk, bar, (F8 ? 128 : 64) * c, w.h, off, page);
-                    tma_load_4d(dv + to, tv, bar, (F8 ? 128 : 64) * c, w.h, off, page);
+                    const uint32_t to = c * (kTileKeys * 128) + lane * p.box_keys * 128;
+                    tma_load_4d(dk + to, tk, bar, (F8 ? 128 : 64) * c, w.h, my_off, my_page);
+                    tma_load_4d(dv + to, tv, bar, (F8 ? 128 : 64) * c, w.h, my_off, my_page);
                 }
                 if constexpr (F8) {
                     // a missing page's codes are zeros: any descale that exists will do
-                    const long long at = ((long long)(page < 0 ? 0 : page) * p.Hkv + w.h) * p.page_size + off;
-                    const uint32_t ds = dk + 2 * C::kHalf + x * p.box_keys * 4;
+                    const long long at = ((long long)(my_page < 0 ? 0 : my_page) * p.Hkv + w.h) * p.page_size + my_off;
+                    const uint32_t ds = dk + 2 * C::kHalf + lane * p.box_keys * 4;
                     bulk_load(ds, p.k_descale + at, p.box_keys * 4, bar);
                     bulk_load(ds + kTileKeys * 4, p.v_descale + at, p.box_keys * 4, bar);
                 }
             }
+            __syncwarp();
         }
     }
-    if (!ok) {
+    if (!ok && lane == 0) {
         atomicOr(p.err, kErrTimeout);
         *((volatile int*)&bars->abort) = 1;
     }
@@ -209,11 +238,11 @@ __device__ __forceinline__ void produce(const CUtensorMap* tk, const CUtensorMap
     }
 }
 
-template <int D, bool F8>
-__global__ void __launch_bounds__(kTreeThreads, D <= 128 ? 2 : 1)
+template <int D, bool F8, int NT>
+__global__ void __launch_bounds__(kTreeThreads, TreeCfg<D, F8, NT>::kCtas)
 attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const __grid_constant__ TreeParams p) {
-    using C = TreeCfg<D, F8>;
+    using C = TreeCfg<D, F8, NT>;
     extern __shared__ __align__(1024) uint8_t smem[];
     TreeBars* bars = reinterpret_cast<TreeBars*>(smem + C::kBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -235,7 +264,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     }
     __syncthreads();
     if (warp == kConsumers) {
-        if (lane == 0) produce<D, F8>(&tk, &tv, smem, bars, p);
+        produce<D, F8, NT>(&tk, &tv, smem, bars, p);
         return;
     }
 
@@ -243,10 +272,13 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     const int qr = lane >> 2, qc = lane & 3;
     const int mi = lane >> 3, ri = lane & 7;
     const int wk0 = warp * 16;
-    // key (of this warp's 16) and column of an accumulator element
-    auto key_of = [&](int nt, int e) { return F8 ? nt * 8 + qc + 4 * (e & 1) : nt * 8 + 2 * qc + (e & 1); };
-    auto col_of = [&](int i, int e) {
-        return F8 ? (i >> 4) * 128 + 64 * (e & 1) + 16 * qc + (i & 15) : i * 8 + 2 * qc + (e & 1);
+    // this lane's two keys of the warp's 16 are k_lane and k_lane + 8 (E4M3: an
+    // order that keeps a quarter-warp's 16-byte loads on different banks)
+    const int k_lane = F8 ? (qr >> 1) + 4 * (qr & 1) : qr;
+    const int v_chunk = (qr >> 1) + 4 * (qr & 1);  // E4M3: 16-byte chunk of a V row's 128 columns
+    // column of an accumulator element: MMA row qr + 8 hi of tile mt
+    auto col_of = [&](int mt, int hi) {
+        return F8 ? (mt >> 3) * 128 + 16 * v_chunk + 2 * (mt & 7) + hi : mt * 16 + qr + 8 * hi;
     };
     float* so = reinterpret_cast<float*>(smem + C::kScratch);
     TreeWalk walk;
@@ -255,41 +287,38 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     long long used = 0;
     bool ok = true, first_piece = true;
     while (ok && walk.next(p, w)) {
-        const int rows = min(kRows, w.drafted * p.G - w.rt * kRows);  // >= 1
+        const int rows = min(C::kRows, w.drafted * p.G - w.rt * C::kRows);  // >= 1
         const int prefix = w.keys - w.drafted;
-        int tok[2];
-        const __nv_bfloat16* qrow[2];
+        // ---- Q operand: lane (qr, qc) holds columns of row qr + 8 nt (rows past
+        // the last repeat it; never written)
+        uint32_t qb[NT][D / 16][2];
+        float qs[NT][2];  // what a product is multiplied with, rows 8 nt + 2 qc + {0, 1}
+        int tok[NT][2];   // drafted token of those rows
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = w.rt * kRows + min(qr + 8 * r, rows - 1);
-            tok[r] = row / p.G;
-            qrow[r] = p.q + (((size_t)w.b * p.Hq + (size_t)w.h * p.G + (row - tok[r] * p.G)) * p.T + tok[r]) * p.dh;
-        }
-        // ---- Q fragments (rows past the last repeat it; never written)
-        uint32_t qa[D / 16][4];
-        float qs[2] = {p.c, p.c};  // what a product is multiplied with
-        if constexpr (!F8) {
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = w.rt * C::kRows + min(qr + 8 * nt, rows - 1);
+            const int t = row / p.G;
+            const __nv_bfloat16* q =
+                p.q + (((size_t)w.b * p.Hq + (size_t)w.h * p.G + (row - t * p.G)) * p.T + t) * p.dh;
+            float scale = p.c;
+            if constexpr (!F8) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
+                for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
+                    for (int hf = 0; hf < 2; ++hf) {
                         const int c0 = ks * 16 + 2 * qc + 8 * hf;
-                        qa[ks][r + 2 * hf] = c0 < p.dh ? *reinterpret_cast<const uint32_t*>(qrow[r] + c0) : 0u;
+                        qb[nt][ks][hf] = c0 < p.dh ? *reinterpret_cast<const uint32_t*>(q + c0) : 0u;
                     }
-        } else {
-            // fp16, each row scaled by a power of two that puts its largest value
-            // in [2^14, 2^15): exact but for values below 2^-38 of it
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
+            } else {
+                // fp16, each row scaled by a power of two that puts its largest value
+                // in [2^14, 2^15): exact but for values below 2^-38 of it
                 float mx = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const int c0 = (ks >> 2) * 64 + 16 * qc + 4 * (ks & 3);
-                    const uint2 v = c0 < p.dh ? *reinterpret_cast<const uint2*>(qrow[r] + c0) : make_uint2(0u, 0u);
-                    qa[ks][r] = v.x;
-                    qa[ks][r + 2] = v.y;
+                    const uint2 v = c0 < p.dh ? *reinterpret_cast<const uint2*>(q + c0) : make_uint2(0u, 0u);
+                    qb[nt][ks][0] = v.x;
+                    qb[nt][ks][1] = v.y;
                     mx = fmaxf(mx, fmaxf(fmaxf(fabsf(bf16lo_to_f32(v.x)), fabsf(bf16hi_to_f32(v.x))),
                                          fmaxf(fabsf(bf16lo_to_f32(v.y)), fabsf(bf16hi_to_f32(v.y)))));
                 }
@@ -298,88 +327,123 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 int e = (int)(__float_as_uint(mx) >> 23) - 127;
                 e = e < -100 ? -100 : (e > 126 ? 126 : e);
                 const float up = pow2i(14 - e);
-                qs[r] = p.c * pow2i(e - 14);
+                scale *= pow2i(e - 14);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    qa[ks][r] = pack_f16x2(bf16lo_to_f32(qa[ks][r]) * up, bf16hi_to_f32(qa[ks][r]) * up);
-                    qa[ks][r + 2] = pack_f16x2(bf16lo_to_f32(qa[ks][r + 2]) * up, bf16hi_to_f32(qa[ks][r + 2]) * up);
-                }
+                for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+                        qb[nt][ks][hf] =
+                            pack_f16x2(bf16lo_to_f32(qb[nt][ks][hf]) * up, bf16hi_to_f32(qb[nt][ks][hf]) * up);
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                qs[nt][r] = __shfl_sync(0xFFFFFFFFu, scale, 4 * (2 * qc + r));
+                tok[nt][r] = __shfl_sync(0xFFFFFFFFu, t, 4 * (2 * qc + r));
             }
         }
-        float acc[D / 8][4];
+        float acc[D / 16][NT][4];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY};
-        float l[2] = {0.f, 0.f};  // this lane's part of the sum that normalises O
-        float xs[2] = {0.f, 0.f};  // ... of the unrounded P (the LSE's)
-        int fexp = -126;           // E4M3: F = 2^fexp
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) acc[i][nt][0] = acc[i][nt][1] = acc[i][nt][2] = acc[i][nt][3] = 0.f;
+        float m[NT][2], l[NT][2], xs[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                m[nt][r] = -INFINITY;
+                l[nt][r] = 0.f;   // this lane's part of the sum that normalises O
+                xs[nt][r] = 0.f;  // ... of the unrounded P (the LSE's)
+            }
+        int fexp = -126;  // E4M3: F = 2^fexp
 
         for (int kt = w.k0; kt < w.k1; ++kt, ++used) {
             const int slot = (int)(used % C::kStages);
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->full[slot]),
                                                    (uint32_t)((used / C::kStages) & 1), abort_flag));
             if (!ok) break;
-            const int key0 = kt * kTileKeys + wk0;          // this warp's first key
+            const int key0 = kt * kTileKeys + wk0;  // this warp's first key
             const int nvalid = min(16, w.keys - key0);
             const uint32_t sK = smem_u32(smem + slot * C::kStage);
             const uint32_t sV = sK + C::kHalf;
             bool wrote = false;
             if (nvalid > 0) {
-                // ---- S
-                float sf[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                float vd[2][2];  // E4M3: V's descale of this lane's keys
-                if constexpr (!F8) {
+                // ---- S^T: elements 0, 1 key k_lane, 2, 3 key k_lane + 8; rows 8 nt + 2 qc + {0, 1}
+                float sf[NT][4];
+                float vd[2] = {1.f, 1.f};  // E4M3: V's descale of this lane's keys
+                {
+                    float s2[NT][4];  // (two chains of products)
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        uint32_t b0, b1, b2, b3;
-                        ldsm4(sK + tile_off(wk0 + (mi >> 1) * 8 + ri, ks * 2 + (mi & 1)), b0, b1, b2, b3);
-                        mma16816<false>(sf[0], qa[ks], b0, b1);
-                        mma16816<false>(sf[1], qa[ks], b2, b3);
-                    }
-                } else {
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const int key = wk0 + nt * 8 + (qr >> 1) + 4 * (qr & 1);
+                        for (int e = 0; e < 4; ++e) sf[nt][e] = s2[nt][e] = 0.f;
+                    if constexpr (!F8) {
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            uint32_t a[4];
+                            ldsm4(sK + tile_off(wk0 + (mi & 1) * 8 + ri, ks * 2 + (mi >> 1)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<false>(ks & 1 ? s2[nt] : sf[nt], a, qb[nt][ks][0], qb[nt][ks][1]);
+                        }
+                    } else {
 #pragma unroll
                         for (int blk = 0; blk < D / 64; ++blk) {
-                            const uint4 kb = lds128(sK + tile_off(key, blk * 4 + qc));
-                            mma16816<true>(sf[nt], qa[4 * blk], e4m3_lo(kb.x), e4m3_hi(kb.x));
-                            mma16816<true>(sf[nt], qa[4 * blk + 1], e4m3_lo(kb.y), e4m3_hi(kb.y));
-                            mma16816<true>(sf[nt], qa[4 * blk + 2], e4m3_lo(kb.z), e4m3_hi(kb.z));
-                            mma16816<true>(sf[nt], qa[4 * blk + 3], e4m3_lo(kb.w), e4m3_hi(kb.w));
+                            const uint4 x = lds128(sK + tile_off(wk0 + k_lane, blk * 4 + qc));
+                            const uint4 y = lds128(sK + tile_off(wk0 + k_lane + 8, blk * 4 + qc));
+                            const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t a[4] = {e4m3_lo(xw[k]), e4m3_lo(yw[k]), e4m3_hi(xw[k]), e4m3_hi(yw[k])};
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma16816<true>(k & 1 ? s2[nt] : sf[nt], a, qb[nt][4 * blk + k][0],
+                                                   qb[nt][4 * blk + k][1]);
+                            }
                         }
                     }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sf[nt][e] += s2[nt][e];
                 }
                 // ---- scale, mask, running maximum
                 const bool drafted = key0 + nvalid > prefix;  // some of the keys are drafted tokens
-                float mx[2] = {-INFINITY, -INFINITY};
+                float kd[2] = {1.f, 1.f};
+                if constexpr (F8) {
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                    for (int g = 0; g < 2; ++g) {
+                        const uint32_t at = sK + 2 * C::kHalf + (wk0 + k_lane + 8 * g) * 4;
+                        kd[g] = lds32f(at);
+                        vd[g] = k_lane + 8 * g < nvalid ? lds32f(at + kTileKeys * 4) : 0.f;
+                    }
+                }
+                float al[NT][2], ms[NT][2];
+                bool moved = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int kk = key_of(nt, e);
-                        float f = qs[e >> 1];
-                        if constexpr (F8) {
-                            const uint32_t at = sK + 2 * C::kHalf + (wk0 + kk) * 4;
-                            f *= lds32f(at);
-                            if (e < 2) vd[nt][e] = kk < nvalid ? lds32f(at + kTileKeys * 4) : 0.f;
-                        }
-                        float v = kk < nvalid ? sf[nt][e] * f : -INFINITY;
+                        const int kk = k_lane + 8 * (e >> 1);
+                        float v = sf[nt][e] * (F8 ? qs[nt][e & 1] * kd[e >> 1] : qs[nt][e & 1]);
+                        if (kk >= nvalid) v = -INFINITY;
                         if (drafted && kk < nvalid && key0 + kk >= prefix &&
-                            !tree_sees(p, w.b, tok[e >> 1], key0 + kk - prefix))
+                            !tree_sees(p, w.b, tok[nt][e & 1], key0 + kk - prefix))
                             v = -INFINITY;
                         sf[nt][e] = v;
-                        mx[e >> 1] = fmaxf(mx[e >> 1], v);
+                        mx[e & 1] = fmaxf(mx[e & 1], v);
                     }
-                float al[2], ms[2];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], 1));
-                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], 2));
-                    const float mn = fmaxf(m[r], mx[r]);
-                    ms[r] = mn == -INFINITY ? 0.f : mn;  // (no key yet: every P is 0)
-                    al[r] = ex2(m[r] - ms[r]);
-                    m[r] = mn;
+                    for (int r = 0; r < 2; ++r) {
+                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], 4));
+                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], 8));
+                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], 16));
+                        const float mn = fmaxf(m[nt][r], mx[r]);
+                        ms[nt][r] = mn == -INFINITY ? 0.f : mn;  // (no key yet: every P is 0)
+                        al[nt][r] = ex2(m[nt][r] - ms[nt][r]);
+                        m[nt][r] = mn;
+                    }
                 }
                 // ---- V rows that must not enter the product
                 unsigned bad = 0u;  // of the 16 keys: drafted rows with a NaN or an infinity
@@ -398,91 +462,91 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     bad = __reduce_or_sync(0xFFFFFFFFu, bad);
                 }
                 // ---- P
-                float add[2] = {0.f, 0.f}, addx[2] = {0.f, 0.f};
-                uint32_t pa[4];
                 float grow = 1.f;  // E4M3: F_old / F_new
-                float wv[2][2];
+                float wv[2] = {1.f, 1.f};
                 if constexpr (F8) {
                     float top = 0.f;
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            if (bad >> key_of(nt, e) & 1u) wv[nt][e] = 0.f;
-                            else wv[nt][e] = vd[nt][e];
-                            top = fmaxf(top, fabsf(wv[nt][e]));
-                        }
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                    // 2^need > top (all rows of the quad's keys: the same in every lane)
+                    for (int g = 0; g < 2; ++g) {
+                        wv[g] = bad >> (k_lane + 8 * g) & 1u ? 0.f : vd[g];
+                        top = fmaxf(top, fabsf(wv[g]));
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+                    // 2^need > top (the same in every lane)
                     const int need = max(min((int)(__float_as_uint(top) >> 23) - 126, 111), -100);
                     if (need > fexp) {
-                        grow = fexp <= -126 ? 0.f : (fexp - need < -126 ? 0.f : pow2i(fexp - need));
+                        grow = fexp - need < -126 ? 0.f : pow2i(fexp - need);
                         fexp = need;
                     }
                     const float fr = kPFrame * pow2i(-fexp);
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) wv[nt][e] *= fr;
+                    wv[0] *= fr;
+                    wv[1] *= fr;
                 }
+                uint32_t pb[NT][2];
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    float pr[4];
+                for (int nt = 0; nt < NT; ++nt) {
+                    float pr[4], add[2] = {0.f, 0.f}, addx[2] = {0.f, 0.f};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        pr[e] = ex2(sf[nt][e] - ms[e >> 1]);
-                        addx[e >> 1] += pr[e];
+                        pr[e] = ex2(sf[nt][e] - ms[nt][e & 1]);
+                        addx[e & 1] += pr[e];
                     }
-                    if constexpr (F8) {
-                        pa[2 * nt] = pack_f16x2(pr[0] * wv[nt][0], pr[1] * wv[nt][1]);
-                        pa[2 * nt + 1] = pack_f16x2(pr[2] * wv[nt][0], pr[3] * wv[nt][1]);
-                    } else {
-                        pa[2 * nt] = pack_bf16x2(pr[0], pr[1]);
-                        pa[2 * nt + 1] = pack_bf16x2(pr[2], pr[3]);
-                        add[0] += bf16lo_to_f32(pa[2 * nt]) + bf16hi_to_f32(pa[2 * nt]);
-                        add[1] += bf16lo_to_f32(pa[2 * nt + 1]) + bf16hi_to_f32(pa[2 * nt + 1]);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if constexpr (F8) {
+                            pb[nt][g] = pack_f16x2(pr[2 * g] * wv[g], pr[2 * g + 1] * wv[g]);
+                        } else {
+                            pb[nt][g] = pack_bf16x2(pr[2 * g], pr[2 * g + 1]);
+                            add[0] += bf16lo_to_f32(pb[nt][g]);
+                            add[1] += bf16hi_to_f32(pb[nt][g]);
+                        }
+                        pb[nt][g] = transpose8x8(pb[nt][g]);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        xs[nt][r] = xs[nt][r] * al[nt][r] + addx[r];
+                        l[nt][r] = l[nt][r] * al[nt][r] + (F8 ? addx[r] : add[r]);
+                        al[nt][r] *= grow;
+                        moved |= al[nt][r] != 1.f;
                     }
                 }
+                if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    xs[r] = xs[r] * al[r] + addx[r];
-                    l[r] = l[r] * al[r] + (F8 ? addx[r] : add[r]);
-                }
-                const float o0 = al[0] * grow, o1 = al[1] * grow;
-                if (!__all_sync(0xFFFFFFFFu, o0 == 1.f && o1 == 1.f)) {
+                    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        acc[i][0] *= o0;
-                        acc[i][1] *= o0;
-                        acc[i][2] *= o1;
-                        acc[i][3] *= o1;
-                    }
+                        for (int nt = 0; nt < NT; ++nt) {
+                            acc[i][nt][0] *= al[nt][0];
+                            acc[i][nt][1] *= al[nt][1];
+                            acc[i][nt][2] *= al[nt][0];
+                            acc[i][nt][3] *= al[nt][1];
+                        }
                 }
                 // ---- rows past the sequence, and rows with a NaN or an infinity:
                 // the latter are added to the rows that see them, both are zeroed
                 if (bad) {
                     for (unsigned left = bad; left; left &= left - 1) {
                         const int kk = __ffs(left) - 1;
-                        const int nt = kk >> 3;
-                        // who holds its P: accumulator column of the key
-                        const int owner = F8 ? (kk & 3) : ((kk & 7) >> 1);
-                        const int el = F8 ? (kk & 7) >> 2 : kk & 1;
-                        float sv[2];
+                        const int qr_of = F8 ? 2 * (kk & 3) + ((kk >> 2) & 1) : kk & 7;  // who holds its scores
+                        float pk[NT][2];
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float mine = nt == 0 ? (el == 0 ? sf[0][2 * r] : sf[0][2 * r + 1])
-                                                       : (el == 0 ? sf[1][2 * r] : sf[1][2 * r + 1]);
-                            sv[r] = __shfl_sync(0xFFFFFFFFu, mine, (lane & ~3) | owner);
-                        }
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const float sv = __shfl_sync(0xFFFFFFFFu, kk < 8 ? sf[nt][r] : sf[nt][2 + r],
+                                                             4 * qr_of + qc);
+                                // (-1: not seen)
+                                pk[nt][r] = sv == -INFINITY ? -1.f : ex2(sv - ms[nt][r]);
+                            }
                         float fr = 1.f;
                         if constexpr (F8)
                             fr = lds32f(sK + 2 * C::kHalf + kTileKeys * 4 + (wk0 + kk) * 4) * kPFrame * pow2i(-fexp);
 #pragma unroll
-                        for (int i = 0; i < D / 8; ++i)
+                        for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int col = col_of(i, e);
+                            for (int hi = 0; hi < 2; ++hi) {
+                                const int col = col_of(i, hi);
                                 float v;
                                 if constexpr (F8) {
                                     const uint32_t at = sV + tile_off(wk0 + kk, col >> 4) + (col & 15);
@@ -495,8 +559,12 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                                     asm volatile("ld.shared.u16 %0, [%1];" : "=r"(half) : "r"(at));
                                     v = __uint_as_float(half << 16);
                                 }
-                                if (sv[0] != -INFINITY) acc[i][e] = fmaf(ex2(sv[0] - ms[0]), v, acc[i][e]);
-                                if (sv[1] != -INFINITY) acc[i][2 + e] = fmaf(ex2(sv[1] - ms[1]), v, acc[i][2 + e]);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                    for (int r = 0; r < 2; ++r)
+                                        if (pk[nt][r] != -1.f)
+                                            acc[i][nt][2 * hi + r] = fmaf(pk[nt][r], v, acc[i][nt][2 * hi + r]);
                             }
                     }
                     __syncwarp();
@@ -508,35 +576,36 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     wrote = true;
                     __syncwarp();
                 }
-                // ---- O += P V
+                // ---- O^T += V^T P^T
                 if constexpr (!F8) {
 #pragma unroll
-                    for (int pr = 0; pr < D / 16; ++pr) {
-                        uint32_t v0, v1, v2, v3;
-                        ldsm4_t(sV + tile_off(wk0 + (mi & 1) * 8 + ri, pr * 2 + (mi >> 1)), v0, v1, v2, v3);
-                        mma16816<false>(acc[2 * pr], pa, v0, v1);
-                        mma16816<false>(acc[2 * pr + 1], pa, v2, v3);
+                    for (int mt = 0; mt < D / 16; ++mt) {
+                        uint32_t a[4];
+                        ldsm4_t(sV + tile_off(wk0 + (mi >> 1) * 8 + ri, mt * 2 + (mi & 1)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816<false>(acc[mt][nt], a, pb[nt][0], pb[nt][1]);
                     }
                 } else {
-                    // P's k index 2 qc + {0, 1, 8, 9} is key qc + {0, 4, 8, 12}; B's
-                    // column qr is chunk (qr >> 1) + 4 (qr & 1) of the 128 columns
-                    const int ch = (qr >> 1) + 4 * (qr & 1);
+                    // P's k index 2 qc + {0, 1, 8, 9} is key qc + {0, 4, 8, 12}
 #pragma unroll
                     for (int hf = 0; hf < D / 128; ++hf) {
-                        const uint4 r0 = lds128(sV + tile_off(wk0 + qc, hf * 8 + ch));
-                        const uint4 r1 = lds128(sV + tile_off(wk0 + qc + 4, hf * 8 + ch));
-                        const uint4 r2 = lds128(sV + tile_off(wk0 + qc + 8, hf * 8 + ch));
-                        const uint4 r3 = lds128(sV + tile_off(wk0 + qc + 12, hf * 8 + ch));
+                        const uint4 r0 = lds128(sV + tile_off(wk0 + qc, hf * 8 + v_chunk));
+                        const uint4 r1 = lds128(sV + tile_off(wk0 + qc + 4, hf * 8 + v_chunk));
+                        const uint4 r2 = lds128(sV + tile_off(wk0 + qc + 8, hf * 8 + v_chunk));
+                        const uint4 r3 = lds128(sV + tile_off(wk0 + qc + 12, hf * 8 + v_chunk));
                         const uint32_t a0[4] = {r0.x, r0.y, r0.z, r0.w}, a1[4] = {r1.x, r1.y, r1.z, r1.w};
                         const uint32_t a2[4] = {r2.x, r2.y, r2.z, r2.w}, a3[4] = {r3.x, r3.y, r3.z, r3.w};
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
                             const uint32_t x01 = __byte_perm(a0[g], a1[g], 0x5140), y01 = __byte_perm(a0[g], a1[g], 0x7362);
                             const uint32_t x23 = __byte_perm(a2[g], a3[g], 0x5140), y23 = __byte_perm(a2[g], a3[g], 0x7362);
-                            mma16816<true>(acc[16 * hf + 4 * g], pa, e4m3_lo(x01), e4m3_lo(x23));
-                            mma16816<true>(acc[16 * hf + 4 * g + 1], pa, e4m3_hi(x01), e4m3_hi(x23));
-                            mma16816<true>(acc[16 * hf + 4 * g + 2], pa, e4m3_lo(y01), e4m3_lo(y23));
-                            mma16816<true>(acc[16 * hf + 4 * g + 3], pa, e4m3_hi(y01), e4m3_hi(y23));
+                            const uint32_t u[4] = {e4m3_lo(x01), e4m3_hi(x01), e4m3_lo(x23), e4m3_hi(x23)};
+                            const uint32_t v[4] = {e4m3_lo(y01), e4m3_hi(y01), e4m3_lo(y23), e4m3_hi(y23)};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma16816<true>(acc[8 * hf + 2 * g][nt], u, pb[nt][0], pb[nt][1]);
+                                mma16816<true>(acc[8 * hf + 2 * g + 1][nt], v, pb[nt][0], pb[nt][1]);
+                            }
                         }
                     }
                 }
@@ -549,91 +618,125 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             ok = false;
             break;
         }
-        // ---- merge the four warps: sums over the quad, then the warps' maxima
+        // ---- merge the four warps: sums over the keys' lanes, then the warps' maxima
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
-            xs[r] += __shfl_xor_sync(0xFFFFFFFFu, xs[r], 1);
-            xs[r] += __shfl_xor_sync(0xFFFFFFFFu, xs[r], 2);
-            if (qc == 0) {
-                bars->m[warp][qr + 8 * r] = m[r];
-                bars->l[warp][qr + 8 * r] = l[r];
-                bars->x[warp][qr + 8 * r] = xs[r];
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    l[nt][r] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][r], off);
+                    xs[nt][r] += __shfl_xor_sync(0xFFFFFFFFu, xs[nt][r], off);
+                }
+                if (qr == 0) {
+                    const int row = 8 * nt + 2 * qc + r;
+                    bars->m[warp][row] = m[nt][r];
+                    bars->l[warp][row] = l[nt][r];
+                    bars->x[warp][row] = xs[nt][r];
+                }
             }
-        }
         if (lane == 0) bars->f[warp] = F8 ? pow2i(max(fexp, -120)) / kPFrame : 1.f;
         tree_consumers_sync();
-        float M[2], sum[2] = {0.f, 0.f}, sumx[2] = {0.f, 0.f}, mine[2];
+        // this warp's O in the common frame and over the common sum
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = qr + 8 * r;
-            M[r] = fmaxf(fmaxf(bars->m[0][row], bars->m[1][row]), fmaxf(bars->m[2][row], bars->m[3][row]));
-            const float Ms = M[r] == -INFINITY ? 0.f : M[r];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int x = 0; x < kConsumers; ++x) {
-                const float wt = ex2(bars->m[x][row] - Ms);
-                sum[r] += wt * bars->l[x][row];
-                sumx[r] += wt * bars->x[x][row];
+            for (int r = 0; r < 2; ++r) {
+                const int row = 8 * nt + 2 * qc + r;
+                const float M = fmaxf(fmaxf(bars->m[0][row], bars->m[1][row]), fmaxf(bars->m[2][row], bars->m[3][row]));
+                const float Ms = M == -INFINITY ? 0.f : M;
+                float sum = 0.f, sumx = 0.f;
+#pragma unroll
+                for (int x = 0; x < kConsumers; ++x) {
+                    const float wt = ex2(bars->m[x][row] - Ms);
+                    sum += wt * bars->l[x][row];
+                    sumx += wt * bars->x[x][row];
+                }
+                const float mine = sum == 0.f ? 0.f : ex2(m[nt][r] - Ms) * bars->f[warp] / sum;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    acc[i][nt][r] *= mine;
+                    acc[i][nt][2 + r] *= mine;
+                }
+                if (warp == 0 && qr == 0 && row < rows) {
+                    const float lse2 = sumx == 0.f ? -INFINITY : M + log2f(sumx);
+                    if (!w.whole) {
+                        p.ws_lse[((size_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * C::kRows + row] = lse2;
+                    } else if (p.lse) {
+                        const int rr = w.rt * C::kRows + row;
+                        p.lse[((size_t)w.b * p.Hq + (size_t)w.h * p.G + (rr - tok[nt][r] * p.G)) * p.T + tok[nt][r]] =
+                            lse2 * kLn2t;
+                    }
+                }
             }
-            mine[r] = ex2(m[r] - Ms) * bars->f[warp];
-        }
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            acc[i][0] *= mine[0];
-            acc[i][1] *= mine[0];
-            acc[i][2] *= mine[1];
-            acc[i][3] *= mine[1];
-        }
         // O of warps 2, 3 to warps 0, 1, then of warp 1 to warp 0 (lane by lane)
 #pragma unroll 1
         for (int from = 2; from >= 1; from >>= 1) {
-            float* buf = so + (size_t)((warp & (from - 1)) * 32 + lane) * 2;
+            float4* buf = reinterpret_cast<float4*>(so) + (warp & (from - 1)) * (C::kRows * D / 4) + lane;
             if (warp >= from && warp < 2 * from) {
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    *reinterpret_cast<float2*>(buf + (2 * i) * 128) = make_float2(acc[i][0], acc[i][1]);
-                    *reinterpret_cast<float2*>(buf + (2 * i + 1) * 128) = make_float2(acc[i][2], acc[i][3]);
-                }
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        buf[(i * NT + nt) * 32] = make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
             }
             tree_consumers_sync();
             if (warp < from) {
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const float2 a = *reinterpret_cast<const float2*>(buf + (2 * i) * 128);
-                    const float2 b = *reinterpret_cast<const float2*>(buf + (2 * i + 1) * 128);
-                    acc[i][0] += a.x;
-                    acc[i][1] += a.y;
-                    acc[i][2] += b.x;
-                    acc[i][3] += b.y;
-                }
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float4 a = buf[(i * NT + nt) * 32];
+                        acc[i][nt][0] += a.x;
+                        acc[i][nt][1] += a.y;
+                        acc[i][nt][2] += a.z;
+                        acc[i][nt][3] += a.w;
+                    }
+            }
+            if (from == 2) tree_consumers_sync();
+        }
+        if (!w.whole) {
+            if (warp == 0) {
+                float* out = p.ws_o + ((size_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * C::kRows * D;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int hi = 0; hi < 2; ++hi)
+                            *reinterpret_cast<float2*>(out + col_of(i, hi) * C::kRows + 8 * nt + 2 * qc) =
+                                make_float2(acc[i][nt][2 * hi], acc[i][nt][2 * hi + 1]);
+            }
+        } else {
+            // rows [kRows][D] to shared memory (past warp 1's part), then out by all warps
+            float* rows_s = so + C::kRows * D;
+            if (warp == 0) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            rows_s[(8 * nt + 2 * qc + (e & 1)) * D + col_of(i, e >> 1)] = acc[i][nt][e];
             }
             tree_consumers_sync();
-        }
-        if (warp == 0) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = qr + 8 * r;
-                if (row >= rows) continue;
-                const float inv = sum[r] == 0.f ? 0.f : 1.0f / sum[r];
-                const float lse2 = sumx[r] == 0.f ? -INFINITY : M[r] + log2f(sumx[r]);
-                const size_t bht = (size_t)(qrow[r] - p.q) / p.dh;  // (b, hq, t)
-                const size_t place = ((size_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * kRows + row;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int col = col_of(i, e);
-                        const float v = acc[i][2 * r + e] * inv;
-                        if (!w.whole) p.ws_o[place * D + col] = v;
-                        else if (col < p.dh) {
-                            if (p.out_f32) static_cast<float*>(p.o)[bht * p.dh + col] = v;
-                            else static_cast<__nv_bfloat16*>(p.o)[bht * p.dh + col] = __float2bfloat16_rn(v);
-                        }
-                    }
-                if (qc == 0) {
-                    if (!w.whole) p.ws_lse[place] = lse2;
-                    else if (p.lse) p.lse[bht] = lse2 * kLn2t;
+            const int per = p.dh / 8;
+            for (int i = threadIdx.x; i < rows * per; i += kConsumers * 32) {
+                const int row = i / per, col = 8 * (i - row * per);
+                const int rr = w.rt * C::kRows + row;
+                const int t = rr / p.G;
+                const size_t at =
+                    (((size_t)w.b * p.Hq + (size_t)w.h * p.G + (rr - t * p.G)) * p.T + t) * p.dh + col;
+                const float4 a = *reinterpret_cast<const float4*>(rows_s + row * D + col);
+                const float4 b = *reinterpret_cast<const float4*>(rows_s + row * D + col + 4);
+                if (p.out_f32) {
+                    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.o) + at);
+                    o[0] = a;
+                    o[1] = b;
+                } else {
+                    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at) =
+                        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
+                                   pack_bf16x2(b.z, b.w));
                 }
             }
         }
@@ -645,119 +748,155 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     }
 }
 
-// One warp per row (b, h, t * G + g): merges the pieces of a cut item by
-// log-sum-exp in piece order, M = max lse_p, O = sum 2^(lse_p - M) o_p / sum
-// 2^(lse_p - M); rows past the sequence's drafted tokens get O = 0, LSE = -inf.
-constexpr int kMergeWarps = 4;
+// A block takes the `group_rows` rows of a (sequence, KV head) that lie next to
+// each other in a partial result and merges the pieces of their item, if it was
+// cut, by log-sum-exp in piece order: M = max lse_p, O = sum 2^(lse_p - M) o_p /
+// sum 2^(lse_p - M).  Rows past the sequence's drafted tokens get O = 0, LSE =
+// -inf.  A thread keeps to one row; the result goes through shared memory so
+// that rows leave in 16-byte pieces.
+constexpr int kMergeThreads = 128;
+constexpr int kMergeCols = 8;  // columns of a thread at a time
 
-__global__ void __launch_bounds__(kMergeWarps * 32)
+__global__ void __launch_bounds__(kMergeThreads)
 attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
-    const int lane = threadIdx.x & 31;
-    const long long at = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    __shared__ float s_o[32][256 + 4];
+    const int gr = p.group_rows;
     const int R = p.T * p.G;
-    if (at >= (long long)p.B * p.Hkv * R) return;
-    const long long bh = at / R;
-    const int r = (int)(at - bh * R);
+    const int groups = (R + gr - 1) / gr;
+    const long long bh = blockIdx.x / groups;
+    const int r0 = (int)(blockIdx.x - bh * groups) * gr;
     const int b = (int)(bh / p.Hkv), h = (int)(bh - (long long)b * p.Hkv);
-    const int t = r / p.G;
-    const size_t bht = ((size_t)b * p.Hq + (size_t)h * p.G + (r - t * p.G)) * p.T + t;
     const TreeSeq s = tree_seq(p, b);
-    int c0 = 0, c1 = -1, n = 1;  // CTAs that hold pieces of the item
+    const int live = s.drafted * p.G;  // rows of the sequence
+    int c0 = 0, c1 = -1, n = 1;        // CTAs that hold pieces of the item
     long long total = 1, start = 0;
-    if (t < s.drafted) {
+    if (r0 < live) {
         total = tree_total(p, false);
         n = tree_ctas(p, total);
-        const int rt = r / p.tile_rows;
-        start = tree_base(p, b) + ((long long)h * s.row_tiles + rt) * s.key_tiles;
+        start = tree_base(p, b) + ((long long)h * s.row_tiles + r0 / p.tile_rows) * s.key_tiles;
         const long long last = start + s.key_tiles - 1;
         c0 = (int)(start * n / total);
         while (c0 + 1 < n && tree_first(total, n, c0 + 1) <= start) ++c0;
         c1 = (int)(last * n / total);
         while (c1 + 1 < n && tree_first(total, n, c1 + 1) <= last) ++c1;
-        if (c0 == c1) return;  // a whole item: the attention kernel wrote it
     }
-    const int row = r % p.tile_rows;
-    auto place = [&](int c) {
-        return ((size_t)c * 2 + (start > tree_first(total, n, c) ? 1 : 0)) * p.tile_rows + row;
-    };
-    float M = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(p.ws_lse + place(c)));
+    const bool whole = c0 == c1;  // the attention kernel wrote the live rows
+    const int r_last = min(gr, R - r0);
+    if (whole && r0 + r_last <= live) return;
+    const int row = threadIdx.x % gr;
+    const bool cut = !whole && r0 + row < live;
+    const int in_tile = (r0 + row) % p.tile_rows;
+    float sum = 0.f, M = -INFINITY, Ms = 0.f;
+    auto place = [&](int c) { return (size_t)c * 2 + (start > tree_first(total, n, c) ? 1 : 0); };
+    if (cut) {
+        for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.ws_lse + place(c) * p.tile_rows + in_tile));
+        Ms = M == -INFINITY ? 0.f : M;
+        for (int c = c0; c <= c1; ++c) sum += ex2(__ldcg(p.ws_lse + place(c) * p.tile_rows + in_tile) - Ms);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    const int step = kMergeThreads / gr;  // columns apart
+    for (int col = threadIdx.x / gr; col < p.dw; col += step * kMergeCols) {
+        float acc[kMergeCols];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
-    const float Ms = M == -INFINITY ? 0.f : M;
-    for (int col = 4 * lane; col < p.dw; col += 128) {
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const size_t pl = place(c);
-            const float wt = ex2(__ldcg(p.ws_lse + pl) - Ms);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.ws_o + pl * p.dw + col));
-            sum += wt;
-            acc.x = fmaf(wt, v.x, acc.x);
-            acc.y = fmaf(wt, v.y, acc.y);
-            acc.z = fmaf(wt, v.z, acc.z);
-            acc.w = fmaf(wt, v.w, acc.w);
+        for (int k = 0; k < kMergeCols; ++k) acc[k] = 0.f;
+        if (cut) {
+            for (int c = c0; c <= c1; ++c) {
+                const size_t pl = place(c);
+                const float wt = ex2(__ldcg(p.ws_lse + pl * p.tile_rows + in_tile) - Ms);
+                const float* src = p.ws_o + (pl * p.tile_rows + (in_tile - row)) * p.dw + row;
+#pragma unroll
+                for (int k = 0; k < kMergeCols; ++k)
+                    if (col + k * step < p.dw) acc[k] = fmaf(wt, __ldcg(src + (size_t)(col + k * step) * gr), acc[k]);
+            }
         }
-        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-        if (col < p.dh) {
-            if (p.out_f32)
-                *reinterpret_cast<float4*>(static_cast<float*>(p.o) + bht * p.dh + col) =
-                    make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-            else
-                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + bht * p.dh + col) =
-                    make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+#pragma unroll
+        for (int k = 0; k < kMergeCols; ++k)
+            if (col + k * step < p.dw) s_o[row][col + k * step] = acc[k] * inv;
+    }
+    if (threadIdx.x < gr && row < r_last && p.lse && (cut || r0 + row >= live)) {
+        const int r = r0 + row, t = r / p.G;
+        p.lse[((size_t)b * p.Hq + (size_t)h * p.G + (r - t * p.G)) * p.T + t] =
+            sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2t;
+    }
+    __syncthreads();
+    const int per = p.dh / 8;
+    for (int i = threadIdx.x; i < r_last * per; i += kMergeThreads) {
+        const int ro = i / per, col = 8 * (i - ro * per);
+        const int r = r0 + ro, t = r / p.G;
+        if (whole && r < live) continue;
+        const size_t at = (((size_t)b * p.Hq + (size_t)h * p.G + (r - t * p.G)) * p.T + t) * p.dh + col;
+        const float4 x = *reinterpret_cast<const float4*>(&s_o[ro][col]);
+        const float4 y = *reinterpret_cast<const float4*>(&s_o[ro][col + 4]);
+        if (p.out_f32) {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.o) + at);
+            o[0] = x;
+            o[1] = y;
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at) =
+                make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y),
+                           pack_bf16x2(y.z, y.w));
         }
-        if (col == 0 && p.lse) p.lse[bht] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2t;
     }
 }
 
-template <int D, bool F8>
+template <int D, bool F8, int NT>
 attn_status_t launch_tree_t(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
                             cudaStream_t stream, const DeviceInfo& dev) {
-    using C = TreeCfg<D, F8>;
+    using C = TreeCfg<D, F8, NT>;
     static int attr_set[64] = {0};
     if (dev.device >= 64 || !attr_set[dev.device]) {
-        if (cudaFuncSetAttribute(attn_tree_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(attn_tree_kernel<D, F8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::kSmem) != cudaSuccess)
             return ATTN_ERR_CUDA;
         if (dev.device < 64) attr_set[dev.device] = 1;
     }
-    attn_tree_kernel<D, F8><<<p.ctas, kTreeThreads, C::kSmem, stream>>>(tk, tv, p);
+    attn_tree_kernel<D, F8, NT><<<p.ctas, kTreeThreads, C::kSmem, stream>>>(tk, tv, p);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// Head dim that a cache runs at: 64, 128 or 256 columns (E4M3: 128 or 256).
-int tree_width(int d, bool f8) { return d <= 64 && !f8 ? 64 : (d <= 128 ? 128 : 256); }
-
-// CTAs of a launch: two to an SM (one at 256 columns of bf16, whose ring fills
-// the shared memory).
-int tree_grid(int d, bool f8, int num_sms) { return num_sms * (tree_width(d, f8) == 256 ? 1 : 2); }
+// Calls f<D, F8, NT>() for a cache of head dim d and `rows` query rows.
+template <typename F>
+auto tree_variant(int d, bool f8, int rows, F f) {
+    using std::integral_constant;
+    auto with_rows = [&](auto D, auto F8) {
+        return rows <= 8 ? f(D, F8, integral_constant<int, 1>()) : f(D, F8, integral_constant<int, 2>());
+    };
+    integral_constant<bool, true> yes;
+    integral_constant<bool, false> no;
+    if (f8) return d <= 128 ? with_rows(integral_constant<int, 128>(), yes) : with_rows(integral_constant<int, 256>(), yes);
+    if (d <= 64) return with_rows(integral_constant<int, 64>(), no);
+    if (d <= 128) return with_rows(integral_constant<int, 128>(), no);
+    return with_rows(integral_constant<int, 256>(), no);
+}
 
 size_t align16(size_t x) { return (x + 15) & ~size_t(15); }
 
 }  // namespace
 
 attn_status_t launch_tree_merge(const TreeParams& p, cudaStream_t stream) {
-    const long long rows = (long long)p.B * p.Hkv * p.T * p.G;
-    const long long blocks = (rows + kMergeWarps - 1) / kMergeWarps;
-    attn_tree_merge_kernel<<<(unsigned)blocks, kMergeWarps * 32, 0, stream>>>(p);
+    const long long groups = (p.T * p.G + p.group_rows - 1) / p.group_rows;
+    const long long blocks = (long long)p.B * p.Hkv * groups;
+    attn_tree_merge_kernel<<<(unsigned)blocks, kMergeThreads, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 // Whether a call runs on the tensor-core kernel of attn_tree_tc_sm103.cu.
-static bool tree_on_tc(int d, int rows) { return d <= 128 && rows > kRows; }
+static bool tree_on_tc(int d, int rows) { return d <= 128 && rows > kMaxRows; }
 
 static void tree_shape(TreeParams& p, int rows, bool f8, int num_sms) {
     if (tree_on_tc(p.dh, rows)) {
         tree_tc_shape(p, f8, num_sms);
         return;
     }
-    p.tile_rows = kRows;
     p.tile_keys = kTileKeys;
-    p.dw = tree_width(p.dh, f8);
-    p.ctas = tree_grid(p.dh, f8, num_sms);
     p.min_units = 2;
+    tree_variant(p.dh, f8, rows, [&](auto D, auto F8, auto NT) {
+        using C = TreeCfg<decltype(D)::value, decltype(F8)::value, decltype(NT)::value>;
+        p.tile_rows = p.group_rows = C::kRows;
+        p.dw = D;
+        p.ctas = num_sms * C::kCtas;
+        return 0;
+    });
 }
 
 size_t tree_workspace_bytes(int Hq, int Hkv, int T, int d, attn_cache_dtype_t cache_dtype, int num_sms) {
@@ -815,10 +954,10 @@ attn_status_t launch_decode_tree(const void* q, const void* k_pages, const void*
     if ((st = encode_tmap_pages(&tk, k_pages, f8, d, Hkv, page_size, num_blocks, p.box_keys)) != ATTN_OK) return st;
     if ((st = encode_tmap_pages(&tv, v_pages, f8, d, Hkv, page_size, num_blocks, p.box_keys)) != ATTN_OK) return st;
     if (tree_on_tc(d, rows_kv)) st = launch_tree_tc(tk, tv, p, f8, stream, dev);
-    else if (f8) st = p.dw == 128 ? launch_tree_t<128, true>(tk, tv, p, stream, dev) : launch_tree_t<256, true>(tk, tv, p, stream, dev);
-    else if (p.dw == 64) st = launch_tree_t<64, false>(tk, tv, p, stream, dev);
-    else if (p.dw == 128) st = launch_tree_t<128, false>(tk, tv, p, stream, dev);
-    else st = launch_tree_t<256, false>(tk, tv, p, stream, dev);
+    else
+        st = tree_variant(d, f8, rows_kv, [&](auto D, auto F8, auto NT) {
+            return launch_tree_t<decltype(D)::value, decltype(F8)::value, decltype(NT)::value>(tk, tv, p, stream, dev);
+        });
     if (st != ATTN_OK) return st;
     return launch_tree_merge(p, stream);
 }

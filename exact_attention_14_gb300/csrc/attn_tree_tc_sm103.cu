@@ -30,6 +30,7 @@
 // 2785 cycles of its share of HBM), the tensor cores and the exponentials above.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "tree_plan.h"
 
@@ -139,37 +140,36 @@ struct TcPiece {
 };
 
 // ------------------------------------------------------------------ producer
-// One lane.  The loads of a piece come in the order the products take them:
-// K of the first tile of each stream, then per tile its V and the K of the
-// stream's next tile.
+// A warp; each of its first lanes copies the tile's box of its own number.  The
+// loads of a piece come in the order the products take them: K of the first
+// tile of each stream, then per tile its V and the K of the stream's next tile.
 template <int D, bool F8>
 __device__ void tc_produce(const CUtensorMap* tk, const CUtensorMap* tv, uint8_t* smem, TcBars* bars,
                            const TreeParams& p) {
     using C = TcCfg<D, F8>;
     constexpr int kSlots = F8 ? C::kRawStages : C::kStages;
     constexpr int kBytes = F8 ? C::kRawTile : C::kTile;
+    const int lane = threadIdx.x & 31;
     uint64_t* full = F8 ? bars->raw_full : bars->full;
     uint64_t* empty = F8 ? bars->raw_empty : bars->empty;
-    uint8_t* ring = smem + (F8 ? C::kRaw : C::kRing);
+    const uint32_t ring = smem_u32(smem + (F8 ? C::kRaw : C::kRing)) + lane * p.box_keys * 128;
     const volatile int* abort_flag = &bars->abort;
-    const int boxes = kTcKeys / p.box_keys;
+    const bool copies = lane < kTcKeys / p.box_keys;
     long long issued = 0;
     bool ok = true;
     TreeWalk walk;
     walk.start(bars->range);
     TcPiece x;
-    auto load = [&](const CUtensorMap* map, int j) {
+    auto load = [&](const CUtensorMap* map, int page, int off) {
         const int slot = (int)(issued % kSlots);
         const long long round = issued / kSlots;
-        if (round > 0) ok = mbar_wait(smem_u32(&empty[slot]), (uint32_t)((round - 1) & 1), abort_flag);
+        if (round > 0) ok = warp_wait(&empty[slot], (uint32_t)(round - 1), abort_flag);
         if (!ok) return;
         const uint32_t bar = smem_u32(&full[slot]);
-        mbar_arrive_expect_tx(bar, kBytes);
-        const uint32_t dst = smem_u32(ring + slot * kBytes);
-        for (int i = 0; i < boxes; ++i) {
-            int off;
-            const int page = tree_page(p, x.w.b, (x.w.k0 + j) * kTcKeys + i * p.box_keys, x.w.keys, off);
-            const uint32_t to = dst + i * p.box_keys * 128;
+        if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
+        __syncwarp();
+        if (copies) {
+            const uint32_t to = ring + slot * kBytes;
             if constexpr (F8) {
                 tma_load_4d(to, map, bar, 0, x.w.h, off, page);
             } else {
@@ -177,22 +177,43 @@ __device__ void tc_produce(const CUtensorMap* tk, const CUtensorMap* tv, uint8_t
                 for (int c = 0; c < D / 64; ++c) tma_load_4d(to + c * 16384, map, bar, 64 * c, x.w.h, off, page);
             }
         }
+        __syncwarp();
         ++issued;
     };
     while (ok && walk.next(p, x.w)) {
         x.set(p);
-        const int ahead = x.pair ? 1 : 2;
-        for (int j = 0; j < ahead && j < x.n && ok; ++j) load(tk, j);
+        // pages of the tiles whose K has been loaded and whose V has not, and of
+        // the next one (looked up before the wait that precedes its loads)
+        int page[3], off[3];
+        auto look = [&](int i, int j) {
+            page[i] = -1;
+            off[i] = 0;
+            if (copies && j < x.n)
+                page[i] = tree_page(p, x.w.b, (x.w.k0 + j) * kTcKeys + lane * p.box_keys, x.w.keys, off[i]);
+        };
+        look(0, 0);
+        look(1, 1);
+        look(2, 2);
+        load(tk, page[0], off[0]);
+        if (!x.pair && x.n > 1 && ok) load(tk, page[1], off[1]);
         for (int j = 0; j < x.n && ok; ++j) {
-            load(tv, j);
-            if (ok && j + ahead < x.n) load(tk, j + ahead);
+            load(tv, page[0], off[0]);
+            if (x.pair) {
+                if (ok && j + 1 < x.n) load(tk, page[1], off[1]);
+            } else {
+                if (ok && j + 2 < x.n) load(tk, page[2], off[2]);
+            }
+            page[0] = page[1]; off[0] = off[1];
+            page[1] = page[2]; off[1] = off[2];
+            look(2, j + 3);
         }
     }
-    if (!ok) tc_abort(bars, p.err);
+    if (!ok && lane == 0) tc_abort(bars, p.err);
     for (int slot = 0; slot < kSlots && slot < issued; ++slot) {  // every copy lands
         const long long n = (issued - slot + kSlots - 1) / kSlots;
         mbar_wait(smem_u32(&full[slot]), (uint32_t)((n - 1) & 1), nullptr);
     }
+    __syncwarp();
 }
 
 // ----------------------------------------------------------------- MMA issuer
@@ -203,78 +224,91 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
     using C = TcCfg<D, F8>;
     const volatile int* abort_flag = &bars->abort;
     // (both operands bf16, or both fp16: format code 0)
-    const int ncols = (p.dh + 15) / 16 * 16;  // columns past the head dim are skipped
-    const int ksteps = ncols / 16;
-    const uint32_t drop = F8 ? (1u << 7) | (1u << 10) : 0u;
-    const uint32_t idS = make_idesc_bf16(128, kTcKeys, 0, 0) & ~drop;
-    const uint32_t idO = make_idesc_bf16(128, ncols, 0, 1) & ~drop;
+    constexpr uint32_t kDrop = F8 ? (1u << 7) | (1u << 10) : 0u;
+    constexpr uint32_t idS = make_idesc_bf16(128, kTcKeys, 0, 0) & ~kDrop;
+    constexpr uint32_t idO = make_idesc_bf16(128, D, 0, 1) & ~kDrop;
     const uint32_t q_lo[2] = {sdesc_lo(smem_u32(smem), 16), sdesc_lo(smem_u32(smem + C::kTile), 16)};
     const uint32_t ring = smem_u32(smem + C::kRing);
-    long long used = 0;  // operand tiles taken
+    uint32_t slot = 0, round = 0;  // of the next operand tile
     uint32_t cnt_q[2] = {0u, 0u}, cnt_p[2] = {0u, 0u}, cnt_fix = 0;
     bool ok = true;
-    auto take = [&](int& slot) {
-        slot = (int)(used % C::kStages);
-        ok = warp_wait(&bars->full[slot], (uint32_t)(used / C::kStages), abort_flag);
-        ++used;
+    auto take = [&]() {
+        const uint32_t mine = slot;
+        ok = warp_wait(&bars->full[mine], round, abort_flag);
+        if (++slot == C::kStages) {
+            slot = 0;
+            ++round;
+        }
         tc_fence_after();
+        return mine;
     };
     TreeWalk walk;
     walk.start(bars->range);
     TcPiece x;
     while (ok && walk.next(p, x.w)) {
         x.set(p);
-        int slot_k = 0, slot_v = 0;
-        auto scores = [&](int t) {
+        const bool pair = x.pair;
+        const int n0 = pair ? x.n : (x.n + 1) / 2, n1 = pair ? x.n : x.n / 2;  // tiles of each stream
+        uint32_t slot_k = 0, slot_v = 0;
+        auto scores = [&](auto T) {
+            constexpr int t = decltype(T)::value;
             const uint32_t k_lo = sdesc_lo(ring + slot_k * C::kTile, 16);
-            const uint32_t a_lo = q_lo[x.pair ? t : 0];
+            const uint32_t a_lo = pair ? q_lo[t] : q_lo[0];
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                if (kk >= ksteps) break;
                 const uint32_t step = (kk >> 2) * (16384 >> 4) + (kk & 3) * (32 >> 4);
                 mma_ss_warp(tmem + t * 128, sdesc_join(a_lo + step, kTcDescHi), sdesc_join(k_lo + step, kTcDescHi),
                             idS, kk > 0 ? 1u : 0u);
             }
             mma_commit_warp(smem_u32(&bars->s_full[t]));
-            if (!x.pair || t == 1) mma_commit_warp(smem_u32(&bars->empty[slot_k]));
+            if (!pair || t == 1) mma_commit_warp(smem_u32(&bars->empty[slot_k]));
         };
-        for (int t = 0; t < 2 && ok; ++t) {
-            if (!x.has(0, t)) continue;
-            if (x.pair || t == 0) {
+        auto begin = [&](auto T) {
+            constexpr int t = decltype(T)::value;
+            if ((t == 0 ? n0 : n1) == 0 || !ok) return;
+            if (pair || t == 0) {
                 ok = warp_wait(&bars->q_full[t], cnt_q[t]++, abort_flag);
-                if (!ok) break;
+                if (!ok) return;
                 tc_fence_after();
             }
-            if (!x.pair || t == 0) take(slot_k);
-            if (ok) scores(t);
-        }
-        for (int s = 0; ok && x.has(s, 0); ++s) {
-            for (int t = 0; t < 2 && ok; ++t) {
-                if (!x.has(s, t)) continue;
-                if (!x.pair || t == 0) {
-                    take(slot_v);
-                    if (!F8 && ok && x.special(x.tile(s, t))) {
-                        ok = warp_wait(&bars->fix_full[cnt_fix % kFix], cnt_fix / kFix, abort_flag);
-                        ++cnt_fix;
-                    }
-                    if (!ok) break;
+            if (!pair || t == 0) slot_k = take();
+            if (ok) scores(T);
+        };
+        auto step = [&](auto T, int s) {
+            constexpr int t = decltype(T)::value;
+            const int n = t == 0 ? n0 : n1;
+            if (s >= n || !ok) return;
+            if (!pair || t == 0) {
+                slot_v = take();
+                if (!F8 && ok && x.special(x.tile(s, t))) {
+                    ok = warp_wait(&bars->fix_full[cnt_fix % kFix], cnt_fix / kFix, abort_flag);
+                    ++cnt_fix;
                 }
-                ok = warp_wait(&bars->p_full[t], cnt_p[t]++, abort_flag, 32);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t v_lo = sdesc_lo(ring + slot_v * C::kTile, 16384);
+                if (!ok) return;
+            }
+            ok = warp_wait(&bars->p_full[t], cnt_p[t]++, abort_flag, 32);
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t v_lo = sdesc_lo(ring + slot_v * C::kTile, 16384);
 #pragma unroll
-                for (int kk = 0; kk < kTcKeys / 16; ++kk)
-                    mma_ts_warp(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
-                                sdesc_join(v_lo + kk * (2048 >> 4), kTcDescHi), idO, (s > 0 || kk > 0) ? 1u : 0u);
-                if (!x.pair || t == 1) mma_commit_warp(smem_u32(&bars->empty[slot_v]));
-                if (x.has(s + 1, t)) {
-                    if (!x.pair || t == 0) take(slot_k);
-                    if (ok) scores(t);  // in order after the product that reads P over it
-                } else {
-                    mma_commit_warp(smem_u32(&bars->o_full[t]));
-                }
+            for (int kk = 0; kk < kTcKeys / 16; ++kk)
+                mma_ts_warp(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
+                            sdesc_join(v_lo + kk * (2048 >> 4), kTcDescHi), idO, (s > 0 || kk > 0) ? 1u : 0u);
+            if (!pair || t == 1) mma_commit_warp(smem_u32(&bars->empty[slot_v]));
+            if (s + 1 < n) {
+                if (!pair || t == 0) slot_k = take();
+                if (ok) scores(T);  // in order after the product that reads P over it
+            } else {
+                mma_commit_warp(smem_u32(&bars->o_full[t]));
             }
+        };
+        std::integral_constant<int, 0> S0;
+        std::integral_constant<int, 1> S1;
+        begin(S0);
+        begin(S1);
+        for (int s = 0; s < n0 && ok; ++s) {
+            step(S0, s);
+            step(S1, s);
         }
     }
     if (!ok && elect_one()) tc_abort(bars, p.err);
@@ -492,25 +526,38 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
 }
 
 // -------------------------------------------------------------------- softmax
-// 32 keys' worth of a row's mask, key u0 + i (counted from the first drafted
-// token; negative: before it) at bit i.
-__device__ __forceinline__ uint32_t tc_allow32(const TreeParams& p, int b, int t, int drafted, int u0) {
-    if (u0 <= -32) return 0xFFFFFFFFu;
+// A row's mask over the 128 keys of a tile: bit i of word w is key u0 + 32 w + i,
+// counted from the first drafted token (negative: before it).
+__device__ __forceinline__ void tc_allow(const TreeParams& p, int b, int t, int drafted, int u0,
+                                         uint32_t (&allow)[4]) {
     const int seen = p.mask ? drafted : min(t + 1, drafted);
-    const int n = seen - u0;  // keys below `seen`
-    const uint32_t range = n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
-    if (!p.mask) return range;
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(p.mask + ((size_t)b * p.T + t) * p.W);
-    uint32_t m;
-    if (u0 < 0) {
-        m = (__ldg(w) << -u0) | ((1u << -u0) - 1u);
-    } else {
-        const int i = u0 >> 5;
-        const uint32_t lo = i < 2 * p.W ? __ldg(w + i) : 0u;
-        const uint32_t hi = i + 1 < 2 * p.W ? __ldg(w + i + 1) : 0u;
-        m = __funnelshift_r(lo, hi, u0 & 31);
+    uint32_t bits[5];
+    const int first = u0 >> 5;  // (floor) 32-bit word of the row's mask that u0 falls in
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+        const int at = first + i;
+        bits[i] = 0xFFFFFFFFu;  // before the drafted tokens, or no mask
+        if (p.mask && at >= 0) {
+            const int last = 2 * p.W - 1;
+            bits[i] = __ldg(reinterpret_cast<const uint32_t*>(p.mask + ((size_t)b * p.T + t) * p.W) + min(at, last));
+        }
     }
-    return m & range;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const int n = seen - (u0 + 32 * w);  // keys below `seen`
+        const uint32_t range = n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
+        allow[w] = __funnelshift_r(bits[w], bits[w + 1], u0 & 31) & range;
+    }
+}
+
+__device__ __forceinline__ void tc_ld16(uint32_t at, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
 }
 
 struct TcRow {
@@ -622,14 +669,7 @@ __device__ __forceinline__ void tc_softmax_tile(uint32_t tS, uint32_t tO, uint32
 #pragma unroll 1
             for (int cc = 0; cc < ncols; cc += 16) {
                 uint32_t o[16];
-                asm volatile(
-                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                    "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                    : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]),
-                      "=r"(o[7]), "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]),
-                      "=r"(o[14]), "=r"(o[15])
-                    : "r"(tO + cc)
-                    : "memory");
+                tc_ld16(tO + cc, o);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
@@ -691,26 +731,27 @@ __device__ __noinline__ void tc_add_bad(const TreeParams& p, const TcPiece& x, c
     }
 }
 
-// Q rows of a stream's tile into shared memory: this warp's 32 rows, 16 lanes
+// Q rows of a stream's tile into shared memory: this warp's 32 rows, D / 8 lanes
 // a row (rows past the last repeat it), 128-byte swizzled 64-column halves.
+// `row_at`: where this lane's own row starts in Q.
 template <int D, bool F8>
-__device__ __forceinline__ void tc_load_q(const TreeParams& p, const TcPiece& x, int row0, int rows, int wq, int lane,
-                                          uint32_t tile, float* qs) {
-    constexpr int kLanes = D / 8;          // lanes of a row
-    constexpr int kPer = 32 / kLanes;      // rows of an instruction
+__device__ __forceinline__ void tc_load_q(const TreeParams& p, size_t row_at, int wq, int lane, uint32_t tile,
+                                          float* qs) {
+    constexpr int kLanes = D / 8;      // lanes of a row
+    constexpr int kPer = 32 / kLanes;  // rows of an instruction
     const int c = lane % kLanes;
+    const bool in = 8 * c < p.dh;
+    const __nv_bfloat16* q = p.q + (in ? 8 * c : 0);
     uint4 v[32 / kPer];
 #pragma unroll
     for (int i = 0; i < 32 / kPer; ++i) {
-        const int r = x.w.rt * kTcRows + row0 + min(wq * 32 + i * kPer + lane / kLanes, rows - 1);
-        const int t = r / p.G;
-        const size_t at = ((size_t)x.w.b * p.Hq + (size_t)x.w.h * p.G + (r - t * p.G)) * p.T + t;
-        v[i] = 8 * c < p.dh ? __ldg(reinterpret_cast<const uint4*>(p.q + at * p.dh + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
+        const size_t at = __shfl_sync(0xFFFFFFFFu, (unsigned long long)row_at, i * kPer + lane / kLanes);
+        v[i] = __ldg(reinterpret_cast<const uint4*>(q + at));
     }
 #pragma unroll
     for (int i = 0; i < 32 / kPer; ++i) {
         const int row = wq * 32 + i * kPer + lane / kLanes;
-        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t w[4] = {in ? v[i].x : 0u, in ? v[i].y : 0u, in ? v[i].z : 0u, in ? v[i].w : 0u};
         if constexpr (F8) {
             float mx = 0.f;
 #pragma unroll
@@ -729,6 +770,64 @@ __device__ __forceinline__ void tc_load_q(const TreeParams& p, const TcPiece& x,
     }
     fence_proxy_async_smem();
     __syncwarp();
+}
+
+// What a thread needs to write its row.
+struct TcOut {
+    int row, tok;      // row of the item, its drafted token
+    bool live, two;    // inside the item; both streams hold a part
+    float inv0, inv1;  // factors of stream 0's and 1's O
+    float m, inv;      // maximum and 1 / sum of the row (for rows added apart)
+    size_t bht, place;
+};
+
+// Columns [col0, col1) of the row: a partial result goes out a column at a time
+// (32 rows side by side), a whole one 32 or 64 bytes of the row at a time.
+template <int D, bool F8, bool BAD>
+__device__ __forceinline__ void tc_write(const TreeParams& p, const TcPiece& x, const TcOut& o, uint32_t tA, int col0,
+                                         int col1, const uint32_t* bad) {
+#pragma unroll 1
+    for (int cc = col0; cc < col1; cc += 16) {
+        uint32_t a[16], b[16];
+        tc_ld16(tA + cc, a);
+        if (o.two) tc_ld16(tA + 128 + cc, b);
+        tmem_wait_ld();
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            v[i] = __uint_as_float(a[i]) * o.inv0;
+            if (o.two) v[i] = fmaf(__uint_as_float(b[i]), o.inv1, v[i]);
+        }
+        if constexpr (BAD) tc_add_bad<F8>(p, x, bad, o.tok, p.q + o.bht * p.dh, o.m, o.inv, cc, v);
+        if (!x.w.whole) {
+            float* out = p.ws_o + (o.place * kTcRows + (o.row & ~31)) * p.dw + cc * 32 + (threadIdx.x & 31);
+            if (o.live) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) out[i * 32] = v[i];
+            }
+        } else if (o.live && p.out_f32) {
+            float* out = static_cast<float*>(p.o) + o.bht * p.dh + cc;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (cc + 4 * i < p.dh)
+                    reinterpret_cast<float4*>(out)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else if (o.live) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + o.bht * p.dh + cc;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (cc + 8 * i < p.dh)
+                    reinterpret_cast<uint4*>(out)[i] =
+                        make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                   pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+        }
+    }
+}
+// The same with the rows that were taken out of the product added; out of line
+// so that its stack does not weigh on the ordinary way.
+template <int D, bool F8>
+__device__ __noinline__ void tc_write_slow(const TreeParams& p, const TcPiece& x, const TcOut& o, uint32_t tA,
+                                           int col0, int col1, const uint32_t* bad) {
+    tc_write<D, F8, true>(p, x, o, tA, col0, col1, bad);
 }
 
 template <int D, bool F8>
@@ -757,7 +856,7 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
         const size_t bht = ((size_t)x.w.b * p.Hq + (size_t)x.w.h * p.G + (r - tok * p.G)) * p.T + tok;
         if (x.pair || t == 0) {
             const int tile = x.pair ? t : 0;
-            if (active) tc_load_q<D, F8>(p, x, row0, rows, wq, lane, smem_u32(smem + tile * C::kTile), bars->qs[tile]);
+            if (active) tc_load_q<D, F8>(p, bht * p.dh, wq, lane, smem_u32(smem + tile * C::kTile), bars->qs[tile]);
             if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[tile]));
         }
         if constexpr (F8) {
@@ -792,9 +891,7 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
             if (active) {
                 uint32_t allow[4];
                 if (x.special(j)) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        allow[i] = tc_allow32(p, x.w.b, tok, x.w.drafted, (x.w.k0 + j) * kTcKeys + 32 * i - x.prefix);
+                    tc_allow(p, x.w.b, tok, x.w.drafted, (x.w.k0 + j) * kTcKeys - x.prefix, allow);
                     tc_softmax_tile<D, F8, true>(tS, tO + 128 * t, kf, wv, fexp, allow, s == 0, c, ncols, st);
                 } else {
                     tc_softmax_tile<D, F8, false>(tS, tO + 128 * t, kf, wv, fexp, allow, s == 0, c, ncols, st);
@@ -820,12 +917,12 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
             tc_fence_after();
         }
         // ---- epilogue
-        float inv0, inv1 = 0.f, m = st.m, lx = st.lx;  // factors of stream 0's and 1's O
+        float inv0, inv1 = 0.f, m = st.m, lx = st.lx, inv_l;  // factors of stream 0's and 1's O
         int col0 = 0, col1 = ncols;
         uint32_t tA = tO + 128 * t;
         if (x.pair) {
-            inv0 = st.l == 0.f ? 0.f : 1.0f / st.l;
-            if constexpr (F8) inv0 *= tc_pow2(st.fexp) / kTcFrame;
+            inv_l = st.l == 0.f ? 0.f : 1.0f / st.l;
+            inv0 = F8 ? inv_l * (tc_pow2(st.fexp) / kTcFrame) : inv_l;
         } else {
             // the streams' statistics meet in shared memory; each warpgroup
             // then merges half of the columns, both O's being in its lanes
@@ -845,9 +942,9 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
             const float a0 = ex2(m0 - ms), a1 = ex2(m1 - ms);
             const float l = a0 * bars->l[0][me] + a1 * bars->l[1][me];
             lx = a0 * bars->lx[0][me] + a1 * bars->lx[1][me];
-            const float inv = l == 0.f ? 0.f : 1.0f / l;
-            inv0 = a0 * inv * bars->fin[0];
-            inv1 = a1 * inv * bars->fin[1];
+            inv_l = l == 0.f ? 0.f : 1.0f / l;
+            inv0 = a0 * inv_l * bars->fin[0];
+            inv1 = a1 * inv_l * bars->fin[1];
             const int half = (ncols / 2 + 15) / 16 * 16;
             col0 = t == 0 ? 0 : half;
             col1 = t == 0 ? half : ncols;
@@ -857,70 +954,24 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
         const uint32_t* bad = &bars->bad[piece % kBadBufs][0][0];
         uint32_t any_bad = 0u;
         for (int i = 0; i < 4 * (x.n - x.first_special()); ++i) any_bad |= *((const volatile uint32_t*)bad + i);
-        const size_t place = ((size_t)blockIdx.x * 2 + (first_piece ? 0 : 1)) * kTcRows + row;
         if (active) {
-#pragma unroll 1
-            for (int cc = col0; cc < col1; cc += 16) {
-                uint32_t a[16], b[16];
-                asm volatile(
-                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                    "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                    : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]),
-                      "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]),
-                      "=r"(a[14]), "=r"(a[15])
-                    : "r"(tA + cc)
-                    : "memory");
-                if (two)
-                    asm volatile(
-                        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                        : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]),
-                          "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]),
-                          "=r"(b[14]), "=r"(b[15])
-                        : "r"(tA + 128 + cc)
-                        : "memory");
-                tmem_wait_ld();
-                float v[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    v[i] = __uint_as_float(a[i]) * inv0;
-                    if (two) v[i] = fmaf(__uint_as_float(b[i]), inv1, v[i]);
-                }
-                if (any_bad) {
-                    const float lsum = x.pair ? st.l : 0.f;
-                    float inv = lsum == 0.f ? 0.f : 1.0f / lsum;
-                    if (!x.pair) {
-                        const float ms = m == -INFINITY ? 0.f : m;
-                        const float l = ex2(bars->m[0][me] - ms) * bars->l[0][me] + ex2(bars->m[1][me] - ms) * bars->l[1][me];
-                        inv = l == 0.f ? 0.f : 1.0f / l;
-                    }
-                    tc_add_bad<F8>(p, x, bad, tok, p.q + bht * p.dh, m, inv, cc, v);
-                }
-                if (me < rows) {
-                    if (!x.w.whole) {
-                        float4* o = reinterpret_cast<float4*>(p.ws_o + place * p.dw + cc);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    } else if (p.out_f32) {
-                        float* o = static_cast<float*>(p.o) + bht * p.dh + cc;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (cc + 4 * i < p.dh)
-                                reinterpret_cast<float4*>(o)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    } else {
-                        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + bht * p.dh + cc;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            if (cc + 8 * i < p.dh)
-                                reinterpret_cast<uint4*>(o)[i] =
-                                    make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                                               pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
-                    }
-                }
-            }
+            const size_t place = (size_t)blockIdx.x * 2 + (first_piece ? 0 : 1);
+            TcOut o;
+            o.row = row;
+            o.live = me < rows;
+            o.two = two;
+            o.inv0 = inv0;
+            o.inv1 = inv1;
+            o.m = m;
+            o.inv = inv_l;
+            o.tok = tok;
+            o.bht = bht;
+            o.place = place;
+            if (any_bad) tc_write_slow<D, F8>(p, x, o, tA, col0, col1, bad);
+            else tc_write<D, F8, false>(p, x, o, tA, col0, col1, bad);
             if (me < rows && (x.pair || t == 0)) {
                 const float lse2 = lx == 0.f ? -INFINITY : m + log2f(lx);
-                if (!x.w.whole) p.ws_lse[place] = lse2;
+                if (!x.w.whole) p.ws_lse[place * kTcRows + row] = lse2;
                 else if (p.lse) p.lse[bht] = lse2 * kTcLn2;
             }
         }
@@ -991,8 +1042,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     if (warp < 4) {
         reg_dealloc<C::kRegsControl>();
         if (warp == 0) {
-            if (lane == 0) tc_produce<D, F8>(&tk, &tv, smem, bars, p);
-            __syncwarp();
+            tc_produce<D, F8>(&tk, &tv, smem, bars, p);
         } else if (warp == 1) {
             tc_mma<D, F8>(smem, bars, tmem, p);
         } else if constexpr (!F8) {
@@ -1037,6 +1087,7 @@ void tree_tc_shape(TreeParams& p, bool f8, int num_sms) {
     p.dw = p.dh <= 64 && !f8 ? 64 : 128;
     p.ctas = num_sms;
     p.min_units = 2;
+    p.group_rows = 32;
 }
 
 attn_status_t launch_tree_tc(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, bool f8,

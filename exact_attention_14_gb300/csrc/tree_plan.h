@@ -41,9 +41,10 @@ struct TreeParams {
     const __nv_bfloat16* q;
     void* o;
     float* lse;
-    float* ws_o;               // [2 * ctas][tile_rows][dw]
+    float* ws_o;               // [2 * ctas][tile_rows / group_rows][dw][group_rows]
     float* ws_lse;             // [2 * ctas][tile_rows], base 2
     int dw;                    // columns of a partial row
+    int group_rows;            // 8, 16 or 32: rows that lie next to each other in a partial
     int out_f32;
     unsigned int* err;
 };
@@ -168,10 +169,17 @@ struct TreeWalk {
             n = tree_units(p, s);
         }
         const long long at = u - base;
-        const long long item = at / s.key_tiles;
-        w.k0 = (int)(at - item * s.key_tiles);
-        w.h = (int)(item / s.row_tiles);
-        w.rt = (int)(item - (long long)w.h * s.row_tiles);
+        if (at <= 0x7FFFFFFFll) {  // (64-bit divisions take hundreds of cycles)
+            const unsigned item = (unsigned)at / (unsigned)s.key_tiles;
+            w.k0 = (int)((unsigned)at - item * (unsigned)s.key_tiles);
+            w.h = (int)(item / (unsigned)s.row_tiles);
+            w.rt = (int)(item - (unsigned)w.h * (unsigned)s.row_tiles);
+        } else {
+            const long long item = at / s.key_tiles;
+            w.k0 = (int)(at - item * s.key_tiles);
+            w.h = (int)(item / s.row_tiles);
+            w.rt = (int)(item - (long long)w.h * s.row_tiles);
+        }
         const long long left = u1 - u;
         w.k1 = (int)(left < s.key_tiles - w.k0 ? w.k0 + left : s.key_tiles);
         w.b = b;
