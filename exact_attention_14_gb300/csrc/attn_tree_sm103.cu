@@ -255,6 +255,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         if (lane == 0) bars->range = r;
     }
     if (threadIdx.x == 32) {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the merge waits by itself)
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(smem_u32(&bars->full[i]), 1);
             mbar_init(smem_u32(&bars->empty[i]), kConsumers);
@@ -748,85 +749,101 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     }
 }
 
-// A block takes the `group_rows` rows of a (sequence, KV head) that lie next to
-// each other in a partial result and merges the pieces of their item, if it was
-// cut, by log-sum-exp in piece order: M = max lse_p, O = sum 2^(lse_p - M) o_p /
-// sum 2^(lse_p - M).  Rows past the sequence's drafted tokens get O = 0, LSE =
-// -inf.  A thread keeps to one row; the result goes through shared memory so
-// that rows leave in 16-byte pieces.
+// A block takes kMergeCols columns for every column lane of the `group_rows`
+// rows of a (sequence, KV head) that lie next to each other in a partial result,
+// and merges the pieces of their item, if it was cut, by log-sum-exp in piece
+// order: M = max lse_p, O = sum 2^(lse_p - M) o_p / sum 2^(lse_p - M).  Rows past
+// the sequence's drafted tokens get O = 0, LSE = -inf.  It is short and all
+// latency, so every load of a step is in flight at once; it starts while the
+// attention kernel ends (programmatic launch) and waits for it before it reads.
 constexpr int kMergeThreads = 128;
-constexpr int kMergeCols = 8;  // columns of a thread at a time
+constexpr int kMergeCols = 4;
+constexpr int kMergePieces = 8;  // pieces whose loads are in flight together
 
 __global__ void __launch_bounds__(kMergeThreads)
 attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
-    __shared__ float s_o[32][256 + 4];
+    extern __shared__ float s_w[];  // [pieces][group_rows]: lse, then weights
+    __shared__ __align__(16) float s_o[kMergeThreads * kMergeCols];
     const int gr = p.group_rows;
     const int R = p.T * p.G;
     const int groups = (R + gr - 1) / gr;
-    const long long bh = blockIdx.x / groups;
-    const int r0 = (int)(blockIdx.x - bh * groups) * gr;
-    const int b = (int)(bh / p.Hkv), h = (int)(bh - (long long)b * p.Hkv);
+    const int bh = blockIdx.x / groups;
+    const int r0 = (blockIdx.x - bh * groups) * gr;
+    const int b = bh / p.Hkv, h = bh - b * p.Hkv;
     const TreeSeq s = tree_seq(p, b);
     const int live = s.drafted * p.G;  // rows of the sequence
     int c0 = 0, c1 = -1, n = 1;        // CTAs that hold pieces of the item
     long long total = 1, start = 0;
     if (r0 < live) {
-        total = tree_total(p, false);
+        total = tree_total_base(p, b, start);
         n = tree_ctas(p, total);
-        start = tree_base(p, b) + ((long long)h * s.row_tiles + r0 / p.tile_rows) * s.key_tiles;
+        start += ((long long)h * s.row_tiles + r0 / p.tile_rows) * s.key_tiles;
         const long long last = start + s.key_tiles - 1;
         c0 = (int)(start * n / total);
         while (c0 + 1 < n && tree_first(total, n, c0 + 1) <= start) ++c0;
         c1 = (int)(last * n / total);
         while (c1 + 1 < n && tree_first(total, n, c1 + 1) <= last) ++c1;
     }
-    const bool whole = c0 == c1;  // the attention kernel wrote the live rows
-    const int r_last = min(gr, R - r0);
-    if (whole && r0 + r_last <= live) return;
-    const int row = threadIdx.x % gr;
-    const bool cut = !whole && r0 + row < live;
-    const int in_tile = (r0 + row) % p.tile_rows;
-    float sum = 0.f, M = -INFINITY, Ms = 0.f;
-    auto place = [&](int c) { return (size_t)c * 2 + (start > tree_first(total, n, c) ? 1 : 0); };
-    if (cut) {
-        for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.ws_lse + place(c) * p.tile_rows + in_tile));
-        Ms = M == -INFINITY ? 0.f : M;
-        for (int c = c0; c <= c1; ++c) sum += ex2(__ldcg(p.ws_lse + place(c) * p.tile_rows + in_tile) - Ms);
-    }
+    const bool whole = c0 == c1;  // the attention kernel writes the live rows
+    const int rows = min(gr, R - r0);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // (every block: the grid may not end before the other)
+    if (whole && r0 + rows <= live) return;
+    const int row = threadIdx.x % gr, lane = threadIdx.x / gr, lanes = kMergeThreads / gr;
+    const int in_tile = r0 % p.tile_rows;  // of the group's first row
+    // only the first piece can be its CTA's last one (place 2c + 1)
+    const int first_place = 2 * c0 + (start > tree_first(total, n, c0) ? 1 : 0);
+    const int pieces = whole ? 0 : c1 - c0 + 1;
+    auto place = [&](int i) { return (size_t)(i == 0 ? first_place : 2 * (c0 + i)); };
+    for (int i = lane; i < pieces; i += lanes)
+        s_w[i * gr + row] = __ldcg(p.ws_lse + place(i) * p.tile_rows + in_tile + row);
+    __syncthreads();
+    const bool cut = pieces > 0 && r0 + row < live;
+    float M = -INFINITY, sum = 0.f;
+    if (cut)
+        for (int i = 0; i < pieces; ++i) M = fmaxf(M, s_w[i * gr + row]);
+    const float Ms = M == -INFINITY ? 0.f : M;
+    if (cut)
+        for (int i = 0; i < pieces; ++i) sum += ex2(s_w[i * gr + row] - Ms);
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-    const int step = kMergeThreads / gr;  // columns apart
-    for (int col = threadIdx.x / gr; col < p.dw; col += step * kMergeCols) {
-        float acc[kMergeCols];
+    const int col0 = blockIdx.y * lanes * kMergeCols;  // this block's columns: col0 + lane + k * lanes
+    float acc[kMergeCols];
 #pragma unroll
-        for (int k = 0; k < kMergeCols; ++k) acc[k] = 0.f;
-        if (cut) {
-            for (int c = c0; c <= c1; ++c) {
-                const size_t pl = place(c);
-                const float wt = ex2(__ldcg(p.ws_lse + pl * p.tile_rows + in_tile) - Ms);
-                const float* src = p.ws_o + (pl * p.tile_rows + (in_tile - row)) * p.dw + row;
+    for (int k = 0; k < kMergeCols; ++k) acc[k] = 0.f;
+    if (cut) {
+        const float* src = p.ws_o + (size_t)in_tile * p.dw + (size_t)(col0 + lane) * gr + row;
+        for (int i0 = 0; i0 < pieces; i0 += kMergePieces) {
+            float v[kMergePieces][kMergeCols];
+#pragma unroll
+            for (int i = 0; i < kMergePieces; ++i)
 #pragma unroll
                 for (int k = 0; k < kMergeCols; ++k)
-                    if (col + k * step < p.dw) acc[k] = fmaf(wt, __ldcg(src + (size_t)(col + k * step) * gr), acc[k]);
+                    v[i][k] = i0 + i < pieces
+                                  ? __ldcg(src + place(i0 + i) * p.tile_rows * p.dw + (size_t)k * lanes * gr)
+                                  : 0.f;
+#pragma unroll
+            for (int i = 0; i < kMergePieces; ++i) {
+                const float wt = i0 + i < pieces ? ex2(s_w[(i0 + i) * gr + row] - Ms) : 0.f;
+#pragma unroll
+                for (int k = 0; k < kMergeCols; ++k) acc[k] = fmaf(wt, v[i][k], acc[k]);
             }
         }
-#pragma unroll
-        for (int k = 0; k < kMergeCols; ++k)
-            if (col + k * step < p.dw) s_o[row][col + k * step] = acc[k] * inv;
     }
-    if (threadIdx.x < gr && row < r_last && p.lse && (cut || r0 + row >= live)) {
+    const int cols = lanes * kMergeCols;
+#pragma unroll
+    for (int k = 0; k < kMergeCols; ++k) s_o[row * cols + lane + k * lanes] = acc[k] * inv;
+    if (blockIdx.y == 0 && threadIdx.x < gr && row < rows && p.lse && (cut || r0 + row >= live)) {
         const int r = r0 + row, t = r / p.G;
         p.lse[((size_t)b * p.Hq + (size_t)h * p.G + (r - t * p.G)) * p.T + t] =
             sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2t;
     }
     __syncthreads();
-    const int per = p.dh / 8;
-    for (int i = threadIdx.x; i < r_last * per; i += kMergeThreads) {
-        const int ro = i / per, col = 8 * (i - ro * per);
+    for (int i = threadIdx.x; i < rows * (cols / 8); i += kMergeThreads) {
+        const int ro = i / (cols / 8), cc = 8 * (i - ro * (cols / 8)), col = col0 + cc;
         const int r = r0 + ro, t = r / p.G;
-        if (whole && r < live) continue;
+        if (col >= p.dh || (whole && r < live)) continue;
         const size_t at = (((size_t)b * p.Hq + (size_t)h * p.G + (r - t * p.G)) * p.T + t) * p.dh + col;
-        const float4 x = *reinterpret_cast<const float4*>(&s_o[ro][col]);
-        const float4 y = *reinterpret_cast<const float4*>(&s_o[ro][col + 4]);
+        const float4 x = *reinterpret_cast<const float4*>(&s_o[ro * cols + cc]);
+        const float4 y = *reinterpret_cast<const float4*>(&s_o[ro * cols + cc + 4]);
         if (p.out_f32) {
             float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.o) + at);
             o[0] = x;
@@ -874,10 +891,19 @@ size_t align16(size_t x) { return (x + 15) & ~size_t(15); }
 }  // namespace
 
 attn_status_t launch_tree_merge(const TreeParams& p, cudaStream_t stream) {
+    const int cols = kMergeThreads / p.group_rows * kMergeCols;  // of a block
     const long long groups = (p.T * p.G + p.group_rows - 1) / p.group_rows;
-    const long long blocks = (long long)p.B * p.Hkv * groups;
-    attn_tree_merge_kernel<<<(unsigned)blocks, kMergeThreads, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hkv * groups), (unsigned)((p.dh + cols - 1) / cols));
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.dynamicSmemBytes = (size_t)p.ctas * p.group_rows * 4;  // (at most as many pieces as CTAs)
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_tree_merge_kernel, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 // Whether a call runs on the tensor-core kernel of attn_tree_tc_sm103.cu.

@@ -15,7 +15,7 @@
 // thread per row; they also lay Q out in shared memory, whose rows are not
 // evenly spaced in a [B, Hq, T, d] tensor).  bf16 caches: warps 2-3 prepare V
 // in the tiles that hold drafted tokens or the end of the sequence.  E4M3
-// caches: warps 12-15 convert every tile from codes to fp16 and prepare V and
+// caches: the same two convert every tile from codes to fp16 and prepare V and
 // the descales as they go; Q (scaled by a power of two per row), K, P and V
 // are fp16 operands, exact but for P.
 //
@@ -45,12 +45,6 @@ constexpr float kTcLn2 = 0.69314718055994530942f;
 
 template <int D, bool F8>
 struct TcCfg {
-    static constexpr int kThreads = F8 ? 512 : 384;
-    // registers of the control, softmax and converter warpgroups: their sum is
-    // the launch's (168 or 128 per thread)
-    static constexpr int kRegsControl = F8 ? 80 : 104;
-    static constexpr int kRegsSoftmax = F8 ? 176 : 200;
-    static constexpr int kRegsConvert = 80;
     static constexpr int kTile = 128 * D * 2;                  // 16-bit operand tile
     static constexpr int kStages = F8 ? 3 : (D == 128 ? 4 : 8);
     static constexpr int kRawTile = 128 * 128;                 // E4M3 codes
@@ -61,7 +55,12 @@ struct TcCfg {
     static constexpr int kSmem = kBar + 12 * 1024;
     static_assert(kSmem <= 232448, "shared memory budget");
 };
-static_assert(128 * (104 + 2 * 200) <= 384 * 168 && 128 * (80 + 2 * 176 + 80) <= 512 * 128, "register split");
+constexpr int kTcThreads = 384;
+// registers of the control and the softmax warpgroups: their sum is the launch's
+// (168 a thread)
+constexpr int kTcRegsControl = 104, kTcRegsSoftmax = 200;
+static_assert(128 * kTcRegsControl + 256 * kTcRegsSoftmax <= kTcThreads * 168, "register split");
+constexpr int kTcHelpers = 2;  // warps 2-3: V's fixers (bf16) or the converters (E4M3)
 
 constexpr int kFix = 8;        // special tiles between the fixer and its readers
 // Marks of the V rows that were taken out: for each of the last pieces, for
@@ -122,15 +121,19 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
 }
 
 // A piece's streams.  Tile s of stream t is key tile k0 + (pair ? s : 2 s + t).
+// Q lies in shared-memory tile t of a pair; split pieces that follow one another
+// change tiles, so that one's Q can be laid out while the other still runs.
 struct TcPiece {
     TreePiece w;
     int rows, n, prefix;
+    int q_tile;  // split: the tile that holds Q
     bool pair;
-    __device__ __forceinline__ void set(const TreeParams& p) {
+    __device__ __forceinline__ void set(const TreeParams& p, const TcPiece* before = nullptr) {
         rows = min(kTcRows, w.drafted * p.G - w.rt * kTcRows);
         n = w.k1 - w.k0;
         prefix = w.keys - w.drafted;
         pair = rows > 128;
+        q_tile = before && !before->pair ? before->q_tile ^ 1 : 0;
     }
     __device__ __forceinline__ int tile(int s, int t) const { return pair ? s : 2 * s + t; }
     __device__ __forceinline__ bool has(int s, int t) const { return tile(s, t) < n; }
@@ -244,16 +247,16 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
     };
     TreeWalk walk;
     walk.start(bars->range);
-    TcPiece x;
-    while (ok && walk.next(p, x.w)) {
-        x.set(p);
+    TcPiece x, last;
+    for (int piece = 0; ok && walk.next(p, x.w); ++piece, last = x) {
+        x.set(p, piece ? &last : nullptr);
         const bool pair = x.pair;
         const int n0 = pair ? x.n : (x.n + 1) / 2, n1 = pair ? x.n : x.n / 2;  // tiles of each stream
         uint32_t slot_k = 0, slot_v = 0;
         auto scores = [&](auto T) {
             constexpr int t = decltype(T)::value;
             const uint32_t k_lo = sdesc_lo(ring + slot_k * C::kTile, 16);
-            const uint32_t a_lo = pair ? q_lo[t] : q_lo[0];
+            const uint32_t a_lo = pair ? q_lo[t] : (x.q_tile ? q_lo[1] : q_lo[0]);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t step = (kk >> 2) * (16384 >> 4) + (kk & 3) * (32 >> 4);
@@ -267,7 +270,8 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
             constexpr int t = decltype(T)::value;
             if ((t == 0 ? n0 : n1) == 0 || !ok) return;
             if (pair || t == 0) {
-                ok = warp_wait(&bars->q_full[t], cnt_q[t]++, abort_flag);
+                const int q = pair ? t : x.q_tile;
+                ok = warp_wait(&bars->q_full[q], q ? cnt_q[1]++ : cnt_q[0]++, abort_flag);
                 if (!ok) return;
                 tc_fence_after();
             }
@@ -331,18 +335,22 @@ __device__ void tc_fix(int wf, uint8_t* smem, TcBars* bars, const TreeParams& p)
     TreeWalk walk;
     walk.start(bars->range);
     TcPiece x;
-    // the next load of the ring (every one is waited for: a barrier's parity
-    // tells only the last phase from the one before)
+    // the next load of the ring (every one is waited for, and its slot not given
+    // back before: a barrier's parity tells only the last phase from the one before)
     auto next_load = [&]() {
         const int slot = (int)(seen % C::kStages);
         ok = warp_wait(&bars->full[slot], (uint32_t)(seen / C::kStages), abort_flag);
         ++seen;
         return slot;
     };
+    auto give = [&](int slot) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->empty[slot]));
+    };
     for (int piece = 0; ok && walk.next(p, x.w); ++piece) {
         x.set(p);
         const int ahead = x.pair ? 1 : 2;
-        for (int j = 0; j < ahead && j < x.n && ok; ++j) next_load();
+        for (int j = 0; j < ahead && j < x.n && ok; ++j) give(next_load());
         for (int j = 0; j < x.n && ok; ++j) {
             const int slot = next_load();
             if (ok && x.special(j)) {
@@ -374,30 +382,30 @@ __device__ void tc_fix(int wf, uint8_t* smem, TcBars* bars, const TreeParams& p)
                 if (lane == 0) mbar_arrive(smem_u32(&bars->fix_full[fixed % kFix]));
                 ++fixed;
             }
-            if (ok && j + ahead < x.n) next_load();
+            give(slot);
+            if (ok && j + ahead < x.n) give(next_load());
         }
     }
     if (!ok && lane == 0) tc_abort(bars, p.err);
 }
 
 // ------------------------------------------------------- codes to fp16, E4M3
-// Four warps.  Eight lanes take a row's 128 codes, 16 each; the two 16-byte
-// results go out in an order that keeps a quarter-warp's stores on different
-// banks.  With K of a tile its descales are laid out for the softmax: K's as
-// they are, V's times frame / F, F = 2^fexp above every one so far.
+// Two warps, 64 keys each.  Eight lanes take a row's 128 codes, 16 each; the two
+// 16-byte results go out in an order that keeps a quarter-warp's stores on
+// different banks.  With K of a tile its descales are laid out for the softmax:
+// K's as they are, V's times frame / F, F = 2^fexp above every one so far.
 template <int D>
 __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams& p) {
     using C = TcCfg<D, true>;
     const int lane = threadIdx.x & 31;
     const volatile int* abort_flag = &bars->abort;
-    long long taken = 0;
-    uint32_t tiles = 0;
+    uint32_t raw_slot = 0, raw_round = 0, out_slot = 0, out_round = 0, tiles = 0;
     bool ok = true;
     TreeWalk walk;
     walk.start(bars->range);
     TcPiece x;
-    float kd = 0.f, vd[4] = {0.f, 0.f, 0.f, 0.f};
-    // descales of tile j: K's of key 32 wc + lane, V's of keys lane + 32 i
+    float kd[2] = {0.f, 0.f}, vd[4] = {0.f, 0.f, 0.f, 0.f};
+    // descales of tile j: K's of keys 64 wc + {0, 32} + lane, V's of keys lane + 32 i
     auto fetch = [&](int j) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -405,83 +413,89 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
             const int page = tree_page(p, x.w.b, (x.w.k0 + j) * kTcKeys + 32 * i + lane, x.w.keys, off);
             const long long at = ((long long)(page < 0 ? 0 : page) * p.Hkv + x.w.h) * p.page_size + off;
             vd[i] = page < 0 ? 0.f : __ldg(p.v_descale + at);
-            if (i == wc) kd = page < 0 ? 0.f : __ldg(p.k_descale + at);
+            if ((i >> 1) == wc) kd[i & 1] = page < 0 ? 0.f : __ldg(p.k_descale + at);
         }
     };
+    const int c = lane & 7;
+    const bool upper = c & 4;  // the upper half's lanes write their odd chunk first
     for (int piece = 0; ok && walk.next(p, x.w); ++piece) {
         x.set(p);
         int fexp = -100;
         const int ahead = x.pair ? 1 : 2;
         // one tile of codes; is_v: rows that must not enter the product are zeroed
         auto convert = [&](int j, bool is_v) {
-            const int rs = (int)(taken % C::kRawStages), os = (int)(taken % C::kStages);
-            ok = warp_wait(&bars->raw_full[rs], (uint32_t)(taken / C::kRawStages), abort_flag);
-            if (ok && taken >= C::kStages)
-                ok = warp_wait(&bars->empty[os], (uint32_t)(taken / C::kStages) - 1u, abort_flag);
+            ok = warp_wait(&bars->raw_full[raw_slot], raw_round, abort_flag);
+            if (ok && out_round > 0) ok = warp_wait(&bars->empty[out_slot], out_round - 1u, abort_flag);
             if (!ok) return;
-            const uint32_t raw = smem_u32(smem + C::kRaw + rs * C::kRawTile);
-            const uint32_t out = smem_u32(smem + C::kRing + os * C::kTile);
-            const int c = lane & 7;
+            const uint32_t raw = smem_u32(smem + C::kRaw + raw_slot * C::kRawTile);
+            const uint32_t out = smem_u32(smem + C::kRing + out_slot * C::kTile) + (c >> 2) * 16384;
             const bool check = is_v && x.special(j);
-            uint4 w[8];
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const int row0 = 64 * wc + 32 * half + (lane >> 3);  // this lane's rows: row0 + 4 i
+                uint4 w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int row = 32 * wc + 4 * i + (lane >> 3);
-                w[i] = tc_lds128(raw + row * 128 + ((c ^ (row & 7)) << 4));
-            }
-            if (check) {
-                uint32_t marks = 0u;
+                for (int i = 0; i < 8; ++i)
+                    w[i] = tc_lds128(raw + (row0 + 4 * i) * 128 + ((c ^ ((row0 + 4 * i) & 7)) << 4));
+                if (check) {
+                    uint32_t marks = 0u;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int key = (x.w.k0 + j) * kTcKeys + row0 + 4 * i;
+                        const bool drafted = key >= x.prefix && key < x.w.keys;
+                        bool hit = false;
+                        if (drafted) {
+                            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) hit |= ((u[e >> 2] >> (8 * (e & 3))) & 0x7Fu) == 0x7Fu;
+                            if (c == 0) {
+                                int off;
+                                const int page = tree_page(p, x.w.b, key, x.w.keys, off);
+                                if (page >= 0)
+                                    hit |= !isfinite(__ldg(p.v_descale + ((long long)page * p.Hkv + x.w.h) * p.page_size + off));
+                            }
+                        }
+                        const unsigned votes = __ballot_sync(0xFFFFFFFFu, hit);
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            if ((votes >> (8 * g)) & 0xFFu) marks |= 1u << (4 * i + g);
+                        if (key >= x.w.keys || ((votes >> (lane & 24)) & 0xFFu)) w[i] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    if (lane == 0) bars->bad[piece % kBadBufs][j - x.first_special()][2 * wc + half] = marks;
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int row = 32 * wc + 4 * i + (lane >> 3);
-                    const int key = (x.w.k0 + j) * kTcKeys + row;
-                    const bool drafted = key >= x.prefix && key < x.w.keys;
-                    bool hit = false;
-                    if (drafted) {
-                        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) hit |= ((u[e >> 2] >> (8 * (e & 3))) & 0x7Fu) == 0x7Fu;
-                        if (c == 0) {
-                            int off;
-                            const int page = tree_page(p, x.w.b, key, x.w.keys, off);
-                            if (page >= 0)
-                                hit |= !isfinite(__ldg(p.v_descale + ((long long)page * p.Hkv + x.w.h) * p.page_size + off));
-                        }
-                    }
-                    const unsigned votes = __ballot_sync(0xFFFFFFFFu, hit);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        if ((votes >> (8 * g)) & 0xFFu) marks |= 1u << (4 * i + g);
-                    if (key >= x.w.keys || ((votes >> (lane & 24)) & 0xFFu)) w[i] = make_uint4(0u, 0u, 0u, 0u);
+                    const int row = row0 + 4 * i;
+                    uint32_t h[8];
+                    tc_e4m3x4(w[i].x, h[0], h[1]);
+                    tc_e4m3x4(w[i].y, h[2], h[3]);
+                    tc_e4m3x4(w[i].z, h[4], h[5]);
+                    tc_e4m3x4(w[i].w, h[6], h[7]);
+                    const uint32_t dst = out + row * 128;
+                    const int ch = 2 * (c & 3) + (upper ? 1 : 0);
+                    sts128(dst + ((ch ^ (row & 7)) << 4), upper ? h[4] : h[0], upper ? h[5] : h[1], upper ? h[6] : h[2],
+                           upper ? h[7] : h[3]);
+                    sts128(dst + (((ch ^ 1) ^ (row & 7)) << 4), upper ? h[0] : h[4], upper ? h[1] : h[5],
+                           upper ? h[2] : h[6], upper ? h[3] : h[7]);
                 }
-                if (lane == 0) bars->bad[piece % kBadBufs][j - x.first_special()][wc] = marks;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int row = 32 * wc + 4 * i + (lane >> 3);
-                uint32_t h[8];
-                tc_e4m3x4(w[i].x, h[0], h[1]);
-                tc_e4m3x4(w[i].y, h[2], h[3]);
-                tc_e4m3x4(w[i].z, h[4], h[5]);
-                tc_e4m3x4(w[i].w, h[6], h[7]);
-                const uint32_t dst = out + (c >> 2) * 16384 + row * 128;
-                const int ch = 2 * (c & 3);
-                const bool swap = c & 4;  // the upper half's lanes write their odd chunk first
-                const uint32_t d0 = dst + (((ch + (swap ? 1 : 0)) ^ (row & 7)) << 4);
-                const uint32_t d1 = dst + (((ch + (swap ? 0 : 1)) ^ (row & 7)) << 4);
-                sts128(d0, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
-                sts128(d1, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(smem_u32(&bars->raw_empty[rs]));
-                mbar_arrive(smem_u32(&bars->full[os]));
+                mbar_arrive(smem_u32(&bars->full[out_slot]));
+                mbar_arrive(smem_u32(&bars->raw_empty[raw_slot]));
             }
-            ++taken;
+            if (++raw_slot == C::kRawStages) {
+                raw_slot = 0;
+                ++raw_round;
+            }
+            if (++out_slot == C::kStages) {
+                out_slot = 0;
+                ++out_round;
+            }
         };
         auto descales = [&](int j) {
-            const int slot = (int)(tiles % kDs);
+            const uint32_t slot = tiles % kDs;
             if (tiles >= kDs) {
                 ok = warp_wait(&bars->ds_empty[slot], tiles / kDs - 1u, abort_flag);
                 if (!ok) return;
@@ -497,11 +511,11 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
             for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
             fexp = max(fexp, min((int)(__float_as_uint(top) >> 23) - 126, 111));
             const float fr = kTcFrame * tc_pow2(-fexp);
-            float mine = vd[0];
 #pragma unroll
-            for (int i = 1; i < 4; ++i) mine = wc == i ? vd[i] : mine;
-            bars->kf[slot][32 * wc + lane] = kd;
-            bars->wv[slot][32 * wc + lane] = mine * fr;
+            for (int i = 0; i < 2; ++i) {
+                bars->kf[slot][64 * wc + 32 * i + lane] = kd[i];
+                bars->wv[slot][64 * wc + 32 * i + lane] = (wc == 0 ? vd[i] : vd[2 + i]) * fr;
+            }
             if (wc == 0 && lane == 0) bars->fexp[slot] = fexp;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full[slot]));
@@ -527,9 +541,10 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
 
 // -------------------------------------------------------------------- softmax
 // A row's mask over the 128 keys of a tile: bit i of word w is key u0 + 32 w + i,
-// counted from the first drafted token (negative: before it).
+// counted from the first drafted token (negative: before it).  `mask`: the row's
+// words where T <= 64.
 __device__ __forceinline__ void tc_allow(const TreeParams& p, int b, int t, int drafted, int u0,
-                                         uint32_t (&allow)[4]) {
+                                         uint2 mask, uint32_t (&allow)[4]) {
     const int seen = p.mask ? drafted : min(t + 1, drafted);
     uint32_t bits[5];
     const int first = u0 >> 5;  // (floor) 32-bit word of the row's mask that u0 falls in
@@ -538,8 +553,12 @@ __device__ __forceinline__ void tc_allow(const TreeParams& p, int b, int t, int 
         const int at = first + i;
         bits[i] = 0xFFFFFFFFu;  // before the drafted tokens, or no mask
         if (p.mask && at >= 0) {
-            const int last = 2 * p.W - 1;
-            bits[i] = __ldg(reinterpret_cast<const uint32_t*>(p.mask + ((size_t)b * p.T + t) * p.W) + min(at, last));
+            if (p.W == 1) {
+                bits[i] = at == 0 ? mask.x : mask.y;
+            } else {
+                const int last = 2 * p.W - 1;
+                bits[i] = __ldg(reinterpret_cast<const uint32_t*>(p.mask + ((size_t)b * p.T + t) * p.W) + min(at, last));
+            }
         }
     }
 #pragma unroll
@@ -772,6 +791,46 @@ __device__ __forceinline__ void tc_load_q(const TreeParams& p, size_t row_at, in
     __syncwarp();
 }
 
+// A thread's row of a piece: `row` of the item, drafted token `tok`, row `bht` of
+// Q and O; `rows` of the warpgroup's tile are live.
+struct TcMine {
+    int rows, row, tok;
+    size_t bht;
+};
+__device__ __forceinline__ TcMine tc_mine(const TreeParams& p, const TcPiece& x, int t, int me) {
+    TcMine a;
+    const int row0 = x.pair ? 128 * t : 0;
+    a.rows = min(128, x.rows - row0);
+    a.row = row0 + min(me, a.rows - 1);
+    const int r = x.w.rt * kTcRows + a.row;
+    a.tok = r / p.G;
+    a.bht = ((size_t)x.w.b * p.Hq + (size_t)x.w.h * p.G + (r - a.tok * p.G)) * p.T + a.tok;
+    return a;
+}
+// Lays out a piece's Q (out of line: its loads all want a register).
+template <int D, bool F8>
+__device__ __noinline__ void tc_piece_q(const TreeParams& p, TcPiece x, int t, uint8_t* smem, TcBars* bars) {
+    using C = TcCfg<D, F8>;
+    if (!x.pair && t == 1) return;  // stream 0's warps lay out a split piece's Q
+    const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const int tile = x.pair ? t : x.q_tile;
+    const TcMine a = tc_mine(p, x, t, wq * 32 + lane);
+    if (wq * 32 < a.rows) tc_load_q<D, F8>(p, a.bht * p.dh, wq, lane, smem_u32(smem + tile * C::kTile), bars->qs[tile]);
+    if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[tile]));
+}
+// The next piece's Q, where its tile is free already: a pair's own tile once its
+// last scores are there, a split piece's other tile at any time.  Returns bit 0:
+// there is a next piece, bit 1: its Q is laid out.
+template <int D, bool F8>
+__device__ __noinline__ int tc_next_q(const TreeParams& p, TreeWalk walk, TcPiece x, int t, uint8_t* smem, TcBars* bars) {
+    TcPiece y;
+    if (!walk.next(p, y.w)) return 0;
+    y.set(p, &x);
+    if (!x.pair && y.pair) return 1;
+    tc_piece_q<D, F8>(p, y, t, smem, bars);
+    return 3;
+}
+
 // What a thread needs to write its row.
 struct TcOut {
     int row, tok;      // row of the item, its drafted token
@@ -786,46 +845,62 @@ struct TcOut {
 template <int D, bool F8, bool BAD>
 __device__ __forceinline__ void tc_write(const TreeParams& p, const TcPiece& x, const TcOut& o, uint32_t tA, int col0,
                                          int col1, const uint32_t* bad) {
+    float* part = p.ws_o + (o.place * kTcRows + (o.row & ~31)) * p.dw + (threadIdx.x & 31);
+    const size_t at = o.bht * p.dh;
+    uint32_t a[2][16], b[2][16];
+    tc_ld16(tA + col0, a[0]);
+    if (o.two) tc_ld16(tA + 128 + col0, b[0]);
 #pragma unroll 1
-    for (int cc = col0; cc < col1; cc += 16) {
-        uint32_t a[16], b[16];
-        tc_ld16(tA + cc, a);
-        if (o.two) tc_ld16(tA + 128 + cc, b);
-        tmem_wait_ld();
-        float v[16];
+    for (int c2 = col0; c2 < col1; c2 += 32) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            v[i] = __uint_as_float(a[i]) * o.inv0;
-            if (o.two) v[i] = fmaf(__uint_as_float(b[i]), o.inv1, v[i]);
-        }
-        if constexpr (BAD) tc_add_bad<F8>(p, x, bad, o.tok, p.q + o.bht * p.dh, o.m, o.inv, cc, v);
-        if (!x.w.whole) {
-            float* out = p.ws_o + (o.place * kTcRows + (o.row & ~31)) * p.dw + cc * 32 + (threadIdx.x & 31);
-            if (o.live) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) out[i * 32] = v[i];
+        for (int h = 0; h < 2; ++h) {
+            const int cc = c2 + 16 * h;
+            if (cc >= col1) break;
+            tmem_wait_ld();
+            if (cc + 16 < col1) {  // the next 16 columns are on their way meanwhile
+                tc_ld16(tA + cc + 16, a[h ^ 1]);
+                if (o.two) tc_ld16(tA + 128 + cc + 16, b[h ^ 1]);
             }
-        } else if (o.live && p.out_f32) {
-            float* out = static_cast<float*>(p.o) + o.bht * p.dh + cc;
+            float v[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (cc + 4 * i < p.dh)
-                    reinterpret_cast<float4*>(out)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else if (o.live) {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + o.bht * p.dh + cc;
+            for (int i = 0; i < 16; ++i) {
+                v[i] = __uint_as_float(a[h][i]) * o.inv0;
+                if (o.two) v[i] = fmaf(__uint_as_float(b[h][i]), o.inv1, v[i]);
+            }
+            if constexpr (BAD) tc_add_bad<F8>(p, x, bad, o.tok, p.q + at, o.m, o.inv, cc, v);
+            if (!x.w.whole) {
+                if (o.live) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (cc + 8 * i < p.dh)
-                    reinterpret_cast<uint4*>(out)[i] =
-                        make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                                   pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+                    for (int i = 0; i < 16; ++i) part[(cc + i) * 32] = v[i];
+                }
+            } else if (o.live && p.out_f32) {
+                float* out = static_cast<float*>(p.o) + at + cc;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (cc + 4 * i < p.dh)
+                        reinterpret_cast<float4*>(out)[i] =
+                            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            } else if (o.live) {
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + at + cc;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (cc + 8 * i < p.dh)
+                        reinterpret_cast<uint4*>(out)[i] = make_uint4(
+                            pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                            pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+            }
         }
     }
 }
-// The same with the rows that were taken out of the product added; out of line
-// so that its stack does not weigh on the ordinary way.
+// Out of line, so that their registers do not weigh on the softmax loop; the
+// second adds the rows that were taken out of the product.
 template <int D, bool F8>
-__device__ __noinline__ void tc_write_slow(const TreeParams& p, const TcPiece& x, const TcOut& o, uint32_t tA,
+__device__ __noinline__ void tc_write_fast(const TreeParams& p, TcPiece x, TcOut o, uint32_t tA,
+                                           int col0, int col1) {
+    tc_write<D, F8, false>(p, x, o, tA, col0, col1, nullptr);
+}
+template <int D, bool F8>
+__device__ __noinline__ void tc_write_slow(const TreeParams& p, TcPiece x, TcOut o, uint32_t tA,
                                            int col0, int col1, const uint32_t* bad) {
     tc_write<D, F8, true>(p, x, o, tA, col0, col1, bad);
 }
@@ -840,33 +915,34 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
     const int ncols = (p.dh + 15) / 16 * 16;
     const int me = wq * 32 + lane;
     uint32_t cnt_s = 0, cnt_o = 0, cnt_x = 0, tiles = 0;
-    bool ok = true, first_piece = true;
+    uint32_t cnt_q0 = 0, cnt_q1 = 0;  // uses of the Q tiles
+    bool ok = true;
     TreeWalk walk;
     walk.start(bars->range);
     TcPiece x;
-    for (int piece = 0; ok && walk.next(p, x.w); ++piece) {
+    bool more = walk.next(p, x.w);
+    if (more) {
         x.set(p);
-        // this warpgroup's row tile, and this thread's row of it
-        const int row0 = x.pair ? 128 * t : 0;
-        const int rows = min(128, x.rows - row0);
-        const bool active = wq * 32 < rows;  // (warp-uniform)
-        const int row = row0 + min(me, rows - 1);
-        const int r = x.w.rt * kTcRows + row;
-        const int tok = r / p.G;
-        const size_t bht = ((size_t)x.w.b * p.Hq + (size_t)x.w.h * p.G + (r - tok * p.G)) * p.T + tok;
-        if (x.pair || t == 0) {
-            const int tile = x.pair ? t : 0;
-            if (active) tc_load_q<D, F8>(p, bht * p.dh, wq, lane, smem_u32(smem + tile * C::kTile), bars->qs[tile]);
-            if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[tile]));
-        }
+        tc_piece_q<D, F8>(p, x, t, smem, bars);
+    }
+    for (int piece = 0; ok && more; ++piece) {
+        const TcMine my = tc_mine(p, x, t, me);
+        const bool active = wq * 32 < my.rows;  // (warp-uniform)
+        const int q_tile = x.pair ? t : x.q_tile;
         if constexpr (F8) {
-            // in split mode stream 1 reads the factors that stream 0's warps wrote
+            // a split piece's stream 1 reads the factors that stream 0's warps wrote
             if (!x.pair && t == 1) {
-                ok = warp_wait(&bars->q_full[0], (uint32_t)piece, abort_flag);
+                ok = warp_wait(&bars->q_full[q_tile], q_tile ? cnt_q1 : cnt_q0, abort_flag);
                 if (!ok) break;
             }
+            if (x.pair || x.q_tile == 0) ++cnt_q0;
+            if (x.pair || x.q_tile == 1) ++cnt_q1;
         }
-        const float c = F8 ? *((volatile float*)&bars->qs[x.pair ? t : 0][me]) : p.c;
+        const float c = F8 ? *((volatile float*)&bars->qs[q_tile][me]) : p.c;
+        // the row's mask, if it fits in 64 bits (used at the piece's last tiles)
+        uint2 mask = make_uint2(0xFFFFFFFFu, 0xFFFFFFFFu);
+        if (p.mask && p.W == 1 && x.w.k1 * kTcKeys > x.prefix)
+            mask = __ldg(reinterpret_cast<const uint2*>(p.mask + (size_t)x.w.b * p.T + my.tok));
         TcRow st;
         st.m = -INFINITY;
         st.l = st.lx = 0.f;
@@ -891,7 +967,7 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
             if (active) {
                 uint32_t allow[4];
                 if (x.special(j)) {
-                    tc_allow(p, x.w.b, tok, x.w.drafted, (x.w.k0 + j) * kTcKeys - x.prefix, allow);
+                    tc_allow(p, x.w.b, my.tok, x.w.drafted, (x.w.k0 + j) * kTcKeys - x.prefix, mask, allow);
                     tc_softmax_tile<D, F8, true>(tS, tO + 128 * t, kf, wv, fexp, allow, s == 0, c, ncols, st);
                 } else {
                     tc_softmax_tile<D, F8, false>(tS, tO + 128 * t, kf, wv, fexp, allow, s == 0, c, ncols, st);
@@ -911,6 +987,7 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
         }
         if (!ok) break;
         tiles += (uint32_t)x.n;
+        const int next = tc_next_q<D, F8>(p, walk, x, t, smem, bars);
         if (s > 0) {
             ok = warp_wait(&bars->o_full[t], cnt_o++, abort_flag);
             if (!ok) break;
@@ -950,29 +1027,27 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
             col1 = t == 0 ? half : ncols;
             tA = tO;
         }
-        const bool two = !x.pair && x.n > 1;
         const uint32_t* bad = &bars->bad[piece % kBadBufs][0][0];
         uint32_t any_bad = 0u;
         for (int i = 0; i < 4 * (x.n - x.first_special()); ++i) any_bad |= *((const volatile uint32_t*)bad + i);
         if (active) {
-            const size_t place = (size_t)blockIdx.x * 2 + (first_piece ? 0 : 1);
             TcOut o;
-            o.row = row;
-            o.live = me < rows;
-            o.two = two;
+            o.row = my.row;
+            o.live = me < my.rows;
+            o.two = !x.pair && x.n > 1;
             o.inv0 = inv0;
             o.inv1 = inv1;
             o.m = m;
             o.inv = inv_l;
-            o.tok = tok;
-            o.bht = bht;
-            o.place = place;
+            o.tok = my.tok;
+            o.bht = my.bht;
+            o.place = (size_t)blockIdx.x * 2 + (piece == 0 ? 0 : 1);
             if (any_bad) tc_write_slow<D, F8>(p, x, o, tA, col0, col1, bad);
-            else tc_write<D, F8, false>(p, x, o, tA, col0, col1, bad);
-            if (me < rows && (x.pair || t == 0)) {
+            else tc_write_fast<D, F8>(p, x, o, tA, col0, col1);
+            if (o.live && (x.pair || t == 0)) {
                 const float lse2 = lx == 0.f ? -INFINITY : m + log2f(lx);
-                if (!x.w.whole) p.ws_lse[place * kTcRows + row] = lse2;
-                else if (p.lse) p.lse[bht] = lse2 * kTcLn2;
+                if (!x.w.whole) p.ws_lse[o.place * kTcRows + my.row] = lse2;
+                else if (p.lse) p.lse[my.bht] = lse2 * kTcLn2;
             }
         }
         // O, the statistics and the marks are read: the next piece may write them
@@ -984,13 +1059,19 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
             ++cnt_x;
             tc_fence_after();
         }
-        first_piece = false;
+        more = next & 1;
+        if (more) {
+            const TcPiece last = x;
+            walk.next(p, x.w);
+            x.set(p, &last);
+            if (ok && !(next & 2)) tc_piece_q<D, F8>(p, x, t, smem, bars);
+        }
     }
     if (!ok && lane == 0) tc_abort(bars, p.err);
 }
 
 template <int D, bool F8>
-__global__ void __launch_bounds__(TcCfg<D, F8>::kThreads, 1)
+__global__ void __launch_bounds__(kTcThreads, 1)
 attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                     const __grid_constant__ TreeParams p) {
     using C = TcCfg<D, F8>;
@@ -1002,6 +1083,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         return;
     }
     if (threadIdx.x == 64) {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the merge waits by itself)
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&bars->q_full[t]), 4);
             mbar_init(smem_u32(&bars->s_full[t]), 1);
@@ -1009,18 +1091,19 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
             mbar_init(smem_u32(&bars->o_full[t]), 1);
         }
         for (int i = 0; i < 8; ++i) {
-            mbar_init(smem_u32(&bars->full[i]), F8 ? 4 : 1);
-            mbar_init(smem_u32(&bars->empty[i]), 1);
+            mbar_init(smem_u32(&bars->full[i]), F8 ? kTcHelpers : 1);
+            // (bf16: the fixers look at every load, and hold its slot until they have)
+            mbar_init(smem_u32(&bars->empty[i]), F8 ? 1 : 1 + kTcHelpers);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(smem_u32(&bars->raw_full[i]), 1);
-            mbar_init(smem_u32(&bars->raw_empty[i]), 4);
+            mbar_init(smem_u32(&bars->raw_empty[i]), kTcHelpers);
         }
         for (int i = 0; i < kDs; ++i) {
-            mbar_init(smem_u32(&bars->ds_full[i]), 4);
+            mbar_init(smem_u32(&bars->ds_full[i]), kTcHelpers);
             mbar_init(smem_u32(&bars->ds_empty[i]), 8);
         }
-        for (int i = 0; i < kFix; ++i) mbar_init(smem_u32(&bars->fix_full[i]), 2);
+        for (int i = 0; i < kFix; ++i) mbar_init(smem_u32(&bars->fix_full[i]), kTcHelpers);
         mbar_init(smem_u32(&bars->stat), 8);
         mbar_init(smem_u32(&bars->done), 8);
         mbar_init(smem_u32(&bars->drain), 1);
@@ -1040,20 +1123,19 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
     if (warp < 4) {
-        reg_dealloc<C::kRegsControl>();
+        reg_dealloc<kTcRegsControl>();
         if (warp == 0) {
             tc_produce<D, F8>(&tk, &tv, smem, bars, p);
         } else if (warp == 1) {
             tc_mma<D, F8>(smem, bars, tmem, p);
-        } else if constexpr (!F8) {
+        } else if constexpr (F8) {
+            tc_convert<D>(warp - 2, smem, bars, p);
+        } else {
             tc_fix<D>(warp - 2, smem, bars, p);
         }
-    } else if (warp < 12) {
-        reg_alloc<C::kRegsSoftmax>();
+    } else {
+        reg_alloc<kTcRegsSoftmax>();
         tc_softmax<D, F8>((warp - 4) >> 2, warp & 3, lane, smem, bars, tmem, p);
-    } else if constexpr (F8) {
-        reg_dealloc<C::kRegsConvert>();
-        tc_convert<D>(warp - 12, smem, bars, p);
     }
     tc_fence_before();
     __syncthreads();
@@ -1075,7 +1157,7 @@ attn_status_t launch_tc_t(const CUtensorMap& tk, const CUtensorMap& tv, const Tr
             return ATTN_ERR_CUDA;
         if (dev.device < 64) attr_set[dev.device] = 1;
     }
-    attn_tree_tc_kernel<D, F8><<<p.ctas, C::kThreads, C::kSmem, stream>>>(tk, tv, p);
+    attn_tree_tc_kernel<D, F8><<<p.ctas, kTcThreads, C::kSmem, stream>>>(tk, tv, p);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -77,24 +77,16 @@ __device__ __forceinline__ long long warp_sum(long long v) {
     return v;
 }
 
-// Units of the whole batch (a full warp calls).  `report`: record lengths out
-// of range in the error word.
-__device__ __forceinline__ long long tree_total(const TreeParams& p, bool report) {
+// Units of the whole batch, and of the sequences before b (a full warp calls).
+__device__ __forceinline__ long long tree_total_base(const TreeParams& p, int b, long long& base) {
     const int lane = threadIdx.x & 31;
-    long long n = 0;
-    for (int b = lane; b < p.B; b += 32) {
-        const TreeSeq s = tree_seq(p, b);
-        if (s.bad && report) atomicOr(p.err, kErrBadSeqlen);
-        n += tree_units(p, s);
+    long long n = 0, before = 0;
+    for (int i = lane; i < p.B; i += 32) {
+        const long long units = tree_units(p, tree_seq(p, i));
+        n += units;
+        if (i < b) before += units;
     }
-    return warp_sum(n);
-}
-
-// Units of the sequences before b (a full warp calls).
-__device__ __forceinline__ long long tree_base(const TreeParams& p, int b) {
-    const int lane = threadIdx.x & 31;
-    long long n = 0;
-    for (int i = lane; i < b; i += 32) n += tree_units(p, tree_seq(p, i));
+    base = warp_sum(before);
     return warp_sum(n);
 }
 
@@ -116,17 +108,26 @@ struct TreeRange {
 __device__ __forceinline__ TreeRange tree_range(const TreeParams& p, int cta) {
     const int lane = threadIdx.x & 31;
     TreeRange r;
-    const long long total = tree_total(p, cta == 0);
-    const int n = tree_ctas(p, total);
     r.u0 = r.u1 = r.base = 0;
     r.b = 0;
+    // the first 32 sequences' units stay in registers for the second look
+    long long first = 0, sum = 0;
+    for (int b = lane; b < p.B; b += 32) {
+        const TreeSeq s = tree_seq(p, b);
+        if (s.bad && cta == 0) atomicOr(p.err, kErrBadSeqlen);
+        const long long units = tree_units(p, s);
+        if (b < 32) first = units;
+        sum += units;
+    }
+    const long long total = warp_sum(sum);
+    const int n = tree_ctas(p, total);
     if (cta >= n || total == 0) return r;
     r.u0 = tree_first(total, n, cta);
     r.u1 = tree_first(total, n, cta + 1);
     long long base = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
-        const long long mine = b < p.B ? tree_units(p, tree_seq(p, b)) : 0;
+        const long long mine = b0 == 0 ? first : (b < p.B ? tree_units(p, tree_seq(p, b)) : 0);
         long long upto = mine;  // inclusive prefix sum over the lanes
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
