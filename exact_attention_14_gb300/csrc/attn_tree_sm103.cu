@@ -749,9 +749,9 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     }
 }
 
-// A block takes kMergeCols columns for every column lane of the `group_rows`
-// rows of a (sequence, KV head) that lie next to each other in a partial result,
-// and merges the pieces of their item, if it was cut, by log-sum-exp in piece
+// A block takes the `group_rows` rows of a (sequence, KV head) that lie next to
+// each other in a partial result, kMergeCols columns of every column lane at a
+// time (other blocks may take other columns), and merges the pieces of their item, if it was cut, by log-sum-exp in piece
 // order: M = max lse_p, O = sum 2^(lse_p - M) o_p / sum 2^(lse_p - M).  Rows past
 // the sequence's drafted tokens get O = 0, LSE = -inf.  It is short and all
 // latency, so every load of a step is in flight at once; it starts while the
@@ -805,53 +805,55 @@ attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
     if (cut)
         for (int i = 0; i < pieces; ++i) sum += ex2(s_w[i * gr + row] - Ms);
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-    const int col0 = blockIdx.y * lanes * kMergeCols;  // this block's columns: col0 + lane + k * lanes
-    float acc[kMergeCols];
-#pragma unroll
-    for (int k = 0; k < kMergeCols; ++k) acc[k] = 0.f;
-    if (cut) {
-        const float* src = p.ws_o + (size_t)in_tile * p.dw + (size_t)(col0 + lane) * gr + row;
-        for (int i0 = 0; i0 < pieces; i0 += kMergePieces) {
-            float v[kMergePieces][kMergeCols];
-#pragma unroll
-            for (int i = 0; i < kMergePieces; ++i)
-#pragma unroll
-                for (int k = 0; k < kMergeCols; ++k)
-                    v[i][k] = i0 + i < pieces
-                                  ? __ldcg(src + place(i0 + i) * p.tile_rows * p.dw + (size_t)k * lanes * gr)
-                                  : 0.f;
-#pragma unroll
-            for (int i = 0; i < kMergePieces; ++i) {
-                const float wt = i0 + i < pieces ? ex2(s_w[(i0 + i) * gr + row] - Ms) : 0.f;
-#pragma unroll
-                for (int k = 0; k < kMergeCols; ++k) acc[k] = fmaf(wt, v[i][k], acc[k]);
-            }
-        }
-    }
-    const int cols = lanes * kMergeCols;
-#pragma unroll
-    for (int k = 0; k < kMergeCols; ++k) s_o[row * cols + lane + k * lanes] = acc[k] * inv;
     if (blockIdx.y == 0 && threadIdx.x < gr && row < rows && p.lse && (cut || r0 + row >= live)) {
         const int r = r0 + row, t = r / p.G;
         p.lse[((size_t)b * p.Hq + (size_t)h * p.G + (r - t * p.G)) * p.T + t] =
             sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2t;
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < rows * (cols / 8); i += kMergeThreads) {
-        const int ro = i / (cols / 8), cc = 8 * (i - ro * (cols / 8)), col = col0 + cc;
-        const int r = r0 + ro, t = r / p.G;
-        if (col >= p.dh || (whole && r < live)) continue;
-        const size_t at = (((size_t)b * p.Hq + (size_t)h * p.G + (r - t * p.G)) * p.T + t) * p.dh + col;
-        const float4 x = *reinterpret_cast<const float4*>(&s_o[ro * cols + cc]);
-        const float4 y = *reinterpret_cast<const float4*>(&s_o[ro * cols + cc + 4]);
-        if (p.out_f32) {
-            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.o) + at);
-            o[0] = x;
-            o[1] = y;
-        } else {
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at) =
-                make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y),
-                           pack_bf16x2(y.z, y.w));
+    const int cols = lanes * kMergeCols;  // at a time: col0 + lane + k * lanes
+    for (int col0 = blockIdx.y * cols; col0 < p.dh; col0 += gridDim.y * cols) {
+        float acc[kMergeCols];
+#pragma unroll
+        for (int k = 0; k < kMergeCols; ++k) acc[k] = 0.f;
+        if (cut) {
+            const float* src = p.ws_o + (size_t)in_tile * p.dw + (size_t)(col0 + lane) * gr + row;
+            for (int i0 = 0; i0 < pieces; i0 += kMergePieces) {
+                float v[kMergePieces][kMergeCols];
+#pragma unroll
+                for (int i = 0; i < kMergePieces; ++i)
+#pragma unroll
+                    for (int k = 0; k < kMergeCols; ++k)
+                        v[i][k] = i0 + i < pieces
+                                      ? __ldcg(src + place(i0 + i) * p.tile_rows * p.dw + (size_t)k * lanes * gr)
+                                      : 0.f;
+#pragma unroll
+                for (int i = 0; i < kMergePieces; ++i) {
+                    const float wt = i0 + i < pieces ? ex2(s_w[(i0 + i) * gr + row] - Ms) : 0.f;
+#pragma unroll
+                    for (int k = 0; k < kMergeCols; ++k) acc[k] = fmaf(wt, v[i][k], acc[k]);
+                }
+            }
+        }
+        __syncthreads();  // (the last columns have been read)
+#pragma unroll
+        for (int k = 0; k < kMergeCols; ++k) s_o[row * cols + lane + k * lanes] = acc[k] * inv;
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows * (cols / 8); i += kMergeThreads) {
+            const int ro = i / (cols / 8), cc = 8 * (i - ro * (cols / 8)), col = col0 + cc;
+            const int r = r0 + ro, t = r / p.G;
+            if (col >= p.dh || (whole && r < live)) continue;
+            const size_t at = (((size_t)b * p.Hq + (size_t)h * p.G + (r - t * p.G)) * p.T + t) * p.dh + col;
+            const float4 x = *reinterpret_cast<const float4*>(&s_o[ro * cols + cc]);
+            const float4 y = *reinterpret_cast<const float4*>(&s_o[ro * cols + cc + 4]);
+            if (p.out_f32) {
+                float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.o) + at);
+                o[0] = x;
+                o[1] = y;
+            } else {
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at) =
+                    make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y),
+                               pack_bf16x2(y.z, y.w));
+            }
         }
     }
 }
@@ -892,12 +894,16 @@ size_t align16(size_t x) { return (x + 15) & ~size_t(15); }
 
 attn_status_t launch_tree_merge(const TreeParams& p, cudaStream_t stream) {
     const int cols = kMergeThreads / p.group_rows * kMergeCols;  // of a block
-    const long long groups = (p.T * p.G + p.group_rows - 1) / p.group_rows;
+    const long long groups = (long long)p.B * p.Hkv * ((p.T * p.G + p.group_rows - 1) / p.group_rows);
+    // columns over several blocks where the rows alone are few (latency), not
+    // where they fill the GPU (each block finds its item's pieces anew)
+    const int most = (p.dh + cols - 1) / cols;
+    const long long split = 1024 / groups;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hkv * groups), (unsigned)((p.dh + cols - 1) / cols));
+    cfg.gridDim = dim3((unsigned)groups, (unsigned)(split < 1 ? 1 : (split > most ? most : split)));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = (size_t)p.ctas * p.group_rows * 4;  // (at most as many pieces as CTAs)
     cfg.stream = stream;

@@ -62,7 +62,6 @@ constexpr int kTcRegsControl = 104, kTcRegsSoftmax = 200;
 static_assert(128 * kTcRegsControl + 256 * kTcRegsSoftmax <= kTcThreads * 168, "register split");
 constexpr int kTcHelpers = 2;  // warps 2-3: V's fixers (bf16) or the converters (E4M3)
 
-constexpr int kFix = 8;        // special tiles between the fixer and its readers
 // Marks of the V rows that were taken out: for each of the last pieces, for
 // each of its special tiles (1024 drafted tokens reach over 10 at most), a bit
 // per key.  A writer is at most 4 pieces ahead of the readers (a piece takes two
@@ -76,11 +75,12 @@ struct TcBars {
     uint64_t full[8], empty[8];       // operand tiles
     uint64_t raw_full[4], raw_empty[4];
     uint64_t ds_full[kDs], ds_empty[kDs];
-    uint64_t fix_full[kFix];
+    uint64_t fix_ask, fix_done;       // V of a special tile is there / is prepared
     uint64_t stat, done, drain;
     TreeRange range;
     uint32_t tmem_base;
     int abort;
+    int fix_slot;
     uint32_t bad[kBadBufs][kBadTiles][4];
     float qs[2][128];                   // E4M3: what a row's products are multiplied with
     float m[2][128], l[2][128], lx[2][128];
@@ -121,19 +121,16 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
 }
 
 // A piece's streams.  Tile s of stream t is key tile k0 + (pair ? s : 2 s + t).
-// Q lies in shared-memory tile t of a pair; split pieces that follow one another
-// change tiles, so that one's Q can be laid out while the other still runs.
+// Q lies in shared-memory tile t of a pair, in tile 0 of a split piece.
 struct TcPiece {
     TreePiece w;
     int rows, n, prefix;
-    int q_tile;  // split: the tile that holds Q
     bool pair;
-    __device__ __forceinline__ void set(const TreeParams& p, const TcPiece* before = nullptr) {
+    __device__ __forceinline__ void set(const TreeParams& p) {
         rows = min(kTcRows, w.drafted * p.G - w.rt * kTcRows);
         n = w.k1 - w.k0;
         prefix = w.keys - w.drafted;
         pair = rows > 128;
-        q_tile = before && !before->pair ? before->q_tile ^ 1 : 0;
     }
     __device__ __forceinline__ int tile(int s, int t) const { return pair ? s : 2 * s + t; }
     __device__ __forceinline__ bool has(int s, int t) const { return tile(s, t) < n; }
@@ -247,16 +244,16 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
     };
     TreeWalk walk;
     walk.start(bars->range);
-    TcPiece x, last;
-    for (int piece = 0; ok && walk.next(p, x.w); ++piece, last = x) {
-        x.set(p, piece ? &last : nullptr);
+    TcPiece x;
+    while (ok && walk.next(p, x.w)) {
+        x.set(p);
         const bool pair = x.pair;
         const int n0 = pair ? x.n : (x.n + 1) / 2, n1 = pair ? x.n : x.n / 2;  // tiles of each stream
         uint32_t slot_k = 0, slot_v = 0;
         auto scores = [&](auto T) {
             constexpr int t = decltype(T)::value;
             const uint32_t k_lo = sdesc_lo(ring + slot_k * C::kTile, 16);
-            const uint32_t a_lo = pair ? q_lo[t] : (x.q_tile ? q_lo[1] : q_lo[0]);
+            const uint32_t a_lo = pair ? q_lo[t] : q_lo[0];
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t step = (kk >> 2) * (16384 >> 4) + (kk & 3) * (32 >> 4);
@@ -270,8 +267,7 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
             constexpr int t = decltype(T)::value;
             if ((t == 0 ? n0 : n1) == 0 || !ok) return;
             if (pair || t == 0) {
-                const int q = pair ? t : x.q_tile;
-                ok = warp_wait(&bars->q_full[q], q ? cnt_q[1]++ : cnt_q[0]++, abort_flag);
+                ok = warp_wait(&bars->q_full[t], cnt_q[t]++, abort_flag);
                 if (!ok) return;
                 tc_fence_after();
             }
@@ -285,8 +281,13 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
             if (!pair || t == 0) {
                 slot_v = take();
                 if (!F8 && ok && x.special(x.tile(s, t))) {
-                    ok = warp_wait(&bars->fix_full[cnt_fix % kFix], cnt_fix / kFix, abort_flag);
-                    ++cnt_fix;
+                    // the fixers work on it while this stream's softmax still runs
+                    if (elect_one()) {
+                        *((volatile int*)&bars->fix_slot) = (int)slot_v;
+                        mbar_arrive(smem_u32(&bars->fix_ask));
+                    }
+                    __syncwarp();
+                    ok = warp_wait(&bars->fix_done, cnt_fix++, abort_flag);
                 }
                 if (!ok) return;
             }
@@ -329,61 +330,44 @@ __device__ void tc_fix(int wf, uint8_t* smem, TcBars* bars, const TreeParams& p)
     using C = TcCfg<D, false>;
     const int lane = threadIdx.x & 31;
     const volatile int* abort_flag = &bars->abort;
-    long long seen = 0;
     uint32_t fixed = 0;
     bool ok = true;
     TreeWalk walk;
     walk.start(bars->range);
     TcPiece x;
-    // the next load of the ring (every one is waited for, and its slot not given
-    // back before: a barrier's parity tells only the last phase from the one before)
-    auto next_load = [&]() {
-        const int slot = (int)(seen % C::kStages);
-        ok = warp_wait(&bars->full[slot], (uint32_t)(seen / C::kStages), abort_flag);
-        ++seen;
-        return slot;
-    };
-    auto give = [&](int slot) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->empty[slot]));
-    };
     for (int piece = 0; ok && walk.next(p, x.w); ++piece) {
         x.set(p);
-        const int ahead = x.pair ? 1 : 2;
-        for (int j = 0; j < ahead && j < x.n && ok; ++j) give(next_load());
-        for (int j = 0; j < x.n && ok; ++j) {
-            const int slot = next_load();
-            if (ok && x.special(j)) {
-                const uint32_t tile = smem_u32(smem + C::kRing + slot * C::kTile);
-                uint32_t* marks = bars->bad[piece % kBadBufs][j - x.first_special()];
+        for (int j = x.first_special(); j < x.n && ok; ++j) {
+            // (the issuer has seen the tile's V arrive, and waits for this)
+            ok = warp_wait(&bars->fix_ask, fixed++, abort_flag);
+            if (!ok) break;
+            const uint32_t tile = smem_u32(smem + C::kRing + *((volatile int*)&bars->fix_slot) * C::kTile);
+            uint32_t* marks = bars->bad[piece % kBadBufs][j - x.first_special()];
 #pragma unroll 1
-                for (int i = 0; i < 2; ++i) {
-                    const int row = wf * 64 + i * 32 + lane;
-                    const int key = (x.w.k0 + j) * kTcKeys + row;
-                    const uint32_t at = tile + row * 128;
-                    bool bad = false;
-                    if (key >= x.prefix && key < x.w.keys) {
-                        for (int c = 0; c < p.dh / 8; ++c) {
-                            const uint4 v = tc_lds128(at + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4));
-                            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            for (int i = 0; i < 2; ++i) {
+                const int row = wf * 64 + i * 32 + lane;
+                const int key = (x.w.k0 + j) * kTcKeys + row;
+                const uint32_t at = tile + row * 128;
+                bool bad = false;
+                if (key >= x.prefix && key < x.w.keys) {
+#pragma unroll 4
+                    for (int c = 0; c < p.dh / 8; ++c) {
+                        const uint4 v = tc_lds128(at + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4));
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                bad |= (u[e] & 0x7F80u) == 0x7F80u || (u[e] & 0x7F800000u) == 0x7F800000u;
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            bad |= (u[e] & 0x7F80u) == 0x7F80u || (u[e] & 0x7F800000u) == 0x7F800000u;
                     }
-                    const uint32_t votes = __ballot_sync(0xFFFFFFFFu, bad);
-                    if (lane == 0) marks[2 * wf + i] = votes;
-                    if (bad || key >= x.w.keys)
-                        for (int c = 0; c < D / 8; ++c)
-                            sts128(at + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4), 0u, 0u, 0u, 0u);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->fix_full[fixed % kFix]));
-                ++fixed;
+                const uint32_t votes = __ballot_sync(0xFFFFFFFFu, bad);
+                if (lane == 0) marks[2 * wf + i] = votes;
+                if (bad || key >= x.w.keys)
+                    for (int c = 0; c < D / 8; ++c)
+                        sts128(at + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4), 0u, 0u, 0u, 0u);
             }
-            give(slot);
-            if (ok && j + ahead < x.n) give(next_load());
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->fix_done));
         }
     }
     if (!ok && lane == 0) tc_abort(bars, p.err);
@@ -761,31 +745,35 @@ __device__ __forceinline__ void tc_load_q(const TreeParams& p, size_t row_at, in
     const int c = lane % kLanes;
     const bool in = 8 * c < p.dh;
     const __nv_bfloat16* q = p.q + (in ? 8 * c : 0);
-    uint4 v[32 / kPer];
+#pragma unroll 1
+    for (int i0 = 0; i0 < 32 / kPer; i0 += 8) {  // eight loads of a lane in flight
+        uint4 v[8];
 #pragma unroll
-    for (int i = 0; i < 32 / kPer; ++i) {
-        const size_t at = __shfl_sync(0xFFFFFFFFu, (unsigned long long)row_at, i * kPer + lane / kLanes);
-        v[i] = __ldg(reinterpret_cast<const uint4*>(q + at));
-    }
-#pragma unroll
-    for (int i = 0; i < 32 / kPer; ++i) {
-        const int row = wq * 32 + i * kPer + lane / kLanes;
-        uint32_t w[4] = {in ? v[i].x : 0u, in ? v[i].y : 0u, in ? v[i].z : 0u, in ? v[i].w : 0u};
-        if constexpr (F8) {
-            float mx = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16lo_to_f32(w[e])), fabsf(bf16hi_to_f32(w[e]))));
-#pragma unroll
-            for (int off = kLanes / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-            // a power of two that puts the row's largest value in [2^14, 2^15)
-            int e = (int)(__float_as_uint(mx) >> 23) - 127;
-            e = e < -100 ? -100 : (e > 126 ? 126 : e);
-            const float up = tc_pow2(14 - e);
-            if (c == 0) qs[row] = p.c * tc_pow2(e - 14);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = tc_pack_f16(bf16lo_to_f32(w[k]) * up, bf16hi_to_f32(w[k]) * up);
+        for (int i = 0; i < 8; ++i) {
+            const size_t at = __shfl_sync(0xFFFFFFFFu, (unsigned long long)row_at, (i0 + i) * kPer + lane / kLanes);
+            v[i] = __ldg(reinterpret_cast<const uint4*>(q + at));
         }
-        sts128(tile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = wq * 32 + (i0 + i) * kPer + lane / kLanes;
+            uint32_t w[4] = {in ? v[i].x : 0u, in ? v[i].y : 0u, in ? v[i].z : 0u, in ? v[i].w : 0u};
+            if constexpr (F8) {
+                float mx = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    mx = fmaxf(mx, fmaxf(fabsf(bf16lo_to_f32(w[e])), fabsf(bf16hi_to_f32(w[e]))));
+#pragma unroll
+                for (int off = kLanes / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
+                // a power of two that puts the row's largest value in [2^14, 2^15)
+                int e = (int)(__float_as_uint(mx) >> 23) - 127;
+                e = e < -100 ? -100 : (e > 126 ? 126 : e);
+                const float up = tc_pow2(14 - e);
+                if (c == 0) qs[row] = p.c * tc_pow2(e - 14);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = tc_pack_f16(bf16lo_to_f32(w[k]) * up, bf16hi_to_f32(w[k]) * up);
+            }
+            sts128(tile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+        }
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -807,30 +795,6 @@ __device__ __forceinline__ TcMine tc_mine(const TreeParams& p, const TcPiece& x,
     a.bht = ((size_t)x.w.b * p.Hq + (size_t)x.w.h * p.G + (r - a.tok * p.G)) * p.T + a.tok;
     return a;
 }
-// Lays out a piece's Q (out of line: its loads all want a register).
-template <int D, bool F8>
-__device__ __noinline__ void tc_piece_q(const TreeParams& p, TcPiece x, int t, uint8_t* smem, TcBars* bars) {
-    using C = TcCfg<D, F8>;
-    if (!x.pair && t == 1) return;  // stream 0's warps lay out a split piece's Q
-    const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-    const int tile = x.pair ? t : x.q_tile;
-    const TcMine a = tc_mine(p, x, t, wq * 32 + lane);
-    if (wq * 32 < a.rows) tc_load_q<D, F8>(p, a.bht * p.dh, wq, lane, smem_u32(smem + tile * C::kTile), bars->qs[tile]);
-    if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[tile]));
-}
-// The next piece's Q, where its tile is free already: a pair's own tile once its
-// last scores are there, a split piece's other tile at any time.  Returns bit 0:
-// there is a next piece, bit 1: its Q is laid out.
-template <int D, bool F8>
-__device__ __noinline__ int tc_next_q(const TreeParams& p, TreeWalk walk, TcPiece x, int t, uint8_t* smem, TcBars* bars) {
-    TcPiece y;
-    if (!walk.next(p, y.w)) return 0;
-    y.set(p, &x);
-    if (!x.pair && y.pair) return 1;
-    tc_piece_q<D, F8>(p, y, t, smem, bars);
-    return 3;
-}
-
 // What a thread needs to write its row.
 struct TcOut {
     int row, tok;      // row of the item, its drafted token
@@ -847,58 +811,43 @@ __device__ __forceinline__ void tc_write(const TreeParams& p, const TcPiece& x, 
                                          int col1, const uint32_t* bad) {
     float* part = p.ws_o + (o.place * kTcRows + (o.row & ~31)) * p.dw + (threadIdx.x & 31);
     const size_t at = o.bht * p.dh;
-    uint32_t a[2][16], b[2][16];
-    tc_ld16(tA + col0, a[0]);
-    if (o.two) tc_ld16(tA + 128 + col0, b[0]);
 #pragma unroll 1
-    for (int c2 = col0; c2 < col1; c2 += 32) {
+    for (int cc = col0; cc < col1; cc += 16) {
+        uint32_t a[16], b[16];
+        tc_ld16(tA + cc, a);
+        if (o.two) tc_ld16(tA + 128 + cc, b);
+        tmem_wait_ld();
+        float v[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int cc = c2 + 16 * h;
-            if (cc >= col1) break;
-            tmem_wait_ld();
-            if (cc + 16 < col1) {  // the next 16 columns are on their way meanwhile
-                tc_ld16(tA + cc + 16, a[h ^ 1]);
-                if (o.two) tc_ld16(tA + 128 + cc + 16, b[h ^ 1]);
+        for (int i = 0; i < 16; ++i) {
+            v[i] = __uint_as_float(a[i]) * o.inv0;
+            if (o.two) v[i] = fmaf(__uint_as_float(b[i]), o.inv1, v[i]);
+        }
+        if constexpr (BAD) tc_add_bad<F8>(p, x, bad, o.tok, p.q + at, o.m, o.inv, cc, v);
+        if (!x.w.whole) {
+            if (o.live) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) part[(cc + i) * 32] = v[i];
             }
-            float v[16];
+        } else if (o.live && p.out_f32) {
+            float* out = static_cast<float*>(p.o) + at + cc;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                v[i] = __uint_as_float(a[h][i]) * o.inv0;
-                if (o.two) v[i] = fmaf(__uint_as_float(b[h][i]), o.inv1, v[i]);
-            }
-            if constexpr (BAD) tc_add_bad<F8>(p, x, bad, o.tok, p.q + at, o.m, o.inv, cc, v);
-            if (!x.w.whole) {
-                if (o.live) {
+            for (int i = 0; i < 4; ++i)
+                if (cc + 4 * i < p.dh)
+                    reinterpret_cast<float4*>(out)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else if (o.live) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + at + cc;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) part[(cc + i) * 32] = v[i];
-                }
-            } else if (o.live && p.out_f32) {
-                float* out = static_cast<float*>(p.o) + at + cc;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (cc + 4 * i < p.dh)
-                        reinterpret_cast<float4*>(out)[i] =
-                            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            } else if (o.live) {
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + at + cc;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (cc + 8 * i < p.dh)
-                        reinterpret_cast<uint4*>(out)[i] = make_uint4(
-                            pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                            pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
-            }
+            for (int i = 0; i < 2; ++i)
+                if (cc + 8 * i < p.dh)
+                    reinterpret_cast<uint4*>(out)[i] =
+                        make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                   pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
         }
     }
 }
-// Out of line, so that their registers do not weigh on the softmax loop; the
-// second adds the rows that were taken out of the product.
-template <int D, bool F8>
-__device__ __noinline__ void tc_write_fast(const TreeParams& p, TcPiece x, TcOut o, uint32_t tA,
-                                           int col0, int col1) {
-    tc_write<D, F8, false>(p, x, o, tA, col0, col1, nullptr);
-}
+// The same with the rows that were taken out of the product added; out of line
+// so that its stack does not weigh on the ordinary way.
 template <int D, bool F8>
 __device__ __noinline__ void tc_write_slow(const TreeParams& p, TcPiece x, TcOut o, uint32_t tA,
                                            int col0, int col1, const uint32_t* bad) {
@@ -915,30 +864,26 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
     const int ncols = (p.dh + 15) / 16 * 16;
     const int me = wq * 32 + lane;
     uint32_t cnt_s = 0, cnt_o = 0, cnt_x = 0, tiles = 0;
-    uint32_t cnt_q0 = 0, cnt_q1 = 0;  // uses of the Q tiles
     bool ok = true;
     TreeWalk walk;
     walk.start(bars->range);
     TcPiece x;
-    bool more = walk.next(p, x.w);
-    if (more) {
+    for (int piece = 0; ok && walk.next(p, x.w); ++piece) {
         x.set(p);
-        tc_piece_q<D, F8>(p, x, t, smem, bars);
-    }
-    for (int piece = 0; ok && more; ++piece) {
         const TcMine my = tc_mine(p, x, t, me);
         const bool active = wq * 32 < my.rows;  // (warp-uniform)
-        const int q_tile = x.pair ? t : x.q_tile;
+        if (x.pair || t == 0) {  // (stream 0's warps lay out a split piece's Q)
+            if (active) tc_load_q<D, F8>(p, my.bht * p.dh, wq, lane, smem_u32(smem + t * C::kTile), bars->qs[t]);
+            if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[t]));
+        }
         if constexpr (F8) {
             // a split piece's stream 1 reads the factors that stream 0's warps wrote
             if (!x.pair && t == 1) {
-                ok = warp_wait(&bars->q_full[q_tile], q_tile ? cnt_q1 : cnt_q0, abort_flag);
+                ok = warp_wait(&bars->q_full[0], (uint32_t)piece, abort_flag);
                 if (!ok) break;
             }
-            if (x.pair || x.q_tile == 0) ++cnt_q0;
-            if (x.pair || x.q_tile == 1) ++cnt_q1;
         }
-        const float c = F8 ? *((volatile float*)&bars->qs[q_tile][me]) : p.c;
+        const float c = F8 ? *((volatile float*)&bars->qs[x.pair ? t : 0][me]) : p.c;
         // the row's mask, if it fits in 64 bits (used at the piece's last tiles)
         uint2 mask = make_uint2(0xFFFFFFFFu, 0xFFFFFFFFu);
         if (p.mask && p.W == 1 && x.w.k1 * kTcKeys > x.prefix)
@@ -987,7 +932,6 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
         }
         if (!ok) break;
         tiles += (uint32_t)x.n;
-        const int next = tc_next_q<D, F8>(p, walk, x, t, smem, bars);
         if (s > 0) {
             ok = warp_wait(&bars->o_full[t], cnt_o++, abort_flag);
             if (!ok) break;
@@ -1043,7 +987,7 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
             o.bht = my.bht;
             o.place = (size_t)blockIdx.x * 2 + (piece == 0 ? 0 : 1);
             if (any_bad) tc_write_slow<D, F8>(p, x, o, tA, col0, col1, bad);
-            else tc_write_fast<D, F8>(p, x, o, tA, col0, col1);
+            else tc_write<D, F8, false>(p, x, o, tA, col0, col1, bad);
             if (o.live && (x.pair || t == 0)) {
                 const float lse2 = lx == 0.f ? -INFINITY : m + log2f(lx);
                 if (!x.w.whole) p.ws_lse[o.place * kTcRows + my.row] = lse2;
@@ -1058,13 +1002,6 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
             ok = warp_wait(&bars->done, cnt_x, abort_flag);
             ++cnt_x;
             tc_fence_after();
-        }
-        more = next & 1;
-        if (more) {
-            const TcPiece last = x;
-            walk.next(p, x.w);
-            x.set(p, &last);
-            if (ok && !(next & 2)) tc_piece_q<D, F8>(p, x, t, smem, bars);
         }
     }
     if (!ok && lane == 0) tc_abort(bars, p.err);
@@ -1092,8 +1029,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         }
         for (int i = 0; i < 8; ++i) {
             mbar_init(smem_u32(&bars->full[i]), F8 ? kTcHelpers : 1);
-            // (bf16: the fixers look at every load, and hold its slot until they have)
-            mbar_init(smem_u32(&bars->empty[i]), F8 ? 1 : 1 + kTcHelpers);
+            mbar_init(smem_u32(&bars->empty[i]), 1);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(smem_u32(&bars->raw_full[i]), 1);
@@ -1103,7 +1039,8 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
             mbar_init(smem_u32(&bars->ds_full[i]), kTcHelpers);
             mbar_init(smem_u32(&bars->ds_empty[i]), 8);
         }
-        for (int i = 0; i < kFix; ++i) mbar_init(smem_u32(&bars->fix_full[i]), kTcHelpers);
+        mbar_init(smem_u32(&bars->fix_ask), 1);
+        mbar_init(smem_u32(&bars->fix_done), kTcHelpers);
         mbar_init(smem_u32(&bars->stat), 8);
         mbar_init(smem_u32(&bars->done), 8);
         mbar_init(smem_u32(&bars->drain), 1);
