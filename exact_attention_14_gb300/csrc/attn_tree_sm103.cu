@@ -47,6 +47,7 @@ constexpr int kConsumers = 4;
 constexpr int kTreeThreads = (kConsumers + 1) * 32;
 constexpr int kTileKeys = 64;
 constexpr int kMaxRows = 16;
+constexpr int kExtraUnits = 2;  // an item's start and end, in 64-key tiles
 constexpr float kLn2t = 0.69314718055994530942f;
 constexpr float kLog2et = 1.44269504088896340736f;
 constexpr float kPFrame = 32768.0f;  // E4M3: P is held times 2^15 / F
@@ -408,6 +409,18 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 #pragma unroll
                         for (int e = 0; e < 4; ++e) sf[nt][e] += s2[nt][e];
                 }
+                // E4M3: V's codes are on their way while the softmax runs
+                uint4 vr[F8 ? D / 128 : 1][4];
+                auto load_v = [&]() {
+                    if constexpr (F8) {
+#pragma unroll
+                        for (int hf = 0; hf < D / 128; ++hf)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                vr[hf][i] = lds128(sV + tile_off(wk0 + qc + 4 * i, hf * 8 + v_chunk));
+                    }
+                };
+                if constexpr (D == 128) load_v();
                 // ---- scale, mask, running maximum
                 const bool drafted = key0 + nvalid > prefix;  // some of the keys are drafted tokens
                 float kd[2] = {1.f, 1.f};
@@ -577,6 +590,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     wrote = true;
                     __syncwarp();
                 }
+                if (F8 && (D > 128 || zero)) load_v();
                 // ---- O^T += V^T P^T
                 if constexpr (!F8) {
 #pragma unroll
@@ -590,10 +604,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     // P's k index 2 qc + {0, 1, 8, 9} is key qc + {0, 4, 8, 12}
 #pragma unroll
                     for (int hf = 0; hf < D / 128; ++hf) {
-                        const uint4 r0 = lds128(sV + tile_off(wk0 + qc, hf * 8 + v_chunk));
-                        const uint4 r1 = lds128(sV + tile_off(wk0 + qc + 4, hf * 8 + v_chunk));
-                        const uint4 r2 = lds128(sV + tile_off(wk0 + qc + 8, hf * 8 + v_chunk));
-                        const uint4 r3 = lds128(sV + tile_off(wk0 + qc + 12, hf * 8 + v_chunk));
+                        const uint4 r0 = vr[hf][0], r1 = vr[hf][1], r2 = vr[hf][2], r3 = vr[hf][3];
                         const uint32_t a0[4] = {r0.x, r0.y, r0.z, r0.w}, a1[4] = {r1.x, r1.y, r1.z, r1.w};
                         const uint32_t a2[4] = {r2.x, r2.y, r2.z, r2.w}, a3[4] = {r3.x, r3.y, r3.z, r3.w};
 #pragma unroll
@@ -777,10 +788,10 @@ attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
     if (r0 < live) {
         total = tree_total_base(p, b, start);
         n = tree_ctas(p, total);
-        start += ((long long)h * s.row_tiles + r0 / p.tile_rows) * s.key_tiles;
-        const long long last = start + s.key_tiles - 1;
-        c0 = (int)(start * n / total);
-        while (c0 + 1 < n && tree_first(total, n, c0 + 1) <= start) ++c0;
+        start += ((long long)h * s.row_tiles + r0 / p.tile_rows) * (s.key_tiles + p.extra);
+        const long long first = start + p.extra, last = first + s.key_tiles - 1;  // of its key tiles
+        c0 = (int)(first * n / total);
+        while (c0 + 1 < n && tree_first(total, n, c0 + 1) <= first) ++c0;
         c1 = (int)(last * n / total);
         while (c1 + 1 < n && tree_first(total, n, c1 + 1) <= last) ++c1;
     }
@@ -790,7 +801,8 @@ attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
     if (whole && r0 + rows <= live) return;
     const int row = threadIdx.x % gr, lane = threadIdx.x / gr, lanes = kMergeThreads / gr;
     const int in_tile = r0 % p.tile_rows;  // of the group's first row
-    // only the first piece can be its CTA's last one (place 2c + 1)
+    // only the first piece can be its CTA's last one (place 2c + 1): that CTA has
+    // a key tile of the item before
     const int first_place = 2 * c0 + (start > tree_first(total, n, c0) ? 1 : 0);
     const int pieces = whole ? 0 : c1 - c0 + 1;
     auto place = [&](int i) { return (size_t)(i == 0 ? first_place : 2 * (c0 + i)); };
@@ -922,6 +934,7 @@ static void tree_shape(TreeParams& p, int rows, bool f8, int num_sms) {
     }
     p.tile_keys = kTileKeys;
     p.min_units = 2;
+    p.extra = kExtraUnits;
     tree_variant(p.dh, f8, rows, [&](auto D, auto F8, auto NT) {
         using C = TreeCfg<decltype(D)::value, decltype(F8)::value, decltype(NT)::value>;
         p.tile_rows = p.group_rows = C::kRows;

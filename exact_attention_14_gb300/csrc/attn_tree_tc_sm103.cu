@@ -112,9 +112,6 @@ __device__ __forceinline__ uint4 tc_lds128(uint32_t a) {
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
     return v;
 }
-__device__ __forceinline__ void tc_lds_2x64(uint32_t a, uint64_t& x, uint64_t& y) {
-    asm volatile("ld.shared.v2.b64 {%0,%1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
-}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort_flag,
                                           int polls = 0) {
     return __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(bar), parity & 1u, abort_flag, polls));
@@ -570,20 +567,19 @@ struct TcRow {
 
 // Half a tile of this row's scores, columns [64 H, 64 H + 64).
 template <bool F8, bool MASKED, int H>
-__device__ __forceinline__ void tc_half(uint32_t tS, uint32_t kf, const uint32_t (&allow)[4], uint32_t (&sr)[64]) {
+__device__ __forceinline__ void tc_half(uint32_t tS, const float* kf, const uint32_t (&allow)[4], uint32_t (&sr)[64]) {
     tmem_ld32(tS + 64 * H, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
     tmem_ld32(tS + 64 * H + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
     tmem_wait_ld();
     if constexpr (F8) {
 #pragma unroll
         for (int i = 0; i < 64; i += 4) {
-            uint64_t a, b;
+            const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(kf + 64 * H + i);
             float u, v;
-            tc_lds_2x64(kf + (64 * H + i) * 4, a, b);
-            f2_split(f2_mul(f2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), a), u, v);
+            f2_split(f2_mul(f2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), k.x), u, v);
             sr[i] = __float_as_uint(u);
             sr[i + 1] = __float_as_uint(v);
-            f2_split(f2_mul(f2(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])), b), u, v);
+            f2_split(f2_mul(f2(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])), k.y), u, v);
             sr[i + 2] = __float_as_uint(u);
             sr[i + 3] = __float_as_uint(v);
         }
@@ -607,7 +603,7 @@ __device__ __forceinline__ float tc_max64(const uint32_t (&sr)[64], float from) 
 }
 // P of half a tile to TMEM (over S's first 64 columns), and its sum.
 template <bool F8, bool MASKED, int H>
-__device__ __forceinline__ float tc_probs(uint32_t tS, uint32_t wv, const uint32_t (&allow)[4],
+__device__ __forceinline__ float tc_probs(uint32_t tS, const float* wv, const uint32_t (&allow)[4],
                                           const uint32_t (&sr)[64], float c, float m) {
     const uint64_t c2 = f2(c, c), nm2 = f2(-m, -m);
     uint64_t s0 = 0, s1 = 0;
@@ -629,10 +625,8 @@ __device__ __forceinline__ float tc_probs(uint32_t tS, uint32_t wv, const uint32
             if (i & 1) s1 = f2_add(s1, pp);
             else s0 = f2_add(s0, pp);
             if constexpr (F8) {
-                uint64_t x, y;
-                tc_lds_2x64(wv + (64 * H + (col & ~3)) * 4, x, y);  // (once for two pairs)
                 float u, v;
-                f2_split(f2_mul(pp, i & 1 ? y : x), u, v);
+                f2_split(f2_mul(pp, *reinterpret_cast<const unsigned long long*>(wv + 64 * H + col)), u, v);
                 pk[i] = tc_pack_f16(u, v);
             } else {
                 pk[i] = pack_bf16x2(p0, p1);
@@ -646,7 +640,7 @@ __device__ __forceinline__ float tc_probs(uint32_t tS, uint32_t wv, const uint32
 }
 
 template <int D, bool F8, bool MASKED>
-__device__ __forceinline__ void tc_softmax_tile(uint32_t tS, uint32_t tO, uint32_t kf, uint32_t wv, int fexp,
+__device__ __forceinline__ void tc_softmax_tile(uint32_t tS, uint32_t tO, const float* kf, const float* wv, int fexp,
                                                 const uint32_t (&allow)[4], bool first, float c, int ncols,
                                                 TcRow& r) {
     uint32_t sr[64];
@@ -898,15 +892,15 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
             ok = warp_wait(&bars->s_full[t], cnt_s++, abort_flag, 32);
             if (!ok) break;
             tc_fence_after();
-            uint32_t kf = 0, wv = 0;
+            const float *kf = nullptr, *wv = nullptr;
             int fexp = 0;
             if constexpr (F8) {
                 const uint32_t g = tiles + (uint32_t)j;
                 const int slot = (int)(g % kDs);
                 ok = warp_wait(&bars->ds_full[slot], g / kDs, abort_flag);
                 if (!ok) break;
-                kf = smem_u32(bars->kf[slot]);
-                wv = smem_u32(bars->wv[slot]);
+                kf = bars->kf[slot];
+                wv = bars->wv[slot];
                 fexp = *((volatile int*)&bars->fexp[slot]);
             }
             if (active) {
@@ -1106,6 +1100,7 @@ void tree_tc_shape(TreeParams& p, bool f8, int num_sms) {
     p.dw = p.dh <= 64 && !f8 ? 64 : 128;
     p.ctas = num_sms;
     p.min_units = 2;
+    p.extra = 6;
     p.group_rows = 32;
 }
 

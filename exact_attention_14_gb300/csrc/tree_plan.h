@@ -2,7 +2,8 @@
 //
 // An item is (sequence b, KV head h, tile of query rows rt); the rows of a
 // (sequence, KV head) are its drafted tokens times the group's heads, row
-// t * G + g.  An item's units are its key tiles.  Items lie one after another
+// t * G + g.  An item's units are its key tiles, after `extra` units that stand
+// for the time its start and end take.  Items lie one after another
 // (b, then h, then rt) and CTA c of n takes the units [c * total / n,
 // (c + 1) * total / n): every CTA has the same number of key tiles to read,
 // whatever the lengths are, and an item is cut only where a CTA's range ends.
@@ -27,7 +28,8 @@ struct TreeParams {
     long long num_blocks;
     int dh;                    // head dim of the tensors
     int ctas;                  // grid size of the attention kernel
-    int min_units;             // key tiles of a CTA, at least
+    int min_units;             // units of a CTA, at least
+    int extra;                 // an item's start and end, in key tiles
     int tile_keys, tile_rows;
     float c;                   // scale * log2(e)
     const int* block_table;
@@ -68,7 +70,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
     return s;
 }
 __device__ __forceinline__ long long tree_units(const TreeParams& p, const TreeSeq& s) {
-    return (long long)p.Hkv * s.row_tiles * s.key_tiles;
+    return s.key_tiles == 0 ? 0 : (long long)p.Hkv * s.row_tiles * (s.key_tiles + p.extra);
 }
 
 __device__ __forceinline__ long long warp_sum(long long v) {
@@ -161,34 +163,39 @@ struct TreeWalk {
         u = r.u0; u1 = r.u1; base = r.base; b = r.b;
     }
     __device__ __forceinline__ bool next(const TreeParams& p, TreePiece& w) {
-        if (u >= u1) return false;
-        TreeSeq s = tree_seq(p, b);
-        long long n = tree_units(p, s);
-        while (u >= base + n) {  // ends: the units sum up to the total
-            base += n;
-            s = tree_seq(p, ++b);
-            n = tree_units(p, s);
+        while (u < u1) {
+            TreeSeq s = tree_seq(p, b);
+            long long n = tree_units(p, s);
+            while (u >= base + n) {  // ends: the units sum up to the total
+                base += n;
+                s = tree_seq(p, ++b);
+                n = tree_units(p, s);
+            }
+            const long long at = u - base;
+            const unsigned len = (unsigned)(s.key_tiles + p.extra);  // units of an item
+            int from, item;
+            if (at <= 0x7FFFFFFFll) {  // (64-bit divisions take hundreds of cycles)
+                item = (int)((unsigned)at / len);
+                from = (int)((unsigned)at - (unsigned)item * len);
+            } else {
+                item = (int)(at / len);
+                from = (int)(at - (long long)item * len);
+            }
+            const long long left = u1 - u;
+            const int to = left < (long long)len - from ? from + (int)left : (int)len;
+            u += to - from;
+            w.k0 = from < p.extra ? 0 : from - p.extra;
+            w.k1 = to < p.extra ? 0 : to - p.extra;
+            if (w.k1 <= w.k0) continue;  // nothing but the item's extra units
+            w.h = (int)((unsigned)item / (unsigned)s.row_tiles);
+            w.rt = item - w.h * s.row_tiles;
+            w.b = b;
+            w.keys = s.keys;
+            w.drafted = s.drafted;
+            w.whole = w.k0 == 0 && w.k1 == s.key_tiles;
+            return true;
         }
-        const long long at = u - base;
-        if (at <= 0x7FFFFFFFll) {  // (64-bit divisions take hundreds of cycles)
-            const unsigned item = (unsigned)at / (unsigned)s.key_tiles;
-            w.k0 = (int)((unsigned)at - item * (unsigned)s.key_tiles);
-            w.h = (int)(item / (unsigned)s.row_tiles);
-            w.rt = (int)(item - (unsigned)w.h * (unsigned)s.row_tiles);
-        } else {
-            const long long item = at / s.key_tiles;
-            w.k0 = (int)(at - item * s.key_tiles);
-            w.h = (int)(item / s.row_tiles);
-            w.rt = (int)(item - (long long)w.h * s.row_tiles);
-        }
-        const long long left = u1 - u;
-        w.k1 = (int)(left < s.key_tiles - w.k0 ? w.k0 + left : s.key_tiles);
-        w.b = b;
-        w.keys = s.keys;
-        w.drafted = s.drafted;
-        w.whole = w.k0 == 0 && w.k1 == s.key_tiles;
-        u += w.k1 - w.k0;
-        return true;
+        return false;
     }
 };
 
