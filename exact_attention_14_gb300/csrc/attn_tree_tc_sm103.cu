@@ -403,14 +403,77 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
         x.set(p);
         int fexp = -100;
         const int ahead = x.pair ? 1 : 2;
-        // one tile of codes; is_v: rows that must not enter the product are zeroed
-        auto convert = [&](int j, bool is_v) {
+        fetch(0);
+        // (one place in the code for every load: its body is long)
+#pragma unroll 1
+        for (int jk = 0, jv = 0; jv < x.n && ok;) {
+            const bool is_v = jk >= x.n || jk >= jv + ahead;
+            const int j = is_v ? jv++ : jk++;
+            if (!is_v) {
+                // ---- the tile's descales
+                const uint32_t slot = tiles % kDs;
+                if (tiles >= kDs) ok = warp_wait(&bars->ds_empty[slot], tiles / kDs - 1u, abort_flag);
+                if (!ok) break;
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool drop = !isfinite(vd[i]) && (x.w.k0 + j) * kTcKeys + 32 * i + lane >= x.prefix;
+                    if (drop) vd[i] = 0.f;  // its row is added apart
+                    top = fmaxf(top, fabsf(vd[i]));
+                }
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+                fexp = max(fexp, min((int)(__float_as_uint(top) >> 23) - 126, 111));
+                const float fr = kTcFrame * tc_pow2(-fexp);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    bars->kf[slot][64 * wc + 32 * i + lane] = kd[i];
+                    bars->wv[slot][64 * wc + 32 * i + lane] = (wc == 0 ? vd[i] : vd[2 + i]) * fr;
+                }
+                if (wc == 0 && lane == 0) bars->fexp[slot] = fexp;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full[slot]));
+                ++tiles;
+                if (j + 1 < x.n) fetch(j + 1);
+            }
+            // ---- the codes
             ok = warp_wait(&bars->raw_full[raw_slot], raw_round, abort_flag);
             if (ok && out_round > 0) ok = warp_wait(&bars->empty[out_slot], out_round - 1u, abort_flag);
-            if (!ok) return;
+            if (!ok) break;
             const uint32_t raw = smem_u32(smem + C::kRaw + raw_slot * C::kRawTile);
             const uint32_t out = smem_u32(smem + C::kRing + out_slot * C::kTile) + (c >> 2) * 16384;
-            const bool check = is_v && x.special(j);
+            if (is_v && x.special(j)) {
+                // rows that must not enter the product become zeros where they lie
+                uint32_t marks[2] = {0u, 0u};
+#pragma unroll 1
+                for (int i = 0; i < 16; ++i) {
+                    const int row = 64 * wc + (lane >> 3) + 4 * i;
+                    const int key = (x.w.k0 + j) * kTcKeys + row;
+                    const uint32_t at = raw + row * 128 + ((c ^ (row & 7)) << 4);
+                    bool hit = false;
+                    if (key >= x.prefix && key < x.w.keys) {
+                        const uint4 v = tc_lds128(at);
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) hit |= ((u[e >> 2] >> (8 * (e & 3))) & 0x7Fu) == 0x7Fu;
+                        if (c == 0) {
+                            int off;
+                            const int page = tree_page(p, x.w.b, key, x.w.keys, off);
+                            if (page >= 0)
+                                hit |= !isfinite(__ldg(p.v_descale + ((long long)page * p.Hkv + x.w.h) * p.page_size + off));
+                        }
+                    }
+                    const unsigned votes = __ballot_sync(0xFFFFFFFFu, hit);
+                    uint32_t m = 0u;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        if ((votes >> (8 * g)) & 0xFFu) m |= 1u << g;
+                    if (i < 8) marks[0] |= m << (4 * i);
+                    else marks[1] |= m << (4 * i - 32);
+                    if (key >= x.w.keys || ((votes >> (lane & 24)) & 0xFFu)) sts128(at, 0u, 0u, 0u, 0u);
+                }
+                if (lane < 2) bars->bad[piece % kBadBufs][j - x.first_special()][2 * wc + lane] = lane ? marks[1] : marks[0];
+            }
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 const int row0 = 64 * wc + 32 * half + (lane >> 3);  // this lane's rows: row0 + 4 i
@@ -418,32 +481,6 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     w[i] = tc_lds128(raw + (row0 + 4 * i) * 128 + ((c ^ ((row0 + 4 * i) & 7)) << 4));
-                if (check) {
-                    uint32_t marks = 0u;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int key = (x.w.k0 + j) * kTcKeys + row0 + 4 * i;
-                        const bool drafted = key >= x.prefix && key < x.w.keys;
-                        bool hit = false;
-                        if (drafted) {
-                            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) hit |= ((u[e >> 2] >> (8 * (e & 3))) & 0x7Fu) == 0x7Fu;
-                            if (c == 0) {
-                                int off;
-                                const int page = tree_page(p, x.w.b, key, x.w.keys, off);
-                                if (page >= 0)
-                                    hit |= !isfinite(__ldg(p.v_descale + ((long long)page * p.Hkv + x.w.h) * p.page_size + off));
-                            }
-                        }
-                        const unsigned votes = __ballot_sync(0xFFFFFFFFu, hit);
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            if ((votes >> (8 * g)) & 0xFFu) marks |= 1u << (4 * i + g);
-                        if (key >= x.w.keys || ((votes >> (lane & 24)) & 0xFFu)) w[i] = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    if (lane == 0) bars->bad[piece % kBadBufs][j - x.first_special()][2 * wc + half] = marks;
-                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int row = row0 + 4 * i;
@@ -473,47 +510,6 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
             if (++out_slot == C::kStages) {
                 out_slot = 0;
                 ++out_round;
-            }
-        };
-        auto descales = [&](int j) {
-            const uint32_t slot = tiles % kDs;
-            if (tiles >= kDs) {
-                ok = warp_wait(&bars->ds_empty[slot], tiles / kDs - 1u, abort_flag);
-                if (!ok) return;
-            }
-            float top = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool drop = !isfinite(vd[i]) && (x.w.k0 + j) * kTcKeys + 32 * i + lane >= x.prefix;
-                if (drop) vd[i] = 0.f;  // its row is added apart
-                top = fmaxf(top, fabsf(vd[i]));
-            }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-            fexp = max(fexp, min((int)(__float_as_uint(top) >> 23) - 126, 111));
-            const float fr = kTcFrame * tc_pow2(-fexp);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                bars->kf[slot][64 * wc + 32 * i + lane] = kd[i];
-                bars->wv[slot][64 * wc + 32 * i + lane] = (wc == 0 ? vd[i] : vd[2 + i]) * fr;
-            }
-            if (wc == 0 && lane == 0) bars->fexp[slot] = fexp;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full[slot]));
-            ++tiles;
-        };
-        fetch(0);
-        for (int j = 0; j < ahead && j < x.n && ok; ++j) {
-            descales(j);
-            if (j + 1 < x.n) fetch(j + 1);
-            if (ok) convert(j, false);
-        }
-        for (int j = 0; j < x.n && ok; ++j) {
-            convert(j, true);
-            if (ok && j + ahead < x.n) {
-                descales(j + ahead);
-                if (j + ahead + 1 < x.n) fetch(j + ahead + 1);
-                if (ok) convert(j + ahead, false);
             }
         }
     }
