@@ -561,16 +561,14 @@ struct TcRow {
     int fexp;        // E4M3: F of what O holds
 };
 
-// Half a tile of this row's scores, columns [64 H, 64 H + 64).
-template <bool F8, bool MASKED, int H>
-__device__ __forceinline__ void tc_half(uint32_t tS, const float* kf, const uint32_t (&allow)[4], uint32_t (&sr)[64]) {
-    tmem_ld32(tS + 64 * H, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-    tmem_ld32(tS + 64 * H + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-    tmem_wait_ld();
+// 32 scores of this row: times K's descales (E4M3), and -inf where `allow` has no
+// bit (`masked`, the same for the warp: some lane's has not).
+template <bool F8>
+__device__ __forceinline__ void tc_scores(uint32_t (&sr)[32], const float* kf, bool masked, uint32_t allow) {
     if constexpr (F8) {
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-            const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(kf + 64 * H + i);
+        for (int i = 0; i < 32; i += 4) {
+            const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(kf + i);
             float u, v;
             f2_split(f2_mul(f2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), k.x), u, v);
             sr[i] = __float_as_uint(u);
@@ -580,71 +578,70 @@ __device__ __forceinline__ void tc_half(uint32_t tS, const float* kf, const uint
             sr[i + 3] = __float_as_uint(v);
         }
     }
-    if constexpr (MASKED) {
+    if (masked) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-            if (!(allow[2 * H + (i >> 5)] >> (i & 31) & 1u)) sr[i] = 0xFF800000u;
+        for (int i = 0; i < 32; ++i)
+            if (!(allow >> i & 1u)) sr[i] = 0xFF800000u;
     }
 }
-__device__ __forceinline__ float tc_max64(const uint32_t (&sr)[64], float from) {
-    float a = from, b = -INFINITY, c = -INFINITY, d = -INFINITY;
+// P of 32 keys to TMEM (16-bit pairs), added to the sums.
+template <bool F8>
+__device__ __forceinline__ void tc_probs(uint32_t tP, const float* wv, const uint32_t (&sr)[32], uint64_t c2,
+                                         uint64_t nm2, uint64_t& s0, uint64_t& s1) {
+    uint32_t pk[16];
 #pragma unroll
-    for (int i = 0; i < 64; i += 8) {
-        a = fmax3(a, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
-        b = fmax3(b, __uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3]));
-        c = fmax3(c, __uint_as_float(sr[i + 4]), __uint_as_float(sr[i + 5]));
-        d = fmax3(d, __uint_as_float(sr[i + 6]), __uint_as_float(sr[i + 7]));
-    }
-    return fmax3(fmaxf(a, b), c, d);
-}
-// P of half a tile to TMEM (over S's first 64 columns), and its sum.
-template <bool F8, bool MASKED, int H>
-__device__ __forceinline__ float tc_probs(uint32_t tS, const float* wv, const uint32_t (&allow)[4],
-                                          const uint32_t (&sr)[64], float c, float m) {
-    const uint64_t c2 = f2(c, c), nm2 = f2(-m, -m);
-    uint64_t s0 = 0, s1 = 0;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int col = 32 * g + 2 * i;
-            float a, b;
-            f2_split(f2_fma(f2(__uint_as_float(sr[col]), __uint_as_float(sr[col + 1])), c2, nm2), a, b);
-            float p0 = ex2(a), p1 = ex2(b);
-            if constexpr (MASKED) {
-                const uint32_t w = allow[2 * H + g];
-                p0 = w >> (2 * i) & 1u ? p0 : 0.f;
-                p1 = w >> (2 * i + 1) & 1u ? p1 : 0.f;
-            }
-            const uint64_t pp = f2(p0, p1);
-            if (i & 1) s1 = f2_add(s1, pp);
-            else s0 = f2_add(s0, pp);
-            if constexpr (F8) {
-                float u, v;
-                f2_split(f2_mul(pp, *reinterpret_cast<const unsigned long long*>(wv + 64 * H + col)), u, v);
-                pk[i] = tc_pack_f16(u, v);
-            } else {
-                pk[i] = pack_bf16x2(p0, p1);
-            }
+    for (int i = 0; i < 16; ++i) {
+        float a, b;
+        f2_split(f2_fma(f2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), c2, nm2), a, b);
+        const float p0 = ex2(a), p1 = ex2(b);
+        const uint64_t pp = f2(p0, p1);
+        if (i & 1) s1 = f2_add(s1, pp);
+        else s0 = f2_add(s0, pp);
+        if constexpr (F8) {
+            float u, v;
+            f2_split(f2_mul(pp, *reinterpret_cast<const unsigned long long*>(wv + 2 * i)), u, v);
+            pk[i] = tc_pack_f16(u, v);
+        } else {
+            pk[i] = pack_bf16x2(p0, p1);
         }
-        tmem_st16(tS + 32 * H + 16 * g, pk);
     }
-    float u, v;
-    f2_split(f2_add(s0, s1), u, v);
-    return u + v;
+    tmem_st16(tP, pk);
 }
 
-template <int D, bool F8, bool MASKED>
+// One 128-key tile of a row: the maximum over all of it, O rescaled if that
+// moved by more than tau (or, E4M3, if F grew), then P over S's first 64 columns
+// (P of keys 32 i .. lies in columns 16 i .., whose scores are read before).
+// The loops stay rolled: unrolled, the instructions of a tile no longer fit the
+// instruction caches and every warp waits for its code (measured: a fifth of all
+// warp cycles; E4M3 softmax 3300 -> see the table beside the kernel).
+template <int D, bool F8>
 __device__ __forceinline__ void tc_softmax_tile(uint32_t tS, uint32_t tO, const float* kf, const float* wv, int fexp,
-                                                const uint32_t (&allow)[4], bool first, float c, int ncols,
-                                                TcRow& r) {
-    uint32_t sr[64];
-    tc_half<F8, MASKED, 1>(tS, kf, allow, sr);
-    float mx = tc_max64(sr, -INFINITY);
-    tc_half<F8, MASKED, 0>(tS, kf, allow, sr);
-    mx = tc_max64(sr, mx);
-    const float mt = MASKED && mx == -INFINITY ? -INFINITY : mx * c;
+                                                bool special, const uint32_t (&allow)[4], bool first, float c,
+                                                int ncols, TcRow& r) {
+    uint32_t a[32], b[32];
+    float mx = -INFINITY;
+    uint32_t w0 = allow[0], w1 = allow[1];
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        tmem_ld32(tS + 64 * h, a);
+        tmem_ld32(tS + 64 * h + 32, b);
+        tmem_wait_ld();
+        tc_scores<F8>(a, kf + 64 * h, special && __any_sync(0xFFFFFFFFu, w0 != 0xFFFFFFFFu), w0);
+        tc_scores<F8>(b, kf + 64 * h + 32, special && __any_sync(0xFFFFFFFFu, w1 != 0xFFFFFFFFu), w1);
+        w0 = allow[2];
+        w1 = allow[3];
+        float m0 = mx, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            m0 = fmax3(m0, __uint_as_float(a[i]), __uint_as_float(a[i + 1]));
+            m1 = fmax3(m1, __uint_as_float(a[i + 2]), __uint_as_float(a[i + 3]));
+            m2 = fmax3(m2, __uint_as_float(b[i]), __uint_as_float(b[i + 1]));
+            m3 = fmax3(m3, __uint_as_float(b[i + 2]), __uint_as_float(b[i + 3]));
+        }
+        mx = fmax3(fmaxf(m0, m1), m2, m3);
+    }
+    tmem_ld32(tS, a);  // the first scores again, on their way during the rest
+    const float mt = mx * c;  // (c > 0)
     const bool need = mt > r.m + kTcTau;
     bool grow = false;
     if constexpr (F8) grow = !first && fexp != r.fexp;
@@ -676,17 +673,33 @@ __device__ __forceinline__ void tc_softmax_tile(uint32_t tS, uint32_t tO, const 
         }
     }
     if constexpr (F8) r.fexp = fexp;
-    const float m = MASKED && r.m == -INFINITY ? 0.f : r.m;
+    const float m = r.m == -INFINITY ? 0.f : r.m;
     if constexpr (!F8) {
         // the tile's largest weight is its rounded P: its error enters l too
-        const float pm = MASKED && mx == -INFINITY ? 0.f : ex2(fmaf(mx, c, -m));
+        const float pm = mx == -INFINITY ? 0.f : ex2(fmaf(mx, c, -m));
         r.l += bf16lo_to_f32(pack_bf16x2(pm, 0.f)) - pm;
     }
-    float sum = tc_probs<F8, MASKED, 0>(tS, wv, allow, sr, c, m);
-    tc_half<F8, MASKED, 1>(tS, kf, allow, sr);
-    sum += tc_probs<F8, MASKED, 1>(tS, wv, allow, sr, c, m);
-    r.l += sum;
-    r.lx += sum;
+    const uint64_t c2 = f2(c, c), nm2 = f2(-m, -m);
+    uint64_t s0 = 0, s1 = 0;
+    w0 = allow[0];
+    w1 = allow[1];
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        tmem_wait_ld();
+        tmem_ld32(tS + 64 * h + 32, b);
+        tc_scores<F8>(a, kf + 64 * h, special && __any_sync(0xFFFFFFFFu, w0 != 0xFFFFFFFFu), w0);
+        tc_probs<F8>(tS + 32 * h, wv + 64 * h, a, c2, nm2, s0, s1);
+        tmem_wait_ld();
+        if (h == 0) tmem_ld32(tS + 64, a);
+        tc_scores<F8>(b, kf + 64 * h + 32, special && __any_sync(0xFFFFFFFFu, w1 != 0xFFFFFFFFu), w1);
+        tc_probs<F8>(tS + 32 * h + 16, wv + 64 * h + 32, b, c2, nm2, s0, s1);
+        w0 = allow[2];
+        w1 = allow[3];
+    }
+    float u, v;
+    f2_split(f2_add(s0, s1), u, v);
+    r.l += u + v;
+    r.lx += u + v;
 }
 
 // Adds the drafted tokens whose V rows were taken out of the product to 16
@@ -873,7 +886,8 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
                 if (!ok) break;
             }
         }
-        const float c = F8 ? *((volatile float*)&bars->qs[x.pair ? t : 0][me]) : p.c;
+        // (above zero, so that a masked -inf stays one)
+        const float c = fmaxf(F8 ? *((volatile float*)&bars->qs[x.pair ? t : 0][me]) : p.c, 1e-37f);
         // the row's mask, if it fits in 64 bits (used at the piece's last tiles)
         uint2 mask = make_uint2(0xFFFFFFFFu, 0xFFFFFFFFu);
         if (p.mask && p.W == 1 && x.w.k1 * kTcKeys > x.prefix)
@@ -900,13 +914,11 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
                 fexp = *((volatile int*)&bars->fexp[slot]);
             }
             if (active) {
-                uint32_t allow[4];
-                if (x.special(j)) {
+                uint32_t allow[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+                const bool special = x.special(j);
+                if (special)
                     tc_allow(p, x.w.b, my.tok, x.w.drafted, (x.w.k0 + j) * kTcKeys - x.prefix, mask, allow);
-                    tc_softmax_tile<D, F8, true>(tS, tO + 128 * t, kf, wv, fexp, allow, s == 0, c, ncols, st);
-                } else {
-                    tc_softmax_tile<D, F8, false>(tS, tO + 128 * t, kf, wv, fexp, allow, s == 0, c, ncols, st);
-                }
+                tc_softmax_tile<D, F8>(tS, tO + 128 * t, kf, wv, fexp, special, allow, s == 0, c, ncols, st);
                 tmem_wait_st();
             }
             tc_fence_before();
