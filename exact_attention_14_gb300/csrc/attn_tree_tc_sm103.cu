@@ -16,8 +16,8 @@
 // evenly spaced in a [B, Hq, T, d] tensor).  bf16 caches: warps 2-3 prepare V
 // in the tiles that hold drafted tokens or the end of the sequence.  E4M3
 // caches: the same two convert every tile from codes to fp16 and prepare V and
-// the descales as they go; Q (scaled by a power of two per row), K, P and V
-// are fp16 operands, exact but for P.
+// the descales as they go; Q (scaled by a power of two per row) and K are exact
+// fp16 operands, P and V (with its descale) rounded ones.
 //
 // Masked places: see attn_tree_sm103.cu.  Here V rows past the sequence, and
 // drafted tokens' V rows with a NaN or an infinity, are zeroed before the
@@ -40,7 +40,10 @@ namespace {
 constexpr int kTcKeys = 128;
 constexpr int kTcRows = 256;
 constexpr float kTcTau = 8.0f;        // rescale threshold (log2 units)
-constexpr float kTcFrame = 128.0f;    // E4M3: P is held times 2^7 / F (P <= 2^8, fp16 < 2^16)
+// E4M3: P and its sums are held times 2^7, so that P, at most 2^(tau + 7), fits
+// fp16 and weights down to 2^-21 of the largest keep its 11 bits
+template <bool F8>
+constexpr float kTcLift = F8 ? 7.0f : 0.0f;
 constexpr float kTcLn2 = 0.69314718055994530942f;
 
 template <int D, bool F8>
@@ -84,9 +87,9 @@ struct TcBars {
     uint32_t bad[kBadBufs][kBadTiles][4];
     float qs[2][128];                   // E4M3: what a row's products are multiplied with
     float m[2][128], l[2][128], lx[2][128];
-    float fin[2];                       // E4M3: F / frame of a stream at the end
+    float fin[2];                       // E4M3: F of a stream at the end
     alignas(16) float kf[kDs][128];     // E4M3: K's descales of a tile
-    alignas(16) float wv[kDs][128];     // E4M3: V's descales times frame / F
+    alignas(16) float wv[kDs][128];     // E4M3: V's descales over F
     int fexp[kDs];
 };
 static_assert(sizeof(TcBars) <= 12 * 1024, "barrier block");
@@ -371,10 +374,10 @@ __device__ void tc_fix(int wf, uint8_t* smem, TcBars* bars, const TreeParams& p)
 }
 
 // ------------------------------------------------------- codes to fp16, E4M3
-// Two warps, 64 keys each.  Eight lanes take a row's 128 codes, 16 each; the two
-// 16-byte results go out in an order that keeps a quarter-warp's stores on
-// different banks.  With K of a tile its descales are laid out for the softmax:
-// K's as they are, V's times frame / F, F = 2^fexp above every one so far.
+// Two warps, 64 keys each.  A lane takes 16 of a row's 128 codes.  V is multiplied with its descale over F, F = 2^fexp above
+// every one so far (two fp16 roundings, of the factor and of the product: less
+// than P's and far less than O's); K's descales, whose rounding would enter the
+// exponent, are left to the softmax.
 template <int D>
 __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams& p) {
     using C = TcCfg<D, true>;
@@ -386,24 +389,36 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
     walk.start(bars->range);
     TcPiece x;
     float kd[2] = {0.f, 0.f}, vd[4] = {0.f, 0.f, 0.f, 0.f};
-    // descales of tile j: K's of keys 64 wc + {0, 32} + lane, V's of keys lane + 32 i
-    auto fetch = [&](int j) {
+    // descales of a tile: K's of keys 64 wc + {0, 32} + lane, V's of keys lane + 32
+    // i; where they lie is looked up a tile earlier still (`at`, -1: no page)
+    long long at[4] = {-1, -1, -1, -1};
+    auto look = [&](int j) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             int off;
             const int page = tree_page(p, x.w.b, (x.w.k0 + j) * kTcKeys + 32 * i + lane, x.w.keys, off);
-            const long long at = ((long long)(page < 0 ? 0 : page) * p.Hkv + x.w.h) * p.page_size + off;
-            vd[i] = page < 0 ? 0.f : __ldg(p.v_descale + at);
-            if ((i >> 1) == wc) kd[i & 1] = page < 0 ? 0.f : __ldg(p.k_descale + at);
+            at[i] = page < 0 ? -1 : ((long long)page * p.Hkv + x.w.h) * p.page_size + off;
+        }
+    };
+    auto fetch = [&]() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            vd[i] = at[i] < 0 ? 0.f : __ldg(p.v_descale + at[i]);
+            if ((i >> 1) == wc) kd[i & 1] = at[i] < 0 ? 0.f : __ldg(p.k_descale + at[i]);
         }
     };
     const int c = lane & 7;
-    const bool upper = c & 4;  // the upper half's lanes write their odd chunk first
+    // lane's row of four, plus 4 i: the lanes of the upper columns take the
+    // neighbour's row, whose swizzle puts their stores on the other banks
+    const int row_in = (lane >> 3) ^ (c >> 2);
+    uint32_t tile_v = 0;       // descale slot of the next V
     for (int piece = 0; ok && walk.next(p, x.w); ++piece) {
         x.set(p);
         int fexp = -100;
         const int ahead = x.pair ? 1 : 2;
-        fetch(0);
+        look(0);
+        fetch();
+        look(1);
         // (one place in the code for every load: its body is long)
 #pragma unroll 1
         for (int jk = 0, jv = 0; jv < x.n && ok;) {
@@ -424,7 +439,7 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
                 fexp = max(fexp, min((int)(__float_as_uint(top) >> 23) - 126, 111));
-                const float fr = kTcFrame * tc_pow2(-fexp);
+                const float fr = tc_pow2(-fexp);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     bars->kf[slot][64 * wc + 32 * i + lane] = kd[i];
@@ -434,7 +449,10 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full[slot]));
                 ++tiles;
-                if (j + 1 < x.n) fetch(j + 1);
+                if (j + 1 < x.n) {
+                    fetch();
+                    look(j + 2);
+                }
             }
             // ---- the codes
             ok = warp_wait(&bars->raw_full[raw_slot], raw_round, abort_flag);
@@ -449,10 +467,10 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
                 for (int i = 0; i < 16; ++i) {
                     const int row = 64 * wc + (lane >> 3) + 4 * i;
                     const int key = (x.w.k0 + j) * kTcKeys + row;
-                    const uint32_t at = raw + row * 128 + ((c ^ (row & 7)) << 4);
+                    const uint32_t piece_at = raw + row * 128 + ((c ^ (row & 7)) << 4);
                     bool hit = false;
                     if (key >= x.prefix && key < x.w.keys) {
-                        const uint4 v = tc_lds128(at);
+                        const uint4 v = tc_lds128(piece_at);
                         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int e = 0; e < 16; ++e) hit |= ((u[e >> 2] >> (8 * (e & 3))) & 0x7Fu) == 0x7Fu;
@@ -470,31 +488,44 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
                         if ((votes >> (8 * g)) & 0xFFu) m |= 1u << g;
                     if (i < 8) marks[0] |= m << (4 * i);
                     else marks[1] |= m << (4 * i - 32);
-                    if (key >= x.w.keys || ((votes >> (lane & 24)) & 0xFFu)) sts128(at, 0u, 0u, 0u, 0u);
+                    if (key >= x.w.keys || ((votes >> (lane & 24)) & 0xFFu)) sts128(piece_at, 0u, 0u, 0u, 0u);
                 }
                 if (lane < 2) bars->bad[piece % kBadBufs][j - x.first_special()][2 * wc + lane] = lane ? marks[1] : marks[0];
+                __syncwarp();  // (other lanes read the rows below)
             }
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
-                const int row0 = 64 * wc + 32 * half + (lane >> 3);  // this lane's rows: row0 + 4 i
+                const int row0 = 64 * wc + 32 * half + row_in;  // this lane's rows: row0 + 4 i
+                // (row & 7 = row_in + 4 (i & 1): two patterns of the swizzle)
+                const uint32_t src[2] = {raw + row0 * 128 + ((c ^ row_in) << 4), raw + row0 * 128 + ((c ^ row_in ^ 4) << 4)};
+                const int ch = 2 * (c & 3);
+                const uint32_t dst[2] = {out + row0 * 128 + ((ch ^ row_in) << 4), out + row0 * 128 + ((ch ^ row_in ^ 4) << 4)};
+                const uint32_t odd = 16 - ((row_in & 1) << 5);  // from an even chunk to its odd neighbour
                 uint4 w[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    w[i] = tc_lds128(raw + (row0 + 4 * i) * 128 + ((c ^ ((row0 + 4 * i) & 7)) << 4));
+                for (int i = 0; i < 8; ++i) w[i] = tc_lds128(src[i & 1] + 512 * i);
+                uint32_t f[8];  // V: its descale over F, twice in fp16
+                if (is_v) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float d = bars->wv[tile_v % kDs][row0 + 4 * i];
+                        f[i] = tc_pack_f16(d, d);
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int row = row0 + 4 * i;
                     uint32_t h[8];
                     tc_e4m3x4(w[i].x, h[0], h[1]);
                     tc_e4m3x4(w[i].y, h[2], h[3]);
                     tc_e4m3x4(w[i].z, h[4], h[5]);
                     tc_e4m3x4(w[i].w, h[6], h[7]);
-                    const uint32_t dst = out + row * 128;
-                    const int ch = 2 * (c & 3) + (upper ? 1 : 0);
-                    sts128(dst + ((ch ^ (row & 7)) << 4), upper ? h[4] : h[0], upper ? h[5] : h[1], upper ? h[6] : h[2],
-                           upper ? h[7] : h[3]);
-                    sts128(dst + (((ch ^ 1) ^ (row & 7)) << 4), upper ? h[0] : h[4], upper ? h[1] : h[5],
-                           upper ? h[2] : h[6], upper ? h[3] : h[7]);
+                    if (is_v) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(f[i]));
+                    }
+                    sts128(dst[i & 1] + 512 * i, h[0], h[1], h[2], h[3]);
+                    sts128(dst[i & 1] + 512 * i + odd, h[4], h[5], h[6], h[7]);
                 }
             }
             fence_proxy_async_smem();
@@ -503,6 +534,7 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
                 mbar_arrive(smem_u32(&bars->full[out_slot]));
                 mbar_arrive(smem_u32(&bars->raw_empty[raw_slot]));
             }
+            if (is_v) ++tile_v;
             if (++raw_slot == C::kRawStages) {
                 raw_slot = 0;
                 ++raw_round;
@@ -557,17 +589,28 @@ __device__ __forceinline__ void tc_ld16(uint32_t at, uint32_t (&r)[16]) {
 }
 
 struct TcRow {
-    float m, l, lx;  // running maximum (log2 units), sums of rounded and of unrounded P
+    float m, l, lx;  // running maximum (log2 units), sums of rounded and of unrounded P (times 2^lift)
     int fexp;        // E4M3: F of what O holds
 };
 
-// 32 scores of this row: times K's descales (E4M3), and -inf where `allow` has no
-// bit (`masked`, the same for the warp: some lane's has not).
-template <bool F8>
-__device__ __forceinline__ void tc_scores(uint32_t (&sr)[32], const float* kf, bool masked, uint32_t allow) {
+// One 128-key tile of a row: the maximum over all of it, O rescaled if that
+// moved by more than tau (or, E4M3, if F grew), then P over S's first 64 columns.
+// The scores stay in registers between the two; E4M3 multiplies them with K's
+// descales, which every lane reads from the same shared address (a wavefront for
+// four bytes: read once, not once for each use).
+template <int D, bool F8>
+__device__ __forceinline__ void tc_softmax_tile(uint32_t tS, uint32_t tO, const float* kf, int fexp, bool special,
+                                                const uint32_t (&allow)[4], bool first, float c, int ncols,
+                                                TcRow& r) {
+    uint32_t sr[128];
+    tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+    tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+    tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
+    tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
+    tmem_wait_ld();
     if constexpr (F8) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
+        for (int i = 0; i < 128; i += 4) {
             const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(kf + i);
             float u, v;
             f2_split(f2_mul(f2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), k.x), u, v);
@@ -578,69 +621,23 @@ __device__ __forceinline__ void tc_scores(uint32_t (&sr)[32], const float* kf, b
             sr[i + 3] = __float_as_uint(v);
         }
     }
-    if (masked) {
+    if (special) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (!(allow >> i & 1u)) sr[i] = 0xFF800000u;
+        for (int i = 0; i < 128; ++i)
+            if (!(allow[i >> 5] >> (i & 31) & 1u)) sr[i] = 0xFF800000u;
     }
-}
-// P of 32 keys to TMEM (16-bit pairs), added to the sums.
-template <bool F8>
-__device__ __forceinline__ void tc_probs(uint32_t tP, const float* wv, const uint32_t (&sr)[32], uint64_t c2,
-                                         uint64_t nm2, uint64_t& s0, uint64_t& s1) {
-    uint32_t pk[16];
+    float mx;
+    {
+        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float a, b;
-        f2_split(f2_fma(f2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), c2, nm2), a, b);
-        const float p0 = ex2(a), p1 = ex2(b);
-        const uint64_t pp = f2(p0, p1);
-        if (i & 1) s1 = f2_add(s1, pp);
-        else s0 = f2_add(s0, pp);
-        if constexpr (F8) {
-            float u, v;
-            f2_split(f2_mul(pp, *reinterpret_cast<const unsigned long long*>(wv + 2 * i)), u, v);
-            pk[i] = tc_pack_f16(u, v);
-        } else {
-            pk[i] = pack_bf16x2(p0, p1);
-        }
-    }
-    tmem_st16(tP, pk);
-}
-
-// One 128-key tile of a row: the maximum over all of it, O rescaled if that
-// moved by more than tau (or, E4M3, if F grew), then P over S's first 64 columns
-// (P of keys 32 i .. lies in columns 16 i .., whose scores are read before).
-// The loops stay rolled: unrolled, the instructions of a tile no longer fit the
-// instruction caches and every warp waits for its code (measured: a fifth of all
-// warp cycles; E4M3 softmax 3300 -> see the table beside the kernel).
-template <int D, bool F8>
-__device__ __forceinline__ void tc_softmax_tile(uint32_t tS, uint32_t tO, const float* kf, const float* wv, int fexp,
-                                                bool special, const uint32_t (&allow)[4], bool first, float c,
-                                                int ncols, TcRow& r) {
-    uint32_t a[32], b[32];
-    float mx = -INFINITY;
-    uint32_t w0 = allow[0], w1 = allow[1];
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-        tmem_ld32(tS + 64 * h, a);
-        tmem_ld32(tS + 64 * h + 32, b);
-        tmem_wait_ld();
-        tc_scores<F8>(a, kf + 64 * h, special && __any_sync(0xFFFFFFFFu, w0 != 0xFFFFFFFFu), w0);
-        tc_scores<F8>(b, kf + 64 * h + 32, special && __any_sync(0xFFFFFFFFu, w1 != 0xFFFFFFFFu), w1);
-        w0 = allow[2];
-        w1 = allow[3];
-        float m0 = mx, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            m0 = fmax3(m0, __uint_as_float(a[i]), __uint_as_float(a[i + 1]));
-            m1 = fmax3(m1, __uint_as_float(a[i + 2]), __uint_as_float(a[i + 3]));
-            m2 = fmax3(m2, __uint_as_float(b[i]), __uint_as_float(b[i + 1]));
-            m3 = fmax3(m3, __uint_as_float(b[i + 2]), __uint_as_float(b[i + 3]));
+        for (int i = 0; i < 128; i += 8) {
+            m0 = fmax3(m0, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+            m1 = fmax3(m1, __uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3]));
+            m2 = fmax3(m2, __uint_as_float(sr[i + 4]), __uint_as_float(sr[i + 5]));
+            m3 = fmax3(m3, __uint_as_float(sr[i + 6]), __uint_as_float(sr[i + 7]));
         }
         mx = fmax3(fmaxf(m0, m1), m2, m3);
     }
-    tmem_ld32(tS, a);  // the first scores again, on their way during the rest
     const float mt = mx * c;  // (c > 0)
     const bool need = mt > r.m + kTcTau;
     bool grow = false;
@@ -673,31 +670,35 @@ __device__ __forceinline__ void tc_softmax_tile(uint32_t tS, uint32_t tO, const 
         }
     }
     if constexpr (F8) r.fexp = fexp;
-    const float m = r.m == -INFINITY ? 0.f : r.m;
+    const float m = (r.m == -INFINITY ? 0.f : r.m) - kTcLift<F8>;
     if constexpr (!F8) {
         // the tile's largest weight is its rounded P: its error enters l too
         const float pm = mx == -INFINITY ? 0.f : ex2(fmaf(mx, c, -m));
         r.l += bf16lo_to_f32(pack_bf16x2(pm, 0.f)) - pm;
     }
     const uint64_t c2 = f2(c, c), nm2 = f2(-m, -m);
-    uint64_t s0 = 0, s1 = 0;
-    w0 = allow[0];
-    w1 = allow[1];
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-        tmem_wait_ld();
-        tmem_ld32(tS + 64 * h + 32, b);
-        tc_scores<F8>(a, kf + 64 * h, special && __any_sync(0xFFFFFFFFu, w0 != 0xFFFFFFFFu), w0);
-        tc_probs<F8>(tS + 32 * h, wv + 64 * h, a, c2, nm2, s0, s1);
-        tmem_wait_ld();
-        if (h == 0) tmem_ld32(tS + 64, a);
-        tc_scores<F8>(b, kf + 64 * h + 32, special && __any_sync(0xFFFFFFFFu, w1 != 0xFFFFFFFFu), w1);
-        tc_probs<F8>(tS + 32 * h + 16, wv + 64 * h + 32, b, c2, nm2, s0, s1);
-        w0 = allow[2];
-        w1 = allow[3];
+    uint64_t s0 = 0, s1 = 0, s2 = 0, s3 = 0;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int col = 32 * g + 2 * i;
+            float a, b;
+            f2_split(f2_fma(f2(__uint_as_float(sr[col]), __uint_as_float(sr[col + 1])), c2, nm2), a, b);
+            const float p0 = ex2(a), p1 = ex2(b);
+            switch (i & 3) {
+                case 0: s0 = f2_add(s0, f2(p0, p1)); break;
+                case 1: s1 = f2_add(s1, f2(p0, p1)); break;
+                case 2: s2 = f2_add(s2, f2(p0, p1)); break;
+                default: s3 = f2_add(s3, f2(p0, p1)); break;
+            }
+            pk[i] = F8 ? tc_pack_f16(p0, p1) : pack_bf16x2(p0, p1);
+        }
+        tmem_st16(tS + 16 * g, pk);
     }
     float u, v;
-    f2_split(f2_add(s0, s1), u, v);
+    f2_split(f2_add(f2_add(s0, s1), f2_add(s2, s3)), u, v);
     r.l += u + v;
     r.lx += u + v;
 }
@@ -731,7 +732,7 @@ __device__ __noinline__ void tc_add_bad(const TreeParams& p, const TcPiece& x, c
         };
         float s = 0.f;
         for (int i = 0; i < p.dh; ++i) s = fmaf(__bfloat162float(q[i]), value(p.k_pages, p.k_descale, i), s);
-        const float w = ex2(s * p.c - m) * inv;
+        const float w = ex2(s * p.c - m + kTcLift<F8>) * inv;
         for (int i = 0; i < 16; ++i)
             if (col + i < p.dh) v[i] = fmaf(w, value(p.v_pages, p.v_descale, col + i), v[i]);
     }
@@ -902,7 +903,7 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
             ok = warp_wait(&bars->s_full[t], cnt_s++, abort_flag, 32);
             if (!ok) break;
             tc_fence_after();
-            const float *kf = nullptr, *wv = nullptr;
+            const float* kf = nullptr;
             int fexp = 0;
             if constexpr (F8) {
                 const uint32_t g = tiles + (uint32_t)j;
@@ -910,7 +911,6 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
                 ok = warp_wait(&bars->ds_full[slot], g / kDs, abort_flag);
                 if (!ok) break;
                 kf = bars->kf[slot];
-                wv = bars->wv[slot];
                 fexp = *((volatile int*)&bars->fexp[slot]);
             }
             if (active) {
@@ -918,7 +918,7 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
                 const bool special = x.special(j);
                 if (special)
                     tc_allow(p, x.w.b, my.tok, x.w.drafted, (x.w.k0 + j) * kTcKeys - x.prefix, mask, allow);
-                tc_softmax_tile<D, F8>(tS, tO + 128 * t, kf, wv, fexp, special, allow, s == 0, c, ncols, st);
+                tc_softmax_tile<D, F8>(tS, tO + 128 * t, kf, fexp, special, allow, s == 0, c, ncols, st);
                 tmem_wait_st();
             }
             tc_fence_before();
@@ -945,14 +945,14 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
         uint32_t tA = tO + 128 * t;
         if (x.pair) {
             inv_l = st.l == 0.f ? 0.f : 1.0f / st.l;
-            inv0 = F8 ? inv_l * (tc_pow2(st.fexp) / kTcFrame) : inv_l;
+            inv0 = F8 ? inv_l * (tc_pow2(st.fexp)) : inv_l;
         } else {
             // the streams' statistics meet in shared memory; each warpgroup
             // then merges half of the columns, both O's being in its lanes
             bars->m[t][me] = st.m;
             bars->l[t][me] = st.l;
             bars->lx[t][me] = st.lx;
-            if (wq == 0 && lane == 0) bars->fin[t] = F8 ? tc_pow2(st.fexp) / kTcFrame : 1.f;
+            if (wq == 0 && lane == 0) bars->fin[t] = F8 ? tc_pow2(st.fexp) : 1.f;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars->stat));
@@ -991,7 +991,7 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
             if (any_bad) tc_write_slow<D, F8>(p, x, o, tA, col0, col1, bad);
             else tc_write<D, F8, false>(p, x, o, tA, col0, col1, bad);
             if (o.live && (x.pair || t == 0)) {
-                const float lse2 = lx == 0.f ? -INFINITY : m + log2f(lx);
+                const float lse2 = lx == 0.f ? -INFINITY : m - kTcLift<F8> + log2f(lx);
                 if (!x.w.whole) p.ws_lse[o.place * kTcRows + my.row] = lse2;
                 else if (p.lse) p.lse[my.bht] = lse2 * kTcLn2;
             }
