@@ -390,21 +390,20 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
     TcPiece x;
     float kd[2] = {0.f, 0.f}, vd[4] = {0.f, 0.f, 0.f, 0.f};
     // descales of a tile: K's of keys 64 wc + {0, 32} + lane, V's of keys lane + 32
-    // i; where they lie is looked up a tile earlier still (`at`, -1: no page)
-    long long at[4] = {-1, -1, -1, -1};
+    // i; the pages they lie in are looked up a tile earlier still, and used only
+    // then, so that neither load is waited for
+    int page[4] = {-1, -1, -1, -1}, off[4] = {0, 0, 0, 0};
     auto look = [&](int j) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            int off;
-            const int page = tree_page(p, x.w.b, (x.w.k0 + j) * kTcKeys + 32 * i + lane, x.w.keys, off);
-            at[i] = page < 0 ? -1 : ((long long)page * p.Hkv + x.w.h) * p.page_size + off;
-        }
+        for (int i = 0; i < 4; ++i)
+            page[i] = tree_page(p, x.w.b, (x.w.k0 + j) * kTcKeys + 32 * i + lane, x.w.keys, off[i]);
     };
     auto fetch = [&]() {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            vd[i] = at[i] < 0 ? 0.f : __ldg(p.v_descale + at[i]);
-            if ((i >> 1) == wc) kd[i & 1] = at[i] < 0 ? 0.f : __ldg(p.k_descale + at[i]);
+            const long long at = ((long long)(page[i] < 0 ? 0 : page[i]) * p.Hkv + x.w.h) * p.page_size + off[i];
+            vd[i] = page[i] < 0 ? 0.f : __ldg(p.v_descale + at);
+            if ((i >> 1) == wc) kd[i & 1] = page[i] < 0 ? 0.f : __ldg(p.k_descale + at);
         }
     };
     const int c = lane & 7;
@@ -493,39 +492,38 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
                 if (lane < 2) bars->bad[piece % kBadBufs][j - x.first_special()][2 * wc + lane] = lane ? marks[1] : marks[0];
                 __syncwarp();  // (other lanes read the rows below)
             }
+            // this lane's rows: row0 + 4 i; row & 7 = row_in + 4 (i & 1), so the
+            // swizzle has two patterns
+            const int row0 = 64 * wc + row_in;
+            const uint32_t src[2] = {raw + row0 * 128 + ((c ^ row_in) << 4), raw + row0 * 128 + ((c ^ row_in ^ 4) << 4)};
+            const int ch = 2 * (c & 3);
+            const uint32_t dst[2] = {out + row0 * 128 + ((ch ^ row_in) << 4), out + row0 * 128 + ((ch ^ row_in ^ 4) << 4)};
+            const uint32_t odd = 16 - ((row_in & 1) << 5);  // from an even chunk to its odd neighbour
+            const float* fv = &bars->wv[tile_v % kDs][row0];
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                const int row0 = 64 * wc + 32 * half + row_in;  // this lane's rows: row0 + 4 i
-                // (row & 7 = row_in + 4 (i & 1): two patterns of the swizzle)
-                const uint32_t src[2] = {raw + row0 * 128 + ((c ^ row_in) << 4), raw + row0 * 128 + ((c ^ row_in ^ 4) << 4)};
-                const int ch = 2 * (c & 3);
-                const uint32_t dst[2] = {out + row0 * 128 + ((ch ^ row_in) << 4), out + row0 * 128 + ((ch ^ row_in ^ 4) << 4)};
-                const uint32_t odd = 16 - ((row_in & 1) << 5);  // from an even chunk to its odd neighbour
-                uint4 w[8];
+            for (int i0 = 0; i0 < 16; i0 += 4) {
+                uint4 w[4];
+                float d[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = tc_lds128(src[i & 1] + 512 * i);
-                uint32_t f[8];  // V: its descale over F, twice in fp16
+                for (int i = 0; i < 4; ++i) w[i] = tc_lds128(src[i & 1] + 512 * (i0 + i));
                 if (is_v) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float d = bars->wv[tile_v % kDs][row0 + 4 * i];
-                        f[i] = tc_pack_f16(d, d);
-                    }
+                    for (int i = 0; i < 4; ++i) d[i] = fv[4 * (i0 + i)];
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < 4; ++i) {
                     uint32_t h[8];
                     tc_e4m3x4(w[i].x, h[0], h[1]);
                     tc_e4m3x4(w[i].y, h[2], h[3]);
                     tc_e4m3x4(w[i].z, h[4], h[5]);
                     tc_e4m3x4(w[i].w, h[6], h[7]);
-                    if (is_v) {
+                    if (is_v) {  // times its descale over F
+                        const uint32_t f = tc_pack_f16(d[i], d[i]);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(f[i]));
+                        for (int e = 0; e < 8; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(f));
                     }
-                    sts128(dst[i & 1] + 512 * i, h[0], h[1], h[2], h[3]);
-                    sts128(dst[i & 1] + 512 * i + odd, h[4], h[5], h[6], h[7]);
+                    sts128(dst[i & 1] + 512 * (i0 + i), h[0], h[1], h[2], h[3]);
+                    sts128(dst[i & 1] + 512 * (i0 + i) + odd, h[4], h[5], h[6], h[7]);
                 }
             }
             fence_proxy_async_smem();
