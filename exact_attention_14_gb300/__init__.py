@@ -15,7 +15,10 @@ the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+
+import torch
 
 __all__ = [
     "ATTN_OUT_BF16", "ATTN_OUT_F32", "AttnError", "attn_fwd", "attn_fwd_workspace_size",
@@ -142,7 +145,6 @@ def _check(code: int, where: str):
 
 
 def _stream_ptr(stream):
-    import torch
     if stream is None:   # the current stream of the current device, without a Stream object
         if not torch.cuda.is_initialized():
             torch.cuda.init()
@@ -155,7 +157,6 @@ def _ptr(t):
 
 
 def _need(t, dtype, name):
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -202,7 +203,6 @@ _HERE = _Here()
 
 
 def _on(dev):
-    import torch
     if dev.index == torch._C._cuda_getDevice():   # (a switch and back costs more than a launch)
         return _HERE
     return torch.cuda.device(dev)
@@ -802,7 +802,6 @@ _Strides = ctypes.c_longlong * 3
 
 def _tensor(t, dtypes, name):
     """A CUDA tensor of one of the given dtypes (any layout)."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
@@ -817,12 +816,14 @@ def _at(t):
 
 
 def _rows(t, name):
-    """(B, H, N, d) and the host strides {batch, head, token} of a [B,H,N,d]
-    view or a packed [total,H,d] one (B = 1), whose rows are contiguous and
-    16-byte aligned."""
+    """(B, H, N, d) and the host strides {batch, head, token} (None: contiguous)
+    of a [B,H,N,d] view or a packed [total,H,d] one (B = 1), whose rows are
+    contiguous and 16-byte aligned."""
     nd = t.ndim
     if nd == 4:
-        B, H, N, d = t.shape
+        B, H, N, d = shape = t.shape
+        if t.is_contiguous() and B and H and N and d and not t.data_ptr() % 16:
+            return shape, None   # (row lengths that are no multiple of 16 bytes the library refuses)
         sb, sh, sn, sd = t.stride()
         if B == 1:
             sb = 0
@@ -848,7 +849,6 @@ def _rows(t, name):
 def _used_on(stream, *tensors):
     """Tensors allocated here and used on a stream of the caller's: freed only
     after that stream's use."""
-    import torch
     if isinstance(stream, torch.cuda.Stream):
         for t in tensors:
             if t is not None:
@@ -877,7 +877,6 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "
                      beta_slow: float = 1.0, device="cuda"):
     """(inv_freq float64 tensor [rotary_dim / 2] on ``device``, magnitude) for
     rope() and rope_backward(); see attn_rope_frequencies."""
-    import torch
     f, mag = attn_rope_frequencies(rotary_dim, base, scaling=scaling, factor=factor,
                                    original_len=original_len, beta_fast=beta_fast,
                                    beta_slow=beta_slow)
@@ -886,7 +885,6 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "
 
 def _rope_inputs(q, k):
     """Checks q and k; returns (B, Hq, Hkv, N, d) and their strides."""
-    import torch
     _tensor(q, (torch.bfloat16, torch.float32), "q")
     (B, Hq, N, d), qs = _rows(q, "q")
     if k is None:
@@ -901,7 +899,6 @@ def _rope_inputs(q, k):
 def _rope_call(q, k, q_out, k_out, positions, inv_freq, shape, qos, kos, interleaved, inverse,
                magnitude, stream):
     """attn_rope once q, k and the outputs are known to be good."""
-    import torch
     B, Hq, Hkv, N, d, qs, ks = shape
     _tensor(positions, (torch.int32,), "positions")
     _need(inv_freq, torch.float64, "inv_freq")
@@ -939,7 +936,6 @@ def attn_rope(q, k, q_out, k_out, positions, inv_freq, *, interleaved: bool = Fa
     tensors); inv_freq float64 [rotary_dim / 2] (rope_frequencies); the columns
     past rotary_dim are copied.  inverse: the gradient.  In place when an output
     is its input.  Asynchronous on ``stream``."""
-    import torch
     shape = _rope_inputs(q, k)
     B, Hq, Hkv, N, d = shape[:5]
     _tensor(q_out, (torch.bfloat16, torch.float32), "q_out")
@@ -960,18 +956,17 @@ def attn_rope(q, k, q_out, k_out, positions, inv_freq, *, interleaved: bool = Fa
 
 def _new_rows(x, dtype, H, N, d):
     """A contiguous output of x's shape and its strides."""
-    import torch
-    out = torch.empty(x.shape, dtype=dtype, device=x.device)
-    if x.ndim == 4:
-        return out, _Strides(H * N * d if x.shape[0] > 1 else 0, N * d if H > 1 else 0, d if N > 1 else 0)
-    return out, _Strides(0, d if H > 1 else 0, H * d if N > 1 else 0)
+    if dtype == x.dtype and x.is_contiguous():
+        out = torch.empty_like(x)
+    else:
+        out = torch.empty(x.shape, dtype=dtype, device=x.device)
+    return out, None if x.ndim == 4 else _Strides(0, d if H > 1 else 0, H * d if N > 1 else 0)
 
 
 def rope(q, k, positions, inv_freq, *, interleaved: bool = False, magnitude: float = 1.0,
          out_dtype=None, stream=None, inverse: bool = False):
     """Allocate the outputs (contiguous, of q's and k's shapes) with torch and
     run attn_rope.  Returns (q_out, k_out); k may be None."""
-    import torch
     shape = _rope_inputs(q, k)
     _, Hq, Hkv, N, d = shape[:5]
     out_dtype = out_dtype or q.dtype
@@ -996,7 +991,6 @@ def rope_backward(dq_out, dk_out, positions, inv_freq, *, interleaved: bool = Fa
 def _check_pages(k_pages, v_pages, k_descale, v_descale):
     """Types, shapes and placement of a paged cache; returns (num_blocks,
     page_size, Hkv, d, cache dtype)."""
-    import torch
     _tensor(k_pages, (torch.bfloat16, torch.uint8), "k_pages")
     _need(k_pages, k_pages.dtype, "k_pages")
     _need(v_pages, k_pages.dtype, "v_pages")
@@ -1022,7 +1016,6 @@ def attn_cache_write(k, v, k_pages, v_pages, slots, k_descale=None, v_descale=No
     uint8 E4M3 codes with k_descale, v_descale fp32 [num_blocks,Hkv,page_size];
     slots int64 [B,N] (or [total]): page * page_size + key in the page, distinct,
     -1 for tokens to leave out.  Asynchronous."""
-    import torch
     _tensor(k, (torch.bfloat16,), "k")
     _tensor(v, (torch.bfloat16,), "v")
     num_blocks, page_size, Hkv, d, kind = _check_pages(k_pages, v_pages, k_descale, v_descale)
@@ -1043,7 +1036,6 @@ def attn_cache_write(k, v, k_pages, v_pages, slots, k_descale=None, v_descale=No
 def _read_call(k_pages, v_pages, block_table, cu_seqlens, k_out, v_out, k_descale, v_descale,
                cache, stream):
     """attn_cache_read once the cache and the outputs are known to be good."""
-    import torch
     num_blocks, page_size, Hkv, d, kind = cache
     _need(block_table, torch.int32, "block_table")
     _need(cu_seqlens, torch.int32, "cu_seqlens")
@@ -1068,7 +1060,6 @@ def attn_cache_read(k_pages, v_pages, block_table, cu_seqlens, k_out, v_out, k_d
     cu_seqlens[b]..cu_seqlens[b+1].  block_table int32 [B,max_blocks],
     cu_seqlens int32 [B+1], both on the device.  Rows outside every sequence
     stay as they were.  Asynchronous."""
-    import torch
     cache = _check_pages(k_pages, v_pages, k_descale, v_descale)
     _tensor(k_out, (torch.bfloat16, torch.float32), "k_out")
     _need(k_out, k_out.dtype, "k_out")
@@ -1083,7 +1074,6 @@ def cache_read(k_pages, v_pages, block_table, cu_seqlens, total: int, k_descale=
                v_descale=None, *, out_dtype=None, stream=None):
     """Allocate k and v [total,Hkv,d] with torch and run attn_cache_read (total
     = cu_seqlens[-1], known to the host)."""
-    import torch
     cache = _check_pages(k_pages, v_pages, k_descale, v_descale)
     out_dtype = out_dtype or torch.bfloat16
     if out_dtype not in (torch.bfloat16, torch.float32):
@@ -1100,7 +1090,6 @@ def cache_read(k_pages, v_pages, block_table, cu_seqlens, total: int, k_descale=
 def tree_mask_words(mask):
     """bool [B,T,T] (mask[b, t, u]: drafted token t sees drafted token u) ->
     the int64 words [B,T,ceil(T/64)] that attn_decode_tree takes."""
-    import torch
     if mask.ndim != 3 or mask.shape[1] != mask.shape[2] or mask.dtype != torch.bool:
         raise ValueError("mask must be bool [B, T, T]")
     B, T, _ = mask.shape
@@ -1116,10 +1105,16 @@ def attn_decode_tree_workspace_size(B: int, Hq: int, Hkv: int, T: int, max_block
                                                       int(bool(e4m3))))
 
 
+@functools.lru_cache(maxsize=1024)
+def _tree_workspace(Hq, Hkv, T, d, kind, device_index):
+    """attn_decode_tree_workspace_size on the current device (device_index), which
+    depends on nothing else.  (0 for what the library will refuse.)"""
+    return int(load().attn_decode_tree_workspace_size(1, Hq, Hkv, T, 1, 16, d, kind))
+
+
 def _tree_call(q, k_pages, v_pages, block_table, seqlens, o, lse, tree_mask, q_lens, k_descale,
                v_descale, scale, workspace, stream):
     """attn_decode_tree once o and lse are known to be good."""
-    import torch
     _need(q, torch.bfloat16, "q")
     num_blocks, page_size, Hkv, d, kind = _check_pages(k_pages, v_pages, k_descale, v_descale)
     _need(block_table, torch.int32, "block_table")
@@ -1146,8 +1141,8 @@ def _tree_call(q, k_pages, v_pages, block_table, seqlens, o, lse, tree_mask, q_l
     lib = load()
     with _on(dev):
         if workspace is None:
-            need = lib.attn_decode_tree_workspace_size(B, Hq, Hkv, T, max_blocks, page_size, d, kind)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(_tree_workspace(Hq, Hkv, T, d, kind, dev.index), dtype=torch.uint8,
+                                    device=dev)
             if stream is not None:
                 _used_on(stream, workspace)
         elif not workspace.is_contiguous():
@@ -1175,7 +1170,6 @@ def attn_decode_tree(q, k_pages, v_pages, block_table, seqlens, o, lse=None, tre
     each sequence, or None for T; workspace: a CUDA tensor of at least
     attn_decode_tree_workspace_size(...) bytes, or None (then one is allocated
     with torch).  T = 1 is plain decode.  Asynchronous."""
-    import torch
     _tensor(o, (torch.bfloat16, torch.float32), "o")
     _need(o, o.dtype, "o")
     if o.shape != q.shape:
@@ -1192,7 +1186,6 @@ def decode_tree(q, k_pages, v_pages, block_table, seqlens, tree_mask=None, q_len
                 k_descale=None, v_descale=None, *, scale: float | None = None, out_dtype=None,
                 return_lse: bool = True, stream=None):
     """Allocate O (and LSE) with torch and run attn_decode_tree."""
-    import torch
     out_dtype = out_dtype or torch.bfloat16
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out_dtype must be bfloat16 or float32")

@@ -291,10 +291,19 @@ namespace {
 
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
+// A contiguous [B, H, N, d] array's strides, for callers that pass none.
+struct Strides {
+    long long s[3];
+    Strides(const long long* given, int H, int N, int d) {
+        s[0] = given ? given[0] : (long long)H * N * d;
+        s[1] = given ? given[1] : (long long)N * d;
+        s[2] = given ? given[2] : d;
+    }
+};
+
 // Strides {batch, head, token} (elements) of a [B, H, N, d] view whose rows are
 // 16-byte aligned; `written`: no two elements may share a place.
 bool strides_ok(const long long* s, int B, int H, int N, int d, int element_bytes, bool written) {
-    if (!s) return false;
     const int sizes[3] = {B, H, N};
     for (int i = 0; i < 3; ++i)
         if (s[i] < 0 || s[i] % (16 / element_bytes) != 0) return false;
@@ -636,6 +645,12 @@ attn_status_t attn_rope(const void* q, const void* k, void* q_out, void* k_out,
     if (!std::isfinite(magnitude) || positions_stride < 0) return ATTN_ERR_INVALID_ARG;
     if (!fwd_head_dim_supported(d)) return ATTN_ERR_UNSUPPORTED;
     const int bi = in_dtype == ATTN_OUT_F32 ? 4 : 2, bo = out_dtype == ATTN_OUT_F32 ? 4 : 2;
+    const Strides sq(q_strides, Hq, N, d), sk(k_strides, Hkv, N, d), sqo(q_out_strides, Hq, N, d),
+        sko(k_out_strides, Hkv, N, d);
+    q_strides = sq.s;
+    k_strides = sk.s;
+    q_out_strides = sqo.s;
+    k_out_strides = sko.s;
     if (!strides_ok(q_strides, B, Hq, N, d, bi, false) || !strides_ok(q_out_strides, B, Hq, N, d, bo, true))
         return ATTN_ERR_INVALID_ARG;
     if (k && (!strides_ok(k_strides, B, Hkv, N, d, bi, false) ||
@@ -667,6 +682,9 @@ attn_status_t attn_cache_write(const void* k, const void* v, const long long* k_
     attn_status_t st = check_pages(Hkv, d, num_blocks, page_size, cache_dtype, k_pages, v_pages,
                                    k_descale, v_descale);
     if (st != ATTN_OK) return st;
+    const Strides sk(k_strides, Hkv, N, d), sv(v_strides, Hkv, N, d);
+    k_strides = sk.s;
+    v_strides = sv.s;
     if (!strides_ok(k_strides, B, Hkv, N, d, 2, false) || !strides_ok(v_strides, B, Hkv, N, d, 2, false))
         return ATTN_ERR_INVALID_ARG;
     DeviceInfo dev;

@@ -14,8 +14,8 @@
 // keeps a NaN code, an infinite one makes its row NaN.
 // Read: code * descale (fp32 product) rounded to the output type.
 //
-// Bound: HBM.  Both kernels move 16 elements per lane with 16-byte accesses;
-// nothing is staged in shared memory, since no element is used twice.
+// Bound: HBM.  Neighbouring lanes move neighbouring 16-byte pieces of the bf16
+// side; nothing is staged in shared memory, since no element is used twice.
 #include <cstdint>
 
 #include "internal.h"
@@ -38,9 +38,9 @@ struct WriteSide {
 struct WriteParams {
     WriteSide side[2];     // k, v
     const long long* slots;  // [B, N]
-    long long tokens, num_slots;
-    int N, Hkv, d, page_size;
-    int lanes;             // lanes of a row (a power of two, 16 elements each)
+    long long num_slots;
+    int tokens, N, Hkv, d, page_size;
+    int lanes_log2;        // lanes of a row: 2^, 16 elements each
     unsigned int* err;
 };
 
@@ -55,83 +55,89 @@ __device__ __forceinline__ float amax2(float m, uint32_t w) {
     return fmaxf(m, fmaxf(fabsf(bf16lo_to_f32(w)), fabsf(bf16hi_to_f32(w))));
 }
 
-// Row r of the call = (tile of 32 tokens, KV head, token in the tile): a
-// block's rows are consecutive tokens of a head, so that the descales of a
-// page are written as whole lines.  Each lane holds 16 columns of the K row and
-// of the V row of its token and head.
+// A block's rows are consecutive tokens of one KV head (blockIdx.y, strided), so
+// that the descales of a page are written as whole lines.  A lane holds the
+// 8-column chunks c and c + lanes of the K row and of the V row of its token.
 template <bool E4M3>
 __global__ void __launch_bounds__(kCacheThreads)
 attn_cache_write_kernel(const __grid_constant__ WriteParams p) {
-    const int lanes = p.lanes;
-    const long long at = (long long)blockIdx.x * kCacheThreads + threadIdx.x;
-    const long long row = at / lanes;
-    const int col = 16 * (int)(at - row * lanes);
-    const long long tile = row / (32 * p.Hkv);
-    const int in_tile = (int)(row - tile * (32 * p.Hkv));
-    const int h = in_tile >> 5;
-    const long long token = tile * 32 + (in_tile & 31);
+    const int lanes = 1 << p.lanes_log2;
+    const int c = threadIdx.x & (lanes - 1);
+    const int token = blockIdx.x * (kCacheThreads >> p.lanes_log2) + (threadIdx.x >> p.lanes_log2);
     const bool live_token = token < p.tokens;
     long long slot = live_token ? __ldg(p.slots + token) : -1;
     if (slot >= p.num_slots || slot < -1) {
-        if (h == 0 && col == 0) atomicOr(p.err, kErrBadSeqlen);
+        if (blockIdx.y == 0 && c == 0) atomicOr(p.err, kErrBadSeqlen);
         slot = -1;
     }
-    const bool live = slot >= 0 && col < p.d;
-    const long long b = token / p.N;
-    const int n = (int)(token - b * p.N);
-    uint4 w[2][2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        w[s][0] = w[s][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (live) {
-            const WriteSide& sd = p.side[s];
-            const uint4* x = reinterpret_cast<const uint4*>(sd.x + b * sd.xb + (long long)h * sd.xh +
-                                                            (long long)n * sd.xn + col);
-            w[s][0] = __ldcs(x);
-            if (col + 8 < p.d) w[s][1] = __ldcs(x + 1);
-        }
-    }
-    const long long out = (slot * p.Hkv + h) * p.d + col;  // element of the cache
-    if constexpr (!E4M3) {
-        if (!live) return;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            uint4* o = reinterpret_cast<uint4*>(p.side[s].pages + 2 * out);
-            o[0] = w[s][0];
-            if (col + 8 < p.d) o[1] = w[s][1];
-        }
-    } else {
-        float m[2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            float a = 0.f;
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                a = amax2(a, w[s][v].x);
-                a = amax2(a, w[s][v].y);
-                a = amax2(a, w[s][v].z);
-                a = amax2(a, w[s][v].w);
-            }
-            m[s] = a;
-        }
-        for (int off = lanes >> 1; off > 0; off >>= 1) {
-            m[0] = fmaxf(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], off));
-            m[1] = fmaxf(m[1], __shfl_xor_sync(0xFFFFFFFFu, m[1], off));
-        }
-        if (!live) return;
-        // (slot, h) -> its descale: 32-bit division where the slot allows it
+    const int col[2] = {8 * c, 8 * (c + lanes)};
+    const bool in[2] = {slot >= 0 && col[0] < p.d, slot >= 0 && col[1] < p.d};
+    const int b = (int)((unsigned)token / (unsigned)p.N);
+    const int n = token - b * p.N;
+    long long dsc = 0;  // E4M3: the descale's place for head 0
+    if (E4M3 && slot >= 0) {
         long long blk;
         if (slot <= 0x7FFFFFFFll) blk = (long long)((unsigned)slot / (unsigned)p.page_size);
         else blk = slot / p.page_size;
-        const long long dsc = (blk * p.Hkv + h) * p.page_size + (slot - blk * p.page_size);
+        dsc = blk * p.Hkv * p.page_size + (slot - blk * p.page_size);
+    }
+    for (int h = blockIdx.y; h < p.Hkv; h += 2 * gridDim.y) {  // two heads' loads in flight
+        uint4 w[2][2][2];  // [head][k, v][chunk]
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const float a = fmaxf(m[s], kTinyAmax);
-            const float scale = m[s] > 0.f ? kE4m3Max / a : 1.0f;
-            *reinterpret_cast<uint4*>(p.side[s].pages + out) =
-                make_uint4(quant4(w[s][0].x, w[s][0].y, scale), quant4(w[s][0].z, w[s][0].w, scale),
-                           quant4(w[s][1].x, w[s][1].y, scale), quant4(w[s][1].z, w[s][1].w, scale));
-            if (col == 0) p.side[s].descale[dsc] = m[s] > 0.f ? a / kE4m3Max : 1.0f;
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const WriteSide& sd = p.side[s];
+                const int hg = h + g * gridDim.y;
+                const __nv_bfloat16* x = sd.x + b * sd.xb + (long long)hg * sd.xh + (long long)n * sd.xn;
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+                    w[g][s][v] = in[v] && hg < p.Hkv ? __ldcs(reinterpret_cast<const uint4*>(x + col[v]))
+                                                     : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int hg = h + g * gridDim.y;
+            if (hg >= p.Hkv) break;
+            const long long row = (slot * p.Hkv + hg) * p.d;  // first element of the cached row
+            if constexpr (!E4M3) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int v = 0; v < 2; ++v)
+                        if (in[v]) *reinterpret_cast<uint4*>(p.side[s].pages + 2 * (row + col[v])) = w[g][s][v];
+            } else {
+                float m[2];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    float a = 0.f;
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        a = amax2(a, w[g][s][v].x);
+                        a = amax2(a, w[g][s][v].y);
+                        a = amax2(a, w[g][s][v].z);
+                        a = amax2(a, w[g][s][v].w);
+                    }
+                    m[s] = a;
+                }
+                for (int off = lanes >> 1; off > 0; off >>= 1) {
+                    m[0] = fmaxf(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], off));
+                    m[1] = fmaxf(m[1], __shfl_xor_sync(0xFFFFFFFFu, m[1], off));
+                }
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const float a = fmaxf(m[s], kTinyAmax);
+                    const float scale = m[s] > 0.f ? kE4m3Max / a : 1.0f;
+#pragma unroll
+                    for (int v = 0; v < 2; ++v)
+                        if (in[v])
+                            *reinterpret_cast<uint2*>(p.side[s].pages + row + col[v]) =
+                                make_uint2(quant4(w[g][s][v].x, w[g][s][v].y, scale),
+                                           quant4(w[g][s][v].z, w[g][s][v].w, scale));
+                    if (c == 0 && slot >= 0)
+                        p.side[s].descale[dsc + (long long)hg * p.page_size] = m[s] > 0.f ? a / kE4m3Max : 1.0f;
+                }
+            }
         }
     }
 }
@@ -148,6 +154,7 @@ struct ReadParams {
 };
 
 constexpr int kReadTokens = 16;  // tokens of a block
+constexpr int kReadFlight = 4;   // pieces of a thread whose loads are in flight
 
 __device__ __forceinline__ float2 e4m3x2_f32(uint32_t pair16) {
     uint32_t h2;
@@ -159,29 +166,28 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t pair16) {
     return f;
 }
 
-template <typename TO>
-__device__ __forceinline__ void store4(TO* p, float a, float b, float c, float d);
-template <>
-__device__ __forceinline__ void store4<float>(float* p, float a, float b, float c, float d) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(a, b, c, d));
+__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
 }
-template <>
-__device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, float a, float b, float c, float d) {
-    __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d)));
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                   pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
 }
 
 // A block reads kReadTokens consecutive packed tokens, all heads, K or V
 // (blockIdx.y).  The first lanes find each token's sequence by bisection and
-// its row in the cache; then every thread streams groups of columns.
+// its row in the cache; then every thread streams pieces of 8 columns.
 template <bool E4M3, typename TO>
 __global__ void __launch_bounds__(kCacheThreads)
 attn_cache_read_kernel(const __grid_constant__ ReadParams p) {
     __shared__ long long s_slot[kReadTokens];  // row in the cache; -1: zeros; -2: leave
+    __shared__ long long s_descale[kReadTokens];  // its descale's place for head 0
     const int side = blockIdx.y;
     const int token0 = blockIdx.x * kReadTokens;
     if (threadIdx.x < kReadTokens) {
         const int token = token0 + threadIdx.x;
-        long long slot = -2;
+        long long slot = -2, ds = 0;
         if (token < p.total) {
             // the last b with cu[b] <= token
             int lo = 0, hi = p.B;
@@ -197,57 +203,67 @@ attn_cache_read_kernel(const __grid_constant__ ReadParams p) {
                     atomicOr(p.err, kErrBadSeqlen);
                 } else if (token >= s && token < e) {
                     const int pos = token - s;
-                    const int blk = pos / p.page_size;
+                    const int blk = pos / p.page_size, off = pos - blk * p.page_size;
                     const long long page = __ldg(p.block_table + (size_t)lo * p.max_blocks + blk);
-                    slot = page >= 0 && page < p.num_blocks
-                               ? page * p.page_size + (pos - blk * p.page_size)
-                               : -1;
+                    if (page >= 0 && page < p.num_blocks) {
+                        slot = page * p.page_size + off;
+                        ds = page * p.Hkv * p.page_size + off;
+                    } else {
+                        slot = -1;
+                    }
                 }
             }
         }
         s_slot[threadIdx.x] = slot;
+        s_descale[threadIdx.x] = ds;
     }
     __syncthreads();
-    constexpr int kCols = E4M3 ? 16 : 8;  // columns of 16 bytes
-    const int per_row = p.d / kCols;
-    const int per_token = p.Hkv * per_row;
+    constexpr int kBytes = E4M3 ? 8 : 16;  // of a piece in the cache
+    const unsigned per_row = p.d / 8;
+    const unsigned per_token = p.Hkv * per_row;
     const uint8_t* pages = p.pages[side];
     const float* descale = p.descale[side];
     TO* out = static_cast<TO*>(p.out[side]);
-    const int n = kReadTokens * per_token;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += kCacheThreads) {
-        const int t = i / per_token;
-        const int c = i - t * per_token;
-        const long long slot = s_slot[t];
-        if (slot == -2) continue;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        float s = 1.0f;
-        if (slot >= 0) {
-            w = __ldcs(reinterpret_cast<const uint4*>(pages + (slot * per_token + c) * 16));
+    const unsigned n = kReadTokens * per_token;
+    for (unsigned i0 = threadIdx.x; i0 < n; i0 += kReadFlight * kCacheThreads) {
+        uint4 w[kReadFlight];
+        float s[kReadFlight];
+#pragma unroll
+        for (int k = 0; k < kReadFlight; ++k) {
+            const unsigned i = i0 + k * kCacheThreads;
+            w[k] = make_uint4(0u, 0u, 0u, 0u);
+            s[k] = 1.0f;
+            if (i >= n) continue;
+            const unsigned t = i / per_token, c = i - t * per_token;
+            const long long slot = s_slot[t];
+            if (slot < 0) continue;
+            const uint8_t* src = pages + (slot * per_token + c) * kBytes;
             if constexpr (E4M3) {
-                const int h = c / per_row;
-                const long long blk = slot / p.page_size;
-                s = __ldg(descale + (blk * p.Hkv + h) * p.page_size + (slot - blk * p.page_size));
+                const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src));
+                w[k].x = v.x;
+                w[k].y = v.y;
+                s[k] = __ldg(descale + s_descale[t] + (long long)(c / per_row) * p.page_size);
+            } else {
+                w[k] = __ldcs(reinterpret_cast<const uint4*>(src));
             }
         }
-        TO* o = out + ((long long)(token0 + t) * per_token + c) * kCols;
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-        if constexpr (E4M3) {
-            float f[16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 a = e4m3x2_f32(ws[j] & 0xFFFFu), b = e4m3x2_f32(ws[j] >> 16);
-                f[4 * j] = a.x * s; f[4 * j + 1] = a.y * s;
-                f[4 * j + 2] = b.x * s; f[4 * j + 3] = b.y * s;
+        for (int k = 0; k < kReadFlight; ++k) {
+            const unsigned i = i0 + k * kCacheThreads;
+            if (i >= n || s_slot[i / per_token] == -2) continue;
+            float f[8];
+            if constexpr (E4M3) {
+                const float2 a = e4m3x2_f32(w[k].x & 0xFFFFu), b = e4m3x2_f32(w[k].x >> 16);
+                const float2 c = e4m3x2_f32(w[k].y & 0xFFFFu), d = e4m3x2_f32(w[k].y >> 16);
+                f[0] = a.x * s[k]; f[1] = a.y * s[k]; f[2] = b.x * s[k]; f[3] = b.y * s[k];
+                f[4] = c.x * s[k]; f[5] = c.y * s[k]; f[6] = d.x * s[k]; f[7] = d.y * s[k];
+            } else {
+                f[0] = bf16lo_to_f32(w[k].x); f[1] = bf16hi_to_f32(w[k].x);
+                f[2] = bf16lo_to_f32(w[k].y); f[3] = bf16hi_to_f32(w[k].y);
+                f[4] = bf16lo_to_f32(w[k].z); f[5] = bf16hi_to_f32(w[k].z);
+                f[6] = bf16lo_to_f32(w[k].w); f[7] = bf16hi_to_f32(w[k].w);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) store4<TO>(o + 4 * j, f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                store4<TO>(o + 4 * j, bf16lo_to_f32(ws[2 * j]), bf16hi_to_f32(ws[2 * j]),
-                           bf16lo_to_f32(ws[2 * j + 1]), bf16hi_to_f32(ws[2 * j + 1]));
+            store8(out + ((long long)token0 * per_token + i) * 8, f);
         }
     }
 }
@@ -272,22 +288,26 @@ attn_status_t launch_cache_write(const void* k, const void* v, const long long* 
     p.side[0] = side(k, k_strides, k_pages, k_descale);
     p.side[1] = side(v, v_strides, v_pages, v_descale);
     p.slots = slots;
-    p.tokens = (long long)B * N;
+    p.tokens = B * N;
     p.num_slots = num_blocks * page_size;
     p.N = N;
     p.Hkv = Hkv;
     p.d = d;
     p.page_size = page_size;
     p.err = dev.err_word;
-    p.lanes = 1;
-    while (p.lanes * 16 < d) p.lanes *= 2;
-    const long long rows = (p.tokens + 31) / 32 * 32 * Hkv;
-    const long long blocks = (rows * p.lanes + kCacheThreads - 1) / kCacheThreads;
-    if (blocks > 0x7FFFFFFFll) return ATTN_ERR_UNSUPPORTED;
+    p.lanes_log2 = 0;
+    while ((16 << p.lanes_log2) < d) ++p.lanes_log2;
+    const int per_block = kCacheThreads >> p.lanes_log2;  // tokens
+    // a thread walks over up to four heads (its slot is looked up once), fewer
+    // where the blocks would not fill the SMs
+    const int tiles = (p.tokens + per_block - 1) / per_block;
+    int split = Hkv;
+    while (split > (Hkv + 3) / 4 && (long long)tiles * ((split + 1) / 2) >= 8ll * dev.num_sms) split = (split + 1) / 2;
+    const dim3 blocks((unsigned)tiles, (unsigned)(split < 65535 ? split : 65535));
     if (cache_dtype == ATTN_CACHE_E4M3)
-        attn_cache_write_kernel<true><<<(unsigned)blocks, kCacheThreads, 0, stream>>>(p);
+        attn_cache_write_kernel<true><<<blocks, kCacheThreads, 0, stream>>>(p);
     else
-        attn_cache_write_kernel<false><<<(unsigned)blocks, kCacheThreads, 0, stream>>>(p);
+        attn_cache_write_kernel<false><<<blocks, kCacheThreads, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -16,6 +16,10 @@
 // Bound: HBM (each element is read and written once).  A thread keeps the
 // cos / sin of its 8 pairs of one token in registers and walks over heads, so
 // the angles (about 40 instructions a pair) are shared by all heads it walks.
+// A row is a list of jobs, two chunks of 16 bytes each: the chunks of a half and
+// their partners, then the columns to copy; neighbouring lanes take neighbouring
+// jobs.  Two heads' loads are in flight at a time, the first ones during the
+// angles.
 #include <cstdint>
 
 #include "internal.h"
@@ -29,9 +33,9 @@ constexpr int kUnitPairs = 8;   // pairs of one thread
 constexpr int kMaxPairs = 128;  // rotary_dim <= 256
 
 enum RopeMode {
-    kHalfVec = 0,      // pairs (i, i + r/2), r/2 a multiple of 8: 8 consecutive pairs, 16-byte accesses
-    kInterVec = 1,     // pairs (2i, 2i + 1): 16 consecutive columns, 16-byte accesses
-    kHalfScalar = 2    // any other r: pairs j, j + P, ...: consecutive lanes on consecutive pairs
+    kHalfVec = 0,      // pairs (i, i + r/2), r/2 a multiple of a chunk
+    kInterVec = 1,     // pairs (2i, 2i + 1): a job is one chunk
+    kHalfScalar = 2    // pairs (i, i + r/2), any other r: chunks of one element
 };
 
 struct RopeSide {
@@ -48,7 +52,9 @@ struct RopeParams {
     long long pos_b;   // positions' batch stride
     const double* inv_freq;
     long long tokens;  // B * N
-    int N, d, pairs, units, pair_units;
+    int N, d, pairs;
+    int turn_jobs, jobs;  // jobs that turn, and all (the rest copies)
+    int units;            // threads of a (token, head)
     int heads, heads_per_thread;
     int inverse;
     float mag;
@@ -68,27 +74,42 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// 8 consecutive elements (16-byte aligned) as fp32.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
-    v[0] = bf16lo_to_f32(w.x); v[1] = bf16hi_to_f32(w.x);
-    v[2] = bf16lo_to_f32(w.y); v[3] = bf16hi_to_f32(w.y);
-    v[4] = bf16lo_to_f32(w.z); v[5] = bf16hi_to_f32(w.z);
-    v[6] = bf16lo_to_f32(w.w); v[7] = bf16hi_to_f32(w.w);
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+// A chunk of E consecutive elements (16-byte aligned pieces) as it is loaded.
+template <typename T, int E>
+struct Chunk {
+    static constexpr int kWords = E * (int)sizeof(T) / 16;
+    uint4 w[kWords];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+    }
+    __device__ __forceinline__ void get(float (&v)[E]) const {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(T) == 4) {
+                    v[4 * i + j] = __uint_as_float(u[j]);
+                } else {
+                    v[8 * i + 2 * j] = bf16lo_to_f32(u[j]);
+                    v[8 * i + 2 * j + 1] = bf16hi_to_f32(u[j]);
+                }
+            }
+        }
+    }
+};
+template <int E>
+__device__ __forceinline__ void store_chunk(__nv_bfloat16* p, const float (&v)[E]) {
+    static_assert(E == 8, "16 bytes of bf16");
     *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+template <int E>
+__device__ __forceinline__ void store_chunk(float* p, const float (&v)[E]) {
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i)
+        reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 
 // f radians as a fraction of a turn in units of 2^-64 (mod 1).  1/(2 pi) is
@@ -104,116 +125,126 @@ __device__ __forceinline__ unsigned long long turn_fraction(double f) {
     return f < 0.0 ? 0ull - u : u;
 }
 
+// An element on its own (chunks of one).
+template <typename T>
+struct Chunk<T, 1> {
+    T w;
+    __device__ __forceinline__ void load(const T* p) { w = *p; }
+    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = to_f32(w); }
+};
+template <>
+__device__ __forceinline__ void store_chunk<1>(__nv_bfloat16* p, const float (&v)[1]) { *p = from_f32<__nv_bfloat16>(v[0]); }
+template <>
+__device__ __forceinline__ void store_chunk<1>(float* p, const float (&v)[1]) { *p = v[0]; }
+
 template <typename TI, typename TO, int MODE>
 __global__ void __launch_bounds__(kRopeThreads)
 attn_rope_kernel(const __grid_constant__ RopeParams p) {
+    // columns of a chunk; jobs of a thread; pairs of a job
+    constexpr int E = MODE == kHalfScalar ? 1 : (sizeof(TI) == 4 && sizeof(TO) == 4 ? 4 : 8);
+    constexpr int kJobPairs = MODE == kInterVec ? E / 2 : E;
+    constexpr int kOwn = kUnitPairs / kJobPairs;
+    constexpr bool kTwo = MODE != kInterVec;  // a job has a second chunk
     __shared__ unsigned long long s_turn[kMaxPairs];
     for (int i = threadIdx.x; i < p.pairs; i += kRopeThreads) s_turn[i] = turn_fraction(p.inv_freq[i]);
     __syncthreads();
     const long long at = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
-    const long long token = at / p.units;
+    long long token;
+    if (at <= 0xFFFFFFFFll) token = (long long)((unsigned)at / (unsigned)p.units);
+    else token = at / p.units;
     if (token >= p.tokens) return;
     const int u = (int)(at - token * p.units);
-    const long long b = token / p.N;
-    const int n = (int)(token - b * p.N);
+    const int b = (int)((unsigned)token / (unsigned)p.N);  // (tokens <= 2^30)
+    const int n = (int)token - b * p.N;
     const int h0 = blockIdx.y * p.heads_per_thread;
     const int h1 = min(h0 + p.heads_per_thread, p.heads);
-    const int half = p.pairs;
-    const bool rotates = u < p.pair_units;
-
+    const int half = p.pairs, copies = p.jobs - p.turn_jobs;
+    // first columns of job v's chunks (second: -1 where there is none); the job turns
+    int col[kOwn], col2[kOwn];
+    bool turns[kOwn];
+#pragma unroll
+    for (int v = 0; v < kOwn; ++v) {
+        const int k = u + p.units * v, kc = k - p.turn_jobs;
+        turns[v] = kc < 0;
+        if constexpr (MODE == kInterVec) {
+            col[v] = k < p.jobs ? E * k : -1;
+            col2[v] = -1;
+        } else {
+            col[v] = k >= p.jobs ? -1 : (turns[v] ? E * k : 2 * half + E * kc);
+            col2[v] = k >= p.jobs ? -1 : (turns[v] ? half + E * k : 2 * half + E * (kc + copies));
+            if (col2[v] >= p.d) col2[v] = -1;
+        }
+    }
+    Chunk<TI, E> a[2][kOwn], c[2][kOwn];
+    auto load = [&](int h) {  // heads h and h + 1 (the last one again past the end)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int hg = min(h + g, h1 - 1);
+            const RopeSide& s = p.side[hg >= p.side[0].H ? 1 : 0];
+            const int hh = hg >= p.side[0].H ? hg - p.side[0].H : hg;
+            const TI* x = static_cast<const TI*>(s.x) + b * s.xb + (long long)hh * s.xh + (long long)n * s.xn;
+#pragma unroll
+            for (int v = 0; v < kOwn; ++v) {
+                if (col[v] >= 0) a[g][v].load(x + col[v]);
+                if (kTwo && col2[v] >= 0) c[g][v].load(x + col2[v]);
+            }
+        }
+    };
+    load(h0);
     // cos and sin of this thread's pairs
     float cs[kUnitPairs], sn[kUnitPairs];
-    int first = 0, step = 1;  // pair of e: first + step * e
-    if (rotates) {
-        if constexpr (MODE == kHalfScalar) {
-            first = u;
-            step = p.pair_units;
-        } else {
-            first = u * kUnitPairs;
-        }
+    {
         const unsigned long long pos = (unsigned long long)(long long)p.positions[b * p.pos_b + n];
 #pragma unroll
         for (int e = 0; e < kUnitPairs; ++e) {
-            const int i = first + step * e;
+            const int i = kJobPairs * (u + p.units * (e / kJobPairs)) + e % kJobPairs;
             cs[e] = 1.f;
             sn[e] = 0.f;
             if (i < half) {
                 const unsigned long long phase = pos * s_turn[i];
                 // [-1, 1): the angle in units of pi
                 const float x = (float)(int)(unsigned)(phase >> 32) * 4.656612873077393e-10f;
-                float s, c;
-                sincospif(x, &s, &c);
-                cs[e] = c * p.mag;
+                float s, co;
+                sincospif(x, &s, &co);
+                cs[e] = co * p.mag;
                 sn[e] = (p.inverse ? -s : s) * p.mag;
             }
         }
     }
-#pragma unroll 2
-    for (int h = h0; h < h1; ++h) {
-        const bool is_k = h >= p.side[0].H;
-        const RopeSide& s = p.side[is_k ? 1 : 0];
-        const int hh = is_k ? h - p.side[0].H : h;
-        const TI* x = static_cast<const TI*>(s.x) + b * s.xb + (long long)hh * s.xh + (long long)n * s.xn;
-        TO* o = static_cast<TO*>(s.out) + b * s.ob + (long long)hh * s.oh + (long long)n * s.on;
-        if constexpr (MODE == kHalfScalar) {
-            if (rotates) {
-                float a[kUnitPairs], c[kUnitPairs];
+    for (int h = h0; h < h1; h += 2) {
 #pragma unroll
-                for (int e = 0; e < kUnitPairs; ++e) {
-                    const int i = first + step * e;
-                    if (i < half) {
-                        a[e] = to_f32(x[i]);
-                        c[e] = to_f32(x[i + half]);
+        for (int g = 0; g < 2; ++g) {
+            if (h + g >= h1) break;
+            const RopeSide& s = p.side[h + g >= p.side[0].H ? 1 : 0];
+            const int hh = h + g >= p.side[0].H ? h + g - p.side[0].H : h + g;
+            TO* o = static_cast<TO*>(s.out) + b * s.ob + (long long)hh * s.oh + (long long)n * s.on;
+#pragma unroll
+            for (int v = 0; v < kOwn; ++v) {
+                if (col[v] < 0) continue;
+                float x0[E], x1[E], y0[E], y1[E];
+                a[g][v].get(x0);
+                if constexpr (kTwo) {
+                    c[g][v].get(x1);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const float co = cs[v * kJobPairs + e], si = sn[v * kJobPairs + e];
+                        y0[e] = turns[v] ? x0[e] * co - x1[e] * si : x0[e];
+                        y1[e] = turns[v] ? x0[e] * si + x1[e] * co : x1[e];
+                    }
+                    if (col2[v] >= 0) store_chunk<E>(o + col2[v], y1);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) {
+                        const float co = cs[v * kJobPairs + e], si = sn[v * kJobPairs + e];
+                        const bool in = col[v] / 2 + e < half;
+                        y0[2 * e] = in ? x0[2 * e] * co - x0[2 * e + 1] * si : x0[2 * e];
+                        y0[2 * e + 1] = in ? x0[2 * e] * si + x0[2 * e + 1] * co : x0[2 * e + 1];
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < kUnitPairs; ++e) {
-                    const int i = first + step * e;
-                    if (i < half) {
-                        o[i] = from_f32<TO>(a[e] * cs[e] - c[e] * sn[e]);
-                        o[i + half] = from_f32<TO>(a[e] * sn[e] + c[e] * cs[e]);
-                    }
-                }
-            } else {
-                for (int i = 2 * half + (u - p.pair_units); i < p.d; i += p.units - p.pair_units)
-                    o[i] = from_f32<TO>(to_f32(x[i]));
-            }
-        } else if (MODE == kHalfVec && rotates) {
-            float a[8], c[8], ra[8], rc[8];
-            load8(x + first, a);
-            load8(x + first + half, c);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                ra[e] = a[e] * cs[e] - c[e] * sn[e];
-                rc[e] = a[e] * sn[e] + c[e] * cs[e];
-            }
-            store8(o + first, ra);
-            store8(o + first + half, rc);
-        } else {
-            // 16 consecutive columns: interleaved pairs, or columns to copy
-            const int col = rotates ? 2 * first : 2 * (MODE == kInterVec ? kUnitPairs * p.pair_units : half) +
-                                                      16 * (u - p.pair_units);
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                if (col + 8 * v < p.d) {
-                    float a[8];
-                    load8(x + col + 8 * v, a);
-                    if (MODE == kInterVec && rotates) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float c = cs[4 * v + e], sx = sn[4 * v + e];
-                            const float r0 = a[2 * e] * c - a[2 * e + 1] * sx;
-                            const float r1 = a[2 * e] * sx + a[2 * e + 1] * c;
-                            if (first + 4 * v + e < half) {  // pairs past the rotated part stay
-                                a[2 * e] = r0;
-                                a[2 * e + 1] = r1;
-                            }
-                        }
-                    }
-                    store8(o + col + 8 * v, a);
-                }
+                store_chunk<E>(o + col[v], y0);
             }
         }
+        if (h + 2 < h1) load(h + 2);
     }
 }
 
@@ -258,18 +289,28 @@ attn_status_t launch_rope(const void* q, const void* k, void* q_out, void* k_out
     p.pairs = rotary_dim / 2;
     p.inverse = inverse;
     p.mag = magnitude;
-    p.pair_units = (p.pairs + kUnitPairs - 1) / kUnitPairs;
-    const int mode = interleaved ? kInterVec : (p.pairs % 8 == 0 ? kHalfVec : kHalfScalar);
-    // columns left to copy, 16 to a unit
-    const int rest = mode == kInterVec ? d - 2 * kUnitPairs * p.pair_units : d - rotary_dim;
-    p.units = p.pair_units + (rest > 0 ? (rest + 15) / 16 : 0);
+    const bool f32 = in_dtype == ATTN_OUT_F32 && out_dtype == ATTN_OUT_F32;
+    const int chunk = f32 ? 4 : 8;  // columns (the kernel's E)
+    const int mode = interleaved ? kInterVec : (p.pairs % chunk == 0 ? kHalfVec : kHalfScalar);
+    if (mode == kInterVec) {
+        p.jobs = d / chunk;
+        p.turn_jobs = p.jobs;  // (pairs past the rotated part stay as they are)
+        p.units = (p.jobs + 16 / chunk - 1) / (16 / chunk);
+    } else {
+        const int e = mode == kHalfVec ? chunk : 1;
+        p.turn_jobs = p.pairs / e;
+        p.jobs = p.turn_jobs + ((d - rotary_dim) / e + 1) / 2;
+        p.units = (p.jobs + kUnitPairs / e - 1) / (kUnitPairs / e);
+    }
     p.heads = Hq + (k ? Hkv : 0);
-    // As many heads to a thread as leave about 1024 threads for every SM: the
-    // angles are computed once per thread, and a call of few tokens spreads
-    // over the heads instead.
+    // Up to 8 heads to a thread (their angles are computed once), fewer where that
+    // leaves less than 1024 threads for every SM: a call of few tokens spreads over
+    // the heads instead.  (All 40 heads of a prefill's token on one thread: 123 us
+    // for 671 MB, 1.35 waves of blocks; 8: see the table of measurements.)
     const long long per_head = p.tokens * p.units;
     long long hpt = per_head * p.heads / ((long long)dev.num_sms * 1024);
-    hpt = hpt < 1 ? 1 : (hpt > p.heads ? p.heads : hpt);
+    hpt = hpt < 1 ? 1 : (hpt > 8 ? 8 : hpt);
+    if (hpt > p.heads) hpt = p.heads;
     const long long groups_min = (p.heads + 65534) / 65535;
     if (hpt < groups_min) hpt = groups_min;
     p.heads_per_thread = (int)hpt;

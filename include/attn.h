@@ -410,9 +410,10 @@ attn_status_t attn_decode_noalloc(const void* q, const void* k_cache, const void
  * Around the attention: positions, the paged cache, drafted tokens.
  *
  * Strides of these entry points are HOST arrays {batch, head, token} in
- * elements of a [B, H, N, d] view whose last dimension is contiguous; rows are
- * 16-byte aligned (strides multiples of 8 bf16 or 4 fp32 elements).  A packed
- * [total, H, d] array is B = 1, N = total with strides {0, d, H * d}.
+ * elements of a [B, H, N, d] view whose last dimension is contiguous (NULL: the
+ * whole array is); rows are 16-byte aligned (strides multiples of 8 bf16 or 4
+ * fp32 elements).  A packed [total, H, d] array is B = 1, N = total with strides
+ * {0, d, H * d}.
  * ------------------------------------------------------------------------- */
 
 typedef enum {

@@ -37,7 +37,7 @@ def rope(lib, **kw):
     (dict(q=None), 1), (dict(qo=None), 1), (dict(pos=None), 1), (dict(f=None), 1), (dict(f=FAKE + 4), 1),
     (dict(q=FAKE + 8), 1), (dict(k=None), 1), (dict(ko=None), 1), (dict(k=None, ko=None), 1), (dict(B=0), 1),
     (dict(N=0), 1), (dict(rot=0), 1), (dict(rot=3), 1), (dict(rot=130), 1), (dict(inter=2), 1), (dict(inv=-1), 1),
-    (dict(mag=float("nan")), 1), (dict(ps=-1), 1), (dict(idt=5), 1), (dict(odt=2), 1), (dict(qs=None), 1),
+    (dict(mag=float("nan")), 1), (dict(ps=-1), 1), (dict(idt=5), 1), (dict(odt=2), 1), (dict(qs=None, d=100, rot=100), 2),
     (dict(qs=strides(4096, 1024, 100)), 1), (dict(qos=strides(4096, 1024, 0)), 1),
     (dict(qos=strides(4096, 1024, 64)), 1), (dict(qos=strides(4096, 64, 128)), 1),
     (dict(qos=strides(2048, 1024, 128)), 1), (dict(qo=FAKE, odt=1), 1),
