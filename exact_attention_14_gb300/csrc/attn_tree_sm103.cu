@@ -11,10 +11,10 @@
 // This file: the kernel for up to 16 query rows at a time on mma.sync
 // (m16n8k16; more rows of head dims up to 128 go to attn_tree_tc_sm103.cu), and
 // the merge of cut items (tree_plan.h has the work list).  A producer warp
-// streams 64-key tiles of K and V (and their descales) by TMA into a ring; each
-// of four consumer warps takes 16 keys of every tile with its own online
-// softmax (base 2), and the four are merged through shared memory at the end of
-// a piece.  Bound: HBM (each cached byte is read once per row tile).
+// streams 64-key tiles of K and V (and their descales) by TMA into a ring; two
+// pairs of consumer warps take the tiles in turn, 32 keys a warp, each with its
+// own online softmax (base 2), and the four are merged through shared memory at
+// the end of a piece.  Bound: HBM (each cached byte is read once per row tile).
 //
 // The products are transposed, S^T = K Q^T and O^T = V^T P^T: keys and columns
 // are the 16 rows of an MMA and the query rows its 8 columns, so up to 8 query
@@ -61,14 +61,17 @@ struct TreeCfg {
     static constexpr int kBoxes = F8 ? D / 128 : D / 64;
     static constexpr int kHalf = kBoxes * kTileKeys * 128;
     static constexpr int kDescale = F8 ? 2 * kTileKeys * 4 : 0;  // kd, vd of a tile
-    static constexpr int kStage = 2 * kHalf + (F8 ? 1024 : 0);   // (tiles stay 1024-byte aligned)
+    static constexpr int kStage = 2 * kHalf + kDescale;  // (the descales lie behind the tiles of all stages)
     static constexpr int kScratchBytes = 2 * kRows * D * 4;      // O of two warps
     // 228 KiB to an SM, 1 KiB of it the system's for each CTA
     static constexpr int kBudget = (228 / kCtas - 1) * 1024;
     static constexpr int kFit = (kBudget - kScratchBytes - 1024) / kStage;
-    static constexpr int kStages = kFit < 6 ? kFit : 6;
+    // an even number: every slot belongs to one pair of warps, which then sees each
+    // of its barrier's phases
+    static constexpr int kStages = kFit < 6 ? kFit / 2 * 2 : 6;
     static_assert(kStages >= 2, "ring");
-    static constexpr int kScratch = kStages * kStage;
+    static constexpr int kDs = kStages * 2 * kHalf;  // the descales
+    static constexpr int kScratch = kDs + kStages * kDescale;
     static constexpr int kBar = kScratch + kScratchBytes;
     static constexpr int kSmem = kBar + 1024;
 };
@@ -209,7 +212,7 @@ __device__ __forceinline__ void produce(const CUtensorMap* tk, const CUtensorMap
             if (lane == 0) mbar_arrive_expect_tx(bar, 2 * C::kHalf + C::kDescale);
             __syncwarp();
             if (lane < boxes) {
-                const uint32_t dk = smem_u32(smem + slot * C::kStage);
+                const uint32_t dk = smem_u32(smem + slot * 2 * C::kHalf);
                 const uint32_t dv = dk + C::kHalf;
 #pragma unroll
                 for (int c = 0; c < C::kBoxes; ++c) {
@@ -220,7 +223,7 @@ __device__ __forceinline__ void produce(const CUtensorMap* tk, const CUtensorMap
                 if constexpr (F8) {
                     // a missing page's codes are zeros: any descale that exists will do
                     const long long at = ((long long)(my_page < 0 ? 0 : my_page) * p.Hkv + w.h) * p.page_size + my_off;
-                    const uint32_t ds = dk + 2 * C::kHalf + lane * p.box_keys * 4;
+                    const uint32_t ds = smem_u32(smem + C::kDs + slot * C::kDescale) + lane * p.box_keys * 4;
                     bulk_load(ds, p.k_descale + at, p.box_keys * 4, bar);
                     bulk_load(ds + kTileKeys * 4, p.v_descale + at, p.box_keys * 4, bar);
                 }
@@ -259,7 +262,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the merge waits by itself)
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(smem_u32(&bars->full[i]), 1);
-            mbar_init(smem_u32(&bars->empty[i]), kConsumers);
+            mbar_init(smem_u32(&bars->empty[i]), 2);
         }
         bars->abort = 0;
         fence_barrier_init();
@@ -273,9 +276,9 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     const volatile int* abort_flag = &bars->abort;
     const int qr = lane >> 2, qc = lane & 3;
     const int mi = lane >> 3, ri = lane & 7;
-    const int wk0 = warp * 16;
-    // this lane's two keys of the warp's 16 are k_lane and k_lane + 8 (E4M3: an
-    // order that keeps a quarter-warp's 16-byte loads on different banks)
+    const int pair = warp >> 1, wk0 = (warp & 1) * 32;
+    // this lane's keys of the warp's 32 are k_lane + 8 i, i < 4 (E4M3: an order that
+    // keeps a quarter-warp's 16-byte loads on different banks)
     const int k_lane = F8 ? (qr >> 1) + 4 * (qr & 1) : qr;
     const int v_chunk = (qr >> 1) + 4 * (qr & 1);  // E4M3: 16-byte chunk of a V row's 128 columns
     // column of an accumulator element: MMA row qr + 8 hi of tile mt
@@ -360,46 +363,49 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         int fexp = -126;  // E4M3: F = 2^fexp
 
         for (int kt = w.k0; kt < w.k1; ++kt, ++used) {
+            if ((int)(used & 1) != pair) continue;  // the other pair's tile
             const int slot = (int)(used % C::kStages);
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->full[slot]),
                                                    (uint32_t)((used / C::kStages) & 1), abort_flag));
             if (!ok) break;
             const int key0 = kt * kTileKeys + wk0;  // this warp's first key
-            const int nvalid = min(16, w.keys - key0);
-            const uint32_t sK = smem_u32(smem + slot * C::kStage);
+            const int nvalid = min(32, w.keys - key0);
+            const uint32_t sK = smem_u32(smem + slot * 2 * C::kHalf);
             const uint32_t sV = sK + C::kHalf;
+            const uint32_t sD = smem_u32(smem + C::kDs + slot * C::kDescale);
             bool wrote = false;
             if (nvalid > 0) {
-                // ---- S^T: elements 0, 1 key k_lane, 2, 3 key k_lane + 8; rows 8 nt + 2 qc + {0, 1}
-                float sf[NT][4];
-                float vd[2] = {1.f, 1.f};  // E4M3: V's descale of this lane's keys
-                {
+                const bool plain = key0 + 32 <= prefix;  // every row sees all 32 keys
+                // ---- S^T: sf[i >> 1][.][2 (i & 1) + r] is key k_lane + 8 i, row 8 nt + 2 qc + r
+                float sf[2][NT][4];
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
                     float s2[NT][4];  // (two chains of products)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sf[nt][e] = s2[nt][e] = 0.f;
+                        for (int e = 0; e < 4; ++e) sf[g][nt][e] = s2[nt][e] = 0.f;
                     if constexpr (!F8) {
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks) {
                             uint32_t a[4];
-                            ldsm4(sK + tile_off(wk0 + (mi & 1) * 8 + ri, ks * 2 + (mi >> 1)), a[0], a[1], a[2], a[3]);
+                            ldsm4(sK + tile_off(wk0 + 16 * g + (mi & 1) * 8 + ri, ks * 2 + (mi >> 1)), a[0], a[1], a[2], a[3]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma16816<false>(ks & 1 ? s2[nt] : sf[nt], a, qb[nt][ks][0], qb[nt][ks][1]);
+                                mma16816<false>(ks & 1 ? s2[nt] : sf[g][nt], a, qb[nt][ks][0], qb[nt][ks][1]);
                         }
                     } else {
 #pragma unroll
                         for (int blk = 0; blk < D / 64; ++blk) {
-                            const uint4 x = lds128(sK + tile_off(wk0 + k_lane, blk * 4 + qc));
-                            const uint4 y = lds128(sK + tile_off(wk0 + k_lane + 8, blk * 4 + qc));
+                            const uint4 x = lds128(sK + tile_off(wk0 + 16 * g + k_lane, blk * 4 + qc));
+                            const uint4 y = lds128(sK + tile_off(wk0 + 16 * g + k_lane + 8, blk * 4 + qc));
                             const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const uint32_t a[4] = {e4m3_lo(xw[k]), e4m3_lo(yw[k]), e4m3_hi(xw[k]), e4m3_hi(yw[k])};
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
-                                    mma16816<true>(k & 1 ? s2[nt] : sf[nt], a, qb[nt][4 * blk + k][0],
+                                    mma16816<true>(k & 1 ? s2[nt] : sf[g][nt], a, qb[nt][4 * blk + k][0],
                                                    qb[nt][4 * blk + k][1]);
                             }
                         }
@@ -407,135 +413,130 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sf[nt][e] += s2[nt][e];
+                        for (int e = 0; e < 4; ++e) sf[g][nt][e] += s2[nt][e];
                 }
-                // E4M3: V's codes are on their way while the softmax runs
-                uint4 vr[F8 ? D / 128 : 1][4];
-                auto load_v = [&]() {
+                // ---- scale, mask
+                float wv[4];  // E4M3: V's descale of this lane's keys
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float kd = 1.f;
+                    wv[i] = 1.f;
                     if constexpr (F8) {
-#pragma unroll
-                        for (int hf = 0; hf < D / 128; ++hf)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                vr[hf][i] = lds128(sV + tile_off(wk0 + qc + 4 * i, hf * 8 + v_chunk));
+                        kd = lds32f(sD + (wk0 + k_lane + 8 * i) * 4);
+                        wv[i] = lds32f(sD + (kTileKeys + wk0 + k_lane + 8 * i) * 4);
                     }
-                };
-                if constexpr (D == 128) load_v();
-                // ---- scale, mask, running maximum
-                const bool drafted = key0 + nvalid > prefix;  // some of the keys are drafted tokens
-                float kd[2] = {1.f, 1.f};
-                if constexpr (F8) {
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const uint32_t at = sK + 2 * C::kHalf + (wk0 + k_lane + 8 * g) * 4;
-                        kd[g] = lds32f(at);
-                        vd[g] = k_lane + 8 * g < nvalid ? lds32f(at + kTileKeys * 4) : 0.f;
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            sf[i >> 1][nt][2 * (i & 1) + r] *= F8 ? qs[nt][r] * kd : qs[nt][r];
                 }
-                float al[NT][2], ms[NT][2];
-                bool moved = false;
+                unsigned bad = 0u;  // of the 32 keys: drafted rows of V with a NaN or an infinity
+                if (!plain) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float mx[2] = {-INFINITY, -INFINITY};
+                    for (int i = 0; i < 4; ++i) {
+                        const int kk = k_lane + 8 * i;
+                        if (kk >= nvalid) wv[i] = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int kk = k_lane + 8 * (e >> 1);
-                        float v = sf[nt][e] * (F8 ? qs[nt][e & 1] * kd[e >> 1] : qs[nt][e & 1]);
-                        if (kk >= nvalid) v = -INFINITY;
-                        if (drafted && kk < nvalid && key0 + kk >= prefix &&
-                            !tree_sees(p, w.b, tok[nt][e & 1], key0 + kk - prefix))
-                            v = -INFINITY;
-                        sf[nt][e] = v;
-                        mx[e & 1] = fmaxf(mx[e & 1], v);
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                if (kk >= nvalid ||
+                                    (key0 + kk >= prefix && !tree_sees(p, w.b, tok[nt][r], key0 + kk - prefix)))
+                                    sf[i >> 1][nt][2 * (i & 1) + r] = -INFINITY;
                     }
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], 4));
-                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], 8));
-                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], 16));
-                        const float mn = fmaxf(m[nt][r], mx[r]);
-                        ms[nt][r] = mn == -INFINITY ? 0.f : mn;  // (no key yet: every P is 0)
-                        al[nt][r] = ex2(m[nt][r] - ms[nt][r]);
-                        m[nt][r] = mn;
-                    }
-                }
-                // ---- V rows that must not enter the product
-                unsigned bad = 0u;  // of the 16 keys: drafted rows with a NaN or an infinity
-                if (drafted) {
-                    for (int i = lane; i < 16 * (F8 ? D / 16 : D / 8); i += 32) {
-                        const int kk = i & 15;
+                    for (int i = lane; i < 32 * (F8 ? D / 16 : D / 8); i += 32) {
+                        const int kk = i & 31;
                         if (kk < nvalid && key0 + kk >= prefix &&
-                            not_finite<F8>(lds128(sV + tile_off(wk0 + kk, i >> 4))))
+                            not_finite<F8>(lds128(sV + tile_off(wk0 + kk, i >> 5))))
                             bad |= 1u << kk;
                     }
                     if constexpr (F8) {
                         if (lane < nvalid && key0 + lane >= prefix &&
-                            !isfinite(lds32f(sK + 2 * C::kHalf + kTileKeys * 4 + (wk0 + lane) * 4)))
+                            !isfinite(lds32f(sD + (kTileKeys + wk0 + lane) * 4)))
                             bad |= 1u << lane;
                     }
                     bad = __reduce_or_sync(0xFFFFFFFFu, bad);
+                    if constexpr (F8) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (bad >> (k_lane + 8 * i) & 1u) wv[i] = 0.f;
+                    }
                 }
-                // ---- P
-                float grow = 1.f;  // E4M3: F_old / F_new
-                float wv[2] = {1.f, 1.f};
-                if constexpr (F8) {
-                    float top = 0.f;
+                // ---- running maximum
+                float mx[NT][2];
+                bool moved = false;
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        wv[g] = bad >> (k_lane + 8 * g) & 1u ? 0.f : vd[g];
-                        top = fmaxf(top, fabsf(wv[g]));
-                    }
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-                    // 2^need > top (the same in every lane)
-                    const int need = max(min((int)(__float_as_uint(top) >> 23) - 126, 111), -100);
-                    if (need > fexp) {
-                        grow = fexp - need < -126 ? 0.f : pow2i(fexp - need);
-                        fexp = need;
-                    }
-                    const float fr = kPFrame * pow2i(-fexp);
-                    wv[0] *= fr;
-                    wv[1] *= fr;
-                }
-                uint32_t pb[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float pr[4], add[2] = {0.f, 0.f}, addx[2] = {0.f, 0.f};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        pr[e] = ex2(sf[nt][e] - ms[nt][e & 1]);
-                        addx[e & 1] += pr[e];
-                    }
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        if constexpr (F8) {
-                            pb[nt][g] = pack_f16x2(pr[2 * g] * wv[g], pr[2 * g + 1] * wv[g]);
-                        } else {
-                            pb[nt][g] = pack_bf16x2(pr[2 * g], pr[2 * g + 1]);
-                            add[0] += bf16lo_to_f32(pb[nt][g]);
-                            add[1] += bf16hi_to_f32(pb[nt][g]);
-                        }
-                        pb[nt][g] = transpose8x8(pb[nt][g]);
-                    }
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        xs[nt][r] = xs[nt][r] * al[nt][r] + addx[r];
-                        l[nt][r] = l[nt][r] * al[nt][r] + (F8 ? addx[r] : add[r]);
-                        al[nt][r] *= grow;
-                        moved |= al[nt][r] != 1.f;
+                        float x = fmaxf(fmaxf(sf[0][nt][r], sf[0][nt][2 + r]), fmaxf(sf[1][nt][r], sf[1][nt][2 + r]));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                        mx[nt][r] = x;
+                        moved |= x > m[nt][r];
                     }
+                if constexpr (F8) {
+                    const float f = pow2i(fexp);
+                    moved |= fmaxf(fmaxf(fabsf(wv[0]), fabsf(wv[1])), fmaxf(fabsf(wv[2]), fabsf(wv[3]))) > f;
                 }
                 if (__any_sync(0xFFFFFFFFu, moved)) {
+                    float grow = 1.f;  // E4M3: F_old / F_new
+                    if constexpr (F8) {
+                        float top = fmaxf(fmaxf(fabsf(wv[0]), fabsf(wv[1])), fmaxf(fabsf(wv[2]), fabsf(wv[3])));
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            acc[i][nt][0] *= al[nt][0];
-                            acc[i][nt][1] *= al[nt][1];
-                            acc[i][nt][2] *= al[nt][0];
-                            acc[i][nt][3] *= al[nt][1];
+                        for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+                        // 2^need > top (the same in every lane)
+                        const int need = max(min((int)(__float_as_uint(top) >> 23) - 126, 111), -100);
+                        if (need > fexp) {
+                            grow = fexp - need < -126 ? 0.f : pow2i(fexp - need);
+                            fexp = need;
                         }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float mn = fmaxf(m[nt][r], mx[nt][r]);
+                            float al = ex2(m[nt][r] - (mn == -INFINITY ? 0.f : mn));  // (no key yet: 0)
+                            m[nt][r] = mn;
+                            xs[nt][r] *= al;
+                            l[nt][r] *= al;
+                            al *= grow;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                acc[i][nt][r] *= al;
+                                acc[i][nt][2 + r] *= al;
+                            }
+                        }
+                }
+                // ---- P^T
+                if constexpr (F8) {
+                    const float fr = kPFrame * pow2i(-fexp);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) wv[i] *= fr;
+                }
+                uint32_t pb[2][NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float p0 = ex2(sf[i >> 1][nt][2 * (i & 1)] - m0);
+                        const float p1 = ex2(sf[i >> 1][nt][2 * (i & 1) + 1] - m1);
+                        xs[nt][0] += p0;
+                        xs[nt][1] += p1;
+                        uint32_t pk;
+                        if constexpr (F8) {
+                            pk = pack_f16x2(p0 * wv[i], p1 * wv[i]);  // (O over the sum of unrounded P)
+                        } else {
+                            pk = pack_bf16x2(p0, p1);
+                            l[nt][0] += bf16lo_to_f32(pk);
+                            l[nt][1] += bf16hi_to_f32(pk);
+                        }
+                        pb[i >> 1][nt][i & 1] = transpose8x8(pk);
+                    }
                 }
                 // ---- rows past the sequence, and rows with a NaN or an infinity:
                 // the latter are added to the rows that see them, both are zeroed
@@ -548,14 +549,14 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
-                                const float sv = __shfl_sync(0xFFFFFFFFu, kk < 8 ? sf[nt][r] : sf[nt][2 + r],
-                                                             4 * qr_of + qc);
+                                const float own = kk < 16 ? (kk < 8 ? sf[0][nt][r] : sf[0][nt][2 + r])
+                                                          : (kk < 24 ? sf[1][nt][r] : sf[1][nt][2 + r]);
+                                const float sv = __shfl_sync(0xFFFFFFFFu, own, 4 * qr_of + qc);
                                 // (-1: not seen)
-                                pk[nt][r] = sv == -INFINITY ? -1.f : ex2(sv - ms[nt][r]);
+                                pk[nt][r] = sv == -INFINITY ? -1.f : ex2(sv - (m[nt][r] == -INFINITY ? 0.f : m[nt][r]));
                             }
                         float fr = 1.f;
-                        if constexpr (F8)
-                            fr = lds32f(sK + 2 * C::kHalf + kTileKeys * 4 + (wk0 + kk) * 4) * kPFrame * pow2i(-fexp);
+                        if constexpr (F8) fr = lds32f(sD + (kTileKeys + wk0 + kk) * 4) * kPFrame * pow2i(-fexp);
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -583,40 +584,44 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     }
                     __syncwarp();
                 }
-                const unsigned zero = bad | (nvalid < 16 ? (0xFFFFu << nvalid) & 0xFFFFu : 0u);
+                const unsigned zero = bad | (nvalid < 32 ? 0xFFFFFFFFu << nvalid : 0u);
                 if (zero) {
-                    for (int i = lane; i < 16 * (F8 ? D / 16 : D / 8); i += 32)
-                        if (zero >> (i & 15) & 1u) sts128(sV + tile_off(wk0 + (i & 15), i >> 4), 0u, 0u, 0u, 0u);
+                    for (int i = lane; i < 32 * (F8 ? D / 16 : D / 8); i += 32)
+                        if (zero >> (i & 31) & 1u) sts128(sV + tile_off(wk0 + (i & 31), i >> 5), 0u, 0u, 0u, 0u);
                     wrote = true;
                     __syncwarp();
                 }
-                if (F8 && (D > 128 || zero)) load_v();
                 // ---- O^T += V^T P^T
-                if constexpr (!F8) {
 #pragma unroll
-                    for (int mt = 0; mt < D / 16; ++mt) {
-                        uint32_t a[4];
-                        ldsm4_t(sV + tile_off(wk0 + (mi >> 1) * 8 + ri, mt * 2 + (mi & 1)), a[0], a[1], a[2], a[3]);
+                for (int g = 0; g < 2; ++g) {
+                    if constexpr (!F8) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816<false>(acc[mt][nt], a, pb[nt][0], pb[nt][1]);
-                    }
-                } else {
-                    // P's k index 2 qc + {0, 1, 8, 9} is key qc + {0, 4, 8, 12}
+                        for (int mt = 0; mt < D / 16; ++mt) {
+                            uint32_t a[4];
+                            ldsm4_t(sV + tile_off(wk0 + 16 * g + (mi >> 1) * 8 + ri, mt * 2 + (mi & 1)), a[0], a[1], a[2], a[3]);
 #pragma unroll
-                    for (int hf = 0; hf < D / 128; ++hf) {
-                        const uint4 r0 = vr[hf][0], r1 = vr[hf][1], r2 = vr[hf][2], r3 = vr[hf][3];
-                        const uint32_t a0[4] = {r0.x, r0.y, r0.z, r0.w}, a1[4] = {r1.x, r1.y, r1.z, r1.w};
-                        const uint32_t a2[4] = {r2.x, r2.y, r2.z, r2.w}, a3[4] = {r3.x, r3.y, r3.z, r3.w};
+                            for (int nt = 0; nt < NT; ++nt) mma16816<false>(acc[mt][nt], a, pb[g][nt][0], pb[g][nt][1]);
+                        }
+                    } else {
+                        // P's k index 2 qc + {0, 1, 8, 9} is key qc + {0, 4, 8, 12}
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const uint32_t x01 = __byte_perm(a0[g], a1[g], 0x5140), y01 = __byte_perm(a0[g], a1[g], 0x7362);
-                            const uint32_t x23 = __byte_perm(a2[g], a3[g], 0x5140), y23 = __byte_perm(a2[g], a3[g], 0x7362);
-                            const uint32_t u[4] = {e4m3_lo(x01), e4m3_hi(x01), e4m3_lo(x23), e4m3_hi(x23)};
-                            const uint32_t v[4] = {e4m3_lo(y01), e4m3_hi(y01), e4m3_lo(y23), e4m3_hi(y23)};
+                        for (int hf = 0; hf < D / 128; ++hf) {
+                            const uint32_t at = sV + tile_off(wk0 + 16 * g + qc, hf * 8 + v_chunk);
+                            const uint32_t at4 = sV + tile_off(wk0 + 16 * g + qc + 4, hf * 8 + v_chunk);
+                            const uint4 r0 = lds128(at), r1 = lds128(at4), r2 = lds128(at + 1024), r3 = lds128(at4 + 1024);
+                            const uint32_t a0[4] = {r0.x, r0.y, r0.z, r0.w}, a1[4] = {r1.x, r1.y, r1.z, r1.w};
+                            const uint32_t a2[4] = {r2.x, r2.y, r2.z, r2.w}, a3[4] = {r3.x, r3.y, r3.z, r3.w};
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                mma16816<true>(acc[8 * hf + 2 * g][nt], u, pb[nt][0], pb[nt][1]);
-                                mma16816<true>(acc[8 * hf + 2 * g + 1][nt], v, pb[nt][0], pb[nt][1]);
+                            for (int q = 0; q < 4; ++q) {
+                                const uint32_t x01 = __byte_perm(a0[q], a1[q], 0x5140), y01 = __byte_perm(a0[q], a1[q], 0x7362);
+                                const uint32_t x23 = __byte_perm(a2[q], a3[q], 0x5140), y23 = __byte_perm(a2[q], a3[q], 0x7362);
+                                const uint32_t u[4] = {e4m3_lo(x01), e4m3_hi(x01), e4m3_lo(x23), e4m3_hi(x23)};
+                                const uint32_t v[4] = {e4m3_lo(y01), e4m3_hi(y01), e4m3_lo(y23), e4m3_hi(y23)};
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    mma16816<true>(acc[8 * hf + 2 * q][nt], u, pb[g][nt][0], pb[g][nt][1]);
+                                    mma16816<true>(acc[8 * hf + 2 * q + 1][nt], v, pb[g][nt][0], pb[g][nt][1]);
+                                }
                             }
                         }
                     }
@@ -643,7 +648,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 if (qr == 0) {
                     const int row = 8 * nt + 2 * qc + r;
                     bars->m[warp][row] = m[nt][r];
-                    bars->l[warp][row] = l[nt][r];
+                    bars->l[warp][row] = F8 ? xs[nt][r] : l[nt][r];
                     bars->x[warp][row] = xs[nt][r];
                 }
             }
