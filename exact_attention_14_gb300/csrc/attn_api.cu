@@ -121,10 +121,14 @@ attn_status_t encode_tmap_pages(CUtensorMap* map, const void* base, bool e4m3, i
                              (cuuint64_t)page_size * Hkv * d * es};
     cuuint32_t box[4] = {(cuuint32_t)(128 / es), 1u, (cuuint32_t)box_keys, 1u};
     cuuint32_t elem[4] = {1u, 1u, 1u, 1u};
+    // a key's row of one head is d * es bytes, its neighbour another head's, which
+    // another CTA reads at another time: 256-byte L2 fetches of 128-byte rows are
+    // half wasted (decode over 8 heads of 128 codes: 4442 -> 5251 GB/s)
     CUresult r = g_encode(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                           const_cast<void*>(base), dims, strides, box, elem,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                          (long long)d * (long long)es < 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                             : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
