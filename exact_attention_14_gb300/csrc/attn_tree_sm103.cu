@@ -766,20 +766,22 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 }
 
 // A block takes the `group_rows` rows of a (sequence, KV head) that lie next to
-// each other in a partial result, kMergeCols columns of every column lane at a
-// time (other blocks may take other columns), and merges the pieces of their item, if it was cut, by log-sum-exp in piece
-// order: M = max lse_p, O = sum 2^(lse_p - M) o_p / sum 2^(lse_p - M).  Rows past
-// the sequence's drafted tokens get O = 0, LSE = -inf.  It is short and all
-// latency, so every load of a step is in flight at once; it starts while the
+// each other in a partial result, and merges the pieces of their item, if it was
+// cut, by log-sum-exp in piece order: M = max lse_p, O = sum 2^(lse_p - M) o_p /
+// sum 2^(lse_p - M).  Rows past the sequence's drafted tokens get O = 0, LSE =
+// -inf.  A thread keeps to one row and CPT of its columns (blocks along y have
+// other columns).  It is short and all latency (list, lse, partials, one after
+// the other), so many loads of a thread are in flight, and it starts while the
 // attention kernel ends (programmatic launch) and waits for it before it reads.
-constexpr int kMergeThreads = 128;
-constexpr int kMergeCols = 4;
-constexpr int kMergePieces = 8;  // pieces whose loads are in flight together
+constexpr int kMergeThreads = 256;
 
-__global__ void __launch_bounds__(kMergeThreads)
+template <int CPT>
+__global__ void __launch_bounds__(kMergeThreads, 4)
 attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
-    extern __shared__ float s_w[];  // [pieces][group_rows]: lse, then weights
-    __shared__ __align__(16) float s_o[kMergeThreads * kMergeCols];
+    // pieces whose loads are in flight together (16 columns: registers for one)
+    constexpr int kPieces = CPT == 16 ? 1 : 32 / CPT;
+    extern __shared__ float s_w[];     // [pieces][group_rows]: lse
+    __shared__ __align__(16) float s_o[kMergeThreads * CPT + 32 * 4];  // rows 4 floats apart (banks)
     const int gr = p.group_rows;
     const int R = p.T * p.G;
     const int groups = (R + gr - 1) / gr;
@@ -795,9 +797,9 @@ attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
         n = tree_ctas(p, total);
         start += ((long long)h * s.row_tiles + r0 / p.tile_rows) * (s.key_tiles + p.extra);
         const long long first = start + p.extra, last = first + s.key_tiles - 1;  // of its key tiles
-        c0 = (int)(first * n / total);
+        c0 = (int)tree_div(first * n, total);
         while (c0 + 1 < n && tree_first(total, n, c0 + 1) <= first) ++c0;
-        c1 = (int)(last * n / total);
+        c1 = (int)tree_div(last * n, total);
         while (c1 + 1 < n && tree_first(total, n, c1 + 1) <= last) ++c1;
     }
     const bool whole = c0 == c1;  // the attention kernel writes the live rows
@@ -811,66 +813,67 @@ attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
     const int first_place = 2 * c0 + (start > tree_first(total, n, c0) ? 1 : 0);
     const int pieces = whole ? 0 : c1 - c0 + 1;
     auto place = [&](int i) { return (size_t)(i == 0 ? first_place : 2 * (c0 + i)); };
+    const bool cut = pieces > 0 && r0 + row < live;
+    // columns col0 + lane + k * lanes; the first pieces' loads do not wait for the lse
+    const size_t stride = (size_t)p.tile_rows * p.dw;  // of a place
+    const int col0 = blockIdx.y * lanes * CPT, cols = min(lanes * CPT, p.dw - col0);
+    const float* src = p.ws_o + (size_t)in_tile * p.dw + (size_t)(col0 + lane) * gr + row;
+    float v[kPieces][CPT], acc[CPT];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+            for (int k = 0; k < CPT; ++k)
+                v[i][k] = cut && i0 + i < pieces && lane + k * lanes < cols
+                              ? __ldcg(src + place(i0 + i) * stride + k * kMergeThreads)  // (lanes * gr)
+                              : 0.f;
+    };
+    load(0);
     for (int i = lane; i < pieces; i += lanes)
         s_w[i * gr + row] = __ldcg(p.ws_lse + place(i) * p.tile_rows + in_tile + row);
     __syncthreads();
-    const bool cut = pieces > 0 && r0 + row < live;
     float M = -INFINITY, sum = 0.f;
     if (cut)
         for (int i = 0; i < pieces; ++i) M = fmaxf(M, s_w[i * gr + row]);
     const float Ms = M == -INFINITY ? 0.f : M;
-    if (cut)
-        for (int i = 0; i < pieces; ++i) sum += ex2(s_w[i * gr + row] - Ms);
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) acc[k] = 0.f;
+    for (int i0 = 0; i0 < pieces; i0 += kPieces) {
+        if (i0 > 0) load(i0);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const float wt = cut && i0 + i < pieces ? ex2(s_w[(i0 + i) * gr + row] - Ms) : 0.f;
+            sum += wt;
+#pragma unroll
+            for (int k = 0; k < CPT; ++k) acc[k] = fmaf(wt, v[i][k], acc[k]);
+        }
+    }
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
     if (blockIdx.y == 0 && threadIdx.x < gr && row < rows && p.lse && (cut || r0 + row >= live)) {
         const int r = r0 + row, t = r / p.G;
         p.lse[((size_t)b * p.Hq + (size_t)h * p.G + (r - t * p.G)) * p.T + t] =
             sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2t;
     }
-    const int cols = lanes * kMergeCols;  // at a time: col0 + lane + k * lanes
-    for (int col0 = blockIdx.y * cols; col0 < p.dh; col0 += gridDim.y * cols) {
-        float acc[kMergeCols];
 #pragma unroll
-        for (int k = 0; k < kMergeCols; ++k) acc[k] = 0.f;
-        if (cut) {
-            const float* src = p.ws_o + (size_t)in_tile * p.dw + (size_t)(col0 + lane) * gr + row;
-            for (int i0 = 0; i0 < pieces; i0 += kMergePieces) {
-                float v[kMergePieces][kMergeCols];
-#pragma unroll
-                for (int i = 0; i < kMergePieces; ++i)
-#pragma unroll
-                    for (int k = 0; k < kMergeCols; ++k)
-                        v[i][k] = i0 + i < pieces
-                                      ? __ldcg(src + place(i0 + i) * p.tile_rows * p.dw + (size_t)k * lanes * gr)
-                                      : 0.f;
-#pragma unroll
-                for (int i = 0; i < kMergePieces; ++i) {
-                    const float wt = i0 + i < pieces ? ex2(s_w[(i0 + i) * gr + row] - Ms) : 0.f;
-#pragma unroll
-                    for (int k = 0; k < kMergeCols; ++k) acc[k] = fmaf(wt, v[i][k], acc[k]);
-                }
-            }
-        }
-        __syncthreads();  // (the last columns have been read)
-#pragma unroll
-        for (int k = 0; k < kMergeCols; ++k) s_o[row * cols + lane + k * lanes] = acc[k] * inv;
-        __syncthreads();
-        for (int i = threadIdx.x; i < rows * (cols / 8); i += kMergeThreads) {
-            const int ro = i / (cols / 8), cc = 8 * (i - ro * (cols / 8)), col = col0 + cc;
-            const int r = r0 + ro, t = r / p.G;
-            if (col >= p.dh || (whole && r < live)) continue;
-            const size_t at = (((size_t)b * p.Hq + (size_t)h * p.G + (r - t * p.G)) * p.T + t) * p.dh + col;
-            const float4 x = *reinterpret_cast<const float4*>(&s_o[ro * cols + cc]);
-            const float4 y = *reinterpret_cast<const float4*>(&s_o[ro * cols + cc + 4]);
-            if (p.out_f32) {
-                float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.o) + at);
-                o[0] = x;
-                o[1] = y;
-            } else {
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at) =
-                    make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y),
-                               pack_bf16x2(y.z, y.w));
-            }
+    for (int k = 0; k < CPT; ++k)
+        if (lane + k * lanes < cols) s_o[row * (cols + 4) + lane + k * lanes] = acc[k] * inv;
+    __syncthreads();
+    const int per = cols / 8;
+    for (int i = threadIdx.x; i < rows * per; i += kMergeThreads) {
+        const int ro = i / per, cc = 8 * (i - ro * per), col = col0 + cc;
+        const int r = r0 + ro, t = r / p.G;
+        if (col >= p.dh || (whole && r < live)) continue;
+        const size_t at = (((size_t)b * p.Hq + (size_t)h * p.G + (r - t * p.G)) * p.T + t) * p.dh + col;
+        const float4 x = *reinterpret_cast<const float4*>(&s_o[ro * (cols + 4) + cc]);
+        const float4 y = *reinterpret_cast<const float4*>(&s_o[ro * (cols + 4) + cc + 4]);
+        if (p.out_f32) {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.o) + at);
+            o[0] = x;
+            o[1] = y;
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at) =
+                make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y),
+                           pack_bf16x2(y.z, y.w));
         }
     }
 }
@@ -909,24 +912,27 @@ size_t align16(size_t x) { return (x + 15) & ~size_t(15); }
 
 }  // namespace
 
-attn_status_t launch_tree_merge(const TreeParams& p, cudaStream_t stream) {
-    const int cols = kMergeThreads / p.group_rows * kMergeCols;  // of a block
-    const long long groups = (long long)p.B * p.Hkv * ((p.T * p.G + p.group_rows - 1) / p.group_rows);
-    // columns over several blocks where the rows alone are few (latency), not
-    // where they fill the GPU (each block finds its item's pieces anew)
-    const int most = (p.dh + cols - 1) / cols;
-    const long long split = 1024 / groups;
+attn_status_t launch_tree_merge(const TreeParams& p, int num_sms, cudaStream_t stream) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)groups, (unsigned)(split < 1 ? 1 : (split > most ? most : split)));
+    cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hkv * ((p.T * p.G + p.group_rows - 1) / p.group_rows)));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = (size_t)p.ctas * p.group_rows * 4;  // (at most as many pieces as CTAs)
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_tree_merge_kernel, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    // columns of a thread, of a row's share of 2 to 16: as few as leave one round
+    // of blocks (four to an SM), since every block finds its item's pieces anew
+    const int share = p.dw * p.group_rows / kMergeThreads;
+    int cpt = 4;
+    while (cpt < share && (long long)cfg.gridDim.x * (share / cpt) > 4ll * num_sms) cpt *= 2;
+    cfg.gridDim.y = (unsigned)(share > cpt ? share / cpt : 1);
+    const cudaError_t e = cpt == 4   ? cudaLaunchKernelEx(&cfg, attn_tree_merge_kernel<4>, p)
+                          : cpt == 8 ? cudaLaunchKernelEx(&cfg, attn_tree_merge_kernel<8>, p)
+                                     : cudaLaunchKernelEx(&cfg, attn_tree_merge_kernel<16>, p);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 // Whether a call runs on the tensor-core kernel of attn_tree_tc_sm103.cu.
@@ -1009,7 +1015,7 @@ attn_status_t launch_decode_tree(const void* q, const void* k_pages, const void*
             return launch_tree_t<decltype(D)::value, decltype(F8)::value, decltype(NT)::value>(tk, tv, p, stream, dev);
         });
     if (st != ATTN_OK) return st;
-    return launch_tree_merge(p, stream);
+    return launch_tree_merge(p, dev.num_sms, stream);
 }
 
 }  // namespace gb300

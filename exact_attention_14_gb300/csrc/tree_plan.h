@@ -97,7 +97,10 @@ __device__ __forceinline__ int tree_ctas(const TreeParams& p, long long total) {
     const long long want = (total + p.min_units - 1) / p.min_units;
     return (int)(want < p.ctas ? (want < 1 ? 1 : want) : p.ctas);
 }
-__device__ __forceinline__ long long tree_first(long long total, int n, int c) { return total * c / n; }
+__device__ __forceinline__ long long tree_div(long long a, long long b) {  // (64-bit divisions take hundreds of cycles)
+    return (a | b) <= 0xFFFFFFFFll ? (long long)((unsigned)a / (unsigned)b) : a / b;  // (neither below 0)
+}
+__device__ __forceinline__ long long tree_first(long long total, int n, int c) { return tree_div(total * c, n); }
 
 // A CTA's place in the list of units: its range, and the sequence that holds
 // its first unit (`base`: units before that sequence).
@@ -224,6 +227,6 @@ attn_status_t launch_tree_tc(const CUtensorMap& tk, const CUtensorMap& tv, const
 
 // Merges the pieces of the items that were cut, and writes the rows past each
 // sequence's drafted tokens (O = 0, LSE = -inf).
-attn_status_t launch_tree_merge(const TreeParams& p, cudaStream_t stream);
+attn_status_t launch_tree_merge(const TreeParams& p, int num_sms, cudaStream_t stream);
 
 }  // namespace gb300
