@@ -54,7 +54,8 @@ struct TcCfg {
     static constexpr int kRawStages = F8 ? 3 : 0;
     static constexpr int kRing = 2 * kTile;                    // after Q0, Q1
     static constexpr int kRaw = kRing + kStages * kTile;
-    static constexpr int kBar = kRaw + kRawStages * kRawTile;
+    static constexpr int kDescale = kRaw + kRawStages * kRawTile;  // K's and V's of a raw K tile
+    static constexpr int kBar = kDescale + kRawStages * 1024;
     static constexpr int kSmem = kBar + 12 * 1024;
     static_assert(kSmem <= 232448, "shared memory budget");
 };
@@ -160,18 +161,26 @@ __device__ void tc_produce(const CUtensorMap* tk, const CUtensorMap* tv, uint8_t
     TreeWalk walk;
     walk.start(bars->range);
     TcPiece x;
-    auto load = [&](const CUtensorMap* map, int page, int off) {
+    auto load = [&](const CUtensorMap* map, int page, int off) {  // (E4M3: the descales come with K)
         const int slot = (int)(issued % kSlots);
         const long long round = issued / kSlots;
         if (round > 0) ok = warp_wait(&empty[slot], (uint32_t)(round - 1), abort_flag);
         if (!ok) return;
         const uint32_t bar = smem_u32(&full[slot]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
+        const bool descales = F8 && map == tk;
+        if (lane == 0) mbar_arrive_expect_tx(bar, kBytes + (descales ? 1024 : 0));
         __syncwarp();
         if (copies) {
             const uint32_t to = ring + slot * kBytes;
             if constexpr (F8) {
                 tma_load_4d(to, map, bar, 0, x.w.h, off, page);
+                if (descales) {
+                    // a missing page's codes are zeros: any descale that exists will do
+                    const long long at = ((long long)(page < 0 ? 0 : page) * p.Hkv + x.w.h) * p.page_size + off;
+                    const uint32_t ds = smem_u32(smem + C::kDescale) + slot * 1024 + lane * p.box_keys * 4;
+                    bulk_load(ds, p.k_descale + at, p.box_keys * 4, bar);
+                    bulk_load(ds + 512, p.v_descale + at, p.box_keys * 4, bar);
+                }
             } else {
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) tma_load_4d(to + c * 16384, map, bar, 64 * c, x.w.h, off, page);
@@ -374,9 +383,9 @@ __device__ void tc_fix(int wf, uint8_t* smem, TcBars* bars, const TreeParams& p)
 }
 
 // ------------------------------------------------------- codes to fp16, E4M3
-// Two warps, 64 keys each.  A lane takes 16 of a row's 128 codes.  V is multiplied with its descale over F, F = 2^fexp above
-// every one so far (two fp16 roundings, of the factor and of the product: less
-// than P's and far less than O's); K's descales, whose rounding would enter the
+// Two warps, 64 keys each.  A lane takes 16 of a row's 128 codes.  V is multiplied
+// with its descale over F, F = 2^fexp above every one so far (two fp16 roundings, of
+// the factor and of the product: less than P's and far less than O's); K's descales, whose rounding would enter the
 // exponent, are left to the softmax.
 template <int D>
 __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams& p) {
@@ -388,24 +397,6 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
     TreeWalk walk;
     walk.start(bars->range);
     TcPiece x;
-    float kd[2] = {0.f, 0.f}, vd[4] = {0.f, 0.f, 0.f, 0.f};
-    // descales of a tile: K's of keys 64 wc + {0, 32} + lane, V's of keys lane + 32
-    // i; the pages they lie in are looked up a tile earlier still, and used only
-    // then, so that neither load is waited for
-    int page[4] = {-1, -1, -1, -1}, off[4] = {0, 0, 0, 0};
-    auto look = [&](int j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            page[i] = tree_page(p, x.w.b, (x.w.k0 + j) * kTcKeys + 32 * i + lane, x.w.keys, off[i]);
-    };
-    auto fetch = [&]() {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const long long at = ((long long)(page[i] < 0 ? 0 : page[i]) * p.Hkv + x.w.h) * p.page_size + off[i];
-            vd[i] = page[i] < 0 ? 0.f : __ldg(p.v_descale + at);
-            if ((i >> 1) == wc) kd[i & 1] = page[i] < 0 ? 0.f : __ldg(p.k_descale + at);
-        }
-    };
     const int c = lane & 7;
     // lane's row of four, plus 4 i: the lanes of the upper columns take the
     // neighbour's row, whose swizzle puts their stores on the other banks
@@ -415,24 +406,27 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
         x.set(p);
         int fexp = -100;
         const int ahead = x.pair ? 1 : 2;
-        look(0);
-        fetch();
-        look(1);
         // (one place in the code for every load: its body is long)
 #pragma unroll 1
         for (int jk = 0, jv = 0; jv < x.n && ok;) {
             const bool is_v = jk >= x.n || jk >= jv + ahead;
             const int j = is_v ? jv++ : jk++;
+            ok = warp_wait(&bars->raw_full[raw_slot], raw_round, abort_flag);
             if (!is_v) {
-                // ---- the tile's descales
+                // ---- the tile's descales: K's of this warp's keys, V's (of all: F)
                 const uint32_t slot = tiles % kDs;
-                if (tiles >= kDs) ok = warp_wait(&bars->ds_empty[slot], tiles / kDs - 1u, abort_flag);
+                if (ok && tiles >= kDs) ok = warp_wait(&bars->ds_empty[slot], tiles / kDs - 1u, abort_flag);
                 if (!ok) break;
-                float top = 0.f;
+                const float* raw_ds = reinterpret_cast<const float*>(smem + C::kDescale + raw_slot * 1024);
+                const float* kd = raw_ds + 64 * wc;
+                const int key0 = (x.w.k0 + j) * kTcKeys + lane;
+                float vd[4], top = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const bool drop = !isfinite(vd[i]) && (x.w.k0 + j) * kTcKeys + 32 * i + lane >= x.prefix;
-                    if (drop) vd[i] = 0.f;  // its row is added apart
+                    vd[i] = raw_ds[128 + 32 * i + lane];
+                    const int key = key0 + 32 * i;
+                    // past the sequence, or a row that is added apart
+                    if (key >= x.w.keys || (key >= x.prefix && !isfinite(vd[i]))) vd[i] = 0.f;
                     top = fmaxf(top, fabsf(vd[i]));
                 }
 #pragma unroll
@@ -441,20 +435,15 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
                 const float fr = tc_pow2(-fexp);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    bars->kf[slot][64 * wc + 32 * i + lane] = kd[i];
+                    bars->kf[slot][64 * wc + 32 * i + lane] = kd[32 * i + lane];
                     bars->wv[slot][64 * wc + 32 * i + lane] = (wc == 0 ? vd[i] : vd[2 + i]) * fr;
                 }
                 if (wc == 0 && lane == 0) bars->fexp[slot] = fexp;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full[slot]));
                 ++tiles;
-                if (j + 1 < x.n) {
-                    fetch();
-                    look(j + 2);
-                }
             }
             // ---- the codes
-            ok = warp_wait(&bars->raw_full[raw_slot], raw_round, abort_flag);
             if (ok && out_round > 0) ok = warp_wait(&bars->empty[out_slot], out_round - 1u, abort_flag);
             if (!ok) break;
             const uint32_t raw = smem_u32(smem + C::kRaw + raw_slot * C::kRawTile);
@@ -473,7 +462,7 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
                         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int e = 0; e < 16; ++e) hit |= ((u[e >> 2] >> (8 * (e & 3))) & 0x7Fu) == 0x7Fu;
-                        if (c == 0) {
+                        if (c == 0) {  // (a path for the last tiles of a sequence)
                             int off;
                             const int page = tree_page(p, x.w.b, key, x.w.keys, off);
                             if (page >= 0)
