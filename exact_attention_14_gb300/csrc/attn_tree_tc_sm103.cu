@@ -48,14 +48,16 @@ constexpr float kTcLn2 = 0.69314718055994530942f;
 
 template <int D, bool F8>
 struct TcCfg {
-    static constexpr int kTile = 128 * D * 2;                  // 16-bit operand tile
-    static constexpr int kStages = F8 ? 3 : (D == 128 ? 4 : 8);
-    static constexpr int kRawTile = 128 * 128;                 // E4M3 codes
-    static constexpr int kRawStages = F8 ? 3 : 0;
+    static constexpr int kTile = 128 * D * 2;                  // 16-bit operand tile (Q's two terms)
+    static constexpr int kStages = F8 ? 2 : (D == 128 ? 4 : 8);  // of K and V, E4M3: of V in fp16
+    static constexpr int kCodes = 128 * 128;                   // E4M3 codes of a tile
+    static constexpr int kKStages = F8 ? 3 : 0;                // K's codes, with K's and V's descales
+    static constexpr int kVStages = F8 ? 2 : 0;                // V's codes
     static constexpr int kRing = 2 * kTile;                    // after Q0, Q1
-    static constexpr int kRaw = kRing + kStages * kTile;
-    static constexpr int kDescale = kRaw + kRawStages * kRawTile;  // K's and V's of a raw K tile
-    static constexpr int kBar = kDescale + kRawStages * 1024;
+    static constexpr int kK = kRing + kStages * kTile;
+    static constexpr int kV = kK + kKStages * kCodes;
+    static constexpr int kDescale = kV + kVStages * kCodes;
+    static constexpr int kBar = kDescale + kKStages * 1024;
     static constexpr int kSmem = kBar + 12 * 1024;
     static_assert(kSmem <= 232448, "shared memory budget");
 };
@@ -76,8 +78,8 @@ constexpr int kDs = 4;
 
 struct TcBars {
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
-    uint64_t full[8], empty[8];       // operand tiles
-    uint64_t raw_full[4], raw_empty[4];
+    uint64_t full[8], empty[8];       // tiles of K and V; E4M3: of V in fp16
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];  // E4M3 codes
     uint64_t ds_full[kDs], ds_empty[kDs];
     uint64_t fix_ask, fix_done;       // V of a special tile is there / is prepared
     uint64_t stat, done, drain;
@@ -110,6 +112,16 @@ __device__ __forceinline__ void tc_e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi
         "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(lo), "=r"(hi)
         : "r"(w));
+}
+__device__ __forceinline__ float2 tc_f16x2_f32(uint32_t h) {
+    float2 f;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(h));
+    return f;
+}
+__device__ __forceinline__ void tc_sts64(uint32_t a, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 __device__ __forceinline__ uint4 tc_lds128(uint32_t a) {
     uint4 v;
@@ -148,47 +160,55 @@ template <int D, bool F8>
 __device__ void tc_produce(const CUtensorMap* tk, const CUtensorMap* tv, uint8_t* smem, TcBars* bars,
                            const TreeParams& p) {
     using C = TcCfg<D, F8>;
-    constexpr int kSlots = F8 ? C::kRawStages : C::kStages;
-    constexpr int kBytes = F8 ? C::kRawTile : C::kTile;
     const int lane = threadIdx.x & 31;
-    uint64_t* full = F8 ? bars->raw_full : bars->full;
-    uint64_t* empty = F8 ? bars->raw_empty : bars->empty;
-    const uint32_t ring = smem_u32(smem + (F8 ? C::kRaw : C::kRing)) + lane * p.box_keys * 128;
+    const uint32_t mine = lane * p.box_keys * 128;
     const volatile int* abort_flag = &bars->abort;
     const bool copies = lane < kTcKeys / p.box_keys;
-    long long issued = 0;
+    struct Ring {
+        uint64_t *full, *empty;
+        int slot;
+        uint32_t round;
+    };
+    Ring ring_k = {F8 ? bars->k_full : bars->full, F8 ? bars->k_empty : bars->empty, 0, 0u};
+    Ring ring_v = {bars->v_full, bars->v_empty, 0, 0u};  // (bf16: K and V share one)
     bool ok = true;
     TreeWalk walk;
     walk.start(bars->range);
     TcPiece x;
-    auto load = [&](const CUtensorMap* map, int page, int off) {  // (E4M3: the descales come with K)
-        const int slot = (int)(issued % kSlots);
-        const long long round = issued / kSlots;
-        if (round > 0) ok = warp_wait(&empty[slot], (uint32_t)(round - 1), abort_flag);
+    auto load = [&](auto IsV, int page, int off) {
+        constexpr bool is_v = decltype(IsV)::value;
+        constexpr int slots = !F8 ? C::kStages : (is_v ? C::kVStages : C::kKStages);
+        Ring& r = F8 && is_v ? ring_v : ring_k;
+        if (r.round > 0) ok = warp_wait(&r.empty[r.slot], r.round - 1u, abort_flag);
         if (!ok) return;
-        const uint32_t bar = smem_u32(&full[slot]);
-        const bool descales = F8 && map == tk;
-        if (lane == 0) mbar_arrive_expect_tx(bar, kBytes + (descales ? 1024 : 0));
+        const CUtensorMap* map = is_v ? tv : tk;
+        const uint32_t bar = smem_u32(&r.full[r.slot]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, !F8 ? C::kTile : (is_v ? C::kCodes : C::kCodes + 1024));
         __syncwarp();
         if (copies) {
-            const uint32_t to = ring + slot * kBytes;
             if constexpr (F8) {
-                tma_load_4d(to, map, bar, 0, x.w.h, off, page);
-                if (descales) {
+                tma_load_4d(smem_u32(smem + (is_v ? C::kV : C::kK)) + r.slot * C::kCodes + mine, map, bar, 0, x.w.h, off, page);
+                if constexpr (!is_v) {
                     // a missing page's codes are zeros: any descale that exists will do
                     const long long at = ((long long)(page < 0 ? 0 : page) * p.Hkv + x.w.h) * p.page_size + off;
-                    const uint32_t ds = smem_u32(smem + C::kDescale) + slot * 1024 + lane * p.box_keys * 4;
+                    const uint32_t ds = smem_u32(smem + C::kDescale) + r.slot * 1024 + lane * p.box_keys * 4;
                     bulk_load(ds, p.k_descale + at, p.box_keys * 4, bar);
                     bulk_load(ds + 512, p.v_descale + at, p.box_keys * 4, bar);
                 }
             } else {
+                const uint32_t to = smem_u32(smem + C::kRing) + r.slot * C::kTile + mine;
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) tma_load_4d(to + c * 16384, map, bar, 64 * c, x.w.h, off, page);
             }
         }
         __syncwarp();
-        ++issued;
+        if (++r.slot == slots) {
+            r.slot = 0;
+            ++r.round;
+        }
     };
+    std::false_type K;
+    std::true_type V;
     while (ok && walk.next(p, x.w)) {
         x.set(p);
         // pages of the tiles whose K has been loaded and whose V has not, and of
@@ -203,14 +223,14 @@ __device__ void tc_produce(const CUtensorMap* tk, const CUtensorMap* tv, uint8_t
         look(0, 0);
         look(1, 1);
         look(2, 2);
-        load(tk, page[0], off[0]);
-        if (!x.pair && x.n > 1 && ok) load(tk, page[1], off[1]);
+        load(K, page[0], off[0]);
+        if (!x.pair && x.n > 1 && ok) load(K, page[1], off[1]);
         for (int j = 0; j < x.n && ok; ++j) {
-            load(tv, page[0], off[0]);
+            load(V, page[0], off[0]);
             if (x.pair) {
-                if (ok && j + 1 < x.n) load(tk, page[1], off[1]);
+                if (ok && j + 1 < x.n) load(K, page[1], off[1]);
             } else {
-                if (ok && j + 2 < x.n) load(tk, page[2], off[2]);
+                if (ok && j + 2 < x.n) load(K, page[2], off[2]);
             }
             page[0] = page[1]; off[0] = off[1];
             page[1] = page[2]; off[1] = off[2];
@@ -218,10 +238,14 @@ __device__ void tc_produce(const CUtensorMap* tk, const CUtensorMap* tv, uint8_t
         }
     }
     if (!ok && lane == 0) tc_abort(bars, p.err);
-    for (int slot = 0; slot < kSlots && slot < issued; ++slot) {  // every copy lands
-        const long long n = (issued - slot + kSlots - 1) / kSlots;
-        mbar_wait(smem_u32(&full[slot]), (uint32_t)((n - 1) & 1), nullptr);
-    }
+    auto land = [&](const Ring& r, int slots) {  // every copy lands
+        for (int i = 0; i < slots; ++i) {
+            const uint32_t n = r.round + (i < r.slot ? 1u : 0u);
+            if (n > 0) mbar_wait(smem_u32(&r.full[i]), (n - 1u) & 1u, nullptr);
+        }
+    };
+    land(ring_k, F8 ? C::kKStages : C::kStages);
+    if constexpr (F8) land(ring_v, C::kVStages);
     __syncwarp();
 }
 
@@ -232,10 +256,9 @@ template <int D, bool F8>
 __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreeParams& p) {
     using C = TcCfg<D, F8>;
     const volatile int* abort_flag = &bars->abort;
-    // (both operands bf16, or both fp16: format code 0)
-    constexpr uint32_t kDrop = F8 ? (1u << 7) | (1u << 10) : 0u;
-    constexpr uint32_t idS = make_idesc_bf16(128, kTcKeys, 0, 0) & ~kDrop;
-    constexpr uint32_t idO = make_idesc_bf16(128, D, 0, 1) & ~kDrop;
+    constexpr uint32_t idS = F8 ? make_idesc_e4m3(128, kTcKeys) : make_idesc_bf16(128, kTcKeys, 0, 0);
+    // (E4M3: P and V both fp16, format code 0)
+    constexpr uint32_t idO = make_idesc_bf16(128, D, 0, 1) & ~(F8 ? (1u << 7) | (1u << 10) : 0u);
     const uint32_t q_lo[2] = {sdesc_lo(smem_u32(smem), 16), sdesc_lo(smem_u32(smem + C::kTile), 16)};
     const uint32_t ring = smem_u32(smem + C::kRing);
     uint32_t slot = 0, round = 0;  // of the next operand tile
@@ -251,6 +274,21 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
         tc_fence_after();
         return mine;
     };
+    uint32_t kslot = 0, kround = 0;
+    auto take_k = [&]() {
+        if constexpr (!F8) {
+            return take();
+        } else {
+            const uint32_t mine = kslot;
+            ok = warp_wait(&bars->k_full[mine], kround, abort_flag);
+            if (++kslot == C::kKStages) {
+                kslot = 0;
+                ++kround;
+            }
+            tc_fence_after();
+            return mine;
+        }
+    };
     TreeWalk walk;
     walk.start(bars->range);
     TcPiece x;
@@ -261,16 +299,26 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
         uint32_t slot_k = 0, slot_v = 0;
         auto scores = [&](auto T) {
             constexpr int t = decltype(T)::value;
-            const uint32_t k_lo = sdesc_lo(ring + slot_k * C::kTile, 16);
             const uint32_t a_lo = pair ? q_lo[t] : q_lo[0];
+            if constexpr (F8) {
+                // both of Q's terms times K's codes
+                const uint32_t k_lo = sdesc_lo(smem_u32(smem + C::kK) + slot_k * C::kCodes, 16);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t step = (kk >> 2) * (16384 >> 4) + (kk & 3) * (32 >> 4);
-                mma_ss_warp(tmem + t * 128, sdesc_join(a_lo + step, kTcDescHi), sdesc_join(k_lo + step, kTcDescHi),
-                            idS, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_ss_f8_warp(tmem + t * 128,
+                                   sdesc_join(a_lo + (kk >> 2) * (16384 >> 4) + (kk & 3) * (32 >> 4), kTcDescHi),
+                                   sdesc_join(k_lo + (kk & 3) * (32 >> 4), kTcDescHi), idS, kk > 0 ? 1u : 0u);
+            } else {
+                const uint32_t k_lo = sdesc_lo(ring + slot_k * C::kTile, 16);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t step = (kk >> 2) * (16384 >> 4) + (kk & 3) * (32 >> 4);
+                    mma_ss_warp(tmem + t * 128, sdesc_join(a_lo + step, kTcDescHi), sdesc_join(k_lo + step, kTcDescHi),
+                                idS, kk > 0 ? 1u : 0u);
+                }
             }
             mma_commit_warp(smem_u32(&bars->s_full[t]));
-            if (!pair || t == 1) mma_commit_warp(smem_u32(&bars->empty[slot_k]));
+            if (!pair || t == 1) mma_commit_warp(smem_u32(F8 ? &bars->k_empty[slot_k] : &bars->empty[slot_k]));
         };
         auto begin = [&](auto T) {
             constexpr int t = decltype(T)::value;
@@ -280,7 +328,7 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
                 if (!ok) return;
                 tc_fence_after();
             }
-            if (!pair || t == 0) slot_k = take();
+            if (!pair || t == 0) slot_k = take_k();
             if (ok) scores(T);
         };
         auto step = [&](auto T, int s) {
@@ -310,7 +358,7 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
                             sdesc_join(v_lo + kk * (2048 >> 4), kTcDescHi), idO, (s > 0 || kk > 0) ? 1u : 0u);
             if (!pair || t == 1) mma_commit_warp(smem_u32(&bars->empty[slot_v]));
             if (s + 1 < n) {
-                if (!pair || t == 0) slot_k = take();
+                if (!pair || t == 0) slot_k = take_k();
                 if (ok) scores(T);  // in order after the product that reads P over it
             } else {
                 mma_commit_warp(smem_u32(&bars->o_full[t]));
@@ -382,17 +430,18 @@ __device__ void tc_fix(int wf, uint8_t* smem, TcBars* bars, const TreeParams& p)
     if (!ok && lane == 0) tc_abort(bars, p.err);
 }
 
-// ------------------------------------------------------- codes to fp16, E4M3
+// ----------------------------------------------- descales, V's codes to fp16, E4M3
 // Two warps, 64 keys each.  A lane takes 16 of a row's 128 codes.  V is multiplied
 // with its descale over F, F = 2^fexp above every one so far (two fp16 roundings, of
-// the factor and of the product: less than P's and far less than O's); K's descales, whose rounding would enter the
+// the factor and of the product: less than P's and far less than O's).  K's codes
+// go into the product as they are, K's descales, whose rounding would enter the
 // exponent, are left to the softmax.
 template <int D>
 __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams& p) {
     using C = TcCfg<D, true>;
     const int lane = threadIdx.x & 31;
     const volatile int* abort_flag = &bars->abort;
-    uint32_t raw_slot = 0, raw_round = 0, out_slot = 0, out_round = 0, tiles = 0;
+    uint32_t raw_slot = 0, raw_round = 0, out_slot = 0, out_round = 0, tiles = 0, kslot = 0, kround = 0;
     bool ok = true;
     TreeWalk walk;
     walk.start(bars->range);
@@ -406,18 +455,16 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
         x.set(p);
         int fexp = -100;
         const int ahead = x.pair ? 1 : 2;
-        // (one place in the code for every load: its body is long)
-#pragma unroll 1
         for (int jk = 0, jv = 0; jv < x.n && ok;) {
             const bool is_v = jk >= x.n || jk >= jv + ahead;
             const int j = is_v ? jv++ : jk++;
-            ok = warp_wait(&bars->raw_full[raw_slot], raw_round, abort_flag);
             if (!is_v) {
                 // ---- the tile's descales: K's of this warp's keys, V's (of all: F)
                 const uint32_t slot = tiles % kDs;
+                ok = warp_wait(&bars->k_full[kslot], kround, abort_flag);
                 if (ok && tiles >= kDs) ok = warp_wait(&bars->ds_empty[slot], tiles / kDs - 1u, abort_flag);
                 if (!ok) break;
-                const float* raw_ds = reinterpret_cast<const float*>(smem + C::kDescale + raw_slot * 1024);
+                const float* raw_ds = reinterpret_cast<const float*>(smem + C::kDescale + kslot * 1024);
                 const float* kd = raw_ds + 64 * wc;
                 const int key0 = (x.w.k0 + j) * kTcKeys + lane;
                 float vd[4], top = 0.f;
@@ -440,15 +487,24 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
                 }
                 if (wc == 0 && lane == 0) bars->fexp[slot] = fexp;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full[slot]));
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&bars->ds_full[slot]));
+                    mbar_arrive(smem_u32(&bars->k_empty[kslot]));
+                }
                 ++tiles;
+                if (++kslot == C::kKStages) {
+                    kslot = 0;
+                    ++kround;
+                }
+                continue;
             }
             // ---- the codes
+            ok = warp_wait(&bars->v_full[raw_slot], raw_round, abort_flag);
             if (ok && out_round > 0) ok = warp_wait(&bars->empty[out_slot], out_round - 1u, abort_flag);
             if (!ok) break;
-            const uint32_t raw = smem_u32(smem + C::kRaw + raw_slot * C::kRawTile);
+            const uint32_t raw = smem_u32(smem + C::kV + raw_slot * C::kCodes);
             const uint32_t out = smem_u32(smem + C::kRing + out_slot * C::kTile) + (c >> 2) * 16384;
-            if (is_v && x.special(j)) {
+            if (x.special(j)) {
                 // rows that must not enter the product become zeros where they lie
                 uint32_t marks[2] = {0u, 0u};
 #pragma unroll 1
@@ -495,10 +551,8 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
                 float d[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[i] = tc_lds128(src[i & 1] + 512 * (i0 + i));
-                if (is_v) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) d[i] = fv[4 * (i0 + i)];
-                }
+                for (int i = 0; i < 4; ++i) d[i] = fv[4 * (i0 + i)];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t h[8];
@@ -506,11 +560,9 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
                     tc_e4m3x4(w[i].y, h[2], h[3]);
                     tc_e4m3x4(w[i].z, h[4], h[5]);
                     tc_e4m3x4(w[i].w, h[6], h[7]);
-                    if (is_v) {  // times its descale over F
-                        const uint32_t f = tc_pack_f16(d[i], d[i]);
+                    const uint32_t f = tc_pack_f16(d[i], d[i]);  // its descale over F
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(f));
-                    }
+                    for (int e = 0; e < 8; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(f));
                     sts128(dst[i & 1] + 512 * (i0 + i), h[0], h[1], h[2], h[3]);
                     sts128(dst[i & 1] + 512 * (i0 + i) + odd, h[4], h[5], h[6], h[7]);
                 }
@@ -519,10 +571,10 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(smem_u32(&bars->full[out_slot]));
-                mbar_arrive(smem_u32(&bars->raw_empty[raw_slot]));
+                mbar_arrive(smem_u32(&bars->v_empty[raw_slot]));
             }
-            if (is_v) ++tile_v;
-            if (++raw_slot == C::kRawStages) {
+            ++tile_v;
+            if (++raw_slot == C::kVStages) {
                 raw_slot = 0;
                 ++raw_round;
             }
@@ -755,15 +807,31 @@ __device__ __forceinline__ void tc_load_q(const TreeParams& p, size_t row_at, in
                     mx = fmaxf(mx, fmaxf(fabsf(bf16lo_to_f32(w[e])), fabsf(bf16hi_to_f32(w[e]))));
 #pragma unroll
                 for (int off = kLanes / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-                // a power of two that puts the row's largest value in [2^14, 2^15)
+                // a power of two that puts the row's largest value in [2^7, 2^8).  A bf16
+                // value is then the sum of two E4M3 ones, exactly down to 2^-9 of the
+                // largest, and to 2^-17 of the largest below that.
                 int e = (int)(__float_as_uint(mx) >> 23) - 127;
+                const bool inf = e > 127;
                 e = e < -100 ? -100 : (e > 126 ? 126 : e);
-                const float up = tc_pow2(14 - e);
-                if (c == 0) qs[row] = p.c * tc_pow2(e - 14);
+                const float up = inf ? __uint_as_float(0x7FFFFFFFu) : tc_pow2(7 - e);  // (an infinity: the row is NaN)
+                if (c == 0) qs[row] = p.c * tc_pow2(e - 7);
+                uint32_t hi[2], lo[2];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = tc_pack_f16(bf16lo_to_f32(w[k]) * up, bf16hi_to_f32(w[k]) * up);
+                for (int k = 0; k < 2; ++k) {
+                    const float f[4] = {bf16lo_to_f32(w[2 * k]) * up, bf16hi_to_f32(w[2 * k]) * up,
+                                        bf16lo_to_f32(w[2 * k + 1]) * up, bf16hi_to_f32(w[2 * k + 1]) * up};
+                    hi[k] = pack_e4m3x2(f[0], f[1]) | pack_e4m3x2(f[2], f[3]) << 16;
+                    uint32_t a, b;
+                    tc_e4m3x4(hi[k], a, b);
+                    const float2 g0 = tc_f16x2_f32(a), g1 = tc_f16x2_f32(b);
+                    lo[k] = pack_e4m3x2(f[0] - g0.x, f[1] - g0.y) | pack_e4m3x2(f[2] - g1.x, f[3] - g1.y) << 16;
+                }
+                const uint32_t at = tile + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + 8 * (c & 1);
+                tc_sts64(at, hi[0], hi[1]);
+                tc_sts64(at + 16384, lo[0], lo[1]);
+            } else {
+                sts128(tile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
             }
-            sts128(tile + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
         }
     }
     fence_proxy_async_smem();
@@ -1021,8 +1089,10 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
             mbar_init(smem_u32(&bars->empty[i]), 1);
         }
         for (int i = 0; i < 4; ++i) {
-            mbar_init(smem_u32(&bars->raw_full[i]), 1);
-            mbar_init(smem_u32(&bars->raw_empty[i]), kTcHelpers);
+            mbar_init(smem_u32(&bars->k_full[i]), 1);
+            mbar_init(smem_u32(&bars->k_empty[i]), kTcHelpers + 1);  // (and the product's commit)
+            mbar_init(smem_u32(&bars->v_full[i]), 1);
+            mbar_init(smem_u32(&bars->v_empty[i]), kTcHelpers);
         }
         for (int i = 0; i < kDs; ++i) {
             mbar_init(smem_u32(&bars->ds_full[i]), kTcHelpers);
