@@ -347,6 +347,8 @@ attn_status_t check_tree_shape(int B, int Hq, int Hkv, int T, int max_blocks, in
     if (cache_dtype != ATTN_CACHE_BF16 && cache_dtype != ATTN_CACHE_E4M3) return ATTN_ERR_INVALID_ARG;
     if ((long long)max_blocks * page_size > kMaxLen) return ATTN_ERR_INVALID_ARG;
     if (T > 1024 || page_size % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    // (rows of a head group, and rows in all, are counted in 32 bits)
+    if ((long long)T * (Hq / Hkv) > (1ll << 20) || (long long)B * Hq * T > (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
     if (!fwd_head_dim_supported(d) || (cache_dtype == ATTN_CACHE_E4M3 && d % 16 != 0))
         return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;

@@ -221,11 +221,10 @@ __device__ __forceinline__ void produce(const CUtensorMap* tk, const CUtensorMap
                     tma_load_4d(dv + to, tv, bar, (F8 ? 128 : 64) * c, w.h, my_off, my_page);
                 }
                 if constexpr (F8) {
-                    // a missing page's codes are zeros: any descale that exists will do
-                    const long long at = ((long long)(my_page < 0 ? 0 : my_page) * p.Hkv + w.h) * p.page_size + my_off;
+                    const long long at = ((long long)my_page * p.Hkv + w.h) * p.page_size + my_off;
                     const uint32_t ds = smem_u32(smem + C::kDs + slot * C::kDescale) + lane * p.box_keys * 4;
-                    bulk_load(ds, p.k_descale + at, p.box_keys * 4, bar);
-                    bulk_load(ds + kTileKeys * 4, p.v_descale + at, p.box_keys * 4, bar);
+                    bulk_load(ds, my_page < 0 ? kTreeNoDescale : p.k_descale + at, p.box_keys * 4, bar);
+                    bulk_load(ds + kTileKeys * 4, my_page < 0 ? kTreeNoDescale : p.v_descale + at, p.box_keys * 4, bar);
                 }
             }
             __syncwarp();

@@ -189,11 +189,10 @@ __device__ void tc_produce(const CUtensorMap* tk, const CUtensorMap* tv, uint8_t
             if constexpr (F8) {
                 tma_load_4d(smem_u32(smem + (is_v ? C::kV : C::kK)) + r.slot * C::kCodes + mine, map, bar, 0, x.w.h, off, page);
                 if constexpr (!is_v) {
-                    // a missing page's codes are zeros: any descale that exists will do
-                    const long long at = ((long long)(page < 0 ? 0 : page) * p.Hkv + x.w.h) * p.page_size + off;
+                    const long long at = ((long long)page * p.Hkv + x.w.h) * p.page_size + off;
                     const uint32_t ds = smem_u32(smem + C::kDescale) + r.slot * 1024 + lane * p.box_keys * 4;
-                    bulk_load(ds, p.k_descale + at, p.box_keys * 4, bar);
-                    bulk_load(ds + 512, p.v_descale + at, p.box_keys * 4, bar);
+                    bulk_load(ds, page < 0 ? kTreeNoDescale : p.k_descale + at, p.box_keys * 4, bar);
+                    bulk_load(ds + 512, page < 0 ? kTreeNoDescale : p.v_descale + at, p.box_keys * 4, bar);
                 }
             } else {
                 const uint32_t to = smem_u32(smem + C::kRing) + r.slot * C::kTile + mine;

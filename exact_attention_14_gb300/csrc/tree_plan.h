@@ -212,6 +212,9 @@ __device__ __forceinline__ int tree_page(const TreeParams& p, int b, int key, in
     return page >= 0 && (long long)page < p.num_blocks ? page : -1;
 }
 
+// The descales of keys that have no page (their codes are zeros): up to 128.
+static __device__ __align__(128) float kTreeNoDescale[128] = {};
+
 // Whether row (drafted token t of sequence b) sees drafted token u.
 __device__ __forceinline__ bool tree_sees(const TreeParams& p, int b, int t, int u) {
     if (!p.mask) return u <= t;

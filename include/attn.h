@@ -556,11 +556,14 @@ size_t attn_decode_tree_workspace_size(int B, int Hq, int Hkv, int T, int max_bl
  * reports ATTN_ERR_INVALID_ARG.  Keys past a sequence's length, and drafted
  * tokens a row does not see, never reach it (NaN included); a block-table entry
  * outside [0, num_blocks) reads as zeros.
- * Numerics: fp32 scores, softmax statistics and O; P is rounded to bf16 for a
- * bf16 cache, and for E4M3 (whose codes are exact in fp16) to fp16 after V's
- * descale.  Results do not change from run to run.
+ * Numerics: fp32 scores, softmax statistics and O.  bf16 cache: P is rounded to
+ * bf16.  E4M3 cache: K's codes and descales enter exactly; P is rounded to fp16,
+ * with V's descale in it or, for many rows (T * Hq / Hkv > 16 and d <= 128), V
+ * times its descale rounded to fp16 too, and Q's elements below 2^-9 of their row's
+ * largest to 2^-17 of that.  Results do not change from run to run.
  * Supported: 8 <= d <= 256, d % 8 == 0 (E4M3: d % 16 == 0); page_size % 16 ==
- * 0; Hq % Hkv == 0; 1 <= T <= 1024; max_blocks * page_size <= 2^24.
+ * 0; Hq % Hkv == 0; 1 <= T <= 1024; T * Hq / Hkv <= 2^20; B * Hq * T <= 2^30;
+ * max_blocks * page_size <= 2^24.
  */
 attn_status_t attn_decode_tree(const void* q, const void* k_pages, const void* v_pages,
                                const float* k_descale, const float* v_descale,

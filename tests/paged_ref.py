@@ -142,6 +142,13 @@ def tree64(q, cache, mask=None, q_lens=None, scale=None):
                 lse[b, h, t] = z
                 # fp32 accumulation of d products (any order): d * 2^-23 of the sum of |q||k|
                 eps[b, h, t] = d * 2.0 ** -23 * scale * (k[js, kv].abs() @ qd[t].abs()).max()
+                if cache.e4m3:
+                    # with many rows Q is the sum of two E4M3 terms, its row scaled to a largest
+                    # value in [2^7, 2^8): 8 bits from 2^-2 up are exact (the residual of 4 of them
+                    # has 4, none below 2^-9), below that off by at most 2^-10, 2^-17 of the largest
+                    a = qd[t].abs()
+                    small = 2.0 ** -17 * a.max() * (a < 2.0 ** -9 * a.max())
+                    eps[b, h, t] += scale * (k[js, kv].abs() @ small).max()
     return o, lse, size, eps
 
 

@@ -98,6 +98,7 @@ def tree(lib, **kw):
     (dict(Hq=7), 1), (dict(T=0), 1), (dict(mb=0), 1), (dict(mb=1 << 21), 1), (dict(scale=-1.0), 1),
     (dict(scale=float("inf")), 1), (dict(odt=3), 1), (dict(kind=3), 1), (dict(nb=0), 1),
     (dict(T=1025), 2), (dict(page=24), 2), (dict(d=72), 2), (dict(kind=0, d=260), 2),
+    (dict(T=1024, Hq=1 << 21, Hkv=1), 2), (dict(T=1024, B=2048, Hq=1024, Hkv=1024), 2),
 ])
 def test_decode_tree_refusals(lib, kw, code):
     assert tree(lib, **kw) == code
