@@ -846,13 +846,25 @@ def _rows(t, name):
     return (B, H, N, d), _Strides(sb, sh, sn)
 
 
-def _used_on(stream, *tensors):
-    """Tensors allocated here and used on a stream of the caller's: freed only
-    after that stream's use."""
-    if isinstance(stream, torch.cuda.Stream):
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _made_on(stream, dev):
+    """Where the outputs and workspaces of a call on ``stream`` are allocated: on
+    that stream, since a block of the current stream's may still be in use by work
+    queued there."""
+    if stream is None:
+        return _HERE
+    if not isinstance(stream, torch.cuda.Stream):
+        at = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(at, device=dev) if at else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
+
+
+def _used_here(dev, *tensors):
+    """Outputs made on a stream of the caller's, which are read on the current one
+    too: a block is given out again only after that use."""
+    here = torch.cuda.current_stream(dev)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(here)
 
 
 def attn_rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "none",
@@ -972,10 +984,11 @@ def rope(q, k, positions, inv_freq, *, interleaved: bool = False, magnitude: flo
     out_dtype = out_dtype or q.dtype
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out_dtype must be bfloat16 or float32")
-    q_out, qos = _new_rows(q, out_dtype, Hq, N, d)
-    k_out, kos = (None, None) if k is None else _new_rows(k, out_dtype, Hkv, N, d)
+    with _made_on(stream, q.device):
+        q_out, qos = _new_rows(q, out_dtype, Hq, N, d)
+        k_out, kos = (None, None) if k is None else _new_rows(k, out_dtype, Hkv, N, d)
     if stream is not None:
-        _used_on(stream, q_out, k_out)
+        _used_here(q.device, q_out, k_out)
     return _rope_call(q, k, q_out, k_out, positions, inv_freq, shape, qos, kos, interleaved,
                       inverse, magnitude, stream)
 
@@ -1079,10 +1092,11 @@ def cache_read(k_pages, v_pages, block_table, cu_seqlens, total: int, k_descale=
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out_dtype must be bfloat16 or float32")
     shape = (total, cache[2], cache[3])
-    k = torch.empty(shape, dtype=out_dtype, device=k_pages.device)
-    v = torch.empty(shape, dtype=out_dtype, device=k_pages.device)
+    with _made_on(stream, k_pages.device):
+        k = torch.empty(shape, dtype=out_dtype, device=k_pages.device)
+        v = torch.empty(shape, dtype=out_dtype, device=k_pages.device)
     if stream is not None:
-        _used_on(stream, k, v)
+        _used_here(k_pages.device, k, v)
     return _read_call(k_pages, v_pages, block_table, cu_seqlens, k, v, k_descale, v_descale, cache,
                       stream)
 
@@ -1141,10 +1155,9 @@ def _tree_call(q, k_pages, v_pages, block_table, seqlens, o, lse, tree_mask, q_l
     lib = load()
     with _on(dev):
         if workspace is None:
-            workspace = torch.empty(_tree_workspace(Hq, Hkv, T, d, kind, dev.index), dtype=torch.uint8,
-                                    device=dev)
-            if stream is not None:
-                _used_on(stream, workspace)
+            with _made_on(stream, dev):
+                workspace = torch.empty(_tree_workspace(Hq, Hkv, T, d, kind, dev.index), dtype=torch.uint8,
+                                        device=dev)
         elif not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         rc = lib.attn_decode_tree(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
@@ -1189,9 +1202,10 @@ def decode_tree(q, k_pages, v_pages, block_table, seqlens, tree_mask=None, q_len
     out_dtype = out_dtype or torch.bfloat16
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out_dtype must be bfloat16 or float32")
-    o = torch.empty(q.shape, dtype=out_dtype, device=q.device)
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
+    with _made_on(stream, q.device):
+        o = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
     if stream is not None:
-        _used_on(stream, o, lse)
+        _used_here(q.device, o, lse)
     return _tree_call(q, k_pages, v_pages, block_table, seqlens, o, lse, tree_mask, q_lens, k_descale,
                       v_descale, scale, None, stream)
