@@ -77,7 +77,8 @@ constexpr int kBadTiles = 10;
 constexpr int kDs = 4;
 
 struct TcBars {
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], s_full[2], o_half[2], o_full[2];
+    uint64_t p_full[2][2];            // [stream][half of the tile's keys]
     uint64_t full[8], empty[8];       // tiles of K and V; E4M3: of V in fp16
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];  // E4M3 codes
     uint64_t ds_full[kDs], ds_empty[kDs];
@@ -295,30 +296,33 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
         x.set(p);
         const bool pair = x.pair;
         const int n0 = pair ? x.n : (x.n + 1) / 2, n1 = pair ? x.n : x.n / 2;  // tiles of each stream
-        uint32_t slot_k = 0, slot_v = 0;
-        auto scores = [&](auto T) {
+        uint32_t slot_k[2] = {0u, 0u}, slot_v[2] = {0u, 0u};  // (a pair's: [0])
+        auto scores = [&](auto T) {  // of stream T's next tile
             constexpr int t = decltype(T)::value;
+            const uint32_t slot = slot_k[pair ? 0 : t];
             const uint32_t a_lo = pair ? q_lo[t] : q_lo[0];
+            const uint32_t to = tmem + t * 128;
             if constexpr (F8) {
                 // both of Q's terms times K's codes
-                const uint32_t k_lo = sdesc_lo(smem_u32(smem + C::kK) + slot_k * C::kCodes, 16);
+                const uint32_t k_lo = sdesc_lo(smem_u32(smem + C::kK) + slot * C::kCodes, 16);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_ss_f8_warp(tmem + t * 128,
-                                   sdesc_join(a_lo + (kk >> 2) * (16384 >> 4) + (kk & 3) * (32 >> 4), kTcDescHi),
+                    mma_ss_f8_warp(to, sdesc_join(a_lo + (kk >> 2) * (16384 >> 4) + (kk & 3) * (32 >> 4), kTcDescHi),
                                    sdesc_join(k_lo + (kk & 3) * (32 >> 4), kTcDescHi), idS, kk > 0 ? 1u : 0u);
             } else {
-                const uint32_t k_lo = sdesc_lo(ring + slot_k * C::kTile, 16);
+                const uint32_t k_lo = sdesc_lo(ring + slot * C::kTile, 16);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t step = (kk >> 2) * (16384 >> 4) + (kk & 3) * (32 >> 4);
-                    mma_ss_warp(tmem + t * 128, sdesc_join(a_lo + step, kTcDescHi), sdesc_join(k_lo + step, kTcDescHi),
-                                idS, kk > 0 ? 1u : 0u);
+                    mma_ss_warp(to, sdesc_join(a_lo + step, kTcDescHi), sdesc_join(k_lo + step, kTcDescHi), idS,
+                                kk > 0 ? 1u : 0u);
                 }
             }
             mma_commit_warp(smem_u32(&bars->s_full[t]));
-            if (!pair || t == 1) mma_commit_warp(smem_u32(F8 ? &bars->k_empty[slot_k] : &bars->empty[slot_k]));
+            if (!pair || t == 1) mma_commit_warp(smem_u32(F8 ? &bars->k_empty[slot] : &bars->empty[slot]));
         };
+        std::integral_constant<int, 0> I0;
+        std::integral_constant<int, 1> I1;
         auto begin = [&](auto T) {
             constexpr int t = decltype(T)::value;
             if ((t == 0 ? n0 : n1) == 0 || !ok) return;
@@ -327,19 +331,20 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
                 if (!ok) return;
                 tc_fence_after();
             }
-            if (!pair || t == 0) slot_k = take_k();
+            if (!pair || t == 0) slot_k[t] = take_k();
             if (ok) scores(T);
         };
-        auto step = [&](auto T, int s) {
-            constexpr int t = decltype(T)::value;
+        // half H of the product with V of stream T's tile s; after the second the next scores
+        auto step = [&](auto T, auto H, int s) {
+            constexpr int t = decltype(T)::value, h = decltype(H)::value;
             const int n = t == 0 ? n0 : n1;
             if (s >= n || !ok) return;
-            if (!pair || t == 0) {
-                slot_v = take();
+            if (h == 0 && (!pair || t == 0)) {
+                slot_v[t] = take();
                 if (!F8 && ok && x.special(x.tile(s, t))) {
                     // the fixers work on it while this stream's softmax still runs
                     if (elect_one()) {
-                        *((volatile int*)&bars->fix_slot) = (int)slot_v;
+                        *((volatile int*)&bars->fix_slot) = (int)slot_v[t];
                         mbar_arrive(smem_u32(&bars->fix_ask));
                     }
                     __syncwarp();
@@ -347,29 +352,36 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
                 }
                 if (!ok) return;
             }
-            ok = warp_wait(&bars->p_full[t], cnt_p[t]++, abort_flag, 32);
+            ok = warp_wait(&bars->p_full[t][h], cnt_p[t], abort_flag, 32);
             if (!ok) return;
             tc_fence_after();
-            const uint32_t v_lo = sdesc_lo(ring + slot_v * C::kTile, 16384);
+            const uint32_t slot = slot_v[pair ? 0 : t];
+            const uint32_t v_lo = sdesc_lo(ring + slot * C::kTile, 16384);
 #pragma unroll
-            for (int kk = 0; kk < kTcKeys / 16; ++kk)
-                mma_ts_warp(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
-                            sdesc_join(v_lo + kk * (2048 >> 4), kTcDescHi), idO, (s > 0 || kk > 0) ? 1u : 0u);
-            if (!pair || t == 1) mma_commit_warp(smem_u32(&bars->empty[slot_v]));
+            for (int kk = 0; kk < kTcKeys / 32; ++kk)
+                mma_ts_warp(tmem + 256 + t * 128, tmem + t * 128 + h * 64 + kk * 8,
+                            sdesc_join(v_lo + (4 * h + kk) * (2048 >> 4), kTcDescHi), idO,
+                            (s > 0 || h > 0 || kk > 0) ? 1u : 0u);
+            if (h == 0) {
+                mma_commit_warp(smem_u32(&bars->o_half[t]));
+                return;
+            }
+            ++cnt_p[t];
+            if (!pair || t == 1) mma_commit_warp(smem_u32(&bars->empty[slot]));
             if (s + 1 < n) {
-                if (!pair || t == 0) slot_k = take_k();
-                if (ok) scores(T);  // in order after the product that reads P over it
+                if (!pair || t == 0) slot_k[t] = take_k();
+                if (ok) scores(T);  // in order after the products that read P over it
             } else {
                 mma_commit_warp(smem_u32(&bars->o_full[t]));
             }
         };
-        std::integral_constant<int, 0> S0;
-        std::integral_constant<int, 1> S1;
-        begin(S0);
-        begin(S1);
+        begin(I0);
+        begin(I1);
         for (int s = 0; s < n0 && ok; ++s) {
-            step(S0, s);
-            step(S1, s);
+            step(I0, I0, s);
+            step(I0, I1, s);
+            step(I1, I0, s);
+            step(I1, I1, s);
         }
     }
     if (!ok && elect_one()) tc_abort(bars, p.err);
@@ -587,16 +599,16 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
 }
 
 // -------------------------------------------------------------------- softmax
-// A row's mask over the 128 keys of a tile: bit i of word w is key u0 + 32 w + i,
+// A row's mask over 64 keys: bit i of word w is key u0 + 32 w + i,
 // counted from the first drafted token (negative: before it).  `mask`: the row's
 // words where T <= 64.
 __device__ __forceinline__ void tc_allow(const TreeParams& p, int b, int t, int drafted, int u0,
-                                         uint2 mask, uint32_t (&allow)[4]) {
+                                         uint2 mask, uint32_t (&allow)[2]) {
     const int seen = p.mask ? drafted : min(t + 1, drafted);
-    uint32_t bits[5];
+    uint32_t bits[3];
     const int first = u0 >> 5;  // (floor) 32-bit word of the row's mask that u0 falls in
 #pragma unroll
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 3; ++i) {
         const int at = first + i;
         bits[i] = 0xFFFFFFFFu;  // before the drafted tokens, or no mask
         if (p.mask && at >= 0) {
@@ -609,7 +621,7 @@ __device__ __forceinline__ void tc_allow(const TreeParams& p, int b, int t, int 
         }
     }
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < 2; ++w) {
         const int n = seen - (u0 + 32 * w);  // keys below `seen`
         const uint32_t range = n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
         allow[w] = __funnelshift_r(bits[w], bits[w + 1], u0 & 31) & range;
@@ -631,24 +643,23 @@ struct TcRow {
     int fexp;        // E4M3: F of what O holds
 };
 
-// One 128-key tile of a row: the maximum over all of it, O rescaled if that
-// moved by more than tau (or, E4M3, if F grew), then P over S's first 64 columns.
+// Half a tile of a row, 64 keys: the maximum over all of it, O rescaled if that
+// moved by more than tau (or, E4M3, if F grew), then P over S's first 32 columns.
 // The scores stay in registers between the two; E4M3 multiplies them with K's
 // descales, which every lane reads from the same shared address (a wavefront for
-// four bytes: read once, not once for each use).
-template <int D, bool F8>
-__device__ __forceinline__ void tc_softmax_tile(uint32_t tS, uint32_t tO, const float* kf, int fexp, bool special,
-                                                const uint32_t (&allow)[4], bool first, float c, int ncols,
-                                                TcRow& r) {
-    uint32_t sr[128];
+// four bytes: read once, not once for each use).  `stable()`: waits until no product
+// is adding to O.
+template <bool F8, class Stable>
+__device__ __forceinline__ void tc_softmax_half(uint32_t tS, uint32_t tO, const float* kf, int fexp, bool special,
+                                                const uint32_t (&allow)[2], bool first, float c, int ncols,
+                                                TcRow& r, Stable stable) {
+    uint32_t sr[64];
     tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
     tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-    tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
-    tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
     tmem_wait_ld();
     if constexpr (F8) {
 #pragma unroll
-        for (int i = 0; i < 128; i += 4) {
+        for (int i = 0; i < 64; i += 4) {
             const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(kf + i);
             float u, v;
             f2_split(f2_mul(f2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), k.x), u, v);
@@ -661,14 +672,14 @@ __device__ __forceinline__ void tc_softmax_tile(uint32_t tS, uint32_t tO, const 
     }
     if (special) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i)
+        for (int i = 0; i < 64; ++i)
             if (!(allow[i >> 5] >> (i & 31) & 1u)) sr[i] = 0xFF800000u;
     }
     float mx;
     {
         float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 128; i += 8) {
+        for (int i = 0; i < 64; i += 8) {
             m0 = fmax3(m0, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
             m1 = fmax3(m1, __uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3]));
             m2 = fmax3(m2, __uint_as_float(sr[i + 4]), __uint_as_float(sr[i + 5]));
@@ -689,7 +700,7 @@ __device__ __forceinline__ void tc_softmax_tile(uint32_t tS, uint32_t tO, const 
         if constexpr (F8)
             if (grow) alpha = r.fexp - fexp < -126 ? 0.f : alpha * tc_pow2(r.fexp - fexp);
         if (!first) {
-            // O is stable: this S was issued after the product before it
+            stable();
             const uint64_t a2 = f2(alpha, alpha);
 #pragma unroll 1
             for (int cc = 0; cc < ncols; cc += 16) {
@@ -710,14 +721,14 @@ __device__ __forceinline__ void tc_softmax_tile(uint32_t tS, uint32_t tO, const 
     if constexpr (F8) r.fexp = fexp;
     const float m = (r.m == -INFINITY ? 0.f : r.m) - kTcLift<F8>;
     if constexpr (!F8) {
-        // the tile's largest weight is its rounded P: its error enters l too
+        // the largest weight is its rounded P: its error enters l too
         const float pm = mx == -INFINITY ? 0.f : ex2(fmaf(mx, c, -m));
         r.l += bf16lo_to_f32(pack_bf16x2(pm, 0.f)) - pm;
     }
     const uint64_t c2 = f2(c, c), nm2 = f2(-m, -m);
     uint64_t s0 = 0, s1 = 0, s2 = 0, s3 = 0;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < 2; ++g) {
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -954,9 +965,6 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
         int s = 0;
         for (; x.has(s, t) && ok; ++s) {
             const int j = x.tile(s, t);
-            ok = warp_wait(&bars->s_full[t], cnt_s++, abort_flag, 32);
-            if (!ok) break;
-            tc_fence_after();
             const float* kf = nullptr;
             int fexp = 0;
             if constexpr (F8) {
@@ -967,19 +975,35 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
                 kf = bars->kf[slot];
                 fexp = *((volatile int*)&bars->fexp[slot]);
             }
-            if (active) {
-                uint32_t allow[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-                const bool special = x.special(j);
-                if (special)
-                    tc_allow(p, x.w.b, my.tok, x.w.drafted, (x.w.k0 + j) * kTcKeys - x.prefix, mask, allow);
-                tc_softmax_tile<D, F8>(tS, tO + 128 * t, kf, fexp, special, allow, s == 0, c, ncols, st);
-                tmem_wait_st();
+            const bool special = x.special(j);
+            ok = warp_wait(&bars->s_full[t], cnt_s, abort_flag, 32);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                if (active) {
+                    uint32_t allow[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+                    if (special)
+                        tc_allow(p, x.w.b, my.tok, x.w.drafted, (x.w.k0 + j) * kTcKeys + 64 * h - x.prefix, mask,
+                                 allow);
+                    // (S was issued after the tile before; of this one the first half's product)
+                    auto stable = [&]() {
+                        if (h == 0) return;
+                        ok = warp_wait(&bars->o_half[t], cnt_s, abort_flag);
+                        tc_fence_after();
+                    };
+                    tc_softmax_half<F8>(tS + 64 * h, tO + 128 * t, F8 ? kf + 64 * h : nullptr, fexp, special, allow,
+                                        s == 0 && h == 0, c, ncols, st, stable);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[t][h]));
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_u32(&bars->p_full[t]));
-                if constexpr (F8) {
+            if (!ok) break;
+            ++cnt_s;
+            if constexpr (F8) {
+                if (lane == 0) {
                     const uint32_t e = smem_u32(&bars->ds_empty[(tiles + (uint32_t)j) % kDs]);
                     mbar_arrive(e);
                     if (!x.pair) mbar_arrive(e);  // (the barrier counts both streams' warps)
@@ -1079,8 +1103,11 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the merge waits by itself)
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&bars->q_full[t]), 4);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(smem_u32(&bars->p_full[t][h]), 4);
+            }
             mbar_init(smem_u32(&bars->s_full[t]), 1);
-            mbar_init(smem_u32(&bars->p_full[t]), 4);
+            mbar_init(smem_u32(&bars->o_half[t]), 1);
             mbar_init(smem_u32(&bars->o_full[t]), 1);
         }
         for (int i = 0; i < 8; ++i) {
