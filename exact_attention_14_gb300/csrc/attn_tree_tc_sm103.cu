@@ -46,14 +46,16 @@ template <bool F8>
 constexpr float kTcLift = F8 ? 7.0f : 0.0f;
 constexpr float kTcLn2 = 0.69314718055994530942f;
 
-template <int D, bool F8>
+// ONE: no item has more than 128 rows (every piece is split): the shared memory of a
+// second Q tile holds more of K and V.
+template <int D, bool F8, bool ONE>
 struct TcCfg {
     static constexpr int kTile = 128 * D * 2;                  // 16-bit operand tile (Q's two terms)
-    static constexpr int kStages = F8 ? 2 : (D == 128 ? 4 : 8);  // of K and V, E4M3: of V in fp16
+    static constexpr int kStages = F8 ? 2 : (D == 128 ? (ONE ? 5 : 4) : 8);  // of K and V, E4M3: of V in fp16
     static constexpr int kCodes = 128 * 128;                   // E4M3 codes of a tile
-    static constexpr int kKStages = F8 ? 3 : 0;                // K's codes, with K's and V's descales
-    static constexpr int kVStages = F8 ? 2 : 0;                // V's codes
-    static constexpr int kRing = 2 * kTile;                    // after Q0, Q1
+    static constexpr int kKStages = F8 ? (ONE ? 4 : 3) : 0;                // K's codes, with K's and V's descales
+    static constexpr int kVStages = F8 ? (ONE ? 3 : 2) : 0;                // V's codes
+    static constexpr int kRing = (ONE ? 1 : 2) * kTile;         // after Q0, Q1
     static constexpr int kK = kRing + kStages * kTile;
     static constexpr int kV = kK + kKStages * kCodes;
     static constexpr int kDescale = kV + kVStages * kCodes;
@@ -61,12 +63,17 @@ struct TcCfg {
     static constexpr int kSmem = kBar + 12 * 1024;
     static_assert(kSmem <= 232448, "shared memory budget");
 };
-constexpr int kTcThreads = 384;
-// registers of the control and the softmax warpgroups: their sum is the launch's
-// (168 a thread)
-constexpr int kTcRegsControl = 104, kTcRegsSoftmax = 200;
-static_assert(128 * kTcRegsControl + 256 * kTcRegsSoftmax <= kTcThreads * 168, "register split");
-constexpr int kTcHelpers = 2;  // warps 2-3: V's fixers (bf16) or the converters (E4M3)
+template <bool F8, bool ONE>
+struct TcRoles {
+    static constexpr bool kMany = F8 && ONE;        // eight control warps
+    static constexpr int kControl = kMany ? 8 : 4;  // the softmax warps come after them
+    static constexpr int kThreads = 32 * (kControl + 8);
+    static constexpr int kConverters = kMany ? 4 : 2;  // E4M3: the last control warps
+    // registers of the control and the softmax warpgroups: their sum is the launch's
+    static constexpr int kLaunch = kMany ? 128 : 168;
+    static constexpr int kRegsControl = kMany ? 80 : 104, kRegsSoftmax = kMany ? 176 : 200;
+    static_assert(32 * kControl * kRegsControl + 256 * kRegsSoftmax <= kThreads * kLaunch, "register split");
+};
 
 // Marks of the V rows that were taken out: for each of the last pieces, for
 // each of its special tiles (1024 drafted tokens reach over 10 at most), a bit
@@ -82,12 +89,11 @@ struct TcBars {
     uint64_t full[8], empty[8];       // tiles of K and V; E4M3: of V in fp16
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];  // E4M3 codes
     uint64_t ds_full[kDs], ds_empty[kDs];
-    uint64_t fix_ask, fix_done;       // V of a special tile is there / is prepared
-    uint64_t stat, done, drain;
+    uint64_t fix_ask[2], fix_done[2];  // V of a special tile (of a stream; a pair's: [0]) is there / is prepared
+    uint64_t stat, done, drain[2];
     TreeRange range;
     uint32_t tmem_base;
     int abort;
-    int fix_slot;
     uint32_t bad[kBadBufs][kBadTiles][4];
     float qs[2][128];                   // E4M3: what a row's products are multiplied with
     float m[2][128], l[2][128], lx[2][128];
@@ -150,67 +156,150 @@ struct TcPiece {
     __device__ __forceinline__ bool has(int s, int t) const { return tile(s, t) < n; }
     // a tile with drafted tokens or past the sequence's end
     __device__ __forceinline__ bool special(int j) const { return (w.k0 + j + 1) * kTcKeys > prefix; }
+    // Where K and V of tile j lie in the order of a piece's 2 n bf16 loads: K of the
+    // first tile of each stream, then per tile its V and the K of the stream's next.
+    __device__ __forceinline__ int place_k(int j) const {
+        const int ahead = pair ? 1 : 2;
+        return j < ahead ? j : 2 * j - ahead + 1;
+    }
+    __device__ __forceinline__ int place_v(int j) const { return j + min(j + (pair ? 1 : 2), n); }
     __device__ __forceinline__ int first_special() const { return max(0, prefix / kTcKeys - w.k0); }
 };
 
 // ------------------------------------------------------------------ producer
+// A ring of tiles that one warp fills.
+struct TcRing {
+    uint64_t *full, *empty;
+    int slots, slot;
+    uint32_t round;
+    // The next slot once it is free, with `bytes` announced; -1: given up.
+    __device__ __forceinline__ int take(int bytes, int lane, const volatile int* abort_flag) {
+        if (round > 0 && !warp_wait(&empty[slot], round - 1u, abort_flag)) return -1;
+        if (lane == 0) mbar_arrive_expect_tx(smem_u32(&full[slot]), bytes);
+        __syncwarp();
+        return slot;
+    }
+    __device__ __forceinline__ void next() {
+        __syncwarp();
+        if (++slot == slots) {
+            slot = 0;
+            ++round;
+        }
+    }
+    __device__ __forceinline__ void land() {  // every copy lands
+        for (int i = 0; i < slots; ++i) {
+            const uint32_t n = round + (i < slot ? 1u : 0u);
+            if (n > 0) mbar_wait(smem_u32(&full[i]), (n - 1u) & 1u, nullptr);
+        }
+        __syncwarp();
+    }
+};
+
+// E4M3, a warp lays out the next tile's descales once its K is there: K's for the
+// softmax, V's over F for the converters, F = 2^fexp above every one of the piece so
+// far.  (K's codes go into the product as they are: rounded descales would enter the
+// exponent.)
+template <class C>
+struct TcDescales {
+    uint32_t tiles, kslot, kround;
+    int fexp;
+    __device__ __forceinline__ bool tile(uint8_t* smem, TcBars* bars, const TreePiece& w, int kt, int lane,
+                                         const volatile int* abort_flag) {
+        const uint32_t slot = tiles % kDs;
+        if (!warp_wait(&bars->k_full[kslot], kround, abort_flag)) return false;
+        if (tiles >= kDs && !warp_wait(&bars->ds_empty[slot], tiles / kDs - 1u, abort_flag)) return false;
+        const float* raw = reinterpret_cast<const float*>(smem + C::kDescale + kslot * 1024);
+        const int key0 = kt * kTcKeys + lane;
+        float kd[4], vd[4], top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            kd[i] = raw[32 * i + lane];
+            vd[i] = raw[128 + 32 * i + lane];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int key = key0 + 32 * i;
+            // past the sequence, or a row that is added apart
+            if (key >= w.keys || (key >= w.keys - w.drafted && !isfinite(vd[i]))) vd[i] = 0.f;
+            top = fmaxf(top, fabsf(vd[i]));
+        }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
+        fexp = max(fexp, min((int)(__float_as_uint(top) >> 23) - 126, 111));
+        const float fr = tc_pow2(-fexp);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            bars->kf[slot][32 * i + lane] = kd[i];
+            bars->wv[slot][32 * i + lane] = vd[i] * fr;
+        }
+        if (lane == 0) bars->fexp[slot] = fexp;
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(smem_u32(&bars->ds_full[slot]));
+            mbar_arrive(smem_u32(&bars->k_empty[kslot]));
+        }
+        ++tiles;
+        if (++kslot == C::kKStages) {
+            kslot = 0;
+            ++kround;
+        }
+        return true;
+    }
+};
+// A lane's box of K's codes, with both descales.
+template <class C>
+__device__ __forceinline__ void tc_copy_k_codes(const CUtensorMap* map, uint8_t* smem, uint32_t bar, int slot, int lane,
+                                                const TreeParams& p, int h, int page, int off) {
+    tma_load_4d(smem_u32(smem + C::kK) + slot * C::kCodes + lane * p.box_keys * 128, map, bar, 0, h, off, page);
+    const long long at = ((long long)page * p.Hkv + h) * p.page_size + off;
+    const uint32_t ds = smem_u32(smem + C::kDescale) + slot * 1024 + lane * p.box_keys * 4;
+    bulk_load(ds, page < 0 ? kTreeNoDescale : p.k_descale + at, p.box_keys * 4, bar);
+    bulk_load(ds + 512, page < 0 ? kTreeNoDescale : p.v_descale + at, p.box_keys * 4, bar);
+}
+
 // A warp; each of its first lanes copies the tile's box of its own number.  The
 // loads of a piece come in the order the products take them: K of the first
 // tile of each stream, then per tile its V and the K of the stream's next tile.
-template <int D, bool F8>
+template <int D, bool F8, bool ONE>
 __device__ void tc_produce(const CUtensorMap* tk, const CUtensorMap* tv, uint8_t* smem, TcBars* bars,
                            const TreeParams& p) {
-    using C = TcCfg<D, F8>;
+    using C = TcCfg<D, F8, ONE>;
     const int lane = threadIdx.x & 31;
     const uint32_t mine = lane * p.box_keys * 128;
     const volatile int* abort_flag = &bars->abort;
     const bool copies = lane < kTcKeys / p.box_keys;
-    struct Ring {
-        uint64_t *full, *empty;
-        int slot;
-        uint32_t round;
-    };
-    Ring ring_k = {F8 ? bars->k_full : bars->full, F8 ? bars->k_empty : bars->empty, 0, 0u};
-    Ring ring_v = {bars->v_full, bars->v_empty, 0, 0u};  // (bf16: K and V share one)
+    TcRing ring_k = {F8 ? bars->k_full : bars->full, F8 ? bars->k_empty : bars->empty, F8 ? C::kKStages : C::kStages, 0, 0u};
+    TcRing ring_v = {bars->v_full, bars->v_empty, C::kVStages, 0, 0u};  // (bf16: K and V share the other)
+    TcDescales<C> descales = {0u, 0u, 0u, 0};
     bool ok = true;
     TreeWalk walk;
     walk.start(bars->range);
     TcPiece x;
-    auto load = [&](auto IsV, int page, int off) {
-        constexpr bool is_v = decltype(IsV)::value;
-        constexpr int slots = !F8 ? C::kStages : (is_v ? C::kVStages : C::kKStages);
-        Ring& r = F8 && is_v ? ring_v : ring_k;
-        if (r.round > 0) ok = warp_wait(&r.empty[r.slot], r.round - 1u, abort_flag);
-        if (!ok) return;
-        const CUtensorMap* map = is_v ? tv : tk;
-        const uint32_t bar = smem_u32(&r.full[r.slot]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, !F8 ? C::kTile : (is_v ? C::kCodes : C::kCodes + 1024));
-        __syncwarp();
-        if (copies) {
-            if constexpr (F8) {
-                tma_load_4d(smem_u32(smem + (is_v ? C::kV : C::kK)) + r.slot * C::kCodes + mine, map, bar, 0, x.w.h, off, page);
-                if constexpr (!is_v) {
-                    const long long at = ((long long)page * p.Hkv + x.w.h) * p.page_size + off;
-                    const uint32_t ds = smem_u32(smem + C::kDescale) + r.slot * 1024 + lane * p.box_keys * 4;
-                    bulk_load(ds, page < 0 ? kTreeNoDescale : p.k_descale + at, p.box_keys * 4, bar);
-                    bulk_load(ds + 512, page < 0 ? kTreeNoDescale : p.v_descale + at, p.box_keys * 4, bar);
-                }
-            } else {
-                const uint32_t to = smem_u32(smem + C::kRing) + r.slot * C::kTile + mine;
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) tma_load_4d(to + c * 16384, map, bar, 64 * c, x.w.h, off, page);
-            }
-        }
-        __syncwarp();
-        if (++r.slot == slots) {
-            r.slot = 0;
-            ++r.round;
-        }
-    };
-    std::false_type K;
-    std::true_type V;
     while (ok && walk.next(p, x.w)) {
         x.set(p);
+        auto load = [&](auto IsV, int page, int off) {
+            constexpr bool is_v = decltype(IsV)::value;
+            TcRing& r = F8 && is_v ? ring_v : ring_k;
+            const int slot = r.take(!F8 ? C::kTile : (is_v ? C::kCodes : C::kCodes + 1024), lane, abort_flag);
+            ok = slot >= 0;
+            if (!ok) return;
+            const uint32_t bar = smem_u32(&r.full[slot]);
+            if (copies) {
+                if constexpr (!F8) {
+                    const uint32_t to = smem_u32(smem + C::kRing) + slot * C::kTile + mine;
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_4d(to + c * 16384, is_v ? tv : tk, bar, 64 * c, x.w.h, off, page);
+                } else if constexpr (is_v) {
+                    tma_load_4d(smem_u32(smem + C::kV) + slot * C::kCodes + mine, tv, bar, 0, x.w.h, off, page);
+                } else {
+                    tc_copy_k_codes<C>(tk, smem, bar, slot, lane, p, x.w.h, page, off);
+                }
+            }
+            r.next();
+        };
+        std::false_type K;
+        std::true_type V;
         // pages of the tiles whose K has been loaded and whose V has not, and of
         // the next one (looked up before the wait that precedes its loads)
         int page[3], off[3];
@@ -223,6 +312,7 @@ __device__ void tc_produce(const CUtensorMap* tk, const CUtensorMap* tv, uint8_t
         look(0, 0);
         look(1, 1);
         look(2, 2);
+        descales.fexp = -100;
         load(K, page[0], off[0]);
         if (!x.pair && x.n > 1 && ok) load(K, page[1], off[1]);
         for (int j = 0; j < x.n && ok; ++j) {
@@ -232,29 +322,77 @@ __device__ void tc_produce(const CUtensorMap* tk, const CUtensorMap* tv, uint8_t
             } else {
                 if (ok && j + 2 < x.n) load(K, page[2], off[2]);
             }
+            if constexpr (F8) ok = ok && descales.tile(smem, bars, x.w, x.w.k0 + j, lane, abort_flag);
             page[0] = page[1]; off[0] = off[1];
             page[1] = page[2]; off[1] = off[2];
             look(2, j + 3);
         }
     }
     if (!ok && lane == 0) tc_abort(bars, p.err);
-    auto land = [&](const Ring& r, int slots) {  // every copy lands
-        for (int i = 0; i < slots; ++i) {
-            const uint32_t n = r.round + (i < r.slot ? 1u : 0u);
-            if (n > 0) mbar_wait(smem_u32(&r.full[i]), (n - 1u) & 1u, nullptr);
+    ring_k.land();
+    if constexpr (F8) ring_v.land();
+}
+
+// E4M3 with eight control warps: a warp for K's codes and descales, another for V's
+// codes that also lays the descales out (all of it in one warp takes longer than the
+// copies themselves).
+template <bool V, class C>
+__device__ void tc_produce_codes(const CUtensorMap* map, uint8_t* smem, TcBars* bars, const TreeParams& p) {
+    const int lane = threadIdx.x & 31;
+    const volatile int* abort_flag = &bars->abort;
+    const bool copies = lane < kTcKeys / p.box_keys;
+    TcRing ring = {V ? bars->v_full : bars->k_full, V ? bars->v_empty : bars->k_empty, V ? C::kVStages : C::kKStages, 0, 0u};
+    TcDescales<C> descales = {0u, 0u, 0u, 0};
+    bool ok = true;
+    TreeWalk walk;
+    walk.start(bars->range);
+    TreePiece w;
+    while (ok && walk.next(p, w)) {
+        descales.fexp = -100;
+        // pages of this lane's box in the next two tiles
+        int page[2], off[2];
+        auto look = [&](int i, int kt) {
+            page[i] = -1;
+            off[i] = 0;
+            if (copies && kt < w.k1) page[i] = tree_page(p, w.b, kt * kTcKeys + lane * p.box_keys, w.keys, off[i]);
+        };
+        look(0, w.k0);
+        look(1, w.k0 + 1);
+        for (int kt = w.k0; kt < w.k1; ++kt) {
+            const int slot = ring.take(V ? C::kCodes : C::kCodes + 1024, lane, abort_flag);
+            ok = slot >= 0;
+            if (!ok) break;
+            if (copies) {
+                const uint32_t bar = smem_u32(&ring.full[slot]);
+                if constexpr (V)
+                    tma_load_4d(smem_u32(smem + C::kV) + slot * C::kCodes + lane * p.box_keys * 128, map, bar, 0, w.h,
+                                off[0], page[0]);
+                else
+                    tc_copy_k_codes<C>(map, smem, bar, slot, lane, p, w.h, page[0], off[0]);
+            }
+            ring.next();
+            page[0] = page[1];
+            off[0] = off[1];
+            look(1, kt + 2);
+            if constexpr (V) {
+                ok = descales.tile(smem, bars, w, kt, lane, abort_flag);
+                if (!ok) break;
+            }
         }
-    };
-    land(ring_k, F8 ? C::kKStages : C::kStages);
-    if constexpr (F8) land(ring_v, C::kVStages);
-    __syncwarp();
+    }
+    if (!ok && lane == 0) tc_abort(bars, p.err);
+    ring.land();
 }
 
 // ----------------------------------------------------------------- MMA issuer
 constexpr uint32_t kTcDescHi = sdesc_hi_sw128(1024);
 
-template <int D, bool F8>
+// One warp for both streams, a stream after the other: while one's products run the
+// other's softmax does, and two warps here let them fall into step (bf16, 64 drafts
+// 246 -> 270 us, E4M3 320 -> 355).
+template <int D, bool F8, bool ONE>
 __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreeParams& p) {
-    using C = TcCfg<D, F8>;
+    using C = TcCfg<D, F8, ONE>;
     const volatile int* abort_flag = &bars->abort;
     constexpr uint32_t idS = F8 ? make_idesc_e4m3(128, kTcKeys) : make_idesc_bf16(128, kTcKeys, 0, 0);
     // (E4M3: P and V both fp16, format code 0)
@@ -262,7 +400,7 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
     const uint32_t q_lo[2] = {sdesc_lo(smem_u32(smem), 16), sdesc_lo(smem_u32(smem + C::kTile), 16)};
     const uint32_t ring = smem_u32(smem + C::kRing);
     uint32_t slot = 0, round = 0;  // of the next operand tile
-    uint32_t cnt_q[2] = {0u, 0u}, cnt_p[2] = {0u, 0u}, cnt_fix = 0;
+    uint32_t cnt_q[2] = {0u, 0u}, cnt_p[2] = {0u, 0u}, cnt_fix[2] = {0u, 0u};
     bool ok = true;
     auto take = [&]() {
         const uint32_t mine = slot;
@@ -343,12 +481,9 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
                 slot_v[t] = take();
                 if (!F8 && ok && x.special(x.tile(s, t))) {
                     // the fixers work on it while this stream's softmax still runs
-                    if (elect_one()) {
-                        *((volatile int*)&bars->fix_slot) = (int)slot_v[t];
-                        mbar_arrive(smem_u32(&bars->fix_ask));
-                    }
+                    if (elect_one()) mbar_arrive(smem_u32(&bars->fix_ask[t]));
                     __syncwarp();
-                    ok = warp_wait(&bars->fix_done, cnt_fix++, abort_flag);
+                    ok = warp_wait(&bars->fix_done[t], cnt_fix[t]++, abort_flag);
                 }
                 if (!ok) return;
             }
@@ -383,22 +518,140 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
             step(I1, I0, s);
             step(I1, I1, s);
         }
+        if (n1 == 0) mma_commit_warp(smem_u32(&bars->o_full[1]));
     }
     if (!ok && elect_one()) tc_abort(bars, p.err);
-    mma_commit_warp(smem_u32(&bars->drain));  // every product is done before TMEM goes
-    mbar_wait(smem_u32(&bars->drain), 0, nullptr);
+    mma_commit_warp(smem_u32(&bars->drain[0]));  // every product is done before TMEM goes
+    mbar_wait(smem_u32(&bars->drain[0]), 0, nullptr);
+    __syncwarp();
+}
+
+// Split pieces only: a warp per stream, so that neither waits for the other's softmax
+// (E4M3, 16 drafts 242 -> 200 us, bf16 186 -> 183).
+template <int D, bool F8, bool ONE>
+__device__ void tc_mma_stream(int t, uint8_t* smem, TcBars* bars, uint32_t tmem, const TreeParams& p) {
+    using C = TcCfg<D, F8, ONE>;
+    const volatile int* abort_flag = &bars->abort;
+    constexpr uint32_t idS = F8 ? make_idesc_e4m3(128, kTcKeys) : make_idesc_bf16(128, kTcKeys, 0, 0);
+    // (E4M3: P and V both fp16, format code 0)
+    constexpr uint32_t idO = make_idesc_bf16(128, D, 0, 1) & ~(F8 ? (1u << 7) | (1u << 10) : 0u);
+    const uint32_t ring = smem_u32(smem + C::kRing);
+    const uint32_t tS = tmem + t * 128, tO = tmem + 256 + t * 128;
+    uint32_t loads = 0;  // tiles (E4M3), loads (bf16) of the pieces before
+    uint32_t cnt_p = 0, cnt_fix = 0;
+    const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
+    bool ok = true;
+    // A ring's tiles are waited for one after another, the other stream's too, and
+    // those are let go of at once: a slot is free when its reader is done with it and
+    // the other has passed it, so that neither ever misses a phase of its barrier.
+    struct Seen {
+        uint64_t *full, *empty;
+        uint32_t slot, round, at;
+    };
+    Seen seen_k = {F8 ? bars->k_full : bars->full, F8 ? bars->k_empty : bars->empty, 0u, 0u, 0u};
+    Seen seen_v = {bars->full, bars->empty, 0u, 0u, 0u};  // (bf16: K and V share one ring)
+    auto see = [&](Seen& s, auto Slots, uint32_t upto, bool mine) {  // `mine`: the last of them
+        while (ok && s.at < upto) {
+            ok = warp_wait(&s.full[s.slot], s.round, abort_flag);
+            ++s.at;
+            if (!(mine && s.at == upto) && elect_one()) mbar_arrive(smem_u32(&s.empty[s.slot]));
+            __syncwarp();
+            if (++s.slot == decltype(Slots)::value) {
+                s.slot = 0;
+                ++s.round;
+            }
+        }
+    };
+    std::integral_constant<uint32_t, F8 ? C::kKStages : C::kStages> SlotsK;
+    std::integral_constant<uint32_t, C::kStages> SlotsV;
+    auto see_k = [&](uint32_t upto, bool mine) { see(seen_k, SlotsK, upto, mine); };
+    auto see_v = [&](uint32_t upto, bool mine) {
+        if constexpr (F8) see(seen_v, SlotsV, upto, mine);
+        else see(seen_k, SlotsK, upto, mine);
+    };
+    TreeWalk walk;
+    walk.start(bars->range);
+    TcPiece x;
+    for (uint32_t piece = 0; ok && walk.next(p, x.w); ++piece) {
+        x.set(p);
+        // (also without a tile: this keeps step with the softmax warps)
+        ok = warp_wait(&bars->q_full[0], piece, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        auto scores = [&](int j) {
+            const uint32_t at = F8 ? loads + j : loads + x.place_k(j);
+            const uint32_t slot = at % (F8 ? C::kKStages : C::kStages);
+            see_k(at + 1u, true);
+            if (!ok) return;
+            tc_fence_after();
+            if constexpr (F8) {
+                // both of Q's terms times K's codes
+                const uint32_t k_lo = sdesc_lo(smem_u32(smem + C::kK) + slot * C::kCodes, 16);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_ss_f8_warp(tS, sdesc_join(q_lo + (kk >> 2) * (16384 >> 4) + (kk & 3) * (32 >> 4), kTcDescHi),
+                                   sdesc_join(k_lo + (kk & 3) * (32 >> 4), kTcDescHi), idS, kk > 0 ? 1u : 0u);
+            } else {
+                const uint32_t k_lo = sdesc_lo(ring + slot * C::kTile, 16);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t step = (kk >> 2) * (16384 >> 4) + (kk & 3) * (32 >> 4);
+                    mma_ss_warp(tS, sdesc_join(q_lo + step, kTcDescHi), sdesc_join(k_lo + step, kTcDescHi), idS,
+                                kk > 0 ? 1u : 0u);
+                }
+            }
+            mma_commit_warp(smem_u32(&bars->s_full[t]));
+            mma_commit_warp(smem_u32(F8 ? &bars->k_empty[slot] : &bars->empty[slot]));
+        };
+        if (x.has(0, t)) scores(x.tile(0, t));
+        for (int s = 0; x.has(s, t) && ok; ++s) {
+            const int j = x.tile(s, t);
+            const uint32_t at = F8 ? loads + j : loads + x.place_v(j);
+            const uint32_t slot = at % C::kStages;
+            see_v(at + 1u, true);
+            if (!F8 && ok && x.special(j)) {
+                // the fixer works on it while this stream's softmax still runs
+                if (elect_one()) mbar_arrive(smem_u32(&bars->fix_ask[t]));
+                __syncwarp();
+                ok = warp_wait(&bars->fix_done[t], cnt_fix++, abort_flag);
+            }
+            const uint32_t v_lo = sdesc_lo(ring + slot * C::kTile, 16384);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ok = ok && warp_wait(&bars->p_full[t][h], cnt_p, abort_flag, 32);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < kTcKeys / 32; ++kk)
+                    mma_ts_warp(tO, tS + h * 64 + kk * 8, sdesc_join(v_lo + (4 * h + kk) * (2048 >> 4), kTcDescHi), idO,
+                                (s > 0 || h > 0 || kk > 0) ? 1u : 0u);
+                if (h == 0) mma_commit_warp(smem_u32(&bars->o_half[t]));
+            }
+            if (!ok) break;
+            ++cnt_p;
+            mma_commit_warp(smem_u32(&bars->empty[slot]));
+            if (x.has(s + 1, t)) scores(x.tile(s + 1, t));  // in order after the products that read P over it
+        }
+        loads += F8 ? x.n : 2 * x.n;
+        see_k(loads, false);
+        if (F8) see_v(loads, false);
+        mma_commit_warp(smem_u32(&bars->o_full[t]));  // (also without a tile)
+    }
+    if (!ok && elect_one()) tc_abort(bars, p.err);
+    mma_commit_warp(smem_u32(&bars->drain[t]));  // every product is done before TMEM goes
+    mbar_wait(smem_u32(&bars->drain[t]), 0, nullptr);
     __syncwarp();
 }
 
 // --------------------------------------------------- V of special tiles, bf16
-// Two warps, two keys a thread: rows past the sequence are zeroed, drafted
+// A warp, four keys a thread: rows past the sequence are zeroed, drafted
 // tokens' rows with a NaN or an infinity are noted and zeroed.
-template <int D>
-__device__ void tc_fix(int wf, uint8_t* smem, TcBars* bars, const TreeParams& p) {
-    using C = TcCfg<D, false>;
+template <int D, bool ONE>
+__device__ void tc_fix(uint8_t* smem, TcBars* bars, const TreeParams& p) {
+    using C = TcCfg<D, false, ONE>;
     const int lane = threadIdx.x & 31;
     const volatile int* abort_flag = &bars->abort;
-    uint32_t fixed = 0;
+    uint32_t fixed[2] = {0u, 0u}, loads = 0;
     bool ok = true;
     TreeWalk walk;
     walk.start(bars->range);
@@ -406,14 +659,16 @@ __device__ void tc_fix(int wf, uint8_t* smem, TcBars* bars, const TreeParams& p)
     for (int piece = 0; ok && walk.next(p, x.w); ++piece) {
         x.set(p);
         for (int j = x.first_special(); j < x.n && ok; ++j) {
-            // (the issuer has seen the tile's V arrive, and waits for this)
-            ok = warp_wait(&bars->fix_ask, fixed++, abort_flag);
+            if (!x.special(j)) continue;
+            // (whoever asks has seen the tile's V arrive, and waits for this)
+            const int b = x.pair ? 0 : j & 1;
+            ok = warp_wait(&bars->fix_ask[b], fixed[b]++, abort_flag);
             if (!ok) break;
-            const uint32_t tile = smem_u32(smem + C::kRing + *((volatile int*)&bars->fix_slot) * C::kTile);
+            const uint32_t tile = smem_u32(smem + C::kRing) + (loads + x.place_v(j)) % C::kStages * C::kTile;
             uint32_t* marks = bars->bad[piece % kBadBufs][j - x.first_special()];
 #pragma unroll 1
-            for (int i = 0; i < 2; ++i) {
-                const int row = wf * 64 + i * 32 + lane;
+            for (int i = 0; i < 4; ++i) {
+                const int row = i * 32 + lane;
                 const int key = (x.w.k0 + j) * kTcKeys + row;
                 const uint32_t at = tile + row * 128;
                 bool bad = false;
@@ -428,31 +683,30 @@ __device__ void tc_fix(int wf, uint8_t* smem, TcBars* bars, const TreeParams& p)
                     }
                 }
                 const uint32_t votes = __ballot_sync(0xFFFFFFFFu, bad);
-                if (lane == 0) marks[2 * wf + i] = votes;
+                if (lane == 0) marks[i] = votes;
                 if (bad || key >= x.w.keys)
                     for (int c = 0; c < D / 8; ++c)
                         sts128(at + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4), 0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->fix_done));
+            if (lane == 0) mbar_arrive(smem_u32(&bars->fix_done[b]));
         }
+        loads += 2 * x.n;
     }
     if (!ok && lane == 0) tc_abort(bars, p.err);
 }
 
-// ----------------------------------------------- descales, V's codes to fp16, E4M3
-// Two warps, 64 keys each.  A lane takes 16 of a row's 128 codes.  V is multiplied
-// with its descale over F, F = 2^fexp above every one so far (two fp16 roundings, of
-// the factor and of the product: less than P's and far less than O's).  K's codes
-// go into the product as they are, K's descales, whose rounding would enter the
-// exponent, are left to the softmax.
-template <int D>
+// ------------------------------------------------------- V's codes to fp16, E4M3
+// NC warps, 128 / NC keys each.  A lane takes 16 of a row's 128 codes, times the row's
+// descale over F: two fp16 roundings, of the factor and of the product, less than
+// P's and far less than O's.
+template <int NC, class C>
 __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams& p) {
-    using C = TcCfg<D, true>;
+    constexpr int kRows = 128 / NC;
     const int lane = threadIdx.x & 31;
     const volatile int* abort_flag = &bars->abort;
-    uint32_t raw_slot = 0, raw_round = 0, out_slot = 0, out_round = 0, tiles = 0, kslot = 0, kround = 0;
+    uint32_t raw_slot = 0, raw_round = 0, out_slot = 0, out_round = 0, tiles = 0;
     bool ok = true;
     TreeWalk walk;
     walk.start(bars->range);
@@ -461,66 +715,22 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
     // lane's row of four, plus 4 i: the lanes of the upper columns take the
     // neighbour's row, whose swizzle puts their stores on the other banks
     const int row_in = (lane >> 3) ^ (c >> 2);
-    uint32_t tile_v = 0;       // descale slot of the next V
     for (int piece = 0; ok && walk.next(p, x.w); ++piece) {
         x.set(p);
-        int fexp = -100;
-        const int ahead = x.pair ? 1 : 2;
-        for (int jk = 0, jv = 0; jv < x.n && ok;) {
-            const bool is_v = jk >= x.n || jk >= jv + ahead;
-            const int j = is_v ? jv++ : jk++;
-            if (!is_v) {
-                // ---- the tile's descales: K's of this warp's keys, V's (of all: F)
-                const uint32_t slot = tiles % kDs;
-                ok = warp_wait(&bars->k_full[kslot], kround, abort_flag);
-                if (ok && tiles >= kDs) ok = warp_wait(&bars->ds_empty[slot], tiles / kDs - 1u, abort_flag);
-                if (!ok) break;
-                const float* raw_ds = reinterpret_cast<const float*>(smem + C::kDescale + kslot * 1024);
-                const float* kd = raw_ds + 64 * wc;
-                const int key0 = (x.w.k0 + j) * kTcKeys + lane;
-                float vd[4], top = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    vd[i] = raw_ds[128 + 32 * i + lane];
-                    const int key = key0 + 32 * i;
-                    // past the sequence, or a row that is added apart
-                    if (key >= x.w.keys || (key >= x.prefix && !isfinite(vd[i]))) vd[i] = 0.f;
-                    top = fmaxf(top, fabsf(vd[i]));
-                }
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-                fexp = max(fexp, min((int)(__float_as_uint(top) >> 23) - 126, 111));
-                const float fr = tc_pow2(-fexp);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    bars->kf[slot][64 * wc + 32 * i + lane] = kd[32 * i + lane];
-                    bars->wv[slot][64 * wc + 32 * i + lane] = (wc == 0 ? vd[i] : vd[2 + i]) * fr;
-                }
-                if (wc == 0 && lane == 0) bars->fexp[slot] = fexp;
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&bars->ds_full[slot]));
-                    mbar_arrive(smem_u32(&bars->k_empty[kslot]));
-                }
-                ++tiles;
-                if (++kslot == C::kKStages) {
-                    kslot = 0;
-                    ++kround;
-                }
-                continue;
-            }
-            // ---- the codes
-            ok = warp_wait(&bars->v_full[raw_slot], raw_round, abort_flag);
+        for (int j = 0; j < x.n; ++j) {
+            const uint32_t ds = tiles % kDs;
+            ok = warp_wait(&bars->ds_full[ds], tiles / kDs, abort_flag) &&
+                 warp_wait(&bars->v_full[raw_slot], raw_round, abort_flag);
             if (ok && out_round > 0) ok = warp_wait(&bars->empty[out_slot], out_round - 1u, abort_flag);
             if (!ok) break;
             const uint32_t raw = smem_u32(smem + C::kV + raw_slot * C::kCodes);
             const uint32_t out = smem_u32(smem + C::kRing + out_slot * C::kTile) + (c >> 2) * 16384;
             if (x.special(j)) {
                 // rows that must not enter the product become zeros where they lie
-                uint32_t marks[2] = {0u, 0u};
+                uint32_t marks = 0u;
 #pragma unroll 1
-                for (int i = 0; i < 16; ++i) {
-                    const int row = 64 * wc + (lane >> 3) + 4 * i;
+                for (int i = 0; i < kRows / 4; ++i) {
+                    const int row = kRows * wc + (lane >> 3) + 4 * i;
                     const int key = (x.w.k0 + j) * kTcKeys + row;
                     const uint32_t piece_at = raw + row * 128 + ((c ^ (row & 7)) << 4);
                     bool hit = false;
@@ -529,7 +739,7 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
                         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int e = 0; e < 16; ++e) hit |= ((u[e >> 2] >> (8 * (e & 3))) & 0x7Fu) == 0x7Fu;
-                        if (c == 0) {  // (a path for the last tiles of a sequence)
+                        if (c == 0) {
                             int off;
                             const int page = tree_page(p, x.w.b, key, x.w.keys, off);
                             if (page >= 0)
@@ -537,27 +747,27 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
                         }
                     }
                     const unsigned votes = __ballot_sync(0xFFFFFFFFu, hit);
-                    uint32_t m = 0u;
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
-                        if ((votes >> (8 * g)) & 0xFFu) m |= 1u << g;
-                    if (i < 8) marks[0] |= m << (4 * i);
-                    else marks[1] |= m << (4 * i - 32);
+                        if ((votes >> (8 * g)) & 0xFFu) marks |= 1u << (4 * (i & 7) + g);
                     if (key >= x.w.keys || ((votes >> (lane & 24)) & 0xFFu)) sts128(piece_at, 0u, 0u, 0u, 0u);
+                    if ((i & 7) == 7) {
+                        if (lane == 0) bars->bad[piece % kBadBufs][j - x.first_special()][kRows / 32 * wc + (i >> 3)] = marks;
+                        marks = 0u;
+                    }
                 }
-                if (lane < 2) bars->bad[piece % kBadBufs][j - x.first_special()][2 * wc + lane] = lane ? marks[1] : marks[0];
                 __syncwarp();  // (other lanes read the rows below)
             }
             // this lane's rows: row0 + 4 i; row & 7 = row_in + 4 (i & 1), so the
             // swizzle has two patterns
-            const int row0 = 64 * wc + row_in;
+            const int row0 = kRows * wc + row_in;
             const uint32_t src[2] = {raw + row0 * 128 + ((c ^ row_in) << 4), raw + row0 * 128 + ((c ^ row_in ^ 4) << 4)};
             const int ch = 2 * (c & 3);
             const uint32_t dst[2] = {out + row0 * 128 + ((ch ^ row_in) << 4), out + row0 * 128 + ((ch ^ row_in ^ 4) << 4)};
             const uint32_t odd = 16 - ((row_in & 1) << 5);  // from an even chunk to its odd neighbour
-            const float* fv = &bars->wv[tile_v % kDs][row0];
+            const float* fv = &bars->wv[ds][row0];
 #pragma unroll 1
-            for (int i0 = 0; i0 < 16; i0 += 4) {
+            for (int i0 = 0; i0 < kRows / 4; i0 += 4) {
                 uint4 w[4];
                 float d[4];
 #pragma unroll
@@ -583,8 +793,9 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
             if (lane == 0) {
                 mbar_arrive(smem_u32(&bars->full[out_slot]));
                 mbar_arrive(smem_u32(&bars->v_empty[raw_slot]));
+                mbar_arrive(smem_u32(&bars->ds_empty[ds]));
             }
-            ++tile_v;
+            ++tiles;
             if (++raw_slot == C::kVStages) {
                 raw_slot = 0;
                 ++raw_round;
@@ -923,16 +1134,16 @@ __device__ __noinline__ void tc_write_slow(const TreeParams& p, TcPiece x, TcOut
     tc_write<D, F8, true>(p, x, o, tA, col0, col1, bad);
 }
 
-template <int D, bool F8>
+template <int D, bool F8, bool ONE>
 __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars, uint32_t tmem, const TreeParams& p) {
-    using C = TcCfg<D, F8>;
+    using C = TcCfg<D, F8, ONE>;
     const volatile int* abort_flag = &bars->abort;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const uint32_t tS = tmem + t * 128 + lanes;
     const uint32_t tO = tmem + 256 + lanes;  // of stream 0; stream 1: + 128
     const int ncols = (p.dh + 15) / 16 * 16;
     const int me = wq * 32 + lane;
-    uint32_t cnt_s = 0, cnt_o = 0, cnt_x = 0, tiles = 0;
+    uint32_t cnt_s = 0, cnt_x = 0, tiles = 0;
     bool ok = true;
     TreeWalk walk;
     walk.start(bars->range);
@@ -965,6 +1176,8 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
         int s = 0;
         for (; x.has(s, t) && ok; ++s) {
             const int j = x.tile(s, t);
+            // (descales are laid out in order, and this stream, or with `done` both, has used
+            // those of the tile before: the place's last phase is over)
             const float* kf = nullptr;
             int fexp = 0;
             if constexpr (F8) {
@@ -1012,11 +1225,9 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
         }
         if (!ok) break;
         tiles += (uint32_t)x.n;
-        if (s > 0) {
-            ok = warp_wait(&bars->o_full[t], cnt_o++, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-        }
+        ok = warp_wait(&bars->o_full[t], (uint32_t)piece, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
         // ---- epilogue
         float inv0, inv1 = 0.f, m = st.m, lx = st.lx, inv_l;  // factors of stream 0's and 1's O
         int col0 = 0, col1 = ncols;
@@ -1087,11 +1298,13 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
     if (!ok && lane == 0) tc_abort(bars, p.err);
 }
 
-template <int D, bool F8>
-__global__ void __launch_bounds__(kTcThreads, 1)
+template <int D, bool F8, bool ONE>
+__global__ void __launch_bounds__((TcRoles<F8, ONE>::kThreads), 1)
 attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                     const __grid_constant__ TreeParams p) {
-    using C = TcCfg<D, F8>;
+    using C = TcCfg<D, F8, ONE>;
+    using Roles = TcRoles<F8, ONE>;
+    constexpr int kIssuers = ONE ? 2 : 1;
     extern __shared__ __align__(1024) uint8_t smem[];
     TcBars* bars = reinterpret_cast<TcBars*>(smem + C::kBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1111,24 +1324,26 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
             mbar_init(smem_u32(&bars->o_full[t]), 1);
         }
         for (int i = 0; i < 8; ++i) {
-            mbar_init(smem_u32(&bars->full[i]), F8 ? kTcHelpers : 1);
-            mbar_init(smem_u32(&bars->empty[i]), 1);
+            mbar_init(smem_u32(&bars->full[i]), F8 ? Roles::kConverters : 1);
+            mbar_init(smem_u32(&bars->empty[i]), kIssuers);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(smem_u32(&bars->k_full[i]), 1);
-            mbar_init(smem_u32(&bars->k_empty[i]), kTcHelpers + 1);  // (and the product's commit)
+            mbar_init(smem_u32(&bars->k_empty[i]), kIssuers + 1);  // (and the descales)
             mbar_init(smem_u32(&bars->v_full[i]), 1);
-            mbar_init(smem_u32(&bars->v_empty[i]), kTcHelpers);
+            mbar_init(smem_u32(&bars->v_empty[i]), Roles::kConverters);
         }
         for (int i = 0; i < kDs; ++i) {
-            mbar_init(smem_u32(&bars->ds_full[i]), kTcHelpers);
-            mbar_init(smem_u32(&bars->ds_empty[i]), 8);
+            mbar_init(smem_u32(&bars->ds_full[i]), 1);
+            mbar_init(smem_u32(&bars->ds_empty[i]), 8 + Roles::kConverters);
         }
-        mbar_init(smem_u32(&bars->fix_ask), 1);
-        mbar_init(smem_u32(&bars->fix_done), kTcHelpers);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&bars->fix_ask[t]), 1);
+            mbar_init(smem_u32(&bars->fix_done[t]), 1);
+            mbar_init(smem_u32(&bars->drain[t]), 1);
+        }
         mbar_init(smem_u32(&bars->stat), 8);
         mbar_init(smem_u32(&bars->done), 8);
-        mbar_init(smem_u32(&bars->drain), 1);
         bars->abort = 0;
         fence_barrier_init();
     }
@@ -1144,20 +1359,26 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
-    if (warp < 4) {
-        reg_dealloc<kTcRegsControl>();
-        if (warp == 0) {
-            tc_produce<D, F8>(&tk, &tv, smem, bars, p);
-        } else if (warp == 1) {
-            tc_mma<D, F8>(smem, bars, tmem, p);
-        } else if constexpr (F8) {
-            tc_convert<D>(warp - 2, smem, bars, p);
+    if (warp < Roles::kControl) {
+        reg_dealloc<Roles::kRegsControl>();
+        constexpr int kFirstConverter = Roles::kControl - Roles::kConverters;
+        if (warp == 1 || (ONE && warp == 2)) {
+            if constexpr (ONE) tc_mma_stream<D, F8, ONE>(warp - 1, smem, bars, tmem, p);
+            else tc_mma<D, F8, ONE>(smem, bars, tmem, p);
+        } else if constexpr (Roles::kMany) {
+            if (warp == 0) tc_produce_codes<false, C>(&tk, smem, bars, p);
+            if (warp == 3) tc_produce_codes<true, C>(&tv, smem, bars, p);
         } else {
-            tc_fix<D>(warp - 2, smem, bars, p);
+            if (warp == 0) tc_produce<D, F8, ONE>(&tk, &tv, smem, bars, p);
+        }
+        if constexpr (F8) {
+            if (warp >= kFirstConverter) tc_convert<Roles::kConverters, C>(warp - kFirstConverter, smem, bars, p);
+        } else {
+            if (warp == 3) tc_fix<D, ONE>(smem, bars, p);
         }
     } else {
-        reg_alloc<kTcRegsSoftmax>();
-        tc_softmax<D, F8>((warp - 4) >> 2, warp & 3, lane, smem, bars, tmem, p);
+        reg_alloc<Roles::kRegsSoftmax>();
+        tc_softmax<D, F8, ONE>((warp - Roles::kControl) >> 2, warp & 3, lane, smem, bars, tmem, p);
     }
     tc_fence_before();
     __syncthreads();
@@ -1168,18 +1389,18 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     }
 }
 
-template <int D, bool F8>
+template <int D, bool F8, bool ONE>
 attn_status_t launch_tc_t(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream,
                           const DeviceInfo& dev) {
-    using C = TcCfg<D, F8>;
+    using C = TcCfg<D, F8, ONE>;
     static int attr_set[64] = {0};
     if (dev.device >= 64 || !attr_set[dev.device]) {
-        if (cudaFuncSetAttribute(attn_tree_tc_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(attn_tree_tc_kernel<D, F8, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::kSmem) != cudaSuccess)
             return ATTN_ERR_CUDA;
         if (dev.device < 64) attr_set[dev.device] = 1;
     }
-    attn_tree_tc_kernel<D, F8><<<p.ctas, kTcThreads, C::kSmem, stream>>>(tk, tv, p);
+    attn_tree_tc_kernel<D, F8, ONE><<<p.ctas, TcRoles<F8, ONE>::kThreads, C::kSmem, stream>>>(tk, tv, p);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -1197,8 +1418,14 @@ void tree_tc_shape(TreeParams& p, bool f8, int num_sms) {
 
 attn_status_t launch_tree_tc(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, bool f8,
                              cudaStream_t stream, const DeviceInfo& dev) {
-    if (f8) return launch_tc_t<128, true>(tk, tv, p, stream, dev);
-    return p.dw == 64 ? launch_tc_t<64, false>(tk, tv, p, stream, dev) : launch_tc_t<128, false>(tk, tv, p, stream, dev);
+    if (p.T * p.G <= 128) {
+        if (f8) return launch_tc_t<128, true, true>(tk, tv, p, stream, dev);
+        if (p.dw == 128) return launch_tc_t<128, false, true>(tk, tv, p, stream, dev);
+        return launch_tc_t<64, false, true>(tk, tv, p, stream, dev);
+    }
+    if (f8) return launch_tc_t<128, true, false>(tk, tv, p, stream, dev);
+    if (p.dw == 128) return launch_tc_t<128, false, false>(tk, tv, p, stream, dev);
+    return launch_tc_t<64, false, false>(tk, tv, p, stream, dev);
 }
 
 }  // namespace gb300
