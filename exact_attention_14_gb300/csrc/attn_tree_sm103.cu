@@ -9,12 +9,17 @@
 // O = sum_j p_j vd_j vc_j / sum_j p_j, the codes exact in fp16.
 //
 // This file: the kernel for up to 16 query rows at a time on mma.sync
-// (m16n8k16; more rows of head dims up to 128 go to attn_tree_tc_sm103.cu), and
+// (m16n8k16; tree_on_tc says which calls go to attn_tree_tc_sm103.cu), and
 // the merge of cut items (tree_plan.h has the work list).  A producer warp
 // streams 64-key tiles of K and V (and their descales) by TMA into a ring; two
 // pairs of consumer warps take the tiles in turn, 32 keys a warp, each with its
 // own online softmax (base 2), and the four are merged through shared memory at
 // the end of a piece.  Bound: HBM (each cached byte is read once per row tile).
+// One token, 16 sequences of 1024..32768 keys: bf16, d = 128, 8 heads 6368 GB/s;
+// E4M3, d = 128, 8 heads 5251 GB/s (104 us with the merge, 570 MB), where the codes'
+// conversion (cvt, 64 lanes a clock and SM) and the MMAs take about as long as the
+// copies; E4M3, d = 256, 4 heads 5560 GB/s.  (32 keys a warp: 16 were 128 -> 110 us
+// slower in E4M3, every shuffle and wait being paid twice as often.)
 //
 // The products are transposed, S^T = K Q^T and O^T = V^T P^T: keys and columns
 // are the 16 rows of an MMA and the query rows its 8 columns, so up to 8 query
@@ -47,7 +52,9 @@ constexpr int kConsumers = 4;
 constexpr int kTreeThreads = (kConsumers + 1) * 32;
 constexpr int kTileKeys = 64;
 constexpr int kMaxRows = 16;
-constexpr int kExtraUnits = 2;  // an item's start and end, in 64-key tiles
+// An item's start and end, in 64-key tiles (16 drafts 188 us either way, 1 token over
+// 16 short and long sequences 110 against 109 with 0: it matters where items are many).
+constexpr int kExtraUnits = 2;
 constexpr float kLn2t = 0.69314718055994530942f;
 constexpr float kLog2et = 1.44269504088896340736f;
 constexpr float kPFrame = 32768.0f;  // E4M3: P is held times 2^15 / F
@@ -934,11 +941,17 @@ attn_status_t launch_tree_merge(const TreeParams& p, int num_sms, cudaStream_t s
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// Whether a call runs on the tensor-core kernel of attn_tree_tc_sm103.cu.
-static bool tree_on_tc(int d, int rows) { return d <= 128 && rows > kMaxRows; }
+// Whether a call runs on the tensor-core kernel of attn_tree_tc_sm103.cu, whose tile
+// of 128 rows costs the same however few are live.  16 sequences of up to 32768 keys,
+// 8 KV heads, this kernel / that one in us: bf16, d = 128, 8 rows 173 / 180, 12 rows
+// 196 / 182, 16 rows 200 / 182, 20 rows 354 (two row tiles) / 186; bf16, d = 64, 16
+// rows 109 / 129; E4M3, d = 128, 16 rows 145 / 195, 20 rows 262 / 196.
+static bool tree_on_tc(int d, bool f8, int rows) {
+    return d <= 128 && rows > (f8 || d <= 64 ? kMaxRows : kMaxRows / 2);
+}
 
 static void tree_shape(TreeParams& p, int rows, bool f8, int num_sms) {
-    if (tree_on_tc(p.dh, rows)) {
+    if (tree_on_tc(p.dh, f8, rows)) {
         tree_tc_shape(p, f8, num_sms);
         return;
     }
@@ -1008,7 +1021,7 @@ attn_status_t launch_decode_tree(const void* q, const void* k_pages, const void*
     attn_status_t st;
     if ((st = encode_tmap_pages(&tk, k_pages, f8, d, Hkv, page_size, num_blocks, p.box_keys)) != ATTN_OK) return st;
     if ((st = encode_tmap_pages(&tv, v_pages, f8, d, Hkv, page_size, num_blocks, p.box_keys)) != ATTN_OK) return st;
-    if (tree_on_tc(d, rows_kv)) st = launch_tree_tc(tk, tv, p, f8, stream, dev);
+    if (tree_on_tc(d, f8, rows_kv)) st = launch_tree_tc(tk, tv, p, f8, stream, dev);
     else
         st = tree_variant(d, f8, rows_kv, [&](auto D, auto F8, auto NT) {
             return launch_tree_t<decltype(D)::value, decltype(F8)::value, decltype(NT)::value>(tk, tv, p, stream, dev);

@@ -10,14 +10,20 @@
 //                          K and V tile;
 //   rows <= 128 ("split"): both hold the same rows, stream t takes every second
 //                          key tile, and the two are merged at the end.
-// Roles: warp 0 TMA producer (K and V tiles in the order the products want
-// them), warp 1 MMA issuer, warps 4-7 and 8-11 softmax of stream 0 and 1 (a
-// thread per row; they also lay Q out in shared memory, whose rows are not
-// evenly spaced in a [B, Hq, T, d] tensor).  bf16 caches: warps 2-3 prepare V
-// in the tiles that hold drafted tokens or the end of the sequence.  E4M3
-// caches: the same two convert every tile from codes to fp16 and prepare V and
-// the descales as they go; Q (scaled by a power of two per row) and K are exact
-// fp16 operands, P and V (with its descale) rounded ones.
+// Roles (TcRoles): a TMA producer, an MMA issuer, two warpgroups of softmax (one a
+// stream, a thread per row; they also lay Q out in shared memory, whose rows are not
+// evenly spaced in a [B, Hq, T, d] tensor), and
+//   bf16: a warp that prepares V in the tiles that hold drafted tokens or the end
+//   of the sequence;
+//   E4M3: warps that convert V's codes to fp16, times descale over F; the producer
+//   lays the descales out.  K's codes and Q, as the sum of two E4M3 terms, go into
+//   an 8-bit product as they are, so K is never converted.
+// Calls of up to 128 rows (ONE) have an issuer for each stream, and in E4M3 a second
+// producer and two more converters.
+//
+// A softmax warp takes 64 keys of S at a time (128 in registers at once spill: E4M3
+// 368 -> 306 us), and the product of a half with V is issued while it works on the
+// other: what stays between two tiles of a stream is half a product with V and S's.
 //
 // Masked places: see attn_tree_sm103.cu.  Here V rows past the sequence, and
 // drafted tokens' V rows with a NaN or an infinity, are zeroed before the
@@ -25,9 +31,13 @@
 // see them, with scores computed anew (a slow path that ordinary data never
 // takes).
 //
-// Bound: HBM up to about 128 rows (2 * 128 rows * 128 keys * 128 columns * 2
-// products take 1075 cycles of an SM's tensor cores, reading the 64 KiB tile
-// 2785 cycles of its share of HBM), the tensor cores and the exponentials above.
+// Bound: HBM up to about 128 rows, then the tensor cores and the softmax.  256 rows
+// by a 128-key tile: the four products take 2150 cycles of an SM's tensor cores, the
+// tile (64 KiB in bf16) 2785 cycles of its share of HBM; measured, 16 sequences of
+// 1024..32768 keys, 8 KV heads: bf16 about 3500 cycles (64 drafts, 4 heads a group,
+// 245 us with the merge, 67% of the floor), E4M3 4600 (300 us), where S's
+// multiplication with the descales (40 us) and fp16 packing lengthen the softmax.
+// 64 rows, bf16: 183 us, 90% of HBM's rate; E4M3 196 us.
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -1412,7 +1422,7 @@ void tree_tc_shape(TreeParams& p, bool f8, int num_sms) {
     p.dw = p.dh <= 64 && !f8 ? 64 : 128;
     p.ctas = num_sms;
     p.min_units = 2;
-    p.extra = 6;
+    p.extra = 6;  // Q's layout, the first copies, O's way out (64 drafts 248 us, with none 308; 16 drafts 188 / 217)
     p.group_rows = 32;
 }
 
