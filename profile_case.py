@@ -7,6 +7,9 @@ profiler captures (ncu) of a single launch configuration.
     python profile_case.py --kernel fp8 --workload long
     python profile_case.py --kernel fp8quant --workload long
     python profile_case.py --kernel varlen
+    python profile_case.py --kernel rope
+    python profile_case.py --kernel cache --cache e4m3
+    python profile_case.py --kernel tree --tokens 64 --cache e4m3
 
 Workloads: prefill (B=4 H=16 N=2048 d=128), prefill2x (B=8: inputs larger
 than L2), prefill256 (the prefill shape at d=256), long (B=1 H=32 N=16384), gqa (B=8 Hq=32 Hkv=8 N=4096), decode
@@ -16,7 +19,10 @@ L2, for multi-pass captures), decode256 (d = 256: B=16 Hq=32 Hkv=8 Nmax=16384,
 lengths 512..16384); varlen is the packed causal prefill batch (16
 sequences of 256..4096 tokens).  fp8 runs attn_fwd_fp8 on E4M3 operands of the
 workload (Q and K rotated by the random-sign Hadamard matrix), fp8quant the
-rotating quantization of its Q.  Inputs come from the seeded generators.
+rotating quantization of its Q.  rope turns Q and K of 8 x 4096 tokens (32 and 8
+heads of 128).  cache writes keys and values of 16 sequences of 256..8192 keys (8
+heads of 128) into 64-key pages and reads them back; tree attends them from --tokens
+drafted tokens a sequence with 32 query heads.  Inputs come from seeded generators.
 """
 from __future__ import annotations
 
@@ -39,13 +45,42 @@ FWD = {
 }
 
 
+def paged(args, dev):
+    """The cache's write and read, or the tree attention over it."""
+    g, gd = torch.Generator().manual_seed(9), torch.Generator(device=dev).manual_seed(9)
+    H, d, page, width = 8, 128, 64, 128
+    lens = torch.randint(256, 8193, (16,), generator=g)
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    table = torch.randperm(16 * width, generator=g).reshape(16, width)
+    slots = torch.cat([table[b, torch.arange(n) // page] * page + torch.arange(n) % page
+                       for b, n in enumerate(lens.tolist())]).to(dev)
+    total = int(cu[-1])
+    k, v = (torch.randn(total, H, d, device=dev, generator=gd).to(torch.bfloat16) for _ in range(2))
+    e4m3 = args.cache == "e4m3"
+    pages = [torch.zeros(16 * width, page, H, d, device=dev, dtype=torch.uint8 if e4m3 else torch.bfloat16)
+             for _ in range(2)]
+    descale = [torch.zeros(16 * width, H, page, device=dev) if e4m3 else None for _ in range(2)]
+    table, cu = table.to(dev, torch.int32), cu.to(dev, torch.int32)
+    ea.attn_cache_write(k, v, *pages, slots, *descale)
+    if args.kernel == "tree":
+        q = torch.randn(16, 32, args.tokens, d, device=dev, generator=gd).to(torch.bfloat16)
+        for _ in range(args.iters):
+            ea.decode_tree(q, *pages, table, lens.to(dev, torch.int32), None, None, *descale)
+        return
+    for _ in range(args.iters):
+        ea.attn_cache_write(k, v, *pages, slots, *descale)
+        ea.cache_read(*pages, table, cu, total, *descale)
+
+
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("--kernel", choices=["fwd", "decode", "bwd", "fp8", "fp8quant", "varlen"],
-                    required=True)
+    ap.add_argument("--kernel", choices=["fwd", "decode", "bwd", "fp8", "fp8quant", "varlen", "rope", "cache",
+                                             "tree"], required=True)
     ap.add_argument("--workload", default="prefill")
     ap.add_argument("--causal", type=int, default=-1, help="-1: the workload's first mode")
     ap.add_argument("--iters", type=int, default=3)
+    ap.add_argument("--cache", choices=["bf16", "e4m3"], default="bf16", help="cache, tree")
+    ap.add_argument("--tokens", type=int, default=1, help="tree: drafted tokens of a sequence")
     args = ap.parse_args()
     dev = torch.device("cuda", 0)
     if args.kernel in ("fp8", "fp8quant"):
@@ -65,6 +100,15 @@ def main():
                                 scale=cfg.scale, rotated=True)
             else:
                 ea.attn_fp8_quantize(q, q8, qd, signs)
+    elif args.kernel == "rope":
+        g = torch.Generator(device=dev).manual_seed(8)
+        qkv = torch.randn(8, 4096, 40, 128, device=dev, generator=g).to(torch.bfloat16)
+        pos = torch.arange(4096, device=dev, dtype=torch.int32)
+        f, mag = ea.rope_frequencies(128)
+        for _ in range(args.iters):
+            ea.rope(qkv[:, :, :32].transpose(1, 2), qkv[:, :, 32:].transpose(1, 2), pos, f, magnitude=mag)
+    elif args.kernel in ("cache", "tree"):
+        paged(args, dev)
     elif args.kernel == "varlen":
         lens = varlen_lengths(VARLEN.n_seqs, VARLEN.len_lo, VARLEN.len_hi, VARLEN.seed)
         q, k, v, cq, ck = (t.to(dev) for t in make_varlen_inputs(lens, lens, VARLEN.Hq, VARLEN.Hkv,
