@@ -1422,7 +1422,7 @@ void tree_tc_shape(TreeParams& p, bool f8, int num_sms) {
     p.dw = p.dh <= 64 && !f8 ? 64 : 128;
     p.ctas = num_sms;
     p.min_units = 2;
-    p.extra = 6;  // Q's layout, the first copies, O's way out (64 drafts 248 us, with none 308; 16 drafts 188 / 217)
+    p.extra = 6;  // Q's layout, the first copies, O's way out (64 drafts: 245 us; 0: 308, 4: 250, 8: 247, 10: 250)
     p.group_rows = 32;
 }
 
