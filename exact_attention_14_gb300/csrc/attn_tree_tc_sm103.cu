@@ -490,7 +490,7 @@ __device__ void tc_mma(uint8_t* smem, TcBars* bars, uint32_t tmem, const TreePar
             if (h == 0 && (!pair || t == 0)) {
                 slot_v[t] = take();
                 if (!F8 && ok && x.special(x.tile(s, t))) {
-                    // the fixers work on it while this stream's softmax still runs
+                    // the fixer works on it while this stream's softmax still runs
                     if (elect_one()) mbar_arrive(smem_u32(&bars->fix_ask[t]));
                     __syncwarp();
                     ok = warp_wait(&bars->fix_done[t], cnt_fix[t]++, abort_flag);

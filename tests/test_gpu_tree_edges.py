@@ -245,3 +245,31 @@ def test_mask_bits_past_the_drafts_count_for_nothing(G, T, e4m3):
     assert ea.attn_last_device_error() == 0
     ref = tree64(q, cache, torch.ones(3, T, T, dtype=torch.bool), q_lens)
     check_tree(o.cpu(), lse.cpu(), ref, e4m3, torch.float32)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("G,T", [(2, 3), (2, 24), (4, 60)])
+def test_bad_lengths_leave_the_other_sequences(G, T, e4m3):
+    """Lengths past the table, drafts past T or past the keys, negative ones: zeros and an error,
+    in each kernel, with the sequences between them as ever."""
+    lengths = [T + 50, T + 9, 2 * T, T + 300, T + 1]
+    cache = Cache(lengths, 2, 128, 16, e4m3, seed=34)
+    q = _q(5, 2 * G, T, 128)
+    ref = tree64(q, cache)
+    a = _args(q, cache, None, [T] * 5)
+    a[4][0] = a[3].shape[1] * 16 + 1
+    a[6][2] = T + 1
+    a[4][4] = -3
+    o, lse = ea.decode_tree(*a, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert ea.attn_last_device_error() == ea.ATTN_ERR_INVALID_ARG
+    for b in (0, 2, 4):
+        assert (o[b] == 0).all() and (lse[b] == -float("inf")).all()
+    for b in (1, 3):
+        check_tree(o[b:b + 1].cpu(), lse[b:b + 1].cpu(), [x[b:b + 1] for x in ref], e4m3, torch.float32)
+    a[4].copy_(torch.tensor(lengths, dtype=torch.int32))
+    a[6].fill_(T)
+    o, lse = ea.decode_tree(*a, out_dtype=torch.float32)           # and the next call is whole again
+    torch.cuda.synchronize()
+    assert ea.attn_last_device_error() == 0
+    check_tree(o.cpu(), lse.cpu(), ref, e4m3, torch.float32)
