@@ -910,7 +910,7 @@ auto tree_variant(int d, bool f8, int rows, F f) {
     integral_constant<bool, false> no;
     if (f8) return d <= 128 ? with_rows(integral_constant<int, 128>(), yes) : with_rows(integral_constant<int, 256>(), yes);
     if (d <= 64) return with_rows(integral_constant<int, 64>(), no);
-    if (d <= 128) return with_rows(integral_constant<int, 128>(), no);
+    if (d <= 128) return f(integral_constant<int, 128>(), no, integral_constant<int, 1>());  // (more rows: tree_on_tc)
     return with_rows(integral_constant<int, 256>(), no);
 }
 
