@@ -615,7 +615,7 @@ attn_status_t attn_rope_frequencies(int rotary_dim, double base, attn_rope_scali
             return rotary_dim * std::log(original_len / (turns * 6.283185307179586)) / (2.0 * std::log(base));
         };
         lo = std::max(std::floor(pair_of(beta_fast)), 0.0);
-        hi = std::min(std::ceil(pair_of(beta_slow)), (double)(n - 1));
+        hi = std::min(std::ceil(pair_of(beta_slow)), (double)(rotary_dim - 1));  // (may lie past the last pair)
     }
     for (int i = 0; i < n; ++i) {
         double f = std::pow(base, -2.0 * i / rotary_dim);

@@ -439,8 +439,13 @@ typedef enum {
  *   ATTN_ROPE_BY_PARTS: pairs that turn at least beta_fast times over
  *               original_len positions keep f_i, those that turn at most
  *               beta_slow times get f_i / factor, linear in the pair's index in
- *               between (the ends rounded outwards to whole pairs); magnitude =
- *               0.1 ln(factor) + 1 (1 for the others)
+ *               between: with p(t) = rotary_dim ln(original_len / (2 pi t)) /
+ *               (2 ln(base)), the (fractional) pair that turns t times, the ramp
+ *               goes from a = max(floor(p(beta_fast)), 0) to z =
+ *               min(ceil(p(beta_slow)), rotary_dim - 1), pair i is at r =
+ *               min(max((i - a) / max(z - a, 0.001), 0), 1) of it and gets (1 - r)
+ *               f_i + r f_i / factor.  z may lie past the last pair: then none is
+ *               divided in full.  magnitude = 0.1 ln(factor) + 1 (1 for the others)
  */
 attn_status_t attn_rope_frequencies(int rotary_dim, double base, attn_rope_scaling_t scaling,
                                     double factor, int original_len, double beta_fast,
