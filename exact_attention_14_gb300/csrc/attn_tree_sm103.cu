@@ -366,7 +366,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 l[nt][r] = 0.f;   // this lane's part of the sum that normalises O
                 xs[nt][r] = 0.f;  // ... of the unrounded P (the LSE's)
             }
-        int fexp = -126;  // E4M3: F = 2^fexp
+        int fexp = -100;  // E4M3: F = 2^fexp (above 2^-111: 2^15 / F is finite where no key counts)
 
         for (int kt = w.k0; kt < w.k1; ++kt, ++used) {
             if ((int)(used & 1) != pair) continue;  // the other pair's tile
@@ -658,7 +658,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     bars->x[warp][row] = xs[nt][r];
                 }
             }
-        if (lane == 0) bars->f[warp] = F8 ? pow2i(max(fexp, -120)) / kPFrame : 1.f;
+        if (lane == 0) bars->f[warp] = F8 ? pow2i(fexp) / kPFrame : 1.f;
         tree_consumers_sync();
         // this warp's O in the common frame and over the common sum
 #pragma unroll
