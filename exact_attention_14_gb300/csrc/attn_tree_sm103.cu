@@ -57,7 +57,7 @@ constexpr int kMaxRows = 16;
 constexpr int kExtraUnits = 2;
 constexpr float kLn2t = 0.69314718055994530942f;
 constexpr float kLog2et = 1.44269504088896340736f;
-constexpr float kPFrame = 32768.0f;  // E4M3: P is held times 2^15 / F
+constexpr int kPFrame = 15;  // E4M3: P is held times 2^15 / F
 
 // D columns, NT tiles of 8 query rows.
 template <int D, bool F8, int NT>
@@ -162,7 +162,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-// Power of two 2^e (e in [-126, 127]).
+// Power of two 2^e (e in [-126, 127]; 128: infinite).
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // Byte offset of 16-byte chunk `ch` (counted over the whole row) of key row
@@ -366,7 +366,9 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 l[nt][r] = 0.f;   // this lane's part of the sum that normalises O
                 xs[nt][r] = 0.f;  // ... of the unrounded P (the LSE's)
             }
-        int fexp = -100;  // E4M3: F = 2^fexp (above 2^-111: 2^15 / F is finite where no key counts)
+        // E4M3: F = 2^fexp, 2^-100 (2^15 / F is finite where no key counts) to 2^128 (above every
+        // finite descale); it is used together with 2^15 alone, so that each factor is in range
+        int fexp = -100;
 
         for (int kt = w.k0; kt < w.k1; ++kt, ++used) {
             if ((int)(used & 1) != pair) continue;  // the other pair's tile
@@ -484,7 +486,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                         moved |= x > m[nt][r];
                     }
                 if constexpr (F8) {
-                    const float f = pow2i(fexp);
+                    const float f = pow2i(fexp);  // (2^128: infinite, above every finite descale)
                     moved |= fmaxf(fmaxf(fabsf(wv[0]), fabsf(wv[1])), fmaxf(fabsf(wv[2]), fabsf(wv[3]))) > f;
                 }
                 if (__any_sync(0xFFFFFFFFu, moved)) {
@@ -494,7 +496,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
                         // 2^need > top (the same in every lane)
-                        const int need = max(min((int)(__float_as_uint(top) >> 23) - 126, 111), -100);
+                        const int need = max(min((int)(__float_as_uint(top) >> 23) - 126, 128), -100);
                         if (need > fexp) {
                             grow = fexp - need < -126 ? 0.f : pow2i(fexp - need);
                             fexp = need;
@@ -519,7 +521,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 }
                 // ---- P^T
                 if constexpr (F8) {
-                    const float fr = kPFrame * pow2i(-fexp);
+                    const float fr = pow2i(kPFrame - fexp);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) wv[i] *= fr;
                 }
@@ -562,7 +564,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                                 pk[nt][r] = sv == -INFINITY ? -1.f : ex2(sv - (m[nt][r] == -INFINITY ? 0.f : m[nt][r]));
                             }
                         float fr = 1.f;
-                        if constexpr (F8) fr = lds32f(sD + (kTileKeys + wk0 + kk) * 4) * kPFrame * pow2i(-fexp);
+                        if constexpr (F8) fr = lds32f(sD + (kTileKeys + wk0 + kk) * 4) * pow2i(kPFrame - fexp);
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -658,7 +660,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     bars->x[warp][row] = xs[nt][r];
                 }
             }
-        if (lane == 0) bars->f[warp] = F8 ? pow2i(fexp) / kPFrame : 1.f;
+        if (lane == 0) bars->f[warp] = F8 ? pow2i(fexp - kPFrame) : 1.f;
         tree_consumers_sync();
         // this warp's O in the common frame and over the common sum
 #pragma unroll
@@ -842,13 +844,16 @@ attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
     if (cut)
         for (int i = 0; i < pieces; ++i) M = fmaxf(M, s_w[i * gr + row]);
     const float Ms = M == -INFINITY ? 0.f : M;
+    // weights times 2^-shift, a sum of at most 1: pieces near fp32's largest value do not overflow
+    const int shift = pieces > 1 ? 32 - __clz(pieces - 1) : 0;
+    const float down = pow2i(-shift);
 #pragma unroll
     for (int k = 0; k < CPT; ++k) acc[k] = 0.f;
     for (int i0 = 0; i0 < pieces; i0 += kPieces) {
         if (i0 > 0) load(i0);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const float wt = cut && i0 + i < pieces ? ex2(s_w[(i0 + i) * gr + row] - Ms) : 0.f;
+            const float wt = cut && i0 + i < pieces ? ex2(s_w[(i0 + i) * gr + row] - Ms) * down : 0.f;
             sum += wt;
 #pragma unroll
             for (int k = 0; k < CPT; ++k) acc[k] = fmaf(wt, v[i][k], acc[k]);
@@ -858,7 +863,7 @@ attn_tree_merge_kernel(const __grid_constant__ TreeParams p) {
     if (blockIdx.y == 0 && threadIdx.x < gr && row < rows && p.lse && (cut || r0 + row >= live)) {
         const int r = r0 + row, t = r / p.G;
         p.lse[((size_t)b * p.Hq + (size_t)h * p.G + (r - t * p.G)) * p.T + t] =
-            sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2t;
+            sum == 0.f ? -INFINITY : (M + (shift + log2f(sum))) * kLn2t;
     }
 #pragma unroll
     for (int k = 0; k < CPT; ++k)

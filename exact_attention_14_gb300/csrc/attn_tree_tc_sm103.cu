@@ -54,6 +54,9 @@ constexpr float kTcTau = 8.0f;        // rescale threshold (log2 units)
 // fp16 and weights down to 2^-21 of the largest keep its 11 bits
 template <bool F8>
 constexpr float kTcLift = F8 ? 7.0f : 0.0f;
+// ... and V's descales over F times 2^7: with codes of at most 448 they fill fp16, and
+// 2^7 / F and F / 2^7 are in fp32's range for every F from 2^-100 to 2^128
+constexpr int kTcVLift = 7;
 constexpr float kTcLn2 = 0.69314718055994530942f;
 
 // ONE: no item has more than 128 rows (every piece is split): the shared memory of a
@@ -107,9 +110,9 @@ struct TcBars {
     uint32_t bad[kBadBufs][kBadTiles][4];
     float qs[2][128];                   // E4M3: what a row's products are multiplied with
     float m[2][128], l[2][128], lx[2][128];
-    float fin[2];                       // E4M3: F of a stream at the end
+    float fin[2];                       // E4M3: F / 2^7 of a stream at the end
     alignas(16) float kf[kDs][128];     // E4M3: K's descales of a tile
-    alignas(16) float wv[kDs][128];     // E4M3: V's descales over F
+    alignas(16) float wv[kDs][128];     // E4M3: V's descales times 2^7 over F
     int fexp[kDs];
 };
 static_assert(sizeof(TcBars) <= 12 * 1024, "barrier block");
@@ -235,8 +238,8 @@ struct TcDescales {
         }
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
-        fexp = max(fexp, min((int)(__float_as_uint(top) >> 23) - 126, 111));
-        const float fr = tc_pow2(-fexp);
+        fexp = max(fexp, min((int)(__float_as_uint(top) >> 23) - 126, 128));
+        const float fr = tc_pow2(kTcVLift - fexp);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             bars->kf[slot][32 * i + lane] = kd[i];
@@ -1244,14 +1247,14 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
         uint32_t tA = tO + 128 * t;
         if (x.pair) {
             inv_l = st.l == 0.f ? 0.f : 1.0f / st.l;
-            inv0 = F8 ? inv_l * (tc_pow2(st.fexp)) : inv_l;
+            inv0 = F8 ? inv_l * tc_pow2(st.fexp - kTcVLift) : inv_l;
         } else {
             // the streams' statistics meet in shared memory; each warpgroup
             // then merges half of the columns, both O's being in its lanes
             bars->m[t][me] = st.m;
             bars->l[t][me] = st.l;
             bars->lx[t][me] = st.lx;
-            if (wq == 0 && lane == 0) bars->fin[t] = F8 ? tc_pow2(st.fexp) : 1.f;
+            if (wq == 0 && lane == 0) bars->fin[t] = F8 ? tc_pow2(st.fexp - kTcVLift) : 1.f;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars->stat));

@@ -67,3 +67,25 @@ def test_a_chain_whose_last_slice_most_rows_do_not_see(d, G, how):
     o, lse = _run(q, cache)
     ref = tree64(q, clean)
     check_tree(o[:, :, :T - 1], lse[:, :, :T - 1], [x[:, :, :T - 1] for x in ref], True, torch.float32)
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d,G,T", [(128, 8, 1), (64, 4, 3), (256, 2, 1), (256, 4, 5), (128, 1, 20), (128, 4, 64)])
+def test_values_up_to_the_largest_bf16(d, G, T, out):
+    """V rows of 1.6e38..3.2e38, written by attn_cache_write; every row's average of them is finite."""
+    lengths, H, page = [2100, T + 40, T], 2, 64
+    v = [((1 + torch.rand(n, H, d, generator=torch.Generator().manual_seed(45 + i))) * 1.6e38).to(torch.bfloat16)
+         for i, n in enumerate(lengths)]
+    cache = Cache(lengths, H, d, page, True, seed=46, v=v)
+    q = _randn(3, H * G, T, d, seed=47).to(torch.bfloat16)
+    a = _args(q, cache)
+    for pages, descale in ((a[1], a[7]), (a[2], a[8])):
+        pages.fill_(0x7F)
+        descale.fill_(float("nan"))
+    ea.attn_cache_write(torch.cat(cache.k).cuda(), torch.cat(v).cuda(), a[1], a[2], torch.cat(cache.slots).cuda(),
+                        a[7], a[8])
+    o, lse = ea.decode_tree(*a, out_dtype=out)
+    torch.cuda.synchronize()
+    assert ea.attn_last_device_error() == 0
+    assert torch.isfinite(o).all()
+    check_tree(o, lse, tree64(q, cache), True, out)
