@@ -31,9 +31,10 @@
 // shared load and spreads them over four k-steps (Q is laid out to match), so
 // K needs no transposition.  V^T needs four keys' codes of one column in a
 // register: four 16-byte rows are transposed with byte permutes.  P multiplies
-// vd_j / F in fp16, F the power of two above the largest vd seen so far (O is
-// rescaled when F grows), times 2^15: weights down to 2^-29 of the largest keep
-// fp16's 11 bits.  bf16 caches use bf16 P, as the library's decode does.
+// vd_j / F in fp16, F the power of two above the largest vd so far of the keys that
+// the row sees (O is rescaled when F grows), times 2^15: weights times descales
+// down to 2^-29 of the largest descale keep fp16's 11 bits, smaller ones are off by at
+// most 2^-40 of F.  bf16 caches use bf16 P, as the library's decode does.
 //
 // Masked places: scores are selected, never added to.  V rows past the
 // sequence are zeroed in shared memory; a drafted token's V row that holds a
@@ -87,7 +88,7 @@ struct TreeBars {
     uint64_t full[6], empty[6];
     TreeRange range;
     int abort;
-    float m[kConsumers][kMaxRows], l[kConsumers][kMaxRows], x[kConsumers][kMaxRows], f[kConsumers];
+    float m[kConsumers][kMaxRows], l[kConsumers][kMaxRows], x[kConsumers][kMaxRows];
 };
 static_assert(sizeof(TreeBars) <= 1024, "barrier block");
 
@@ -358,6 +359,9 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) acc[i][nt][0] = acc[i][nt][1] = acc[i][nt][2] = acc[i][nt][3] = 0.f;
         float m[NT][2], l[NT][2], xs[NT][2];
+        // E4M3: a row's F = 2^fexp, 2^-100 (2^15 / F is finite where no key counts) to 2^128 (above every
+        // finite descale); it is used together with 2^15 alone, so that each factor is in range
+        int fexp[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -365,10 +369,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                 m[nt][r] = -INFINITY;
                 l[nt][r] = 0.f;   // this lane's part of the sum that normalises O
                 xs[nt][r] = 0.f;  // ... of the unrounded P (the LSE's)
+                fexp[nt][r] = -100;
             }
-        // E4M3: F = 2^fexp, 2^-100 (2^15 / F is finite where no key counts) to 2^128 (above every
-        // finite descale); it is used together with 2^15 alone, so that each factor is in range
-        int fexp = -100;
 
         for (int kt = w.k0; kt < w.k1; ++kt, ++used) {
             if ((int)(used & 1) != pair) continue;  // the other pair's tile
@@ -465,10 +467,10 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                             bad |= 1u << lane;
                     }
                     bad = __reduce_or_sync(0xFFFFFFFFu, bad);
-                    if constexpr (F8) {
+                    if constexpr (F8) {  // (a finite descale still counts for F)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (bad >> (k_lane + 8 * i) & 1u) wv[i] = 0.f;
+                            if (bad >> (k_lane + 8 * i) & 1u && !isfinite(wv[i])) wv[i] = 0.f;
                     }
                 }
                 // ---- running maximum
@@ -485,27 +487,38 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                         mx[nt][r] = x;
                         moved |= x > m[nt][r];
                     }
+                // (E4M3) the largest descale of V of this lane's keys that a row sees
+                auto top_of = [&](int nt, int r) {
+                    float top = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        top = fmaxf(top, plain || sf[i >> 1][nt][2 * (i & 1) + r] != -INFINITY ? fabsf(wv[i]) : 0.f);
+                    return top;
+                };
                 if constexpr (F8) {
-                    const float f = pow2i(fexp);  // (2^128: infinite, above every finite descale)
-                    moved |= fmaxf(fmaxf(fabsf(wv[0]), fabsf(wv[1])), fmaxf(fabsf(wv[2]), fabsf(wv[3]))) > f;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)  // (2^128: infinite, above every finite descale)
+                            moved |= top_of(nt, r) > pow2i(fexp[nt][r]);
                 }
                 if (__any_sync(0xFFFFFFFFu, moved)) {
-                    float grow = 1.f;  // E4M3: F_old / F_new
-                    if constexpr (F8) {
-                        float top = fmaxf(fmaxf(fabsf(wv[0]), fabsf(wv[1])), fmaxf(fabsf(wv[2]), fabsf(wv[3])));
-#pragma unroll
-                        for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-                        // 2^need > top (the same in every lane)
-                        const int need = max(min((int)(__float_as_uint(top) >> 23) - 126, 128), -100);
-                        if (need > fexp) {
-                            grow = fexp - need < -126 ? 0.f : pow2i(fexp - need);
-                            fexp = need;
-                        }
-                    }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
+                            float grow = 1.f;  // E4M3: F_old / F_new
+                            if constexpr (F8) {
+                                float top = top_of(nt, r);
+#pragma unroll
+                                for (int off = 4; off < 32; off <<= 1)
+                                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+                                const int old = fexp[nt][r];
+                                // 2^need > top
+                                const int need = max(min((int)(__float_as_uint(top) >> 23) - 126, 128), old);
+                                grow = old - need < -126 ? 0.f : pow2i(old - need);
+                                fexp[nt][r] = need;
+                            }
                             const float mn = fmaxf(m[nt][r], mx[nt][r]);
                             float al = ex2(m[nt][r] - (mn == -INFINITY ? 0.f : mn));  // (no key yet: 0)
                             m[nt][r] = mn;
@@ -520,15 +533,16 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                         }
                 }
                 // ---- P^T
-                if constexpr (F8) {
-                    const float fr = pow2i(kPFrame - fexp);
+                if constexpr (F8) {  // (rows that are added apart)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) wv[i] *= fr;
+                    for (int i = 0; i < 4; ++i)
+                        if (bad >> (k_lane + 8 * i) & 1u) wv[i] = 0.f;
                 }
                 uint32_t pb[2][NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+                    const float f0 = F8 ? pow2i(kPFrame - fexp[nt][0]) : 1.f, f1 = F8 ? pow2i(kPFrame - fexp[nt][1]) : 1.f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float p0 = ex2(sf[i >> 1][nt][2 * (i & 1)] - m0);
@@ -537,7 +551,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                         xs[nt][1] += p1;
                         uint32_t pk;
                         if constexpr (F8) {
-                            pk = pack_f16x2(p0 * wv[i], p1 * wv[i]);  // (O over the sum of unrounded P)
+                            // (O over the sum of unrounded P; an unseen key's 0 before F, which may be far below it)
+                            pk = pack_f16x2(p0 * wv[i] * f0, p1 * wv[i] * f1);
                         } else {
                             pk = pack_bf16x2(p0, p1);
                             l[nt][0] += bf16lo_to_f32(pk);
@@ -562,9 +577,11 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                                 const float sv = __shfl_sync(0xFFFFFFFFu, own, 4 * qr_of + qc);
                                 // (-1: not seen)
                                 pk[nt][r] = sv == -INFINITY ? -1.f : ex2(sv - (m[nt][r] == -INFINITY ? 0.f : m[nt][r]));
+                                if constexpr (F8)
+                                    if (sv != -INFINITY) pk[nt][r] *= pow2i(kPFrame - fexp[nt][r]);
                             }
-                        float fr = 1.f;
-                        if constexpr (F8) fr = lds32f(sD + (kTileKeys + wk0 + kk) * 4) * pow2i(kPFrame - fexp);
+                        float ds = 1.f;
+                        if constexpr (F8) ds = lds32f(sD + (kTileKeys + wk0 + kk) * 4);
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -575,7 +592,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                                     const uint32_t at = sV + tile_off(wk0 + kk, col >> 4) + (col & 15);
                                     uint32_t byte;
                                     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(at));
-                                    v = e4m3_f32(byte) * fr;
+                                    v = e4m3_f32(byte) * ds;
                                 } else {
                                     const uint32_t at = sV + tile_off(wk0 + kk, col >> 3) + 2 * (col & 7);
                                     uint32_t half;
@@ -660,7 +677,6 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     bars->x[warp][row] = xs[nt][r];
                 }
             }
-        if (lane == 0) bars->f[warp] = F8 ? pow2i(fexp - kPFrame) : 1.f;
         tree_consumers_sync();
         // this warp's O in the common frame and over the common sum
 #pragma unroll
@@ -677,7 +693,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     sum += wt * bars->l[x][row];
                     sumx += wt * bars->x[x][row];
                 }
-                const float mine = sum == 0.f ? 0.f : ex2(m[nt][r] - Ms) * bars->f[warp] / sum;
+                const float mine =
+                    sum == 0.f ? 0.f : ex2(m[nt][r] - Ms) * (F8 ? pow2i(fexp[nt][r] - kPFrame) : 1.f) / sum;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     acc[i][nt][r] *= mine;

@@ -29,7 +29,8 @@
 // drafted tokens' V rows with a NaN or an infinity, are zeroed before the
 // product; the latter are added again at the end of a piece to the rows that
 // see them, with scores computed anew (a slow path that ordinary data never
-// takes).
+// takes).  E4M3: so are keys of these tiles whose descales are far from the others'
+// (TcDescales), which fp16 could not hold with them.
 //
 // Bound: HBM up to about 128 rows, then the tensor cores and the softmax.  256 rows
 // by a 128-key tile: the four products take 2150 cycles of an SM's tensor cores, the
@@ -38,6 +39,7 @@
 // 245 us with the merge, 67% of the floor), E4M3 4600 (300 us), where S's
 // multiplication with the descales (40 us) and fp16 packing lengthen the softmax.
 // 64 rows, bf16: 183 us, 90% of HBM's rate; E4M3 196 us.
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -57,6 +59,11 @@ constexpr float kTcLift = F8 ? 7.0f : 0.0f;
 // ... and V's descales over F times 2^7: with codes of at most 448 they fill fp16, and
 // 2^7 / F and F / 2^7 are in fp32's range for every F from 2^-100 to 2^128
 constexpr int kTcVLift = 7;
+// E4M3, a special tile's keys are held with F when their descales are in (F / 2^12, F]: 2^7
+// descale / F times a code, at least 2^-9, is then a normal fp16 number.  A drafted token
+// raises the F of the keys before by up to 2^8.  Keys outside are added apart.
+constexpr int kTcSpan = 12;
+constexpr int kTcOver = 8;
 constexpr float kTcLn2 = 0.69314718055994530942f;
 
 // ONE: no item has more than 128 rows (every piece is split): the shared memory of a
@@ -88,7 +95,7 @@ struct TcRoles {
     static_assert(32 * kControl * kRegsControl + 256 * kRegsSoftmax <= kThreads * kLaunch, "register split");
 };
 
-// Marks of the V rows that were taken out: for each of the last pieces, for
+// Marks of the V rows that were taken out of the product: for each of the last pieces, for
 // each of its special tiles (1024 drafted tokens reach over 10 at most), a bit
 // per key.  A writer is at most 4 pieces ahead of the readers (a piece takes two
 // of at most 8 ring slots), so 8 buffers need no hand-shake.
@@ -114,6 +121,7 @@ struct TcBars {
     alignas(16) float kf[kDs][128];     // E4M3: K's descales of a tile
     alignas(16) float wv[kDs][128];     // E4M3: V's descales times 2^7 over F
     int fexp[kDs];
+    uint32_t skip[kDs][4];              // E4M3: keys of a special tile that are added apart, by their descales
 };
 static_assert(sizeof(TcBars) <= 12 * 1024, "barrier block");
 
@@ -211,11 +219,50 @@ struct TcRing {
 // E4M3, a warp lays out the next tile's descales once its K is there: K's for the
 // softmax, V's over F for the converters, F = 2^fexp above every one of the piece so
 // far.  (K's codes go into the product as they are: rounded descales would enter the
-// exponent.)
+// exponent.)  A drafted token that a row does not see may not cost it bits, so F and
+// the keys that fit it are chosen anew in each special tile (`choose`).
 template <class C>
 struct TcDescales {
     uint32_t tiles, kslot, kround;
     int fexp;
+    // A special tile, keys key0 + 32 i: F and the keys that are added apart, vd 0 for those.
+    __device__ __forceinline__ void choose(const TreePiece& w, int key0, int lane, uint32_t* skip, float (&vd)[4]) {
+        constexpr int kNone = INT_MIN;
+        int e[4], base = kNone, hi = kNone, lo = INT_MAX;  // 2^e above a descale
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = fabsf(vd[i]);
+            e[i] = a > 0.f && a < INFINITY ? max((int)(__float_as_uint(a) >> 23) - 126, -100) : kNone;
+            if (e[i] == kNone) continue;
+            if (key0 + 32 * i < w.keys - w.drafted) base = max(base, e[i]);
+            hi = max(hi, e[i]);
+            lo = min(lo, e[i]);
+        }
+        base = max(__reduce_max_sync(0xFFFFFFFFu, base), fexp);
+        hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+        lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+        if (base > -100) {  // there are keys before: F is theirs
+            int top = base;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (e[i] <= base + kTcOver) top = max(top, e[i]);
+            fexp = __reduce_max_sync(0xFFFFFFFFu, top);
+        } else if (hi != kNone) {  // the first keys of the piece: F for the largest or for the smallest, whichever are more
+            int many = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                many += __popc(__ballot_sync(0xFFFFFFFFu, e[i] > hi - kTcSpan)) -
+                        __popc(__ballot_sync(0xFFFFFFFFu, e[i] != kNone && e[i] < lo + kTcSpan));
+            fexp = many >= 0 ? hi : lo + kTcSpan - 1;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool apart = e[i] != kNone ? e[i] > fexp || e[i] <= fexp - kTcSpan : vd[i] != 0.f;
+            const uint32_t votes = __ballot_sync(0xFFFFFFFFu, apart);
+            if (lane == 0) skip[i] = votes;
+            if (apart) vd[i] = 0.f;
+        }
+    }
     __device__ __forceinline__ bool tile(uint8_t* smem, TcBars* bars, const TreePiece& w, int kt, int lane,
                                          const volatile int* abort_flag) {
         const uint32_t slot = tiles % kDs;
@@ -223,22 +270,23 @@ struct TcDescales {
         if (tiles >= kDs && !warp_wait(&bars->ds_empty[slot], tiles / kDs - 1u, abort_flag)) return false;
         const float* raw = reinterpret_cast<const float*>(smem + C::kDescale + kslot * 1024);
         const int key0 = kt * kTcKeys + lane;
-        float kd[4], vd[4], top = 0.f;
+        float kd[4], vd[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             kd[i] = raw[32 * i + lane];
             vd[i] = raw[128 + 32 * i + lane];
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int key = key0 + 32 * i;
-            // past the sequence, or a row that is added apart
-            if (key >= w.keys || (key >= w.keys - w.drafted && !isfinite(vd[i]))) vd[i] = 0.f;
-            top = fmaxf(top, fabsf(vd[i]));
-        }
+        for (int i = 0; i < 4; ++i)
+            if (key0 + 32 * i >= w.keys) vd[i] = 0.f;  // past the sequence
+        if ((kt + 1) * kTcKeys > w.keys - w.drafted) {
+            choose(w, key0, lane, bars->skip[slot], vd);
+        } else {
+            float top = fmaxf(fmaxf(fabsf(vd[0]), fabsf(vd[1])), fmaxf(fabsf(vd[2]), fabsf(vd[3])));
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
-        fexp = max(fexp, min((int)(__float_as_uint(top) >> 23) - 126, 128));
+            for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
+            fexp = max(fexp, min((int)(__float_as_uint(top) >> 23) - 126, 128));
+        }
         const float fr = tc_pow2(kTcVLift - fexp);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -752,13 +800,8 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
                         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int e = 0; e < 16; ++e) hit |= ((u[e >> 2] >> (8 * (e & 3))) & 0x7Fu) == 0x7Fu;
-                        if (c == 0) {
-                            int off;
-                            const int page = tree_page(p, x.w.b, key, x.w.keys, off);
-                            if (page >= 0)
-                                hit |= !isfinite(__ldg(p.v_descale + ((long long)page * p.Hkv + x.w.h) * p.page_size + off));
-                        }
                     }
+                    if (c == 0) hit |= (*((volatile uint32_t*)&bars->skip[ds][row >> 5]) >> (row & 31)) & 1u;
                     const unsigned votes = __ballot_sync(0xFFFFFFFFu, hit);
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
@@ -976,17 +1019,17 @@ __device__ __forceinline__ void tc_softmax_half(uint32_t tS, uint32_t tO, const 
     r.lx += u + v;
 }
 
-// Adds the drafted tokens whose V rows were taken out of the product to 16
-// columns of a finished row (rare; scores computed anew in fp32).
+// Adds the keys whose V rows were taken out of the product to 16 columns of a
+// finished row (rare; scores computed anew in fp32).
 template <bool F8>
 __device__ __noinline__ void tc_add_bad(const TreeParams& p, const TcPiece& x, const uint32_t* bad, int t,
                                         const __nv_bfloat16* q, float m, float inv, int col, float (&v)[16]) {
     const int key0 = (x.w.k0 + x.first_special()) * kTcKeys;
     const int end = min(x.w.k1 * kTcKeys, x.w.keys);
-    for (int key = max(key0, x.prefix); key < end; ++key) {
+    for (int key = key0; key < end; ++key) {
         const int i = key - key0;
         if (!(*((const volatile uint32_t*)bad + (i >> 5)) >> (i & 31) & 1u)) continue;
-        if (!tree_sees(p, x.w.b, t, key - x.prefix)) continue;
+        if (key >= x.prefix && !tree_sees(p, x.w.b, t, key - x.prefix)) continue;
         int off;
         const int page = tree_page(p, x.w.b, key, x.w.keys, off);
         if (page < 0) continue;

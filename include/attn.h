@@ -562,10 +562,21 @@ size_t attn_decode_tree_workspace_size(int B, int Hq, int Hkv, int T, int max_bl
  * tokens a row does not see, never reach it (NaN included); a block-table entry
  * outside [0, num_blocks) reads as zeros.
  * Numerics: fp32 scores, softmax statistics and O.  bf16 cache: P is rounded to
- * bf16.  E4M3 cache: K's codes and descales enter exactly; P is rounded to fp16,
- * with V's descale in it or, for many rows (T * Hq / Hkv > 16 and d <= 128), V
- * times its descale rounded to fp16 too, and Q's elements below 2^-9 of their row's
- * largest to 2^-17 of that.  Results do not change from run to run.
+ * bf16; O is divided by the sum of the rounded P or, for many rows (T * Hq / Hkv > 8
+ * and 64 < d <= 128, or > 16 and d <= 64), by the sum of the unrounded P with the
+ * largest weight's rounding added.  E4M3 cache: K's codes and descales enter
+ * exactly, O is divided by the sum of the unrounded P; P is rounded to fp16, with V's
+ * descale in it or, for many rows (T * Hq / Hkv > 16 and d <= 128), V times its
+ * descale rounded to fp16 too, in two steps, and Q's elements below 2^-9 of their
+ * row's largest to 2^-17 of that.
+ * The size of V's rows (E4M3): few rows: weight times descale is held relative to the
+ * largest descale D of the keys that the row sees; below 2^-28 D it is off by up to
+ * 2^-39 D.  Many rows: among the keys before the drafted ones, descales below 2^-12
+ * of the largest, D, put up to (|code| + 1) 2^-31 D on their V; drafted tokens keep
+ * their bits whatever their sizes are, slowly where a descale is more than 2^8 above
+ * those of the keys before it, or less than 2^-12 of them.  A V row 2^126 times
+ * smaller than another that its row sees may count as zero.
+ * Results do not change from run to run.
  * Supported: 8 <= d <= 256, d % 8 == 0 (E4M3: d % 16 == 0); page_size % 16 ==
  * 0; Hq % Hkv == 0; 1 <= T <= 1024; T * Hq / Hkv <= 2^20; B * Hq * T <= 2^30;
  * max_blocks * page_size <= 2^24.

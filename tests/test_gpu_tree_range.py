@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import exact_attention_14_gb300 as ea
-from paged_ref import Cache, check_tree, tree64
+from paged_ref import Cache, check_tree, random_trees, tree64
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +89,85 @@ def test_values_up_to_the_largest_bf16(d, G, T, out):
     assert ea.attn_last_device_error() == 0
     assert torch.isfinite(o).all()
     check_tree(o, lse, tree64(q, cache), True, out)
+
+
+ROWS = [(128, 1, 6), (64, 2, 8), (256, 1, 12), (256, 4, 6), (128, 1, 20), (64, 4, 20), (128, 4, 60)]
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e6, 1e30, 3e38])
+@pytest.mark.parametrize("prefix", [0, 50, 700])
+@pytest.mark.parametrize("d,G,T", ROWS)
+def test_unseen_drafts_of_any_finite_size(d, G, T, prefix, size):
+    """A drafted token whose V row is far larger (or smaller) than the others': rows that do not see
+    it keep every bit, and so do rows that do."""
+    lengths = [T + prefix, T + prefix // 2]
+    v = [_randn(n, 1, d, seed=48 + i) for i, n in enumerate(lengths)]
+    for x in v:
+        x[-T + 3] *= size / x[-T + 3].abs().max()
+    cache = Cache(lengths, 1, d, 16, True, seed=49, v=[x.to(torch.bfloat16) for x in v])
+    mask = random_trees(2, T, 50)
+    mask[:, 4:, 3] = False
+    mask[:, T - 1, 3] = True
+    q = _randn(2, G, T, d, seed=51).to(torch.bfloat16)
+    o, lse = _run(q, cache, mask)
+    check_tree(o, lse, tree64(q, cache, mask), True, torch.float32)
+
+
+def _descale_floor(q, cache, mask, unit, one):
+    """What a row's V rows may be off by, apart from their own roundings, where they are held in
+    steps of `unit` times the largest descale that the row sees: sum_j (|code_j| + one) * unit * that."""
+    B, Hq, T, d = q.shape
+    out = torch.zeros(B, Hq, T, d, dtype=torch.float64)
+    for b in range(B):
+        L = cache.lengths[b]
+        codes = cache.v_pages.view(-1, *cache.v_pages.shape[2:])[cache.slots[b]].view(torch.float8_e4m3fn).double().abs()
+        ds = cache.v_descale[cache.slots[b] // cache.page, :, cache.slots[b] % cache.page].double()
+        see = torch.ones(T, L, dtype=torch.bool)
+        see[:, L - T:] = torch.tril(torch.ones(T, T, dtype=torch.bool)) if mask is None else mask[b]
+        for h in range(Hq):
+            kv = h // (Hq // ds.shape[1])
+            for t in range(T):
+                js = see[t].nonzero().squeeze(1)
+                if js.numel():
+                    out[b, h, t] = unit * ds[js, kv].max() * (codes[js, kv] + one).sum(0)
+    return out
+
+
+@pytest.mark.parametrize("d,G,T", ROWS)
+def test_drafts_of_all_sizes_without_a_prefix(d, G, T):
+    """V rows from 1e-12 to 1e12, seen by some rows and not by others."""
+    v = _randn(T, 1, d, seed=52) * 10.0 ** (24 * torch.rand(T, 1, 1, generator=torch.Generator().manual_seed(53)) - 12)
+    cache = Cache([T], 1, d, 16, True, seed=54, v=[v.to(torch.bfloat16)])
+    mask = random_trees(1, T, 55)
+    q = _randn(1, G, T, d, seed=56).to(torch.bfloat16)
+    o, lse = _run(q, cache, mask)
+    ro, rl, size, eps = tree64(q, cache, mask)
+    if T * G <= 16 or d > 128:
+        # weights times descales are held in fp16 times 2^15 over a power of two that is at most
+        # twice the row's largest descale: steps of 2^-24, half of one, 2^-39 of it; a weight
+        # relative to the largest one, over a sum of at least 1
+        size = size + _descale_floor(q, cache, mask, 2.0 ** -39, 0) / (3 * 2.0 ** -11)
+    check_tree(o, lse, (ro, rl, size, eps), True, torch.float32)
+
+
+@pytest.mark.parametrize("big", [1e3, 1e6, 1e8])
+@pytest.mark.parametrize("d,G,T", [(128, 8, 1), (64, 2, 3), (256, 1, 2), (256, 2, 20), (128, 1, 20), (128, 4, 40)])
+def test_a_large_value_of_almost_no_weight(d, G, T, big):
+    """A key of the context with a large V row and next to no weight: the others keep the bits that
+    the documentation says."""
+    n = 400
+    k, v = _randn(n, 1, d, seed=57) * 0.5, _randn(n, 1, d, seed=58)
+    q = _randn(1, G, T, d, seed=59) * 0.3 + 1.0
+    k[5] = -30.0 / d ** 0.5                                          # q . k / sqrt(d) about -30
+    v[5] *= big
+    cache = Cache([n], 1, d, 16, True, k=[k.to(torch.bfloat16)], v=[v.to(torch.bfloat16)])
+    q = q.to(torch.bfloat16)
+    o, lse = _run(q, cache)
+    ro, rl, size, eps = tree64(q, cache)
+    if T * G <= 16 or d > 128:
+        size = size + _descale_floor(q, cache, None, 2.0 ** -39, 0) / (3 * 2.0 ** -11)
+    else:
+        # code * fp16(2^7 descale / F), F at most twice the largest descale: the factor and the product
+        # are in steps of 2^-24, half of one over 2^7 is 2^-31 of that descale
+        size = size + _descale_floor(q, cache, None, 2.0 ** -31, 1) / (3 * 2.0 ** -11)
+    check_tree(o, lse, (ro, rl, size, eps), True, torch.float32)
