@@ -30,7 +30,7 @@
 // product; the latter are added again at the end of a piece to the rows that
 // see them, with scores computed anew (a slow path that ordinary data never
 // takes).  E4M3: so are keys of these tiles whose descales are far from the others'
-// (TcDescales), which fp16 could not hold with them.
+// (tc_choose), which fp16 could not hold with them.
 //
 // Bound: HBM up to about 128 rows, then the tensor cores and the softmax.  256 rows
 // by a 128-key tile: the four products take 2150 cycles of an SM's tensor cores, the
@@ -216,53 +216,62 @@ struct TcRing {
     }
 };
 
+// The F = 2^x of a special tile and the keys that are added apart, marked in `skip`: bit i
+// of y for key 32 i + lane.  vd: the tile's descales of V; keys below `prefix` come before
+// the drafted ones, those from `keys` on are past the sequence.  (Out of line: inside the
+// producer's loop it costs 64 drafts 340 -> 364 us.)
+__device__ __noinline__ int2 tc_choose(const float* vd, int prefix, int keys, int fexp, uint32_t* skip) {
+    constexpr int kNone = INT_MIN;
+    const int lane = threadIdx.x & 31;
+    int e[4], base = kNone, hi = kNone, lo = INT_MAX;  // 2^e above a descale
+    bool lost[4];                                      // not finite
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = 32 * i + lane < keys ? fabsf(vd[32 * i + lane]) : 0.f;
+        lost[i] = !(a < INFINITY);
+        e[i] = a > 0.f && a < INFINITY ? max((int)(__float_as_uint(a) >> 23) - 126, -100) : kNone;
+        if (e[i] == kNone) continue;
+        if (32 * i + lane < prefix) base = max(base, e[i]);
+        hi = max(hi, e[i]);
+        lo = min(lo, e[i]);
+    }
+    base = max(__reduce_max_sync(0xFFFFFFFFu, base), fexp);
+    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+    if (base > -100) {  // there are keys before: F is theirs
+        int top = base;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (e[i] <= base + kTcOver) top = max(top, e[i]);
+        fexp = __reduce_max_sync(0xFFFFFFFFu, top);
+    } else if (hi != kNone) {  // the first keys of the piece: F for the largest or for the smallest, whichever are more
+        int many = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            many += __popc(__ballot_sync(0xFFFFFFFFu, e[i] > hi - kTcSpan)) -
+                    __popc(__ballot_sync(0xFFFFFFFFu, e[i] != kNone && e[i] < lo + kTcSpan));
+        fexp = many >= 0 ? hi : lo + kTcSpan - 1;
+    }
+    int apart = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool out = lost[i] || (e[i] != kNone && (e[i] > fexp || e[i] <= fexp - kTcSpan));
+        const uint32_t votes = __ballot_sync(0xFFFFFFFFu, out);
+        if (lane == 0) skip[i] = votes;
+        apart |= (int)out << i;
+    }
+    return make_int2(fexp, apart);
+}
+
 // E4M3, a warp lays out the next tile's descales once its K is there: K's for the
 // softmax, V's over F for the converters, F = 2^fexp above every one of the piece so
 // far.  (K's codes go into the product as they are: rounded descales would enter the
 // exponent.)  A drafted token that a row does not see may not cost it bits, so F and
-// the keys that fit it are chosen anew in each special tile (`choose`).
+// the keys that fit it are chosen anew in each special tile (tc_choose).
 template <class C>
 struct TcDescales {
     uint32_t tiles, kslot, kround;
     int fexp;
-    // A special tile, keys key0 + 32 i: F and the keys that are added apart, vd 0 for those.
-    __device__ __forceinline__ void choose(const TreePiece& w, int key0, int lane, uint32_t* skip, float (&vd)[4]) {
-        constexpr int kNone = INT_MIN;
-        int e[4], base = kNone, hi = kNone, lo = INT_MAX;  // 2^e above a descale
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = fabsf(vd[i]);
-            e[i] = a > 0.f && a < INFINITY ? max((int)(__float_as_uint(a) >> 23) - 126, -100) : kNone;
-            if (e[i] == kNone) continue;
-            if (key0 + 32 * i < w.keys - w.drafted) base = max(base, e[i]);
-            hi = max(hi, e[i]);
-            lo = min(lo, e[i]);
-        }
-        base = max(__reduce_max_sync(0xFFFFFFFFu, base), fexp);
-        hi = __reduce_max_sync(0xFFFFFFFFu, hi);
-        lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-        if (base > -100) {  // there are keys before: F is theirs
-            int top = base;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (e[i] <= base + kTcOver) top = max(top, e[i]);
-            fexp = __reduce_max_sync(0xFFFFFFFFu, top);
-        } else if (hi != kNone) {  // the first keys of the piece: F for the largest or for the smallest, whichever are more
-            int many = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                many += __popc(__ballot_sync(0xFFFFFFFFu, e[i] > hi - kTcSpan)) -
-                        __popc(__ballot_sync(0xFFFFFFFFu, e[i] != kNone && e[i] < lo + kTcSpan));
-            fexp = many >= 0 ? hi : lo + kTcSpan - 1;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool apart = e[i] != kNone ? e[i] > fexp || e[i] <= fexp - kTcSpan : vd[i] != 0.f;
-            const uint32_t votes = __ballot_sync(0xFFFFFFFFu, apart);
-            if (lane == 0) skip[i] = votes;
-            if (apart) vd[i] = 0.f;
-        }
-    }
     __device__ __forceinline__ bool tile(uint8_t* smem, TcBars* bars, const TreePiece& w, int kt, int lane,
                                          const volatile int* abort_flag) {
         const uint32_t slot = tiles % kDs;
@@ -276,11 +285,12 @@ struct TcDescales {
             kd[i] = raw[32 * i + lane];
             vd[i] = raw[128 + 32 * i + lane];
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (key0 + 32 * i >= w.keys) vd[i] = 0.f;  // past the sequence
         if ((kt + 1) * kTcKeys > w.keys - w.drafted) {
-            choose(w, key0, lane, bars->skip[slot], vd);
+            const int2 c = tc_choose(raw + 128, w.keys - w.drafted - kt * kTcKeys, w.keys - kt * kTcKeys, fexp, bars->skip[slot]);
+            fexp = c.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c.y >> i & 1 || key0 + 32 * i >= w.keys) vd[i] = 0.f;  // (or past the sequence)
         } else {
             float top = fmaxf(fmaxf(fabsf(vd[0]), fabsf(vd[1])), fmaxf(fabsf(vd[2]), fabsf(vd[3])));
 #pragma unroll
@@ -801,7 +811,7 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
 #pragma unroll
                         for (int e = 0; e < 16; ++e) hit |= ((u[e >> 2] >> (8 * (e & 3))) & 0x7Fu) == 0x7Fu;
                     }
-                    if (c == 0) hit |= (*((volatile uint32_t*)&bars->skip[ds][row >> 5]) >> (row & 31)) & 1u;
+                    hit |= (*((volatile uint32_t*)&bars->skip[ds][row >> 5]) >> (row & 31)) & 1u;
                     const unsigned votes = __ballot_sync(0xFFFFFFFFu, hit);
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
