@@ -18,8 +18,6 @@ import ctypes
 import functools
 import os
 
-import torch
-
 __all__ = [
     "ATTN_OUT_BF16", "ATTN_OUT_F32", "AttnError", "attn_fwd", "attn_fwd_workspace_size",
     "attn_fwd_varlen", "forward_varlen",
@@ -50,6 +48,18 @@ ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgb300_attn.so")
 _lib = None
+
+
+class _Torch:
+    """Stands in for torch until a call needs it: the host-only plans and
+    frequencies work without torch and its import time."""
+    def __getattr__(self, name):
+        global torch
+        import torch
+        return getattr(torch, name)
+
+
+torch = _Torch()
 
 # Every symbol the header declares, with its ctypes signature.
 _c_int, _c_ll, _c_sz, _c_f, _vp = (ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t,

@@ -1,0 +1,55 @@
+"""The binding's host side: what it imports, asks torch for and remembers (no GPU)."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    from exact_attention_14_gb300 import _build
+    _build.build()
+
+
+def test_plans_need_no_torch():
+    """The package and its host-only functions, where torch cannot be imported at all."""
+    code = """
+import sys
+sys.modules["torch"] = None                       # an import of torch raises
+import exact_attention_14_gb300 as ea
+assert ea.attn_decode_num_splits(4, 8, 4096) >= 1
+assert ea.attn_fwd_num_units(1, 4, 4, 512, 512, 128, True) >= 1
+assert ea.attn_kv_tiles(0, 256, 512, 512, 128, 1) >= 1
+f, mag = ea.attn_rope_frequencies(64, 10000.0)
+assert len(f) == 32 and mag == 1.0
+assert ea.attn_status_string(0) == "ATTN_OK"
+try:
+    ea.rope(None, None, None, None)
+except ImportError:
+    print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr
+
+
+def test_torch_comes_with_the_first_call_that_needs_it():
+    code = """
+import sys
+import exact_attention_14_gb300 as ea
+assert "torch" not in sys.modules
+ea.attn_rope_frequencies(64, 10000.0)
+assert "torch" not in sys.modules
+try:
+    ea.rope([], None, None, None)
+except TypeError as e:
+    assert "torch.Tensor" in str(e)
+import torch
+assert ea.torch is torch
+m = ea.tree_mask_words(torch.ones(1, 2, 2, dtype=torch.bool))
+print(m.flatten().tolist())
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "[3, 3]", r.stderr
