@@ -154,11 +154,16 @@ def _check(code: int, where: str):
         raise AttnError(code, where)
 
 
+def _current_stream(device):
+    """Handle of a device's current stream; without a Stream object (1 us of a small
+    call's 17) where torch has the call that its generated code makes."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+
+
 def _stream_ptr(stream):
-    if stream is None:   # the current stream of the current device, without a Stream object
-        if not torch.cuda.is_initialized():
-            torch.cuda.init()
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if stream is None:   # the current stream of the current device
+        return _current_stream(torch.cuda.current_device())
     return ctypes.c_void_p(int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -213,7 +218,7 @@ _HERE = _Here()
 
 
 def _on(dev):
-    if dev.index == torch._C._cuda_getDevice():   # (a switch and back costs more than a launch)
+    if dev.index == torch.cuda.current_device():   # (a switch and back costs more than a launch)
         return _HERE
     return torch.cuda.device(dev)
 

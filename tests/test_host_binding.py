@@ -2,6 +2,7 @@
 import os
 import subprocess
 import sys
+import types
 
 import pytest
 
@@ -53,3 +54,19 @@ print(m.flatten().tolist())
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "[3, 3]", r.stderr
+
+
+def test_current_stream_without_torch_internals(monkeypatch):
+    """Where torch does not have its internal call, its public ones give the same handle."""
+    import torch
+
+    import exact_attention_14_gb300 as ea
+    ea.tree_mask_words(torch.ones(1, 1, 1, dtype=torch.bool))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: types.SimpleNamespace(cuda_stream=1000 + d))
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    assert ea._stream_ptr(None) == 1003
+    assert ea._on(torch.device("cuda", 3)) is ea._HERE
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 2000 + d, raising=False)
+    assert ea._stream_ptr(None) == 2003
