@@ -1135,10 +1135,21 @@ def attn_decode_tree_workspace_size(B: int, Hq: int, Hkv: int, T: int, max_block
 
 
 @functools.lru_cache(maxsize=1024)
+def _tree_workspace_known(Hq, Hkv, T, d, kind, device_index):
+    n = int(load().attn_decode_tree_workspace_size(1, Hq, Hkv, T, 1, 16, d, kind))
+    if n == 0:
+        raise LookupError   # (not remembered)
+    return n
+
+
 def _tree_workspace(Hq, Hkv, T, d, kind, device_index):
     """attn_decode_tree_workspace_size on the current device (device_index), which
-    depends on nothing else.  (0 for what the library will refuse.)"""
-    return int(load().attn_decode_tree_workspace_size(1, Hq, Hkv, T, 1, 16, d, kind))
+    depends on nothing else.  0, for what the library will refuse or when the device
+    does not answer, is asked for again the next time."""
+    try:
+        return _tree_workspace_known(Hq, Hkv, T, d, kind, device_index)
+    except LookupError:
+        return 0
 
 
 def _tree_call(q, k_pages, v_pages, block_table, seqlens, o, lse, tree_mask, q_lens, k_descale,

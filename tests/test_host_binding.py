@@ -70,3 +70,18 @@ def test_current_stream_without_torch_internals(monkeypatch):
     assert ea._on(torch.device("cuda", 3)) is ea._HERE
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 2000 + d, raising=False)
     assert ea._stream_ptr(None) == 2003
+
+
+def test_a_workspace_size_of_zero_is_not_remembered(monkeypatch):
+    """A device that did not answer once, or a shape that was refused, does not stay at 0 bytes."""
+    import exact_attention_14_gb300 as ea
+    sizes = [0, 0, 4096, 8192]
+    asked = []
+
+    def size(*a):
+        asked.append(a)
+        return sizes[len(asked) - 1]
+    monkeypatch.setattr(ea, "load", lambda: types.SimpleNamespace(attn_decode_tree_workspace_size=size))
+    args = (6, 2, 5, 96, 0, 77)
+    assert [ea._tree_workspace(*args) for _ in range(4)] == [0, 0, 4096, 4096]
+    assert len(asked) == 3
