@@ -155,8 +155,8 @@ def _check(code: int, where: str):
 
 
 def _current_stream(device):
-    """Handle of a device's current stream; without a Stream object (1 us of a small
-    call's 17) where torch has the call that its generated code makes."""
+    """Handle of a device's current stream; without a Stream object (2 us of a small
+    call's 20) where torch has the call that its generated code makes."""
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 

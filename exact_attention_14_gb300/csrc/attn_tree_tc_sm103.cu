@@ -216,10 +216,10 @@ struct TcRing {
     }
 };
 
-// The F = 2^x of a special tile and the keys that are added apart, marked in `skip`: bit i
-// of y for key 32 i + lane.  vd: the tile's descales of V; keys below `prefix` come before
-// the drafted ones, those from `keys` on are past the sequence.  (Out of line: inside the
-// producer's loop it costs 64 drafts 340 -> 364 us.)
+// The F = 2^x of a special tile and the keys that are added apart, marked in `skip`; bit i
+// of y: key 32 i + lane is one, or past the sequence.  vd: the tile's descales of V; keys
+// below `prefix` come before the drafted ones, those from `keys` on are past the sequence.
+// (Out of line: inside the producer's loop it took 64 drafts from 340 to 364 us.)
 __device__ __noinline__ int2 tc_choose(const float* vd, int prefix, int keys, int fexp, uint32_t* skip) {
     constexpr int kNone = INT_MIN;
     const int lane = threadIdx.x & 31;
@@ -258,7 +258,7 @@ __device__ __noinline__ int2 tc_choose(const float* vd, int prefix, int keys, in
         const bool out = lost[i] || (e[i] != kNone && (e[i] > fexp || e[i] <= fexp - kTcSpan));
         const uint32_t votes = __ballot_sync(0xFFFFFFFFu, out);
         if (lane == 0) skip[i] = votes;
-        apart |= (int)out << i;
+        apart |= (int)(out || 32 * i + lane >= keys) << i;
     }
     return make_int2(fexp, apart);
 }
@@ -290,7 +290,7 @@ struct TcDescales {
             fexp = c.x;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (c.y >> i & 1 || key0 + 32 * i >= w.keys) vd[i] = 0.f;  // (or past the sequence)
+                if (c.y >> i & 1) vd[i] = 0.f;  // (past the sequence too)
         } else {
             float top = fmaxf(fmaxf(fabsf(vd[0]), fabsf(vd[1])), fmaxf(fabsf(vd[2]), fabsf(vd[3])));
 #pragma unroll
@@ -811,7 +811,7 @@ __device__ void tc_convert(int wc, uint8_t* smem, TcBars* bars, const TreeParams
 #pragma unroll
                         for (int e = 0; e < 16; ++e) hit |= ((u[e >> 2] >> (8 * (e & 3))) & 0x7Fu) == 0x7Fu;
                     }
-                    hit |= (*((volatile uint32_t*)&bars->skip[ds][row >> 5]) >> (row & 31)) & 1u;
+                    if (c == 0) hit |= (*((volatile uint32_t*)&bars->skip[ds][row >> 5]) >> (row & 31)) & 1u;
                     const unsigned votes = __ballot_sync(0xFFFFFFFFu, hit);
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
@@ -1029,41 +1029,6 @@ __device__ __forceinline__ void tc_softmax_half(uint32_t tS, uint32_t tO, const 
     r.lx += u + v;
 }
 
-// Adds the keys whose V rows were taken out of the product to 16 columns of a
-// finished row (rare; scores computed anew in fp32).
-template <bool F8>
-__device__ __noinline__ void tc_add_bad(const TreeParams& p, const TcPiece& x, const uint32_t* bad, int t,
-                                        const __nv_bfloat16* q, float m, float inv, int col, float (&v)[16]) {
-    const int key0 = (x.w.k0 + x.first_special()) * kTcKeys;
-    const int end = min(x.w.k1 * kTcKeys, x.w.keys);
-    for (int key = key0; key < end; ++key) {
-        const int i = key - key0;
-        if (!(*((const volatile uint32_t*)bad + (i >> 5)) >> (i & 31) & 1u)) continue;
-        if (key >= x.prefix && !tree_sees(p, x.w.b, t, key - x.prefix)) continue;
-        int off;
-        const int page = tree_page(p, x.w.b, key, x.w.keys, off);
-        if (page < 0) continue;
-        const long long row = (((long long)page * p.page_size + off) * p.Hkv + x.w.h) * p.dh;
-        const long long ds = ((long long)page * p.Hkv + x.w.h) * p.page_size + off;
-        auto value = [&](const uint8_t* pages, const float* descale, int i) {
-            if constexpr (F8) {
-                uint32_t lo, hi;
-                tc_e4m3x4(pages[row + i], lo, hi);
-                float f;
-                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(f) : "r"(lo));
-                return f * descale[ds];
-            } else {
-                return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(pages)[row + i]);
-            }
-        };
-        float s = 0.f;
-        for (int i = 0; i < p.dh; ++i) s = fmaf(__bfloat162float(q[i]), value(p.k_pages, p.k_descale, i), s);
-        const float w = ex2(s * p.c - m + kTcLift<F8>) * inv;
-        for (int i = 0; i < 16; ++i)
-            if (col + i < p.dh) v[i] = fmaf(w, value(p.v_pages, p.v_descale, col + i), v[i]);
-    }
-}
-
 // Q rows of a stream's tile into shared memory: this warp's 32 rows, D / 8 lanes
 // a row (rows past the last repeat it), 128-byte swizzled 64-column halves.
 // `row_at`: where this lane's own row starts in Q.
@@ -1152,9 +1117,8 @@ struct TcOut {
 
 // Columns [col0, col1) of the row: a partial result goes out a column at a time
 // (32 rows side by side), a whole one 32 or 64 bytes of the row at a time.
-template <int D, bool F8, bool BAD>
 __device__ __forceinline__ void tc_write(const TreeParams& p, const TcPiece& x, const TcOut& o, uint32_t tA, int col0,
-                                         int col1, const uint32_t* bad) {
+                                         int col1) {
     float* part = p.ws_o + (o.place * kTcRows + (o.row & ~31)) * p.dw + (threadIdx.x & 31);
     const size_t at = o.bht * p.dh;
 #pragma unroll 1
@@ -1169,7 +1133,6 @@ __device__ __forceinline__ void tc_write(const TreeParams& p, const TcPiece& x, 
             v[i] = __uint_as_float(a[i]) * o.inv0;
             if (o.two) v[i] = fmaf(__uint_as_float(b[i]), o.inv1, v[i]);
         }
-        if constexpr (BAD) tc_add_bad<F8>(p, x, bad, o.tok, p.q + at, o.m, o.inv, cc, v);
         if (!x.w.whole) {
             if (o.live) {
 #pragma unroll
@@ -1192,12 +1155,124 @@ __device__ __forceinline__ void tc_write(const TreeParams& p, const TcPiece& x, 
         }
     }
 }
-// The same with the rows that were taken out of the product added; out of line
-// so that its stack does not weigh on the ordinary way.
-template <int D, bool F8>
-__device__ __noinline__ void tc_write_slow(const TreeParams& p, TcPiece x, TcOut o, uint32_t tA,
-                                           int col0, int col1, const uint32_t* bad) {
-    tc_write<D, F8, true>(p, x, o, tA, col0, col1, bad);
+
+// Eight bf16 values; eight E4M3 ones.
+__device__ __forceinline__ void tc_values(uint4 v, float (&f)[8]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16lo_to_f32(u[i]);
+        f[2 * i + 1] = bf16hi_to_f32(u[i]);
+    }
+}
+__device__ __forceinline__ void tc_values(uint32_t a, uint32_t b, float (&f)[8]) {
+    uint32_t h[4];
+    tc_e4m3x4(a, h[0], h[1]);
+    tc_e4m3x4(b, h[2], h[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = tc_f16x2_f32(h[i]);
+        f[2 * i] = x.x;
+        f[2 * i + 1] = x.y;
+    }
+}
+
+// The same with the keys whose V rows were taken out of the product: O scaled (and the
+// streams' added), then those keys that the row sees, with their scores computed anew in
+// fp32 from the row of Q in shared memory.  Rare, so out of line.
+template <int D, bool F8, bool ONE>
+__device__ __noinline__ void tc_write_apart(const TreeParams& p, TcPiece x, TcOut o, uint32_t tA, int col0, int col1,
+                                            const uint32_t* bad, const TcBars* bars, int tile) {
+    const int me = threadIdx.x & 127;
+    const uint32_t q = smem_u32(bars) - TcCfg<D, F8, ONE>::kBar + tile * TcCfg<D, F8, ONE>::kTile + me * 128;
+    const float c = fmaxf(F8 ? bars->qs[tile][me] : p.c, 1e-37f);
+#pragma unroll 1
+    for (int cc = col0; cc < col1; cc += 16) {
+        uint32_t a[16], b[16];
+        tc_ld16(tA + cc, a);
+        if (o.two) tc_ld16(tA + 128 + cc, b);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v = __uint_as_float(a[i]) * o.inv0;
+            if (o.two) v = fmaf(__uint_as_float(b[i]), o.inv1, v);
+            a[i] = __float_as_uint(v);
+        }
+        tmem_st16(tA + cc, a);
+    }
+    tmem_wait_st();
+    o.inv0 = 1.0f;
+    o.two = false;
+    const int key0 = (x.w.k0 + x.first_special()) * kTcKeys;
+    const int end = min(x.w.k1 * kTcKeys, x.w.keys);
+#pragma unroll 1
+    for (int key = key0; key < end; ++key) {
+        const int i = key - key0;
+        if (!(*((const volatile uint32_t*)bad + (i >> 5)) >> (i & 31) & 1u)) continue;
+        const bool sees = key < x.prefix || tree_sees(p, x.w.b, o.tok, key - x.prefix);
+        if (!__any_sync(0xFFFFFFFFu, sees)) continue;
+        int off;
+        const int page = tree_page(p, x.w.b, key, x.w.keys, off);
+        if (page < 0) continue;  // (zeros)
+        const long long row = (((long long)page * p.page_size + off) * p.Hkv + x.w.h) * p.dh;
+        const uint8_t* k = p.k_pages + row * (F8 ? 1 : 2);
+        const uint8_t* v = p.v_pages + row * (F8 ? 1 : 2);
+        float s = 0.f, vd = 1.f;
+        if constexpr (F8) {
+            const long long ds = ((long long)page * p.Hkv + x.w.h) * p.page_size + off;
+#pragma unroll 1
+            for (int ch = 0; ch < p.dh / 16; ++ch) {
+                const uint32_t at = q + ((ch ^ (me & 7)) << 4);
+                const uint4 a = tc_lds128(at), b = tc_lds128(at + 16384);
+                const uint4 kc = __ldg(reinterpret_cast<const uint4*>(k) + ch);
+                const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+                const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w};
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    float fa[8], fb[8], fk[8];
+                    tc_values(aw[2 * g], aw[2 * g + 1], fa);
+                    tc_values(bw[2 * g], bw[2 * g + 1], fb);
+                    tc_values(kw[2 * g], kw[2 * g + 1], fk);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s = fmaf(fa[e] + fb[e], fk[e], s);
+                }
+            }
+            s *= __ldg(p.k_descale + ds);
+            vd = __ldg(p.v_descale + ds);
+        } else {
+#pragma unroll 1
+            for (int ch = 0; ch < p.dh / 8; ++ch) {
+                float fq[8], fk[8];
+                tc_values(tc_lds128(q + (ch >> 3) * 16384 + (((ch & 7) ^ (me & 7)) << 4)), fq);
+                tc_values(__ldg(reinterpret_cast<const uint4*>(k) + ch), fk);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s = fmaf(fq[e], fk[e], s);
+            }
+        }
+        const float w = ex2(s * c - o.m + kTcLift<F8>) * o.inv;
+#pragma unroll 1
+        for (int cc = col0; cc < col1; cc += 16) {
+            uint32_t a[16];
+            tc_ld16(tA + cc, a);
+            float f[2][8] = {};
+            if constexpr (F8) {
+                const uint4 vc = __ldg(reinterpret_cast<const uint4*>(v + cc));
+                tc_values(vc.x, vc.y, f[0]);
+                tc_values(vc.z, vc.w, f[1]);
+            } else {
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    if (cc + 8 * g < p.dh) tc_values(__ldg(reinterpret_cast<const uint4*>(v + 2 * (cc + 8 * g))), f[g]);
+            }
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (sees) a[e] = __float_as_uint(fmaf(w, f[e >> 3][e & 7] * vd, __uint_as_float(a[e])));
+            tmem_st16(tA + cc, a);
+        }
+        tmem_wait_st();
+    }
+    tc_write(p, x, o, tA, col0, col1);
 }
 
 template <int D, bool F8, bool ONE>
@@ -1343,8 +1418,8 @@ __device__ void tc_softmax(int t, int wq, int lane, uint8_t* smem, TcBars* bars,
             o.tok = my.tok;
             o.bht = my.bht;
             o.place = (size_t)blockIdx.x * 2 + (piece == 0 ? 0 : 1);
-            if (any_bad) tc_write_slow<D, F8>(p, x, o, tA, col0, col1, bad);
-            else tc_write<D, F8, false>(p, x, o, tA, col0, col1, bad);
+            if (any_bad) tc_write_apart<D, F8, ONE>(p, x, o, tA, col0, col1, bad, bars, x.pair ? t : 0);
+            else tc_write(p, x, o, tA, col0, col1);
             if (o.live && (x.pair || t == 0)) {
                 const float lse2 = lx == 0.f ? -INFINITY : m - kTcLift<F8> + log2f(lx);
                 if (!x.w.whole) p.ws_lse[o.place * kTcRows + my.row] = lse2;
