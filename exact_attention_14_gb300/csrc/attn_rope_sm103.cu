@@ -13,8 +13,12 @@
 // 32-bit position: no range reduction and no loss far into a context.  Its top
 // 32 bits give cos and sin through sincospif.
 //
-// Bound: HBM (each element is read and written once): 671 MB in 105.4 us, 6370 GB/s,
-// 94% of a plain copy's rate; a single token's call is a launch, 3 us on the GPU.  A thread keeps the
+// Bound: HBM (each element is read and written once): 671 MB in 108 us, 6210 GB/s,
+// 92% of a plain copy's rate, call after call on changing inputs; a single token's call is
+// a launch, 3 us on the GPU.  Half pairs whose rotary_dim / 2 is no multiple of a chunk go
+// an element at a time (kHalfScalar), since a chunk's partners lie at other alignments:
+// the same 671 MB in 222 us (rotary_dim 40) to 248 us (30), fp32's 1342 MB in 246 us (34).
+// A thread keeps the
 // cos / sin of its 8 pairs of one token in registers and walks over heads, so
 // the angles (about 40 instructions a pair) are shared by all heads it walks.
 // A row is a list of jobs, two chunks of 16 bytes each: the chunks of a half and
@@ -306,8 +310,8 @@ attn_status_t launch_rope(const void* q, const void* k, void* q_out, void* k_out
     p.heads = Hq + (k ? Hkv : 0);
     // Up to 8 heads to a thread (their angles are computed once), fewer where that
     // leaves less than 1024 threads for every SM: a call of few tokens spreads over
-    // the heads instead.  (40 heads, 32768 tokens, 671 MB: all heads on one thread
-    // 123 us, 16 heads 106.5, 8 heads 105.4, 4 heads 109.)
+    // the heads instead.  (40 heads, 32768 tokens, 671 MB, replayed in a graph: all heads on
+    // one thread 123 us, 16 heads 106.5, 8 heads 105.4, 4 heads 109.)
     const long long per_head = p.tokens * p.units;
     long long hpt = per_head * p.heads / ((long long)dev.num_sms * 1024);
     hpt = hpt < 1 ? 1 : (hpt > 8 ? 8 : hpt);

@@ -15,11 +15,13 @@
 // pairs of consumer warps take the tiles in turn, 32 keys a warp, each with its
 // own online softmax (base 2), and the four are merged through shared memory at
 // the end of a piece.  Bound: HBM (each cached byte is read once per row tile).
-// One token, 16 sequences of 1024..32768 keys: bf16, d = 128, 8 heads 6368 GB/s;
-// E4M3, d = 128, 8 heads 5251 GB/s (104 us with the merge, 570 MB), where the codes'
-// conversion (cvt, 64 lanes a clock and SM) and the MMAs take about as long as the
-// copies; E4M3, d = 256, 4 heads 5560 GB/s.  (32 keys a warp: 16 were 128 -> 110 us
-// slower in E4M3, every shuffle and wait being paid twice as often.)
+// One token, 16 sequences of 1024..32768 keys, calls on changing inputs, with the merge:
+// bf16, d = 128, 8 heads 178 us, 6230 GB/s; E4M3, d = 128, 8 heads 107..116 us (cards
+// differ), 4950..5350 GB/s, where the codes' conversion (cvt, 64 lanes a clock and SM) and
+// the MMAs take about as long as the copies; E4M3, d = 256, 4 heads 108 us, 5200 GB/s;
+// d = 64 in E4M3 takes a 128-column tile half of zeros: 98 us, 3000 GB/s.  (32 keys a
+// warp: with 16 E4M3 took 128 us where this took 110, every shuffle and wait being paid
+// twice as often.)
 //
 // The products are transposed, S^T = K Q^T and O^T = V^T P^T: keys and columns
 // are the 16 rows of an MMA and the query rows its 8 columns, so up to 8 query
@@ -34,7 +36,9 @@
 // vd_j / F in fp16, F the power of two above the largest vd so far of the keys that
 // the row sees (O is rescaled when F grows), times 2^15: weights times descales
 // down to 2^-29 of the largest descale keep fp16's 11 bits, smaller ones are off by at
-// most 2^-40 of F.  bf16 caches use bf16 P, as the library's decode does.
+// most 2^-40 of F.  Each row has its own F, so that a V row which it does not see costs
+// it no bits (one F for a warp's rows: 148 us where this takes 154 at 16 rows, the same
+// at 8).  bf16 caches use bf16 P, as the library's decode does.
 //
 // Masked places: scores are selected, never added to.  V rows past the
 // sequence are zeroed in shared memory; a drafted token's V row that holds a
@@ -323,7 +327,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                     }
             } else {
                 // fp16, each row scaled by a power of two that puts its largest value
-                // in [2^14, 2^15): exact but for values below 2^-38 of it
+                // in [2^14, 2^15): exact down to 2^-31 of it (8 bits above 2^-24), and off by
+                // at most half a step, 2^-39 of it, below that
                 float mx = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
@@ -967,7 +972,10 @@ attn_status_t launch_tree_merge(const TreeParams& p, int num_sms, cudaStream_t s
 // of 128 rows costs the same however few are live.  16 sequences of up to 32768 keys,
 // 8 KV heads, this kernel / that one in us: bf16, d = 128, 8 rows 173 / 180, 12 rows
 // 196 / 182, 16 rows 200 / 182, 20 rows 354 (two row tiles) / 186; bf16, d = 64, 16
-// rows 109 / 129; E4M3, d = 128, 16 rows 145 / 195, 20 rows 262 / 196.
+// rows 114 / 136, 20 rows 195 / 136; E4M3, d = 128, 12 rows 153 / 204, 16 rows 156 / 205,
+// 20 rows 282 / 205; E4M3, d = 64, 16 rows 154 / 205, 20 rows 279 / 205.  That kernel has
+// no columns above 128: with d > 128 every 16 rows read the cache again here (bf16,
+// d = 256, 4 KV heads: 8 rows 177 us, 32 rows 439, 256 rows 3300; E4M3 108, 340, 2600).
 static bool tree_on_tc(int d, bool f8, int rows) {
     return d <= 128 && rows > (f8 || d <= 64 ? kMaxRows : kMaxRows / 2);
 }

@@ -36,9 +36,11 @@
 // by a 128-key tile: the four products take 2150 cycles of an SM's tensor cores, the
 // tile (64 KiB in bf16) 2785 cycles of its share of HBM; measured, 16 sequences of
 // 1024..32768 keys, 8 KV heads: bf16 about 3500 cycles (64 drafts, 4 heads a group,
-// 245 us with the merge, 67% of the floor), E4M3 4600 (300 us), where S's
-// multiplication with the descales (40 us) and fp16 packing lengthen the softmax.
-// 64 rows, bf16: 183 us, 90% of HBM's rate; E4M3 196 us.
+// 250..262 us as a call, with the merge, 64% of the floor), E4M3 4600 (322 us on some
+// cards, 347 on others), where S's multiplication with the descales (40 us) and fp16
+// packing lengthen the softmax.  64 rows, bf16: 185..191 us, 87% of HBM's rate; E4M3
+// 204 us, where both streams compute and convert for 128 rows.  d = 64 in E4M3 takes a
+// 128-column tile half of zeros: 64 drafts 340 us.
 #include <climits>
 #include <cmath>
 #include <cstdint>

@@ -7,7 +7,10 @@
 // (b, then h, then rt) and CTA c of n takes the units [c * total / n,
 // (c + 1) * total / n): every CTA has the same number of key tiles to read,
 // whatever the lengths are, and an item is cut only where a CTA's range ends.
-// The lengths live on the device, so each CTA works the ranges out itself.
+// The lengths live on the device, so each CTA works the ranges out itself.  An item
+// has all key tiles of its sequence, those that no row of its tile sees too: a chain of
+// 1024 tokens (4 sequences, 32 / 8 heads of 128, bf16) takes 217 us without a prefix and
+// 608 us after 8192 keys, where its visible products need 18 and 307 us.
 // A piece that is not a whole item leaves a partial result in the workspace:
 // a CTA has at most two such pieces, its first (place 2c) and its last
 // (2c + 1), so the workspace does not grow with the batch.  The merge kernel
