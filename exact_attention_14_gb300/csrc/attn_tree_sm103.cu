@@ -37,8 +37,8 @@
 // the row sees (O is rescaled when F grows), times 2^15: weights times descales
 // down to 2^-29 of the largest descale keep fp16's 11 bits, smaller ones are off by at
 // most 2^-40 of F.  Each row has its own F, so that a V row which it does not see costs
-// it no bits (one F for a warp's rows: 148 us where this takes 154 at 16 rows, the same
-// at 8).  bf16 caches use bf16 P, as the library's decode does.
+// it no bits (one F for a warp's rows took 1% less; with F and the maximum raised in one
+// branch 16 rows took 154 us instead of 149).  bf16 caches use bf16 P, as the library's decode does.
 //
 // Masked places: scores are selected, never added to.  V rows past the
 // sequence are zeroed in shared memory; a drafted token's V row that holds a
@@ -492,44 +492,46 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
                         mx[nt][r] = x;
                         moved |= x > m[nt][r];
                     }
-                // (E4M3) the largest descale of V of this lane's keys that a row sees
-                auto top_of = [&](int nt, int r) {
-                    float top = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        top = fmaxf(top, plain || sf[i >> 1][nt][2 * (i & 1) + r] != -INFINITY ? fabsf(wv[i]) : 0.f);
-                    return top;
-                };
                 if constexpr (F8) {
+                    int least = min(fexp[0][0], fexp[0][1]);
+                    if constexpr (NT == 2) least = min(least, min(fexp[1][0], fexp[1][1]));
+                    const float top_here = fmaxf(fmaxf(fabsf(wv[0]), fabsf(wv[1])), fmaxf(fabsf(wv[2]), fabsf(wv[3])));
+                    if (__any_sync(0xFFFFFFFFu, top_here > pow2i(least))) {  // (2^128: infinite, above every finite descale)
+                        // ---- F: the power of two above the largest descale of V of the keys that a row sees
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r)  // (2^128: infinite, above every finite descale)
-                            moved |= top_of(nt, r) > pow2i(fexp[nt][r]);
-                }
-                if (__any_sync(0xFFFFFFFFu, moved)) {
+                            for (int r = 0; r < 2; ++r) {
+                                float top = 0.f;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            float grow = 1.f;  // E4M3: F_old / F_new
-                            if constexpr (F8) {
-                                float top = top_of(nt, r);
+                                for (int i = 0; i < 4; ++i)
+                                    if (sf[i >> 1][nt][2 * (i & 1) + r] != -INFINITY) top = fmaxf(top, fabsf(wv[i]));
 #pragma unroll
                                 for (int off = 4; off < 32; off <<= 1)
                                     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
                                 const int old = fexp[nt][r];
                                 // 2^need > top
                                 const int need = max(min((int)(__float_as_uint(top) >> 23) - 126, 128), old);
-                                grow = old - need < -126 ? 0.f : pow2i(old - need);
+                                const float grow = old - need < -126 ? 0.f : pow2i(old - need);  // F_old / F_new
                                 fexp[nt][r] = need;
+#pragma unroll
+                                for (int i = 0; i < D / 16; ++i) {
+                                    acc[i][nt][r] *= grow;
+                                    acc[i][nt][2 + r] *= grow;
+                                }
                             }
+                    }
+                }
+                if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
                             const float mn = fmaxf(m[nt][r], mx[nt][r]);
-                            float al = ex2(m[nt][r] - (mn == -INFINITY ? 0.f : mn));  // (no key yet: 0)
+                            const float al = ex2(m[nt][r] - (mn == -INFINITY ? 0.f : mn));  // (no key yet: 0)
                             m[nt][r] = mn;
                             xs[nt][r] *= al;
                             l[nt][r] *= al;
-                            al *= grow;
 #pragma unroll
                             for (int i = 0; i < D / 16; ++i) {
                                 acc[i][nt][r] *= al;
@@ -972,10 +974,10 @@ attn_status_t launch_tree_merge(const TreeParams& p, int num_sms, cudaStream_t s
 // of 128 rows costs the same however few are live.  16 sequences of up to 32768 keys,
 // 8 KV heads, this kernel / that one in us: bf16, d = 128, 8 rows 173 / 180, 12 rows
 // 196 / 182, 16 rows 200 / 182, 20 rows 354 (two row tiles) / 186; bf16, d = 64, 16
-// rows 114 / 136, 20 rows 195 / 136; E4M3, d = 128, 12 rows 153 / 204, 16 rows 156 / 205,
-// 20 rows 282 / 205; E4M3, d = 64, 16 rows 154 / 205, 20 rows 279 / 205.  That kernel has
+// rows 114 / 136, 20 rows 195 / 136; E4M3, d = 128, 12 rows 148 / 204, 16 rows 149 / 205,
+// 20 rows 269 / 205; E4M3, d = 64, 16 rows 148 / 205, 20 rows 266 / 205.  That kernel has
 // no columns above 128: with d > 128 every 16 rows read the cache again here (bf16,
-// d = 256, 4 KV heads: 8 rows 177 us, 32 rows 439, 256 rows 3300; E4M3 108, 340, 2600).
+// d = 256, 4 KV heads: 8 rows 177 us, 32 rows 439, 256 rows 3300; E4M3 108, 335, 2530).
 static bool tree_on_tc(int d, bool f8, int rows) {
     return d <= 128 && rows > (f8 || d <= 64 ? kMaxRows : kMaxRows / 2);
 }

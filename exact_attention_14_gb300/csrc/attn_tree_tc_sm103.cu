@@ -40,7 +40,7 @@
 // cards, 347 on others), where S's multiplication with the descales (40 us) and fp16
 // packing lengthen the softmax.  64 rows, bf16: 185..191 us, 87% of HBM's rate; E4M3
 // 204 us, where both streams compute and convert for 128 rows.  d = 64 in E4M3 takes a
-// 128-column tile half of zeros: 64 drafts 340 us.
+// 128-column tile half of zeros: 64 drafts 321..340 us.
 #include <climits>
 #include <cmath>
 #include <cstdint>
