@@ -1,7 +1,8 @@
 """GB300 (sm_103a) exact attention: fused forward (dense and packed
-variable-length), backward, and split-KV decode (contiguous or paged cache); and
-around it rotary positions, writing and reading the paged cache (bf16 or E4M3),
-and attention of a tree of drafted tokens over that cache.
+variable-length), backward, and split-KV decode (contiguous or paged cache), each
+also with a learned relative position bias; and around it rotary positions, writing
+and reading the paged cache (bf16 or E4M3), its block tables and slots built from
+the requests' lengths, and attention of a tree of drafted tokens over that cache.
 
 Thin ctypes binding over the C ABI in ``include/attn.h`` (library
 ``libgb300_attn.so`` built in-tree by ``_build.build()``).  The functions here
@@ -32,6 +33,11 @@ __all__ = [
     "attn_rope", "rope", "rope_backward", "attn_rope_frequencies", "rope_frequencies",
     "attn_cache_write", "attn_cache_read", "cache_read", "attn_decode_tree",
     "attn_decode_tree_workspace_size", "decode_tree", "tree_mask_words",
+    "attn_bias_buckets", "bias_buckets", "attn_fwd_bias", "forward_bias", "attn_fwd_varlen_bias",
+    "forward_varlen_bias", "attn_bwd_bias", "attn_bwd_bias_workspace_size", "backward_bias",
+    "attn_bwd_varlen_bias", "attn_bwd_varlen_bias_workspace_size", "backward_varlen_bias",
+    "attn_decode_paged_bias", "decode_paged_bias",
+    "attn_page_pool_init", "page_pool", "attn_pages_extend", "pages_extend", "attn_pages_trim", "pages_trim",
 ]
 
 ATTN_OK = 0
@@ -111,6 +117,22 @@ SIGNATURES = {
     "attn_decode_tree_workspace_size": (_c_sz, [_c_int] * 8),
     "attn_decode_tree": (_c_int, [_vp] * 11 + [_c_int] * 4 + [_c_ll] + [_c_int] * 3 +
                          [_c_f, _c_int, _vp, _c_sz, _c_int, _vp]),
+    "attn_bias_buckets": (_c_int, [_c_int] * 3 + [ctypes.POINTER(_c_int), _c_int] + [ctypes.POINTER(_c_int)] * 2),
+    "attn_fwd_bias": (_c_int, [_vp] * 4 + [_c_int, _vp] + [_c_int] * 3 + [_vp] * 2 + [_c_int] * 7 +
+                      [_c_f, _c_int, _vp, _c_sz, _vp]),
+    "attn_fwd_varlen_bias": (_c_int, [_vp] * 4 + [_c_int, _vp] + [_c_int] * 3 + [_vp] * 4 + [_c_int] * 9 +
+                             [_c_f, _c_int, _vp]),
+    "attn_bwd_bias_workspace_size": (_c_sz, [_c_int] * 7),
+    "attn_bwd_bias": (_c_int, [_vp] * 7 + [_c_int, _vp] + [_c_int] * 3 + [_vp] * 4 + [_c_int] * 7 +
+                      [_c_f, _c_int, _c_int, _vp, _c_sz, _vp]),
+    "attn_bwd_varlen_bias_workspace_size": (_c_sz, [_c_int] * 7),
+    "attn_bwd_varlen_bias": (_c_int, [_vp] * 7 + [_c_int, _vp] + [_c_int] * 3 + [_vp] * 6 + [_c_int] * 9 +
+                             [_c_f, _c_int, _c_int, _vp, _c_sz, _vp]),
+    "attn_decode_paged_bias": (_c_int, [_vp] * 6 + [_c_int, _vp] + [_c_int] * 3 + [_vp] * 2 + [_c_int] * 3 +
+                               [_c_ll] + [_c_int] * 3 + [_c_f, _c_int, _vp, _c_sz, _c_int, _vp]),
+    "attn_page_pool_init": (_c_int, [_vp, _c_int, _vp]),
+    "attn_pages_extend": (_c_int, [_vp, _c_int] + [_vp] * 7 + [_c_int] * 5 + [_vp]),
+    "attn_pages_trim": (_c_int, [_vp, _c_int] + [_vp] * 3 + [_c_int] * 3 + [_vp]),
     "attn_fwd_split_plan": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
                                      _c_int, ctypes.POINTER(ctypes.c_int),
                                      ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]),
@@ -1235,3 +1257,438 @@ def decode_tree(q, k_pages, v_pages, block_table, seqlens, tree_mask=None, q_len
         _used_here(q.device, o, lse)
     return _tree_call(q, k_pages, v_pages, block_table, seqlens, o, lse, tree_mask, q_lens, k_descale,
                       v_descale, scale, None, stream)
+
+
+# ------------------------- learned relative position bias -------------------------
+def attn_bias_buckets(num_buckets: int, max_distance: int, bidirectional: bool = False):
+    """([bucket of each distance from first on], first) as Python ints: half of a
+    direction's buckets hold one distance each, the rest grow geometrically up to
+    max_distance; bidirectional gives each direction half of the buckets."""
+    first, span = _c_int(), _c_int()
+    args = (int(num_buckets), int(max_distance), int(bool(bidirectional)))
+    at = (ctypes.byref(first), ctypes.byref(span))
+    _check(load().attn_bias_buckets(*args, None, 0, *at), "attn_bias_buckets")
+    out = (_c_int * span.value)()
+    _check(load().attn_bias_buckets(*args, out, span.value, *at), "attn_bias_buckets")
+    return list(out), first.value
+
+
+def bias_buckets(num_buckets: int, max_distance: int, bidirectional: bool = False, *, device="cuda"):
+    """(buckets int32 tensor [span] on ``device``, first) for the calls with a
+    bias; see attn_bias_buckets.  Any other map of distances to buckets works as
+    well: buckets[i] is the one of distance first + i (key - query), and farther
+    distances have those of its ends."""
+    buckets, first = attn_bias_buckets(num_buckets, max_distance, bidirectional)
+    return torch.tensor(buckets, dtype=torch.int32, device=device), first
+
+
+def _bias(table, buckets, first, Hq):
+    """The bias arguments of a call: (table, type, buckets, first, span, num_buckets)."""
+    _tensor(table, (torch.bfloat16, torch.float32), "table")
+    _need(table, table.dtype, "table")
+    _need(buckets, torch.int32, "buckets")
+    if table.ndim != 2 or table.shape[1] != Hq:
+        raise ValueError("table must be [num_buckets, Hq]")
+    if buckets.ndim != 1:
+        raise ValueError("buckets must be [span]")
+    return (table.data_ptr(), ATTN_OUT_F32 if table.dtype == torch.float32 else ATTN_OUT_BF16,
+            buckets.data_ptr(), int(first), buckets.shape[0], table.shape[0])
+
+
+def _out_type(t, name):
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be bfloat16 or float32")
+    _need(t, t.dtype, name)
+    return ATTN_OUT_F32 if t.dtype == torch.float32 else ATTN_OUT_BF16
+
+
+def _dense_shape(q, k, v):
+    """(B, Hq, Hkv, Nq, Nk, d) of a dense problem's inputs."""
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _need(t, torch.bfloat16, n)
+        if t.ndim != 4:
+            raise ValueError(f"{n} must be [B, H, N, d]")
+    B, Hq, Nq, d = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    if k.shape != (B, Hkv, Nk, d) or v.shape != k.shape:
+        raise ValueError("k/v shape mismatch")
+    return B, Hq, Hkv, Nq, Nk, d
+
+
+def _packed_shape(q, k, v, cu_seqlens_q, cu_seqlens_k):
+    """(B, Hq, Hkv, total_q, total_k, d) of a packed batch's inputs."""
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _need(t, torch.bfloat16, n)
+        if t.ndim != 3:
+            raise ValueError(f"{n} must be [total, H, d]")
+    for t, n in ((cu_seqlens_q, "cu_seqlens_q"), (cu_seqlens_k, "cu_seqlens_k")):
+        _need(t, torch.int32, n)
+    total_q, Hq, d = q.shape
+    total_k, Hkv = k.shape[0], k.shape[1]
+    if k.shape != (total_k, Hkv, d) or v.shape != k.shape:
+        raise ValueError("k/v shape mismatch")
+    B = cu_seqlens_q.numel() - 1
+    if cu_seqlens_q.shape != (B + 1,) or cu_seqlens_k.shape != (B + 1,) or B < 1:
+        raise ValueError("cu_seqlens_q / cu_seqlens_k must both have B + 1 entries")
+    return B, Hq, Hkv, total_q, total_k, d
+
+
+def _out_and_lse(q, o, lse, lse_shape):
+    """Checks a forward's outputs; O's type."""
+    odt = _out_type(o, "o")
+    if o.shape != q.shape:
+        raise ValueError("o shape mismatch")
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        if lse.shape != lse_shape:
+            raise ValueError("lse shape mismatch")
+    return odt
+
+
+def attn_fwd_bias(q, k, v, table, buckets, first: int, o, lse=None, *, causal: bool = False,
+                  scale: float | None = None, workspace=None, stream=None):
+    """attn_fwd with a learned relative position bias added to the scaled scores:
+    table [num_buckets,Hq] fp32 or bf16, buckets int32 [span] on the device and
+    first as bias_buckets makes them: query i, key j and head h get
+    table[buckets[min(max(j - (i + Nk - Nq) - first, 0), span - 1)], h].  d <= 128."""
+    shape = _dense_shape(q, k, v)
+    B, Hq, Hkv, Nq, Nk, d = shape
+    odt = _out_and_lse(q, o, lse, (B, Hq, Nq))
+    bias = _bias(table, buckets, first, Hq)
+    dev = _one_device(q, k, v, o, lse, table, buckets, workspace)
+    lib = load()
+    with _on(dev):
+        need = lib.attn_fwd_workspace_size(*shape, int(bool(causal))) if workspace is None else 0
+        if need > 0:
+            with _made_on(stream, dev):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_ptr, ws_bytes = _workspace(workspace)
+        rc = lib.attn_fwd_bias(q.data_ptr(), k.data_ptr(), v.data_ptr(), *bias, o.data_ptr(), _at(lse), *shape,
+                               int(bool(causal)), d ** -0.5 if scale is None else scale, odt, ws_ptr, ws_bytes,
+                               _stream_ptr(stream))
+    _check(rc, "attn_fwd_bias")
+    return o, lse
+
+
+def forward_bias(q, k, v, table, buckets, first: int, *, causal: bool = False, scale: float | None = None,
+                 out_dtype=None, return_lse: bool = True, stream=None):
+    """Allocate O (and LSE) with torch and run attn_fwd_bias."""
+    with _made_on(stream, q.device):
+        o = torch.empty(q.shape, dtype=out_dtype or torch.bfloat16, device=q.device)
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if return_lse else None
+    if stream is not None:
+        _used_here(q.device, o, lse)
+    return attn_fwd_bias(q, k, v, table, buckets, first, o, lse, causal=causal, scale=scale, stream=stream)
+
+
+def attn_fwd_varlen_bias(q, k, v, table, buckets, first: int, o, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
+                         max_seqlen_k: int, lse=None, *, causal: bool = False, scale: float | None = None,
+                         stream=None):
+    """attn_fwd_varlen with a relative position bias (attn_fwd_bias; distances are
+    those within a sequence)."""
+    shape = _packed_shape(q, k, v, cu_seqlens_q, cu_seqlens_k)
+    d = shape[-1]
+    odt = _out_and_lse(q, o, lse, (q.shape[1], q.shape[0]))
+    bias = _bias(table, buckets, first, q.shape[1])
+    with _on(_one_device(q, k, v, o, lse, table, buckets, cu_seqlens_q, cu_seqlens_k)):
+        rc = load().attn_fwd_varlen_bias(q.data_ptr(), k.data_ptr(), v.data_ptr(), *bias, o.data_ptr(), _at(lse),
+                                         cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), *shape[:5],
+                                         int(max_seqlen_q), int(max_seqlen_k), d, int(bool(causal)),
+                                         d ** -0.5 if scale is None else scale, odt, _stream_ptr(stream))
+    _check(rc, "attn_fwd_varlen_bias")
+    return o, lse
+
+
+def forward_varlen_bias(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max_seqlen_k: int, table,
+                        buckets, first: int, *, causal: bool = False, scale: float | None = None,
+                        out_dtype=None, return_lse: bool = True, stream=None):
+    """Allocate O (and LSE [Hq, total_q]) with torch and run attn_fwd_varlen_bias."""
+    with _made_on(stream, q.device):
+        o = torch.empty(q.shape, dtype=out_dtype or torch.bfloat16, device=q.device)
+        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device) if return_lse else None
+    if stream is not None:
+        _used_here(q.device, o, lse)
+    return attn_fwd_varlen_bias(q, k, v, table, buckets, first, o, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                                max_seqlen_k, lse, causal=causal, scale=scale, stream=stream)
+
+
+def attn_bwd_bias_workspace_size(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int, span: int) -> int:
+    return int(load().attn_bwd_bias_workspace_size(B, Hq, Hkv, Nq, Nk, d, span))
+
+
+def attn_bwd_varlen_bias_workspace_size(B: int, Hq: int, Hkv: int, total_q: int, max_seqlen_k: int, d: int,
+                                        span: int) -> int:
+    return int(load().attn_bwd_varlen_bias_workspace_size(B, Hq, Hkv, total_q, max_seqlen_k, d, span))
+
+
+def _grads(q, k, v, o, dout, lse, dq, dk, dv, table, dtable, lse_shape):
+    """Checks a backward's further arrays; the types of O and of the gradients."""
+    odt, gdt = _out_type(o, "o"), _out_type(dq, "dq")
+    _need(dout, torch.bfloat16, "dout")
+    _need(lse, torch.float32, "lse")
+    for t, n in ((dk, "dk"), (dv, "dv")):
+        _need(t, dq.dtype, n)
+    _need(dtable, torch.float32, "dtable")
+    if o.shape != q.shape or dout.shape != q.shape or dq.shape != q.shape:
+        raise ValueError("o/dout/dq shape mismatch")
+    if dk.shape != k.shape or dv.shape != v.shape:
+        raise ValueError("dk/dv shape mismatch")
+    if lse.shape != lse_shape:
+        raise ValueError("lse shape mismatch")
+    if dtable.shape != table.shape:
+        raise ValueError("dtable shape mismatch")
+    return odt, gdt
+
+
+def attn_bwd_bias(q, k, v, o, dout, lse, table, buckets, first: int, dq, dk, dv, dtable, *,
+                  causal: bool = False, scale: float | None = None, workspace=None, stream=None):
+    """The gradients of attn_fwd_bias into caller-provided arrays: attn_bwd's, and
+    dtable fp32 [num_buckets,Hq]; workspace: a CUDA tensor of at least
+    attn_bwd_bias_workspace_size(...) bytes, or None (then one is allocated with
+    torch).  Asynchronous."""
+    shape = _dense_shape(q, k, v)
+    B, Hq, Hkv, Nq, Nk, d = shape
+    bias = _bias(table, buckets, first, Hq)
+    odt, gdt = _grads(q, k, v, o, dout, lse, dq, dk, dv, table, dtable, (B, Hq, Nq))
+    dev = _one_device(q, k, v, o, dout, lse, table, buckets, dq, dk, dv, dtable, workspace)
+    lib = load()
+    with _on(dev):
+        if workspace is None:
+            with _made_on(stream, dev):
+                workspace = torch.empty(lib.attn_bwd_bias_workspace_size(*shape, buckets.shape[0]),
+                                        dtype=torch.uint8, device=dev)
+        ws_ptr, ws_bytes = _workspace(workspace)
+        rc = lib.attn_bwd_bias(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
+                               lse.data_ptr(), *bias, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                               dtable.data_ptr(), *shape, int(bool(causal)), d ** -0.5 if scale is None else scale,
+                               odt, gdt, ws_ptr, ws_bytes, _stream_ptr(stream))
+    _check(rc, "attn_bwd_bias")
+    return dq, dk, dv, dtable
+
+
+def _new_grads(q, k, v, table, grad_dtype, stream):
+    """dQ, dK, dV and the table's gradient, allocated where the call runs."""
+    with _made_on(stream, q.device):
+        grads = tuple(torch.empty(t.shape, dtype=grad_dtype or torch.bfloat16, device=q.device)
+                      for t in (q, k, v)) + (torch.empty(table.shape, dtype=torch.float32, device=q.device),)
+    if stream is not None:
+        _used_here(q.device, *grads)
+    return grads
+
+
+def backward_bias(q, k, v, o, dout, lse, table, buckets, first: int, *, causal: bool = False,
+                  scale: float | None = None, grad_dtype=None, stream=None):
+    """Allocate dQ, dK, dV, the table's gradient (fp32) and the workspace with
+    torch and run attn_bwd_bias.  Returns (dq, dk, dv, dtable)."""
+    return attn_bwd_bias(q, k, v, o, dout, lse, table, buckets, first,
+                         *_new_grads(q, k, v, table, grad_dtype, stream), causal=causal, scale=scale,
+                         stream=stream)
+
+
+def attn_bwd_varlen_bias(q, k, v, o, dout, lse, table, buckets, first: int, dq, dk, dv, dtable, cu_seqlens_q,
+                         cu_seqlens_k, max_seqlen_q: int, max_seqlen_k: int, *, causal: bool = False,
+                         scale: float | None = None, workspace=None, stream=None):
+    """The gradients of attn_fwd_varlen_bias into caller-provided arrays
+    (attn_bwd_varlen's, and dtable fp32 [num_buckets,Hq] summed over the
+    sequences); workspace as attn_bwd_varlen_bias_workspace_size.  Asynchronous."""
+    shape = _packed_shape(q, k, v, cu_seqlens_q, cu_seqlens_k)
+    B, Hq, Hkv, total_q, total_k, d = shape
+    bias = _bias(table, buckets, first, Hq)
+    odt, gdt = _grads(q, k, v, o, dout, lse, dq, dk, dv, table, dtable, (Hq, total_q))
+    dev = _one_device(q, k, v, o, dout, lse, table, buckets, dq, dk, dv, dtable, cu_seqlens_q, cu_seqlens_k,
+                      workspace)
+    lib = load()
+    with _on(dev):
+        if workspace is None:
+            with _made_on(stream, dev):
+                workspace = torch.empty(lib.attn_bwd_varlen_bias_workspace_size(B, Hq, Hkv, total_q,
+                                                                                int(max_seqlen_k), d,
+                                                                                buckets.shape[0]),
+                                        dtype=torch.uint8, device=dev)
+        ws_ptr, ws_bytes = _workspace(workspace)
+        rc = lib.attn_bwd_varlen_bias(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
+                                      lse.data_ptr(), *bias, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                      dtable.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
+                                      B, Hq, Hkv, total_q, total_k, int(max_seqlen_q), int(max_seqlen_k), d,
+                                      int(bool(causal)), d ** -0.5 if scale is None else scale, odt, gdt, ws_ptr,
+                                      ws_bytes, _stream_ptr(stream))
+    _check(rc, "attn_bwd_varlen_bias")
+    return dq, dk, dv, dtable
+
+
+def backward_varlen_bias(q, k, v, o, dout, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
+                         max_seqlen_k: int, table, buckets, first: int, *, causal: bool = False,
+                         scale: float | None = None, grad_dtype=None, stream=None):
+    """Allocate dQ, dK, dV, the table's gradient (fp32) and the workspace with
+    torch and run attn_bwd_varlen_bias.  Returns (dq, dk, dv, dtable)."""
+    return attn_bwd_varlen_bias(q, k, v, o, dout, lse, table, buckets, first,
+                                *_new_grads(q, k, v, table, grad_dtype, stream), cu_seqlens_q, cu_seqlens_k,
+                                max_seqlen_q, max_seqlen_k, causal=causal, scale=scale, stream=stream)
+
+
+def _decode_bias_call(q, k_pages, v_pages, block_table, seqlens, table, buckets, first, o, lse, scale, num_splits,
+                      workspace, stream):
+    """attn_decode_paged_bias once o and lse are known to be good."""
+    _need(q, torch.bfloat16, "q")
+    num_blocks, page_size, Hkv, d, kind = _check_pages(k_pages, v_pages, None, None)
+    if kind != ATTN_CACHE_BF16:
+        raise TypeError("k_pages and v_pages must be bfloat16")
+    _need(block_table, torch.int32, "block_table")
+    _need(seqlens, torch.int32, "seqlens")
+    if q.ndim != 4 or q.shape[2] != 1 or q.shape[3] != d:
+        raise ValueError("q / page shapes mismatch")
+    B, Hq = q.shape[:2]
+    if block_table.ndim != 2 or block_table.shape[0] != B or seqlens.shape != (B,):
+        raise ValueError("block_table must be [B, max_blocks] and seqlens [B]")
+    max_blocks = block_table.shape[1]
+    bias = _bias(table, buckets, first, Hq)
+    dev = _one_device(q, k_pages, v_pages, block_table, seqlens, o, lse, table, buckets, workspace)
+    lib = load()
+    with _on(dev):
+        if workspace is None:
+            need = lib.attn_decode_workspace_size(B, Hq, Hkv, max_blocks * page_size, d, num_splits)
+            with _made_on(stream, dev):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_ptr, ws_bytes = _workspace(workspace)
+        rc = lib.attn_decode_paged_bias(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                        block_table.data_ptr(), seqlens.data_ptr(), *bias, o.data_ptr(), _at(lse),
+                                        B, Hq, Hkv, num_blocks, page_size, max_blocks, d,
+                                        d ** -0.5 if scale is None else scale, num_splits, ws_ptr, ws_bytes,
+                                        ATTN_OUT_F32 if o.dtype == torch.float32 else ATTN_OUT_BF16,
+                                        _stream_ptr(stream))
+    _check(rc, "attn_decode_paged_bias")
+    return o, lse
+
+
+def attn_decode_paged_bias(q, k_pages, v_pages, block_table, seqlens, table, buckets, first: int, o, lse=None, *,
+                           scale: float | None = None, num_splits: int = 0, workspace=None, stream=None):
+    """attn_decode_paged with a relative position bias: the query token is the
+    sequence's last key, so a key t tokens back has distance -t (attn_fwd_bias).
+    workspace: at least attn_decode_workspace_size(...) bytes, or None (then one is
+    allocated with torch)."""
+    _out_and_lse(q, o, lse, q.shape[:3])
+    return _decode_bias_call(q, k_pages, v_pages, block_table, seqlens, table, buckets, first, o, lse, scale,
+                             num_splits, workspace, stream)
+
+
+def decode_paged_bias(q, k_pages, v_pages, block_table, seqlens, table, buckets, first: int, *,
+                      scale: float | None = None, num_splits: int = 0, out_dtype=None, stream=None):
+    """Allocate O and LSE with torch and run attn_decode_paged_bias."""
+    out_dtype = out_dtype or torch.bfloat16
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be bfloat16 or float32")
+    with _made_on(stream, q.device):
+        o = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    if stream is not None:
+        _used_here(q.device, o, lse)
+    return _decode_bias_call(q, k_pages, v_pages, block_table, seqlens, table, buckets, first, o, lse, scale,
+                             num_splits, None, stream)
+
+
+# ------------------------- the paged cache's tables -------------------------
+POOL_HEADER = 4   # words of a page pool before its stack of free pages
+
+
+def attn_page_pool_init(pool, *, stream=None):
+    """Fill a page pool (int32 [4 + num_blocks]) with every page of a cache."""
+    _need(pool, torch.int32, "pool")
+    if pool.ndim != 1 or pool.shape[0] <= POOL_HEADER:
+        raise ValueError("pool must be [4 + num_blocks]")
+    with _on(_one_device(pool)):
+        _check(load().attn_page_pool_init(pool.data_ptr(), pool.shape[0] - POOL_HEADER, _stream_ptr(stream)),
+               "attn_page_pool_init")
+    return pool
+
+
+def page_pool(num_blocks: int, *, device="cuda", stream=None):
+    """Allocate a pool of num_blocks free pages with torch (pool[0] is how many
+    there are); calls on one pool must be ordered."""
+    device = torch.device(device)
+    if device.index is None:
+        device = torch.device(device.type, torch.cuda.current_device())
+    with _made_on(stream, device):
+        pool = torch.empty(POOL_HEADER + num_blocks, dtype=torch.int32, device=device)
+    if stream is not None:
+        _used_here(device, pool)
+    return attn_page_pool_init(pool, stream=stream)
+
+
+def _page_tables(pool, block_table, seqlens, lens, name):
+    for t, n in ((pool, "pool"), (block_table, "block_table"), (seqlens, "seqlens"), (lens, name)):
+        _need(t, torch.int32, n)
+    if pool.ndim != 1 or pool.shape[0] <= POOL_HEADER:
+        raise ValueError("pool must be [4 + num_blocks]")
+    if block_table.ndim != 2 or seqlens.shape != block_table.shape[:1] or lens.shape != seqlens.shape:
+        raise ValueError(f"block_table must be [B, max_blocks], seqlens and {name} [B]")
+    return block_table.shape
+
+
+def attn_pages_extend(pool, block_table, seqlens, new_lens, page_size: int, slots, positions=None,
+                      cu_seqlens=None, granted=None, *, stream=None):
+    """Pages, slots and positions of new_lens int32 [B] more tokens of each request,
+    one launch: takes pages off the pool into block_table int32 [B,max_blocks] and
+    adds to seqlens int32 [B], both in place.
+
+    slots int64 and positions int32 (or None), alike [B,width] (a request's tokens
+    first in its row) or packed [total] (with cu_seqlens int32 [B+1], or None);
+    granted int32 [B] or None: new_lens, or 0 for requests the pool had no pages for
+    (those keep their length and have slots -1; see attn.h for which).  Asynchronous."""
+    B, max_blocks = _page_tables(pool, block_table, seqlens, new_lens, "new_lens")
+    _need(slots, torch.int64, "slots")
+    if slots.ndim == 2:
+        width, total = slots.shape[1], 0
+        if slots.shape[0] != B or width < 1 or cu_seqlens is not None:
+            raise ValueError("padded slots are [B, width], and cu_seqlens None")
+    elif slots.ndim == 1:
+        width, total = 0, slots.shape[0]
+    else:
+        raise ValueError("slots must be [B, width] or [total]")
+    for t, n, shape in ((positions, "positions", slots.shape), (cu_seqlens, "cu_seqlens", (B + 1,)),
+                        (granted, "granted", (B,))):
+        if t is not None:
+            _need(t, torch.int32, n)
+            if t.shape != shape:
+                raise ValueError(f"{n} shape mismatch")
+    with _on(_one_device(pool, block_table, seqlens, new_lens, slots, positions, cu_seqlens, granted)):
+        rc = load().attn_pages_extend(pool.data_ptr(), pool.shape[0] - POOL_HEADER, block_table.data_ptr(),
+                                      seqlens.data_ptr(), new_lens.data_ptr(), slots.data_ptr(), _at(positions),
+                                      _at(cu_seqlens), _at(granted), B, max_blocks, int(page_size), width, total,
+                                      _stream_ptr(stream))
+    _check(rc, "attn_pages_extend")
+
+
+def pages_extend(pool, block_table, seqlens, new_lens, page_size: int, *, width: int | None = None,
+                 total: int | None = None, stream=None):
+    """Allocate the outputs with torch and run attn_pages_extend.  width: padded
+    rows, returns (slots [B,width], positions [B,width], granted [B]); total (at least
+    the sum of new_lens): packed rows, returns (slots [total], positions [total],
+    cu_seqlens [B+1], granted [B])."""
+    if (width is None) == (total is None):
+        raise ValueError("give either width or total")
+    B, dev = seqlens.shape[0], seqlens.device
+    with _made_on(stream, dev):
+        shape = (B, width) if total is None else (total,)
+        slots = torch.empty(shape, dtype=torch.int64, device=dev)
+        positions = torch.empty(shape, dtype=torch.int32, device=dev)
+        cu = torch.empty(B + 1, dtype=torch.int32, device=dev) if width is None else None
+        granted = torch.empty(B, dtype=torch.int32, device=dev)
+    if stream is not None:
+        _used_here(dev, slots, positions, cu, granted)
+    attn_pages_extend(pool, block_table, seqlens, new_lens, page_size, slots, positions, cu, granted, stream=stream)
+    return (slots, positions, granted) if cu is None else (slots, positions, cu, granted)
+
+
+def attn_pages_trim(pool, block_table, seqlens, keep_lens, page_size: int, *, stream=None):
+    """Cut each request to its first keep_lens int32 [B] tokens (0: the request is
+    done; more than it has: all stay): its pages past them go back on the pool and
+    seqlens is set, in place.  Asynchronous."""
+    B, max_blocks = _page_tables(pool, block_table, seqlens, keep_lens, "keep_lens")
+    with _on(_one_device(pool, block_table, seqlens, keep_lens)):
+        rc = load().attn_pages_trim(pool.data_ptr(), pool.shape[0] - POOL_HEADER, block_table.data_ptr(),
+                                    seqlens.data_ptr(), keep_lens.data_ptr(), B, max_blocks, int(page_size),
+                                    _stream_ptr(stream))
+    _check(rc, "attn_pages_trim")
+
+
+pages_trim = attn_pages_trim   # (allocates nothing)

@@ -17,8 +17,8 @@ LIB = os.path.join(PKG, "libgb300_attn.so")
 
 SOURCES = ["attn_api.cu", "attn_fwd_sm103.cu", "attn_fwd_wide_sm103.cu", "attn_decode_sm103.cu",
            "attn_bwd_sm103.cu", "attn_fp8_sm103.cu", "attn_rope_sm103.cu", "attn_cache_sm103.cu",
-           "attn_tree_sm103.cu", "attn_tree_tc_sm103.cu"]
-HEADERS = ["ptx.cuh", "fwd_sched.h", "internal.h", "tree_plan.h"]
+           "attn_tree_sm103.cu", "attn_tree_tc_sm103.cu", "attn_pages_sm103.cu"]
+HEADERS = ["bias.cuh", "ptx.cuh", "fwd_sched.h", "internal.h", "tree_plan.h"]
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -11,6 +11,7 @@
 #include <numeric>
 #include <vector>
 
+#include "bias.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 #include "fwd_sched.h"
@@ -26,6 +27,7 @@ namespace {
 constexpr int kMaxDevices = 64;
 constexpr long long kMaxLen = 1ll << 24;
 constexpr long long kMaxHeads = 1ll << 24;
+constexpr int kMaxBiasSpan = 1 << 16;   // distances of a bias map, and buckets
 constexpr int kMaxPackedRows = 1 << 30;  // rows of a packed batch (ragged maps, fwd_sched.h)
 
 struct DevState {
@@ -354,6 +356,92 @@ attn_status_t check_tree_shape(int B, int Hq, int Hkv, int T, int max_blocks, in
     return ATTN_OK;
 }
 
+// Packed batches: the offsets' pointers and the row counts.
+attn_status_t check_varlen(const int* cu_q, const int* cu_k, int total_q, int total_k, int max_q, int max_k) {
+    if (!cu_q || !cu_k || !aligned4(cu_q) || !aligned4(cu_k)) return ATTN_ERR_INVALID_ARG;
+    if (total_q < 1 || total_k < 1 || total_q > kMaxPackedRows || total_k > kMaxPackedRows)
+        return ATTN_ERR_INVALID_ARG;
+    if (max_q > total_q || max_k > total_k) return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+// A backward's further arrays.
+attn_status_t check_grads(const void* dout, const float* lse, const void* dq, const void* dk, const void* dv,
+                          attn_out_dtype_t grad_dtype) {
+    if (!dout || !lse || !dq || !dk || !dv) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv)) return ATTN_ERR_INVALID_ARG;
+    if (grad_dtype != ATTN_OUT_BF16 && grad_dtype != ATTN_OUT_F32) return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+attn_status_t check_decode_paged(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
+                                 const int* seqlens, const void* o, const float* lse, int B, int Hq, int Hkv,
+                                 long long num_blocks, int page_size, int max_blocks, int d, float scale,
+                                 int num_splits, attn_out_dtype_t o_dtype) {
+    if (!q || !k_pages || !v_pages || !block_table || !seqlens || !o) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) ||
+        !aligned4(seqlens) || !aligned4(block_table))
+        return ATTN_ERR_INVALID_ARG;
+    if (lse && !aligned4(lse)) return ATTN_ERR_INVALID_ARG;
+    if (num_blocks < 1 || max_blocks < 1 || page_size < 64) return ATTN_ERR_INVALID_ARG;
+    if (page_size % 64 != 0) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)max_blocks * page_size > kMaxLen || num_blocks >= (1ll << 31))
+        return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_common(B, Hq, Hkv, d, scale, o_dtype);
+    if (st != ATTN_OK) return st;
+    return check_decode_shape(B, Hq, Hkv, max_blocks * page_size, d, num_splits);
+}
+
+attn_status_t check_page_tables(const int* pool, int num_blocks, const int* block_table, const int* seqlens,
+                                const int* lens, int B, int max_blocks, int page_size) {
+    if (!pool || !block_table || !seqlens || !lens) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(pool) || !aligned4(block_table) || !aligned4(seqlens) || !aligned4(lens))
+        return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || max_blocks < 1 || page_size < 1 || num_blocks < 1) return ATTN_ERR_INVALID_ARG;
+    if ((long long)max_blocks * page_size > kMaxLen) return ATTN_ERR_INVALID_ARG;
+    if (num_blocks > kMaxPackedRows) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+// A relative position bias: what the host can see of it (the buckets live on the
+// device, where each is checked as it is read), and the kernels' limits.
+attn_status_t check_bias(const void* table, attn_out_dtype_t table_dtype, const int* buckets, int first,
+                         int span, int num_buckets, int d) {
+    if (!table || !buckets || !aligned4(buckets)) return ATTN_ERR_INVALID_ARG;
+    if (table_dtype != ATTN_OUT_BF16 && table_dtype != ATTN_OUT_F32) return ATTN_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(table) % (table_dtype == ATTN_OUT_F32 ? 4 : 2) != 0) return ATTN_ERR_INVALID_ARG;
+    if (span < 1 || num_buckets < 1 || first < -kMaxLen || first > kMaxLen) return ATTN_ERR_INVALID_ARG;
+    if (span > kMaxBiasSpan || num_buckets > kMaxBiasSpan || !head_dim_supported(d)) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+BiasArgs bias_args(const void* table, attn_out_dtype_t table_dtype, const int* buckets, int first, int span,
+                   int num_buckets) {
+    return BiasArgs{table, buckets, first, span, num_buckets, table_dtype == ATTN_OUT_BF16};
+}
+
+// base^n and products of such, exactly: whether r^s e^k >= D^k e^s.
+bool bucket_reached(long long r, int s, long long e, int k, long long D) {
+    auto times = [](std::vector<uint32_t>& x, long long by, int n) {
+        for (; n > 0; --n) {
+            uint64_t carry = 0;
+            for (uint32_t& w : x) {
+                carry += (uint64_t)w * (uint64_t)by;
+                w = (uint32_t)carry;
+                carry >>= 32;
+            }
+            if (carry) x.push_back((uint32_t)carry);
+        }
+    };
+    std::vector<uint32_t> a{1}, b{1};
+    times(a, r, s);
+    times(a, e, k);
+    times(b, D, k);
+    times(b, e, s);
+    if (a.size() != b.size()) return a.size() > b.size();
+    return !std::lexicographical_compare(a.rbegin(), a.rend(), b.rbegin(), b.rend());
+}
+
 // SM count of the current device, for the size queries (the launches read the
 // same per-device value).  -1 when no device can be queried.
 int current_num_sms(int* sms) {
@@ -448,13 +536,10 @@ attn_status_t attn_fwd_varlen(const void* q, const void* k, const void* v, void*
                               int Hkv, int total_q, int total_k, int max_seqlen_q,
                               int max_seqlen_k, int d, int causal, float scale,
                               attn_out_dtype_t o_dtype, void* stream) {
-    if (!cu_seqlens_q || !cu_seqlens_k || !aligned4(cu_seqlens_q) || !aligned4(cu_seqlens_k))
-        return ATTN_ERR_INVALID_ARG;
-    if (total_q < 1 || total_k < 1 || total_q > kMaxPackedRows || total_k > kMaxPackedRows)
-        return ATTN_ERR_INVALID_ARG;
-    if (max_seqlen_q > total_q || max_seqlen_k > total_k) return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_varlen(cu_seqlens_q, cu_seqlens_k, total_q, total_k, max_seqlen_q, max_seqlen_k);
+    if (st != ATTN_OK) return st;
     // (the per-sequence causal condition is checked on the device)
-    attn_status_t st = check_fwd(q, k, v, o, lse, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, d, 0,
+    st = check_fwd(q, k, v, o, lse, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, d, 0,
                                  scale, o_dtype);
     if (st != ATTN_OK) return st;
     if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
@@ -485,10 +570,7 @@ attn_status_t attn_bwd(const void* q, const void* k, const void* v, const void* 
     attn_status_t st = check_fwd(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, causal, scale, o_dtype);
     if (st != ATTN_OK) return st;
     // (check_fwd has limited d to the forward's head dims, which the backward takes too)
-    if (!dout || !lse || !dq || !dk || !dv) return ATTN_ERR_INVALID_ARG;
-    if (!aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
-        return ATTN_ERR_INVALID_ARG;
-    if (grad_dtype != ATTN_OUT_BF16 && grad_dtype != ATTN_OUT_F32) return ATTN_ERR_INVALID_ARG;
+    if ((st = check_grads(dout, lse, dq, dk, dv, grad_dtype)) != ATTN_OK) return st;
     const size_t need = bwd_workspace_bytes(B, Hq, Nq, d);
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
     DeviceInfo dev;
@@ -510,20 +592,14 @@ attn_status_t attn_bwd_varlen(const void* q, const void* k, const void* v, const
                               int max_seqlen_k, int d, int causal, float scale,
                               attn_out_dtype_t o_dtype, attn_out_dtype_t grad_dtype,
                               void* workspace, size_t workspace_bytes, void* stream) {
-    if (!cu_seqlens_q || !cu_seqlens_k || !aligned4(cu_seqlens_q) || !aligned4(cu_seqlens_k))
-        return ATTN_ERR_INVALID_ARG;
-    if (total_q < 1 || total_k < 1 || total_q > kMaxPackedRows || total_k > kMaxPackedRows)
-        return ATTN_ERR_INVALID_ARG;
-    if (max_seqlen_q > total_q || max_seqlen_k > total_k) return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_varlen(cu_seqlens_q, cu_seqlens_k, total_q, total_k, max_seqlen_q, max_seqlen_k);
+    if (st != ATTN_OK) return st;
     // (the per-sequence causal condition is checked on the device)
-    attn_status_t st = check_fwd(q, k, v, o, lse, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, d, 0,
+    st = check_fwd(q, k, v, o, lse, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, d, 0,
                                  scale, o_dtype);
     if (st != ATTN_OK) return st;
     if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
-    if (!dout || !lse || !dq || !dk || !dv) return ATTN_ERR_INVALID_ARG;
-    if (!aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
-        return ATTN_ERR_INVALID_ARG;
-    if (grad_dtype != ATTN_OUT_BF16 && grad_dtype != ATTN_OUT_F32) return ATTN_ERR_INVALID_ARG;
+    if ((st = check_grads(dout, lse, dq, dk, dv, grad_dtype)) != ATTN_OK) return st;
     if (!fwd_head_dim_supported(d)) return ATTN_ERR_UNSUPPORTED;
     const size_t need = bwd_varlen_workspace_bytes(B, Hq, total_q);
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
@@ -572,19 +648,10 @@ attn_status_t attn_decode_paged(const void* q, const void* k_pages, const void* 
                                 int B, int Hq, int Hkv, long long num_blocks, int page_size,
                                 int max_blocks, int d, float scale, int num_splits, void* workspace,
                                 size_t workspace_bytes, attn_out_dtype_t o_dtype, void* stream) {
-    if (!q || !k_pages || !v_pages || !block_table || !seqlens || !o) return ATTN_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) ||
-        !aligned4(seqlens) || !aligned4(block_table))
-        return ATTN_ERR_INVALID_ARG;
-    if (lse && !aligned4(lse)) return ATTN_ERR_INVALID_ARG;
-    if (num_blocks < 1 || max_blocks < 1 || page_size < 64) return ATTN_ERR_INVALID_ARG;
-    if (page_size % 64 != 0) return ATTN_ERR_UNSUPPORTED;
-    if ((long long)max_blocks * page_size > kMaxLen || num_blocks >= (1ll << 31))
-        return ATTN_ERR_INVALID_ARG;
-    const int Nmax = max_blocks * page_size;
-    attn_status_t st = check_common(B, Hq, Hkv, d, scale, o_dtype);
+    attn_status_t st = check_decode_paged(q, k_pages, v_pages, block_table, seqlens, o, lse, B, Hq, Hkv,
+                                          num_blocks, page_size, max_blocks, d, scale, num_splits, o_dtype);
     if (st != ATTN_OK) return st;
-    if ((st = check_decode_shape(B, Hq, Hkv, Nmax, d, num_splits)) != ATTN_OK) return st;
+    const int Nmax = max_blocks * page_size;
     DeviceInfo dev;
     if ((st = current_device_info(&dev)) != ATTN_OK) return st;
     const int chunk = decode_chunk(Nmax, B, Hkv, dev.num_sms, num_splits);
@@ -593,6 +660,201 @@ attn_status_t attn_decode_paged(const void* q, const void* k_pages, const void* 
     return launch_decode_paged(q, k_pages, v_pages, block_table, seqlens, o, lse, B, Hq, Hkv,
                                num_blocks, page_size, max_blocks, d, scale, chunk, workspace,
                                o_dtype, static_cast<cudaStream_t>(stream), dev);
+}
+
+attn_status_t attn_bias_buckets(int num_buckets, int max_distance, int bidirectional, int* buckets,
+                                int capacity, int* first, int* span) try {
+    if (!first || !span || (bidirectional != 0 && bidirectional != 1)) return ATTN_ERR_INVALID_ARG;
+    if (num_buckets < (bidirectional ? 4 : 2) || (bidirectional && num_buckets % 2 != 0)) return ATTN_ERR_INVALID_ARG;
+    const int n = bidirectional ? num_buckets / 2 : num_buckets, e = n / 2, s = n - e;
+    if (max_distance <= e) return ATTN_ERR_INVALID_ARG;
+    if (num_buckets > 1024 || max_distance > kMaxLen) return ATTN_ERR_UNSUPPORTED;
+    // the smallest distance of bucket e + k: ceil(e (D / e)^(k / s)).  Where that is
+    // too near a whole number for floating point, whole numbers decide.
+    std::vector<long long> from(s);
+    for (int k = 0; k < s; ++k) {
+        const double t = (double)e * std::pow((double)max_distance / e, (double)k / s);
+        const double m = std::round(t);
+        from[k] = std::fabs(t - m) > 1e-6 * t ? (long long)std::ceil(t)
+                                              : (long long)m + (bucket_reached((long long)m, s, e, k, max_distance) ? 0 : 1);
+    }
+    const long long far = from[s - 1];
+    const long long length = bidirectional ? 2 * far + 1 : far + 1;
+    if (length > kMaxBiasSpan) return ATTN_ERR_UNSUPPORTED;
+    *first = (int)-far;
+    *span = (int)length;
+    if (!buckets) return ATTN_OK;
+    if (capacity < length) return ATTN_ERR_INVALID_ARG;
+    for (long long r = 0, k = 0; r <= far; ++r) {
+        while (k + 1 < s && r >= from[k + 1]) ++k;
+        const int b = (int)(r < e ? r : e + k);
+        buckets[far - r] = b;
+        if (bidirectional && r > 0) buckets[far + r] = n + b;
+    }
+    return ATTN_OK;
+} catch (...) {   // (no memory for a few kilobytes of host vectors)
+    return ATTN_ERR_UNSUPPORTED;
+}
+
+attn_status_t attn_fwd_bias(const void* q, const void* k, const void* v, const void* table,
+                            attn_out_dtype_t table_dtype, const int* buckets, int first, int span,
+                            int num_buckets, void* o, float* lse, int B, int Hq, int Hkv, int Nq, int Nk,
+                            int d, int causal, float scale, attn_out_dtype_t o_dtype, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    attn_status_t st = check_fwd(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, causal, scale, o_dtype);
+    if (st != ATTN_OK) return st;
+    if ((st = check_bias(table, table_dtype, buckets, first, span, num_buckets, d)) != ATTN_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != ATTN_OK) return st;
+    const size_t need = fwd_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, causal, dev.num_sms);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+        return ATTN_ERR_WORKSPACE;
+    const BiasArgs bias = bias_args(table, table_dtype, buckets, first, span, num_buckets);
+    return launch_fwd(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, causal, scale, o_dtype, workspace,
+                      static_cast<cudaStream_t>(stream), dev, &bias);
+}
+
+attn_status_t attn_fwd_varlen_bias(const void* q, const void* k, const void* v, const void* table,
+                                   attn_out_dtype_t table_dtype, const int* buckets, int first, int span,
+                                   int num_buckets, void* o, float* lse, const int* cu_seqlens_q,
+                                   const int* cu_seqlens_k, int B, int Hq, int Hkv, int total_q, int total_k,
+                                   int max_seqlen_q, int max_seqlen_k, int d, int causal, float scale,
+                                   attn_out_dtype_t o_dtype, void* stream) {
+    attn_status_t st = check_varlen(cu_seqlens_q, cu_seqlens_k, total_q, total_k, max_seqlen_q, max_seqlen_k);
+    if (st != ATTN_OK) return st;
+    // (the per-sequence causal condition is checked on the device)
+    st = check_fwd(q, k, v, o, lse, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, d, 0, scale, o_dtype);
+    if (st != ATTN_OK) return st;
+    if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+    if ((st = check_bias(table, table_dtype, buckets, first, span, num_buckets, d)) != ATTN_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != ATTN_OK) return st;
+    const BiasArgs bias = bias_args(table, table_dtype, buckets, first, span, num_buckets);
+    return launch_fwd_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, B, Hq, Hkv, total_q, total_k,
+                             max_seqlen_q, max_seqlen_k, d, causal, scale, o_dtype,
+                             static_cast<cudaStream_t>(stream), dev, &bias);
+}
+
+size_t attn_bwd_bias_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int d, int span) {
+    const size_t base = attn_bwd_workspace_size(B, Hq, Hkv, Nq, Nk, d);
+    if (base == 0 || !head_dim_supported(d) || span < 1 || span > kMaxBiasSpan) return 0;
+    return base + bwd_bias_workspace_bytes(B, Hq, Nk, span);
+}
+
+attn_status_t attn_bwd_bias(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                            const float* lse, const void* table, attn_out_dtype_t table_dtype,
+                            const int* buckets, int first, int span, int num_buckets, void* dq, void* dk,
+                            void* dv, float* dtable, int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                            int causal, float scale, attn_out_dtype_t o_dtype, attn_out_dtype_t grad_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    attn_status_t st = check_fwd(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, causal, scale, o_dtype);
+    if (st != ATTN_OK) return st;
+    if ((st = check_grads(dout, lse, dq, dk, dv, grad_dtype)) != ATTN_OK) return st;
+    if (!dtable || !aligned4(dtable)) return ATTN_ERR_INVALID_ARG;
+    if ((st = check_bias(table, table_dtype, buckets, first, span, num_buckets, d)) != ATTN_OK) return st;
+    const size_t need = bwd_workspace_bytes(B, Hq, Nq, d) + bwd_bias_workspace_bytes(B, Hq, Nk, span);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != ATTN_OK) return st;
+    const BiasArgs bias = bias_args(table, table_dtype, buckets, first, span, num_buckets);
+    return launch_bwd(q, k, v, o, dout, lse, dq, dk, dv, B, Hq, Hkv, Nq, Nk, d, causal, scale, o_dtype,
+                      grad_dtype, workspace, static_cast<cudaStream_t>(stream), dev, &bias, dtable);
+}
+
+size_t attn_bwd_varlen_bias_workspace_size(int B, int Hq, int Hkv, int total_q, int max_seqlen_k, int d,
+                                           int span) {
+    const size_t base = attn_bwd_varlen_workspace_size(B, Hq, Hkv, total_q, d);
+    if (base == 0 || !head_dim_supported(d) || span < 1 || span > kMaxBiasSpan) return 0;
+    if (max_seqlen_k < 1 || max_seqlen_k > kMaxLen) return 0;
+    return base + bwd_bias_workspace_bytes(B, Hq, max_seqlen_k, span);
+}
+
+attn_status_t attn_bwd_varlen_bias(const void* q, const void* k, const void* v, const void* o,
+                                   const void* dout, const float* lse, const void* table,
+                                   attn_out_dtype_t table_dtype, const int* buckets, int first, int span,
+                                   int num_buckets, void* dq, void* dk, void* dv, float* dtable,
+                                   const int* cu_seqlens_q, const int* cu_seqlens_k, int B, int Hq, int Hkv,
+                                   int total_q, int total_k, int max_seqlen_q, int max_seqlen_k, int d,
+                                   int causal, float scale, attn_out_dtype_t o_dtype,
+                                   attn_out_dtype_t grad_dtype, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+    attn_status_t st = check_varlen(cu_seqlens_q, cu_seqlens_k, total_q, total_k, max_seqlen_q, max_seqlen_k);
+    if (st != ATTN_OK) return st;
+    st = check_fwd(q, k, v, o, lse, B, Hq, Hkv, max_seqlen_q, max_seqlen_k, d, 0, scale, o_dtype);
+    if (st != ATTN_OK) return st;
+    if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+    if ((st = check_grads(dout, lse, dq, dk, dv, grad_dtype)) != ATTN_OK) return st;
+    if (!dtable || !aligned4(dtable)) return ATTN_ERR_INVALID_ARG;
+    if ((st = check_bias(table, table_dtype, buckets, first, span, num_buckets, d)) != ATTN_OK) return st;
+    const size_t need = bwd_varlen_workspace_bytes(B, Hq, total_q) +
+                        bwd_bias_workspace_bytes(B, Hq, max_seqlen_k, span);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != ATTN_OK) return st;
+    const BiasArgs bias = bias_args(table, table_dtype, buckets, first, span, num_buckets);
+    return launch_bwd_varlen(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens_q, cu_seqlens_k, B, Hq, Hkv,
+                             total_q, total_k, max_seqlen_q, max_seqlen_k, d, causal, scale, o_dtype,
+                             grad_dtype, workspace, static_cast<cudaStream_t>(stream), dev, &bias, dtable);
+}
+
+attn_status_t attn_decode_paged_bias(const void* q, const void* k_pages, const void* v_pages,
+                                     const int* block_table, const int* seqlens, const void* table,
+                                     attn_out_dtype_t table_dtype, const int* buckets, int first, int span,
+                                     int num_buckets, void* o, float* lse, int B, int Hq, int Hkv,
+                                     long long num_blocks, int page_size, int max_blocks, int d, float scale,
+                                     int num_splits, void* workspace, size_t workspace_bytes,
+                                     attn_out_dtype_t o_dtype, void* stream) {
+    attn_status_t st = check_decode_paged(q, k_pages, v_pages, block_table, seqlens, o, lse, B, Hq, Hkv,
+                                          num_blocks, page_size, max_blocks, d, scale, num_splits, o_dtype);
+    if (st != ATTN_OK) return st;
+    if ((st = check_bias(table, table_dtype, buckets, first, span, num_buckets, d)) != ATTN_OK) return st;
+    const int Nmax = max_blocks * page_size;
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != ATTN_OK) return st;
+    const int chunk = decode_chunk(Nmax, B, Hkv, dev.num_sms, num_splits);
+    const size_t need = decode_workspace_bytes(B, Hq, Nmax, decode_pad_head_dim(d), chunk);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
+    const BiasArgs bias = bias_args(table, table_dtype, buckets, first, span, num_buckets);
+    return launch_decode_paged(q, k_pages, v_pages, block_table, seqlens, o, lse, B, Hq, Hkv, num_blocks,
+                               page_size, max_blocks, d, scale, chunk, workspace, o_dtype,
+                               static_cast<cudaStream_t>(stream), dev, &bias);
+}
+
+attn_status_t attn_page_pool_init(int* pool, int num_blocks, void* stream) {
+    if (!pool || !aligned16(pool) || num_blocks < 1) return ATTN_ERR_INVALID_ARG;
+    if (num_blocks > kMaxPackedRows) return ATTN_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    attn_status_t st = current_device_info(&dev);
+    if (st != ATTN_OK) return st;
+    return launch_pages_init(pool, num_blocks, static_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_pages_extend(int* pool, int num_blocks, int* block_table, int* seqlens,
+                                const int* new_lens, long long* slots, int* positions, int* cu_seqlens,
+                                int* granted, int B, int max_blocks, int page_size, int width, int total,
+                                void* stream) {
+    attn_status_t st = check_page_tables(pool, num_blocks, block_table, seqlens, new_lens, B, max_blocks, page_size);
+    if (st != ATTN_OK) return st;
+    if (width < 0 || total < 0 || (width > 0 && (total != 0 || cu_seqlens))) return ATTN_ERR_INVALID_ARG;
+    const long long n = width > 0 ? (long long)B * width : total;
+    if (n > kMaxPackedRows) return ATTN_ERR_INVALID_ARG;
+    if ((n > 0 && !slots) || !aligned16(slots) || !aligned16(positions) || !aligned4(cu_seqlens) ||
+        !aligned4(granted))
+        return ATTN_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != ATTN_OK) return st;
+    return launch_pages_extend(pool, num_blocks, block_table, seqlens, new_lens, slots, positions, cu_seqlens,
+                               granted, B, max_blocks, page_size, width, n, static_cast<cudaStream_t>(stream), dev);
+}
+
+attn_status_t attn_pages_trim(int* pool, int num_blocks, const int* block_table, int* seqlens,
+                              const int* keep_lens, int B, int max_blocks, int page_size, void* stream) {
+    attn_status_t st = check_page_tables(pool, num_blocks, block_table, seqlens, keep_lens, B, max_blocks, page_size);
+    if (st != ATTN_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device_info(&dev)) != ATTN_OK) return st;
+    return launch_pages_trim(pool, num_blocks, block_table, seqlens, keep_lens, B, max_blocks, page_size,
+                             static_cast<cudaStream_t>(stream), dev);
 }
 
 attn_status_t attn_rope_frequencies(int rotary_dim, double base, attn_rope_scaling_t scaling,

@@ -64,7 +64,9 @@
 // (phase 1) overlap dQ_j and dP_{j+1}.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
+#include "bias.cuh"
 #include "fwd_sched.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -92,7 +94,17 @@ struct BwdCfg {
     static constexpr int kSmemBytes =
         kLayout + 1024 < kMaxSmemPerBlock ? kLayout + 1024 : kMaxSmemPerBlock;
     static_assert(kLayout <= kMaxSmemPerBlock, "shared memory budget");
+    // BIAS (dK and dV leave from registers): in the staging, two bias windows and
+    // two sets of the warps' diagonal sums of dS^T
+    static constexpr int kWin = kStg;
+    static constexpr int kDiag = kWin + 2 * kBiasWindow * 4;
+    static constexpr int kDiagBytes = 8 * 96 * 4;
+    static_assert(kDiag + 2 * kDiagBytes <= kLD, "bias windows and sums fit the staging");
 };
+
+// BIAS: registers of the control warps and of the P/dS warps (384 at 168).
+constexpr int kBwdRegsControl = 104, kBwdRegsPds = 200;
+static_assert(128 * kBwdRegsControl + 256 * kBwdRegsPds <= kBwdThreadsEw * 168, "register split");
 
 struct BwdParams {
     int B, Hq, Hkv, Nq, Nk, Nq_pad, group, off, n_kt, causal;
@@ -112,7 +124,15 @@ struct BwdParams {
     const int* cu_q;
     const int* cu_k;
     int total_q, total_k, vstride;
+    // the BIAS instantiations; partial: [B, n_kt, Hq, span + 16] fp32, a key tile's
+    // sums of dS over each distance of the map, then over the distances before
+    // and after it (8 warps' each)
+    BiasArgs bias;
+    float* partial;
 };
+
+// Floats of one (key tile, head)'s sums.
+__host__ __device__ inline int bias_partial_floats(int span) { return span + 16; }
 
 // Row of sequence b's first query in a head's rows of lse2 / dvec for packed
 // batches: the packed row rounded up to 4 floats (16-byte bulk copies), plus
@@ -138,6 +158,7 @@ struct __align__(8) BwdBars {
     uint64_t kv_full, kv_empty;  // K and V of an item; read by its last S^T and dP^T
     uint64_t qd_full[2], qd_empty[2];
     uint64_t s_full, dp_full, p_full, ds_full, acc_full, drain;
+    uint64_t win_full, diag_full;  // BIAS: a bias window, a set of diagonal sums is filled
     uint32_t tmem_base;
     int abort;
 };
@@ -446,10 +467,15 @@ __device__ void bwd_mma(uint8_t* smem, BwdBars* bars, uint32_t tmem, const BwdPa
 // P^T = 2^(S^T c - lse2) for 32 query columns [qc, qc + 32) of this thread's
 // key row, kept in fp32 (pf) and packed to bf16 pairs (pp).  lim: query column
 // qc + x is allowed iff qc + x >= lim (causal), else all.  The tile's lse2
-// comes from shared memory 4 at a time (broadcast).
-template <bool MASKED>
+// comes from shared memory 4 at a time (broadcast).  With a bias (BM) it joins
+// -lse2: bc for every column, or query column q's own from shared address
+// win - 4 q.
+enum : int { kNoBias = 0, kOneBias = 1, kWindowBias = 2 };
+
+template <bool MASKED, int BM = kNoBias>
 __device__ __forceinline__ void p_chunk(const uint32_t (&s)[32], uint32_t lse2s, int qc, float c,
-                                        int lim, float (&pf)[32], uint32_t (&pp)[16]) {
+                                        int lim, float (&pf)[32], uint32_t (&pp)[16], float bc = 0.f,
+                                        uint32_t win = 0) {
     const uint64_t c2 = f2(c, c);
 #pragma unroll
     for (int x4 = 0; x4 < 8; ++x4) {
@@ -458,7 +484,9 @@ __device__ __forceinline__ void p_chunk(const uint32_t (&s)[32], uint32_t lse2s,
         for (int h = 0; h < 2; ++h) {
             const int x = 2 * x4 + h;
             const int q = qc + 2 * x;
-            const uint64_t nl = h == 0 ? f2(-l4.x, -l4.y) : f2(-l4.z, -l4.w);
+            uint64_t nl = h == 0 ? f2(-l4.x, -l4.y) : f2(-l4.z, -l4.w);
+            if constexpr (BM == kOneBias) nl = f2_add(nl, f2(bc, bc));
+            if constexpr (BM == kWindowBias) nl = f2_add(nl, f2(lds_f32(win - 4 * q), lds_f32(win - 4 * q - 4)));
             float a0, a1;
             f2_split(f2_fma(f2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), c2, nl), a0, a1);
             float p0 = ex2(a0), p1 = ex2(a1);
@@ -473,9 +501,21 @@ __device__ __forceinline__ void p_chunk(const uint32_t (&s)[32], uint32_t lse2s,
     }
 }
 
-// dS^T = P^T o (dP^T - D) for the same 32 query columns, packed to bf16 pairs.
+// Sum of dS over a warp's diagonals (BIAS).  Lane s collects the elements whose
+// key - query is s, s - 32 or s - 64 in its 32 x 64 block: of query column x it
+// takes the value of lane (s + x) % 32, for the first of them while that does
+// not wrap, and so on.  One shuffle and one add an element; column order.
+struct DiagSums {
+    float a[3];   // distance s - 32 k
+    uint64_t far; // tiles with one bias: every element
+};
+
+// dS^T = P^T o (dP^T - D) for the same 32 query columns, packed to bf16 pairs;
+// with a bias (BM), summed in fp32 as well: over diagonals, or (kOneBias) all.
+template <int BM = kNoBias, int HALF = 0>
 __device__ __forceinline__ void ds_chunk_t(const float (&pf)[32], const uint32_t (&dp)[32],
-                                           uint32_t ds_vec, int qc, uint32_t (&dd)[16]) {
+                                           uint32_t ds_vec, int qc, uint32_t (&dd)[16],
+                                           DiagSums* sums = nullptr, int lane = 0) {
 #pragma unroll
     for (int x4 = 0; x4 < 8; ++x4) {
         const float4 d4 = lds128_f32(ds_vec + 4u * (qc + 4 * x4));
@@ -488,6 +528,13 @@ __device__ __forceinline__ void ds_chunk_t(const float (&pf)[32], const uint32_t
                             f2_add(f2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1])), nd)),
                      d0, d1);
             dd[x] = pack_bf16x2(d0, d1);
+            if constexpr (BM == kOneBias) sums->far = f2_add(sums->far, f2(d0, d1));
+            if constexpr (BM == kWindowBias) {
+                const float v0 = __shfl_sync(0xFFFFFFFFu, d0, lane + 2 * x);
+                if (lane < 32 - 2 * x) sums->a[HALF] += v0; else sums->a[HALF + 1] += v0;
+                const float v1 = __shfl_sync(0xFFFFFFFFu, d1, lane + 2 * x + 1);
+                if (lane < 31 - 2 * x) sums->a[HALF] += v1; else sums->a[HALF + 1] += v1;
+            }
         }
     }
 }
@@ -538,7 +585,7 @@ __device__ __forceinline__ void store_rows32_pairs(void* base, size_t row0, size
     }
 }
 
-template <int D, bool OUT_F32, bool VARLEN>
+template <int D, bool OUT_F32, bool VARLEN, bool BIAS>
 __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars, uint32_t tmem,
                         const CUtensorMap* tdk, const CUtensorMap* tdv, const BwdParams& p,
                         unsigned n_items, unsigned int* err) {
@@ -552,21 +599,86 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
     bool ok = true;
     int g = 0;  // Q tiles done, over the CTA's items
     int u = 0;  // items with work
+    // BIAS: this thread's number among the 256, the windows filled and read, and
+    // the sets of diagonal sums exchanged (two buffers each; a buffer is written
+    // again only by a warp that has seen all eight arrive for the next one, each
+    // after its reads of the buffer)
+    const int et = grp * 128 + j;
+    uint32_t cnt_fill = 0, cnt_win = 0, cnt_diag = 0;
     for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
         const BwdWork w = bwd_item<VARLEN>(p, idx, err);
         const int jg = w.k0 + j;
+        // BIAS.  Q tile i of the item meets the distances base(i) .. + 254; their
+        // sums of dS are held by the thread of the same number modulo 256 (each
+        // distance is in at most two Q tiles of a head, one after the other) and
+        // stored when the head's next tile does not have them.
+        auto q0_of = [&](int i) { return (w.qt_first + i % w.n_qt_cta) * kBT; };
+        auto base_of = [&](int i) { return w.k0 - (q0_of(i) + w.off) - (kBT - 1); };
+        auto head_of = [&](int i) { return w.g * p.group + i / w.n_qt_cta; };
+        auto sums_of = [&](int hq) {
+            return p.partial + (((size_t)w.b * p.n_kt + w.kt) * p.Hq + hq) * bias_partial_floats(p.bias.span);
+        };
+        auto fill = [&](float v) {
+            sts_f32(smem_u32(smem + C::kWin) + ((cnt_fill & 1) * kBiasWindow + et) * 4, v);
+            ++cnt_fill;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->win_full));
+        };
+        float wv = 0.f, bias_l = 0.f, bias_r = 0.f, own = 0.f, far_l = 0.f, far_r = 0.f;
+        if constexpr (BIAS) {
+            if (w.n_tiles == 0) {
+                for (int h = 0; h < p.group; ++h) {
+                    float* out = sums_of(w.g * p.group + h);
+                    for (int x = et; x < bias_partial_floats(p.bias.span); x += 256) out[x] = 0.f;
+                }
+            } else {
+                if (bias_near(p.bias, base_of(0)))
+                    fill(bias_at(p.bias, p.Hq, head_of(0), base_of(0) + et, err));
+                if (w.n_tiles > 1 && bias_near(p.bias, base_of(1)))
+                    wv = bias_at(p.bias, p.Hq, head_of(1), base_of(1) + et, err);
+            }
+        }
         for (int i = 0; i < w.n_tiles && ok; ++i) {
             const int gi = g + i;
             const int st = gi & 1;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->s_full), gi & 1, abort_flag, 32));
             if (!ok) break;
             tc_fence_after();
-            const int q0 = (w.qt_first + i % w.n_qt_cta) * kBT;
+            const int q0 = q0_of(i);
             const uint32_t lse2s = smem_u32(smem + C::kLD + st * 1024);
             const uint32_t ds_vec = lse2s + kBT * 4;
             // causal: query q0 + x sees key jg iff x >= jg - off - q0
-            const int lim = jg - w.off - q0;
-            const bool masked = p.causal && (q0 + w.off < w.k0 + kBT - 1);
+            int lim = jg - w.off - q0;
+            bool masked = p.causal && (q0 + w.off < w.k0 + kBT - 1);
+            const int base = BIAS ? base_of(i) : 0;
+            const bool near = BIAS && bias_near(p.bias, base);
+            float bc = 0.f;
+            uint32_t win = 0;
+            if constexpr (BIAS) {
+                // keys past the sequence have dS = 0 (their rows of K are zeros)
+                if (w.k0 + kBT > w.nk) {
+                    if (!p.causal) lim = -kBT;
+                    if (jg >= w.nk) lim = kBT;
+                    masked = true;
+                }
+                if (i % w.n_qt_cta == 0) {   // a head begins
+                    const int hq = head_of(i);
+                    bias_l = bias_at(p.bias, p.Hq, hq, p.bias.first, err);
+                    bias_r = bias_at(p.bias, p.Hq, hq, p.bias.first + p.bias.span - 1, err);
+                    float* out = sums_of(hq);
+                    for (int x = (et - p.bias.first) & 255; x < p.bias.span; x += 256) out[x] = 0.f;
+                    far_l = far_r = 0.f;
+                }
+                if (near) {
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_full), cnt_win & 1, abort_flag, 32));
+                    if (!ok) break;
+                    // query column x of key row j is distance base + j - x + 127
+                    win = smem_u32(smem + C::kWin) + ((cnt_win & 1) * kBiasWindow + j + kBT - 1) * 4;
+                    ++cnt_win;
+                } else {
+                    bc = base + 254 <= p.bias.first ? bias_l : bias_r;
+                }
+            }
             // Phase 1: P^T from S^T for this warpgroup's 64 query columns, kept
             // in registers and written as bf16 over the S^T columns it has read;
             // with the other warpgroup's, releases dV(i) and S^T(i+1).
@@ -575,7 +687,15 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
                 uint32_t sv[32], pp[16];
                 tmem_ld32(tS + cc * 32, sv);
                 tmem_wait_ld();
-                if (masked)
+                if constexpr (BIAS) {
+                    if (near) {
+                        if (masked) p_chunk<true, kWindowBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, 0.f, win);
+                        else p_chunk<false, kWindowBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, 0.f, win);
+                    } else {
+                        if (masked) p_chunk<true, kOneBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, bc);
+                        else p_chunk<false, kOneBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, bc);
+                    }
+                } else if (masked)
                     p_chunk<true>(sv, lse2s, cc * 32, p.c, lim, pf, pp);
                 else
                     p_chunk<false>(sv, lse2s, cc * 32, p.c, lim, pf, pp);
@@ -587,26 +707,88 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
+            if constexpr (BIAS) {
+                if (i + 1 < w.n_tiles && bias_near(p.bias, base_of(i + 1))) fill(wv);
+                if (i + 2 < w.n_tiles && bias_near(p.bias, base_of(i + 2)))
+                    wv = bias_at(p.bias, p.Hq, head_of(i + 2), base_of(i + 2) + et, err);
+            }
             // Phase 2: dS^T from P^T and dP^T, written as bf16 over the dP^T
             // columns already read; releases dK(i) and dP^T(i+1).
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->dp_full), gi & 1, abort_flag, 32));
             if (!ok) break;
             tc_fence_after();
-            auto phase2 = [&](int cc, const float (&pf)[32]) {
+            DiagSums sums = {{0.f, 0.f, 0.f}, 0};
+            auto phase2 = [&](auto half, const float (&pf)[32]) {
+                constexpr int kHalf = decltype(half)::value;
+                const int cc = 2 * grp + kHalf;
                 uint32_t dp[32], dd[16];
                 tmem_ld32(tdP + cc * 32, dp);
                 tmem_wait_ld();
-                ds_chunk_t(pf, dp, ds_vec, cc * 32, dd);
+                if constexpr (BIAS) {
+                    if (near) ds_chunk_t<kWindowBias, kHalf>(pf, dp, ds_vec, cc * 32, dd, &sums, lane);
+                    else ds_chunk_t<kOneBias>(pf, dp, ds_vec, cc * 32, dd, &sums);
+                } else {
+                    ds_chunk_t(pf, dp, ds_vec, cc * 32, dd);
+                }
                 tmem_st16(tdP + a_chunk_col(cc), dd);
             };
-            phase2(2 * grp, pf0);
-            phase2(2 * grp + 1, pf1);
+            phase2(std::integral_constant<int, 0>{}, pf0);
+            phase2(std::integral_constant<int, 1>{}, pf1);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(smem_u32(&bars->ds_full));
                 mbar_arrive(smem_u32(&bars->qd_empty[st]));
+            }
+            if constexpr (BIAS) {
+                const bool head_ends = (i + 1) % w.n_qt_cta == 0;
+                float* out = sums_of(head_of(i));
+                if (near) {
+                    // the warps' diagonals meet: warp (wq, grp) holds distance
+                    // base + 127 + 32 wq - 64 grp + (s - 32 k) in place 32 k + s
+                    float* set = reinterpret_cast<float*>(smem + C::kDiag + (cnt_diag & 1) * C::kDiagBytes);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) set[(grp * 4 + wq) * 96 + 32 * k + lane] = sums.a[k];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars->diag_full));
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->diag_full), cnt_diag & 1, abort_flag, 32));
+                    if (!ok) break;
+                    ++cnt_diag;
+                    const int at = (et - base) & 255;   // this thread's distance: base + at
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int d = at - 127 - 32 * (e & 3) + 64 * (e >> 2);   // s - 32 k
+                        if (d >= -63 && d <= 31) {
+                            const int k = (31 - d) >> 5;
+                            own += set[e * 96 + 64 * k + d];
+                        }
+                    }
+                    const bool stays = !head_ends && at <= 126 && bias_near(p.bias, base - kBT);
+                    if (!stays) {
+                        const int x = base + at - p.bias.first;
+                        if (x < 0) far_l += own;
+                        else if (x >= p.bias.span) far_r += own;
+                        else if (at <= 254) out[x] = own;
+                        own = 0.f;
+                    }
+                } else {
+                    float a, b;
+                    f2_split(sums.far, a, b);
+                    if (base + 254 <= p.bias.first) far_l += a + b; else far_r += a + b;
+                }
+                if (head_ends) {
+                    float a = far_l, b = far_r;
+#pragma unroll
+                    for (int s = 16; s > 0; s >>= 1) {
+                        a += __shfl_xor_sync(0xFFFFFFFFu, a, s);
+                        b += __shfl_xor_sync(0xFFFFFFFFu, b, s);
+                    }
+                    if (lane == 0) {
+                        out[p.bias.span + grp * 4 + wq] = a;
+                        out[p.bias.span + 8 + grp * 4 + wq] = b;
+                    }
+                }
             }
         }
         if (!ok) break;
@@ -638,7 +820,7 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
         tc_fence_after();
         // The next item's dV and dK (accumulate = 0) are issued only after this
         // warpgroup's next P^T arrival, which follows these reads.
-        if constexpr (D == 128) {
+        if constexpr (D == 128 && !BIAS) {
             // dV, then dK (x scale): boxes of 32 rows x 128 bytes written into the
             // warp's 4 KiB of shared memory (128-byte swizzle) and stored by the
             // tensor-memory accelerator, so the stores drain while the next item
@@ -715,7 +897,7 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
     __syncwarp();
 }
 
-template <int D, bool OUT_F32, bool VARLEN>
+template <int D, bool OUT_F32, bool VARLEN, bool BIAS>
 __global__ void __launch_bounds__(kBwdThreadsEw, 1)
 attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -747,6 +929,8 @@ attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         mbar_init(smem_u32(&bars->p_full), 8);
         mbar_init(smem_u32(&bars->ds_full), 8);
         mbar_init(smem_u32(&bars->acc_full), 1);
+        mbar_init(smem_u32(&bars->win_full), 8);
+        mbar_init(smem_u32(&bars->diag_full), 8);
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort = 0;
         fence_barrier_init();
@@ -764,10 +948,14 @@ attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
 
+    if constexpr (BIAS) {
+        if (warp < 4) reg_dealloc<kBwdRegsControl>();
+        else reg_alloc<kBwdRegsPds>();
+    }
     if (warp == 0) bwd_producer<D, VARLEN>(&tq, &tk, &tv, &tdo, smem, bars, p, n_items, err);
     else if (warp == 1) bwd_mma<D, VARLEN>(smem, bars, tmem, p, n_items, err);
     else if (warp >= 4)
-        bwd_pds<D, OUT_F32, VARLEN>(warp & 3, (warp - 4) >> 2, lane, smem, bars, tmem, &tdk, &tdv, p, n_items, err);
+        bwd_pds<D, OUT_F32, VARLEN, BIAS>(warp & 3, (warp - 4) >> 2, lane, smem, bars, tmem, &tdk, &tdv, p, n_items, err);
 
     tc_fence_before();
     __syncthreads();
@@ -781,7 +969,7 @@ attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
 // ---------------------------------------------------------------------------
 // dQ pass (Q-outer)
 // ---------------------------------------------------------------------------
-template <int D>
+template <int D, bool BIAS>
 struct DqCfg {
     static constexpr int kTile = kBT * D * 2;
     static constexpr int kQ = 0;
@@ -789,7 +977,8 @@ struct DqCfg {
     static constexpr int kKRing = 2 * kTile;    // 3 stages of K
     static constexpr int kVRing = 5 * kTile;    // 2 stages of V
     static constexpr int kBar = 7 * kTile;
-    static constexpr int kLayout = kBar + 256;
+    static constexpr int kWin = kBar + 256;     // BIAS: two bias windows
+    static constexpr int kLayout = kWin + (BIAS ? 2 * kBiasWindow * 4 : 0);
     static constexpr int kSmemBytes =
         kLayout + 1024 < kMaxSmemPerBlock ? kLayout + 1024 : kMaxSmemPerBlock;
     static_assert(kLayout <= kMaxSmemPerBlock, "shared memory budget");
@@ -799,6 +988,7 @@ struct __align__(8) DqBars {
     uint64_t q_full, q_empty;  // Q and dO of an item; read by its last S and dP
     uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
     uint64_t s_full[2], dp_full, ds_full, dq_full, drain;  // s_full[b]: the S in buffer b
+    uint64_t win_full;  // BIAS: a bias window is filled
     uint32_t tmem_base;
     int abort;
 };
@@ -894,11 +1084,11 @@ __device__ __forceinline__ DqWork dq_item(const BwdParams& p, unsigned idx, unsi
     else return dq_work(p, idx);
 }
 
-template <int D, bool VARLEN>
+template <int D, bool VARLEN, bool BIAS>
 __device__ void dq_producer(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
                             const CUtensorMap* tdo, uint8_t* smem, DqBars* bars, const BwdParams& p,
                             unsigned n_items, unsigned int* err) {
-    using C = DqCfg<D>;
+    using C = DqCfg<D, BIAS>;
     const volatile int* abort_flag = &bars->abort;
     const bool leader = elect_one();
     bool ok = true;
@@ -993,10 +1183,10 @@ __device__ void dq_producer(const CUtensorMap* tq, const CUtensorMap* tk, const 
     __syncwarp();
 }
 
-template <int D, bool VARLEN>
+template <int D, bool VARLEN, bool BIAS>
 __device__ void dq_mma(uint8_t* smem, DqBars* bars, uint32_t tmem, const BwdParams& p, unsigned n_items,
                        unsigned int* err) {
-    using C = DqCfg<D>;
+    using C = DqCfg<D, BIAS>;
     const volatile int* abort_flag = &bars->abort;
     const bool leader = elect_one();
     const uint32_t idS = make_idesc_bf16(128, 128, 0, 0);
@@ -1072,14 +1262,18 @@ __device__ void dq_mma(uint8_t* smem, DqBars* bars, uint32_t tmem, const BwdPara
 
 // P = 2^(S c - lse2) for 32 key columns [kc, kc + 32) of this thread's query
 // row (fp32).  lim: key column kc + x is allowed iff kc + x <= lim (causal).
-template <bool MASKED>
+// WINDOW: column k's bias, from shared address win + 4 k, joins -lse2 (one bias for
+// the whole tile is in nl2 already).
+template <bool MASKED, bool WINDOW = false>
 __device__ __forceinline__ void p_row_chunk(const uint32_t (&s)[32], uint64_t c2, uint64_t nl2,
-                                            int kc, int lim, float (&pf)[32]) {
+                                            int kc, int lim, float (&pf)[32], uint32_t win = 0) {
 #pragma unroll
     for (int x = 0; x < 16; ++x) {
         const int col = kc + 2 * x;
         float a0, a1;
-        f2_split(f2_fma(f2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), c2, nl2), a0, a1);
+        uint64_t add = nl2;
+        if constexpr (WINDOW) add = f2_add(nl2, f2(lds_f32(win + 4 * col), lds_f32(win + 4 * col + 4)));
+        f2_split(f2_fma(f2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), c2, add), a0, a1);
         float p0 = ex2(a0), p1 = ex2(a1);
         if constexpr (MASKED) {
             p0 = col <= lim ? p0 : 0.f;
@@ -1103,9 +1297,10 @@ __device__ __forceinline__ void ds_row_chunk(const float (&pf)[32], const uint32
     }
 }
 
-template <int D, bool OUT_F32, bool VARLEN>
-__device__ void dq_ds(int wq, int grp, int lane, DqBars* bars, uint32_t tmem, const BwdParams& p,
-                      unsigned n_items, unsigned int* err) {
+template <int D, bool OUT_F32, bool VARLEN, bool BIAS>
+__device__ void dq_ds(int wq, int grp, int lane, uint8_t* smem, DqBars* bars, uint32_t tmem,
+                      const BwdParams& p, unsigned n_items, unsigned int* err) {
+    using C = DqCfg<D, BIAS>;
     const volatile int* abort_flag = &bars->abort;
     const uint32_t lane_off = uint32_t(wq * 32) << 16;
     const uint32_t tdP = tmem + 128 + lane_off;
@@ -1113,6 +1308,8 @@ __device__ void dq_ds(int wq, int grp, int lane, DqBars* bars, uint32_t tmem, co
     bool ok = true;
     int t0 = 0;  // K/V tiles before this item, over the CTA's items
     int u = 0;   // items with work
+    const int et = grp * 128 + wq * 32 + lane;   // BIAS: as in the dK/dV pass
+    uint32_t cnt_fill = 0, cnt_win = 0;
     for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
         const DqWork w = dq_item<VARLEN>(p, idx, err);
         const int row = w.q0 + wq * 32 + lane;
@@ -1123,15 +1320,57 @@ __device__ void dq_ds(int wq, int grp, int lane, DqBars* bars, uint32_t tmem, co
         // its rows may lie past the sequence's rows of lse2 / dvec)
         const float lse2 = w.n_kv > 0 ? p.lse2[vrow] : INFINITY;
         const float dval = w.n_kv > 0 ? p.dvec[vrow] : 0.f;
-        const uint64_t nl2 = f2(-lse2, -lse2), nd2 = f2(-dval, -dval);
+        uint64_t nl2 = f2(-lse2, -lse2);
+        const uint64_t nd2 = f2(-dval, -dval);
+        // BIAS: K/V tile j meets the distances base0 + 128 j .. + 254
+        const int base0 = -(w.q0 + kBT - 1) - w.off;
+        auto fill = [&](float v) {
+            sts_f32(smem_u32(smem + C::kWin) + ((cnt_fill & 1) * kBiasWindow + et) * 4, v);
+            ++cnt_fill;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->win_full));
+        };
+        float wv = 0.f, bias_l = 0.f, bias_r = 0.f;
+        if constexpr (BIAS) {
+            if (w.n_kv > 0) {
+                bias_l = bias_at(p.bias, p.Hq, w.hq, p.bias.first, err);
+                bias_r = bias_at(p.bias, p.Hq, w.hq, p.bias.first + p.bias.span - 1, err);
+                if (bias_near(p.bias, base0)) fill(bias_at(p.bias, p.Hq, w.hq, base0 + et, err));
+                if (w.n_kv > 1 && bias_near(p.bias, base0 + kBT))
+                    wv = bias_at(p.bias, p.Hq, w.hq, base0 + kBT + et, err);
+            }
+        }
         for (int j = 0; j < w.n_kv && ok; ++j) {
             const int t = t0 + j;
             const uint32_t tS = tmem + ((t & 1) ? 384u : 0u) + lane_off;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->s_full[t & 1]), (t >> 1) & 1, abort_flag, 32));
             if (!ok) break;
             tc_fence_after();
-            const int lim = row + w.off - j * kBT;  // causal: key column c allowed iff c <= lim
-            const bool masked = __any_sync(0xFFFFFFFFu, p.causal && lim < kBT - 1);
+            int lim = row + w.off - j * kBT;  // causal: key column c allowed iff c <= lim
+            bool masked = __any_sync(0xFFFFFFFFu, p.causal && lim < kBT - 1);
+            bool near = false;
+            uint32_t win = 0;
+            if constexpr (BIAS) {
+                // keys past the sequence: P = 0 (a bias can put their 2^-lse2 past
+                // fp32's range, and infinity times their zero rows of K is NaN)
+                const int last = w.nk - 1 - j * kBT;
+                lim = p.causal && lim < last ? lim : last;
+                masked = __any_sync(0xFFFFFFFFu, lim < kBT - 1);
+                const int base = base0 + j * kBT;
+                near = bias_near(p.bias, base);
+                if (near) {
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_full), cnt_win & 1, abort_flag, 32));
+                    if (!ok) break;
+                    // key column c of query row i is distance base + c - i + 127
+                    win = smem_u32(smem + C::kWin) +
+                          ((cnt_win & 1) * kBiasWindow + kBT - 1 - (wq * 32 + lane)) * 4;
+                    ++cnt_win;
+                    nl2 = f2(-lse2, -lse2);
+                } else {
+                    const float add = (base + 254 <= p.bias.first ? bias_l : bias_r) - lse2;
+                    nl2 = f2(add, add);
+                }
+            }
             // Phase 1: P from S for this warpgroup's 64 key columns (needs S_j
             // only; runs while dQ_{j-1} and dP_j compute)
             float pf0[32], pf1[32];
@@ -1139,13 +1378,26 @@ __device__ void dq_ds(int wq, int grp, int lane, DqBars* bars, uint32_t tmem, co
                 uint32_t sv[32];
                 tmem_ld32(tS + cc * 32, sv);
                 tmem_wait_ld();
-                if (masked)
+                if constexpr (BIAS) {
+                    if (near) {
+                        if (masked) p_row_chunk<true, true>(sv, c2, nl2, cc * 32, lim, pf, win);
+                        else p_row_chunk<false, true>(sv, c2, nl2, cc * 32, kBT, pf, win);
+                    } else {
+                        if (masked) p_row_chunk<true>(sv, c2, nl2, cc * 32, lim, pf);
+                        else p_row_chunk<false>(sv, c2, nl2, cc * 32, kBT, pf);
+                    }
+                } else if (masked)
                     p_row_chunk<true>(sv, c2, nl2, cc * 32, p.causal ? lim : kBT, pf);
                 else
                     p_row_chunk<false>(sv, c2, nl2, cc * 32, kBT, pf);
             };
             phase1(2 * grp, pf0);
             phase1(2 * grp + 1, pf1);
+            if constexpr (BIAS) {
+                if (j + 1 < w.n_kv && bias_near(p.bias, base0 + (j + 1) * kBT)) fill(wv);
+                if (j + 2 < w.n_kv && bias_near(p.bias, base0 + (j + 2) * kBT))
+                    wv = bias_at(p.bias, p.Hq, w.hq, base0 + (j + 2) * kBT + et, err);
+            }
             // Phase 2: dS from P and dP, as bf16 over the S columns this
             // warpgroup read
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->dp_full), t & 1, abort_flag, 32));
@@ -1209,12 +1461,12 @@ __device__ void dq_ds(int wq, int grp, int lane, DqBars* bars, uint32_t tmem, co
     }
 }
 
-template <int D, bool OUT_F32, bool VARLEN>
+template <int D, bool OUT_F32, bool VARLEN, bool BIAS>
 __global__ void __launch_bounds__(kBwdThreadsEw, 1)
 attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                    const BwdParams p, unsigned int* err) {
-    using C = DqCfg<D>;
+    using C = DqCfg<D, BIAS>;
     extern __shared__ uint8_t smem_raw[];
     const uintptr_t raw = reinterpret_cast<uintptr_t>(smem_raw);
     uint8_t* smem = reinterpret_cast<uint8_t*>((raw + 1023) & ~uintptr_t(1023));
@@ -1241,6 +1493,7 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         mbar_init(smem_u32(&bars->dp_full), 1);
         mbar_init(smem_u32(&bars->ds_full), 8);
         mbar_init(smem_u32(&bars->dq_full), 1);
+        mbar_init(smem_u32(&bars->win_full), 8);
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort = 0;
         fence_barrier_init();
@@ -1257,9 +1510,10 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
-    if (warp == 0) dq_producer<D, VARLEN>(&tq, &tk, &tv, &tdo, smem, bars, p, n_items, err);
-    else if (warp == 1) dq_mma<D, VARLEN>(smem, bars, tmem, p, n_items, err);
-    else if (warp >= 4) dq_ds<D, OUT_F32, VARLEN>(warp & 3, (warp - 4) >> 2, lane, bars, tmem, p, n_items, err);
+    if (warp == 0) dq_producer<D, VARLEN, BIAS>(&tq, &tk, &tv, &tdo, smem, bars, p, n_items, err);
+    else if (warp == 1) dq_mma<D, VARLEN, BIAS>(smem, bars, tmem, p, n_items, err);
+    else if (warp >= 4)
+        dq_ds<D, OUT_F32, VARLEN, BIAS>(warp & 3, (warp - 4) >> 2, lane, smem, bars, tmem, p, n_items, err);
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -1272,6 +1526,11 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 // ---------------------------------------------------------------------------
 // prep
 // ---------------------------------------------------------------------------
+// LSE in base 2; +inf for a row that attended no key (LSE = -inf): its P = 0.
+__device__ __forceinline__ float row_lse2(float lse) {
+    return lse == -INFINITY ? INFINITY : lse * kBwdLog2e;
+}
+
 // D = dO . O and lse2 = LSE log2(e) for every padded query row (padding: 0
 // and +inf).  LPR lanes share a row, each reading 8 consecutive elements of
 // dO and of O per 16-byte load (rows start on 16-byte boundaries: d % 8 == 0
@@ -1321,7 +1580,7 @@ attn_bwd_prep_kernel(const void* __restrict__ o, int o_f32, const __nv_bfloat16*
     for (int s = LPR / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
     if (live_row && sub == 0) {
         dvec[r] = i < Nq ? sum : 0.f;
-        lse2[r] = i < Nq ? lse[(size_t)bh * Nq + i] * kBwdLog2e : INFINITY;
+        lse2[r] = i < Nq ? row_lse2(lse[(size_t)bh * Nq + i]) : INFINITY;
     }
 }
 
@@ -1383,7 +1642,7 @@ attn_bwd_prep_varlen_kernel(const void* __restrict__ o, int o_f32, const __nv_bf
     if (live_row && sub == 0) {
         const size_t r = (size_t)hq * vstride + (size_t)(varlen_vbase(q0, b) + i);
         dvec[r] = valid ? sum : 0.f;
-        lse2[r] = valid ? lse[(size_t)hq * total_q + (size_t)(q0 + i)] * kBwdLog2e : INFINITY;
+        lse2[r] = valid ? row_lse2(lse[(size_t)hq * total_q + (size_t)(q0 + i)]) : INFINITY;
     }
 }
 
@@ -1425,20 +1684,89 @@ attn_status_t launch_bwd_prep(const void* o, int o_f32, const void* dout, const 
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-template <int D, bool OUT_F32, bool VARLEN = false>
+// The bias table's gradient from the dK/dV pass's sums, in two steps of a fixed
+// order.  1: sums over the B n_kt key tiles, every distance of a head; block z takes
+// tiles z, z + gridDim.z, ... (8 groups of them side by side).
+__global__ void __launch_bounds__(256)
+attn_bwd_bias_sum_kernel(const float* __restrict__ partial, float* __restrict__ sums, int tiles, int Hq,
+                         int floats) {
+    __shared__ float part[8][32];
+    const int x = blockIdx.x * 32 + (threadIdx.x & 31), grp = threadIdx.x >> 5, h = blockIdx.y;
+    float a = 0.f;
+    if (x < floats) {
+        const size_t step = (size_t)8 * gridDim.z;
+#pragma unroll 8
+        for (size_t t = blockIdx.z + (size_t)grp * gridDim.z; t < (size_t)tiles; t += step)
+            a += __ldg(partial + (t * Hq + h) * floats + x);
+    }
+    part[grp][threadIdx.x & 31] = a;
+    __syncthreads();
+    if (grp == 0 && x < floats) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += part[i][threadIdx.x];
+        sums[((size_t)blockIdx.z * Hq + h) * floats + x] = v;
+    }
+}
+
+// 2: a warp per (head, bucket) adds up the distances that the map gives the bucket;
+// those beyond the map go with its ends.
+__global__ void __launch_bounds__(256)
+attn_bwd_bias_table_kernel(const float* __restrict__ sums, const int* __restrict__ buckets,
+                           float* __restrict__ dtable, int parts, int Hq, int span, int num_buckets) {
+    const int h = blockIdx.y, lane = threadIdx.x & 31;
+    const int bk = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (bk >= num_buckets) return;
+    const int floats = bias_partial_floats(span);
+    float a = 0.f;
+#pragma unroll 4
+    for (int x = lane; x < floats; x += 32) {
+        const int at = x < span ? x : x < span + 8 ? 0 : span - 1;
+        if (__ldg(buckets + at) == bk)
+            for (int z = 0; z < parts; ++z) a += __ldg(sums + ((size_t)z * Hq + h) * floats + x);
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, s);
+    if (lane == 0) dtable[(size_t)bk * Hq + h] = a;
+}
+
+// Blocks that share a distance's key tiles in step 1: 128 tiles each, at most 32.
+inline int bias_sum_parts(long long tiles) {
+    const long long z = (tiles + 127) / 128;
+    return (int)(z < 32 ? z : 32);
+}
+
+// fp32 of workspace for the table's gradient: the dK/dV pass's sums and step 1's.
+inline size_t bias_workspace_floats(long long tiles, int Hq, int span) {
+    return (size_t)(tiles + bias_sum_parts(tiles)) * Hq * bias_partial_floats(span);
+}
+
+attn_status_t launch_bias_grad(const BwdParams& p, float* dtable, cudaStream_t stream) {
+    const int floats = bias_partial_floats(p.bias.span);
+    const int tiles = p.B * p.n_kt, parts = bias_sum_parts(tiles);
+    float* sums = p.partial + (size_t)tiles * p.Hq * floats;
+    attn_bwd_bias_sum_kernel<<<dim3((unsigned)((floats + 31) / 32), (unsigned)p.Hq, (unsigned)parts), 256, 0,
+                               stream>>>(p.partial, sums, tiles, p.Hq, floats);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+    attn_bwd_bias_table_kernel<<<dim3((unsigned)((p.bias.num_buckets + 7) / 8), (unsigned)p.Hq), 256, 0, stream>>>(
+        sums, p.bias.buckets, dtable, parts, p.Hq, p.bias.span, p.bias.num_buckets);
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+template <int D, bool OUT_F32, bool VARLEN, bool BIAS>
 attn_status_t launch_bwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv,
                            const BwdParams& p, const void* o, int o_f32,
-                           const void* dout, const float* lse, float* lse2, float* dvec,
+                           const void* dout, const float* lse, float* lse2, float* dvec, float* dtable,
                            cudaStream_t stream, const DeviceInfo& dev) {
     static int attr_set[64] = {0};
     if (dev.device < 64 && !attr_set[dev.device]) {
-        if (cudaFuncSetAttribute(attn_bwd_dkdv_kernel<D, OUT_F32, VARLEN>,
+        if (cudaFuncSetAttribute(attn_bwd_dkdv_kernel<D, OUT_F32, VARLEN, BIAS>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  BwdCfg<D>::kSmemBytes) != cudaSuccess ||
-            cudaFuncSetAttribute(attn_bwd_dq_kernel<D, OUT_F32, VARLEN>,
+            cudaFuncSetAttribute(attn_bwd_dq_kernel<D, OUT_F32, VARLEN, BIAS>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 DqCfg<D>::kSmemBytes) != cudaSuccess)
+                                 DqCfg<D, BIAS>::kSmemBytes) != cudaSuccess)
             return ATTN_ERR_CUDA;
         attr_set[dev.device] = 1;
     }
@@ -1455,14 +1783,16 @@ attn_status_t launch_bwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const C
     // CTA per SM, each taking every gridDim.x-th key tile.
     const long long kv_items = (long long)p.B * p.Hkv * p.n_kt;
     const long long kv_ctas = kv_items < dev.num_sms ? kv_items : dev.num_sms;
-    attn_bwd_dkdv_kernel<D, OUT_F32, VARLEN><<<(unsigned)kv_ctas, kBwdThreadsEw, BwdCfg<D>::kSmemBytes,
+    attn_bwd_dkdv_kernel<D, OUT_F32, VARLEN, BIAS><<<(unsigned)kv_ctas, kBwdThreadsEw, BwdCfg<D>::kSmemBytes,
                                                stream>>>(tq, tk, tv, tdo, tdk, tdv, p, dev.err_word);
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
     const long long q_items = (long long)p.B * p.Hq * ((p.Nq + kBT - 1) / kBT);
     const long long q_ctas = q_items < dev.num_sms ? q_items : dev.num_sms;  // persistent, as above
-    attn_bwd_dq_kernel<D, OUT_F32, VARLEN><<<(unsigned)q_ctas, kBwdThreadsEw, DqCfg<D>::kSmemBytes,
+    attn_bwd_dq_kernel<D, OUT_F32, VARLEN, BIAS><<<(unsigned)q_ctas, kBwdThreadsEw, DqCfg<D, BIAS>::kSmemBytes,
                                              stream>>>(tq, tk, tv, tdo, p, dev.err_word);
-    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+    if constexpr (BIAS) return launch_bias_grad(p, dtable, stream);
+    return ATTN_OK;
 }
 
 // ---------------------------------------------------------------------------
@@ -2330,12 +2660,17 @@ size_t bwd_varlen_workspace_bytes(int B, int Hq, int total_q) {
     return 2 * (size_t)Hq * vstride * 4;
 }
 
+size_t bwd_bias_workspace_bytes(int B, int Hq, int Nk, int span) {
+    return bias_workspace_floats((long long)B * ((Nk + kBT - 1) / kBT), Hq, span) * 4;
+}
+
 attn_status_t launch_bwd_varlen(const void* q, const void* k, const void* v, const void* o,
                                 const void* dout, const float* lse, void* dq, void* dk, void* dv,
                                 const int* cu_q, const int* cu_k, int B, int Hq, int Hkv, int total_q,
                                 int total_k, int max_q, int max_k, int d, int causal, float scale,
                                 attn_out_dtype_t o_dtype, attn_out_dtype_t grad_dtype,
-                                void* workspace, cudaStream_t stream, const DeviceInfo& dev) {
+                                void* workspace, cudaStream_t stream, const DeviceInfo& dev,
+                                const BiasArgs* bias, float* dtable) {
     BwdParams p;
     p.B = B;
     p.Hq = Hq;
@@ -2363,6 +2698,8 @@ attn_status_t launch_bwd_varlen(const void* q, const void* k, const void* v, con
     p.dq = dq;
     p.dk = dk;
     p.dv = dv;
+    p.bias = bias ? *bias : BiasArgs{};
+    p.partial = dvec + (size_t)Hq * p.vstride;
     if ((long long)B * Hkv * p.n_kt >= (1ll << 31) || (long long)B * Hq * (p.Nq_pad / kBT) >= (1ll << 31) ||
         (long long)Hq * p.vstride >= (1ll << 31))
         return ATTN_ERR_UNSUPPORTED;
@@ -2393,15 +2730,19 @@ attn_status_t launch_bwd_varlen(const void* q, const void* k, const void* v, con
     if (pad_head_dim(d) == 128) {
         if ((st = encode_tmap_ragged(&tdk, dk, g32, d, Hkv, g32 ? 32 : 64, 32, true)) != ATTN_OK) return st;
         if ((st = encode_tmap_ragged(&tdv, dv, g32, d, Hkv, g32 ? 32 : 64, 32, true)) != ATTN_OK) return st;
-        return g32 ? launch_bwd_t<128, true, true>(tq, tk, tv, tdo, tdk, tdv, p, o, o_f32, dout, lse, lse2, dvec,
-                                                   stream, dev)
-                   : launch_bwd_t<128, false, true>(tq, tk, tv, tdo, tdk, tdv, p, o, o_f32, dout, lse, lse2, dvec,
-                                                    stream, dev);
     }
-    return g32 ? launch_bwd_t<64, true, true>(tq, tk, tv, tdo, tdk, tdv, p, o, o_f32, dout, lse, lse2, dvec, stream,
-                                              dev)
-               : launch_bwd_t<64, false, true>(tq, tk, tv, tdo, tdk, tdv, p, o, o_f32, dout, lse, lse2, dvec, stream,
-                                               dev);
+    auto launch = [&](auto dim, auto out32, auto with_bias) {
+        return launch_bwd_t<decltype(dim)::value, decltype(out32)::value, true, decltype(with_bias)::value>(
+            tq, tk, tv, tdo, tdk, tdv, p, o, o_f32, dout, lse, lse2, dvec, dtable, stream, dev);
+    };
+    auto by_dim = [&](auto out32, auto with_bias) {
+        return pad_head_dim(d) == 128 ? launch(std::integral_constant<int, 128>{}, out32, with_bias)
+                                      : launch(std::integral_constant<int, 64>{}, out32, with_bias);
+    };
+    auto by_type = [&](auto with_bias) {
+        return g32 ? by_dim(std::true_type{}, with_bias) : by_dim(std::false_type{}, with_bias);
+    };
+    return bias ? by_type(std::true_type{}) : by_type(std::false_type{});
 }
 
 size_t bwd_workspace_bytes(int B, int Hq, int Nq, int d) {
@@ -2414,7 +2755,7 @@ attn_status_t launch_bwd(const void* q, const void* k, const void* v, const void
                          const void* dout, const float* lse, void* dq, void* dk, void* dv, int B,
                          int Hq, int Hkv, int Nq, int Nk, int d, int causal, float scale,
                          attn_out_dtype_t o_dtype, attn_out_dtype_t grad_dtype, void* workspace,
-                         cudaStream_t stream, const DeviceInfo& dev) {
+                         cudaStream_t stream, const DeviceInfo& dev, const BiasArgs* bias, float* dtable) {
     BwdParams p;
     p.B = B;
     p.Hq = Hq;
@@ -2447,6 +2788,8 @@ attn_status_t launch_bwd(const void* q, const void* k, const void* v, const void
     p.dv = dv;
     p.cu_q = p.cu_k = nullptr;
     p.total_q = p.total_k = p.vstride = 0;
+    p.bias = bias ? *bias : BiasArgs{};
+    p.partial = dvec + rows;
     if ((long long)B * Hkv * p.n_kt >= (1ll << 31) ||
         (long long)B * Hq * (p.Nq_pad / kBT) >= (1ll << 31))
         return ATTN_ERR_UNSUPPORTED;
@@ -2471,9 +2814,10 @@ attn_status_t launch_bwd(const void* q, const void* k, const void* v, const void
                    : launch_bwd_wide_t<false>(tq, tk, tv, tdo, tq64, tk64, tv64, tdo64, p, o, o_f32,
                                               dout, lse, lse2, dvec, stream, dev);
     }
+    // dK / dV output maps for the d = 128 kernel's staged stores: boxes of 32
+    // rows x 128 bytes
+    CUtensorMap tdk = tq, tdv = tq;
     if (pad_head_dim(d) == 128) {
-        // dK / dV output maps for the staged stores: boxes of 32 rows x 128 bytes
-        CUtensorMap tdk, tdv;
         if (g32) {
             if ((st = encode_tmap_f32_sw128_3d(&tdk, dk, d, Nk, (long long)B * Hkv, 32)) != ATTN_OK) return st;
             if ((st = encode_tmap_f32_sw128_3d(&tdv, dv, d, Nk, (long long)B * Hkv, 32)) != ATTN_OK) return st;
@@ -2481,15 +2825,19 @@ attn_status_t launch_bwd(const void* q, const void* k, const void* v, const void
             if ((st = encode_tmap_bf16_3d(&tdk, dk, d, Nk, (long long)B * Hkv, 32)) != ATTN_OK) return st;
             if ((st = encode_tmap_bf16_3d(&tdv, dv, d, Nk, (long long)B * Hkv, 32)) != ATTN_OK) return st;
         }
-        return g32 ? launch_bwd_t<128, true>(tq, tk, tv, tdo, tdk, tdv, p, o, o_f32, dout, lse, lse2, dvec, stream,
-                                             dev)
-                   : launch_bwd_t<128, false>(tq, tk, tv, tdo, tdk, tdv, p, o, o_f32, dout, lse, lse2, dvec, stream,
-                                              dev);
     }
-    if (pad_head_dim(d) == 64)
-        return g32 ? launch_bwd_t<64, true>(tq, tk, tv, tdo, tq, tq, p, o, o_f32, dout, lse, lse2, dvec, stream, dev)
-                   : launch_bwd_t<64, false>(tq, tk, tv, tdo, tq, tq, p, o, o_f32, dout, lse, lse2, dvec, stream, dev);
-    return ATTN_ERR_UNSUPPORTED;
+    auto launch = [&](auto dim, auto out32, auto with_bias) {
+        return launch_bwd_t<decltype(dim)::value, decltype(out32)::value, false, decltype(with_bias)::value>(
+            tq, tk, tv, tdo, tdk, tdv, p, o, o_f32, dout, lse, lse2, dvec, dtable, stream, dev);
+    };
+    auto by_dim = [&](auto out32, auto with_bias) {
+        return pad_head_dim(d) == 128 ? launch(std::integral_constant<int, 128>{}, out32, with_bias)
+                                      : launch(std::integral_constant<int, 64>{}, out32, with_bias);
+    };
+    auto by_type = [&](auto with_bias) {
+        return g32 ? by_dim(std::true_type{}, with_bias) : by_dim(std::false_type{}, with_bias);
+    };
+    return bias ? by_type(std::true_type{}) : by_type(std::false_type{});
 }
 
 }  // namespace gb300

@@ -33,7 +33,9 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
+#include "bias.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -72,6 +74,7 @@ struct DecParams {
     const int* block_table;
     int page_size, max_blocks;
     int dh;    // the tensors' head dim (<= D: columns past dh are zeros in the tiles)
+    BiasArgs bias;  // the BIAS instantiations
 };
 
 // Arrival counters of the in-kernel merge: one per (b, KV head) group and
@@ -113,7 +116,7 @@ __device__ __forceinline__ uint32_t swz_off(int key, int ch) {
     return (uint32_t)((ch >> 3) * (kStageKeys * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
 }
 
-template <int D, bool OUT_F32>
+template <int D, bool OUT_F32, bool BIAS>
 __global__ void __launch_bounds__(kDecThreads)
 attn_decode_split_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                          const __nv_bfloat16* __restrict__ q, const int* __restrict__ seqlens,
@@ -241,9 +244,36 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tk, const __grid_co
     const float c = p.c;
     const int wk0 = warp * 16;
     bool ok = true;
+    // BIAS: the query is at the last key; rows past the group take head 0's bias
+    const int h0 = g * G + (qr < G ? qr : 0), h1 = g * G + (qr + 8 < G ? qr + 8 : 0);
+    float left0 = 0.f, left1 = 0.f, right0 = 0.f, right1 = 0.f;
+    if constexpr (BIAS) {
+        const int last = p.bias.first + p.bias.span - 1;
+        left0 = bias_at(p.bias, p.Hq, h0, p.bias.first, err);
+        left1 = bias_at(p.bias, p.Hq, h1, p.bias.first, err);
+        right0 = bias_at(p.bias, p.Hq, h0, last, err);
+        right1 = bias_at(p.bias, p.Hq, h1, last, err);
+    }
 
     for (int st = 0; st < n_stages; ++st) {
         const int slot = st % kDecStages;
+        // BIAS: this thread's 4 keys x 2 heads, looked up while the stage arrives.  A
+        // stage wholly before the map (most of a long cache) or past it has one a head.
+        float bv[2][4];
+        if constexpr (BIAS) {
+            const int r0 = t0 + st * kStageKeys - (L - 1);   // the stage's first distance
+            const bool before = r0 + kStageKeys - 1 <= p.bias.first;
+            const bool near = !before && r0 < p.bias.first + p.bias.span - 1;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (near)
+                        bv[nt][e] = bias_at(p.bias, p.Hq, e < 2 ? h0 : h1, r0 + wk0 + nt * 8 + 2 * qc + (e & 1), err);
+                    else
+                        bv[nt][e] = e < 2 ? (before ? left0 : right0) : (before ? left1 : right1);
+                }
+        }
         // warp-uniform: ldmatrix and mma.sync below need every lane
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&full[slot]), (st / kDecStages) & 1, abort_flag));
         if (!ok) break;
@@ -285,7 +315,8 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tk, const __grid_co
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int key = wk0 + nt * 8 + 2 * qc + (e & 1);
-                    const float v = key < nvalid ? sfr[nt][e] * c : -INFINITY;
+                    const float sc = BIAS ? fmaf(sfr[nt][e], c, bv[nt][e]) : sfr[nt][e] * c;
+                    const float v = key < nvalid ? sc : -INFINITY;
                     x[nt][e] = v;
                     if (e < 2) mx0 = fmaxf(mx0, v); else mx1 = fmaxf(mx1, v);
                 }
@@ -294,16 +325,18 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tk, const __grid_co
             mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, 1));
             mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, 2));
             const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-            // mn is finite: key wk0 (< nvalid) is unmasked in every row
-            const float a0 = ex2(m0 - mn0), a1 = ex2(m1 - mn1);
+            // mn is finite: key wk0 (< nvalid) is unmasked in every row (unless its
+            // bias is -inf: exponents are then taken relative to 0, and P = 0)
+            const float mu0 = BIAS && mn0 == -INFINITY ? 0.f : mn0, mu1 = BIAS && mn1 == -INFINITY ? 0.f : mn1;
+            const float a0 = ex2(m0 - mu0), a1 = ex2(m1 - mu1);
             m0 = mn0;
             m1 = mn1;
             uint32_t pa[4];
             float ps0 = 0.f, ps1 = 0.f, px0 = 0.f, px1 = 0.f;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-                const float e0 = ex2(x[nt][0] - mn0), e1 = ex2(x[nt][1] - mn0);
-                const float e2 = ex2(x[nt][2] - mn1), e3 = ex2(x[nt][3] - mn1);
+                const float e0 = ex2(x[nt][0] - mu0), e1 = ex2(x[nt][1] - mu0);
+                const float e2 = ex2(x[nt][2] - mu1), e3 = ex2(x[nt][3] - mu1);
                 const uint32_t lo = pack_bf16x2(e0, e1);
                 const uint32_t hi = pack_bf16x2(e2, e3);
                 ps0 += bf16lo_to_f32(lo) + bf16hi_to_f32(lo);
@@ -393,7 +426,7 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tk, const __grid_co
             xsum += wt * sx[w * kMaxGroup + h];
             acc += wt * so[(w * kMaxGroup + h) * D + col];
         }
-        const float val = acc / wsum;
+        const float val = BIAS && wsum == 0.f ? 0.f : acc / wsum;   // (no key at all: 0 and -inf)
         const float lse2 = M + log2f(xsum);
         const size_t bh = (size_t)b * p.Hq + (size_t)g * G + h;
         if (nsplit_b == 1) {
@@ -437,14 +470,14 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tk, const __grid_co
         for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
         float sum = 0.f;
         for (int sp = lane; sp < nsplit_b; sp += 32) {
-            const float w = ex2(s_w[h * nsplit_b + sp] - M);
+            const float w = BIAS && M == -INFINITY ? 0.f : ex2(s_w[h * nsplit_b + sp] - M);
             s_w[h * nsplit_b + sp] = w;
             sum += w;
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
         if (lane == 0) {
-            s_head[2 * h] = 1.0f / sum;
+            s_head[2 * h] = BIAS && sum == 0.f ? 0.f : 1.0f / sum;
             s_head[2 * h + 1] = (M + log2f(sum)) * kLn2f;
         }
     }
@@ -483,7 +516,7 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tk, const __grid_co
     if (tid == 0) *count = 0u;
 }
 
-template <int D, bool OUT_F32>
+template <int D, bool OUT_F32, bool BIAS>
 __global__ void __launch_bounds__(D)
 attn_decode_combine_kernel(const int* __restrict__ seqlens, const float* __restrict__ ws_o,
                            const float* __restrict__ ws_lse, void* __restrict__ o,
@@ -504,11 +537,11 @@ attn_decode_combine_kernel(const int* __restrict__ seqlens, const float* __restr
         for (int s = 0; s < ns; ++s) M = fmaxf(M, ls[s]);
         float wsum = 0.f, acc = 0.f;
         for (int s = 0; s < ns; ++s) {
-            const float w = ex2(ls[s] - M);
+            const float w = BIAS && M == -INFINITY ? 0.f : ex2(ls[s] - M);
             wsum += w;
             acc += w * ws_o[(bh * p.max_splits + s) * D + col];
         }
-        val = acc / wsum;
+        val = BIAS && wsum == 0.f ? 0.f : acc / wsum;
         lse_nat = (M + log2f(wsum)) * kLn2f;
     }
     if (col < p.dh) {
@@ -518,14 +551,14 @@ attn_decode_combine_kernel(const int* __restrict__ seqlens, const float* __restr
     if (col == 0 && lse) lse[bh] = lse_nat;
 }
 
-template <int D, bool OUT_F32>
+template <int D, bool OUT_F32, bool BIAS>
 attn_status_t launch_decode_t(const CUtensorMap& tk, const CUtensorMap& tv, const void* q,
                               const int* seqlens, void* o, float* lse, float* ws_o, float* ws_lse,
                               const DecParams& p, cudaStream_t stream, const DeviceInfo& dev) {
     using C = DecCfg<D>;
     static int attr_set[64] = {0};
     if (dev.device < 64 && !attr_set[dev.device]) {
-        if (cudaFuncSetAttribute(attn_decode_split_kernel<D, OUT_F32>,
+        if (cudaFuncSetAttribute(attn_decode_split_kernel<D, OUT_F32, BIAS>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::kSmemBytes) != cudaSuccess)
             return ATTN_ERR_CUDA;
@@ -533,13 +566,13 @@ attn_status_t launch_decode_t(const CUtensorMap& tk, const CUtensorMap& tv, cons
     }
     const DecParams& pk = p;
     dim3 grid((unsigned)p.max_splits, (unsigned)p.Hkv, (unsigned)p.B);
-    attn_decode_split_kernel<D, OUT_F32><<<grid, kDecThreads, C::kSmemBytes, stream>>>(
+    attn_decode_split_kernel<D, OUT_F32, BIAS><<<grid, kDecThreads, C::kSmemBytes, stream>>>(
         tk, tv, static_cast<const __nv_bfloat16*>(q), seqlens, o, lse, ws_o, ws_lse, pk,
         dev.err_word);
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
     if (pk.slot >= 0) return ATTN_OK;  // merged in the split kernel
     dim3 cgrid((unsigned)p.Hq, (unsigned)p.B);
-    attn_decode_combine_kernel<D, OUT_F32><<<cgrid, D, 0, stream>>>(seqlens, ws_o, ws_lse, o, lse, pk);
+    attn_decode_combine_kernel<D, OUT_F32, BIAS><<<cgrid, D, 0, stream>>>(seqlens, ws_o, ws_lse, o, lse, pk);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -579,22 +612,25 @@ namespace {
 attn_status_t launch_decode_common(const CUtensorMap& tk, const CUtensorMap& tv, const void* q,
                                    const int* seqlens, void* o, float* lse, DecParams& p, int d,
                                    void* workspace, attn_out_dtype_t o_dtype, cudaStream_t stream,
-                                   const DeviceInfo& dev) {
+                                   const DeviceInfo& dev, bool bias) {
     d = decode_pad_head_dim(d);  // the kernel's tile width (columns past p.dh are zeros)
     const size_t rows = (size_t)p.B * p.Hq * p.max_splits;
     float* ws_o = static_cast<float*>(workspace);
     float* ws_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align16(rows * d * 4));
     const bool f32 = o_dtype == ATTN_OUT_F32;
+    auto launch = [&](auto dim, auto out32, auto with_bias) {
+        return launch_decode_t<decltype(dim)::value, decltype(out32)::value, decltype(with_bias)::value>(
+            tk, tv, q, seqlens, o, lse, ws_o, ws_lse, p, stream, dev);
+    };
+    auto by_dim = [&](auto out32, auto with_bias) {
+        return d == 128 ? launch(std::integral_constant<int, 128>{}, out32, with_bias)
+                        : launch(std::integral_constant<int, 64>{}, out32, with_bias);
+    };
+    if (bias) return f32 ? by_dim(std::true_type{}, std::true_type{}) : by_dim(std::false_type{}, std::true_type{});
     if (d == 256)
-        return f32 ? launch_decode_t<256, true>(tk, tv, q, seqlens, o, lse, ws_o, ws_lse, p, stream, dev)
-                   : launch_decode_t<256, false>(tk, tv, q, seqlens, o, lse, ws_o, ws_lse, p, stream, dev);
-    if (d == 128)
-        return f32 ? launch_decode_t<128, true>(tk, tv, q, seqlens, o, lse, ws_o, ws_lse, p, stream, dev)
-                   : launch_decode_t<128, false>(tk, tv, q, seqlens, o, lse, ws_o, ws_lse, p, stream, dev);
-    if (d == 64)
-        return f32 ? launch_decode_t<64, true>(tk, tv, q, seqlens, o, lse, ws_o, ws_lse, p, stream, dev)
-                   : launch_decode_t<64, false>(tk, tv, q, seqlens, o, lse, ws_o, ws_lse, p, stream, dev);
-    return ATTN_ERR_UNSUPPORTED;  // d is the padded head dim here
+        return f32 ? launch(std::integral_constant<int, 256>{}, std::true_type{}, std::false_type{})
+                   : launch(std::integral_constant<int, 256>{}, std::false_type{}, std::false_type{});
+    return f32 ? by_dim(std::true_type{}, std::false_type{}) : by_dim(std::false_type{}, std::false_type{});
 }
 
 DecParams make_dec_params(int B, int Hq, int Hkv, int Nmax, int d, float scale, int chunk) {
@@ -615,6 +651,7 @@ DecParams make_dec_params(int B, int Hq, int Hkv, int Nmax, int d, float scale, 
     p.page_size = 0;
     p.max_blocks = 0;
     p.dh = d;
+    p.bias = BiasArgs{};
     return p;
 }
 }  // namespace
@@ -628,24 +665,26 @@ attn_status_t launch_decode(const void* q, const void* k_cache, const void* v_ca
     attn_status_t st;
     if ((st = encode_tmap_bf16_3d(&tk, k_cache, d, Nmax, (long long)B * Hkv, kStageKeys)) != ATTN_OK) return st;
     if ((st = encode_tmap_bf16_3d(&tv, v_cache, d, Nmax, (long long)B * Hkv, kStageKeys)) != ATTN_OK) return st;
-    return launch_decode_common(tk, tv, q, seqlens, o, lse, p, d, workspace, o_dtype, stream, dev);
+    return launch_decode_common(tk, tv, q, seqlens, o, lse, p, d, workspace, o_dtype, stream, dev, false);
 }
 
 attn_status_t launch_decode_paged(const void* q, const void* k_pages, const void* v_pages,
                                   const int* block_table, const int* seqlens, void* o, float* lse,
                                   int B, int Hq, int Hkv, long long num_blocks, int page_size,
                                   int max_blocks, int d, float scale, int chunk, void* workspace,
-                                  attn_out_dtype_t o_dtype, cudaStream_t stream, const DeviceInfo& dev) {
+                                  attn_out_dtype_t o_dtype, cudaStream_t stream, const DeviceInfo& dev,
+                                  const BiasArgs* bias) {
     const int Nmax = max_blocks * page_size;
     DecParams p = make_dec_params(B, Hq, Hkv, Nmax, d, scale, chunk);
     p.block_table = block_table;
     p.page_size = page_size;
     p.max_blocks = max_blocks;
+    if (bias) p.bias = *bias;
     CUtensorMap tk, tv;
     attn_status_t st;
     if ((st = encode_tmap_paged_kv(&tk, k_pages, d, Hkv, page_size, num_blocks)) != ATTN_OK) return st;
     if ((st = encode_tmap_paged_kv(&tv, v_pages, d, Hkv, page_size, num_blocks)) != ATTN_OK) return st;
-    return launch_decode_common(tk, tv, q, seqlens, o, lse, p, d, workspace, o_dtype, stream, dev);
+    return launch_decode_common(tk, tv, q, seqlens, o, lse, p, d, workspace, o_dtype, stream, dev, bias != nullptr);
 }
 
 }  // namespace gb300

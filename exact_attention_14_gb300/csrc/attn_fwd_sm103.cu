@@ -46,7 +46,9 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
+#include "bias.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 #include "fwd_sched.h"
@@ -99,6 +101,7 @@ struct FwdParams {
     const int* cu_q;  // [B + 1] row offsets of the sequences in the packed Q / O
     const int* cu_k;  // [B + 1] row offsets in the packed K / V
     int total_q, total_k;
+    BiasArgs bias;    // the BIAS instantiations
 };
 
 // Work queues.  Per slot: word 0 the ticket counter (the next work item),
@@ -141,6 +144,7 @@ struct __align__(8) Bars {
     uint64_t kv_full[8], kv_empty[8];
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t unit_full[2], unit_empty[2];
+    uint64_t win_full[2];  // BIAS: a Q tile's next window is filled (its 4 softmax warps)
     uint64_t drain;
     WorkItem item[2];
     uint32_t tmem_base;
@@ -494,10 +498,23 @@ __device__ void run_mma(uint8_t* smem, Bars* bars, uint32_t tmem, const FwdParam
 // denominator, for the LSE) and l, which normalises O: lx plus the rounding
 // error of the tile's largest P, so that the weight of the dominant key of a
 // tile in O is exactly its rounded P over the sum.
-template <int D, bool MASKED>
+//
+// With a bias (BM: kBiasConst, one value bc for the tile; kBiasTile, a value per
+// distance, column c's at shared address win + 4 c) x = s*c + bias takes the place
+// of s*c: a window is added before the maximum, a constant to it and to the
+// exponent's own term.  A row whose keys all have bias -inf so far has m = -inf;
+// its exponents are taken relative to 0 instead, so P = 0 and l = lx = 0.
+enum : int { kBiasNone = 0, kBiasConst = 1, kBiasTile = 2 };
+
+template <int D, bool MASKED, int BM = kBiasNone>
 __device__ __forceinline__ void softmax_tile(uint32_t (&sr)[128], int lim, int j, float c,
                                              uint32_t tS, uint32_t tO, float& m, float& l,
-                                             float& lx) {
+                                             float& lx, float bc = 0.f, uint32_t win = 0) {
+    if constexpr (BM == kBiasTile) {
+#pragma unroll
+        for (int cc = 0; cc < 128; ++cc)
+            sr[cc] = __float_as_uint(fmaf(__uint_as_float(sr[cc]), c, lds_f32(win + 4 * cc)));
+    }
     if constexpr (MASKED) {
 #pragma unroll
         for (int cc = 0; cc < 128; ++cc)
@@ -511,11 +528,12 @@ __device__ __forceinline__ void softmax_tile(uint32_t (&sr)[128], int lim, int j
         mx2 = fmax3(mx2, __uint_as_float(sr[cc + 4]), __uint_as_float(sr[cc + 5]));
         mx3 = fmax3(mx3, __uint_as_float(sr[cc + 6]), __uint_as_float(sr[cc + 7]));
     }
-    const float mt = fmax3(fmaxf(mx0, mx1), mx2, mx3) * c;
+    const float mr = fmax3(fmaxf(mx0, mx1), mx2, mx3);
+    const float mt = BM == kBiasTile ? mr : BM == kBiasConst ? fmaf(mr, c, bc) : mr * c;
     const bool need = mt > m + kTau;
     if (__any_sync(0xFFFFFFFFu, need)) {
         const float m_new = fmaxf(m, mt);
-        const float alpha = ex2(m - m_new);
+        const float alpha = ex2(m - (BM != kBiasNone && m_new == -INFINITY ? 0.f : m_new));
         l *= alpha;
         lx *= alpha;
         if (j > 0) {
@@ -538,13 +556,16 @@ __device__ __forceinline__ void softmax_tile(uint32_t (&sr)[128], int lim, int j
         }
         m = m_new;
     }
+    // the exponent's constant term: -m, with a tile's one bias in it
+    const float mu = BM != kBiasNone && m == -INFINITY ? 0.f : m;
+    const float nm = BM == kBiasConst ? bc - mu : -mu;
     // rounding error of the tile's largest probability (same arithmetic as below)
     {
-        const float pmax = ex2(fmaf(fmax3(fmaxf(mx0, mx1), mx2, mx3), c, -m));
+        const float pmax = ex2(BM == kBiasTile ? mr + nm : fmaf(mr, c, nm));
         l += bf16lo_to_f32(pack_bf16x2(pmax, 0.f)) - pmax;
     }
     // p = 2^(s*c - m) on pairs; P rounded to bf16 into TMEM; unrounded row sum
-    const uint64_t c2 = f2(c, c), nm2 = f2(-m, -m);
+    const uint64_t c2 = f2(c, c), nm2 = f2(nm, nm);
     uint64_t acc_x0 = 0, acc_x1 = 0, acc_x2 = 0, acc_x3 = 0;  // (0.f, 0.f) pairs
 #pragma unroll
     for (int cc = 0; cc < 4; ++cc) {
@@ -553,7 +574,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t (&sr)[128], int lim, int j
         for (int i = 0; i < 16; ++i) {
             const int col = cc * 32 + 2 * i;
             float x0, x1;
-            f2_split(f2_fma(f2(__uint_as_float(sr[col]), __uint_as_float(sr[col + 1])), c2, nm2), x0, x1);
+            const uint64_t s2 = f2(__uint_as_float(sr[col]), __uint_as_float(sr[col + 1]));
+            f2_split(BM == kBiasTile ? f2_add(s2, nm2) : f2_fma(s2, c2, nm2), x0, x1);
             float p0 = ex2(x0), p1 = ex2(x1);
             if constexpr (MASKED) {
                 p0 = col <= lim ? p0 : 0.f;
@@ -582,7 +604,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t (&sr)[128], int lim, int j
 // store_o_pairs): staged 32 rows x 64 bytes at a time in shared memory (two
 // buffers per warp) and written by TMA stores (rows past Nq are clipped by the
 // hardware).  Packed batches are never split, so the rows are (row0, bh).
-template <bool OUT_F32>
+// BIAS: the warp's second buffer holds bias windows, so every box takes the first.
+template <bool OUT_F32, bool BIAS>
 __device__ __forceinline__ void store_o_cols(const float (&v)[32], int cc, uint8_t* stg,
                                              uint32_t& epi_buf, int lane, const CUtensorMap* to,
                                              int row0, int bh, int d_act) {
@@ -591,8 +614,8 @@ __device__ __forceinline__ void store_o_cols(const float (&v)[32], int cc, uint8
     for (int h = 0; h < 32 / kCols; ++h) {
         if (cc + h * kCols >= d_act) break;  // columns past the head dim (a box that
                                              // crosses it is clipped by the hardware)
-        uint8_t* buf = stg + (epi_buf & 1) * 2048;
-        if (lane == 0) bulk_wait_group_read<1>();  // this buffer's previous store has read it
+        uint8_t* buf = stg + (BIAS ? 0 : (epi_buf & 1) * 2048);
+        if (lane == 0) bulk_wait_group_read<BIAS ? 0 : 1>();  // this buffer's previous store has read it
         __syncwarp();
         const uint32_t dst = smem_u32(buf) + lane * 64;
         if constexpr (OUT_F32) {
@@ -673,14 +696,15 @@ __device__ __forceinline__ void store_o_pairs(const float (&v)[32], int cc, int 
 //   O = sum_p w_p l_p (O_p / l_p) / sum_p w_p l_p,
 //   LSE = ln2 * (M + log2 sum_p w_p lx_p).
 // Kept out of line so that its registers do not weigh on the softmax loop.
-template <int D, bool OUT_F32>
+// BIAS: a row may have no key in a piece, or in any (m = -inf, l = 0): it weighs 0.
+template <int D, bool OUT_F32, bool BIAS>
 __device__ __noinline__ void split_piece_epilogue(unsigned int* merge_count, float* partial,
                                                   int parts, uint32_t cell, int part, int lane,
                                                   uint32_t tO, float m, float l, float lx,
                                                   uint8_t* stg, uint32_t* epi_buf,
                                                   const CUtensorMap* to, int row0, int bh,
                                                   float* lse_out, int d_act) {
-    const float inv_l = 1.0f / l;
+    const float inv_l = BIAS && l == 0.f ? 0.f : 1.0f / l;
     float* blocks = partial + (size_t)cell * parts * partial_block_floats<D>();
     float* mine = blocks + (size_t)part * partial_block_floats<D>();
 #pragma unroll 1
@@ -726,12 +750,12 @@ __device__ __noinline__ void split_piece_epilogue(unsigned int* merge_count, flo
     float w[kMaxSplitParts];
 #pragma unroll
     for (int q = 0; q < kMaxSplitParts; ++q) {
-        const float e = ex2(mq[q] - mmax);  // 0 for absent pieces
+        const float e = BIAS && mq[q] == -INFINITY ? 0.f : ex2(mq[q] - mmax);  // 0 for absent pieces
         w[q] = e * lq[q];
         wsum += w[q];
         wxsum += e * lxq[q];
     }
-    const float inv_w = 1.0f / wsum;
+    const float inv_w = BIAS && wsum == 0.f ? 0.f : 1.0f / wsum;
 #pragma unroll
     for (int q = 0; q < kMaxSplitParts; ++q) w[q] *= inv_w;  // weight of piece q's O / l
     const int q0 = part == 0 ? 1 : 0;
@@ -771,12 +795,12 @@ __device__ __noinline__ void split_piece_epilogue(unsigned int* merge_count, flo
                 for (int i = 0; i < 32; ++i) v[i] = fmaf(wq_, __ldcg(bq + i * 32), v[i]);
             }
         }
-        store_o_cols<OUT_F32>(v, cc, stg, *epi_buf, lane, to, row0, bh, d_act);
+        store_o_cols<OUT_F32, BIAS>(v, cc, stg, *epi_buf, lane, to, row0, bh, d_act);
     }
     if (lse_out) *lse_out = (mmax + log2f(wxsum)) * kLn2;
 }
 
-template <int D, bool OUT_F32, bool VARLEN>
+template <int D, bool OUT_F32, bool VARLEN, bool BIAS>
 __device__ void run_softmax(int t, int wq, int lane, uint8_t* smem, Bars* bars, uint32_t tmem,
                             const FwdParams& p, const CUtensorMap* to, float* __restrict__ lse_ptr,
                             unsigned int* err) {
@@ -793,6 +817,11 @@ __device__ void run_softmax(int t, int wq, int lane, uint8_t* smem, Bars* bars, 
     uint8_t* stg = smem + C::kStgOff + (t * 4 + wq) * C::kStgBytesPerWarp;
     uint32_t epi_buf = 0;
     uint32_t cnt_s = 0, cnt_o = 0;
+    // BIAS: the Q tile's two windows (in the second store buffer of its first
+    // warp), how many were filled and how many read
+    const uint32_t win0 = smem_u32(smem + C::kStgOff + t * 4 * C::kStgBytesPerWarp + 2048);
+    const uint32_t bar_w = smem_u32(&bars->win_full[t]);
+    uint32_t cnt_fill = 0, cnt_win = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
         WorkItem w;
@@ -810,6 +839,43 @@ __device__ void run_softmax(int t, int wq, int lane, uint8_t* smem, Bars* bars, 
             const int lk = row + (VARLEN ? nk - nq : p.off);
             last_key = lk < last_key ? lk : last_key;
         }
+        // BIAS: a tile's distances start at 128 j + base0; tiles inside the map, and
+        // masked ones (an instantiation less), read a window.  The warps fill the
+        // next tile's once they have read this one's: whoever fills a buffer again
+        // has seen all four warps' arrivals for the window in between, each after
+        // its reads of the buffer's last.  (A window's bucket and table entries are
+        // fetched a whole tile before they are stored.)
+        const int off = VARLEN ? nk - nq : p.off;
+        const int hq_b = BIAS ? bh - (bh / s.Hq) * s.Hq : 0;
+        const int row0 = mb * kUnitRows + t * kTileM;
+        const int base0 = -(row0 + kTileM - 1) - off;
+        const int lim0 = s.causal && row0 + off < nk - 1 ? row0 + off : nk - 1;
+        float bias_l = 0.f, bias_r = 0.f, wv0 = 0.f, wv1 = 0.f;
+        auto windowed = [&](int j) {
+            return bias_near(p.bias, base0 + j * kTileN) || lim0 - j * kTileN < kTileN - 1;
+        };
+        auto fetch = [&](int j) {
+            const int r = base0 + j * kTileN + wq * 32 + lane;
+            wv0 = bias_at(p.bias, s.Hq, hq_b, r, err);
+            wv1 = bias_at(p.bias, s.Hq, hq_b, r + 128, err);
+        };
+        auto fill = [&]() {
+            const uint32_t a = win0 + (cnt_fill & 1) * (kBiasWindow * 4) + (wq * 32 + lane) * 4;
+            sts_f32(a, wv0);
+            sts_f32(a + 512, wv1);
+            ++cnt_fill;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_w);
+        };
+        if constexpr (BIAS) {
+            bias_l = bias_at(p.bias, s.Hq, hq_b, p.bias.first, err);
+            bias_r = bias_at(p.bias, s.Hq, hq_b, p.bias.first + p.bias.span - 1, err);
+            if (windowed(j0)) {
+                fetch(j0);
+                fill();
+            }
+            if (j0 + 1 < n_t && windowed(j0 + 1)) fetch(j0 + 1);
+        }
         float m = -INFINITY;  // running max of scaled scores, log2 units
         float l = 0.f;        // normaliser of O (see softmax_tile)
         float lx = 0.f;       // running sum of the unrounded probabilities (gives the LSE)
@@ -825,7 +891,22 @@ __device__ void run_softmax(int t, int wq, int lane, uint8_t* smem, Bars* bars, 
             tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
             tmem_wait_ld();
             const int lim = last_key - j * kTileN;  // column c allowed iff c <= lim
-            if (__any_sync(0xFFFFFFFFu, lim < kTileN - 1))
+            if constexpr (BIAS) {
+                if (windowed(j)) {
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_w, cnt_win & 1, abort_flag, 32));
+                    if (!ok) break;
+                    // column c of row i is distance base + c - i + 127
+                    const uint32_t win = win0 + (cnt_win & 1) * (kBiasWindow * 4) + (127 - wq * 32 - lane) * 4;
+                    ++cnt_win;
+                    if (__any_sync(0xFFFFFFFFu, lim < kTileN - 1))
+                        softmax_tile<D, true, kBiasTile>(sr, lim, j - j0, c, tS, tO, m, l, lx, 0.f, win);
+                    else
+                        softmax_tile<D, false, kBiasTile>(sr, lim, j - j0, c, tS, tO, m, l, lx, 0.f, win);
+                } else {
+                    softmax_tile<D, false, kBiasConst>(sr, lim, j - j0, c, tS, tO, m, l, lx,
+                                                       base0 + j * kTileN + 254 <= p.bias.first ? bias_l : bias_r);
+                }
+            } else if (__any_sync(0xFFFFFFFFu, lim < kTileN - 1))
                 softmax_tile<D, true>(sr, lim, j - j0, c, tS, tO, m, l, lx);
             else
                 softmax_tile<D, false>(sr, lim, j - j0, c, tS, tO, m, l, lx);
@@ -833,6 +914,10 @@ __device__ void run_softmax(int t, int wq, int lane, uint8_t* smem, Bars* bars, 
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_p);
+            if constexpr (BIAS) {
+                if (j + 1 < n_t && windowed(j + 1)) fill();
+                if (j + 2 < n_t && windowed(j + 2)) fetch(j + 2);
+            }
         }
         if (!ok) break;
         // Epilogue: O = O_acc / l, LSE = ln2 * (m + log2 lx)
@@ -841,7 +926,7 @@ __device__ void run_softmax(int t, int wq, int lane, uint8_t* smem, Bars* bars, 
         if (!ok) break;
         tc_fence_after();
         const bool live = row < nq;
-        const float inv_l = 1.0f / l;
+        const float inv_l = BIAS && l == 0.f ? 0.f : 1.0f / l;
         const int hq = bh - (bh / s.Hq) * s.Hq;
         // LSE: [B, Hq, Nq], or [Hq, total_q] for packed batches
         const size_t row_idx = VARLEN ? (size_t)hq * p.total_q + (size_t)(w.q0 + row)
@@ -872,9 +957,9 @@ __device__ void run_softmax(int t, int wq, int lane, uint8_t* smem, Bars* bars, 
         if constexpr (!VARLEN) {  // packed batches are never split
             // (cell: this warp's slot among the split units' merge counters and blocks)
             const uint32_t cell = w.cell + (uint32_t)t * 4u + (uint32_t)wq;
-            const int row0 = mb * kUnitRows + t * kTileM + wq * 32;
-            split_piece_epilogue<D, OUT_F32>(g_fwd_queue[p.slot] + 2, p.partial, p.split.parts, cell,
-                                             part, lane, tO, m, l, lx, stg, &epi_buf, to, row0, bh,
+            const int wrow0 = mb * kUnitRows + t * kTileM + wq * 32;
+            split_piece_epilogue<D, OUT_F32, BIAS>(g_fwd_queue[p.slot] + 2, p.partial, p.split.parts, cell,
+                                             part, lane, tO, m, l, lx, stg, &epi_buf, to, wrow0, bh,
                                              (live && lse_ptr) ? lse_ptr + row_idx : nullptr, p.d_act);
         }
     }
@@ -883,7 +968,7 @@ __device__ void run_softmax(int t, int wq, int lane, uint8_t* smem, Bars* bars, 
     if (!ok) raise_abort(bars, err);
 }
 
-template <int D, bool OUT_F32, bool VARLEN>
+template <int D, bool OUT_F32, bool VARLEN, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
@@ -903,6 +988,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             mbar_init(smem_u32(&bars->s_full[t]), 1);
             mbar_init(smem_u32(&bars->p_full[t]), 4);
             mbar_init(smem_u32(&bars->o_full[t]), 1);
+            mbar_init(smem_u32(&bars->win_full[t]), 4);
         }
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(smem_u32(&bars->kv_full[i]), 1);
@@ -936,7 +1022,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     } else {
         reg_alloc<kRegsSoftmax>();
         const int t = (warp - 4) >> 2;
-        run_softmax<D, OUT_F32, VARLEN>(t, warp & 3, lane, smem, bars, tmem, p, &to, lse_ptr, err);
+        run_softmax<D, OUT_F32, VARLEN, BIAS>(t, warp & 3, lane, smem, bars, tmem, p, &to, lse_ptr, err);
     }
     tc_fence_before();
     __syncthreads();
@@ -962,25 +1048,25 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     }
 }
 
-template <int D, bool OUT_F32, bool VARLEN = false>
+template <int D, bool OUT_F32, bool VARLEN, bool BIAS>
 attn_status_t launch_fwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const CUtensorMap& to, float* lse, const FwdParams& p, int grid,
                            cudaStream_t stream, const DeviceInfo& dev) {
     using C = FwdCfg<D>;
     static int attr_set[64] = {0};
     if (dev.device < 64 && !attr_set[dev.device]) {
-        if (cudaFuncSetAttribute(attn_fwd_kernel<D, OUT_F32, VARLEN>,
+        if (cudaFuncSetAttribute(attn_fwd_kernel<D, OUT_F32, VARLEN, BIAS>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::kSmemBytes) != cudaSuccess)
             return ATTN_ERR_CUDA;
         attr_set[dev.device] = 1;
     }
-    attn_fwd_kernel<D, OUT_F32, VARLEN><<<(unsigned)grid, kThreads, C::kSmemBytes, stream>>>(
+    attn_fwd_kernel<D, OUT_F32, VARLEN, BIAS><<<(unsigned)grid, kThreads, C::kSmemBytes, stream>>>(
         tq, tk, tv, to, lse, p, dev.err_word);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-template <int D, bool OUT_F32>
+template <int D, bool OUT_F32, bool BIAS>
 attn_status_t launch_with_partials(const CUtensorMap& tq, const CUtensorMap& tk,
                                    const CUtensorMap& tv, const CUtensorMap& to, float* lse,
                                    FwdParams& p, int grid, void* workspace, cudaStream_t stream,
@@ -988,7 +1074,7 @@ attn_status_t launch_with_partials(const CUtensorMap& tq, const CUtensorMap& tk,
     // the split units' partial results live in the caller's workspace
     // (fwd_workspace_bytes of it, checked by the caller of launch_fwd)
     p.partial = p.split.n_split > 0 ? static_cast<float*>(workspace) : nullptr;
-    return launch_fwd_t<D, OUT_F32>(tq, tk, tv, to, lse, p, grid, stream, dev);
+    return launch_fwd_t<D, OUT_F32, false, BIAS>(tq, tk, tv, to, lse, p, grid, stream, dev);
 }
 
 uint32_t next_queue_slot() {
@@ -1009,7 +1095,7 @@ size_t fwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int ca
 attn_status_t launch_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
                          int B, int Hq, int Hkv, int Nq, int Nk, int d, int causal, float scale,
                          attn_out_dtype_t o_dtype, void* workspace, cudaStream_t stream,
-                         const DeviceInfo& dev) {
+                         const DeviceInfo& dev, const BiasArgs* bias) {
     if (d > 128)
         return launch_fwd_wide(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, causal, scale, o_dtype, stream,
                                dev);
@@ -1024,6 +1110,7 @@ attn_status_t launch_fwd(const void* q, const void* k, const void* v, void* o, f
     p.split = plan_tail_split(p.shape, dev.num_sms);
     p.cu_q = p.cu_k = nullptr;
     p.total_q = p.total_k = 0;
+    p.bias = bias ? *bias : BiasArgs{};
     const uint32_t items = split_items(p.split);
     const int grid = (int)(items < (uint32_t)dev.num_sms ? items : (uint32_t)dev.num_sms);
     p.partial = nullptr;
@@ -1037,13 +1124,18 @@ attn_status_t launch_fwd(const void* q, const void* k, const void* v, void* o, f
     if ((st = encode_tmap_out_3d(&to, o, f32, d, Nq, (long long)B * Hq, kEpiCols(f32), 32)) != ATTN_OK)
         return st;
     // head dims below 64 / 128 run on those kernels (TMA zero-fills the rest)
-    if (pad_head_dim(d) == 128)
-        return f32 ? launch_with_partials<128, true>(tq, tk, tv, to, lse, p, grid, workspace, stream, dev)
-                   : launch_with_partials<128, false>(tq, tk, tv, to, lse, p, grid, workspace, stream, dev);
-    if (pad_head_dim(d) == 64)
-        return f32 ? launch_with_partials<64, true>(tq, tk, tv, to, lse, p, grid, workspace, stream, dev)
-                   : launch_with_partials<64, false>(tq, tk, tv, to, lse, p, grid, workspace, stream, dev);
-    return ATTN_ERR_UNSUPPORTED;
+    auto launch = [&](auto dim, auto out32, auto with_bias) {
+        return launch_with_partials<decltype(dim)::value, decltype(out32)::value, decltype(with_bias)::value>(
+            tq, tk, tv, to, lse, p, grid, workspace, stream, dev);
+    };
+    auto by_dim = [&](auto out32, auto with_bias) {
+        return pad_head_dim(d) == 128 ? launch(std::integral_constant<int, 128>{}, out32, with_bias)
+                                      : launch(std::integral_constant<int, 64>{}, out32, with_bias);
+    };
+    auto by_type = [&](auto with_bias) {
+        return f32 ? by_dim(std::true_type{}, with_bias) : by_dim(std::false_type{}, with_bias);
+    };
+    return bias ? by_type(std::true_type{}) : by_type(std::false_type{});
 }
 
 }  // namespace gb300
@@ -1054,7 +1146,7 @@ attn_status_t launch_fwd_varlen(const void* q, const void* k, const void* v, voi
                                 const int* cu_q, const int* cu_k, int B, int Hq, int Hkv,
                                 int total_q, int total_k, int max_q, int max_k, int d, int causal,
                                 float scale, attn_out_dtype_t o_dtype, cudaStream_t stream,
-                                const DeviceInfo& dev) {
+                                const DeviceInfo& dev, const BiasArgs* bias) {
     FwdParams p;
     // units cover every sequence at the maximum lengths; the producer skips
     // the m-blocks past each sequence's own length
@@ -1074,6 +1166,7 @@ attn_status_t launch_fwd_varlen(const void* q, const void* k, const void* v, voi
     p.cu_k = cu_k;
     p.total_q = total_q;
     p.total_k = total_k;
+    p.bias = bias ? *bias : BiasArgs{};
     const long long items = p.shape.units;
     const int grid = (int)(items < dev.num_sms ? items : dev.num_sms);
     CUtensorMap tq, tk, tv, to;
@@ -1085,13 +1178,18 @@ attn_status_t launch_fwd_varlen(const void* q, const void* k, const void* v, voi
     // (O of a packed batch is written from registers, never by this map; it
     // is still encoded, which checks O's alignment like the other maps)
     if ((st = encode_tmap_ragged(&to, o, f32, d, Hq, kEpiCols(f32), 32, false)) != ATTN_OK) return st;
-    if (pad_head_dim(d) == 128)
-        return f32 ? launch_fwd_t<128, true, true>(tq, tk, tv, to, lse, p, grid, stream, dev)
-                   : launch_fwd_t<128, false, true>(tq, tk, tv, to, lse, p, grid, stream, dev);
-    if (pad_head_dim(d) == 64)
-        return f32 ? launch_fwd_t<64, true, true>(tq, tk, tv, to, lse, p, grid, stream, dev)
-                   : launch_fwd_t<64, false, true>(tq, tk, tv, to, lse, p, grid, stream, dev);
-    return ATTN_ERR_UNSUPPORTED;
+    auto launch = [&](auto dim, auto out32, auto with_bias) {
+        return launch_fwd_t<decltype(dim)::value, decltype(out32)::value, true, decltype(with_bias)::value>(
+            tq, tk, tv, to, lse, p, grid, stream, dev);
+    };
+    auto by_dim = [&](auto out32, auto with_bias) {
+        return pad_head_dim(d) == 128 ? launch(std::integral_constant<int, 128>{}, out32, with_bias)
+                                      : launch(std::integral_constant<int, 64>{}, out32, with_bias);
+    };
+    auto by_type = [&](auto with_bias) {
+        return f32 ? by_dim(std::true_type{}, with_bias) : by_dim(std::false_type{}, with_bias);
+    };
+    return bias ? by_type(std::true_type{}) : by_type(std::false_type{});
 }
 
 }  // namespace gb300

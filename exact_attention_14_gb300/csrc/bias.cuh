@@ -1,0 +1,66 @@
+// bias.cuh -- the learned relative position bias as the attention kernels read it.
+//
+// The bias of query head h at relative distance r = (key) - (query + Nk - Nq) is
+// table[buckets[clamp(r - first, 0, span - 1)], h]: the map lists the distances
+// first .. first + span - 1, and farther ones count as its ends.  The kernels
+// hold it times log2(e), since their scores are in base 2.
+//
+// A tile of 128 query rows and 128 keys meets 255 distances, base .. base + 254.
+// Where they all lie on one side of the map (or at its end) the whole tile has one
+// bias, which costs a term of the exponent that is there anyway; other tiles take
+// theirs from a window of 256 floats in shared memory, one per distance, that the
+// warps fill a tile ahead.  Lanes of a warp hold consecutive rows, so a column's
+// 32 reads are 32 consecutive floats: no bank conflict.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "ptx.cuh"
+
+namespace gb300 {
+
+struct BiasArgs {
+    const void* table;   // [num_buckets, Hq], fp32 or bf16
+    const int* buckets;  // [span]
+    int first, span, num_buckets, bf16;
+};
+
+constexpr int kBiasWindow = 256;         // floats of one tile's window
+constexpr float kBiasLog2e = 1.44269504088896340736f;
+// A bias below this (a type's lowest value used as a mask) counts as -inf: its key
+// is left out.  Above it, bias + score keeps at least the bias's own 24 bits.
+constexpr float kBiasMasked = -1e30f;
+
+// Bias of head h at distance r, times log2(e).  A bucket outside the table adds
+// nothing and is recorded in the error word.
+__device__ __forceinline__ float bias_at(const BiasArgs& a, int Hq, int h, int r, unsigned int* err) {
+    int i = r - a.first;
+    i = i < 0 ? 0 : (i < a.span ? i : a.span - 1);
+    const int bk = __ldg(a.buckets + i);
+    if ((unsigned)bk >= (unsigned)a.num_buckets) {
+        atomicOr(err, kErrBadSeqlen);
+        return 0.f;
+    }
+    const size_t at = (size_t)bk * Hq + h;
+    const float v = a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.table)[at])
+                           : __ldg(static_cast<const float*>(a.table) + at);
+    return v < kBiasMasked ? -INFINITY : v * kBiasLog2e;
+}
+
+// Whether the 255 distances from `base` on need a window: some of them lie strictly
+// inside the map.  Otherwise all of them have the bias of its left end (base + 254
+// <= first) or of its right one.
+__device__ __forceinline__ bool bias_near(const BiasArgs& a, int base) {
+    return base + 254 > a.first && base < a.first + a.span - 1;
+}
+
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+}  // namespace gb300

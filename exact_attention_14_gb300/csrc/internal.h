@@ -27,6 +27,8 @@ struct DeviceInfo {
     unsigned int* err_word;  // device address of the library's error word
 };
 
+struct BiasArgs;  // relative position bias (bias.cuh); d <= 128 where it is given
+
 // Per-device facts for the current device, initialised once per device.
 attn_status_t current_device_info(DeviceInfo* out);
 
@@ -85,7 +87,7 @@ size_t fwd_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int ca
 attn_status_t launch_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
                          int B, int Hq, int Hkv, int Nq, int Nk, int d, int causal, float scale,
                          attn_out_dtype_t o_dtype, void* workspace, cudaStream_t stream,
-                         const DeviceInfo& dev);
+                         const DeviceInfo& dev, const BiasArgs* bias = nullptr);
 
 // Dense forward for 128 < d <= 256.
 attn_status_t launch_fwd_wide(const void* q, const void* k, const void* v, void* o, float* lse,
@@ -98,7 +100,7 @@ attn_status_t launch_fwd_varlen(const void* q, const void* k, const void* v, voi
                                 const int* cu_q, const int* cu_k, int B, int Hq, int Hkv,
                                 int total_q, int total_k, int max_q, int max_k, int d, int causal,
                                 float scale, attn_out_dtype_t o_dtype, cudaStream_t stream,
-                                const DeviceInfo& dev);
+                                const DeviceInfo& dev, const BiasArgs* bias = nullptr);
 // The same for 128 < d <= 256.
 attn_status_t launch_fwd_wide_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
                                      const int* cu_q, const int* cu_k, int B, int Hq, int Hkv,
@@ -115,12 +117,17 @@ attn_status_t launch_bwd_varlen(const void* q, const void* k, const void* v, con
                                 const int* cu_q, const int* cu_k, int B, int Hq, int Hkv, int total_q,
                                 int total_k, int max_q, int max_k, int d, int causal, float scale,
                                 attn_out_dtype_t o_dtype, attn_out_dtype_t grad_dtype,
-                                void* workspace, cudaStream_t stream, const DeviceInfo& dev);
+                                void* workspace, cudaStream_t stream, const DeviceInfo& dev,
+                                const BiasArgs* bias = nullptr, float* dtable = nullptr);
 attn_status_t launch_bwd(const void* q, const void* k, const void* v, const void* o,
                          const void* dout, const float* lse, void* dq, void* dk, void* dv, int B,
                          int Hq, int Hkv, int Nq, int Nk, int d, int causal, float scale,
                          attn_out_dtype_t o_dtype, attn_out_dtype_t grad_dtype, void* workspace,
-                         cudaStream_t stream, const DeviceInfo& dev);
+                         cudaStream_t stream, const DeviceInfo& dev, const BiasArgs* bias = nullptr,
+                         float* dtable = nullptr);
+// What the gradient of a bias table of `span` distances needs behind that
+// workspace (Nk: the longest key length of a packed batch).
+size_t bwd_bias_workspace_bytes(int B, int Hq, int Nk, int span);
 
 // Decode: the argument checks of attn_decode (pointers, alignment, shape,
 // scale, split request, output type); touches no device.
@@ -146,7 +153,18 @@ attn_status_t launch_decode_paged(const void* q, const void* k_pages, const void
                                   const int* block_table, const int* seqlens, void* o, float* lse,
                                   int B, int Hq, int Hkv, long long num_blocks, int page_size,
                                   int max_blocks, int d, float scale, int chunk, void* workspace,
-                                  attn_out_dtype_t o_dtype, cudaStream_t stream, const DeviceInfo& dev);
+                                  attn_out_dtype_t o_dtype, cudaStream_t stream, const DeviceInfo& dev,
+                                  const BiasArgs* bias = nullptr);
+
+// The paged cache's tables (attn_pages_sm103.cu).
+attn_status_t launch_pages_init(int* pool, int num_blocks, cudaStream_t stream);
+attn_status_t launch_pages_extend(int* pool, int num_blocks, int* block_table, int* seqlens, const int* new_lens,
+                                  long long* slots, int* positions, int* cu_seqlens, int* granted, int B,
+                                  int max_blocks, int page_size, int width, long long total,
+                                  cudaStream_t stream, const DeviceInfo& dev);
+attn_status_t launch_pages_trim(int* pool, int num_blocks, const int* block_table, int* seqlens,
+                                const int* keep_lens, int B, int max_blocks, int page_size,
+                                cudaStream_t stream, const DeviceInfo& dev);
 
 // Rotary positions of q [B, Hq, N, d] and k [B, Hkv, N, d] (k may be NULL);
 // strides are {batch, head, token} in elements.

@@ -25,6 +25,11 @@
  *                online softmax" section 7.1), with query heads that share a
  *                KV head packed as rows of one tile (lecture notes 6.2);
  *                attn_decode_paged reads the cache through a block table;
+ *   attn_fwd_bias, attn_fwd_varlen_bias, attn_bwd_bias, attn_bwd_varlen_bias,
+ *   attn_decode_paged_bias  the same with a learned relative position bias, and
+ *                the gradient of its table;
+ *   attn_pages_extend, attn_pages_trim  block tables, slots and positions of new
+ *                tokens from the requests' lengths, and pages taken back;
  *   attn_rope    rotary positions on Q and K, and their gradient;
  *   attn_cache_write, attn_cache_read  keys and values into a paged cache (bf16
  *                or E4M3 with a descale per row) and back;
@@ -588,6 +593,177 @@ attn_status_t attn_decode_tree(const void* q, const void* k_pages, const void* v
                                int Hkv, int T, long long num_blocks, int page_size, int max_blocks,
                                int d, float scale, attn_cache_dtype_t cache_dtype, void* workspace,
                                size_t workspace_bytes, attn_out_dtype_t o_dtype, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention with a learned relative position bias.
+ *
+ *   O = softmax(scale Q K^T + bias) V,   bias[h, i, j] = table[buckets[clamp(r)], h]
+ *
+ * with r = j - (i + Nk - Nq) the distance from query i to key j (the last query
+ * stands at the last key, as in causal masking; key - query when Nq = Nk) and
+ * clamp(r) = min(max(r - first, 0), span - 1): the map names a bucket for each
+ * distance first .. first + span - 1, farther ones count as its ends.  The five
+ * entry points take
+ *
+ *   table        [num_buckets, Hq], element type table_dtype (bf16 or fp32)
+ *   buckets      int32 (device) [span], each in [0, num_buckets) (one that is not
+ *                adds nothing, and attn_last_device_error() reports
+ *                ATTN_ERR_INVALID_ARG)
+ *   first, span  the map's first distance and its length, 1 <= span <= 65536
+ *
+ * and, apart from the bias, what the entry point without _bias in its name
+ * takes, for 8 <= d <= 128 (ATTN_ERR_UNSUPPORTED above).  A bias of -inf, or
+ * below -1e30, leaves a key out (V must still be finite there: its weight is 0);
+ * a row without any key has O = 0, LSE = -inf and adds nothing to a gradient.
+ * The bias is added in fp32.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * attn_bias_buckets -- the map of distances to buckets that grow geometrically
+ * (host only; touches no GPU).  Fills buckets[*span] for the distances *first ..
+ * *first + *span - 1; buckets = NULL (capacity ignored) only asks for those two.
+ *
+ * With n buckets a direction (num_buckets, or half of them when bidirectional =
+ * 1) and e = n / 2: distance r < e back has bucket r, a farther one min(n - 1, e +
+ * floor((n - e) ln(r / e) / ln(max_distance / e))), decided exactly at the
+ * borders.  Keys after the query: the same with n added (bidirectional = 1), or
+ * bucket 0.
+ * Supported: num_buckets 2..1024 (4.. and even when bidirectional),
+ * max_distance > e, *span <= 65536.
+ */
+attn_status_t attn_bias_buckets(int num_buckets, int max_distance, int bidirectional, int* buckets,
+                                int capacity, int* first, int* span);
+
+/*
+ * attn_fwd_bias -- attn_fwd with a bias; the workspace is attn_fwd's
+ * (attn_fwd_workspace_size).
+ */
+attn_status_t attn_fwd_bias(const void* q, const void* k, const void* v, const void* table,
+                            attn_out_dtype_t table_dtype, const int* buckets, int first, int span,
+                            int num_buckets, void* o, float* lse, int B, int Hq, int Hkv, int Nq, int Nk,
+                            int d, int causal, float scale, attn_out_dtype_t o_dtype, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* attn_fwd_varlen_bias -- attn_fwd_varlen with a bias; distances are those within a sequence. */
+attn_status_t attn_fwd_varlen_bias(const void* q, const void* k, const void* v, const void* table,
+                                   attn_out_dtype_t table_dtype, const int* buckets, int first, int span,
+                                   int num_buckets, void* o, float* lse, const int* cu_seqlens_q,
+                                   const int* cu_seqlens_k, int B, int Hq, int Hkv, int total_q, int total_k,
+                                   int max_seqlen_q, int max_seqlen_k, int d, int causal, float scale,
+                                   attn_out_dtype_t o_dtype, void* stream);
+
+/*
+ * attn_bwd_bias_workspace_size -- bytes of device workspace attn_bwd_bias needs:
+ * attn_bwd's, and 4 Hq (span + 16) for each 128-key tile of the batch and each
+ * 128 of those (at most 32): sums of dS over the distances.  Returns 0 for
+ * arguments attn_bwd_bias would reject.
+ */
+size_t attn_bwd_bias_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int d, int span);
+
+/*
+ * attn_bwd_bias -- the gradients of attn_fwd_bias: attn_bwd's with P from the
+ * biased scores, and
+ *
+ *   dtable[b, h] = sum of dS[h, i, j] over the batch and all (i, j) of bucket b,
+ *
+ * fp32 [num_buckets, Hq], written whole (0 for a bucket no distance has), from
+ * the unrounded dS = P o (dP - D).  All gradients are bit-identical from run to
+ * run.
+ */
+attn_status_t attn_bwd_bias(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                            const float* lse, const void* table, attn_out_dtype_t table_dtype,
+                            const int* buckets, int first, int span, int num_buckets, void* dq, void* dk,
+                            void* dv, float* dtable, int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                            int causal, float scale, attn_out_dtype_t o_dtype, attn_out_dtype_t grad_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* As attn_bwd_bias_workspace_size, for attn_bwd_varlen_bias (key tiles: B times those of max_seqlen_k). */
+size_t attn_bwd_varlen_bias_workspace_size(int B, int Hq, int Hkv, int total_q, int max_seqlen_k, int d,
+                                           int span);
+
+/* attn_bwd_varlen_bias -- the gradients of attn_fwd_varlen_bias; dtable sums over the sequences. */
+attn_status_t attn_bwd_varlen_bias(const void* q, const void* k, const void* v, const void* o,
+                                   const void* dout, const float* lse, const void* table,
+                                   attn_out_dtype_t table_dtype, const int* buckets, int first, int span,
+                                   int num_buckets, void* dq, void* dk, void* dv, float* dtable,
+                                   const int* cu_seqlens_q, const int* cu_seqlens_k, int B, int Hq, int Hkv,
+                                   int total_q, int total_k, int max_seqlen_q, int max_seqlen_k, int d,
+                                   int causal, float scale, attn_out_dtype_t o_dtype,
+                                   attn_out_dtype_t grad_dtype, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * attn_decode_paged_bias -- attn_decode_paged with a bias: the query token is the
+ * sequence's last key (distances -(L - 1) .. 0).  Workspace as attn_decode_paged.
+ */
+attn_status_t attn_decode_paged_bias(const void* q, const void* k_pages, const void* v_pages,
+                                     const int* block_table, const int* seqlens, const void* table,
+                                     attn_out_dtype_t table_dtype, const int* buckets, int first, int span,
+                                     int num_buckets, void* o, float* lse, int B, int Hq, int Hkv,
+                                     long long num_blocks, int page_size, int max_blocks, int d, float scale,
+                                     int num_splits, void* workspace, size_t workspace_bytes,
+                                     attn_out_dtype_t o_dtype, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged cache's tables, built on the GPU from the requests' lengths.
+ *
+ *   pool         int32 (device) [4 + num_blocks], 16-byte aligned: the number of
+ *                free pages, three words of the library's, then the free pages, a
+ *                stack whose last one goes out first.  attn_page_pool_init fills it
+ *                with every page, page 0 on top.  Calls on one pool must not
+ *                overlap on the GPU.
+ *   block_table  int32 (device) [B, max_blocks], as for attn_decode_paged; entries
+ *                past a request's pages mean nothing
+ *   seqlens      int32 (device) [B]: tokens of each request, updated in place
+ *
+ * Supported: B <= 4096, max_blocks * page_size <= 2^24, num_blocks <= 2^30.
+ * ------------------------------------------------------------------------- */
+
+attn_status_t attn_page_pool_init(int* pool, int num_blocks, void* stream);
+
+/*
+ * attn_pages_extend -- room for new_lens[b] more tokens of every request: pages
+ * off the pool into block_table, and where the tokens go.
+ *
+ *   new_lens   int32 (device) [B], 0 or more
+ *   slots      int64 (device), what attn_cache_write takes; 16-byte aligned
+ *   positions  int32 (device), what attn_rope takes, of the same shape, 16-byte
+ *              aligned, or NULL
+ *   width      > 0: slots and positions are [B, width], request b's tokens first
+ *              in its row (width >= new_lens[b]); total = 0, cu_seqlens = NULL
+ *              0: packed [total], the requests one after the other
+ *   total      >= the sum of new_lens (packed); may be 0
+ *   cu_seqlens int32 (device) [B + 1], packed: each request's first row, or NULL
+ *   granted    int32 (device) [B]: new_lens[b], or 0 where the pool ran out; or NULL
+ *
+ * Pages are given in the order of the requests, and only whole requests are
+ * served: from the first one that would need more pages than are left, every
+ * request that needs any gets none (its length stays, its slots are -1).  Token t
+ * of request b has position seqlens[b] + t (before the call) and, if granted, slot
+ * page * page_size + position % page_size; rows past a request's tokens, or past
+ * every request, have slot -1 and position 0.
+ * A request with a negative length, more than max_blocks * page_size tokens or (in
+ * padded rows) more than width new ones counts as new_lens[b] = 0, and rows past
+ * `total` are not written; attn_last_device_error() then reports
+ * ATTN_ERR_INVALID_ARG, as it does for a page outside [0, num_blocks) (its slots
+ * are -1).
+ */
+attn_status_t attn_pages_extend(int* pool, int num_blocks, int* block_table, int* seqlens,
+                                const int* new_lens, long long* slots, int* positions, int* cu_seqlens,
+                                int* granted, int B, int max_blocks, int page_size, int width, int total,
+                                void* stream);
+
+/*
+ * attn_pages_trim -- seqlens[b] = min(seqlens[b], max(keep_lens[b], 0)): drafted
+ * tokens that were not accepted, or (0) a finished request; the pages past the kept
+ * tokens go back on the pool, such that the pages of an attn_pages_extend given
+ * back at once come out again in the same order.  block_table is not written.
+ * More pages than the cache has (some given back twice) leave everything as it
+ * was, and a length outside [0, max_blocks * page_size] leaves that request as
+ * it was; attn_last_device_error() then reports ATTN_ERR_INVALID_ARG.
+ */
+attn_status_t attn_pages_trim(int* pool, int num_blocks, const int* block_table, int* seqlens,
+                              const int* keep_lens, int B, int max_blocks, int page_size, void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* attn_status_string(attn_status_t status);
