@@ -124,15 +124,15 @@ struct BwdParams {
     const int* cu_q;
     const int* cu_k;
     int total_q, total_k, vstride;
-    // the BIAS instantiations; partial: [B, n_kt, Hq, span + 16] fp32, a key tile's
-    // sums of dS over each distance of the map, then over the distances before
-    // and after it (8 warps' each)
+    // the BIAS instantiations; partial: [B, n_kt, Hq, span + 18] fp32, a key tile's
+    // sums of dS over each distance of the map, then over the distances before it (8
+    // warps' parts), after it (8), and a ninth part of each
     BiasArgs bias;
     float* partial;
 };
 
 // Floats of one (key tile, head)'s sums.
-__host__ __device__ inline int bias_partial_floats(int span) { return span + 16; }
+__host__ __device__ inline int bias_partial_floats(int span) { return span + 18; }
 
 // Row of sequence b's first query in a head's rows of lse2 / dvec for packed
 // batches: the packed row rounded up to 4 floats (16-byte bulk copies), plus
@@ -154,11 +154,21 @@ __device__ __forceinline__ bool bwd_varlen_seq(const BwdParams& p, int b, int& q
            (!p.causal || qe - qs <= ke - ks);
 }
 
+// BIAS: what the looking-up warp says of a tile: whether its biases are in the
+// slot's window, else the one that it has and the side of the map it lies on.
+enum : int { kBiasBefore = 0, kBiasAfter = 1, kBiasInWindow = 2 };
+struct __align__(8) TileBias {
+    int kind;
+    float value;
+};
+
 struct __align__(8) BwdBars {
     uint64_t kv_full, kv_empty;  // K and V of an item; read by its last S^T and dP^T
     uint64_t qd_full[2], qd_empty[2];
     uint64_t s_full, dp_full, p_full, ds_full, acc_full, drain;
-    uint64_t win_full, diag_full;  // BIAS: a bias window, a set of diagonal sums is filled
+    // BIAS: a Q tile's bias, a set of diagonal sums is there / has been read
+    uint64_t win_full[2], win_empty[2], diag_full[2], diag_empty[2];
+    TileBias bias[2];
     uint32_t tmem_base;
     int abort;
 };
@@ -585,6 +595,135 @@ __device__ __forceinline__ void store_rows32_pairs(void* base, size_t row0, size
     }
 }
 
+// ---------------------------------------------------------------------------
+// BIAS: the warps that look up biases and that add up diagonals
+// ---------------------------------------------------------------------------
+// Where the sums of (key tile, head) go.
+__device__ __forceinline__ float* bias_sums(const BwdParams& p, const BwdWork& w, int hq) {
+    return p.partial + (((size_t)w.b * p.n_kt + w.kt) * p.Hq + hq) * bias_partial_floats(p.bias.span);
+}
+
+// The bias of a tile whose distances are base .. base + 254, for head hq, into its
+// slot (whole warp): a window, or the value of the map's end.
+__device__ __forceinline__ void give_bias(const BiasArgs& a, int Hq, int hq, int base, float left, float right,
+                                          uint32_t window, TileBias* tb, int lane, unsigned int* err) {
+    const bool near = bias_near(a, base);
+    if (near) {
+        float v[kBiasWindow / 32];
+#pragma unroll
+        for (int i = 0; i < kBiasWindow / 32; ++i) v[i] = bias_at(a, Hq, hq, base + 32 * i + lane, err);
+#pragma unroll
+        for (int i = 0; i < kBiasWindow / 32; ++i) sts_f32(window + (32 * i + lane) * 4, v[i]);
+    }
+    const bool before = base + 254 <= a.first;
+    if (lane == 0) *tb = TileBias{near ? kBiasInWindow : before ? kBiasBefore : kBiasAfter, before ? left : right};
+    __syncwarp();
+}
+
+// Looks up each Q tile's biases, up to two tiles ahead of the P/dS warps.
+template <int D, bool VARLEN>
+__device__ void bwd_bias_lookup(int lane, uint8_t* smem, BwdBars* bars, const BwdParams& p, unsigned n_items,
+                                unsigned int* err) {
+    using C = BwdCfg<D>;
+    const volatile int* abort_flag = &bars->abort;
+    bool ok = true;
+    int n = 0;   // Q tiles done
+    for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
+        const BwdWork w = bwd_item<VARLEN>(p, idx, err);
+        for (int h = 0; h < p.group && w.n_tiles > 0 && ok; ++h) {
+            const int hq = w.g * p.group + h;
+            const float left = bias_at(p.bias, p.Hq, hq, p.bias.first, err);
+            const float right = bias_at(p.bias, p.Hq, hq, p.bias.first + p.bias.span - 1, err);
+            for (int i = 0; i < w.n_qt_cta; ++i, ++n) {
+                const int st = n & 1;
+                if (n >= 2)
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_empty[st]), ((n >> 1) - 1) & 1,
+                                                           abort_flag));
+                if (!ok) break;
+                give_bias(p.bias, p.Hq, hq, w.k0 - ((w.qt_first + i) * kBT + w.off) - (kBT - 1), left, right,
+                          smem_u32(smem + C::kWin) + st * kBiasWindow * 4, &bars->bias[st], lane, err);
+                if (lane == 0) mbar_arrive(smem_u32(&bars->win_full[st]));
+            }
+        }
+    }
+    if (!ok && lane == 0) bwd_abort(bars, err);
+    __syncwarp();
+}
+
+// Adds up dS over distances.  A Q tile with a window has 255 of them, base .. base +
+// 254, each with parts from up to 8 warps; the head's next tile has those from base
+// - 128 on.  The running sum of distance r is held by lane r % 32, register r / 32 %
+// 8, and stored once the head's next tile does not have it (a distance beyond the
+// map goes to the sum of its side).  Each (key tile, head) of the workspace is written
+// whole: here, and the far tiles' sums by the P/dS warps.
+template <int D, bool VARLEN>
+__device__ void bwd_bias_sums(int lane, uint8_t* smem, BwdBars* bars, const BwdParams& p, unsigned n_items,
+                              unsigned int* err) {
+    using C = BwdCfg<D>;
+    const volatile int* abort_flag = &bars->abort;
+    const int first = p.bias.first, span = p.bias.span;
+    bool ok = true;
+    uint32_t n = 0;   // sets of diagonal sums read
+    for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
+        const BwdWork w = bwd_item<VARLEN>(p, idx, err);
+        for (int h = 0; h < p.group && ok; ++h) {
+            float* out = bias_sums(p, w, w.g * p.group + h);
+            // (each lane clears what it may store to)
+            for (int x = (lane - first) & 31; x < span; x += 32) out[x] = 0.f;
+            if (w.n_tiles == 0) {
+                if (lane < 18) out[span + lane] = 0.f;
+                continue;
+            }
+            float own[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            float side_l = 0.f, side_r = 0.f;
+            for (int i = 0; i < w.n_qt_cta; ++i) {
+                const int base = w.k0 - ((w.qt_first + i) * kBT + w.off) - (kBT - 1);
+                if (!bias_near(p.bias, base)) continue;
+                const uint32_t set = n & 1;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->diag_full[set]), (n >> 1) & 1, abort_flag));
+                if (!ok) break;
+                ++n;
+                const uint32_t from = smem_u32(smem + C::kDiag) + set * C::kDiagBytes;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const int at = (32 * r + lane - base) & 255;   // the distance, from base
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        // warp e = 4 grp + wq holds distance base + 127 + 32 wq - 64 grp + d,
+                        // d = s - 32 k, in place 32 k + s
+                        const int d = at - 127 - 32 * (e & 3) + 64 * (e >> 2);
+                        if (d >= -63 && d <= 31) own[r] += lds_f32(from + (e * 96 + 64 * ((31 - d) >> 5) + d) * 4);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->diag_empty[set]));
+                const bool more = i + 1 < w.n_qt_cta && bias_near(p.bias, base - kBT);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const int at = (32 * r + lane - base) & 255;
+                    if (more && at <= 126) continue;
+                    const int x = base + at - first;
+                    if (x < 0) side_l += own[r];
+                    else if (x >= span) side_r += own[r];
+                    else if (at < 255) out[x] = own[r];
+                    own[r] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) {
+                side_l += __shfl_xor_sync(0xFFFFFFFFu, side_l, s);
+                side_r += __shfl_xor_sync(0xFFFFFFFFu, side_r, s);
+            }
+            if (lane == 0) {
+                out[span + 16] = side_l;
+                out[span + 17] = side_r;
+            }
+        }
+    }
+    if (!ok && lane == 0) bwd_abort(bars, err);
+    __syncwarp();
+}
+
 template <int D, bool OUT_F32, bool VARLEN, bool BIAS>
 __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars, uint32_t tmem,
                         const CUtensorMap* tdk, const CUtensorMap* tdv, const BwdParams& p,
@@ -599,60 +738,27 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
     bool ok = true;
     int g = 0;  // Q tiles done, over the CTA's items
     int u = 0;  // items with work
-    // BIAS: this thread's number among the 256, the windows filled and read, and
-    // the sets of diagonal sums exchanged (two buffers each; a buffer is written
-    // again only by a warp that has seen all eight arrive for the next one, each
-    // after its reads of the buffer)
-    const int et = grp * 128 + j;
-    uint32_t cnt_fill = 0, cnt_win = 0, cnt_diag = 0;
+    uint32_t cnt_diag = 0;   // BIAS: sets of diagonal sums written
     for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
         const BwdWork w = bwd_item<VARLEN>(p, idx, err);
         const int jg = w.k0 + j;
-        // BIAS.  Q tile i of the item meets the distances base(i) .. + 254; their
-        // sums of dS are held by the thread of the same number modulo 256 (each
-        // distance is in at most two Q tiles of a head, one after the other) and
-        // stored when the head's next tile does not have them.
-        auto q0_of = [&](int i) { return (w.qt_first + i % w.n_qt_cta) * kBT; };
-        auto base_of = [&](int i) { return w.k0 - (q0_of(i) + w.off) - (kBT - 1); };
-        auto head_of = [&](int i) { return w.g * p.group + i / w.n_qt_cta; };
-        auto sums_of = [&](int hq) {
-            return p.partial + (((size_t)w.b * p.n_kt + w.kt) * p.Hq + hq) * bias_partial_floats(p.bias.span);
-        };
-        auto fill = [&](float v) {
-            sts_f32(smem_u32(smem + C::kWin) + ((cnt_fill & 1) * kBiasWindow + et) * 4, v);
-            ++cnt_fill;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->win_full));
-        };
-        float wv = 0.f, bias_l = 0.f, bias_r = 0.f, own = 0.f, far_l = 0.f, far_r = 0.f;
-        if constexpr (BIAS) {
-            if (w.n_tiles == 0) {
-                for (int h = 0; h < p.group; ++h) {
-                    float* out = sums_of(w.g * p.group + h);
-                    for (int x = et; x < bias_partial_floats(p.bias.span); x += 256) out[x] = 0.f;
-                }
-            } else {
-                if (bias_near(p.bias, base_of(0)))
-                    fill(bias_at(p.bias, p.Hq, head_of(0), base_of(0) + et, err));
-                if (w.n_tiles > 1 && bias_near(p.bias, base_of(1)))
-                    wv = bias_at(p.bias, p.Hq, head_of(1), base_of(1) + et, err);
-            }
-        }
+        // BIAS: the Q tile, its head, and this thread's sums of the head's tiles on
+        // either side of the map
+        int qt = w.qt_first, hq = w.g * p.group;
+        float far_l = 0.f, far_r = 0.f;
         for (int i = 0; i < w.n_tiles && ok; ++i) {
             const int gi = g + i;
             const int st = gi & 1;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->s_full), gi & 1, abort_flag, 32));
             if (!ok) break;
             tc_fence_after();
-            const int q0 = q0_of(i);
+            const int q0 = (BIAS ? qt : w.qt_first + i % w.n_qt_cta) * kBT;
             const uint32_t lse2s = smem_u32(smem + C::kLD + st * 1024);
             const uint32_t ds_vec = lse2s + kBT * 4;
             // causal: query q0 + x sees key jg iff x >= jg - off - q0
             int lim = jg - w.off - q0;
             bool masked = p.causal && (q0 + w.off < w.k0 + kBT - 1);
-            const int base = BIAS ? base_of(i) : 0;
-            const bool near = BIAS && bias_near(p.bias, base);
-            float bc = 0.f;
+            TileBias tb{kBiasBefore, 0.f};
             uint32_t win = 0;
             if constexpr (BIAS) {
                 // keys past the sequence have dS = 0 (their rows of K are zeros)
@@ -661,24 +767,13 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
                     if (jg >= w.nk) lim = kBT;
                     masked = true;
                 }
-                if (i % w.n_qt_cta == 0) {   // a head begins
-                    const int hq = head_of(i);
-                    bias_l = bias_at(p.bias, p.Hq, hq, p.bias.first, err);
-                    bias_r = bias_at(p.bias, p.Hq, hq, p.bias.first + p.bias.span - 1, err);
-                    float* out = sums_of(hq);
-                    for (int x = (et - p.bias.first) & 255; x < p.bias.span; x += 256) out[x] = 0.f;
-                    far_l = far_r = 0.f;
-                }
-                if (near) {
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_full), cnt_win & 1, abort_flag, 32));
-                    if (!ok) break;
-                    // query column x of key row j is distance base + j - x + 127
-                    win = smem_u32(smem + C::kWin) + ((cnt_win & 1) * kBiasWindow + j + kBT - 1) * 4;
-                    ++cnt_win;
-                } else {
-                    bc = base + 254 <= p.bias.first ? bias_l : bias_r;
-                }
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_full[st]), (gi >> 1) & 1, abort_flag));
+                if (!ok) break;
+                tb = bars->bias[st];
+                // query column x of key row j is distance base + j - x + 127
+                win = smem_u32(smem + C::kWin) + (st * kBiasWindow + j + kBT - 1) * 4;
             }
+            const bool window = BIAS && tb.kind == kBiasInWindow;
             // Phase 1: P^T from S^T for this warpgroup's 64 query columns, kept
             // in registers and written as bf16 over the S^T columns it has read;
             // with the other warpgroup's, releases dV(i) and S^T(i+1).
@@ -688,12 +783,12 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
                 tmem_ld32(tS + cc * 32, sv);
                 tmem_wait_ld();
                 if constexpr (BIAS) {
-                    if (near) {
+                    if (window) {
                         if (masked) p_chunk<true, kWindowBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, 0.f, win);
                         else p_chunk<false, kWindowBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, 0.f, win);
                     } else {
-                        if (masked) p_chunk<true, kOneBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, bc);
-                        else p_chunk<false, kOneBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, bc);
+                        if (masked) p_chunk<true, kOneBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, tb.value);
+                        else p_chunk<false, kOneBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, tb.value);
                     }
                 } else if (masked)
                     p_chunk<true>(sv, lse2s, cc * 32, p.c, lim, pf, pp);
@@ -708,9 +803,7 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
             if constexpr (BIAS) {
-                if (i + 1 < w.n_tiles && bias_near(p.bias, base_of(i + 1))) fill(wv);
-                if (i + 2 < w.n_tiles && bias_near(p.bias, base_of(i + 2)))
-                    wv = bias_at(p.bias, p.Hq, head_of(i + 2), base_of(i + 2) + et, err);
+                if (lane == 0) mbar_arrive(smem_u32(&bars->win_empty[st]));
             }
             // Phase 2: dS^T from P^T and dP^T, written as bf16 over the dP^T
             // columns already read; releases dK(i) and dP^T(i+1).
@@ -725,7 +818,7 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
                 tmem_ld32(tdP + cc * 32, dp);
                 tmem_wait_ld();
                 if constexpr (BIAS) {
-                    if (near) ds_chunk_t<kWindowBias, kHalf>(pf, dp, ds_vec, cc * 32, dd, &sums, lane);
+                    if (window) ds_chunk_t<kWindowBias, kHalf>(pf, dp, ds_vec, cc * 32, dd, &sums, lane);
                     else ds_chunk_t<kOneBias>(pf, dp, ds_vec, cc * 32, dd, &sums);
                 } else {
                     ds_chunk_t(pf, dp, ds_vec, cc * 32, dd);
@@ -742,52 +835,38 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
                 mbar_arrive(smem_u32(&bars->qd_empty[st]));
             }
             if constexpr (BIAS) {
-                const bool head_ends = (i + 1) % w.n_qt_cta == 0;
-                float* out = sums_of(head_of(i));
-                if (near) {
-                    // the warps' diagonals meet: warp (wq, grp) holds distance
-                    // base + 127 + 32 wq - 64 grp + (s - 32 k) in place 32 k + s
-                    float* set = reinterpret_cast<float*>(smem + C::kDiag + (cnt_diag & 1) * C::kDiagBytes);
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) set[(grp * 4 + wq) * 96 + 32 * k + lane] = sums.a[k];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&bars->diag_full));
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->diag_full), cnt_diag & 1, abort_flag, 32));
+                if (window) {
+                    const uint32_t set = cnt_diag & 1;
+                    if (cnt_diag >= 2)
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->diag_empty[set]),
+                                                               ((cnt_diag >> 1) - 1) & 1, abort_flag));
                     if (!ok) break;
-                    ++cnt_diag;
-                    const int at = (et - base) & 255;   // this thread's distance: base + at
+                    const uint32_t out = smem_u32(smem + C::kDiag) + set * C::kDiagBytes +
+                                         ((grp * 4 + wq) * 96 + lane) * 4;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int d = at - 127 - 32 * (e & 3) + 64 * (e >> 2);   // s - 32 k
-                        if (d >= -63 && d <= 31) {
-                            const int k = (31 - d) >> 5;
-                            own += set[e * 96 + 64 * k + d];
-                        }
-                    }
-                    const bool stays = !head_ends && at <= 126 && bias_near(p.bias, base - kBT);
-                    if (!stays) {
-                        const int x = base + at - p.bias.first;
-                        if (x < 0) far_l += own;
-                        else if (x >= p.bias.span) far_r += own;
-                        else if (at <= 254) out[x] = own;
-                        own = 0.f;
-                    }
+                    for (int k = 0; k < 3; ++k) sts_f32(out + 128 * k, sums.a[k]);
+                    ++cnt_diag;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars->diag_full[set]));
                 } else {
                     float a, b;
                     f2_split(sums.far, a, b);
-                    if (base + 254 <= p.bias.first) far_l += a + b; else far_r += a + b;
+                    if (tb.kind == kBiasBefore) far_l += a + b; else far_r += a + b;
                 }
-                if (head_ends) {
-                    float a = far_l, b = far_r;
+                if (++qt == w.qt_first + w.n_qt_cta) {   // the head ends
 #pragma unroll
                     for (int s = 16; s > 0; s >>= 1) {
-                        a += __shfl_xor_sync(0xFFFFFFFFu, a, s);
-                        b += __shfl_xor_sync(0xFFFFFFFFu, b, s);
+                        far_l += __shfl_xor_sync(0xFFFFFFFFu, far_l, s);
+                        far_r += __shfl_xor_sync(0xFFFFFFFFu, far_r, s);
                     }
                     if (lane == 0) {
-                        out[p.bias.span + grp * 4 + wq] = a;
-                        out[p.bias.span + 8 + grp * 4 + wq] = b;
+                        float* out = bias_sums(p, w, hq) + p.bias.span + grp * 4 + wq;
+                        out[0] = far_l;
+                        out[8] = far_r;
                     }
+                    far_l = far_r = 0.f;
+                    qt = w.qt_first;
+                    ++hq;
                 }
             }
         }
@@ -929,8 +1008,12 @@ attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         mbar_init(smem_u32(&bars->p_full), 8);
         mbar_init(smem_u32(&bars->ds_full), 8);
         mbar_init(smem_u32(&bars->acc_full), 1);
-        mbar_init(smem_u32(&bars->win_full), 8);
-        mbar_init(smem_u32(&bars->diag_full), 8);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&bars->win_full[s]), 1);
+            mbar_init(smem_u32(&bars->win_empty[s]), 8);
+            mbar_init(smem_u32(&bars->diag_full[s]), 8);
+            mbar_init(smem_u32(&bars->diag_empty[s]), 1);
+        }
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort = 0;
         fence_barrier_init();
@@ -949,10 +1032,19 @@ attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     const uint32_t tmem = bars->tmem_base;
 
     if constexpr (BIAS) {
-        if (warp < 4) reg_dealloc<kBwdRegsControl>();
-        else reg_alloc<kBwdRegsPds>();
-    }
-    if (warp == 0) bwd_producer<D, VARLEN>(&tq, &tk, &tv, &tdo, smem, bars, p, n_items, err);
+        // (roles in the branches of the register split, which the compiler then keeps to)
+        if (warp < 4) {
+            reg_dealloc<kBwdRegsControl>();
+            if (warp == 0) bwd_producer<D, VARLEN>(&tq, &tk, &tv, &tdo, smem, bars, p, n_items, err);
+            else if (warp == 1) bwd_mma<D, VARLEN>(smem, bars, tmem, p, n_items, err);
+            else if (warp == 2) bwd_bias_lookup<D, VARLEN>(lane, smem, bars, p, n_items, err);
+            else bwd_bias_sums<D, VARLEN>(lane, smem, bars, p, n_items, err);
+        } else {
+            reg_alloc<kBwdRegsPds>();
+            bwd_pds<D, OUT_F32, VARLEN, BIAS>(warp & 3, (warp - 4) >> 2, lane, smem, bars, tmem, &tdk, &tdv, p, n_items,
+                                              err);
+        }
+    } else if (warp == 0) bwd_producer<D, VARLEN>(&tq, &tk, &tv, &tdo, smem, bars, p, n_items, err);
     else if (warp == 1) bwd_mma<D, VARLEN>(smem, bars, tmem, p, n_items, err);
     else if (warp >= 4)
         bwd_pds<D, OUT_F32, VARLEN, BIAS>(warp & 3, (warp - 4) >> 2, lane, smem, bars, tmem, &tdk, &tdv, p, n_items, err);
@@ -988,7 +1080,8 @@ struct __align__(8) DqBars {
     uint64_t q_full, q_empty;  // Q and dO of an item; read by its last S and dP
     uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
     uint64_t s_full[2], dp_full, ds_full, dq_full, drain;  // s_full[b]: the S in buffer b
-    uint64_t win_full;  // BIAS: a bias window is filled
+    uint64_t win_full[2], win_empty[2];  // BIAS, as in BwdBars
+    TileBias bias[2];
     uint32_t tmem_base;
     int abort;
 };
@@ -1297,6 +1390,33 @@ __device__ __forceinline__ void ds_row_chunk(const float (&pf)[32], const uint32
     }
 }
 
+// BIAS: looks up each K/V tile's biases, up to two tiles ahead of the dS warps.
+template <int D, bool VARLEN>
+__device__ void dq_bias_lookup(int lane, uint8_t* smem, DqBars* bars, const BwdParams& p, unsigned n_items,
+                               unsigned int* err) {
+    using C = DqCfg<D, true>;
+    const volatile int* abort_flag = &bars->abort;
+    bool ok = true;
+    int n = 0;   // K/V tiles done
+    for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
+        const DqWork w = dq_item<VARLEN>(p, idx, err);
+        if (w.n_kv == 0) continue;
+        const float left = bias_at(p.bias, p.Hq, w.hq, p.bias.first, err);
+        const float right = bias_at(p.bias, p.Hq, w.hq, p.bias.first + p.bias.span - 1, err);
+        for (int j = 0; j < w.n_kv; ++j, ++n) {
+            const int st = n & 1;
+            if (n >= 2)
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_empty[st]), ((n >> 1) - 1) & 1, abort_flag));
+            if (!ok) break;
+            give_bias(p.bias, p.Hq, w.hq, j * kBT - (w.q0 + kBT - 1) - w.off, left, right,
+                      smem_u32(smem + C::kWin) + st * kBiasWindow * 4, &bars->bias[st], lane, err);
+            if (lane == 0) mbar_arrive(smem_u32(&bars->win_full[st]));
+        }
+    }
+    if (!ok && lane == 0) atomicOr(err, kErrTimeout), *((volatile int*)&bars->abort) = 1;
+    __syncwarp();
+}
+
 template <int D, bool OUT_F32, bool VARLEN, bool BIAS>
 __device__ void dq_ds(int wq, int grp, int lane, uint8_t* smem, DqBars* bars, uint32_t tmem,
                       const BwdParams& p, unsigned n_items, unsigned int* err) {
@@ -1308,8 +1428,6 @@ __device__ void dq_ds(int wq, int grp, int lane, uint8_t* smem, DqBars* bars, ui
     bool ok = true;
     int t0 = 0;  // K/V tiles before this item, over the CTA's items
     int u = 0;   // items with work
-    const int et = grp * 128 + wq * 32 + lane;   // BIAS: as in the dK/dV pass
-    uint32_t cnt_fill = 0, cnt_win = 0;
     for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
         const DqWork w = dq_item<VARLEN>(p, idx, err);
         const int row = w.q0 + wq * 32 + lane;
@@ -1322,24 +1440,6 @@ __device__ void dq_ds(int wq, int grp, int lane, uint8_t* smem, DqBars* bars, ui
         const float dval = w.n_kv > 0 ? p.dvec[vrow] : 0.f;
         uint64_t nl2 = f2(-lse2, -lse2);
         const uint64_t nd2 = f2(-dval, -dval);
-        // BIAS: K/V tile j meets the distances base0 + 128 j .. + 254
-        const int base0 = -(w.q0 + kBT - 1) - w.off;
-        auto fill = [&](float v) {
-            sts_f32(smem_u32(smem + C::kWin) + ((cnt_fill & 1) * kBiasWindow + et) * 4, v);
-            ++cnt_fill;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->win_full));
-        };
-        float wv = 0.f, bias_l = 0.f, bias_r = 0.f;
-        if constexpr (BIAS) {
-            if (w.n_kv > 0) {
-                bias_l = bias_at(p.bias, p.Hq, w.hq, p.bias.first, err);
-                bias_r = bias_at(p.bias, p.Hq, w.hq, p.bias.first + p.bias.span - 1, err);
-                if (bias_near(p.bias, base0)) fill(bias_at(p.bias, p.Hq, w.hq, base0 + et, err));
-                if (w.n_kv > 1 && bias_near(p.bias, base0 + kBT))
-                    wv = bias_at(p.bias, p.Hq, w.hq, base0 + kBT + et, err);
-            }
-        }
         for (int j = 0; j < w.n_kv && ok; ++j) {
             const int t = t0 + j;
             const uint32_t tS = tmem + ((t & 1) ? 384u : 0u) + lane_off;
@@ -1348,7 +1448,7 @@ __device__ void dq_ds(int wq, int grp, int lane, uint8_t* smem, DqBars* bars, ui
             tc_fence_after();
             int lim = row + w.off - j * kBT;  // causal: key column c allowed iff c <= lim
             bool masked = __any_sync(0xFFFFFFFFu, p.causal && lim < kBT - 1);
-            bool near = false;
+            bool window = false;
             uint32_t win = 0;
             if constexpr (BIAS) {
                 // keys past the sequence: P = 0 (a bias can put their 2^-lse2 past
@@ -1356,20 +1456,15 @@ __device__ void dq_ds(int wq, int grp, int lane, uint8_t* smem, DqBars* bars, ui
                 const int last = w.nk - 1 - j * kBT;
                 lim = p.causal && lim < last ? lim : last;
                 masked = __any_sync(0xFFFFFFFFu, lim < kBT - 1);
-                const int base = base0 + j * kBT;
-                near = bias_near(p.bias, base);
-                if (near) {
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_full), cnt_win & 1, abort_flag, 32));
-                    if (!ok) break;
-                    // key column c of query row i is distance base + c - i + 127
-                    win = smem_u32(smem + C::kWin) +
-                          ((cnt_win & 1) * kBiasWindow + kBT - 1 - (wq * 32 + lane)) * 4;
-                    ++cnt_win;
-                    nl2 = f2(-lse2, -lse2);
-                } else {
-                    const float add = (base + 254 <= p.bias.first ? bias_l : bias_r) - lse2;
-                    nl2 = f2(add, add);
-                }
+                const int st = t & 1;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_full[st]), (t >> 1) & 1, abort_flag));
+                if (!ok) break;
+                const TileBias tb = bars->bias[st];
+                window = tb.kind == kBiasInWindow;
+                // key column c of query row i is distance base + c - i + 127
+                win = smem_u32(smem + C::kWin) + (st * kBiasWindow + kBT - 1 - (wq * 32 + lane)) * 4;
+                const float add = (window ? 0.f : tb.value) - lse2;
+                nl2 = f2(add, add);
             }
             // Phase 1: P from S for this warpgroup's 64 key columns (needs S_j
             // only; runs while dQ_{j-1} and dP_j compute)
@@ -1379,7 +1474,7 @@ __device__ void dq_ds(int wq, int grp, int lane, uint8_t* smem, DqBars* bars, ui
                 tmem_ld32(tS + cc * 32, sv);
                 tmem_wait_ld();
                 if constexpr (BIAS) {
-                    if (near) {
+                    if (window) {
                         if (masked) p_row_chunk<true, true>(sv, c2, nl2, cc * 32, lim, pf, win);
                         else p_row_chunk<false, true>(sv, c2, nl2, cc * 32, kBT, pf, win);
                     } else {
@@ -1394,9 +1489,7 @@ __device__ void dq_ds(int wq, int grp, int lane, uint8_t* smem, DqBars* bars, ui
             phase1(2 * grp, pf0);
             phase1(2 * grp + 1, pf1);
             if constexpr (BIAS) {
-                if (j + 1 < w.n_kv && bias_near(p.bias, base0 + (j + 1) * kBT)) fill(wv);
-                if (j + 2 < w.n_kv && bias_near(p.bias, base0 + (j + 2) * kBT))
-                    wv = bias_at(p.bias, p.Hq, w.hq, base0 + (j + 2) * kBT + et, err);
+                if (lane == 0) mbar_arrive(smem_u32(&bars->win_empty[t & 1]));
             }
             // Phase 2: dS from P and dP, as bf16 over the S columns this
             // warpgroup read
@@ -1493,7 +1586,10 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         mbar_init(smem_u32(&bars->dp_full), 1);
         mbar_init(smem_u32(&bars->ds_full), 8);
         mbar_init(smem_u32(&bars->dq_full), 1);
-        mbar_init(smem_u32(&bars->win_full), 8);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&bars->win_full[s]), 1);
+            mbar_init(smem_u32(&bars->win_empty[s]), 8);
+        }
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort = 0;
         fence_barrier_init();
@@ -1512,6 +1608,7 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     const uint32_t tmem = bars->tmem_base;
     if (warp == 0) dq_producer<D, VARLEN, BIAS>(&tq, &tk, &tv, &tdo, smem, bars, p, n_items, err);
     else if (warp == 1) dq_mma<D, VARLEN, BIAS>(smem, bars, tmem, p, n_items, err);
+    else if (BIAS && warp == 2) dq_bias_lookup<D, VARLEN>(lane, smem, bars, p, n_items, err);
     else if (warp >= 4)
         dq_ds<D, OUT_F32, VARLEN, BIAS>(warp & 3, (warp - 4) >> 2, lane, smem, bars, tmem, p, n_items, err);
     tc_fence_before();
@@ -1721,7 +1818,7 @@ attn_bwd_bias_table_kernel(const float* __restrict__ sums, const int* __restrict
     float a = 0.f;
 #pragma unroll 4
     for (int x = lane; x < floats; x += 32) {
-        const int at = x < span ? x : x < span + 8 ? 0 : span - 1;
+        const int at = x < span ? x : x < span + 8 || x == span + 16 ? 0 : span - 1;
         if (__ldg(buckets + at) == bk)
             for (int z = 0; z < parts; ++z) a += __ldg(sums + ((size_t)z * Hq + h) * floats + x);
     }

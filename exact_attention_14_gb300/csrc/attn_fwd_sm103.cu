@@ -26,7 +26,8 @@
 //               O (a row dominated by one key then gets exactly that V row).
 //               A warp reaches TMEM lanes 32*(warp % 4) .. +31, so each
 //               warpgroup covers the tile's 128 rows.
-//   warps 2-3   idle.
+//   warps 2-3   idle; with a relative position bias (BIAS), warp 2 + t looks up
+//               the biases of Q tile t, a K/V tile ahead of its softmax.
 // Registers: launched at 168 per thread; the first warpgroup (producer, MMA
 // issuer) gives back to 104 and the softmax warpgroups take 200 each
 // (128*104 + 256*200 = 384*168, the launch allocation; no spills).
@@ -121,9 +122,9 @@ __device__ unsigned int g_fwd_queue[kQueueSlots][kQueueWords];
 template <int D>
 __host__ __device__ constexpr int partial_block_floats() { return (D + 3) * 32; }
 
-// Roles that take each work item from the producer: the MMA warp and 8
-// softmax warps.
-constexpr int kUnitConsumers = 9;
+// Roles that take each work item from the producer: the MMA warp, 8 softmax
+// warps and (BIAS) 2 warps that look up biases.
+__host__ __device__ constexpr int unit_consumers(bool bias) { return bias ? 11 : 9; }
 
 // A work item as the producer decodes it for the other roles, so that their
 // unit boundaries carry no index arithmetic.
@@ -144,9 +145,12 @@ struct __align__(8) Bars {
     uint64_t kv_full[8], kv_empty[8];
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t unit_full[2], unit_empty[2];
-    uint64_t win_full[2];  // BIAS: a Q tile's next window is filled (its 4 softmax warps)
+    // BIAS: a Q tile's next bias (window or value) is there; its 4 softmax warps have
+    // read it.  bias[t][slot]: {whether it is a window, else its value}
+    uint64_t win_full[2][2], win_empty[2][2];
     uint64_t drain;
     WorkItem item[2];
+    float2 bias[2][2];
     uint32_t tmem_base;
     int abort;
 };
@@ -511,9 +515,15 @@ __device__ __forceinline__ void softmax_tile(uint32_t (&sr)[128], int lim, int j
                                              uint32_t tS, uint32_t tO, float& m, float& l,
                                              float& lx, float bc = 0.f, uint32_t win = 0) {
     if constexpr (BM == kBiasTile) {
+        const uint64_t cb = f2(c, c);
 #pragma unroll
-        for (int cc = 0; cc < 128; ++cc)
-            sr[cc] = __float_as_uint(fmaf(__uint_as_float(sr[cc]), c, lds_f32(win + 4 * cc)));
+        for (int cc = 0; cc < 128; cc += 2) {
+            float x0, x1;
+            f2_split(f2_fma(f2(__uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1])), cb,
+                            f2(lds_f32(win + 4 * cc), lds_f32(win + 4 * cc + 4))), x0, x1);
+            sr[cc] = __float_as_uint(x0);
+            sr[cc + 1] = __float_as_uint(x1);
+        }
     }
     if constexpr (MASKED) {
 #pragma unroll
@@ -800,6 +810,70 @@ __device__ __noinline__ void split_piece_epilogue(unsigned int* merge_count, flo
     if (lse_out) *lse_out = (mmax + log2f(wxsum)) * kLn2;
 }
 
+// ---------------------------------------------------------------------------
+// BIAS: the warp that looks up Q tile t's biases
+// ---------------------------------------------------------------------------
+// Of K/V tile j, the distances base0 + 128 j .. + 254 of the window, or the one bias
+// that they share.  Masked tiles get a window in either case (the softmax then has
+// an instantiation less).  Two slots: the warp runs a tile ahead of the softmax, so
+// that nobody waits for the two dependent loads of a look-up.  The windows lie in
+// the second store buffer of the tile's first softmax warp.
+template <int D>
+__host__ __device__ constexpr int window_off(int t) {
+    return FwdCfg<D>::kStgOff + t * 4 * FwdCfg<D>::kStgBytesPerWarp + 2048;
+}
+
+template <int D, bool VARLEN>
+__device__ void run_bias(int t, int lane, uint8_t* smem, Bars* bars, const FwdParams& p, unsigned int* err) {
+    const volatile int* abort_flag = &bars->abort;
+    const FwdShape& s = p.shape;
+    const BiasArgs& a = p.bias;
+    const uint32_t windows = smem_u32(smem + window_off<D>(t));
+    uint32_t n = 0;   // biases given
+    bool ok = true;
+    for (uint32_t k = 0; ok; ++k) {
+        WorkItem w;
+        ok = take_item<VARLEN>(bars, k, w, abort_flag);
+        if (!ok || w.bh < 0) break;
+        const int n_t = t == 0 ? w.e[0] : w.e[1];
+        if (n_t <= w.j0) continue;
+        const int nk = VARLEN ? w.nk : s.Nk;
+        const int off = VARLEN ? nk - w.nq : p.off;
+        const int hq = w.bh - (w.bh / s.Hq) * s.Hq;
+        const int row0 = w.mb * kUnitRows + t * kTileM;
+        const int base0 = -(row0 + kTileM - 1) - off;
+        const int lim0 = s.causal && row0 + off < nk - 1 ? row0 + off : nk - 1;   // the first row's last key
+        const float left = bias_at(a, s.Hq, hq, a.first, err);
+        const float right = bias_at(a, s.Hq, hq, a.first + a.span - 1, err);
+        for (int j = w.j0; j < n_t; ++j, ++n) {
+            const uint32_t slot = n & 1;
+            const int base = base0 + j * kTileN;
+            const bool window = bias_near(a, base) || lim0 - j * kTileN < kTileN - 1;
+            float v[kBiasWindow / 32];
+            if (window) {
+#pragma unroll
+                for (int i = 0; i < kBiasWindow / 32; ++i) v[i] = bias_at(a, s.Hq, hq, base + 32 * i + lane, err);
+            }
+            if (n >= 2) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_empty[t][slot]), ((n >> 1) - 1) & 1,
+                                                       abort_flag));
+                if (!ok) break;
+            }
+            if (window) {
+#pragma unroll
+                for (int i = 0; i < kBiasWindow / 32; ++i)
+                    sts_f32(windows + slot * (kBiasWindow * 4) + (32 * i + lane) * 4, v[i]);
+            }
+            if (lane == 0)
+                bars->bias[t][slot] = make_float2(window ? 1.f : 0.f, base + 254 <= a.first ? left : right);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->win_full[t][slot]));
+        }
+    }
+    if (!ok && lane == 0) raise_abort(bars, err);
+    __syncwarp();
+}
+
 template <int D, bool OUT_F32, bool VARLEN, bool BIAS>
 __device__ void run_softmax(int t, int wq, int lane, uint8_t* smem, Bars* bars, uint32_t tmem,
                             const FwdParams& p, const CUtensorMap* to, float* __restrict__ lse_ptr,
@@ -817,11 +891,7 @@ __device__ void run_softmax(int t, int wq, int lane, uint8_t* smem, Bars* bars, 
     uint8_t* stg = smem + C::kStgOff + (t * 4 + wq) * C::kStgBytesPerWarp;
     uint32_t epi_buf = 0;
     uint32_t cnt_s = 0, cnt_o = 0;
-    // BIAS: the Q tile's two windows (in the second store buffer of its first
-    // warp), how many were filled and how many read
-    const uint32_t win0 = smem_u32(smem + C::kStgOff + t * 4 * C::kStgBytesPerWarp + 2048);
-    const uint32_t bar_w = smem_u32(&bars->win_full[t]);
-    uint32_t cnt_fill = 0, cnt_win = 0;
+    const uint32_t windows = smem_u32(smem + window_off<D>(t));  // BIAS
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
         WorkItem w;
@@ -839,47 +909,18 @@ __device__ void run_softmax(int t, int wq, int lane, uint8_t* smem, Bars* bars, 
             const int lk = row + (VARLEN ? nk - nq : p.off);
             last_key = lk < last_key ? lk : last_key;
         }
-        // BIAS: a tile's distances start at 128 j + base0; tiles inside the map, and
-        // masked ones (an instantiation less), read a window.  The warps fill the
-        // next tile's once they have read this one's: whoever fills a buffer again
-        // has seen all four warps' arrivals for the window in between, each after
-        // its reads of the buffer's last.  (A window's bucket and table entries are
-        // fetched a whole tile before they are stored.)
-        const int off = VARLEN ? nk - nq : p.off;
-        const int hq_b = BIAS ? bh - (bh / s.Hq) * s.Hq : 0;
-        const int row0 = mb * kUnitRows + t * kTileM;
-        const int base0 = -(row0 + kTileM - 1) - off;
-        const int lim0 = s.causal && row0 + off < nk - 1 ? row0 + off : nk - 1;
-        float bias_l = 0.f, bias_r = 0.f, wv0 = 0.f, wv1 = 0.f;
-        auto windowed = [&](int j) {
-            return bias_near(p.bias, base0 + j * kTileN) || lim0 - j * kTileN < kTileN - 1;
-        };
-        auto fetch = [&](int j) {
-            const int r = base0 + j * kTileN + wq * 32 + lane;
-            wv0 = bias_at(p.bias, s.Hq, hq_b, r, err);
-            wv1 = bias_at(p.bias, s.Hq, hq_b, r + 128, err);
-        };
-        auto fill = [&]() {
-            const uint32_t a = win0 + (cnt_fill & 1) * (kBiasWindow * 4) + (wq * 32 + lane) * 4;
-            sts_f32(a, wv0);
-            sts_f32(a + 512, wv1);
-            ++cnt_fill;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_w);
-        };
-        if constexpr (BIAS) {
-            bias_l = bias_at(p.bias, s.Hq, hq_b, p.bias.first, err);
-            bias_r = bias_at(p.bias, s.Hq, hq_b, p.bias.first + p.bias.span - 1, err);
-            if (windowed(j0)) {
-                fetch(j0);
-                fill();
-            }
-            if (j0 + 1 < n_t && windowed(j0 + 1)) fetch(j0 + 1);
-        }
         float m = -INFINITY;  // running max of scaled scores, log2 units
         float l = 0.f;        // normaliser of O (see softmax_tile)
         float lx = 0.f;       // running sum of the unrounded probabilities (gives the LSE)
         for (int j = j0; j < n_t; ++j) {
+            float2 bias = make_float2(0.f, 0.f);
+            const uint32_t wslot = cnt_s & 1;
+            if constexpr (BIAS) {   // (a bias a tile: counted as the S tiles are)
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_full[t][wslot]), (cnt_s >> 1) & 1,
+                                                       abort_flag));
+                if (!ok) break;
+                bias = *const_cast<const float2*>(&bars->bias[t][wslot]);
+            }
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_s, cnt_s & 1, abort_flag, 32));
             ++cnt_s;
             if (!ok) break;
@@ -892,19 +933,15 @@ __device__ void run_softmax(int t, int wq, int lane, uint8_t* smem, Bars* bars, 
             tmem_wait_ld();
             const int lim = last_key - j * kTileN;  // column c allowed iff c <= lim
             if constexpr (BIAS) {
-                if (windowed(j)) {
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_w, cnt_win & 1, abort_flag, 32));
-                    if (!ok) break;
+                if (bias.x != 0.f) {
                     // column c of row i is distance base + c - i + 127
-                    const uint32_t win = win0 + (cnt_win & 1) * (kBiasWindow * 4) + (127 - wq * 32 - lane) * 4;
-                    ++cnt_win;
+                    const uint32_t win = windows + wslot * (kBiasWindow * 4) + (127 - wq * 32 - lane) * 4;
                     if (__any_sync(0xFFFFFFFFu, lim < kTileN - 1))
                         softmax_tile<D, true, kBiasTile>(sr, lim, j - j0, c, tS, tO, m, l, lx, 0.f, win);
                     else
                         softmax_tile<D, false, kBiasTile>(sr, lim, j - j0, c, tS, tO, m, l, lx, 0.f, win);
                 } else {
-                    softmax_tile<D, false, kBiasConst>(sr, lim, j - j0, c, tS, tO, m, l, lx,
-                                                       base0 + j * kTileN + 254 <= p.bias.first ? bias_l : bias_r);
+                    softmax_tile<D, false, kBiasConst>(sr, lim, j - j0, c, tS, tO, m, l, lx, bias.y);
                 }
             } else if (__any_sync(0xFFFFFFFFu, lim < kTileN - 1))
                 softmax_tile<D, true>(sr, lim, j - j0, c, tS, tO, m, l, lx);
@@ -915,8 +952,7 @@ __device__ void run_softmax(int t, int wq, int lane, uint8_t* smem, Bars* bars, 
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_p);
             if constexpr (BIAS) {
-                if (j + 1 < n_t && windowed(j + 1)) fill();
-                if (j + 2 < n_t && windowed(j + 2)) fetch(j + 2);
+                if (lane == 0) mbar_arrive(smem_u32(&bars->win_empty[t][wslot]));
             }
         }
         if (!ok) break;
@@ -988,7 +1024,10 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             mbar_init(smem_u32(&bars->s_full[t]), 1);
             mbar_init(smem_u32(&bars->p_full[t]), 4);
             mbar_init(smem_u32(&bars->o_full[t]), 1);
-            mbar_init(smem_u32(&bars->win_full[t]), 4);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_u32(&bars->win_full[t][i]), 1);
+                mbar_init(smem_u32(&bars->win_empty[t][i]), 4);
+            }
         }
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(smem_u32(&bars->kv_full[i]), 1);
@@ -996,7 +1035,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bars->unit_full[i]), 1);
-            mbar_init(smem_u32(&bars->unit_empty[i]), kUnitConsumers);
+            mbar_init(smem_u32(&bars->unit_empty[i]), unit_consumers(BIAS));
         }
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort = 0;
@@ -1019,6 +1058,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         reg_dealloc<kRegsControl>();
         if (warp == 0) run_producer<D, VARLEN>(&tq, &tk, &tv, smem, bars, p, err);
         if (warp == 1) run_mma<D>(smem, bars, tmem, p, err);
+        if constexpr (BIAS) {
+            if (warp >= 2) run_bias<D, VARLEN>(warp - 2, lane, smem, bars, p, err);
+        }
     } else {
         reg_alloc<kRegsSoftmax>();
         const int t = (warp - 4) >> 2;
