@@ -604,20 +604,24 @@ __device__ __forceinline__ float* bias_sums(const BwdParams& p, const BwdWork& w
 }
 
 // The bias of a tile whose distances are base .. base + 254, for head hq, into its
-// slot (whole warp): a window, or the value of the map's end.
-__device__ __forceinline__ void give_bias(const BiasArgs& a, int Hq, int hq, int base, float left, float right,
-                                          uint32_t window, TileBias* tb, int lane, unsigned int* err) {
-    const bool near = bias_near(a, base);
+// slot (whole warp): a window, or the value of the map's end.  Fetched before the
+// slot is awaited (its phase `parity`, where `wait`).
+__device__ __forceinline__ bool give_bias(const BiasArgs& a, int Hq, int hq, int base, float left, float right,
+                                          uint32_t window, TileBias* tb, uint64_t* full, uint64_t* empty, bool wait,
+                                          uint32_t parity, const volatile int* abort_flag, int lane,
+                                          unsigned int* err) {
+    const bool near = bias_near(a, base), before = base + 254 <= a.first;
+    float v[kBiasWindow / 32];
+    if (near) bias_at(a, Hq, hq, base + lane, v, err);
+    if (wait && !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(empty), parity, abort_flag))) return false;
     if (near) {
-        float v[kBiasWindow / 32];
-#pragma unroll
-        for (int i = 0; i < kBiasWindow / 32; ++i) v[i] = bias_at(a, Hq, hq, base + 32 * i + lane, err);
 #pragma unroll
         for (int i = 0; i < kBiasWindow / 32; ++i) sts_f32(window + (32 * i + lane) * 4, v[i]);
     }
-    const bool before = base + 254 <= a.first;
     if (lane == 0) *tb = TileBias{near ? kBiasInWindow : before ? kBiasBefore : kBiasAfter, before ? left : right};
     __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(full));
+    return true;
 }
 
 // Looks up each Q tile's biases, up to two tiles ahead of the P/dS warps.
@@ -636,13 +640,10 @@ __device__ void bwd_bias_lookup(int lane, uint8_t* smem, BwdBars* bars, const Bw
             const float right = bias_at(p.bias, p.Hq, hq, p.bias.first + p.bias.span - 1, err);
             for (int i = 0; i < w.n_qt_cta; ++i, ++n) {
                 const int st = n & 1;
-                if (n >= 2)
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_empty[st]), ((n >> 1) - 1) & 1,
-                                                           abort_flag));
+                ok = give_bias(p.bias, p.Hq, hq, w.k0 - ((w.qt_first + i) * kBT + w.off) - (kBT - 1), left, right,
+                               smem_u32(smem + C::kWin) + st * kBiasWindow * 4, &bars->bias[st], &bars->win_full[st],
+                               &bars->win_empty[st], n >= 2, ((n >> 1) - 1) & 1, abort_flag, lane, err);
                 if (!ok) break;
-                give_bias(p.bias, p.Hq, hq, w.k0 - ((w.qt_first + i) * kBT + w.off) - (kBT - 1), left, right,
-                          smem_u32(smem + C::kWin) + st * kBiasWindow * 4, &bars->bias[st], lane, err);
-                if (lane == 0) mbar_arrive(smem_u32(&bars->win_full[st]));
             }
         }
     }
@@ -650,12 +651,14 @@ __device__ void bwd_bias_lookup(int lane, uint8_t* smem, BwdBars* bars, const Bw
     __syncwarp();
 }
 
-// Adds up dS over distances.  A Q tile with a window has 255 of them, base .. base +
-// 254, each with parts from up to 8 warps; the head's next tile has those from base
-// - 128 on.  The running sum of distance r is held by lane r % 32, register r / 32 %
-// 8, and stored once the head's next tile does not have it (a distance beyond the
-// map goes to the sum of its side).  Each (key tile, head) of the workspace is written
-// whole: here, and the far tiles' sums by the P/dS warps.
+// Adds up dS over distances.  Warp e = 4 grp + wq of the P/dS warps leaves, in place
+// 32 k + s of its 96, the sum at distance base + 127 + 32 wq - 64 grp + s - 32 k (DiagSums):
+// base - 1 + 32 m + s with m = 4 + wq - 2 grp - k in 0..7, so lane s holds a tile's 255
+// distances (base - 1 has no element) in 8 registers without any index arithmetic.
+// The head's next tile starts 128 lower: its registers 4..7 are this one's 0..3,
+// and this one's 4..7 are done.  A distance beyond the map goes to the sum of its
+// side.  Each (key tile, head) of the workspace is written whole: here, and the far
+// tiles' sums by the P/dS warps.
 template <int D, bool VARLEN>
 __device__ void bwd_bias_sums(int lane, uint8_t* smem, BwdBars* bars, const BwdParams& p, unsigned n_items,
                               unsigned int* err) {
@@ -666,47 +669,52 @@ __device__ void bwd_bias_sums(int lane, uint8_t* smem, BwdBars* bars, const BwdP
     uint32_t n = 0;   // sets of diagonal sums read
     for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
         const BwdWork w = bwd_item<VARLEN>(p, idx, err);
+        const int base0 = w.k0 - (w.qt_first * kBT + w.off) - (kBT - 1);
         for (int h = 0; h < p.group && ok; ++h) {
             float* out = bias_sums(p, w, w.g * p.group + h);
             // (each lane clears what it may store to)
-            for (int x = (lane - first) & 31; x < span; x += 32) out[x] = 0.f;
+            for (int x = (lane + base0 - 1 - first) & 31; x < span; x += 32) out[x] = 0.f;
             if (w.n_tiles == 0) {
                 if (lane < 18) out[span + lane] = 0.f;
                 continue;
             }
             float own[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             float side_l = 0.f, side_r = 0.f;
+            auto done = [&](int m, int base) {
+                const int x = base - 1 + 32 * m + lane - first;
+                if (x < 0) side_l += own[m];
+                else if (x >= span) side_r += own[m];
+                else if (m > 0 || lane > 0) out[x] = own[m];
+            };
             for (int i = 0; i < w.n_qt_cta; ++i) {
-                const int base = w.k0 - ((w.qt_first + i) * kBT + w.off) - (kBT - 1);
+                const int base = base0 - i * kBT;
                 if (!bias_near(p.bias, base)) continue;
                 const uint32_t set = n & 1;
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->diag_full[set]), (n >> 1) & 1, abort_flag));
                 if (!ok) break;
                 ++n;
-                const uint32_t from = smem_u32(smem + C::kDiag) + set * C::kDiagBytes;
+                const uint32_t from = smem_u32(smem + C::kDiag) + set * C::kDiagBytes + lane * 4;
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const int at = (32 * r + lane - base) & 255;   // the distance, from base
+                for (int e = 0; e < 8; ++e)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        // warp e = 4 grp + wq holds distance base + 127 + 32 wq - 64 grp + d,
-                        // d = s - 32 k, in place 32 k + s
-                        const int d = at - 127 - 32 * (e & 3) + 64 * (e >> 2);
-                        if (d >= -63 && d <= 31) own[r] += lds_f32(from + (e * 96 + 64 * ((31 - d) >> 5) + d) * 4);
+                    for (int k = 0; k < 3; ++k) {
+                        constexpr int kTop = 4;
+                        own[kTop + (e & 3) - 2 * (e >> 2) - k] += lds_f32(from + (e * 96 + 32 * k) * 4);
                     }
-                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars->diag_empty[set]));
-                const bool more = i + 1 < w.n_qt_cta && bias_near(p.bias, base - kBT);
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const int at = (32 * r + lane - base) & 255;
-                    if (more && at <= 126) continue;
-                    const int x = base + at - first;
-                    if (x < 0) side_l += own[r];
-                    else if (x >= span) side_r += own[r];
-                    else if (at < 255) out[x] = own[r];
-                    own[r] = 0.f;
+                for (int m = 4; m < 8; ++m) done(m, base);
+                if (i + 1 < w.n_qt_cta && bias_near(p.bias, base - kBT)) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        own[m + 4] = own[m];
+                        own[m] = 0.f;
+                    }
+                } else {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) done(m, base);
+                    break;   // (the head's later tiles lie before the map)
                 }
             }
 #pragma unroll
@@ -1405,12 +1413,10 @@ __device__ void dq_bias_lookup(int lane, uint8_t* smem, DqBars* bars, const BwdP
         const float right = bias_at(p.bias, p.Hq, w.hq, p.bias.first + p.bias.span - 1, err);
         for (int j = 0; j < w.n_kv; ++j, ++n) {
             const int st = n & 1;
-            if (n >= 2)
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_empty[st]), ((n >> 1) - 1) & 1, abort_flag));
+            ok = give_bias(p.bias, p.Hq, w.hq, j * kBT - (w.q0 + kBT - 1) - w.off, left, right,
+                           smem_u32(smem + C::kWin) + st * kBiasWindow * 4, &bars->bias[st], &bars->win_full[st],
+                           &bars->win_empty[st], n >= 2, ((n >> 1) - 1) & 1, abort_flag, lane, err);
             if (!ok) break;
-            give_bias(p.bias, p.Hq, w.hq, j * kBT - (w.q0 + kBT - 1) - w.off, left, right,
-                      smem_u32(smem + C::kWin) + st * kBiasWindow * 4, &bars->bias[st], lane, err);
-            if (lane == 0) mbar_arrive(smem_u32(&bars->win_full[st]));
         }
     }
     if (!ok && lane == 0) atomicOr(err, kErrTimeout), *((volatile int*)&bars->abort) = 1;

@@ -850,10 +850,7 @@ __device__ void run_bias(int t, int lane, uint8_t* smem, Bars* bars, const FwdPa
             const int base = base0 + j * kTileN;
             const bool window = bias_near(a, base) || lim0 - j * kTileN < kTileN - 1;
             float v[kBiasWindow / 32];
-            if (window) {
-#pragma unroll
-                for (int i = 0; i < kBiasWindow / 32; ++i) v[i] = bias_at(a, s.Hq, hq, base + 32 * i + lane, err);
-            }
+            if (window) bias_at(a, s.Hq, hq, base + lane, v, err);
             if (n >= 2) {
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_empty[t][slot]), ((n >> 1) - 1) & 1,
                                                        abort_flag));

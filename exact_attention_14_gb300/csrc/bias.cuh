@@ -31,20 +31,33 @@ constexpr float kBiasLog2e = 1.44269504088896340736f;
 // is left out.  Above it, bias + score keeps at least the bias's own 24 bits.
 constexpr float kBiasMasked = -1e30f;
 
-// Bias of head h at distance r, times log2(e).  A bucket outside the table adds
-// nothing and is recorded in the error word.
-__device__ __forceinline__ float bias_at(const BiasArgs& a, int Hq, int h, int r, unsigned int* err) {
-    int i = r - a.first;
-    i = i < 0 ? 0 : (i < a.span ? i : a.span - 1);
-    const int bk = __ldg(a.buckets + i);
-    if ((unsigned)bk >= (unsigned)a.num_buckets) {
-        atomicOr(err, kErrBadSeqlen);
-        return 0.f;
+// Biases of head h at the distances r, r + 32, ..., times log2(e).  A bucket outside
+// the table adds nothing and is recorded in the error word.  Every bucket is fetched
+// before the first table entry: two waits for memory, however many there are.
+template <int N>
+__device__ __forceinline__ void bias_at(const BiasArgs& a, int Hq, int h, int r, float (&v)[N], unsigned int* err) {
+    int bk[N];
+    bool bad = false;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int i = r + 32 * n - a.first;
+        bk[n] = __ldg(a.buckets + min(max(i, 0), a.span - 1));
     }
-    const size_t at = (size_t)bk * Hq + h;
-    const float v = a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.table)[at])
-                           : __ldg(static_cast<const float*>(a.table) + at);
-    return v < kBiasMasked ? -INFINITY : v * kBiasLog2e;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const bool ok = (unsigned)bk[n] < (unsigned)a.num_buckets;
+        const size_t at = (size_t)(ok ? bk[n] : 0) * Hq + h;
+        const float x = a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.table)[at])
+                               : __ldg(static_cast<const float*>(a.table) + at);
+        v[n] = !ok ? 0.f : x < kBiasMasked ? -INFINITY : x * kBiasLog2e;
+        bad |= !ok;
+    }
+    if (bad) atomicOr(err, kErrBadSeqlen);
+}
+__device__ __forceinline__ float bias_at(const BiasArgs& a, int Hq, int h, int r, unsigned int* err) {
+    float v[1];
+    bias_at(a, Hq, h, r, v, err);
+    return v[0];
 }
 
 // Whether the 255 distances from `base` on need a window: some of them lie strictly
