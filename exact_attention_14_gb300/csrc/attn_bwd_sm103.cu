@@ -511,21 +511,12 @@ __device__ __forceinline__ void p_chunk(const uint32_t (&s)[32], uint32_t lse2s,
     }
 }
 
-// Sum of dS over a warp's diagonals (BIAS).  Lane s collects the elements whose
-// key - query is s, s - 32 or s - 64 in its 32 x 64 block: of query column x it
-// takes the value of lane (s + x) % 32, for the first of them while that does
-// not wrap, and so on.  One shuffle and one add an element; column order.
-struct DiagSums {
-    float a[3];   // distance s - 32 k
-    uint64_t far; // tiles with one bias: every element
-};
-
-// dS^T = P^T o (dP^T - D) for the same 32 query columns, packed to bf16 pairs;
-// with a bias (BM), summed in fp32 as well: over diagonals, or (kOneBias) all.
-template <int BM = kNoBias, int HALF = 0>
-__device__ __forceinline__ void ds_chunk_t(const float (&pf)[32], const uint32_t (&dp)[32],
-                                           uint32_t ds_vec, int qc, uint32_t (&dd)[16],
-                                           DiagSums* sums = nullptr, int lane = 0) {
+// dS^T = P^T o (dP^T - D) for the same 32 query columns, packed to bf16 pairs.  With a
+// bias its fp32 values are needed too: all of them summed (kOneBias, far), or left
+// in place of P^T (kWindowBias).
+template <int BM = kNoBias>
+__device__ __forceinline__ void ds_chunk_t(float (&pf)[32], const uint32_t (&dp)[32],
+                                           uint32_t ds_vec, int qc, uint32_t (&dd)[16], uint64_t* far = nullptr) {
 #pragma unroll
     for (int x4 = 0; x4 < 8; ++x4) {
         const float4 d4 = lds128_f32(ds_vec + 4u * (qc + 4 * x4));
@@ -538,15 +529,34 @@ __device__ __forceinline__ void ds_chunk_t(const float (&pf)[32], const uint32_t
                             f2_add(f2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1])), nd)),
                      d0, d1);
             dd[x] = pack_bf16x2(d0, d1);
-            if constexpr (BM == kOneBias) sums->far = f2_add(sums->far, f2(d0, d1));
+            if constexpr (BM == kOneBias) *far = f2_add(*far, f2(d0, d1));
             if constexpr (BM == kWindowBias) {
-                const float v0 = __shfl_sync(0xFFFFFFFFu, d0, lane + 2 * x);
-                if (lane < 32 - 2 * x) sums->a[HALF] += v0; else sums->a[HALF + 1] += v0;
-                const float v1 = __shfl_sync(0xFFFFFFFFu, d1, lane + 2 * x + 1);
-                if (lane < 31 - 2 * x) sums->a[HALF] += v1; else sums->a[HALF + 1] += v1;
+                pf[2 * x] = d0;
+                pf[2 * x + 1] = d1;
             }
         }
     }
+}
+
+// Sums of a warp's 32 keys x 64 queries of dS over their diagonals (BIAS): lane s
+// gets those of key - query = s, s - 32 and s - 64 (a, b, c).  Of query column x it
+// takes the value of lane (s + x) % 32, which is in a's diagonal (of the second 32
+// columns: b's) while s + x < 32, then in b's (c's).  b is what is left of the
+// sums of everything, so an element costs a shuffle and two adds.  Fixed order.
+__device__ __forceinline__ void diagonal_sums(const float (&lo)[32], const float (&hi)[32], int lane, float& a,
+                                              float& b, float& c) {
+    uint64_t all = 0;   // (0.f, 0.f): of lo, of hi
+    a = c = 0.f;
+#pragma unroll
+    for (int x = 0; x < 32; ++x) {
+        const float v = __shfl_sync(0xFFFFFFFFu, lo[x], lane + x), u = __shfl_sync(0xFFFFFFFFu, hi[x], lane + x);
+        if (lane < 32 - x) a += v;
+        else c += u;
+        all = f2_add(all, f2(v, u));
+    }
+    float v, u;
+    f2_split(all, v, u);
+    b = (v - a) + (u - c);
 }
 
 // Store of 32 columns [cc, cc + 32) of this warp's 32 rows of an output
@@ -604,13 +614,13 @@ __device__ __forceinline__ float* bias_sums(const BwdParams& p, const BwdWork& w
 }
 
 // The bias of a tile whose distances are base .. base + 254, for head hq, into its
-// slot (whole warp): a window, or the value of the map's end.  Fetched before the
-// slot is awaited (its phase `parity`, where `wait`).
-__device__ __forceinline__ bool give_bias(const BiasArgs& a, int Hq, int hq, int base, float left, float right,
-                                          uint32_t window, TileBias* tb, uint64_t* full, uint64_t* empty, bool wait,
+// slot (whole warp): a window (where it has masked keys, in any case), or the value
+// of the map's end.  Fetched before the slot is awaited (its phase `parity`, where `wait`).
+__device__ __forceinline__ bool give_bias(const BiasArgs& a, int Hq, int hq, int base, bool masked, float left,
+                                          float right, uint32_t window, TileBias* tb, uint64_t* full, uint64_t* empty, bool wait,
                                           uint32_t parity, const volatile int* abort_flag, int lane,
                                           unsigned int* err) {
-    const bool near = bias_near(a, base), before = base + 254 <= a.first;
+    const bool near = masked || bias_near(a, base), before = base + 254 <= a.first;
     float v[kBiasWindow / 32];
     if (near) bias_at(a, Hq, hq, base + lane, v, err);
     if (wait && !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(empty), parity, abort_flag))) return false;
@@ -622,6 +632,15 @@ __device__ __forceinline__ bool give_bias(const BiasArgs& a, int Hq, int hq, int
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(full));
     return true;
+}
+
+// Whether the tile with distances base .. base + 254 has masked keys: those past the
+// sequence's last, or (causal) past a query.
+__device__ __forceinline__ bool bwd_masked(const BwdParams& p, const BwdWork& w, int base) {
+    return w.k0 + kBT > w.nk || (p.causal && base + 254 > 0);
+}
+__device__ __forceinline__ bool bwd_window(const BwdParams& p, const BwdWork& w, int base) {
+    return bias_near(p.bias, base) || bwd_masked(p, w, base);
 }
 
 // Looks up each Q tile's biases, up to two tiles ahead of the P/dS warps.
@@ -640,8 +659,8 @@ __device__ void bwd_bias_lookup(int lane, uint8_t* smem, BwdBars* bars, const Bw
             const float right = bias_at(p.bias, p.Hq, hq, p.bias.first + p.bias.span - 1, err);
             for (int i = 0; i < w.n_qt_cta; ++i, ++n) {
                 const int st = n & 1;
-                ok = give_bias(p.bias, p.Hq, hq, w.k0 - ((w.qt_first + i) * kBT + w.off) - (kBT - 1), left, right,
-                               smem_u32(smem + C::kWin) + st * kBiasWindow * 4, &bars->bias[st], &bars->win_full[st],
+                const int base = w.k0 - ((w.qt_first + i) * kBT + w.off) - (kBT - 1);
+                ok = give_bias(p.bias, p.Hq, hq, base, bwd_masked(p, w, base), left, right, smem_u32(smem + C::kWin) + st * kBiasWindow * 4, &bars->bias[st], &bars->win_full[st],
                                &bars->win_empty[st], n >= 2, ((n >> 1) - 1) & 1, abort_flag, lane, err);
                 if (!ok) break;
             }
@@ -688,7 +707,7 @@ __device__ void bwd_bias_sums(int lane, uint8_t* smem, BwdBars* bars, const BwdP
             };
             for (int i = 0; i < w.n_qt_cta; ++i) {
                 const int base = base0 - i * kBT;
-                if (!bias_near(p.bias, base)) continue;
+                if (!bwd_window(p, w, base)) continue;
                 const uint32_t set = n & 1;
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->diag_full[set]), (n >> 1) & 1, abort_flag));
                 if (!ok) break;
@@ -705,7 +724,7 @@ __device__ void bwd_bias_sums(int lane, uint8_t* smem, BwdBars* bars, const BwdP
                 if (lane == 0) mbar_arrive(smem_u32(&bars->diag_empty[set]));
 #pragma unroll
                 for (int m = 4; m < 8; ++m) done(m, base);
-                if (i + 1 < w.n_qt_cta && bias_near(p.bias, base - kBT)) {
+                if (i + 1 < w.n_qt_cta && bwd_window(p, w, base - kBT)) {
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
                         own[m + 4] = own[m];
@@ -713,8 +732,12 @@ __device__ void bwd_bias_sums(int lane, uint8_t* smem, BwdBars* bars, const BwdP
                     }
                 } else {
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) done(m, base);
-                    break;   // (the head's later tiles lie before the map)
+                    for (int m = 0; m < 4; ++m) {
+                        done(m, base);
+                        own[m] = 0.f;
+                    }
+#pragma unroll
+                    for (int m = 4; m < 8; ++m) own[m] = 0.f;
                 }
             }
 #pragma unroll
@@ -770,6 +793,7 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
             uint32_t win = 0;
             if constexpr (BIAS) {
                 // keys past the sequence have dS = 0 (their rows of K are zeros)
+                // (a tile with masked keys has a window, an instantiation less)
                 if (w.k0 + kBT > w.nk) {
                     if (!p.causal) lim = -kBT;
                     if (jg >= w.nk) lim = kBT;
@@ -795,8 +819,7 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
                         if (masked) p_chunk<true, kWindowBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, 0.f, win);
                         else p_chunk<false, kWindowBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, 0.f, win);
                     } else {
-                        if (masked) p_chunk<true, kOneBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, tb.value);
-                        else p_chunk<false, kOneBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, tb.value);
+                        p_chunk<false, kOneBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, tb.value);
                     }
                 } else if (masked)
                     p_chunk<true>(sv, lse2s, cc * 32, p.c, lim, pf, pp);
@@ -818,23 +841,21 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->dp_full), gi & 1, abort_flag, 32));
             if (!ok) break;
             tc_fence_after();
-            DiagSums sums = {{0.f, 0.f, 0.f}, 0};
-            auto phase2 = [&](auto half, const float (&pf)[32]) {
-                constexpr int kHalf = decltype(half)::value;
-                const int cc = 2 * grp + kHalf;
+            uint64_t far = 0;   // BIAS: (0.f, 0.f), a tile of one bias
+            auto phase2 = [&](int cc, float (&pf)[32]) {
                 uint32_t dp[32], dd[16];
                 tmem_ld32(tdP + cc * 32, dp);
                 tmem_wait_ld();
                 if constexpr (BIAS) {
-                    if (window) ds_chunk_t<kWindowBias, kHalf>(pf, dp, ds_vec, cc * 32, dd, &sums, lane);
-                    else ds_chunk_t<kOneBias>(pf, dp, ds_vec, cc * 32, dd, &sums);
+                    if (window) ds_chunk_t<kWindowBias>(pf, dp, ds_vec, cc * 32, dd);
+                    else ds_chunk_t<kOneBias>(pf, dp, ds_vec, cc * 32, dd, &far);
                 } else {
                     ds_chunk_t(pf, dp, ds_vec, cc * 32, dd);
                 }
                 tmem_st16(tdP + a_chunk_col(cc), dd);
             };
-            phase2(std::integral_constant<int, 0>{}, pf0);
-            phase2(std::integral_constant<int, 1>{}, pf1);
+            phase2(2 * grp, pf0);
+            phase2(2 * grp + 1, pf1);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -843,7 +864,9 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
                 mbar_arrive(smem_u32(&bars->qd_empty[st]));
             }
             if constexpr (BIAS) {
-                if (window) {
+                if (window) {   // (while the tensor cores are at dK)
+                    float da, db, dc;
+                    diagonal_sums(pf0, pf1, lane, da, db, dc);
                     const uint32_t set = cnt_diag & 1;
                     if (cnt_diag >= 2)
                         ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->diag_empty[set]),
@@ -851,14 +874,15 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
                     if (!ok) break;
                     const uint32_t out = smem_u32(smem + C::kDiag) + set * C::kDiagBytes +
                                          ((grp * 4 + wq) * 96 + lane) * 4;
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) sts_f32(out + 128 * k, sums.a[k]);
+                    sts_f32(out, da);
+                    sts_f32(out + 128, db);
+                    sts_f32(out + 256, dc);
                     ++cnt_diag;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&bars->diag_full[set]));
                 } else {
                     float a, b;
-                    f2_split(sums.far, a, b);
+                    f2_split(far, a, b);
                     if (tb.kind == kBiasBefore) far_l += a + b; else far_r += a + b;
                 }
                 if (++qt == w.qt_first + w.n_qt_cta) {   // the head ends
@@ -1413,7 +1437,7 @@ __device__ void dq_bias_lookup(int lane, uint8_t* smem, DqBars* bars, const BwdP
         const float right = bias_at(p.bias, p.Hq, w.hq, p.bias.first + p.bias.span - 1, err);
         for (int j = 0; j < w.n_kv; ++j, ++n) {
             const int st = n & 1;
-            ok = give_bias(p.bias, p.Hq, w.hq, j * kBT - (w.q0 + kBT - 1) - w.off, left, right,
+            ok = give_bias(p.bias, p.Hq, w.hq, j * kBT - (w.q0 + kBT - 1) - w.off, false, left, right,
                            smem_u32(smem + C::kWin) + st * kBiasWindow * 4, &bars->bias[st], &bars->win_full[st],
                            &bars->win_empty[st], n >= 2, ((n >> 1) - 1) & 1, abort_flag, lane, err);
             if (!ok) break;
