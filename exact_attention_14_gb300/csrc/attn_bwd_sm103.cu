@@ -99,7 +99,8 @@ struct BwdCfg {
     static constexpr int kWin = kStg;
     static constexpr int kDiag = kWin + 2 * kBiasWindow * 4;
     static constexpr int kDiagBytes = 8 * 96 * 4;
-    static_assert(kDiag + 2 * kDiagBytes <= kLD, "bias windows and sums fit the staging");
+    static constexpr int kNoKey = kDiag + 2 * kDiagBytes;   // 128 floats of -inf
+    static_assert(kNoKey + 512 <= kLD, "bias windows and sums fit the staging");
 };
 
 // BIAS: registers of the control warps and of the P/dS warps (384 at 168).
@@ -616,13 +617,13 @@ __device__ __forceinline__ float* bias_sums(const BwdParams& p, const BwdWork& w
 // The bias of a tile whose distances are base .. base + 254, for head hq, into its
 // slot (whole warp): a window (where it has masked keys, in any case), or the value
 // of the map's end.  Fetched before the slot is awaited (its phase `parity`, where `wait`).
-__device__ __forceinline__ bool give_bias(const BiasArgs& a, int Hq, int hq, int base, bool masked, float left,
+__device__ __forceinline__ bool give_bias(const BiasArgs& a, int Hq, int hq, int base, int last, bool masked, float left,
                                           float right, uint32_t window, TileBias* tb, uint64_t* full, uint64_t* empty, bool wait,
                                           uint32_t parity, const volatile int* abort_flag, int lane,
                                           unsigned int* err) {
     const bool near = masked || bias_near(a, base), before = base + 254 <= a.first;
     float v[kBiasWindow / 32];
-    if (near) bias_at(a, Hq, hq, base + lane, v, err);
+    if (near) bias_at(a, Hq, hq, base + lane, last, v, err);
     if (wait && !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(empty), parity, abort_flag))) return false;
     if (near) {
 #pragma unroll
@@ -660,7 +661,7 @@ __device__ void bwd_bias_lookup(int lane, uint8_t* smem, BwdBars* bars, const Bw
             for (int i = 0; i < w.n_qt_cta; ++i, ++n) {
                 const int st = n & 1;
                 const int base = w.k0 - ((w.qt_first + i) * kBT + w.off) - (kBT - 1);
-                ok = give_bias(p.bias, p.Hq, hq, base, bwd_masked(p, w, base), left, right, smem_u32(smem + C::kWin) + st * kBiasWindow * 4, &bars->bias[st], &bars->win_full[st],
+                ok = give_bias(p.bias, p.Hq, hq, base, p.causal ? 0 : INT_MAX, bwd_masked(p, w, base), left, right, smem_u32(smem + C::kWin) + st * kBiasWindow * 4, &bars->bias[st], &bars->win_full[st],
                                &bars->win_empty[st], n >= 2, ((n >> 1) - 1) & 1, abort_flag, lane, err);
                 if (!ok) break;
             }
@@ -770,6 +771,10 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
     int g = 0;  // Q tiles done, over the CTA's items
     int u = 0;  // items with work
     uint32_t cnt_diag = 0;   // BIAS: sets of diagonal sums written
+    if constexpr (BIAS) {    // (each warp the same words, for its own reads)
+        for (int x = lane; x < kBT; x += 32) sts_f32(smem_u32(smem + C::kNoKey) + 4 * x, -INFINITY);
+        __syncwarp();
+    }
     for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
         const BwdWork w = bwd_item<VARLEN>(p, idx, err);
         const int jg = w.k0 + j;
@@ -787,23 +792,18 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
             const uint32_t lse2s = smem_u32(smem + C::kLD + st * 1024);
             const uint32_t ds_vec = lse2s + kBT * 4;
             // causal: query q0 + x sees key jg iff x >= jg - off - q0
-            int lim = jg - w.off - q0;
-            bool masked = p.causal && (q0 + w.off < w.k0 + kBT - 1);
+            const int lim = jg - w.off - q0;
+            const bool masked = p.causal && (q0 + w.off < w.k0 + kBT - 1);
             TileBias tb{kBiasBefore, 0.f};
             uint32_t win = 0;
             if constexpr (BIAS) {
-                // keys past the sequence have dS = 0 (their rows of K are zeros)
-                // (a tile with masked keys has a window, an instantiation less)
-                if (w.k0 + kBT > w.nk) {
-                    if (!p.causal) lim = -kBT;
-                    if (jg >= w.nk) lim = kBT;
-                    masked = true;
-                }
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_full[st]), (gi >> 1) & 1, abort_flag));
                 if (!ok) break;
                 tb = bars->bias[st];
-                // query column x of key row j is distance base + j - x + 127
+                // query column x of key row j is distance base + j - x + 127; a key past
+                // the sequence takes -inf throughout (its row of K is zeros)
                 win = smem_u32(smem + C::kWin) + (st * kBiasWindow + j + kBT - 1) * 4;
+                if (jg >= w.nk) win = smem_u32(smem + C::kNoKey) + (kBT - 1) * 4;
             }
             const bool window = BIAS && tb.kind == kBiasInWindow;
             // Phase 1: P^T from S^T for this warpgroup's 64 query columns, kept
@@ -816,8 +816,7 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
                 tmem_wait_ld();
                 if constexpr (BIAS) {
                     if (window) {
-                        if (masked) p_chunk<true, kWindowBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, 0.f, win);
-                        else p_chunk<false, kWindowBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, 0.f, win);
+                        p_chunk<false, kWindowBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, 0.f, win);
                     } else {
                         p_chunk<false, kOneBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, tb.value);
                     }
@@ -1437,7 +1436,9 @@ __device__ void dq_bias_lookup(int lane, uint8_t* smem, DqBars* bars, const BwdP
         const float right = bias_at(p.bias, p.Hq, w.hq, p.bias.first + p.bias.span - 1, err);
         for (int j = 0; j < w.n_kv; ++j, ++n) {
             const int st = n & 1;
-            ok = give_bias(p.bias, p.Hq, w.hq, j * kBT - (w.q0 + kBT - 1) - w.off, false, left, right,
+            const int base = j * kBT - (w.q0 + kBT - 1) - w.off;
+            const bool masked = (j + 1) * kBT > w.nk || (p.causal && base + 254 > 0);
+            ok = give_bias(p.bias, p.Hq, w.hq, base, p.causal ? 0 : INT_MAX, masked, left, right,
                            smem_u32(smem + C::kWin) + st * kBiasWindow * 4, &bars->bias[st], &bars->win_full[st],
                            &bars->win_empty[st], n >= 2, ((n >> 1) - 1) & 1, abort_flag, lane, err);
             if (!ok) break;
@@ -1482,10 +1483,11 @@ __device__ void dq_ds(int wq, int grp, int lane, uint8_t* smem, DqBars* bars, ui
             uint32_t win = 0;
             if constexpr (BIAS) {
                 // keys past the sequence: P = 0 (a bias can put their 2^-lse2 past
-                // fp32's range, and infinity times their zero rows of K is NaN)
+                // fp32's range, and infinity times their zero rows of K is NaN).  The
+                // causal limit is in the window.
                 const int last = w.nk - 1 - j * kBT;
-                lim = p.causal && lim < last ? lim : last;
-                masked = __any_sync(0xFFFFFFFFu, lim < kBT - 1);
+                lim = last;
+                masked = last < kBT - 1;
                 const int st = t & 1;
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_full[st]), (t >> 1) & 1, abort_flag));
                 if (!ok) break;
@@ -1508,8 +1510,7 @@ __device__ void dq_ds(int wq, int grp, int lane, uint8_t* smem, DqBars* bars, ui
                         if (masked) p_row_chunk<true, true>(sv, c2, nl2, cc * 32, lim, pf, win);
                         else p_row_chunk<false, true>(sv, c2, nl2, cc * 32, kBT, pf, win);
                     } else {
-                        if (masked) p_row_chunk<true>(sv, c2, nl2, cc * 32, lim, pf);
-                        else p_row_chunk<false>(sv, c2, nl2, cc * 32, kBT, pf);
+                        p_row_chunk<false>(sv, c2, nl2, cc * 32, kBT, pf);
                     }
                 } else if (masked)
                     p_row_chunk<true>(sv, c2, nl2, cc * 32, p.causal ? lim : kBT, pf);

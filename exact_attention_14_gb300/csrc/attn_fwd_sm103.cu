@@ -850,7 +850,7 @@ __device__ void run_bias(int t, int lane, uint8_t* smem, Bars* bars, const FwdPa
             const int base = base0 + j * kTileN;
             const bool window = bias_near(a, base) || lim0 - j * kTileN < kTileN - 1;
             float v[kBiasWindow / 32];
-            if (window) bias_at(a, s.Hq, hq, base + lane, v, err);
+            if (window) bias_at(a, s.Hq, hq, base + lane, s.causal ? 0 : INT_MAX, v, err);
             if (n >= 2) {
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_empty[t][slot]), ((n >> 1) - 1) & 1,
                                                        abort_flag));
@@ -928,12 +928,13 @@ __device__ void run_softmax(int t, int wq, int lane, uint8_t* smem, Bars* bars, 
             tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
             tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
             tmem_wait_ld();
-            const int lim = last_key - j * kTileN;  // column c allowed iff c <= lim
+            // column c allowed iff c <= lim (BIAS: the causal limit is in the window)
+            const int lim = (BIAS ? nk - 1 : last_key) - j * kTileN;
             if constexpr (BIAS) {
                 if (bias.x != 0.f) {
                     // column c of row i is distance base + c - i + 127
                     const uint32_t win = windows + wslot * (kBiasWindow * 4) + (127 - wq * 32 - lane) * 4;
-                    if (__any_sync(0xFFFFFFFFu, lim < kTileN - 1))
+                    if (nk - 1 - j * kTileN < kTileN - 1)   // (causal masking is in the window)
                         softmax_tile<D, true, kBiasTile>(sr, lim, j - j0, c, tS, tO, m, l, lx, 0.f, win);
                     else
                         softmax_tile<D, false, kBiasTile>(sr, lim, j - j0, c, tS, tO, m, l, lx, 0.f, win);

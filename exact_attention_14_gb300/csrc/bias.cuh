@@ -8,11 +8,12 @@
 // A tile of 128 query rows and 128 keys meets 255 distances, base .. base + 254.
 // Where they all lie on one side of the map (or at its end) the whole tile has one
 // bias, which costs a term of the exponent that is there anyway; other tiles take
-// theirs from a window of 256 floats in shared memory, one per distance, that the
-// warps fill a tile ahead.  Lanes of a warp hold consecutive rows, so a column's
+// theirs from a window of 256 floats in shared memory, one per distance, that a warp
+// of its own fills up to two tiles ahead.  Lanes of a warp hold consecutive rows, so a column's
 // 32 reads are 32 consecutive floats: no bank conflict.
 #pragma once
 
+#include <climits>
 #include <cuda_bf16.h>
 
 #include "ptx.cuh"
@@ -31,11 +32,13 @@ constexpr float kBiasLog2e = 1.44269504088896340736f;
 // is left out.  Above it, bias + score keeps at least the bias's own 24 bits.
 constexpr float kBiasMasked = -1e30f;
 
-// Biases of head h at the distances r, r + 32, ..., times log2(e).  A bucket outside
-// the table adds nothing and is recorded in the error word.  Every bucket is fetched
+// Biases of head h at the distances r, r + 32, ..., times log2(e); -inf for those above
+// `last` (causal masking is a bias of -inf at every distance above 0, so a window
+// masks by itself).  A bucket outside the table adds nothing and is recorded in the
+// error word.  Every bucket is fetched
 // before the first table entry: two waits for memory, however many there are.
 template <int N>
-__device__ __forceinline__ void bias_at(const BiasArgs& a, int Hq, int h, int r, float (&v)[N], unsigned int* err) {
+__device__ __forceinline__ void bias_at(const BiasArgs& a, int Hq, int h, int r, int last, float (&v)[N], unsigned int* err) {
     int bk[N];
     bool bad = false;
 #pragma unroll
@@ -49,14 +52,14 @@ __device__ __forceinline__ void bias_at(const BiasArgs& a, int Hq, int h, int r,
         const size_t at = (size_t)(ok ? bk[n] : 0) * Hq + h;
         const float x = a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.table)[at])
                                : __ldg(static_cast<const float*>(a.table) + at);
-        v[n] = !ok ? 0.f : x < kBiasMasked ? -INFINITY : x * kBiasLog2e;
+        v[n] = r + 32 * n > last || (ok && x < kBiasMasked) ? -INFINITY : ok ? x * kBiasLog2e : 0.f;
         bad |= !ok;
     }
     if (bad) atomicOr(err, kErrBadSeqlen);
 }
 __device__ __forceinline__ float bias_at(const BiasArgs& a, int Hq, int h, int r, unsigned int* err) {
     float v[1];
-    bias_at(a, Hq, h, r, v, err);
+    bias_at(a, Hq, h, r, INT_MAX, v, err);
     return v[0];
 }
 
