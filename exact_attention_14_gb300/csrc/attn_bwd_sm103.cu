@@ -756,6 +756,75 @@ __device__ void bwd_bias_sums(int lane, uint8_t* smem, BwdBars* bars, const BwdP
     __syncwarp();
 }
 
+// One Q tile of a P/dS warp, with a bias: bwd_pds's two phases.  A tile with a window
+// leaves the sums of its diagonals in the next of two sets; one with a single bias adds
+// all of dS to `far`.  (Whole tiles of either kind in a piece of code of their own: as
+// alternatives inside the phases the loop fetched instructions 1.3 times as long, 171
+// and 130 us for 32 heads of 2048 positions whose tiles all have windows.)
+template <bool WINDOW>
+__device__ __forceinline__ bool pds_tile_bias(uint32_t tS, uint32_t tdP, uint32_t lse2s, int grp, int lane, float c,
+                                              uint32_t win, float bc, int gi, BwdBars* bars,
+                                              const volatile int* abort_flag, uint32_t diag, int set_bytes,
+                                              uint32_t& cnt_diag, float& far) {
+    constexpr int BM = WINDOW ? kWindowBias : kOneBias;
+    const int st = gi & 1;
+    float pf0[32], pf1[32];
+    auto phase1 = [&](int cc, float (&pf)[32]) {
+        uint32_t sv[32], pp[16];
+        tmem_ld32(tS + cc * 32, sv);
+        tmem_wait_ld();
+        p_chunk<false, BM>(sv, lse2s, cc * 32, c, 0, pf, pp, bc, win);
+        tmem_st16(tS + a_chunk_col(cc), pp);
+    };
+    phase1(2 * grp, pf0);
+    phase1(2 * grp + 1, pf1);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+        mbar_arrive(smem_u32(&bars->p_full));
+        mbar_arrive(smem_u32(&bars->win_empty[st]));
+    }
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->dp_full), gi & 1, abort_flag, 32))) return false;
+    tc_fence_after();
+    uint64_t all = 0;   // (0.f, 0.f)
+    auto phase2 = [&](int cc, float (&pf)[32]) {
+        uint32_t dp[32], dd[16];
+        tmem_ld32(tdP + cc * 32, dp);
+        tmem_wait_ld();
+        ds_chunk_t<BM>(pf, dp, lse2s + kBT * 4, cc * 32, dd, &all);
+        tmem_st16(tdP + a_chunk_col(cc), dd);
+    };
+    phase2(2 * grp, pf0);
+    phase2(2 * grp + 1, pf1);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+        mbar_arrive(smem_u32(&bars->ds_full));
+        mbar_arrive(smem_u32(&bars->qd_empty[st]));
+    }
+    if constexpr (WINDOW) {   // (while the tensor cores are at dK)
+        float da, db, dc;
+        diagonal_sums(pf0, pf1, lane, da, db, dc);
+        const uint32_t set = cnt_diag & 1;
+        if (cnt_diag >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->diag_empty[set]),
+                                                                ((cnt_diag >> 1) - 1) & 1, abort_flag)))
+            return false;
+        sts_f32(diag + set * set_bytes, da);
+        sts_f32(diag + set * set_bytes + 128, db);
+        sts_f32(diag + set * set_bytes + 256, dc);
+        ++cnt_diag;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->diag_full[set]));
+    } else {
+        float a, b;
+        f2_split(all, a, b);
+        far += a + b;
+    }
+    return true;
+}
+
 template <int D, bool OUT_F32, bool VARLEN, bool BIAS>
 __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars, uint32_t tmem,
                         const CUtensorMap* tdk, const CUtensorMap* tdv, const BwdParams& p,
@@ -794,96 +863,23 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
             // causal: query q0 + x sees key jg iff x >= jg - off - q0
             const int lim = jg - w.off - q0;
             const bool masked = p.causal && (q0 + w.off < w.k0 + kBT - 1);
-            TileBias tb{kBiasBefore, 0.f};
-            uint32_t win = 0;
             if constexpr (BIAS) {
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_full[st]), (gi >> 1) & 1, abort_flag));
                 if (!ok) break;
-                tb = bars->bias[st];
-                // query column x of key row j is distance base + j - x + 127; a key past
-                // the sequence takes -inf throughout (its row of K is zeros)
-                win = smem_u32(smem + C::kWin) + (st * kBiasWindow + j + kBT - 1) * 4;
-                if (jg >= w.nk) win = smem_u32(smem + C::kNoKey) + (kBT - 1) * 4;
-            }
-            const bool window = BIAS && tb.kind == kBiasInWindow;
-            // Phase 1: P^T from S^T for this warpgroup's 64 query columns, kept
-            // in registers and written as bf16 over the S^T columns it has read;
-            // with the other warpgroup's, releases dV(i) and S^T(i+1).
-            float pf0[32], pf1[32];
-            auto phase1 = [&](int cc, float (&pf)[32]) {
-                uint32_t sv[32], pp[16];
-                tmem_ld32(tS + cc * 32, sv);
-                tmem_wait_ld();
-                if constexpr (BIAS) {
-                    if (window) {
-                        p_chunk<false, kWindowBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, 0.f, win);
-                    } else {
-                        p_chunk<false, kOneBias>(sv, lse2s, cc * 32, p.c, lim, pf, pp, tb.value);
-                    }
-                } else if (masked)
-                    p_chunk<true>(sv, lse2s, cc * 32, p.c, lim, pf, pp);
-                else
-                    p_chunk<false>(sv, lse2s, cc * 32, p.c, lim, pf, pp);
-                tmem_st16(tS + a_chunk_col(cc), pp);
-            };
-            phase1(2 * grp, pf0);
-            phase1(2 * grp + 1, pf1);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
-            if constexpr (BIAS) {
-                if (lane == 0) mbar_arrive(smem_u32(&bars->win_empty[st]));
-            }
-            // Phase 2: dS^T from P^T and dP^T, written as bf16 over the dP^T
-            // columns already read; releases dK(i) and dP^T(i+1).
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->dp_full), gi & 1, abort_flag, 32));
-            if (!ok) break;
-            tc_fence_after();
-            uint64_t far = 0;   // BIAS: (0.f, 0.f), a tile of one bias
-            auto phase2 = [&](int cc, float (&pf)[32]) {
-                uint32_t dp[32], dd[16];
-                tmem_ld32(tdP + cc * 32, dp);
-                tmem_wait_ld();
-                if constexpr (BIAS) {
-                    if (window) ds_chunk_t<kWindowBias>(pf, dp, ds_vec, cc * 32, dd);
-                    else ds_chunk_t<kOneBias>(pf, dp, ds_vec, cc * 32, dd, &far);
+                const TileBias tb = bars->bias[st];
+                if (tb.kind == kBiasInWindow) {
+                    // query column x of key row j is distance base + j - x + 127; a key
+                    // past the sequence takes -inf throughout (its row of K is zeros)
+                    uint32_t win = smem_u32(smem + C::kWin) + (st * kBiasWindow + j + kBT - 1) * 4;
+                    if (jg >= w.nk) win = smem_u32(smem + C::kNoKey) + (kBT - 1) * 4;
+                    ok = pds_tile_bias<true>(tS, tdP, lse2s, grp, lane, p.c, win, 0.f, gi, bars, abort_flag,
+                                             smem_u32(smem + C::kDiag) + ((grp * 4 + wq) * 96 + lane) * 4,
+                                             C::kDiagBytes, cnt_diag, far_l);
                 } else {
-                    ds_chunk_t(pf, dp, ds_vec, cc * 32, dd);
+                    ok = pds_tile_bias<false>(tS, tdP, lse2s, grp, lane, p.c, 0u, tb.value, gi, bars, abort_flag, 0u,
+                                              0, cnt_diag, tb.kind == kBiasBefore ? far_l : far_r);
                 }
-                tmem_st16(tdP + a_chunk_col(cc), dd);
-            };
-            phase2(2 * grp, pf0);
-            phase2(2 * grp + 1, pf1);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_u32(&bars->ds_full));
-                mbar_arrive(smem_u32(&bars->qd_empty[st]));
-            }
-            if constexpr (BIAS) {
-                if (window) {   // (while the tensor cores are at dK)
-                    float da, db, dc;
-                    diagonal_sums(pf0, pf1, lane, da, db, dc);
-                    const uint32_t set = cnt_diag & 1;
-                    if (cnt_diag >= 2)
-                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->diag_empty[set]),
-                                                               ((cnt_diag >> 1) - 1) & 1, abort_flag));
-                    if (!ok) break;
-                    const uint32_t out = smem_u32(smem + C::kDiag) + set * C::kDiagBytes +
-                                         ((grp * 4 + wq) * 96 + lane) * 4;
-                    sts_f32(out, da);
-                    sts_f32(out + 128, db);
-                    sts_f32(out + 256, dc);
-                    ++cnt_diag;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&bars->diag_full[set]));
-                } else {
-                    float a, b;
-                    f2_split(far, a, b);
-                    if (tb.kind == kBiasBefore) far_l += a + b; else far_r += a + b;
-                }
+                if (!ok) break;
                 if (++qt == w.qt_first + w.n_qt_cta) {   // the head ends
 #pragma unroll
                     for (int s = 16; s > 0; s >>= 1) {
@@ -899,6 +895,48 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
                     qt = w.qt_first;
                     ++hq;
                 }
+                continue;
+            }
+            // Phase 1: P^T from S^T for this warpgroup's 64 query columns, kept
+            // in registers and written as bf16 over the S^T columns it has read;
+            // with the other warpgroup's, releases dV(i) and S^T(i+1).
+            float pf0[32], pf1[32];
+            auto phase1 = [&](int cc, float (&pf)[32]) {
+                uint32_t sv[32], pp[16];
+                tmem_ld32(tS + cc * 32, sv);
+                tmem_wait_ld();
+                if (masked)
+                    p_chunk<true>(sv, lse2s, cc * 32, p.c, lim, pf, pp);
+                else
+                    p_chunk<false>(sv, lse2s, cc * 32, p.c, lim, pf, pp);
+                tmem_st16(tS + a_chunk_col(cc), pp);
+            };
+            phase1(2 * grp, pf0);
+            phase1(2 * grp + 1, pf1);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
+            // Phase 2: dS^T from P^T and dP^T, written as bf16 over the dP^T
+            // columns already read; releases dK(i) and dP^T(i+1).
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->dp_full), gi & 1, abort_flag, 32));
+            if (!ok) break;
+            tc_fence_after();
+            auto phase2 = [&](int cc, float (&pf)[32]) {
+                uint32_t dp[32], dd[16];
+                tmem_ld32(tdP + cc * 32, dp);
+                tmem_wait_ld();
+                ds_chunk_t(pf, dp, ds_vec, cc * 32, dd);
+                tmem_st16(tdP + a_chunk_col(cc), dd);
+            };
+            phase2(2 * grp, pf0);
+            phase2(2 * grp + 1, pf1);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&bars->ds_full));
+                mbar_arrive(smem_u32(&bars->qd_empty[st]));
             }
         }
         if (!ok) break;
