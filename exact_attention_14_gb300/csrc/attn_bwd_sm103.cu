@@ -80,6 +80,9 @@ constexpr int kBT = 128;  // keys per K/V tile, query rows per Q tile
 constexpr float kBwdLog2e = 1.44269504088896340736f;
 constexpr int kMaxSmemPerBlock = 232448;
 
+// BIAS: the sums of dS over diagonals of a P/dS warp's threads, [22][33] (pds_tile_bias).
+constexpr int kDiagRow = 33, kDiagHalf = 11 * kDiagRow, kDiagFloats = 2 * kDiagHalf;
+
 template <int D>
 struct BwdCfg {
     static constexpr int kTile = kBT * D * 2;   // one 128-row bf16 tile
@@ -94,13 +97,14 @@ struct BwdCfg {
     static constexpr int kSmemBytes =
         kLayout + 1024 < kMaxSmemPerBlock ? kLayout + 1024 : kMaxSmemPerBlock;
     static_assert(kLayout <= kMaxSmemPerBlock, "shared memory budget");
-    // BIAS (dK and dV leave from registers): in the staging, two bias windows and
-    // two sets of the warps' diagonal sums of dS^T
+    // BIAS (dK and dV leave from registers): in the staging, two bias windows, the
+    // threads' sums of dS^T along diagonals (kDiagFloats a P/dS warp), and two sets of
+    // the warps' sums, 96 each
     static constexpr int kWin = kStg;
     static constexpr int kDiag = kWin + 2 * kBiasWindow * 4;
-    static constexpr int kDiagBytes = 8 * 96 * 4;
-    static constexpr int kNoKey = kDiag + 2 * kDiagBytes;   // 128 floats of -inf
-    static_assert(kNoKey + 512 <= kLD, "bias windows and sums fit the staging");
+    static constexpr int kSet = kDiag + 8 * kDiagFloats * 4;
+    static constexpr int kSetBytes = 8 * 96 * 4;
+    static_assert(kSet + 2 * kSetBytes <= kLD, "bias windows and sums fit the staging");
 };
 
 // BIAS: registers of the control warps and of the P/dS warps (384 at 168).
@@ -155,19 +159,15 @@ __device__ __forceinline__ bool bwd_varlen_seq(const BwdParams& p, int b, int& q
            (!p.causal || qe - qs <= ke - ks);
 }
 
-// BIAS: what the looking-up warp says of a tile: whether its biases are in the
-// slot's window, else the one that it has and the side of the map it lies on.
-enum : int { kBiasBefore = 0, kBiasAfter = 1, kBiasInWindow = 2 };
-struct __align__(8) TileBias {
-    int kind;
-    float value;
-};
+// BIAS: what the looking-up warp says of a tile whose biases are in the slot's window:
+// whether all of them are the one of the map's left or right end.
+enum TileBias : int { kBiasBefore = 0, kBiasAfter = 1, kBiasInside = 2 };
 
 struct __align__(8) BwdBars {
     uint64_t kv_full, kv_empty;  // K and V of an item; read by its last S^T and dP^T
     uint64_t qd_full[2], qd_empty[2];
     uint64_t s_full, dp_full, p_full, ds_full, acc_full, drain;
-    // BIAS: a Q tile's bias, a set of diagonal sums is there / has been read
+    // BIAS: a Q tile's bias is there / has been read; its diagonal sums
     uint64_t win_full[2], win_empty[2], diag_full[2], diag_empty[2];
     TileBias bias[2];
     uint32_t tmem_base;
@@ -478,15 +478,10 @@ __device__ void bwd_mma(uint8_t* smem, BwdBars* bars, uint32_t tmem, const BwdPa
 // P^T = 2^(S^T c - lse2) for 32 query columns [qc, qc + 32) of this thread's
 // key row, kept in fp32 (pf) and packed to bf16 pairs (pp).  lim: query column
 // qc + x is allowed iff qc + x >= lim (causal), else all.  The tile's lse2
-// comes from shared memory 4 at a time (broadcast).  With a bias (BM) it joins
-// -lse2: bc for every column, or query column q's own from shared address
-// win - 4 q.
-enum : int { kNoBias = 0, kOneBias = 1, kWindowBias = 2 };
-
-template <bool MASKED, int BM = kNoBias>
+// comes from shared memory 4 at a time (broadcast).
+template <bool MASKED>
 __device__ __forceinline__ void p_chunk(const uint32_t (&s)[32], uint32_t lse2s, int qc, float c,
-                                        int lim, float (&pf)[32], uint32_t (&pp)[16], float bc = 0.f,
-                                        uint32_t win = 0) {
+                                        int lim, float (&pf)[32], uint32_t (&pp)[16]) {
     const uint64_t c2 = f2(c, c);
 #pragma unroll
     for (int x4 = 0; x4 < 8; ++x4) {
@@ -495,9 +490,7 @@ __device__ __forceinline__ void p_chunk(const uint32_t (&s)[32], uint32_t lse2s,
         for (int h = 0; h < 2; ++h) {
             const int x = 2 * x4 + h;
             const int q = qc + 2 * x;
-            uint64_t nl = h == 0 ? f2(-l4.x, -l4.y) : f2(-l4.z, -l4.w);
-            if constexpr (BM == kOneBias) nl = f2_add(nl, f2(bc, bc));
-            if constexpr (BM == kWindowBias) nl = f2_add(nl, f2(lds_f32(win - 4 * q), lds_f32(win - 4 * q - 4)));
+            const uint64_t nl = h == 0 ? f2(-l4.x, -l4.y) : f2(-l4.z, -l4.w);
             float a0, a1;
             f2_split(f2_fma(f2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), c2, nl), a0, a1);
             float p0 = ex2(a0), p1 = ex2(a1);
@@ -512,12 +505,9 @@ __device__ __forceinline__ void p_chunk(const uint32_t (&s)[32], uint32_t lse2s,
     }
 }
 
-// dS^T = P^T o (dP^T - D) for the same 32 query columns, packed to bf16 pairs.  With a
-// bias its fp32 values are needed too: all of them summed (kOneBias, far), or left
-// in place of P^T (kWindowBias).
-template <int BM = kNoBias>
-__device__ __forceinline__ void ds_chunk_t(float (&pf)[32], const uint32_t (&dp)[32],
-                                           uint32_t ds_vec, int qc, uint32_t (&dd)[16], uint64_t* far = nullptr) {
+// dS^T = P^T o (dP^T - D) for the same 32 query columns, packed to bf16 pairs.
+__device__ __forceinline__ void ds_chunk_t(const float (&pf)[32], const uint32_t (&dp)[32],
+                                           uint32_t ds_vec, int qc, uint32_t (&dd)[16]) {
 #pragma unroll
     for (int x4 = 0; x4 < 8; ++x4) {
         const float4 d4 = lds128_f32(ds_vec + 4u * (qc + 4 * x4));
@@ -530,34 +520,8 @@ __device__ __forceinline__ void ds_chunk_t(float (&pf)[32], const uint32_t (&dp)
                             f2_add(f2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1])), nd)),
                      d0, d1);
             dd[x] = pack_bf16x2(d0, d1);
-            if constexpr (BM == kOneBias) *far = f2_add(*far, f2(d0, d1));
-            if constexpr (BM == kWindowBias) {
-                pf[2 * x] = d0;
-                pf[2 * x + 1] = d1;
-            }
         }
     }
-}
-
-// Sums of a warp's 32 keys x 64 queries of dS over their diagonals (BIAS): lane s
-// gets those of key - query = s, s - 32 and s - 64 (a, b, c).  Of query column x it
-// takes the value of lane (s + x) % 32, which is in a's diagonal (of the second 32
-// columns: b's) while s + x < 32, then in b's (c's).  b is what is left of the
-// sums of everything, so an element costs a shuffle and two adds.  Fixed order.
-__device__ __forceinline__ void diagonal_sums(const float (&lo)[32], const float (&hi)[32], int lane, float& a,
-                                              float& b, float& c) {
-    uint64_t all = 0;   // (0.f, 0.f): of lo, of hi
-    a = c = 0.f;
-#pragma unroll
-    for (int x = 0; x < 32; ++x) {
-        const float v = __shfl_sync(0xFFFFFFFFu, lo[x], lane + x), u = __shfl_sync(0xFFFFFFFFu, hi[x], lane + x);
-        if (lane < 32 - x) a += v;
-        else c += u;
-        all = f2_add(all, f2(v, u));
-    }
-    float v, u;
-    f2_split(all, v, u);
-    b = (v - a) + (u - c);
 }
 
 // Store of 32 columns [cc, cc + 32) of this warp's 32 rows of an output
@@ -614,34 +578,29 @@ __device__ __forceinline__ float* bias_sums(const BwdParams& p, const BwdWork& w
     return p.partial + (((size_t)w.b * p.n_kt + w.kt) * p.Hq + hq) * bias_partial_floats(p.bias.span);
 }
 
-// The bias of a tile whose distances are base .. base + 254, for head hq, into its
-// slot (whole warp): a window (where it has masked keys, in any case), or the value
-// of the map's end.  Fetched before the slot is awaited (its phase `parity`, where `wait`).
-__device__ __forceinline__ bool give_bias(const BiasArgs& a, int Hq, int hq, int base, int last, bool masked, float left,
-                                          float right, uint32_t window, TileBias* tb, uint64_t* full, uint64_t* empty, bool wait,
-                                          uint32_t parity, const volatile int* abort_flag, int lane,
-                                          unsigned int* err) {
-    const bool near = masked || bias_near(a, base), before = base + 254 <= a.first;
+// The biases of a tile whose distances are base .. base + 254, for head hq, into its
+// slot's window (whole warp); -inf at the distances above `last`.  Fetched before the
+// slot is awaited (its phase `parity`, where `wait`).  A tile whose distances all have
+// the bias of the map's end, and none above `last`, fetches nothing.
+__device__ __forceinline__ bool give_bias(const BiasArgs& a, int Hq, int hq, int base, int last, float left,
+                                          float right, uint32_t window, TileBias* kind, uint64_t* full,
+                                          uint64_t* empty, bool wait, uint32_t parity,
+                                          const volatile int* abort_flag, int lane, unsigned int* err) {
+    const bool inside = bias_near(a, base), before = base + 254 <= a.first;
     float v[kBiasWindow / 32];
-    if (near) bias_at(a, Hq, hq, base + lane, last, v, err);
-    if (wait && !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(empty), parity, abort_flag))) return false;
-    if (near) {
+    if (inside || base + 254 > last) {
+        bias_at(a, Hq, hq, base + lane, last, v, err);
+    } else {
 #pragma unroll
-        for (int i = 0; i < kBiasWindow / 32; ++i) sts_f32(window + (32 * i + lane) * 4, v[i]);
+        for (int i = 0; i < kBiasWindow / 32; ++i) v[i] = before ? left : right;
     }
-    if (lane == 0) *tb = TileBias{near ? kBiasInWindow : before ? kBiasBefore : kBiasAfter, before ? left : right};
+    if (wait && !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(empty), parity, abort_flag))) return false;
+#pragma unroll
+    for (int i = 0; i < kBiasWindow / 32; ++i) sts_f32(window + (32 * i + lane) * 4, v[i]);
+    if (lane == 0) *kind = inside ? kBiasInside : before ? kBiasBefore : kBiasAfter;
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(full));
     return true;
-}
-
-// Whether the tile with distances base .. base + 254 has masked keys: those past the
-// sequence's last, or (causal) past a query.
-__device__ __forceinline__ bool bwd_masked(const BwdParams& p, const BwdWork& w, int base) {
-    return w.k0 + kBT > w.nk || (p.causal && base + 254 > 0);
-}
-__device__ __forceinline__ bool bwd_window(const BwdParams& p, const BwdWork& w, int base) {
-    return bias_near(p.bias, base) || bwd_masked(p, w, base);
 }
 
 // Looks up each Q tile's biases, up to two tiles ahead of the P/dS warps.
@@ -661,7 +620,7 @@ __device__ void bwd_bias_lookup(int lane, uint8_t* smem, BwdBars* bars, const Bw
             for (int i = 0; i < w.n_qt_cta; ++i, ++n) {
                 const int st = n & 1;
                 const int base = w.k0 - ((w.qt_first + i) * kBT + w.off) - (kBT - 1);
-                ok = give_bias(p.bias, p.Hq, hq, base, p.causal ? 0 : INT_MAX, bwd_masked(p, w, base), left, right, smem_u32(smem + C::kWin) + st * kBiasWindow * 4, &bars->bias[st], &bars->win_full[st],
+                ok = give_bias(p.bias, p.Hq, hq, base, p.causal ? 0 : INT_MAX, left, right, smem_u32(smem + C::kWin) + st * kBiasWindow * 4, &bars->bias[st], &bars->win_full[st],
                                &bars->win_empty[st], n >= 2, ((n >> 1) - 1) & 1, abort_flag, lane, err);
                 if (!ok) break;
             }
@@ -671,14 +630,14 @@ __device__ void bwd_bias_lookup(int lane, uint8_t* smem, BwdBars* bars, const Bw
     __syncwarp();
 }
 
-// Adds up dS over distances.  Warp e = 4 grp + wq of the P/dS warps leaves, in place
-// 32 k + s of its 96, the sum at distance base + 127 + 32 wq - 64 grp + s - 32 k (DiagSums):
-// base - 1 + 32 m + s with m = 4 + wq - 2 grp - k in 0..7, so lane s holds a tile's 255
-// distances (base - 1 has no element) in 8 registers without any index arithmetic.
-// The head's next tile starts 128 lower: its registers 4..7 are this one's 0..3,
-// and this one's 4..7 are done.  A distance beyond the map goes to the sum of its
-// side.  Each (key tile, head) of the workspace is written whole: here, and the far
-// tiles' sums by the P/dS warps.
+// Adds up dS over distances.  A P/dS warp (wq, grp) has left in place 32 k + s of its 96
+// the sum at distance base + 127 + 32 wq - 64 grp + s - 32 k: place s of group m = 4 + wq
+// - 2 grp - k of the tile's 8 groups of 32 (group m starts at base - 1 + 32 m), so lane s
+// holds a tile's 255 distances (base - 1 has no element) in 8 registers without any
+// index arithmetic.  The last four groups are then done; the first four are the last
+// four of the head's next tile, which starts 128 lower.  A distance beyond the map goes
+// to the sum of its side.  Each (key tile, head) of the workspace is written whole:
+// here, and the sums of tiles beyond the map by the P/dS warps.
 template <int D, bool VARLEN>
 __device__ void bwd_bias_sums(int lane, uint8_t* smem, BwdBars* bars, const BwdParams& p, unsigned n_items,
                               unsigned int* err) {
@@ -686,7 +645,7 @@ __device__ void bwd_bias_sums(int lane, uint8_t* smem, BwdBars* bars, const BwdP
     const volatile int* abort_flag = &bars->abort;
     const int first = p.bias.first, span = p.bias.span;
     bool ok = true;
-    uint32_t n = 0;   // sets of diagonal sums read
+    uint32_t n = 0;   // tiles' sums read
     for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
         const BwdWork w = bwd_item<VARLEN>(p, idx, err);
         const int base0 = w.k0 - (w.qt_first * kBT + w.off) - (kBT - 1);
@@ -698,47 +657,39 @@ __device__ void bwd_bias_sums(int lane, uint8_t* smem, BwdBars* bars, const BwdP
                 if (lane < 18) out[span + lane] = 0.f;
                 continue;
             }
-            float own[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             float side_l = 0.f, side_r = 0.f;
-            auto done = [&](int m, int base) {
-                const int x = base - 1 + 32 * m + lane - first;
-                if (x < 0) side_l += own[m];
-                else if (x >= span) side_r += own[m];
-                else if (m > 0 || lane > 0) out[x] = own[m];
-            };
+            float own[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             for (int i = 0; i < w.n_qt_cta; ++i) {
                 const int base = base0 - i * kBT;
-                if (!bwd_window(p, w, base)) continue;
+                if (!bias_near(p.bias, base)) continue;
                 const uint32_t set = n & 1;
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->diag_full[set]), (n >> 1) & 1, abort_flag));
                 if (!ok) break;
                 ++n;
-                const uint32_t from = smem_u32(smem + C::kDiag) + set * C::kDiagBytes + lane * 4;
+                const uint32_t from = smem_u32(smem + C::kSet) + set * C::kSetBytes + lane * 4;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
+                for (int e = 0; e < 8; ++e) {
+                    constexpr int kTop = 4;
+                    const int m = kTop + (e & 3) - 2 * (e >> 2);
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        constexpr int kTop = 4;
-                        own[kTop + (e & 3) - 2 * (e >> 2) - k] += lds_f32(from + (e * 96 + 32 * k) * 4);
-                    }
+                    for (int k = 0; k < 3; ++k) own[m - k] += lds_f32(from + (e * 96 + 32 * k) * 4);
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars->diag_empty[set]));
+                const bool more = i + 1 < w.n_qt_cta && bias_near(p.bias, base - kBT);
 #pragma unroll
-                for (int m = 4; m < 8; ++m) done(m, base);
-                if (i + 1 < w.n_qt_cta && bwd_window(p, w, base - kBT)) {
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        own[m + 4] = own[m];
-                        own[m] = 0.f;
+                for (int m = 7; m >= 0; --m) {
+                    if (m >= 4 || !more) {
+                        const int x = base - 1 + 32 * m + lane - first;
+                        if (x < 0) side_l += own[m];
+                        else if (x >= span) side_r += own[m];
+                        else if (m > 0 || lane > 0) out[x] = own[m];
                     }
-                } else {
+                }
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        done(m, base);
-                        own[m] = 0.f;
-                    }
-#pragma unroll
-                    for (int m = 4; m < 8; ++m) own[m] = 0.f;
+                for (int m = 0; m < 4; ++m) {
+                    own[m + 4] = more ? own[m] : 0.f;
+                    own[m] = 0.f;
                 }
             }
 #pragma unroll
@@ -756,28 +707,53 @@ __device__ void bwd_bias_sums(int lane, uint8_t* smem, BwdBars* bars, const BwdP
     __syncwarp();
 }
 
-// One Q tile of a P/dS warp, with a bias: bwd_pds's two phases.  A tile with a window
-// leaves the sums of its diagonals in the next of two sets; one with a single bias adds
-// all of dS to `far`.  (Whole tiles of either kind in a piece of code of their own: as
-// alternatives inside the phases the loop fetched instructions 1.3 times as long, 171
-// and 130 us for 32 heads of 2048 positions whose tiles all have windows.)
-template <bool WINDOW>
-__device__ __forceinline__ bool pds_tile_bias(uint32_t tS, uint32_t tdP, uint32_t lse2s, int grp, int lane, float c,
-                                              uint32_t win, float bc, int gi, BwdBars* bars,
-                                              const volatile int* abort_flag, uint32_t diag, int set_bytes,
-                                              uint32_t& cnt_diag, float& far) {
-    constexpr int BM = WINDOW ? kWindowBias : kOneBias;
+// One Q tile of a P/dS warp, with a bias: bwd_pds's two phases on the fragments of
+// tmem_ld_16x256b_x8.  Thread (a, b) = (lane / 4, lane % 4) has key rows a + 8 i, i < 4,
+// and query columns 8 j + 2 b + e, j < 8, e < 2, of the warp's 32 x 64 block: key -
+// query is a - 2 b - e + 8 (i - j), one of 22 distances.  So it reads 22 biases for
+// its 64 elements, and adds those of dS up to 22 sums in registers, two at a time; a row
+// a thread needs 64 of each, and the sums 64 shuffles.  (With a row a thread 147 us, so
+// 128 us: 32 heads of 2048 positions, every tile inside the map; without a bias 106.)
+// The threads' sums meet in `diag` ([e][k][lane] with k = i - j + 7, rows of 33), where
+// lane s finds, for every 2 b + e, its parts of distance s, s - 32 and s - 64 (`part`,
+// no bank conflicts but one), and go to the next of two sets; where the whole tile has
+// one bias, all to `far`.  (Read there by bwd_bias_sums alone they kept the P/dS warps
+// waiting, 162 us, or unrolled for speed filled the instruction cache, 154.)
+__device__ __forceinline__ bool pds_tile_bias(uint32_t tS, uint32_t tdP, uint32_t cols, int lane, float c,
+                                              uint32_t win, int rows_live, TileBias kind, int gi, BwdBars* bars,
+                                              const volatile int* abort_flag, uint32_t diag,
+                                              const uint32_t (&part)[8], uint32_t set, int set_bytes,
+                                              uint32_t& cnt_diag, float& far_l, float& far_r) {
     const int st = gi & 1;
-    float pf0[32], pf1[32];
-    auto phase1 = [&](int cc, float (&pf)[32]) {
-        uint32_t sv[32], pp[16];
-        tmem_ld32(tS + cc * 32, sv);
-        tmem_wait_ld();
-        p_chunk<false, BM>(sv, lse2s, cc * 32, c, 0, pf, pp, bc, win);
-        tmem_st16(tS + a_chunk_col(cc), pp);
-    };
-    phase1(2 * grp, pf0);
-    phase1(2 * grp + 1, pf1);
+    uint32_t s[2][32];   // S^T, then P^T, of rows [0, 16) and [16, 32)
+    tmem_ld_16x256b_x8(tS, s[0]);
+    tmem_ld_16x256b_x8(tS + (16u << 16), s[1]);
+    uint64_t bias[11];
+#pragma unroll
+    for (int k = 0; k < 11; ++k) bias[k] = f2(lds_f32(win + 32 * (k - 7)), lds_f32(win + 32 * (k - 7) - 4));
+    tmem_wait_ld();
+    const uint64_t c2 = f2(c, c), neg = f2(-1.f, -1.f);
+    uint32_t pp[2][16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float2 l = lds64_f32(cols + 32 * j);
+        const uint64_t l2 = f2(l.x, l.y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t& r0 = s[i >> 1][4 * j + 2 * (i & 1)];
+            uint32_t& r1 = s[i >> 1][4 * j + 2 * (i & 1) + 1];
+            float x0, x1;
+            f2_split(f2_fma(f2(__uint_as_float(r0), __uint_as_float(r1)), c2, f2_fma(l2, neg, bias[i - j + 7])), x0,
+                     x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            pp[i >> 1][2 * j + (i & 1)] = pack_bf16x2(x0, x1);
+            r0 = __float_as_uint(x0);
+            r1 = __float_as_uint(x1);
+        }
+    }
+    tmem_st_16x128b_x8(tS, pp[0]);
+    tmem_st_16x128b_x8(tS + (16u << 16), pp[1]);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
@@ -785,18 +761,42 @@ __device__ __forceinline__ bool pds_tile_bias(uint32_t tS, uint32_t tdP, uint32_
         mbar_arrive(smem_u32(&bars->p_full));
         mbar_arrive(smem_u32(&bars->win_empty[st]));
     }
+    if (rows_live < 32) {   // keys past the sequence (zero rows of K) have no dS
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((lane >> 2) + 8 * i >= rows_live) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[i >> 1][4 * j + 2 * (i & 1)] = s[i >> 1][4 * j + 2 * (i & 1) + 1] = 0u;
+            }
+    }
     if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->dp_full), gi & 1, abort_flag, 32))) return false;
     tc_fence_after();
-    uint64_t all = 0;   // (0.f, 0.f)
-    auto phase2 = [&](int cc, float (&pf)[32]) {
+    uint64_t sum[11];
+#pragma unroll
+    for (int k = 0; k < 11; ++k) sum[k] = 0;   // (0.f, 0.f)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
         uint32_t dp[32], dd[16];
-        tmem_ld32(tdP + cc * 32, dp);
+        tmem_ld_16x256b_x8(tdP + ((uint32_t)(16 * h) << 16), dp);
         tmem_wait_ld();
-        ds_chunk_t<BM>(pf, dp, lse2s + kBT * 4, cc * 32, dd, &all);
-        tmem_st16(tdP + a_chunk_col(cc), dd);
-    };
-    phase2(2 * grp, pf0);
-    phase2(2 * grp + 1, pf1);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 dv = lds64_f32(cols + kBT * 4 + 32 * j);
+            const uint64_t d2 = f2(dv.x, dv.y);
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                const int r = 4 * j + 2 * hi;
+                const uint64_t ds =
+                    f2_mul(f2(__uint_as_float(s[h][r]), __uint_as_float(s[h][r + 1])),
+                           f2_fma(d2, neg, f2(__uint_as_float(dp[r]), __uint_as_float(dp[r + 1]))));
+                float x0, x1;
+                f2_split(ds, x0, x1);
+                dd[2 * j + hi] = pack_bf16x2(x0, x1);
+                sum[2 * h + hi - j + 7] = f2_add(sum[2 * h + hi - j + 7], ds);
+            }
+        }
+        tmem_st_16x128b_x8(tdP + ((uint32_t)(16 * h) << 16), dd);
+    }
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
@@ -804,23 +804,39 @@ __device__ __forceinline__ bool pds_tile_bias(uint32_t tS, uint32_t tdP, uint32_
         mbar_arrive(smem_u32(&bars->ds_full));
         mbar_arrive(smem_u32(&bars->qd_empty[st]));
     }
-    if constexpr (WINDOW) {   // (while the tensor cores are at dK)
-        float da, db, dc;
-        diagonal_sums(pf0, pf1, lane, da, db, dc);
-        const uint32_t set = cnt_diag & 1;
-        if (cnt_diag >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->diag_empty[set]),
+    if (kind == kBiasInside) {
+#pragma unroll
+        for (int k = 0; k < 11; ++k) {
+            float x0, x1;
+            f2_split(sum[k], x0, x1);
+            sts_f32(diag + k * kDiagRow * 4, x0);
+            sts_f32(diag + (k * kDiagRow + kDiagHalf) * 4, x1);
+        }
+        __syncwarp();
+        // a thread (a, b)'s sum k is at d = a - 2 b - e + 8 (k - 7): with c = 2 b + e,
+        // lane s's d = s - 32 q is row k = (s + c) / 8 + 7 - 4 q (of 0..10) at a = (s + c) % 8
+        float t[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            if (lane + x < 32) t[0] += lds_f32(part[x] + 7 * kDiagRow * 4);
+            t[1] += lds_f32(part[x] + 3 * kDiagRow * 4);
+            if (lane + x >= 8) t[2] += lds_f32(part[x] - kDiagRow * 4);
+        }
+        const uint32_t which = cnt_diag & 1;
+        if (cnt_diag >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->diag_empty[which]),
                                                                 ((cnt_diag >> 1) - 1) & 1, abort_flag)))
             return false;
-        sts_f32(diag + set * set_bytes, da);
-        sts_f32(diag + set * set_bytes + 128, db);
-        sts_f32(diag + set * set_bytes + 256, dc);
         ++cnt_diag;
+#pragma unroll
+        for (int q = 0; q < 3; ++q) sts_f32(set + which * set_bytes + 128 * q, t[q]);
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->diag_full[set]));
+        if (lane == 0) mbar_arrive(smem_u32(&bars->diag_full[which]));
     } else {
-        float a, b;
-        f2_split(all, a, b);
-        far += a + b;
+#pragma unroll
+        for (int k = 1; k < 11; ++k) sum[0] = f2_add(sum[0], sum[k]);
+        float x0, x1;
+        f2_split(sum[0], x0, x1);
+        if (kind == kBiasBefore) far_l += x0 + x1; else far_r += x0 + x1;
     }
     return true;
 }
@@ -840,9 +856,12 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
     int g = 0;  // Q tiles done, over the CTA's items
     int u = 0;  // items with work
     uint32_t cnt_diag = 0;   // BIAS: sets of diagonal sums written
-    if constexpr (BIAS) {    // (each warp the same words, for its own reads)
-        for (int x = lane; x < kBT; x += 32) sts_f32(smem_u32(smem + C::kNoKey) + 4 * x, -INFINITY);
-        __syncwarp();
+    uint32_t part[8];        // and where this lane finds their parts (pds_tile_bias)
+    if constexpr (BIAS) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            part[x] = smem_u32(smem + C::kDiag) + ((grp * 4 + wq) * kDiagFloats + (x & 1) * kDiagHalf +
+                                                   ((lane + x) >> 3) * kDiagRow + 4 * ((lane + x) & 7) + (x >> 1)) * 4;
     }
     for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
         const BwdWork w = bwd_item<VARLEN>(p, idx, err);
@@ -866,19 +885,16 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
             if constexpr (BIAS) {
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_full[st]), (gi >> 1) & 1, abort_flag));
                 if (!ok) break;
-                const TileBias tb = bars->bias[st];
-                if (tb.kind == kBiasInWindow) {
-                    // query column x of key row j is distance base + j - x + 127; a key
-                    // past the sequence takes -inf throughout (its row of K is zeros)
-                    uint32_t win = smem_u32(smem + C::kWin) + (st * kBiasWindow + j + kBT - 1) * 4;
-                    if (jg >= w.nk) win = smem_u32(smem + C::kNoKey) + (kBT - 1) * 4;
-                    ok = pds_tile_bias<true>(tS, tdP, lse2s, grp, lane, p.c, win, 0.f, gi, bars, abort_flag,
-                                             smem_u32(smem + C::kDiag) + ((grp * 4 + wq) * 96 + lane) * 4,
-                                             C::kDiagBytes, cnt_diag, far_l);
-                } else {
-                    ok = pds_tile_bias<false>(tS, tdP, lse2s, grp, lane, p.c, 0u, tb.value, gi, bars, abort_flag, 0u,
-                                              0, cnt_diag, tb.kind == kBiasBefore ? far_l : far_r);
-                }
+                const TileBias kind = bars->bias[st];
+                // this thread's first query column in lse2 (and D), and its first key
+                // row's distance there, base + row - column + 127
+                const int row = wq * 32 + (lane >> 2), col = grp * 64 + 2 * (lane & 3);
+                ok = pds_tile_bias(tS + grp * 64, tdP + grp * 64, lse2s + col * 4, lane, p.c,
+                                   smem_u32(smem + C::kWin) + (st * kBiasWindow + row - col + kBT - 1) * 4,
+                                   w.nk - w.k0 - wq * 32, kind, gi, bars, abort_flag,
+                                   smem_u32(smem + C::kDiag) + ((grp * 4 + wq) * kDiagFloats + lane) * 4, part,
+                                   smem_u32(smem + C::kSet) + ((grp * 4 + wq) * 96 + lane) * 4, C::kSetBytes, cnt_diag,
+                                   far_l, far_r);
                 if (!ok) break;
                 if (++qt == w.qt_first + w.n_qt_cta) {   // the head ends
 #pragma unroll
@@ -1424,18 +1440,14 @@ __device__ void dq_mma(uint8_t* smem, DqBars* bars, uint32_t tmem, const BwdPara
 
 // P = 2^(S c - lse2) for 32 key columns [kc, kc + 32) of this thread's query
 // row (fp32).  lim: key column kc + x is allowed iff kc + x <= lim (causal).
-// WINDOW: column k's bias, from shared address win + 4 k, joins -lse2 (one bias for
-// the whole tile is in nl2 already).
-template <bool MASKED, bool WINDOW = false>
+template <bool MASKED>
 __device__ __forceinline__ void p_row_chunk(const uint32_t (&s)[32], uint64_t c2, uint64_t nl2,
-                                            int kc, int lim, float (&pf)[32], uint32_t win = 0) {
+                                            int kc, int lim, float (&pf)[32]) {
 #pragma unroll
     for (int x = 0; x < 16; ++x) {
         const int col = kc + 2 * x;
         float a0, a1;
-        uint64_t add = nl2;
-        if constexpr (WINDOW) add = f2_add(nl2, f2(lds_f32(win + 4 * col), lds_f32(win + 4 * col + 4)));
-        f2_split(f2_fma(f2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), c2, add), a0, a1);
+        f2_split(f2_fma(f2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), c2, nl2), a0, a1);
         float p0 = ex2(a0), p1 = ex2(a1);
         if constexpr (MASKED) {
             p0 = col <= lim ? p0 : 0.f;
@@ -1459,6 +1471,74 @@ __device__ __forceinline__ void ds_row_chunk(const float (&pf)[32], const uint32
     }
 }
 
+// One K/V tile of a dS warp, with a bias: dq_ds's two phases on fragments, as
+// pds_tile_bias has them: thread (a, b) has query rows a + 8 i and key columns 8 j +
+// 2 b + e, whose key - query is one of 22 distances.  keys_live: key columns of the
+// warp's 64 inside the sequence (P = 0 past them: a bias can put their 2^-lse2 past
+// fp32's range, and infinity times their zero rows of K is NaN).
+__device__ __forceinline__ bool dq_tile_bias(uint32_t tS, uint32_t tdP, int lane, float c, const float (&lse2)[4],
+                                             const float (&dval)[4], uint32_t win, int keys_live, int t,
+                                             DqBars* bars, const volatile int* abort_flag) {
+    uint32_t s[2][32];   // S, then P, of rows [0, 16) and [16, 32)
+    tmem_ld_16x256b_x8(tS, s[0]);
+    tmem_ld_16x256b_x8(tS + (16u << 16), s[1]);
+    uint64_t bias[11];   // at key - query = 2 b + e - a + 8 (k - 3), k = j - i + 3
+#pragma unroll
+    for (int k = 0; k < 11; ++k) bias[k] = f2(lds_f32(win + 32 * (k - 3)), lds_f32(win + 32 * (k - 3) + 4));
+    tmem_wait_ld();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->win_empty[t & 1]));
+    const uint64_t c2 = f2(c, c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t nl2 = f2(-lse2[i], -lse2[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint32_t& r0 = s[i >> 1][4 * j + 2 * (i & 1)];
+            uint32_t& r1 = s[i >> 1][4 * j + 2 * (i & 1) + 1];
+            float x0, x1;
+            f2_split(f2_fma(f2(__uint_as_float(r0), __uint_as_float(r1)), c2, f2_add(nl2, bias[j - i + 3])), x0, x1);
+            r0 = __float_as_uint(ex2(x0));
+            r1 = __float_as_uint(ex2(x1));
+        }
+    }
+    if (keys_live < 64) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (8 * j + 2 * (lane & 3) + e >= keys_live) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[i >> 1][4 * j + 2 * (i & 1) + e] = 0u;
+                }
+    }
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->dp_full), t & 1, abort_flag, 32))) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t dp[32], dd[16];
+        tmem_ld_16x256b_x8(tdP + ((uint32_t)(16 * h) << 16), dp);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                const int r = 4 * j + 2 * hi;
+                const float nd = -dval[2 * h + hi];
+                float x0, x1;
+                f2_split(f2_mul(f2(__uint_as_float(s[h][r]), __uint_as_float(s[h][r + 1])),
+                                f2_add(f2(__uint_as_float(dp[r]), __uint_as_float(dp[r + 1])), f2(nd, nd))), x0, x1);
+                dd[2 * j + hi] = pack_bf16x2(x0, x1);
+            }
+        tmem_st_16x128b_x8(tS + ((uint32_t)(16 * h) << 16), dd);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full));
+    return true;
+}
+
 // BIAS: looks up each K/V tile's biases, up to two tiles ahead of the dS warps.
 template <int D, bool VARLEN>
 __device__ void dq_bias_lookup(int lane, uint8_t* smem, DqBars* bars, const BwdParams& p, unsigned n_items,
@@ -1475,8 +1555,7 @@ __device__ void dq_bias_lookup(int lane, uint8_t* smem, DqBars* bars, const BwdP
         for (int j = 0; j < w.n_kv; ++j, ++n) {
             const int st = n & 1;
             const int base = j * kBT - (w.q0 + kBT - 1) - w.off;
-            const bool masked = (j + 1) * kBT > w.nk || (p.causal && base + 254 > 0);
-            ok = give_bias(p.bias, p.Hq, w.hq, base, p.causal ? 0 : INT_MAX, masked, left, right,
+            ok = give_bias(p.bias, p.Hq, w.hq, base, p.causal ? 0 : INT_MAX, left, right,
                            smem_u32(smem + C::kWin) + st * kBiasWindow * 4, &bars->bias[st], &bars->win_full[st],
                            &bars->win_empty[st], n >= 2, ((n >> 1) - 1) & 1, abort_flag, lane, err);
             if (!ok) break;
@@ -1507,35 +1586,37 @@ __device__ void dq_ds(int wq, int grp, int lane, uint8_t* smem, DqBars* bars, ui
         // its rows may lie past the sequence's rows of lse2 / dvec)
         const float lse2 = w.n_kv > 0 ? p.lse2[vrow] : INFINITY;
         const float dval = w.n_kv > 0 ? p.dvec[vrow] : 0.f;
-        uint64_t nl2 = f2(-lse2, -lse2);
-        const uint64_t nd2 = f2(-dval, -dval);
+        const uint64_t nl2 = f2(-lse2, -lse2), nd2 = f2(-dval, -dval);
+        // BIAS: the same of the thread's four query rows (dq_tile_bias)
+        float lse4[4], d4[4];
+        if constexpr (BIAS) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = (lane >> 2) + 8 * i;
+                lse4[i] = __shfl_sync(0xFFFFFFFFu, lse2, r);
+                d4[i] = __shfl_sync(0xFFFFFFFFu, dval, r);
+            }
+        }
         for (int j = 0; j < w.n_kv && ok; ++j) {
             const int t = t0 + j;
             const uint32_t tS = tmem + ((t & 1) ? 384u : 0u) + lane_off;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->s_full[t & 1]), (t >> 1) & 1, abort_flag, 32));
             if (!ok) break;
             tc_fence_after();
-            int lim = row + w.off - j * kBT;  // causal: key column c allowed iff c <= lim
-            bool masked = __any_sync(0xFFFFFFFFu, p.causal && lim < kBT - 1);
-            bool window = false;
-            uint32_t win = 0;
             if constexpr (BIAS) {
-                // keys past the sequence: P = 0 (a bias can put their 2^-lse2 past
-                // fp32's range, and infinity times their zero rows of K is NaN).  The
-                // causal limit is in the window.
-                const int last = w.nk - 1 - j * kBT;
-                lim = last;
-                masked = last < kBT - 1;
                 const int st = t & 1;
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->win_full[st]), (t >> 1) & 1, abort_flag));
                 if (!ok) break;
-                const TileBias tb = bars->bias[st];
-                window = tb.kind == kBiasInWindow;
-                // key column c of query row i is distance base + c - i + 127
-                win = smem_u32(smem + C::kWin) + (st * kBiasWindow + kBT - 1 - (wq * 32 + lane)) * 4;
-                const float add = (window ? 0.f : tb.value) - lse2;
-                nl2 = f2(add, add);
+                // the first query row's and key column's distance there: base + column - row + 127
+                const int qr = wq * 32 + (lane >> 2), col = grp * 64 + 2 * (lane & 3);
+                ok = dq_tile_bias(tS + grp * 64, tdP + grp * 64, lane, p.c, lse4, d4,
+                                  smem_u32(smem + C::kWin) + (st * kBiasWindow + col - qr + kBT - 1) * 4,
+                                  w.nk - j * kBT - grp * 64, t, bars, abort_flag);
+                if (!ok) break;
+                continue;
             }
+            const int lim = row + w.off - j * kBT;  // causal: key column c allowed iff c <= lim
+            const bool masked = __any_sync(0xFFFFFFFFu, p.causal && lim < kBT - 1);
             // Phase 1: P from S for this warpgroup's 64 key columns (needs S_j
             // only; runs while dQ_{j-1} and dP_j compute)
             float pf0[32], pf1[32];
@@ -1543,23 +1624,13 @@ __device__ void dq_ds(int wq, int grp, int lane, uint8_t* smem, DqBars* bars, ui
                 uint32_t sv[32];
                 tmem_ld32(tS + cc * 32, sv);
                 tmem_wait_ld();
-                if constexpr (BIAS) {
-                    if (window) {
-                        if (masked) p_row_chunk<true, true>(sv, c2, nl2, cc * 32, lim, pf, win);
-                        else p_row_chunk<false, true>(sv, c2, nl2, cc * 32, kBT, pf, win);
-                    } else {
-                        p_row_chunk<false>(sv, c2, nl2, cc * 32, kBT, pf);
-                    }
-                } else if (masked)
+                if (masked)
                     p_row_chunk<true>(sv, c2, nl2, cc * 32, p.causal ? lim : kBT, pf);
                 else
                     p_row_chunk<false>(sv, c2, nl2, cc * 32, kBT, pf);
             };
             phase1(2 * grp, pf0);
             phase1(2 * grp + 1, pf1);
-            if constexpr (BIAS) {
-                if (lane == 0) mbar_arrive(smem_u32(&bars->win_empty[t & 1]));
-            }
             // Phase 2: dS from P and dP, as bf16 over the S columns this
             // warpgroup read
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->dp_full), t & 1, abort_flag, 32));
