@@ -134,6 +134,7 @@ struct BwdParams {
     // warps' parts), after it (8), and a ninth part of each
     BiasArgs bias;
     float* partial;
+    unsigned int* queue;   // [2]: items taken off the dK/dV and the dQ pass's lists
 };
 
 // Floats of one (key tile, head)'s sums.
@@ -163,6 +164,12 @@ __device__ __forceinline__ bool bwd_varlen_seq(const BwdParams& p, int b, int& q
 // whether all of them are the one of the map's left or right end.
 enum TileBias : int { kBiasBefore = 0, kBiasAfter = 1, kBiasInside = 2 };
 
+// BIAS: items reach the roles through two slots, filled by the producer.
+struct __align__(8) ItemRing {
+    uint64_t full[2], empty[2];
+    unsigned item[2];
+};
+
 struct __align__(8) BwdBars {
     uint64_t kv_full, kv_empty;  // K and V of an item; read by its last S^T and dP^T
     uint64_t qd_full[2], qd_empty[2];
@@ -170,6 +177,7 @@ struct __align__(8) BwdBars {
     // BIAS: a Q tile's bias is there / has been read; its diagonal sums
     uint64_t win_full[2], win_empty[2], diag_full[2], diag_empty[2];
     TileBias bias[2];
+    ItemRing items;
     uint32_t tmem_base;
     int abort;
 };
@@ -264,6 +272,64 @@ __device__ __forceinline__ BwdWork bwd_item(const BwdParams& p, unsigned idx, un
     else return bwd_work(p, idx);
 }
 
+// With a bias an item's cost depends on the sequence and on where the tiles lie on the
+// map, so a CTA takes its next item when it is ready for one: the first is its own
+// index, the others come off the pass's counter (in the workspace, zeroed by the prep
+// kernel).  (16 packed sequences of 256..4096 rows, 16 heads, whose items cost 1 to 32
+// tiles: 1770 us with every (grid size)-th item, so 1490.)  take_item: the role's k-th
+// item, every (grid size)-th one without a bias; false after the last or on abort.
+template <bool BIAS>
+__device__ __forceinline__ bool take_item(ItemRing& ring, unsigned k, unsigned n_items, unsigned& idx, bool& ok,
+                                          const volatile int* abort_flag) {
+    if constexpr (!BIAS) {
+        idx = k == 0 ? blockIdx.x : idx + gridDim.x;
+        return ok && idx < n_items;
+    } else {
+        if (!ok) return false;
+        const unsigned i = k & 1;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ring.full[i]), (k >> 1) & 1, abort_flag));
+        if (!ok) return false;
+        idx = *const_cast<volatile unsigned*>(&ring.item[i]);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ring.empty[i]));
+        return idx < n_items;
+    }
+}
+
+// The producer's side: takes its k-th item off the list and hands it on.
+template <bool BIAS>
+__device__ __forceinline__ bool fetch_item(ItemRing& ring, unsigned k, unsigned n_items, unsigned& idx, bool& ok,
+                                           unsigned int* counter, bool leader, const volatile int* abort_flag) {
+    if constexpr (!BIAS) {
+        return take_item<false>(ring, k, n_items, idx, ok, abort_flag);
+    } else {
+        if (!ok) return false;
+        const unsigned i = k & 1;
+        if (k >= 2)
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ring.empty[i]), ((k >> 1) - 1) & 1, abort_flag));
+        if (!ok) return false;
+        const int from = __ffs(__ballot_sync(0xFFFFFFFFu, leader)) - 1;
+        idx = blockIdx.x;
+        if (k > 0) {
+            if (leader) idx = gridDim.x + atomicAdd(counter, 1u);
+            idx = __shfl_sync(0xFFFFFFFFu, idx, from);
+        }
+        if (leader) {
+            *const_cast<volatile unsigned*>(&ring.item[i]) = idx;
+            mbar_arrive(smem_u32(&ring.full[i]));
+        }
+        __syncwarp();
+        return idx < n_items;
+    }
+}
+
+__device__ __forceinline__ void init_items(ItemRing& ring, int consumers) {
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&ring.full[i]), 1);
+        mbar_init(smem_u32(&ring.empty[i]), (uint32_t)consumers);
+    }
+}
+
 __device__ __forceinline__ void bwd_abort(BwdBars* bars, unsigned int* err) {
     atomicOr(err, kErrTimeout);
     *((volatile int*)&bars->abort) = 1;
@@ -272,7 +338,7 @@ __device__ __forceinline__ void bwd_abort(BwdBars* bars, unsigned int* err) {
 // ---------------------------------------------------------------------------
 // Producer
 // ---------------------------------------------------------------------------
-template <int D, bool VARLEN>
+template <int D, bool VARLEN, bool BIAS>
 __device__ void bwd_producer(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
                              const CUtensorMap* tdo, uint8_t* smem, BwdBars* bars,
                              const BwdParams& p, unsigned n_items, unsigned int* err) {
@@ -282,7 +348,8 @@ __device__ void bwd_producer(const CUtensorMap* tq, const CUtensorMap* tk, const
     bool ok = true;
     int issued = 0;   // Q / dO tiles issued, over the CTA's items
     int kv_uses = 0;  // K / V loads issued (items with work)
-    for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
+    unsigned idx = 0;
+    for (unsigned item = 0; fetch_item<BIAS>(bars->items, item, n_items, idx, ok, p.queue, leader, abort_flag); ++item) {
         const BwdWork w = bwd_item<VARLEN>(p, idx, err);
         if (w.n_tiles == 0) continue;
         // K and V of the item, once the previous item's last S^T and dP^T have
@@ -390,7 +457,7 @@ __device__ __forceinline__ void issue_tmem_a(uint32_t d_tmem, uint32_t a_tmem, u
                     sdesc_join(b_lo + kk * (2048 >> 4), kBwdDescHi), idesc, (accumulate || kk > 0) ? 1u : 0u);
 }
 
-template <int D, bool VARLEN>
+template <int D, bool VARLEN, bool BIAS>
 __device__ void bwd_mma(uint8_t* smem, BwdBars* bars, uint32_t tmem, const BwdParams& p,
                         unsigned n_items, unsigned int* err) {
     using C = BwdCfg<D>;
@@ -411,7 +478,8 @@ __device__ void bwd_mma(uint8_t* smem, BwdBars* bars, uint32_t tmem, const BwdPa
     bool ok = true;
     int g = 0;  // Q / dO tiles consumed, over the CTA's items
     int u = 0;  // items with work
-    for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
+    unsigned idx = 0;
+    for (unsigned item = 0; take_item<BIAS>(bars->items, item, n_items, idx, ok, abort_flag); ++item) {
         const BwdWork w = bwd_item<VARLEN>(p, idx, err);
         const int n = w.n_tiles;
         if (n == 0) continue;
@@ -611,7 +679,8 @@ __device__ void bwd_bias_lookup(int lane, uint8_t* smem, BwdBars* bars, const Bw
     const volatile int* abort_flag = &bars->abort;
     bool ok = true;
     int n = 0;   // Q tiles done
-    for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
+    unsigned idx = 0;
+    for (unsigned item = 0; take_item<true>(bars->items, item, n_items, idx, ok, abort_flag); ++item) {
         const BwdWork w = bwd_item<VARLEN>(p, idx, err);
         for (int h = 0; h < p.group && w.n_tiles > 0 && ok; ++h) {
             const int hq = w.g * p.group + h;
@@ -646,7 +715,8 @@ __device__ void bwd_bias_sums(int lane, uint8_t* smem, BwdBars* bars, const BwdP
     const int first = p.bias.first, span = p.bias.span;
     bool ok = true;
     uint32_t n = 0;   // tiles' sums read
-    for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
+    unsigned idx = 0;
+    for (unsigned item = 0; take_item<true>(bars->items, item, n_items, idx, ok, abort_flag); ++item) {
         const BwdWork w = bwd_item<VARLEN>(p, idx, err);
         const int base0 = w.k0 - (w.qt_first * kBT + w.off) - (kBT - 1);
         for (int h = 0; h < p.group && ok; ++h) {
@@ -863,7 +933,8 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
             part[x] = smem_u32(smem + C::kDiag) + ((grp * 4 + wq) * kDiagFloats + (x & 1) * kDiagHalf +
                                                    ((lane + x) >> 3) * kDiagRow + 4 * ((lane + x) & 7) + (x >> 1)) * 4;
     }
-    for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
+    unsigned idx = 0;
+    for (unsigned item = 0; take_item<BIAS>(bars->items, item, n_items, idx, ok, abort_flag); ++item) {
         const BwdWork w = bwd_item<VARLEN>(p, idx, err);
         const int jg = w.k0 + j;
         // BIAS: the Q tile, its head, and this thread's sums of the head's tiles on
@@ -1093,6 +1164,7 @@ attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         mbar_init(smem_u32(&bars->p_full), 8);
         mbar_init(smem_u32(&bars->ds_full), 8);
         mbar_init(smem_u32(&bars->acc_full), 1);
+        init_items(bars->items, 11);   // every role but the producer
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&bars->win_full[s]), 1);
             mbar_init(smem_u32(&bars->win_empty[s]), 8);
@@ -1120,8 +1192,8 @@ attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         // (roles in the branches of the register split, which the compiler then keeps to)
         if (warp < 4) {
             reg_dealloc<kBwdRegsControl>();
-            if (warp == 0) bwd_producer<D, VARLEN>(&tq, &tk, &tv, &tdo, smem, bars, p, n_items, err);
-            else if (warp == 1) bwd_mma<D, VARLEN>(smem, bars, tmem, p, n_items, err);
+            if (warp == 0) bwd_producer<D, VARLEN, BIAS>(&tq, &tk, &tv, &tdo, smem, bars, p, n_items, err);
+            else if (warp == 1) bwd_mma<D, VARLEN, BIAS>(smem, bars, tmem, p, n_items, err);
             else if (warp == 2) bwd_bias_lookup<D, VARLEN>(lane, smem, bars, p, n_items, err);
             else bwd_bias_sums<D, VARLEN>(lane, smem, bars, p, n_items, err);
         } else {
@@ -1129,8 +1201,8 @@ attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
             bwd_pds<D, OUT_F32, VARLEN, BIAS>(warp & 3, (warp - 4) >> 2, lane, smem, bars, tmem, &tdk, &tdv, p, n_items,
                                               err);
         }
-    } else if (warp == 0) bwd_producer<D, VARLEN>(&tq, &tk, &tv, &tdo, smem, bars, p, n_items, err);
-    else if (warp == 1) bwd_mma<D, VARLEN>(smem, bars, tmem, p, n_items, err);
+    } else if (warp == 0) bwd_producer<D, VARLEN, BIAS>(&tq, &tk, &tv, &tdo, smem, bars, p, n_items, err);
+    else if (warp == 1) bwd_mma<D, VARLEN, BIAS>(smem, bars, tmem, p, n_items, err);
     else if (warp >= 4)
         bwd_pds<D, OUT_F32, VARLEN, BIAS>(warp & 3, (warp - 4) >> 2, lane, smem, bars, tmem, &tdk, &tdv, p, n_items, err);
 
@@ -1167,6 +1239,7 @@ struct __align__(8) DqBars {
     uint64_t s_full[2], dp_full, ds_full, dq_full, drain;  // s_full[b]: the S in buffer b
     uint64_t win_full[2], win_empty[2];  // BIAS, as in BwdBars
     TileBias bias[2];
+    ItemRing items;
     uint32_t tmem_base;
     int abort;
 };
@@ -1272,7 +1345,8 @@ __device__ void dq_producer(const CUtensorMap* tq, const CUtensorMap* tk, const 
     bool ok = true;
     int q_uses = 0;      // Q / dO loads issued (items with work)
     int nk = 0, nv = 0;  // K and V loads issued, over the CTA's items
-    for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
+    unsigned idx = 0;
+    for (unsigned item = 0; fetch_item<BIAS>(bars->items, item, n_items, idx, ok, p.queue + 1, leader, abort_flag); ++item) {
         const DqWork w = dq_item<VARLEN>(p, idx, err);
         if (w.n_kv == 0) continue;
         // Q and dO of the item, once the previous item's last S and dP have
@@ -1406,7 +1480,8 @@ __device__ void dq_mma(uint8_t* smem, DqBars* bars, uint32_t tmem, const BwdPara
     bool ok = true;
     int t0 = 0;  // K/V tiles before this item
     int u = 0;   // items with work
-    for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
+    unsigned idx = 0;
+    for (unsigned item = 0; take_item<BIAS>(bars->items, item, n_items, idx, ok, abort_flag); ++item) {
         const DqWork w = dq_item<VARLEN>(p, idx, err);
         const int n = w.n_kv;
         if (n == 0) continue;
@@ -1547,7 +1622,8 @@ __device__ void dq_bias_lookup(int lane, uint8_t* smem, DqBars* bars, const BwdP
     const volatile int* abort_flag = &bars->abort;
     bool ok = true;
     int n = 0;   // K/V tiles done
-    for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
+    unsigned idx = 0;
+    for (unsigned item = 0; take_item<true>(bars->items, item, n_items, idx, ok, abort_flag); ++item) {
         const DqWork w = dq_item<VARLEN>(p, idx, err);
         if (w.n_kv == 0) continue;
         const float left = bias_at(p.bias, p.Hq, w.hq, p.bias.first, err);
@@ -1576,7 +1652,8 @@ __device__ void dq_ds(int wq, int grp, int lane, uint8_t* smem, DqBars* bars, ui
     bool ok = true;
     int t0 = 0;  // K/V tiles before this item, over the CTA's items
     int u = 0;   // items with work
-    for (unsigned idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
+    unsigned idx = 0;
+    for (unsigned item = 0; take_item<BIAS>(bars->items, item, n_items, idx, ok, abort_flag); ++item) {
         const DqWork w = dq_item<VARLEN>(p, idx, err);
         const int row = w.q0 + wq * 32 + lane;
         const size_t bh = (size_t)w.b * p.Hq + w.hq;
@@ -1726,6 +1803,7 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         mbar_init(smem_u32(&bars->dp_full), 1);
         mbar_init(smem_u32(&bars->ds_full), 8);
         mbar_init(smem_u32(&bars->dq_full), 1);
+        init_items(bars->items, 10);
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&bars->win_full[s]), 1);
             mbar_init(smem_u32(&bars->win_empty[s]), 8);
@@ -1777,7 +1855,8 @@ template <int LPR>
 __global__ void __launch_bounds__(256)
 attn_bwd_prep_kernel(const void* __restrict__ o, int o_f32, const __nv_bfloat16* __restrict__ dout,
                      const float* __restrict__ lse, float* __restrict__ lse2, float* __restrict__ dvec,
-                     long long rows_pad, int Nq, int Nq_pad, int dh) {
+                     long long rows_pad, int Nq, int Nq_pad, int dh, unsigned int* __restrict__ queue) {
+    if (queue && blockIdx.x == 0 && threadIdx.x < 2) queue[threadIdx.x] = 0u;
     constexpr int kRowsPerWarp = 32 / LPR;
     const int lane = threadIdx.x & 31;
     const int sub = lane % LPR;
@@ -1831,7 +1910,8 @@ __global__ void __launch_bounds__(256)
 attn_bwd_prep_varlen_kernel(const void* __restrict__ o, int o_f32, const __nv_bfloat16* __restrict__ dout,
                             const float* __restrict__ lse, float* __restrict__ lse2,
                             float* __restrict__ dvec, const int* __restrict__ cu_q, int Hq,
-                            int total_q, int vstride, int chunks, int dh) {
+                            int total_q, int vstride, int chunks, int dh, unsigned int* __restrict__ queue) {
+    if (queue && blockIdx.x == 0 && threadIdx.x < 2) queue[threadIdx.x] = 0u;
     constexpr int kRowsPerWarp = 32 / LPR;
     constexpr int kRowsPerBlock = 8 * kRowsPerWarp;
     const int lane = threadIdx.x & 31;
@@ -1896,7 +1976,7 @@ attn_status_t launch_bwd_prep_varlen(const void* o, int o_f32, const void* dout,
 #define GB300_PREP_VARLEN(L)                                                                       \
     attn_bwd_prep_varlen_kernel<L><<<(unsigned)grid, 256, 0, stream>>>(o, o_f32, g, lse, lse2, dvec, \
                                                                        p.cu_q, p.Hq, p.total_q,      \
-                                                                       p.vstride, chunks, dh)
+                                                                       p.vstride, chunks, dh, p.queue)
     if (lpr == 8) GB300_PREP_VARLEN(8);
     else if (lpr == 16) GB300_PREP_VARLEN(16);
     else GB300_PREP_VARLEN(32);
@@ -1907,17 +1987,17 @@ attn_status_t launch_bwd_prep_varlen(const void* o, int o_f32, const void* dout,
 // The prep launch for head dim dh (<= 256): 8, 16 or 32 lanes per row.
 attn_status_t launch_bwd_prep(const void* o, int o_f32, const void* dout, const float* lse,
                               float* lse2, float* dvec, long long rows_pad, int Nq, int Nq_pad,
-                              int dh, cudaStream_t stream) {
+                              int dh, cudaStream_t stream, unsigned int* queue) {
     const auto* g = static_cast<const __nv_bfloat16*>(dout);
     const int lpr = dh <= 64 ? 8 : dh <= 128 ? 16 : 32;
     const long long rows_per_block = 8ll * (32 / lpr);
     const unsigned grid = (unsigned)((rows_pad + rows_per_block - 1) / rows_per_block);
     if (lpr == 8)
-        attn_bwd_prep_kernel<8><<<grid, 256, 0, stream>>>(o, o_f32, g, lse, lse2, dvec, rows_pad, Nq, Nq_pad, dh);
+        attn_bwd_prep_kernel<8><<<grid, 256, 0, stream>>>(o, o_f32, g, lse, lse2, dvec, rows_pad, Nq, Nq_pad, dh, queue);
     else if (lpr == 16)
-        attn_bwd_prep_kernel<16><<<grid, 256, 0, stream>>>(o, o_f32, g, lse, lse2, dvec, rows_pad, Nq, Nq_pad, dh);
+        attn_bwd_prep_kernel<16><<<grid, 256, 0, stream>>>(o, o_f32, g, lse, lse2, dvec, rows_pad, Nq, Nq_pad, dh, queue);
     else
-        attn_bwd_prep_kernel<32><<<grid, 256, 0, stream>>>(o, o_f32, g, lse, lse2, dvec, rows_pad, Nq, Nq_pad, dh);
+        attn_bwd_prep_kernel<32><<<grid, 256, 0, stream>>>(o, o_f32, g, lse, lse2, dvec, rows_pad, Nq, Nq_pad, dh, queue);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -1973,9 +2053,10 @@ inline int bias_sum_parts(long long tiles) {
     return (int)(z < 32 ? z : 32);
 }
 
-// fp32 of workspace for the table's gradient: the dK/dV pass's sums and step 1's.
+// fp32 of workspace that a bias takes: the passes' item counters (16 bytes), the dK/dV
+// pass's sums and step 1's.
 inline size_t bias_workspace_floats(long long tiles, int Hq, int span) {
-    return (size_t)(tiles + bias_sum_parts(tiles)) * Hq * bias_partial_floats(span);
+    return 4 + (size_t)(tiles + bias_sum_parts(tiles)) * Hq * bias_partial_floats(span);
 }
 
 attn_status_t launch_bias_grad(const BwdParams& p, float* dtable, cudaStream_t stream) {
@@ -2012,7 +2093,7 @@ attn_status_t launch_bwd_t(const CUtensorMap& tq, const CUtensorMap& tk, const C
         st = launch_bwd_prep_varlen(o, o_f32, dout, lse, lse2, dvec, p, stream);
     } else {
         const long long rows_pad = (long long)p.B * p.Hq * p.Nq_pad;
-        st = launch_bwd_prep(o, o_f32, dout, lse, lse2, dvec, rows_pad, p.Nq, p.Nq_pad, p.d_act, stream);
+        st = launch_bwd_prep(o, o_f32, dout, lse, lse2, dvec, rows_pad, p.Nq, p.Nq_pad, p.d_act, stream, p.queue);
     }
     if (st != ATTN_OK) return st;
     // (packed batches: units at the longest lengths; the tiles past a
@@ -2877,7 +2958,7 @@ attn_status_t launch_bwd_wide_t(const CUtensorMap& tq, const CUtensorMap& tk, co
         st = launch_bwd_prep_varlen(o, o_f32, dout, lse, lse2, dvec, p, stream);
     } else {
         const long long rows_pad = (long long)p.B * p.Hq * p.Nq_pad;
-        st = launch_bwd_prep(o, o_f32, dout, lse, lse2, dvec, rows_pad, p.Nq, p.Nq_pad, p.d_act, stream);
+        st = launch_bwd_prep(o, o_f32, dout, lse, lse2, dvec, rows_pad, p.Nq, p.Nq_pad, p.d_act, stream, p.queue);
     }
     if (st != ATTN_OK) return st;
     const long long kv_ctas = 2ll * p.B * p.Hkv * p.n_kt;  // two column halves per key tile
@@ -2936,7 +3017,8 @@ attn_status_t launch_bwd_varlen(const void* q, const void* k, const void* v, con
     p.dk = dk;
     p.dv = dv;
     p.bias = bias ? *bias : BiasArgs{};
-    p.partial = dvec + (size_t)Hq * p.vstride;
+    p.queue = bias ? reinterpret_cast<unsigned int*>(dvec + (size_t)Hq * p.vstride) : nullptr;
+    p.partial = dvec + (size_t)Hq * p.vstride + 4;
     if ((long long)B * Hkv * p.n_kt >= (1ll << 31) || (long long)B * Hq * (p.Nq_pad / kBT) >= (1ll << 31) ||
         (long long)Hq * p.vstride >= (1ll << 31))
         return ATTN_ERR_UNSUPPORTED;
@@ -3026,7 +3108,8 @@ attn_status_t launch_bwd(const void* q, const void* k, const void* v, const void
     p.cu_q = p.cu_k = nullptr;
     p.total_q = p.total_k = p.vstride = 0;
     p.bias = bias ? *bias : BiasArgs{};
-    p.partial = dvec + rows;
+    p.queue = bias ? reinterpret_cast<unsigned int*>(dvec + rows) : nullptr;
+    p.partial = dvec + rows + 4;
     if ((long long)B * Hkv * p.n_kt >= (1ll << 31) ||
         (long long)B * Hq * (p.Nq_pad / kBT) >= (1ll << 31))
         return ATTN_ERR_UNSUPPORTED;

@@ -83,11 +83,11 @@ def test_backward_refusals(lib, packed, kw, code):
 
 def test_backward_workspace(lib):
     base = ea.attn_bwd_workspace_size(2, 4, 2, 100, 300, 64)
-    assert ea.attn_bwd_bias_workspace_size(2, 4, 2, 100, 300, 64, 114) == base + 4 * 4 * 132 * (6 + 1)
+    assert ea.attn_bwd_bias_workspace_size(2, 4, 2, 100, 300, 64, 114) == base + 16 + 4 * 4 * 132 * (6 + 1)
     assert ea.attn_bwd_bias_workspace_size(200, 1, 1, 100, 300, 64, 1) == \
-        ea.attn_bwd_workspace_size(200, 1, 1, 100, 300, 64) + 4 * 19 * (600 + 5)
+        ea.attn_bwd_workspace_size(200, 1, 1, 100, 300, 64) + 16 + 4 * 19 * (600 + 5)
     assert ea.attn_bwd_varlen_bias_workspace_size(2, 4, 2, 100, 300, 64, 114) == \
-        ea.attn_bwd_varlen_workspace_size(2, 4, 2, 100, 64) + 4 * 4 * 132 * (6 + 1)
+        ea.attn_bwd_varlen_workspace_size(2, 4, 2, 100, 64) + 16 + 4 * 4 * 132 * (6 + 1)
     for bad in (dict(d=136), dict(span=0), dict(span=65537), dict(Hq=3)):
         a = dict(Hq=4, d=64, span=114)
         a.update(bad)
