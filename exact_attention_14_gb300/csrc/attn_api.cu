@@ -751,6 +751,7 @@ attn_status_t attn_bwd_bias(const void* q, const void* k, const void* v, const v
     if (st != ATTN_OK) return st;
     if ((st = check_grads(dout, lse, dq, dk, dv, grad_dtype)) != ATTN_OK) return st;
     if (!dtable || !aligned4(dtable)) return ATTN_ERR_INVALID_ARG;
+    if (Hq > 65535) return ATTN_ERR_UNSUPPORTED;   // (a grid's second dimension)
     if ((st = check_bias(table, table_dtype, buckets, first, span, num_buckets, d)) != ATTN_OK) return st;
     const size_t need = bwd_workspace_bytes(B, Hq, Nq, d) + bwd_bias_workspace_bytes(B, Hq, Nk, span);
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
@@ -785,6 +786,7 @@ attn_status_t attn_bwd_varlen_bias(const void* q, const void* k, const void* v, 
     if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
     if ((st = check_grads(dout, lse, dq, dk, dv, grad_dtype)) != ATTN_OK) return st;
     if (!dtable || !aligned4(dtable)) return ATTN_ERR_INVALID_ARG;
+    if (Hq > 65535) return ATTN_ERR_UNSUPPORTED;   // (a grid's second dimension)
     if ((st = check_bias(table, table_dtype, buckets, first, span, num_buckets, d)) != ATTN_OK) return st;
     const size_t need = bwd_varlen_workspace_bytes(B, Hq, total_q) +
                         bwd_bias_workspace_bytes(B, Hq, max_seqlen_k, span);

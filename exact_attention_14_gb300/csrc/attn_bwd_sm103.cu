@@ -129,7 +129,7 @@ struct BwdParams {
     const int* cu_q;
     const int* cu_k;
     int total_q, total_k, vstride;
-    // the BIAS instantiations; partial: [B, n_kt, Hq, span + 18] fp32, a key tile's
+    // the BIAS instantiations; partial: [B, n_kt, Hq, bias_partial_floats] fp32, a key tile's
     // sums of dS over each distance of the map, then over the distances before it (8
     // warps' parts), after it (8), and a ninth part of each
     BiasArgs bias;
@@ -137,8 +137,9 @@ struct BwdParams {
     unsigned int* queue;   // [2]: items taken off the dK/dV and the dQ pass's lists
 };
 
-// Floats of one (key tile, head)'s sums.
-__host__ __device__ inline int bias_partial_floats(int span) { return span + 18; }
+// Floats of one (key tile, head)'s sums: the map's and 18 more, in 16-byte pieces (the
+// last ones up to that are never used).
+__host__ __device__ inline int bias_partial_floats(int span) { return (span + 18 + 3) & ~3; }
 
 // Row of sequence b's first query in a head's rows of lse2 / dvec for packed
 // batches: the packed row rounded up to 4 floats (16-byte bulk copies), plus
@@ -2001,55 +2002,134 @@ attn_status_t launch_bwd_prep(const void* o, int o_f32, const void* dout, const 
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// The bias table's gradient from the dK/dV pass's sums, in two steps of a fixed
-// order.  1: sums over the B n_kt key tiles, every distance of a head; block z takes
-// tiles z, z + gridDim.z, ... (8 groups of them side by side).
+// The bias table's gradient from the dK/dV pass's sums, everything in a fixed order.
+// Adds up 4 consecutive distances of head h over key tiles t0, t0 + step, ...
+__device__ __forceinline__ float4 sum_tiles(const float4* __restrict__ partial, int t0, int step, int tiles,
+                                            int Hq, int h, int pieces, int x) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int t = t0; t < tiles; t += step) {
+        const float4 v = __ldg(partial + ((size_t)t * Hq + h) * pieces + x);
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+    }
+    return a;
+}
+
+// Place of a distance's sum (of a (key tile, head)'s floats) on the map: those
+// beyond it go with its ends, the padding nowhere.
+__device__ __forceinline__ int bias_place(int x, int span) {
+    return x < span ? x : x < span + 8 || x == span + 16 ? 0 : x < span + 18 ? span - 1 : -1;
+}
+
+// Few tiles and a short map: one block a head adds the tiles up (16 groups of them
+// side by side) and hands out the sums to the buckets, a warp a bucket.
+constexpr int kBiasSmallFloats = 4096;   // of a head's sums in shared memory
+__global__ void __launch_bounds__(1024)
+attn_bwd_bias_small_kernel(const float* __restrict__ partial, const int* __restrict__ buckets,
+                           float* __restrict__ dtable, int tiles, int Hq, int span, int num_buckets) {
+    __shared__ float4 part[16][64];
+    __shared__ float sums[kBiasSmallFloats];
+    __shared__ int ids[kBiasSmallFloats];
+    const int h = blockIdx.x, pieces = bias_partial_floats(span) / 4;
+    const int col = threadIdx.x & 63, grp = threadIdx.x >> 6;
+    for (int x = threadIdx.x; x < 4 * pieces; x += 1024) {
+        const int at = bias_place(x, span);
+        ids[x] = at < 0 ? -1 : __ldg(buckets + at);
+    }
+    for (int x0 = 0; x0 < pieces; x0 += 64) {
+        if (x0 + col < pieces)
+            part[grp][col] = sum_tiles(reinterpret_cast<const float4*>(partial), grp, 16, tiles, Hq, h, pieces, x0 + col);
+        __syncthreads();
+        if (grp == 0 && x0 + col < pieces) {
+            float4 a = part[0][col];
+#pragma unroll
+            for (int g = 1; g < 16; ++g) {
+                const float4 v = part[g][col];
+                a.x += v.x;
+                a.y += v.y;
+                a.z += v.z;
+                a.w += v.w;
+            }
+            *reinterpret_cast<float4*>(&sums[4 * (x0 + col)]) = a;
+        }
+        __syncthreads();
+    }
+    const int lane = threadIdx.x & 31;
+    for (int bk = threadIdx.x >> 5; bk < num_buckets; bk += 32) {
+        float a = 0.f;
+        for (int x = lane; x < 4 * pieces; x += 32)
+            if (ids[x] == bk) a += sums[x];
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, s);
+        if (lane == 0) dtable[(size_t)bk * Hq + h] = a;
+    }
+}
+
+// Otherwise in two steps.  1: sums over the key tiles, block z tiles z, z + gridDim.z,
+// ... in 8 groups side by side.
 __global__ void __launch_bounds__(256)
 attn_bwd_bias_sum_kernel(const float* __restrict__ partial, float* __restrict__ sums, int tiles, int Hq,
                          int floats) {
-    __shared__ float part[8][32];
-    const int x = blockIdx.x * 32 + (threadIdx.x & 31), grp = threadIdx.x >> 5, h = blockIdx.y;
-    float a = 0.f;
-    if (x < floats) {
-        const size_t step = (size_t)8 * gridDim.z;
-#pragma unroll 8
-        for (size_t t = blockIdx.z + (size_t)grp * gridDim.z; t < (size_t)tiles; t += step)
-            a += __ldg(partial + (t * Hq + h) * floats + x);
-    }
-    part[grp][threadIdx.x & 31] = a;
+    __shared__ float4 part[8][32];
+    const int pieces = floats / 4, col = threadIdx.x & 31, grp = threadIdx.x >> 5, h = blockIdx.y;
+    const int x = blockIdx.x * 32 + col;
+    if (x < pieces)
+        part[grp][col] = sum_tiles(reinterpret_cast<const float4*>(partial), blockIdx.z + grp * gridDim.z, 8 * gridDim.z,
+                                   tiles, Hq, h, pieces, x);
     __syncthreads();
-    if (grp == 0 && x < floats) {
-        float v = 0.f;
+    if (grp == 0 && x < pieces) {
+        float4 a = part[0][col];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v += part[i][threadIdx.x];
-        sums[((size_t)blockIdx.z * Hq + h) * floats + x] = v;
+        for (int g = 1; g < 8; ++g) {
+            const float4 v = part[g][col];
+            a.x += v.x;
+            a.y += v.y;
+            a.z += v.z;
+            a.w += v.w;
+        }
+        reinterpret_cast<float4*>(sums)[((size_t)blockIdx.z * Hq + h) * pieces + x] = a;
     }
 }
 
-// 2: a warp per (head, bucket) adds up the distances that the map gives the bucket;
-// those beyond the map go with its ends.
+// 2: a warp per (head, bucket) goes through the map, 1024 distances at a time in shared
+// memory, and adds up those of the bucket.
 __global__ void __launch_bounds__(256)
 attn_bwd_bias_table_kernel(const float* __restrict__ sums, const int* __restrict__ buckets,
                            float* __restrict__ dtable, int parts, int Hq, int span, int num_buckets) {
+    __shared__ float val[1024];
+    __shared__ int ids[1024];
     const int h = blockIdx.y, lane = threadIdx.x & 31;
     const int bk = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (bk >= num_buckets) return;
     const int floats = bias_partial_floats(span);
     float a = 0.f;
-#pragma unroll 4
-    for (int x = lane; x < floats; x += 32) {
-        const int at = x < span ? x : x < span + 8 || x == span + 16 ? 0 : span - 1;
-        if (__ldg(buckets + at) == bk)
-            for (int z = 0; z < parts; ++z) a += __ldg(sums + ((size_t)z * Hq + h) * floats + x);
+    for (int x0 = 0; x0 < floats; x0 += 1024) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int x = x0 + 256 * i + threadIdx.x;
+            const int at = x < floats ? bias_place(x, span) : -1;
+            ids[256 * i + threadIdx.x] = at < 0 ? -1 : __ldg(buckets + at);
+            float v = 0.f;
+            if (at >= 0)
+                for (int z = 0; z < parts; ++z) v += __ldg(sums + ((size_t)z * Hq + h) * floats + x);
+            val[256 * i + threadIdx.x] = v;
+        }
+        __syncthreads();
+#pragma unroll 8
+        for (int x = lane; x < 1024; x += 32)
+            if (ids[x] == bk) a += val[x];
     }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, s);
-    if (lane == 0) dtable[(size_t)bk * Hq + h] = a;
+    if (lane == 0 && bk < num_buckets) dtable[(size_t)bk * Hq + h] = a;
 }
 
-// Blocks that share a distance's key tiles in step 1: 128 tiles each, at most 32.
+// Blocks that share a distance's key tiles in step 1: 512 tiles each, at most 32.
 inline int bias_sum_parts(long long tiles) {
-    const long long z = (tiles + 127) / 128;
+    const long long z = (tiles + 511) / 512;
     return (int)(z < 32 ? z : 32);
 }
 
@@ -2062,8 +2142,15 @@ inline size_t bias_workspace_floats(long long tiles, int Hq, int span) {
 attn_status_t launch_bias_grad(const BwdParams& p, float* dtable, cudaStream_t stream) {
     const int floats = bias_partial_floats(p.bias.span);
     const int tiles = p.B * p.n_kt, parts = bias_sum_parts(tiles);
+    // one launch while a head's sums are at most 128 KB (4 x 2048 positions, 245 floats a
+    // tile: 6.1 us against 12.3 in two; packed 16 x 4096, 3.9 MB a head: two)
+    if (floats <= kBiasSmallFloats && (long long)tiles * floats <= 32768) {
+        attn_bwd_bias_small_kernel<<<(unsigned)p.Hq, 1024, 0, stream>>>(p.partial, p.bias.buckets, dtable, tiles, p.Hq,
+                                                                        p.bias.span, p.bias.num_buckets);
+        return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    }
     float* sums = p.partial + (size_t)tiles * p.Hq * floats;
-    attn_bwd_bias_sum_kernel<<<dim3((unsigned)((floats + 31) / 32), (unsigned)p.Hq, (unsigned)parts), 256, 0,
+    attn_bwd_bias_sum_kernel<<<dim3((unsigned)((floats + 127) / 128), (unsigned)p.Hq, (unsigned)parts), 256, 0,
                                stream>>>(p.partial, sums, tiles, p.Hq, floats);
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
     attn_bwd_bias_table_kernel<<<dim3((unsigned)((p.bias.num_buckets + 7) / 8), (unsigned)p.Hq), 256, 0, stream>>>(

@@ -654,8 +654,8 @@ attn_status_t attn_fwd_varlen_bias(const void* q, const void* k, const void* v, 
 
 /*
  * attn_bwd_bias_workspace_size -- bytes of device workspace attn_bwd_bias needs:
- * attn_bwd's, 16, and 4 Hq (span + 18) for each 128-key tile of the batch and
- * each 128 of those (at most 32): sums of dS over the distances.  Returns 0 for
+ * attn_bwd's, 16, and 4 Hq (span + 18, in whole fours) for each 128-key tile of
+ * the batch and each 512 of those (at most 32): sums of dS over the distances.  Returns 0 for
  * arguments attn_bwd_bias would reject.
  */
 size_t attn_bwd_bias_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int d, int span);
@@ -668,7 +668,7 @@ size_t attn_bwd_bias_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int 
  *
  * fp32 [num_buckets, Hq], written whole (0 for a bucket no distance has), from
  * the unrounded dS = P o (dP - D).  All gradients are bit-identical from run to
- * run.
+ * run.  Hq <= 65535.
  */
 attn_status_t attn_bwd_bias(const void* q, const void* k, const void* v, const void* o, const void* dout,
                             const float* lse, const void* table, attn_out_dtype_t table_dtype,

@@ -75,7 +75,7 @@ def bwd(lib, packed, **kw):
 @pytest.mark.parametrize("packed", [False, True])
 @pytest.mark.parametrize("kw,code", BAD_BIAS + [
     (dict(q=None), 1), (dict(do=None), 1), (dict(lse=None), 1), (dict(dq=FAKE + 8), 1), (dict(dk=None), 1),
-    (dict(dt=None), 1), (dict(dt=FAKE + 2), 1), (dict(gt=3), 1), (dict(Hq=5), 1), (dict(n=65), 1),
+    (dict(dt=None), 1), (dict(dt=FAKE + 2), 1), (dict(gt=3), 1), (dict(Hq=65536), 2), (dict(Hq=5), 1), (dict(n=65), 1),
     (dict(ws=None), 5), (dict(wsb=64), 5), (dict(ws=FAKE + 8), 5)])
 def test_backward_refusals(lib, packed, kw, code):
     assert bwd(lib, packed, **kw) == code
@@ -85,7 +85,7 @@ def test_backward_workspace(lib):
     base = ea.attn_bwd_workspace_size(2, 4, 2, 100, 300, 64)
     assert ea.attn_bwd_bias_workspace_size(2, 4, 2, 100, 300, 64, 114) == base + 16 + 4 * 4 * 132 * (6 + 1)
     assert ea.attn_bwd_bias_workspace_size(200, 1, 1, 100, 300, 64, 1) == \
-        ea.attn_bwd_workspace_size(200, 1, 1, 100, 300, 64) + 16 + 4 * 19 * (600 + 5)
+        ea.attn_bwd_workspace_size(200, 1, 1, 100, 300, 64) + 16 + 4 * 20 * (600 + 2)
     assert ea.attn_bwd_varlen_bias_workspace_size(2, 4, 2, 100, 300, 64, 114) == \
         ea.attn_bwd_varlen_workspace_size(2, 4, 2, 100, 64) + 16 + 4 * 4 * 132 * (6 + 1)
     for bad in (dict(d=136), dict(span=0), dict(span=65537), dict(Hq=3)):
