@@ -1291,6 +1291,8 @@ def _bias(table, buckets, first, Hq):
         raise ValueError("table must be [num_buckets, Hq]")
     if buckets.ndim != 1:
         raise ValueError("buckets must be [span]")
+    if not -(1 << 24) <= first <= 1 << 24:
+        raise ValueError("first must be a distance of at most 2^24")
     return (table.data_ptr(), ATTN_OUT_F32 if table.dtype == torch.float32 else ATTN_OUT_BF16,
             buckets.data_ptr(), int(first), buckets.shape[0], table.shape[0])
 
@@ -1614,13 +1616,15 @@ def page_pool(num_blocks: int, *, device="cuda", stream=None):
     return attn_page_pool_init(pool, stream=stream)
 
 
-def _page_tables(pool, block_table, seqlens, lens, name):
+def _page_tables(pool, block_table, seqlens, lens, page_size, name):
     for t, n in ((pool, "pool"), (block_table, "block_table"), (seqlens, "seqlens"), (lens, name)):
         _need(t, torch.int32, n)
     if pool.ndim != 1 or pool.shape[0] <= POOL_HEADER:
         raise ValueError("pool must be [4 + num_blocks]")
     if block_table.ndim != 2 or seqlens.shape != block_table.shape[:1] or lens.shape != seqlens.shape:
         raise ValueError(f"block_table must be [B, max_blocks], seqlens and {name} [B]")
+    if not 1 <= page_size <= 1 << 24:
+        raise ValueError("page_size must be 1..2^24")
     return block_table.shape
 
 
@@ -1634,7 +1638,7 @@ def attn_pages_extend(pool, block_table, seqlens, new_lens, page_size: int, slot
     first in its row) or packed [total] (with cu_seqlens int32 [B+1], or None);
     granted int32 [B] or None: new_lens, or 0 for requests the pool had no pages for
     (those keep their length and have slots -1; see attn.h for which).  Asynchronous."""
-    B, max_blocks = _page_tables(pool, block_table, seqlens, new_lens, "new_lens")
+    B, max_blocks = _page_tables(pool, block_table, seqlens, new_lens, page_size, "new_lens")
     _need(slots, torch.int64, "slots")
     if slots.ndim == 2:
         width, total = slots.shape[1], 0
@@ -1683,7 +1687,7 @@ def attn_pages_trim(pool, block_table, seqlens, keep_lens, page_size: int, *, st
     """Cut each request to its first keep_lens int32 [B] tokens (0: the request is
     done; more than it has: all stay): its pages past them go back on the pool and
     seqlens is set, in place.  Asynchronous."""
-    B, max_blocks = _page_tables(pool, block_table, seqlens, keep_lens, "keep_lens")
+    B, max_blocks = _page_tables(pool, block_table, seqlens, keep_lens, page_size, "keep_lens")
     with _on(_one_device(pool, block_table, seqlens, keep_lens)):
         rc = load().attn_pages_trim(pool.data_ptr(), pool.shape[0] - POOL_HEADER, block_table.data_ptr(),
                                     seqlens.data_ptr(), keep_lens.data_ptr(), B, max_blocks, int(page_size),

@@ -843,6 +843,9 @@ attn_status_t attn_pages_extend(int* pool, int num_blocks, int* block_table, int
     if ((n > 0 && !slots) || !aligned16(slots) || !aligned16(positions) || !aligned4(cu_seqlens) ||
         !aligned4(granted))
         return ATTN_ERR_INVALID_ARG;
+    // (every block reads the lengths while the first one writes these)
+    for (const int* out : {positions, cu_seqlens, granted})
+        if (out && (out == new_lens || out == seqlens || out == pool || out == block_table)) return ATTN_ERR_INVALID_ARG;
     DeviceInfo dev;
     if ((st = current_device_info(&dev)) != ATTN_OK) return st;
     return launch_pages_extend(pool, num_blocks, block_table, seqlens, new_lens, slots, positions, cu_seqlens,

@@ -612,10 +612,12 @@ attn_status_t attn_decode_tree(const void* q, const void* k_pages, const void* v
  *   first, span  the map's first distance and its length, 1 <= span <= 65536
  *
  * and, apart from the bias, what the entry point without _bias in its name
- * takes, for 8 <= d <= 128 (ATTN_ERR_UNSUPPORTED above).  A bias of -inf, or
- * below -1e30, leaves a key out (V must still be finite there: its weight is 0);
- * a row without any key has O = 0, LSE = -inf and adds nothing to a gradient.
- * The bias is added in fp32.
+ * takes, for 8 <= d <= 128 (ATTN_ERR_UNSUPPORTED above).  Biases are finite and
+ * at most 1e30 in size, or leave a key out: -inf, or anything below -1e30 (the
+ * lowest value of a type).  A row without any key has O = 0, LSE = -inf and adds
+ * nothing to a gradient.  K and V have to be finite at keys that are left out,
+ * by the bias or by causal masking (-inf + NaN and 0 * NaN are NaN); keys past a
+ * sequence's end are not read.  The bias is added in fp32.
  * ------------------------------------------------------------------------- */
 
 /*
@@ -734,7 +736,8 @@ attn_status_t attn_page_pool_init(int* pool, int num_blocks, void* stream);
  *              0: packed [total], the requests one after the other
  *   total      >= the sum of new_lens (packed); may be 0
  *   cu_seqlens int32 (device) [B + 1], packed: each request's first row, or NULL
- *   granted    int32 (device) [B]: new_lens[b], or 0 where the pool ran out; or NULL
+ *   granted    int32 (device) [B]: new_lens[b], or 0 where the pool ran out; or
+ *              NULL.  (The outputs are none of the inputs.)
  *
  * Pages are given in the order of the requests, and only whole requests are
  * served: from the first one that would need more pages than are left, every

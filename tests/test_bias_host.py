@@ -113,8 +113,8 @@ def test_decode_refusals(lib, kw, code):
 
 
 def extend(lib, **kw):
-    a = dict(pool=FAKE, blocks=100, bt=FAKE, sl=FAKE, new=FAKE, slots=FAKE, pos=FAKE, cu=FAKE, granted=FAKE, B=4, mb=8,
-             page=16, width=0, total=50)
+    a = dict(pool=FAKE, blocks=100, bt=FAKE, sl=FAKE, new=FAKE, slots=FAKE, pos=2 * FAKE, cu=2 * FAKE,
+             granted=2 * FAKE, B=4, mb=8, page=16, width=0, total=50)
     a.update(kw)
     return lib.attn_pages_extend(a["pool"], a["blocks"], a["bt"], a["sl"], a["new"], a["slots"], a["pos"], a["cu"],
                                  a["granted"], a["B"], a["mb"], a["page"], a["width"], a["total"], None)
@@ -122,8 +122,9 @@ def extend(lib, **kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(pool=None), 1), (dict(pool=FAKE + 4), 1), (dict(bt=None), 1), (dict(sl=None), 1), (dict(new=FAKE + 1), 1),
-    (dict(slots=None), 1), (dict(slots=FAKE + 8), 1), (dict(pos=FAKE + 4), 1), (dict(cu=FAKE + 2), 1),
-    (dict(granted=FAKE + 2), 1), (dict(blocks=0), 1), (dict(B=0), 1), (dict(mb=0), 1), (dict(page=0), 1),
+    (dict(slots=None), 1), (dict(slots=FAKE + 8), 1), (dict(pos=2 * FAKE + 4), 1), (dict(cu=2 * FAKE + 2), 1),
+    (dict(granted=2 * FAKE + 2), 1), (dict(blocks=0), 1),
+    (dict(new=3 * FAKE, granted=3 * FAKE), 1), (dict(sl=3 * FAKE, cu=3 * FAKE), 1), (dict(B=0), 1), (dict(mb=0), 1), (dict(page=0), 1),
     (dict(width=-1), 1), (dict(total=-1), 1), (dict(width=3), 1), (dict(width=3, total=0), 1),
     (dict(width=1 << 29, total=0, cu=None), 1), (dict(mb=1 << 20, page=32), 1), (dict(blocks=(1 << 30) + 1), 2)])
 def test_extend_refusals(lib, kw, code):

@@ -219,6 +219,47 @@ def test_serving_run():
     assert ea.attn_last_device_error() == 0
 
 
+def test_captured_decode_steps():
+    """A whole decode step captured once (pages, the cache's write, attention with the bias) and
+    replayed over 90 tokens, one sequence starting over on the way."""
+    B, Hq, Hkv, d, page = 2, 4, 4, 128, 64
+    g = torch.Generator().manual_seed(2)
+    buckets, first = ea.bias_buckets(32, 128)
+    weights = torch.randn(32, Hq, generator=g)
+    pool = ea.page_pool(4)
+    table = torch.full((B, 2), -1, dtype=torch.int32, device="cuda")
+    seqlens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    kp, vp = (torch.zeros((4, page, Hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q, k, v = (torch.zeros((B, h, 1, d), dtype=torch.bfloat16, device="cuda") for h in (Hq, Hkv, Hkv))
+    one, wg = _int([1] * B), weights.cuda()
+
+    def step():
+        slots, pos, granted = ea.pages_extend(pool, table, seqlens, one, page, width=1)
+        ea.attn_cache_write(k, v, kp, vp, slots)
+        return (pos, *ea.decode_paged_bias(q, kp, vp, table, seqlens, wg, buckets, first))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pos, o, lse = step()
+    ks, vs = [[], []], [[], []]
+    for n in range(90):
+        if n == 40:      # sequence 1 is done, another begins in its place
+            ea.attn_pages_trim(pool, table, seqlens, _int([1000, 0]), page)
+            ks[1], vs[1] = [], []
+        new = [torch.randn(B, h, 1, d, generator=g).to(torch.bfloat16) for h in (Hq, Hkv, Hkv)]
+        for dst, src in zip((q, k, v), new):
+            dst.copy_(src)
+        graph.replay()
+        for b in range(B):
+            ks[b].append(new[1][b])
+            vs[b].append(new[2][b])
+        assert pos[:, 0].tolist() == [len(x) - 1 for x in ks]
+        if n % 13 == 0 or n == 89:
+            for b in range(B):
+                Problem(new[0][b], torch.cat(ks[b], 1), torch.cat(vs[b], 1), weights, buckets.cpu(),
+                        first).check_forward(o[b], lse[b])
+    assert ea.attn_last_device_error() == 0
+
+
 def test_training_run():
     """Forward, backward and an update of the table, three times: each step's gradients are
     those of its table."""
