@@ -28,6 +28,7 @@ constexpr int kMaxDevices = 64;
 constexpr long long kMaxLen = 1ll << 24;
 constexpr long long kMaxHeads = 1ll << 24;
 constexpr int kMaxBiasSpan = 1 << 16;   // distances of a bias map, and buckets
+constexpr long long kMaxBiasTiles = 1ll << 30;  // key tiles whose sums a table's gradient adds up
 constexpr int kMaxPackedRows = 1 << 30;  // rows of a packed batch (ragged maps, fwd_sched.h)
 
 struct DevState {
@@ -415,6 +416,10 @@ attn_status_t check_bias(const void* table, attn_out_dtype_t table_dtype, const 
     return ATTN_OK;
 }
 
+// Whether a backward's key tiles (the longest sequence's for each of a packed batch) are
+// too many for its sums' index arithmetic.
+bool too_many_bias_tiles(int B, int Nk) { return (long long)B * ((Nk + 127) / 128) > kMaxBiasTiles; }
+
 BiasArgs bias_args(const void* table, attn_out_dtype_t table_dtype, const int* buckets, int first, int span,
                    int num_buckets) {
     return BiasArgs{table, buckets, first, span, num_buckets, table_dtype == ATTN_OUT_BF16};
@@ -738,6 +743,7 @@ attn_status_t attn_fwd_varlen_bias(const void* q, const void* k, const void* v, 
 size_t attn_bwd_bias_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int d, int span) {
     const size_t base = attn_bwd_workspace_size(B, Hq, Hkv, Nq, Nk, d);
     if (base == 0 || !head_dim_supported(d) || span < 1 || span > kMaxBiasSpan) return 0;
+    if (Hq > 65535 || too_many_bias_tiles(B, Nk)) return 0;
     return base + bwd_bias_workspace_bytes(B, Hq, Nk, span);
 }
 
@@ -751,7 +757,7 @@ attn_status_t attn_bwd_bias(const void* q, const void* k, const void* v, const v
     if (st != ATTN_OK) return st;
     if ((st = check_grads(dout, lse, dq, dk, dv, grad_dtype)) != ATTN_OK) return st;
     if (!dtable || !aligned4(dtable)) return ATTN_ERR_INVALID_ARG;
-    if (Hq > 65535) return ATTN_ERR_UNSUPPORTED;   // (a grid's second dimension)
+    if (Hq > 65535 || too_many_bias_tiles(B, Nk)) return ATTN_ERR_UNSUPPORTED;   // (Hq: a grid's second dimension)
     if ((st = check_bias(table, table_dtype, buckets, first, span, num_buckets, d)) != ATTN_OK) return st;
     const size_t need = bwd_workspace_bytes(B, Hq, Nq, d) + bwd_bias_workspace_bytes(B, Hq, Nk, span);
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
@@ -766,7 +772,7 @@ size_t attn_bwd_varlen_bias_workspace_size(int B, int Hq, int Hkv, int total_q, 
                                            int span) {
     const size_t base = attn_bwd_varlen_workspace_size(B, Hq, Hkv, total_q, d);
     if (base == 0 || !head_dim_supported(d) || span < 1 || span > kMaxBiasSpan) return 0;
-    if (max_seqlen_k < 1 || max_seqlen_k > kMaxLen) return 0;
+    if (max_seqlen_k < 1 || max_seqlen_k > kMaxLen || Hq > 65535 || too_many_bias_tiles(B, max_seqlen_k)) return 0;
     return base + bwd_bias_workspace_bytes(B, Hq, max_seqlen_k, span);
 }
 
@@ -786,7 +792,7 @@ attn_status_t attn_bwd_varlen_bias(const void* q, const void* k, const void* v, 
     if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
     if ((st = check_grads(dout, lse, dq, dk, dv, grad_dtype)) != ATTN_OK) return st;
     if (!dtable || !aligned4(dtable)) return ATTN_ERR_INVALID_ARG;
-    if (Hq > 65535) return ATTN_ERR_UNSUPPORTED;   // (a grid's second dimension)
+    if (Hq > 65535 || too_many_bias_tiles(B, max_seqlen_k)) return ATTN_ERR_UNSUPPORTED;
     if ((st = check_bias(table, table_dtype, buckets, first, span, num_buckets, d)) != ATTN_OK) return st;
     const size_t need = bwd_varlen_workspace_bytes(B, Hq, total_q) +
                         bwd_bias_workspace_bytes(B, Hq, max_seqlen_k, span);

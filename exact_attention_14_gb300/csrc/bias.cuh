@@ -28,9 +28,11 @@ struct BiasArgs {
 
 constexpr int kBiasWindow = 256;         // floats of one tile's window
 constexpr float kBiasLog2e = 1.44269504088896340736f;
-// A bias below this (a type's lowest value used as a mask) counts as -inf: its key
-// is left out.  Above it, bias + score keeps at least the bias's own 24 bits.
-constexpr float kBiasMasked = -1e30f;
+// A bias below this (-1e9, a type's lowest value: masks) counts as -inf: its key is
+// left out.  Were a whole row at -1e9, the backward's P = 2^(score + bias - LSE) would
+// be the rounding of LSE (64 there) to the power of 2, infinite or 0; at 1e6 that rounding is
+// below 2^0.5.
+constexpr float kBiasMasked = -1e6f;
 
 // Biases of head h at the distances r, r + 32, ..., times log2(e); -inf for those above
 // `last` (causal masking is a bias of -inf at every distance above 0, so a window

@@ -612,12 +612,14 @@ attn_status_t attn_decode_tree(const void* q, const void* k_pages, const void* v
  *   first, span  the map's first distance and its length, 1 <= span <= 65536
  *
  * and, apart from the bias, what the entry point without _bias in its name
- * takes, for 8 <= d <= 128 (ATTN_ERR_UNSUPPORTED above).  Biases are finite and
- * at most 1e30 in size, or leave a key out: -inf, or anything below -1e30 (the
- * lowest value of a type).  A row without any key has O = 0, LSE = -inf and adds
- * nothing to a gradient.  K and V have to be finite at keys that are left out,
- * by the bias or by causal masking (-inf + NaN and 0 * NaN are NaN); keys past a
- * sequence's end are not read.  The bias is added in fp32.
+ * takes, for 8 <= d <= 128 (ATTN_ERR_UNSUPPORTED above).  Biases are at most 1e6
+ * in size, or leave a key out: -inf, or anything below -1e6 (-1e9, the lowest value
+ * of a type).  A row without any key has O = 0, LSE = -inf and adds nothing to a
+ * gradient.  K and V have to be finite at keys that are left out, by the bias or by
+ * causal masking (-inf + NaN and 0 * NaN are NaN); keys past a sequence's end are not
+ * read.  The bias is added in fp32.  The gradients take P from the stored LSE, whose
+ * rounding changes it by a factor of at most 2^(|LSE| 2^-21) (0.3 % where all of a row's
+ * biases are 1e4).
  * ------------------------------------------------------------------------- */
 
 /*
@@ -670,7 +672,8 @@ size_t attn_bwd_bias_workspace_size(int B, int Hq, int Hkv, int Nq, int Nk, int 
  *
  * fp32 [num_buckets, Hq], written whole (0 for a bucket no distance has), from
  * the unrounded dS = P o (dP - D).  All gradients are bit-identical from run to
- * run.  Hq <= 65535.
+ * run.  Hq <= 65535; at most 2^30 key tiles of 128 in the batch (in a packed one: B
+ * times those of max_seqlen_k).
  */
 attn_status_t attn_bwd_bias(const void* q, const void* k, const void* v, const void* o, const void* dout,
                             const float* lse, const void* table, attn_out_dtype_t table_dtype,

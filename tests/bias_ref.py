@@ -20,11 +20,11 @@ def bucket(r, n, D):
 
 
 def bias64(table, buckets, first, n, m):
-    """[H, n, m]: the bias of query i and key j; what is below -1e30 is -inf."""
+    """[H, n, m]: the bias of query i and key j; what is below -1e6 is -inf."""
     r = torch.arange(m) - (torch.arange(n)[:, None] + m - n)
     b = buckets.cpu().long()[(r - first).clamp(0, len(buckets) - 1)]
     t = table.cpu().double()
-    t = torch.where(t < -1e30, torch.full_like(t, -math.inf), t)
+    t = torch.where(t < -1e6, torch.full_like(t, -math.inf), t)
     return t.t()[:, b], b
 
 

@@ -63,13 +63,13 @@ def test_packed_forward_refusals(lib, kw, code):
 
 def bwd(lib, packed, **kw):
     a = dict(BIAS, q=FAKE, o=FAKE, do=FAKE, lse=FAKE, dq=FAKE, dk=FAKE, dt=FAKE, cq=FAKE, Hq=4, d=64, gt=0, ws=FAKE,
-             wsb=1 << 40, n=64)
+             wsb=1 << 40, n=64, B=1, m=64)
     a.update(kw)
     head = (a["q"], FAKE, FAKE, a["o"], a["do"], a["lse"], *_bias(a), a["dq"], a["dk"], FAKE, a["dt"])
     if packed:
         return lib.attn_bwd_varlen_bias(*head, a["cq"], FAKE, 1, a["Hq"], 2, 64, 64, a["n"], 64, a["d"], 1, 0.125, 0,
                                         a["gt"], a["ws"], a["wsb"], None)
-    return lib.attn_bwd_bias(*head, 1, a["Hq"], 2, a["n"], 64, a["d"], 1, 0.125, 0, a["gt"], a["ws"], a["wsb"], None)
+    return lib.attn_bwd_bias(*head, a["B"], a["Hq"], 2, a["n"], a["m"], a["d"], 1, 0.125, 0, a["gt"], a["ws"], a["wsb"], None)
 
 
 @pytest.mark.parametrize("packed", [False, True])
@@ -88,7 +88,11 @@ def test_backward_workspace(lib):
         ea.attn_bwd_workspace_size(200, 1, 1, 100, 300, 64) + 16 + 4 * 20 * (600 + 2)
     assert ea.attn_bwd_varlen_bias_workspace_size(2, 4, 2, 100, 300, 64, 114) == \
         ea.attn_bwd_varlen_workspace_size(2, 4, 2, 100, 64) + 16 + 4 * 4 * 132 * (6 + 1)
-    for bad in (dict(d=136), dict(span=0), dict(span=65537), dict(Hq=3)):
+    assert ea.attn_bwd_varlen_bias_workspace_size(1 << 13, 1, 1, 100, 1 << 24, 64, 1) > 0
+    assert ea.attn_bwd_varlen_bias_workspace_size((1 << 13) + 1, 1, 1, 100, 1 << 24, 64, 1) == 0
+    assert ea.attn_bwd_bias_workspace_size((1 << 13) + 1, 1, 1, 100, 1 << 24, 64, 1) == 0
+    assert bwd(lib, False, B=(1 << 13) + 1, m=1 << 24) == 2
+    for bad in (dict(d=136), dict(span=0), dict(span=65537), dict(Hq=3), dict(Hq=131072)):
         a = dict(Hq=4, d=64, span=114)
         a.update(bad)
         assert ea.attn_bwd_bias_workspace_size(2, a["Hq"], 2, 100, 300, a["d"], a["span"]) == 0

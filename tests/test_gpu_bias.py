@@ -97,7 +97,7 @@ def test_forward_split_tail():
     Problem(q[0], k[0], v[0], table, ids, -1000).check_forward(o[0], lse[0])
 
 
-@pytest.mark.parametrize("low", [-math.inf, torch.finfo(torch.float32).min, torch.finfo(torch.bfloat16).min])
+@pytest.mark.parametrize("low", [-math.inf, -1e9, torch.finfo(torch.float32).min, torch.finfo(torch.bfloat16).min])
 @pytest.mark.parametrize("causal", [False, True])
 def test_masked_buckets(causal, low):
     """Buckets that leave their keys out: forward, gradients, rows without any key."""
@@ -118,6 +118,18 @@ def test_masked_buckets(causal, low):
     grads, bounds = ref.gradients(o[0], dout[0], lse[0], nb)
     check_gradients([got[0][0], got[1][0], got[2][0], got[3]], grads, bounds)
     assert (got[3][:, 2] == 0).all() and (got[0][0, 2] == 0).all()
+
+
+@pytest.mark.parametrize("by", [9.99e5, -9.99e5])
+def test_large_biases_stay_finite(by):
+    """All biases near the largest allowed: O and LSE hold (scores keep 2^-4 there), gradients are finite."""
+    q, k, v, dout, g = _inputs(1, 2, 2, 200, 200, 64)
+    ids, table = torch.arange(9, dtype=torch.int32), torch.full((9, 2), by)
+    qg, kg, vg, tg, ig, dg = _gpu(q, k, v, table, ids, dout)
+    o, lse = ea.forward_bias(qg, kg, vg, tg, ig, -4)
+    assert (lse - by).abs().max() < 16 and torch.isfinite(o.float()).all()
+    for x in ea.backward_bias(qg, kg, vg, o, dg, lse, tg, ig, -4):
+        assert torch.isfinite(x.float()).all()
 
 
 @pytest.mark.parametrize("kind", MAPS)
