@@ -2094,37 +2094,58 @@ attn_bwd_bias_sum_kernel(const float* __restrict__ partial, float* __restrict__ 
     }
 }
 
-// 2: a warp per (head, bucket) goes through the map, 1024 distances at a time in shared
-// memory, and adds up those of the bucket.
+// 2: a block finds where on the map each of its up to 64 buckets begins and ends (one pass
+// over the map, whose runs' borders alone are compared), then a warp per (bucket,
+// head) adds up what lies between: the map once in all where buckets are runs of
+// distances, whatever their number.  (32767 buckets, one a distance,
+// 16 heads of 16384 positions: the backward 11.6 ms with a walk over the whole map for
+// each bucket, so 5.7; without a bias 4.7.)
+constexpr int kTableBuckets = 64;
 __global__ void __launch_bounds__(256)
 attn_bwd_bias_table_kernel(const float* __restrict__ sums, const int* __restrict__ buckets,
-                           float* __restrict__ dtable, int parts, int Hq, int span, int num_buckets) {
-    __shared__ float val[1024];
-    __shared__ int ids[1024];
-    const int h = blockIdx.y, lane = threadIdx.x & 31;
-    const int bk = blockIdx.x * 8 + (threadIdx.x >> 5);
+                           float* __restrict__ dtable, int parts, int Hq, int span, int num_buckets, int own) {
+    __shared__ int lo[kTableBuckets], hi[kTableBuckets];
+    const int lane = threadIdx.x & 31, b0 = blockIdx.x * own;
     const int floats = bias_partial_floats(span);
-    float a = 0.f;
-    for (int x0 = 0; x0 < floats; x0 += 1024) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int x = x0 + 256 * i + threadIdx.x;
-            const int at = x < floats ? bias_place(x, span) : -1;
-            ids[256 * i + threadIdx.x] = at < 0 ? -1 : __ldg(buckets + at);
-            float v = 0.f;
-            if (at >= 0)
-                for (int z = 0; z < parts; ++z) v += __ldg(sums + ((size_t)z * Hq + h) * floats + x);
-            val[256 * i + threadIdx.x] = v;
-        }
-        __syncthreads();
-#pragma unroll 8
-        for (int x = lane; x < 1024; x += 32)
-            if (ids[x] == bk) a += val[x];
+    if (threadIdx.x < kTableBuckets) {
+        lo[threadIdx.x] = span;
+        hi[threadIdx.x] = -1;
     }
+    __syncthreads();
+#pragma unroll 8
+    for (int x = threadIdx.x; x < span; x += 256) {
+        const int id = __ldg(buckets + x), k = id - b0;
+        const int before = __ldg(buckets + max(x - 1, 0)), after = __ldg(buckets + min(x + 1, span - 1));
+        if ((unsigned)k < (unsigned)own) {
+            if (x == 0 || before != id) atomicMin(&lo[k], x);
+            if (x == span - 1 || after != id) atomicMax(&hi[k], x);
+        }
+    }
+    __syncthreads();
+    const int at_first = __ldg(buckets) - b0, at_last = __ldg(buckets + span - 1) - b0;
+    for (int k = threadIdx.x >> 5; k < own && b0 + k < num_buckets; k += 8)
+        for (int h = blockIdx.y; h < Hq; h += gridDim.y) {
+            auto sum_at = [&](int x) {
+                float v = 0.f;
+                for (int z = 0; z < parts; ++z) v += __ldg(sums + ((size_t)z * Hq + h) * floats + x);
+                return v;
+            };
+            float a = 0.f;
+            const int to = hi[k];
+#pragma unroll 8
+            for (int x = lo[k] + lane; x <= to; x += 32) {
+                const float v = sum_at(x);
+                a += __ldg(buckets + x) == b0 + k ? v : 0.f;
+            }
+            // the distances beyond the map (bias_place)
+            if (lane < 18) {
+                const bool left = lane < 8 || lane == 16;
+                if (k == (left ? at_first : at_last)) a += sum_at(span + lane);
+            }
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, s);
-    if (lane == 0 && bk < num_buckets) dtable[(size_t)bk * Hq + h] = a;
+            for (int s = 16; s > 0; s >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, s);
+            if (lane == 0) dtable[(size_t)(b0 + k) * Hq + h] = a;
+        }
 }
 
 // Blocks that share a distance's key tiles in step 1: 512 tiles each, at most 32.
@@ -2143,8 +2164,10 @@ attn_status_t launch_bias_grad(const BwdParams& p, float* dtable, cudaStream_t s
     const int floats = bias_partial_floats(p.bias.span);
     const int tiles = p.B * p.n_kt, parts = bias_sum_parts(tiles);
     // one launch while a head's sums are at most 128 KB (4 x 2048 positions, 245 floats a
-    // tile: 6.1 us against 12.3 in two; packed 16 x 4096, 3.9 MB a head: two)
-    if (floats <= kBiasSmallFloats && (long long)tiles * floats <= 32768) {
+    // tile: 6.1 us against 12.3 in two; packed 16 x 4096, 3.9 MB a head: two) and its
+    // warps' walks over the map, one a bucket, are short
+    if (floats <= kBiasSmallFloats && (long long)tiles * floats <= 32768 &&
+        (long long)p.bias.num_buckets * floats <= 1 << 19) {
         attn_bwd_bias_small_kernel<<<(unsigned)p.Hq, 1024, 0, stream>>>(p.partial, p.bias.buckets, dtable, tiles, p.Hq,
                                                                         p.bias.span, p.bias.num_buckets);
         return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
@@ -2153,8 +2176,13 @@ attn_status_t launch_bias_grad(const BwdParams& p, float* dtable, cudaStream_t s
     attn_bwd_bias_sum_kernel<<<dim3((unsigned)((floats + 127) / 128), (unsigned)p.Hq, (unsigned)parts), 256, 0,
                                stream>>>(p.partial, sums, tiles, p.Hq, floats);
     if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-    attn_bwd_bias_table_kernel<<<dim3((unsigned)((p.bias.num_buckets + 7) / 8), (unsigned)p.Hq), 256, 0, stream>>>(
-        sums, p.bias.buckets, dtable, parts, p.Hq, p.bias.span, p.bias.num_buckets);
+    // few buckets: 8 and a head a block, a warp each; many: 64, and some heads one after
+    // the other, so that the map is not searched for each of them (2048 blocks)
+    const int own = p.bias.num_buckets <= 1024 ? 8 : kTableBuckets;
+    const unsigned rows = (unsigned)((p.bias.num_buckets + own - 1) / own);
+    const unsigned heads = rows >= 2048 ? 1 : 2048 / rows;
+    attn_bwd_bias_table_kernel<<<dim3(rows, heads < (unsigned)p.Hq ? heads : (unsigned)p.Hq), 256, 0, stream>>>(
+        sums, p.bias.buckets, dtable, parts, p.Hq, p.bias.span, p.bias.num_buckets, own);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

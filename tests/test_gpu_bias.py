@@ -275,6 +275,31 @@ def test_large_biases():
         check_gradients([got[0][0], got[1][0], got[2][0], got[3]], grads, bounds)
 
 
+@pytest.mark.parametrize("nb,kind", [(2400, "a distance each"), (1025, "runs"), (40000, "scrambled"), (1 << 16, "one")])
+def test_many_buckets(nb, kind):
+    """The table's gradient where a block has 64 buckets, and several heads one after the other."""
+    q, k, v, dout, g = _inputs(1, 6, 3, 200, 330, 64, seed=nb)
+    if kind == "a distance each":
+        ids, first = torch.arange(nb, dtype=torch.int32), -1300
+    elif kind == "runs":
+        ids, first = torch.arange(3000, dtype=torch.int32) // 3 + 25, -1500
+    elif kind == "scrambled":
+        ids, first = torch.randint(0, nb, (900,), generator=g, dtype=torch.int32), -400
+        ids[::7] = nb - 1
+    else:
+        ids, first = torch.full((300,), nb - 1, dtype=torch.int32), -100
+    table = _table(g, nb, 6)
+    o, lse = ea.forward_bias(*_gpu(q, k, v, table, ids), first)
+    ref = Problem(q[0], k[0], v[0], table, ids, first)
+    ref.check_forward(o[0], lse[0])
+    got = ea.backward_bias(*_gpu(q, k, v), o, dout.cuda(), lse, *_gpu(table, ids), first, grad_dtype=torch.float32)
+    grads, bounds = ref.gradients(o[0], dout[0], lse[0], nb)
+    check_gradients([got[0][0], got[1][0], got[2][0], got[3]], grads, bounds)
+    used = torch.zeros(nb, dtype=torch.bool)
+    used[ids.long()] = True
+    assert (got[3].cpu()[~used] == 0).all()
+
+
 def test_wrong_buckets_are_reported():
     q, k, v, dout, g = _inputs(1, 2, 2, 40, 40, 64)
     ids = torch.tensor([0, 5, 1], dtype=torch.int32)          # bucket 5 of 3: adds nothing
