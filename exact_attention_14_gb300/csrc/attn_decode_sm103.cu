@@ -264,15 +264,15 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tk, const __grid_co
             const int r0 = t0 + st * kStageKeys - (L - 1);   // the stage's first distance
             const bool before = r0 + kStageKeys - 1 <= p.bias.first;
             const bool near = !before && r0 < p.bias.first + p.bias.span - 1;
+            if (near) {
+                bias_at(p.bias, p.Hq, h0, h1, r0 + wk0 + 2 * qc, bv, err);
+            } else {
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+                for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (near)
-                        bv[nt][e] = bias_at(p.bias, p.Hq, e < 2 ? h0 : h1, r0 + wk0 + nt * 8 + 2 * qc + (e & 1), err);
-                    else
+                    for (int e = 0; e < 4; ++e)
                         bv[nt][e] = e < 2 ? (before ? left0 : right0) : (before ? left1 : right1);
-                }
+            }
         }
         // warp-uniform: ldmatrix and mma.sync below need every lane
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&full[slot]), (st / kDecStages) & 1, abort_flag));

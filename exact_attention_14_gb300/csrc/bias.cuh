@@ -59,6 +59,32 @@ __device__ __forceinline__ void bias_at(const BiasArgs& a, int Hq, int h, int r,
     }
     if (bad) atomicOr(err, kErrBadSeqlen);
 }
+// The decode's: heads h0 (v[n][0], v[n][1]) and h1 (v[n][2], v[n][3]) at the distances
+// r + 8 n and r + 8 n + 1, n < 2.
+__device__ __forceinline__ void bias_at(const BiasArgs& a, int Hq, int h0, int h1, int r, float (&v)[2][4],
+                                        unsigned int* err) {
+    int bk[4];
+    bool bad = false;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const int i = r + 8 * (n >> 1) + (n & 1) - a.first;
+        bk[n] = __ldg(a.buckets + min(max(i, 0), a.span - 1));
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const bool ok = (unsigned)bk[n] < (unsigned)a.num_buckets;
+        const size_t row = (size_t)(ok ? bk[n] : 0) * Hq;
+        bad |= !ok;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const size_t at = row + (e ? h1 : h0);
+            const float x = a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.table)[at])
+                                   : __ldg(static_cast<const float*>(a.table) + at);
+            v[n >> 1][2 * e + (n & 1)] = ok && x < kBiasMasked ? -INFINITY : ok ? x * kBiasLog2e : 0.f;
+        }
+    }
+    if (bad) atomicOr(err, kErrBadSeqlen);
+}
 __device__ __forceinline__ float bias_at(const BiasArgs& a, int Hq, int h, int r, unsigned int* err) {
     float v[1];
     bias_at(a, Hq, h, r, INT_MAX, v, err);
