@@ -259,6 +259,8 @@ attn_decode_split_kernel(const __grid_constant__ CUtensorMap tk, const __grid_co
         const int slot = st % kDecStages;
         // BIAS: this thread's 4 keys x 2 heads, looked up while the stage arrives.  A
         // stage wholly before the map (most of a long cache) or past it has one a head.
+        // (16 sequences of 1024..32768 keys, 32 / 8 heads of 128: 195 us with a map of 128
+        // distances, 201 with 2048, 205 with 16384; 193 without a bias.)
         float bv[2][4];
         if constexpr (BIAS) {
             const int r0 = t0 + st * kStageKeys - (L - 1);   // the stage's first distance

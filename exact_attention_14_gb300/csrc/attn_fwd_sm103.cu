@@ -817,7 +817,9 @@ __device__ __noinline__ void split_piece_epilogue(unsigned int* merge_count, flo
 // that they share.  Masked tiles get a window in either case (the softmax then has
 // an instantiation less).  Two slots: the warp runs a tile ahead of the softmax, so
 // that nobody waits for the two dependent loads of a look-up.  The windows lie in
-// the second store buffer of the tile's first softmax warp.
+// the second store buffer of the tile's first softmax warp.  (8 x 16 heads x 4096
+// positions, not causal: 642 us without a bias, 672 with one for all distances, 690
+// with a map of 128 distances either way, 838 with every tile inside the map.)
 template <int D>
 __host__ __device__ constexpr int window_off(int t) {
     return FwdCfg<D>::kStgOff + t * 4 * FwdCfg<D>::kStgBytesPerWarp + 2048;

@@ -5,12 +5,16 @@
 // first .. first + span - 1, and farther ones count as its ends.  The kernels
 // hold it times log2(e), since their scores are in base 2.
 //
-// A tile of 128 query rows and 128 keys meets 255 distances, base .. base + 254.
-// Where they all lie on one side of the map (or at its end) the whole tile has one
-// bias, which costs a term of the exponent that is there anyway; other tiles take
-// theirs from a window of 256 floats in shared memory, one per distance, that a warp
-// of its own fills up to two tiles ahead.  Lanes of a warp hold consecutive rows, so a column's
-// 32 reads are 32 consecutive floats: no bank conflict.
+// A tile of 128 query rows and 128 keys meets 255 distances, base .. base + 254: a
+// window of 256 floats in shared memory, one per distance, that a warp of its own
+// fills up to two tiles ahead of those that use it.
+// Forward: where all distances lie on one side of the map (or at its end) the whole
+// tile has one bias, which costs a term of the exponent that is there anyway; other
+// tiles take theirs from the window.  Lanes of a warp hold consecutive rows, so a
+// column's 32 reads are 32 consecutive floats: no bank conflict.
+// Backward: always from the window, on MMA-like fragments of which a thread's 64
+// elements meet 22 distances (pds_tile_bias).
+// Decode: a thread looks up its own 4 keys x 2 heads.
 #pragma once
 
 #include <climits>

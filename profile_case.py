@@ -10,6 +10,10 @@ profiler captures (ncu) of a single launch configuration.
     python profile_case.py --kernel rope
     python profile_case.py --kernel cache --cache e4m3
     python profile_case.py --kernel tree --tokens 64 --cache e4m3
+    python profile_case.py --kernel bias --workload prefill2x --distance 128
+    python profile_case.py --kernel biasbwd --workload prefill --distance 2048
+    python profile_case.py --kernel biasdecode
+    python profile_case.py --kernel pages
 
 Workloads: prefill (B=4 H=16 N=2048 d=128), prefill2x (B=8: inputs larger
 than L2), prefill256 (the prefill shape at d=256), long (B=1 H=32 N=16384), gqa (B=8 Hq=32 Hkv=8 N=4096), decode
@@ -22,7 +26,10 @@ workload (Q and K rotated by the random-sign Hadamard matrix), fp8quant the
 rotating quantization of its Q.  rope turns Q and K of 8 x 4096 tokens (32 and 8
 heads of 128).  cache writes keys and values of 16 sequences of 256..8192 keys (8
 heads of 128) into 64-key pages and reads them back; tree attends them from --tokens
-drafted tokens a sequence with 32 query heads.  Inputs come from seeded generators.
+drafted tokens a sequence with 32 query heads.  bias and biasbwd are fwd and bwd with a
+relative position bias of 32 buckets over --distance positions, biasdecode one new token
+over the pages of cache; pages admits 512 prompts of 17..4096 tokens to 16-token pages
+and takes them back.  Inputs come from seeded generators.
 """
 from __future__ import annotations
 
@@ -62,6 +69,13 @@ def paged(args, dev):
     descale = [torch.zeros(16 * width, H, page, device=dev) if e4m3 else None for _ in range(2)]
     table, cu = table.to(dev, torch.int32), cu.to(dev, torch.int32)
     ea.attn_cache_write(k, v, *pages, slots, *descale)
+    if args.kernel == "biasdecode":
+        q = torch.randn(16, 32, 1, d, device=dev, generator=gd).to(torch.bfloat16)
+        ids, first = ea.bias_buckets(32, args.distance)
+        bias = torch.randn(32, 32, device=dev, generator=gd)
+        for _ in range(args.iters):
+            ea.decode_paged_bias(q, *pages, table, lens.to(dev, torch.int32), bias, ids, first)
+        return
     if args.kernel == "tree":
         q = torch.randn(16, 32, args.tokens, d, device=dev, generator=gd).to(torch.bfloat16)
         for _ in range(args.iters):
@@ -72,15 +86,28 @@ def paged(args, dev):
         ea.cache_read(*pages, table, cu, total, *descale)
 
 
+def page_tables(args, dev):
+    """512 prompts admitted at once, and taken back."""
+    lens = (torch.arange(512, dtype=torch.int32) * 4079 // 511 + 17)[torch.randperm(512, generator=torch.Generator().manual_seed(3))]
+    total, lens = int(lens.sum()), lens.to(dev)
+    pool = ea.page_pool(512 * 256)
+    table = torch.full((512, 257), -1, dtype=torch.int32, device=dev)
+    seqlens, none = (torch.zeros(512, dtype=torch.int32, device=dev) for _ in range(2))
+    for _ in range(args.iters):
+        ea.pages_extend(pool, table, seqlens, lens, 16, total=total)
+        ea.pages_trim(pool, table, seqlens, none, 16)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--kernel", choices=["fwd", "decode", "bwd", "fp8", "fp8quant", "varlen", "rope", "cache",
-                                             "tree"], required=True)
+                                             "tree", "bias", "biasbwd", "biasdecode", "pages"], required=True)
     ap.add_argument("--workload", default="prefill")
     ap.add_argument("--causal", type=int, default=-1, help="-1: the workload's first mode")
     ap.add_argument("--iters", type=int, default=3)
     ap.add_argument("--cache", choices=["bf16", "e4m3"], default="bf16", help="cache, tree")
     ap.add_argument("--tokens", type=int, default=1, help="tree: drafted tokens of a sequence")
+    ap.add_argument("--distance", type=int, default=128, help="bias, biasbwd, biasdecode: the buckets' reach")
     args = ap.parse_args()
     dev = torch.device("cuda", 0)
     if args.kernel in ("fp8", "fp8quant"):
@@ -107,8 +134,10 @@ def main():
         f, mag = ea.rope_frequencies(128)
         for _ in range(args.iters):
             ea.rope(qkv[:, :, :32].transpose(1, 2), qkv[:, :, 32:].transpose(1, 2), pos, f, magnitude=mag)
-    elif args.kernel in ("cache", "tree"):
+    elif args.kernel in ("cache", "tree", "biasdecode"):
         paged(args, dev)
+    elif args.kernel == "pages":
+        page_tables(args, dev)
     elif args.kernel == "varlen":
         lens = varlen_lengths(VARLEN.n_seqs, VARLEN.len_lo, VARLEN.len_hi, VARLEN.seed)
         q, k, v, cq, ck = (t.to(dev) for t in make_varlen_inputs(lens, lens, VARLEN.Hq, VARLEN.Hkv,
@@ -117,25 +146,37 @@ def main():
         lse = torch.empty((VARLEN.Hq, q.shape[0]), dtype=torch.float32, device=dev)
         for _ in range(args.iters):
             ea.attn_fwd_varlen(q, k, v, o, cq, ck, max(lens), max(lens), lse, causal=VARLEN.causal)
-    elif args.kernel == "bwd":
+    elif args.kernel in ("bwd", "biasbwd"):
         cfg = FWD[args.workload]
         causal = cfg.causal[0] if args.causal < 0 else bool(args.causal)
         q, k, v = (t.to(dev) for t in make_fwd_inputs(cfg.B, cfg.Hq, cfg.Hkv, cfg.N, cfg.N, cfg.d,
                                                      cfg.seed, cfg.outlier_channels))
         g = torch.Generator().manual_seed(cfg.seed + 100)
         dout = torch.randn(q.shape, generator=g, dtype=torch.float32).to(torch.bfloat16).to(dev)
-        o, lse = ea.forward(q, k, v, causal=causal)
-        for _ in range(args.iters):
-            ea.backward(q, k, v, o, dout, lse, causal=causal)
-    elif args.kernel == "fwd":
+        if args.kernel == "biasbwd":
+            ids, first = ea.bias_buckets(32, args.distance, not causal)
+            bias = torch.randn(32, cfg.Hq, generator=g).to(dev)
+            o, lse = ea.forward_bias(q, k, v, bias, ids, first, causal=causal)
+            for _ in range(args.iters):
+                ea.backward_bias(q, k, v, o, dout, lse, bias, ids, first, causal=causal)
+        else:
+            o, lse = ea.forward(q, k, v, causal=causal)
+            for _ in range(args.iters):
+                ea.backward(q, k, v, o, dout, lse, causal=causal)
+    elif args.kernel in ("fwd", "bias"):
         cfg = FWD[args.workload]
         causal = cfg.causal[0] if args.causal < 0 else bool(args.causal)
         q, k, v = (t.to(dev) for t in make_fwd_inputs(cfg.B, cfg.Hq, cfg.Hkv, cfg.N, cfg.N, cfg.d,
                                                      cfg.seed, cfg.outlier_channels))
         o = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
         lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
+        ids, first = ea.bias_buckets(32, args.distance, not causal)
+        bias = torch.randn(32, cfg.Hq, generator=torch.Generator().manual_seed(cfg.seed)).to(dev)
         for _ in range(args.iters):
-            ea.attn_fwd(q, k, v, o, lse, causal=causal)
+            if args.kernel == "bias":
+                ea.attn_fwd_bias(q, k, v, bias, ids, first, o, lse, causal=causal)
+            else:
+                ea.attn_fwd(q, k, v, o, lse, causal=causal)
     elif args.workload == "decode256":
         # decode at d = 256: B16 Hq32 Hkv8, cache [16, 8, 16384, 256], lengths U[512, 16384]
         # (the bench's d = 256 decode leg; drawn on the GPU from seeded generators)
