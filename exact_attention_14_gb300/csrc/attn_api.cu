@@ -148,19 +148,29 @@ attn_status_t encode_tmap_f32_sw128_3d(CUtensorMap* map, void* base, int d, int 
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-attn_status_t encode_tmap_ragged(CUtensorMap* map, const void* base, bool f32, int d, int heads,
-                                 int box_cols, int box_rows, bool swizzle128) {
+attn_status_t encode_tmap_ragged(CUtensorMap* map, int* col, const void* base, int rows, bool f32, int d,
+                                 int heads, int box_cols, int box_rows, bool swizzle128) {
     if (!load_encoder()) return ATTN_ERR_CUDA;
     const cuuint64_t es = f32 ? 4 : 2;
     const cuuint64_t rs = (cuuint64_t)heads * d * es;  // row stride (bytes)
     if (rs >= (1ull << 34)) return ATTN_ERR_UNSUPPORTED;
-    cuuint64_t dims[5] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)kRaggedWindow,
+    // Rows outside a sequence are filled with zeros, but for these maps (not for dense
+    // ones) the hardware looks at memory up to 128 KB past the map's base: a shorter array
+    // that begins near the end of its 2 MB block (the unit in which device memory is
+    // mapped) gets a map that begins 256 KB lower, and its columns start that far on.
+    // (Seen on pages of host memory becoming resident.  A 9 KB array 25 KB before the
+    // end of what was mapped gave an invalid access.)
+    constexpr uintptr_t kReach = 256 << 10, kBlock = 2 << 20;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(base);
+    const uintptr_t lower = (cuuint64_t)rows * rs < kReach && at % kBlock > kBlock - kReach ? kReach : 0;
+    *col = (int)(lower / es);
+    cuuint64_t dims[5] = {(cuuint64_t)(d + *col), (cuuint64_t)heads, (cuuint64_t)kRaggedWindow,
                           (cuuint64_t)kRaggedOuterExtent, (cuuint64_t)kRaggedOuterExtent};
     cuuint64_t strides[4] = {(cuuint64_t)d * es, rs, rs, (1ull << 34) - rs};
     cuuint32_t box[5] = {(cuuint32_t)box_cols, 1u, (cuuint32_t)box_rows, 1u, 1u};
     cuuint32_t elem[5] = {1u, 1u, 1u, 1u, 1u};
     CUresult r = g_encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                          5, const_cast<void*>(base), dims, strides, box, elem,
+                          5, reinterpret_cast<void*>(at - lower), dims, strides, box, elem,
                           CU_TENSOR_MAP_INTERLEAVE_NONE,
                           swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                           swizzle128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,

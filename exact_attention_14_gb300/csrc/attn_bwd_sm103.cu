@@ -140,6 +140,7 @@ struct BwdParams {
     const int* cu_q;
     const int* cu_k;
     int total_q, total_k, vstride;
+    int col_q, col_k, col_v, col_do, col_dk, col_dv;   // the maps' first columns
     // the BIAS instantiations; partial: [B, n_kt, Hq, bias_partial_floats] fp32, a key tile's
     // sums of dS over each distance of the map, then over the distances before it (8
     // warps' parts), after it (8), and a ninth part of each
@@ -378,9 +379,9 @@ __device__ void bwd_producer(const CUtensorMap* tq, const CUtensorMap* tk, const
             for (int c = 0; c < D / 64; ++c) {
                 if constexpr (VARLEN) {
                     const int r = kRaggedWindow - w.nk + w.k0;
-                    tma_load_5d(smem_u32(smem + C::kK) + c * 16384, tk, bar, 64 * c, kvh, r, w.kb + w.nk,
+                    tma_load_5d(smem_u32(smem + C::kK) + c * 16384, tk, bar, p.col_k + 64 * c, kvh, r, w.kb + w.nk,
                                 kRaggedWindow);
-                    tma_load_5d(smem_u32(smem + C::kV) + c * 16384, tv, bar, 64 * c, kvh, r, w.kb + w.nk,
+                    tma_load_5d(smem_u32(smem + C::kV) + c * 16384, tv, bar, p.col_v + 64 * c, kvh, r, w.kb + w.nk,
                                 kRaggedWindow);
                 } else {
                     tma_load_3d(smem_u32(smem + C::kK) + c * 16384, tk, bar, 64 * c, w.k0, kvh);
@@ -406,9 +407,9 @@ __device__ void bwd_producer(const CUtensorMap* tq, const CUtensorMap* tk, const
                 for (int c = 0; c < D / 64; ++c) {
                     if constexpr (VARLEN) {
                         const int r = kRaggedWindow - w.nq + q0;
-                        tma_load_5d(smem_u32(smem + C::kQ + st * C::kTile) + c * 16384, tq, bar, 64 * c, hq, r,
+                        tma_load_5d(smem_u32(smem + C::kQ + st * C::kTile) + c * 16384, tq, bar, p.col_q + 64 * c, hq, r,
                                     w.qb + w.nq, kRaggedWindow);
-                        tma_load_5d(smem_u32(smem + C::kDO + st * C::kTile) + c * 16384, tdo, bar, 64 * c, hq,
+                        tma_load_5d(smem_u32(smem + C::kDO + st * C::kTile) + c * 16384, tdo, bar, p.col_do + 64 * c, hq,
                                     r, w.qb + w.nq, kRaggedWindow);
                     } else {
                         tma_load_3d(smem_u32(smem + C::kQ + st * C::kTile) + c * 16384, tq, bar, 64 * c, q0,
@@ -1108,7 +1109,7 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
                         const CUtensorMap* map = t ? tdk : tdv;
                         const int col = cc_lo + c0;
                         if constexpr (VARLEN)
-                            tma_store_5d(map, stg, col, w.g, kRaggedWindow - w.nk + w.k0 + wq * 32, w.kb + w.nk,
+                            tma_store_5d(map, stg, (t ? p.col_dk : p.col_dv) + col, w.g, kRaggedWindow - w.nk + w.k0 + wq * 32, w.kb + w.nk,
                                          kRaggedWindow);
                         else
                             tma_store_3d(map, stg, col, w.k0 + wq * 32, w.b * p.Hkv + w.g);
@@ -1377,9 +1378,9 @@ __device__ void dq_producer(const CUtensorMap* tq, const CUtensorMap* tk, const 
             for (int c = 0; c < D / 64; ++c) {
                 if constexpr (VARLEN) {
                     const int r = kRaggedWindow - w.nq + w.q0;
-                    tma_load_5d(smem_u32(smem + C::kQ) + c * 16384, tq, bar, 64 * c, w.hq, r, w.qb + w.nq,
+                    tma_load_5d(smem_u32(smem + C::kQ) + c * 16384, tq, bar, p.col_q + 64 * c, w.hq, r, w.qb + w.nq,
                                 kRaggedWindow);
-                    tma_load_5d(smem_u32(smem + C::kDO) + c * 16384, tdo, bar, 64 * c, w.hq, r, w.qb + w.nq,
+                    tma_load_5d(smem_u32(smem + C::kDO) + c * 16384, tdo, bar, p.col_do + 64 * c, w.hq, r, w.qb + w.nq,
                                 kRaggedWindow);
                 } else {
                     tma_load_3d(smem_u32(smem + C::kQ) + c * 16384, tq, bar, 64 * c, w.q0, bh);
@@ -1405,7 +1406,7 @@ __device__ void dq_producer(const CUtensorMap* tq, const CUtensorMap* tk, const 
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     if constexpr (VARLEN)
-                        tma_load_5d(dst + c * 16384, tk, bar, 64 * c, kvh, kRaggedWindow - w.nk + j * kBT,
+                        tma_load_5d(dst + c * 16384, tk, bar, p.col_k + 64 * c, kvh, kRaggedWindow - w.nk + j * kBT,
                                     w.kb + w.nk, kRaggedWindow);
                     else
                         tma_load_3d(dst + c * 16384, tk, bar, 64 * c, j * kBT, kvh);
@@ -1424,7 +1425,7 @@ __device__ void dq_producer(const CUtensorMap* tq, const CUtensorMap* tk, const 
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     if constexpr (VARLEN)
-                        tma_load_5d(dst + c * 16384, tv, bar, 64 * c, kvh, kRaggedWindow - w.nk + j * kBT,
+                        tma_load_5d(dst + c * 16384, tv, bar, p.col_v + 64 * c, kvh, kRaggedWindow - w.nk + j * kBT,
                                     w.kb + w.nk, kRaggedWindow);
                     else
                         tma_load_3d(dst + c * 16384, tv, bar, 64 * c, j * kBT, kvh);
@@ -2490,9 +2491,9 @@ attn_bwd_wide_dkdv_kernel(const __grid_constant__ CUtensorMap tq64, const __grid
             for (int c = 0; c < kWD / 64; ++c) {
                 if constexpr (VARLEN) {
                     const int r = kRaggedWindow - w.nk + w.k0;
-                    tma_load_5d(smem_u32(smem + C::kK) + c * 16384, &tk, bar, 64 * c, kvh, r, w.kb + w.nk,
+                    tma_load_5d(smem_u32(smem + C::kK) + c * 16384, &tk, bar, p.col_k + 64 * c, kvh, r, w.kb + w.nk,
                                 kRaggedWindow);
-                    tma_load_5d(smem_u32(smem + C::kV) + c * 16384, &tv, bar, 64 * c, kvh, r, w.kb + w.nk,
+                    tma_load_5d(smem_u32(smem + C::kV) + c * 16384, &tv, bar, p.col_v + 64 * c, kvh, r, w.kb + w.nk,
                                 kRaggedWindow);
                 } else {
                     tma_load_3d(smem_u32(smem + C::kK) + c * 16384, &tk, bar, 64 * c, w.k0, kvh);
@@ -2510,11 +2511,11 @@ attn_bwd_wide_dkdv_kernel(const __grid_constant__ CUtensorMap tq64, const __grid
         };
         // the 64-row tile of Q or dO at q0 (packed: rows past the sequence's
         // queries read as zeros)
-        auto load_rows = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int q0, int bh) {
+        auto load_rows = [&](uint32_t dst, const CUtensorMap* map, int col, uint32_t bar, int q0, int bh) {
 #pragma unroll
             for (int c = 0; c < kWD / 64; ++c) {
                 if constexpr (VARLEN)
-                    tma_load_5d(dst + c * 8192, map, bar, 64 * c, bh, kRaggedWindow - w.nq + q0, w.qb + w.nq,
+                    tma_load_5d(dst + c * 8192, map, bar, col + 64 * c, bh, kRaggedWindow - w.nq + q0, w.qb + w.nq,
                                 kRaggedWindow);
                 else
                     tma_load_3d(dst + c * 8192, map, bar, 64 * c, q0, bh);
@@ -2533,7 +2534,7 @@ attn_bwd_wide_dkdv_kernel(const __grid_constant__ CUtensorMap tq64, const __grid
             if (leader) {
                 const uint32_t bar = smem_u32(&bars->q_full[qb]);
                 mbar_arrive_expect_tx(bar, C::kSmall + 2 * kWQ * 4);
-                load_rows(smem_u32(smem + C::kQ + qb * C::kSmall), &tq64, bar, q0, bh);
+                load_rows(smem_u32(smem + C::kQ + qb * C::kSmall), &tq64, p.col_q, bar, q0, bh);
                 const size_t row = VARLEN ? (size_t)bh * p.vstride + (size_t)(w.vbase + q0)
                                           : (size_t)bh * p.Nq_pad + q0;
                 const uint32_t ld = smem_u32(smem + C::kLD + qb * 512);
@@ -2552,7 +2553,7 @@ attn_bwd_wide_dkdv_kernel(const __grid_constant__ CUtensorMap tq64, const __grid
             if (leader) {
                 const uint32_t bar = smem_u32(&bars->do_full);
                 mbar_arrive_expect_tx(bar, C::kSmall);
-                load_rows(smem_u32(smem + C::kDO), &tdo64, bar, q0, bh);
+                load_rows(smem_u32(smem + C::kDO), &tdo64, p.col_do, bar, q0, bh);
             }
             __syncwarp();
             ++ndo;
@@ -2847,9 +2848,9 @@ attn_bwd_wide_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
             for (int c = 0; c < kWD / 64; ++c) {
                 if constexpr (VARLEN) {
                     const int r = kRaggedWindow - w.nq + w.q0;
-                    tma_load_5d(smem_u32(smem + C::kQ) + c * 16384, &tq, bar, 64 * c, qh, r, w.qb + w.nq,
+                    tma_load_5d(smem_u32(smem + C::kQ) + c * 16384, &tq, bar, p.col_q + 64 * c, qh, r, w.qb + w.nq,
                                 kRaggedWindow);
-                    tma_load_5d(smem_u32(smem + C::kDO) + c * 16384, &tdo, bar, 64 * c, qh, r, w.qb + w.nq,
+                    tma_load_5d(smem_u32(smem + C::kDO) + c * 16384, &tdo, bar, p.col_do + 64 * c, qh, r, w.qb + w.nq,
                                 kRaggedWindow);
                 } else {
                     tma_load_3d(smem_u32(smem + C::kQ) + c * 16384, &tq, bar, 64 * c, w.q0, qh);
@@ -2860,11 +2861,11 @@ attn_bwd_wide_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
         __syncwarp();
         // the 64-key tile j of K or V (packed: rows past the sequence's keys
         // read as zeros)
-        auto load_keys = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int j) {
+        auto load_keys = [&](uint32_t dst, const CUtensorMap* map, int col, uint32_t bar, int j) {
 #pragma unroll
             for (int c = 0; c < kWD / 64; ++c) {
                 if constexpr (VARLEN)
-                    tma_load_5d(dst + c * 8192, map, bar, 64 * c, kvh, kRaggedWindow - w.nk + j * kWQ,
+                    tma_load_5d(dst + c * 8192, map, bar, col + 64 * c, kvh, kRaggedWindow - w.nk + j * kWQ,
                                 w.kb + w.nk, kRaggedWindow);
                 else
                     tma_load_3d(dst + c * 8192, map, bar, 64 * c, j * kWQ, kvh);
@@ -2881,7 +2882,7 @@ attn_bwd_wide_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
             if (leader) {
                 const uint32_t bar = smem_u32(&bars->k_full[kb]);
                 mbar_arrive_expect_tx(bar, C::kSmall);
-                load_keys(smem_u32(smem + C::kK + kb * C::kSmall), &tk64, bar, j);
+                load_keys(smem_u32(smem + C::kK + kb * C::kSmall), &tk64, p.col_k, bar, j);
             }
             __syncwarp();
             ++nk;
@@ -2893,7 +2894,7 @@ attn_bwd_wide_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_con
             if (leader) {
                 const uint32_t bar = smem_u32(&bars->v_full);
                 mbar_arrive_expect_tx(bar, C::kSmall);
-                load_keys(smem_u32(smem + C::kV), &tv64, bar, j);
+                load_keys(smem_u32(smem + C::kV), &tv64, p.col_v, bar, j);
             }
             __syncwarp();
             ++nv;
@@ -3135,6 +3136,7 @@ attn_status_t launch_bwd_varlen(const void* q, const void* k, const void* v, con
     p.cu_k = cu_k;
     p.total_q = total_q;
     p.total_k = total_k;
+    p.col_q = p.col_k = p.col_v = p.col_do = p.col_dk = p.col_dv = 0;
     p.vstride = (int)(((size_t)total_q + 132 * (size_t)B + 3) & ~(size_t)3);
     float* lse2 = static_cast<float*>(workspace);
     float* dvec = lse2 + (size_t)Hq * p.vstride;
@@ -3151,20 +3153,20 @@ attn_status_t launch_bwd_varlen(const void* q, const void* k, const void* v, con
         return ATTN_ERR_UNSUPPORTED;
     CUtensorMap tq, tk, tv, tdo;
     attn_status_t st;
-    if ((st = encode_tmap_ragged(&tq, q, false, d, Hq, 64, kBT, true)) != ATTN_OK) return st;
-    if ((st = encode_tmap_ragged(&tk, k, false, d, Hkv, 64, kBT, true)) != ATTN_OK) return st;
-    if ((st = encode_tmap_ragged(&tv, v, false, d, Hkv, 64, kBT, true)) != ATTN_OK) return st;
-    if ((st = encode_tmap_ragged(&tdo, dout, false, d, Hq, 64, kBT, true)) != ATTN_OK) return st;
+    if ((st = encode_tmap_ragged(&tq, &p.col_q, q, total_q, false, d, Hq, 64, kBT, true)) != ATTN_OK) return st;
+    if ((st = encode_tmap_ragged(&tk, &p.col_k, k, total_k, false, d, Hkv, 64, kBT, true)) != ATTN_OK) return st;
+    if ((st = encode_tmap_ragged(&tv, &p.col_v, v, total_k, false, d, Hkv, 64, kBT, true)) != ATTN_OK) return st;
+    if ((st = encode_tmap_ragged(&tdo, &p.col_do, dout, total_q, false, d, Hq, 64, kBT, true)) != ATTN_OK) return st;
     const int o_f32 = o_dtype == ATTN_OUT_F32;
     const bool g32 = grad_dtype == ATTN_OUT_F32;
     if (d > 128) {
         // 64-row boxes for the streamed tiles of the wide passes
         if ((long long)B * Hkv * p.n_kt * 2 >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
         CUtensorMap tq64, tk64, tv64, tdo64;
-        if ((st = encode_tmap_ragged(&tq64, q, false, d, Hq, 64, kWQ, true)) != ATTN_OK) return st;
-        if ((st = encode_tmap_ragged(&tk64, k, false, d, Hkv, 64, kWQ, true)) != ATTN_OK) return st;
-        if ((st = encode_tmap_ragged(&tv64, v, false, d, Hkv, 64, kWQ, true)) != ATTN_OK) return st;
-        if ((st = encode_tmap_ragged(&tdo64, dout, false, d, Hq, 64, kWQ, true)) != ATTN_OK) return st;
+        if ((st = encode_tmap_ragged(&tq64, &p.col_q, q, total_q, false, d, Hq, 64, kWQ, true)) != ATTN_OK) return st;
+        if ((st = encode_tmap_ragged(&tk64, &p.col_k, k, total_k, false, d, Hkv, 64, kWQ, true)) != ATTN_OK) return st;
+        if ((st = encode_tmap_ragged(&tv64, &p.col_v, v, total_k, false, d, Hkv, 64, kWQ, true)) != ATTN_OK) return st;
+        if ((st = encode_tmap_ragged(&tdo64, &p.col_do, dout, total_q, false, d, Hq, 64, kWQ, true)) != ATTN_OK) return st;
         return g32 ? launch_bwd_wide_t<true, true>(tq, tk, tv, tdo, tq64, tk64, tv64, tdo64, p, o, o_f32,
                                                    dout, lse, lse2, dvec, stream, dev)
                    : launch_bwd_wide_t<false, true>(tq, tk, tv, tdo, tq64, tk64, tv64, tdo64, p, o, o_f32,
@@ -3174,8 +3176,8 @@ attn_status_t launch_bwd_varlen(const void* q, const void* k, const void* v, con
     // rows x 128 bytes (64 bf16 or 32 fp32 columns)
     CUtensorMap tdk = tq, tdv = tq;
     if (pad_head_dim(d) == 128) {
-        if ((st = encode_tmap_ragged(&tdk, dk, g32, d, Hkv, g32 ? 32 : 64, 32, true)) != ATTN_OK) return st;
-        if ((st = encode_tmap_ragged(&tdv, dv, g32, d, Hkv, g32 ? 32 : 64, 32, true)) != ATTN_OK) return st;
+        if ((st = encode_tmap_ragged(&tdk, &p.col_dk, dk, total_k, g32, d, Hkv, g32 ? 32 : 64, 32, true)) != ATTN_OK) return st;
+        if ((st = encode_tmap_ragged(&tdv, &p.col_dv, dv, total_k, g32, d, Hkv, g32 ? 32 : 64, 32, true)) != ATTN_OK) return st;
     }
     auto launch = [&](auto dim, auto out32, auto with_bias) {
         return launch_bwd_t<decltype(dim)::value, decltype(out32)::value, true, decltype(with_bias)::value>(
@@ -3234,6 +3236,7 @@ attn_status_t launch_bwd(const void* q, const void* k, const void* v, const void
     p.dv = dv;
     p.cu_q = p.cu_k = nullptr;
     p.total_q = p.total_k = p.vstride = 0;
+    p.col_q = p.col_k = p.col_v = p.col_do = p.col_dk = p.col_dv = 0;
     p.bias = bias ? *bias : BiasArgs{};
     p.queue = bias ? reinterpret_cast<unsigned int*>(dvec + rows) : nullptr;
     p.partial = dvec + rows + 4;

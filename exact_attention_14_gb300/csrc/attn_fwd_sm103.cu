@@ -102,6 +102,7 @@ struct FwdParams {
     const int* cu_q;  // [B + 1] row offsets of the sequences in the packed Q / O
     const int* cu_k;  // [B + 1] row offsets in the packed K / V
     int total_q, total_k;
+    int col_q, col_k, col_v;   // the maps' first columns
     BiasArgs bias;    // the BIAS instantiations
 };
 
@@ -300,7 +301,7 @@ __device__ void run_producer(const CUtensorMap* tq, const CUtensorMap* tk, const
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     if constexpr (VARLEN)
-                        tma_load_5d(dst + c * 16384, tq, bar, 64 * c, hq, kRaggedWindow - nq + row,
+                        tma_load_5d(dst + c * 16384, tq, bar, p.col_q + 64 * c, hq, kRaggedWindow - nq + row,
                                     q0 + nq, kRaggedWindow);
                     else
                         tma_load_3d(dst + c * 16384, tq, bar, 64 * c, row, bh);
@@ -326,7 +327,7 @@ __device__ void run_producer(const CUtensorMap* tq, const CUtensorMap* tk, const
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c) {
                         if constexpr (VARLEN)
-                            tma_load_5d(dst + c * 16384, map, bar, 64 * c, hq / p.group,
+                            tma_load_5d(dst + c * 16384, map, bar, (which == 0 ? p.col_k : p.col_v) + 64 * c, hq / p.group,
                                         kRaggedWindow - nk + kTileN * j, k0 + nk, kRaggedWindow);
                         else
                             tma_load_3d(dst + c * 16384, map, bar, 64 * c, kTileN * j, bkv);
@@ -1152,6 +1153,7 @@ attn_status_t launch_fwd(const void* q, const void* k, const void* v, void* o, f
     p.split = plan_tail_split(p.shape, dev.num_sms);
     p.cu_q = p.cu_k = nullptr;
     p.total_q = p.total_k = 0;
+    p.col_q = p.col_k = p.col_v = 0;
     p.bias = bias ? *bias : BiasArgs{};
     const uint32_t items = split_items(p.split);
     const int grid = (int)(items < (uint32_t)dev.num_sms ? items : (uint32_t)dev.num_sms);
@@ -1214,12 +1216,13 @@ attn_status_t launch_fwd_varlen(const void* q, const void* k, const void* v, voi
     CUtensorMap tq, tk, tv, to;
     attn_status_t st;
     const bool f32 = o_dtype == ATTN_OUT_F32;
-    if ((st = encode_tmap_ragged(&tq, q, false, d, Hq, 64, kTileM, true)) != ATTN_OK) return st;
-    if ((st = encode_tmap_ragged(&tk, k, false, d, Hkv, 64, kTileN, true)) != ATTN_OK) return st;
-    if ((st = encode_tmap_ragged(&tv, v, false, d, Hkv, 64, kTileN, true)) != ATTN_OK) return st;
+    if ((st = encode_tmap_ragged(&tq, &p.col_q, q, total_q, false, d, Hq, 64, kTileM, true)) != ATTN_OK) return st;
+    if ((st = encode_tmap_ragged(&tk, &p.col_k, k, total_k, false, d, Hkv, 64, kTileN, true)) != ATTN_OK) return st;
+    if ((st = encode_tmap_ragged(&tv, &p.col_v, v, total_k, false, d, Hkv, 64, kTileN, true)) != ATTN_OK) return st;
     // (O of a packed batch is written from registers, never by this map; it
     // is still encoded, which checks O's alignment like the other maps)
-    if ((st = encode_tmap_ragged(&to, o, f32, d, Hq, kEpiCols(f32), 32, false)) != ATTN_OK) return st;
+    int col_o;
+    if ((st = encode_tmap_ragged(&to, &col_o, o, total_q, f32, d, Hq, kEpiCols(f32), 32, false)) != ATTN_OK) return st;
     auto launch = [&](auto dim, auto out32, auto with_bias) {
         return launch_fwd_t<decltype(dim)::value, decltype(out32)::value, true, decltype(with_bias)::value>(
             tq, tk, tv, to, lse, p, grid, stream, dev);

@@ -86,6 +86,7 @@ struct WideParams {
     const int* cu_q;  // [B + 1] row offsets in the packed Q / O
     const int* cu_k;  // [B + 1] row offsets in the packed K / V
     int total_q, total_k;
+    int col_q, col_k, col_v;   // the maps' first columns
 };
 
 constexpr uint32_t kWideQueueSlots = 256;
@@ -232,7 +233,7 @@ __device__ void wide_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 if constexpr (VARLEN)
-                    tma_load_5d(smem_u32(smem) + c * (kWM * 128), tq, bar, 64 * c, hq,
+                    tma_load_5d(smem_u32(smem) + c * (kWM * 128), tq, bar, p.col_q + 64 * c, hq,
                                 kRaggedWindow - nq + mt * kWM, q0 + nq, kRaggedWindow);
                 else
                     tma_load_3d(smem_u32(smem) + c * (kWM * 128), tq, bar, 64 * c, mt * kWM, bh);
@@ -256,7 +257,7 @@ __device__ void wide_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
                     const int pieces = C::kKChunkBytes(c) / (kWN * 128);
                     for (int pc = 0; pc < pieces; ++pc) {
                         if constexpr (VARLEN)
-                            tma_load_5d(dst + pc * (kWN * 128), tk, bar, 128 * c + 64 * pc, kvh,
+                            tma_load_5d(dst + pc * (kWN * 128), tk, bar, p.col_k + 128 * c + 64 * pc, kvh,
                                         kRaggedWindow - nk + j * kWN, k0 + nk, kRaggedWindow);
                         else
                             tma_load_3d(dst + pc * (kWN * 128), tk, bar, 128 * c + 64 * pc, j * kWN, kvh);
@@ -280,7 +281,7 @@ __device__ void wide_producer(const CUtensorMap* tq, const CUtensorMap* tk, cons
 #pragma unroll
                     for (int pc = 0; pc < D / 64; ++pc) {
                         if constexpr (VARLEN)
-                            tma_load_5d(dst + pc * (kWV * 128), tv, bar, 64 * pc, kvh,
+                            tma_load_5d(dst + pc * (kWV * 128), tv, bar, p.col_v + 64 * pc, kvh,
                                         kRaggedWindow - nk + j * kWN + kWV * h, k0 + nk, kRaggedWindow);
                         else
                             tma_load_3d(dst + pc * (kWV * 128), tv, bar, 64 * pc, j * kWN + kWV * h, kvh);
@@ -769,12 +770,13 @@ attn_status_t launch_fwd_wide_varlen(const void* q, const void* k, const void* v
     CUtensorMap tq, tk, tv, to;
     attn_status_t st;
     const bool f32 = o_dtype == ATTN_OUT_F32;
-    if ((st = encode_tmap_ragged(&tq, q, false, d, Hq, 64, kWM, true)) != ATTN_OK) return st;
-    if ((st = encode_tmap_ragged(&tk, k, false, d, Hkv, 64, kWN, true)) != ATTN_OK) return st;
-    if ((st = encode_tmap_ragged(&tv, v, false, d, Hkv, 64, kWV, true)) != ATTN_OK) return st;
+    if ((st = encode_tmap_ragged(&tq, &p.col_q, q, total_q, false, d, Hq, 64, kWM, true)) != ATTN_OK) return st;
+    if ((st = encode_tmap_ragged(&tk, &p.col_k, k, total_k, false, d, Hkv, 64, kWN, true)) != ATTN_OK) return st;
+    if ((st = encode_tmap_ragged(&tv, &p.col_v, v, total_k, false, d, Hkv, 64, kWV, true)) != ATTN_OK) return st;
     // (O is written from registers, never by this map; it is still encoded,
     // which checks O's alignment like the other maps)
-    if ((st = encode_tmap_ragged(&to, o, f32, d, Hq, wide_epi_cols(f32), 32, false)) != ATTN_OK) return st;
+    int col_o;
+    if ((st = encode_tmap_ragged(&to, &col_o, o, total_q, f32, d, Hq, wide_epi_cols(f32), 32, false)) != ATTN_OK) return st;
     if (d <= 192)
         return f32 ? launch_wide_t<192, true, true>(tq, tk, tv, to, lse, p, grid, stream, dev)
                    : launch_wide_t<192, false, true>(tq, tk, tv, to, lse, p, grid, stream, dev);

@@ -61,8 +61,9 @@ attn_status_t encode_tmap_pages(CUtensorMap* map, const void* base, bool e4m3, i
 // outputs) addressed per sequence: see the ragged layout in fwd_sched.h.  Box of
 // box_cols x 1 head x box_rows rows; 128-byte swizzle for the operand loads,
 // none for the staged output stores.
-attn_status_t encode_tmap_ragged(CUtensorMap* map, const void* base, bool f32, int d, int heads,
-                                 int box_cols, int box_rows, bool swizzle128);
+// The array's first column is column *col of the map; rows: of the packed array.
+attn_status_t encode_tmap_ragged(CUtensorMap* map, int* col, const void* base, int rows, bool f32, int d,
+                                 int heads, int box_cols, int box_rows, bool swizzle128);
 
 // 3-D uint8 tensor map over [heads, rows, inner] with a row pitch in bytes
 // (a multiple of 16), 128-byte-swizzled box of box_inner x box_rows x 1.
