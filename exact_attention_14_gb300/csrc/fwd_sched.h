@@ -220,6 +220,7 @@ GB300_HD void unit_of(const FwdShape& s, uint32_t i, int& bh, int& mb) {
 // r = W - L + row, e = s + L, f = W with W = 2^30: the f term is
 // W*2^34 - W*rs = 2^64 - W*rs, so the address is base + (s + row)*rs, and
 // r < W (the extent of r) holds exactly when row < L.
+// (The columns c may start at an offset, see encode_tmap_ragged.)
 constexpr int kRaggedWindow = 1 << 30;     // W: extent of r, and the f coordinate
 constexpr unsigned kRaggedOuterExtent = 0x7FFFFFFFu;  // extents of e and f (> W)
 
