@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kPagesThreads = 256;
 constexpr int kPagesMaxRequests = 4096;
-constexpr int kPoolHeader = 4;       // count, blocks arrived, two words unused
+constexpr int kPoolHeader = 4;       // count, blocks arrived, whether one saw a bad page, one word unused
 constexpr int kTokensPerThread = 4;  // two 16-byte stores of slots, one of positions
 
 __device__ __forceinline__ int sat_add(int a, int b) {   // of numbers >= 0
@@ -244,7 +244,9 @@ attn_pages_extend_kernel(const ExtendArgs a, unsigned int* err) {
 // Request b gives back the pages past its first keep_b tokens.  Freed page i (in
 // the order of the requests, and of each one's table) becomes entry count + F - 1 -
 // i of the stack, F of them in all, so a step's pages given back go out again in the
-// same order.
+// same order.  What lies past the stack's count means nothing, so the pages are
+// written there while they are checked, and the last block counts them in, or, where
+// one of them was no page of the cache, leaves the call without effect.
 __global__ void __launch_bounds__(kPagesThreads)
 attn_pages_trim_kernel(int* pool, int num_blocks, const int* block_table, int* seqlens, const int* keep_lens,
                        int B, int max_blocks, int page_size, unsigned int* err) {
@@ -287,18 +289,24 @@ attn_pages_trim_kernel(int* pool, int num_blocks, const int* block_table, int* s
             const int b = find(freed, B, i);
             lens(b, now, keep);
             const int page = __ldg(block_table + (size_t)b * max_blocks + pages_of(keep, page_size) + (i - freed[b]));
-            bad |= (unsigned)page >= (unsigned)num_blocks;
+            if ((unsigned)page >= (unsigned)num_blocks) {
+                bad = true;
+                atomicExch(pool + 2, 1);
+                __threadfence();   // (seen by the last block, which this one's arrival follows)
+            }
             stack[count + all - 1 - i] = page;
         }
     }
     if (bad) atomicOr(err, kErrBadSeqlen);
     if (!last_block(pool)) return;
-    if (fits) {
+    const bool all_pages = *reinterpret_cast<volatile int*>(pool + 2) == 0;
+    __syncthreads();   // (before the word is cleared)
+    if (fits && all_pages) {
         for (int b = tid; b < B; b += kPagesThreads)
             if (lens(b, now, keep) && keep < now) seqlens[b] = keep;
         if (tid == 0) pool[0] = count + all;
     }
-    if (tid == 0) pool[1] = 0;
+    if (tid == 0) pool[1] = pool[2] = 0;
 }
 
 __global__ void __launch_bounds__(kPagesThreads) attn_pages_init_kernel(int* pool, int num_blocks) {

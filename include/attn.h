@@ -764,9 +764,10 @@ attn_status_t attn_pages_extend(int* pool, int num_blocks, int* block_table, int
  * tokens that were not accepted, or (0) a finished request; the pages past the kept
  * tokens go back on the pool, such that the pages of an attn_pages_extend given
  * back at once come out again in the same order.  block_table is not written.
- * More pages than the cache has (some given back twice) leave everything as it
- * was, and a length outside [0, max_blocks * page_size] leaves that request as
- * it was; attn_last_device_error() then reports ATTN_ERR_INVALID_ARG.
+ * More pages than the cache has (some given back twice), or an entry to give back
+ * outside [0, num_blocks), leave everything as it was, and a length outside [0,
+ * max_blocks * page_size] leaves that request as it was; attn_last_device_error()
+ * then reports ATTN_ERR_INVALID_ARG.
  */
 attn_status_t attn_pages_trim(int* pool, int num_blocks, const int* block_table, int* seqlens,
                               const int* keep_lens, int B, int max_blocks, int page_size, void* stream);
