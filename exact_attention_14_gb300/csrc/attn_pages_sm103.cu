@@ -136,10 +136,30 @@ attn_pages_extend_kernel(const ExtendArgs a, unsigned int* err) {
     }
     int all_rows, all_want;
     r = block_scan(r, warp_sums, all_rows);
+    // packed rows for fewer tokens: from the first request whose tokens end past them on,
+    // new tokens count as none (`at`: the sum with them, which says which requests these are)
+    const int limit = a.width > 0 ? 0x7FFFFFFF : a.total;
+    int at = r;
+    if (all_rows > limit) {
+        bad = true;
+        r = w = 0;
+        int end = at;
+        for (int b = b0; b < b1; ++b) {
+            int len, add;
+            request(a, b, len, add);
+            end = sat_add(end, add);
+            if (end > limit) add = 0;
+            r += add;
+            w = sat_add(w, pages_of(len + add, a.page_size) - pages_of(len, a.page_size));
+        }
+        r = block_scan(r, warp_sums, all_rows);
+    }
     w = block_scan(w, warp_sums, all_want);
     for (int b = b0; b < b1; ++b) {
         int len, add;
         request(a, b, len, add);
+        at = sat_add(at, add);
+        if (at > limit) add = 0;
         rows[b] = r;
         want[b] = w;
         r = sat_add(r, add);
@@ -150,7 +170,6 @@ attn_pages_extend_kernel(const ExtendArgs a, unsigned int* err) {
         want[a.B] = all_want;
     }
     __syncthreads();
-    bad |= a.width == 0 && all_rows > a.total;
     auto given = [&](int b) { return want[b + 1] == want[b] || want[b + 1] <= count; };
     const int* stack = a.pool + kPoolHeader;
 

@@ -749,10 +749,10 @@ attn_status_t attn_page_pool_init(int* pool, int num_blocks, void* stream);
  * page * page_size + position % page_size; rows past a request's tokens, or past
  * every request, have slot -1 and position 0.
  * A request with a negative length, more than max_blocks * page_size tokens or (in
- * padded rows) more than width new ones counts as new_lens[b] = 0, and rows past
- * `total` are not written; attn_last_device_error() then reports
- * ATTN_ERR_INVALID_ARG, as it does for a page outside [0, num_blocks) (its slots
- * are -1).
+ * padded rows) more than width new ones counts as new_lens[b] = 0, and so does, in
+ * packed rows, every request with new tokens from the first one whose rows end past
+ * `total`; attn_last_device_error() then reports ATTN_ERR_INVALID_ARG, as it does for
+ * a page outside [0, num_blocks) (its slots are -1).
  */
 attn_status_t attn_pages_extend(int* pool, int num_blocks, int* block_table, int* seqlens,
                                 const int* new_lens, long long* slots, int* positions, int* cu_seqlens,

@@ -50,3 +50,82 @@ def test_trim_of_what_is_no_page(B, max_blocks, bad):
     slots, _, granted = ea.pages_extend(pool, table, seqlens, _int(new), page, width=60)
     assert granted.tolist() == new and (slots >= 0).sum() == sum(new)
     assert ea.attn_last_device_error() == 0
+
+
+def _packed(new, total, page=16, blocks=40, max_blocks=8, held=None):
+    """One packed extend: (slots with a guard behind them, positions, cu_seqlens, granted,
+    lengths, free pages, the tables)."""
+    B = len(new)
+    pool = ea.page_pool(blocks)
+    table = torch.full((B, max_blocks), -1, dtype=torch.int32, device="cuda")
+    seqlens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    if held is not None:
+        ea.pages_extend(pool, table, seqlens, _int(held), page, total=sum(held))
+    slots = torch.full((total + 4,), 77, dtype=torch.int64, device="cuda")
+    pos = torch.full((total + 4,), 77, dtype=torch.int32, device="cuda")
+    cu, granted = torch.empty(B + 1, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+    ea.attn_pages_extend(pool, table, seqlens, _int(new), page, slots[:total], pos[:total], cu, granted)
+    assert (slots[total:] == 77).all() and (pos[total:] == 77).all()
+    return slots[:total].tolist(), pos[:total].tolist(), cu.tolist(), granted.tolist(), seqlens.tolist(), pool, table
+
+
+def test_packed_rows_for_fewer_tokens():
+    """From the first request whose tokens end past the rows on, new tokens count as none: no
+    length holds a token without a slot, and no page is taken for one."""
+    held = [5, 0, 30, 16, 1]
+    slots, pos, cu, granted, lens, pool, table = _packed([4, 0, 20, 1, 0], 10, held=held)
+    _reported()
+    # (held: page 0 for request 0, 1 and 2 for request 2, 3 for request 3, 4 for request 4)
+    assert slots == [5, 6, 7, 8] + [-1] * 6 and pos == [5, 6, 7, 8] + [0] * 6
+    assert cu == [0, 4, 4, 4, 4, 4] and granted == [4, 0, 0, 0, 0]
+    assert lens == [9, 0, 30, 16, 1] and pool[0] == 35 and (table[3, 1:] == -1).all()
+    # the same with a row more than all of them need, and with as many
+    for total in (26, 25):
+        slots, pos, cu, granted, lens, pool, _ = _packed([4, 0, 20, 1, 0], total, held=held)
+        assert ea.attn_last_device_error() == 0
+        assert cu == [0, 4, 4, 24, 25, 25] and granted == [4, 0, 20, 1, 0] and lens == [9, 0, 50, 17, 1]
+        assert (-1 in slots) == (total == 26) and pool[0] == 35 - 3
+    # one row short: the last request that has any gets none
+    slots, pos, cu, granted, lens, pool, _ = _packed([4, 0, 20, 1, 0], 24, held=held)
+    _reported()
+    assert cu == [0, 4, 4, 24, 24, 24] and granted == [4, 0, 20, 0, 0] and lens == [9, 0, 50, 16, 1]
+    assert -1 not in slots and pool[0] == 35 - 2
+    # no rows at all
+    slots, pos, cu, granted, lens, pool, _ = _packed([4, 0, 20, 1, 0], 0, held=held)
+    _reported()
+    assert cu == [0] * 6 and granted == [0] * 5 and lens == held and pool[0] == 35
+
+
+def test_packed_rows_and_pages_that_both_run_out():
+    """Rows end at request 3, pages at request 1: what is served fits both."""
+    slots, pos, cu, granted, lens, pool, _ = _packed([16, 40, 10, 50], 70, blocks=3)
+    _reported()
+    assert cu == [0, 16, 56, 66, 66] and granted == [16, 0, 0, 0] and lens == [16, 0, 0, 0]
+    assert slots == list(range(16)) + [-1] * 54 and pool[0] == 2
+
+
+@pytest.mark.parametrize("B", [257, 2000])
+def test_packed_rows_of_many_requests(B):
+    """Several requests a thread: the border lies inside a thread's share, and past it."""
+    new = [(7 * b) % 5 for b in range(B)]
+    ends = torch.tensor(new).cumsum(0).tolist()
+    for at in (0, 1, B // 3, B - 2):
+        total = ends[at] + 1        # (below the next request with 2 or more tokens' end)
+        fits = [e <= total for e in ends]
+        want = [n if ok else 0 for n, ok in zip(new, fits)]
+        slots, pos, cu, granted, lens, pool, _ = _packed(want, total, blocks=2 * B)
+        assert ea.attn_last_device_error() == 0
+        got = _packed(new, total, blocks=2 * B)
+        _reported()
+        assert got[:5] == (slots, pos, cu, granted, lens) and torch.equal(got[5], pool)
+        assert granted == want and lens == want and cu[-1] == sum(want)
+
+
+def test_packed_sums_past_31_bits():
+    """Requests of 2^24 tokens, one page each: the sums pass 2^31, lengths and pages do not
+    drift apart."""
+    page, B = 1 << 24, 200
+    slots, pos, cu, granted, lens, pool, table = _packed([page] * B, 50, page=page, blocks=B, max_blocks=1)
+    _reported()
+    assert lens == [0] * B and granted == [0] * B and cu == [0] * (B + 1)
+    assert pool[0] == B and (table == -1).all() and slots == [-1] * 50
