@@ -27,7 +27,7 @@ __all__ = [
     "attn_decode",
     "attn_decode_workspace_size", "attn_decode_noalloc", "attn_status_string", "attn_last_device_error",
     "attn_decode_num_splits", "attn_list_schedule", "attn_kv_tiles",
-    "attn_fwd_num_units", "attn_fwd_schedule", "attn_fwd_split_plan", "attn_decode_kernel_launches",
+    "attn_fwd_num_units", "attn_fwd_schedule", "attn_fwd_split_plan", "attn_packed_map_shift", "attn_decode_kernel_launches",
     "attn_bwd", "attn_bwd_workspace_size", "backward", "attn_bwd_varlen",
     "attn_bwd_varlen_workspace_size", "backward_varlen", "attn_decode_paged", "decode_paged", "forward", "decode", "library_path", "load",
     "attn_rope", "rope", "rope_backward", "attn_rope_frequencies", "rope_frequencies",
@@ -133,6 +133,7 @@ SIGNATURES = {
     "attn_page_pool_init": (_c_int, [_vp, _c_int, _vp]),
     "attn_pages_extend": (_c_int, [_vp, _c_int] + [_vp] * 7 + [_c_int] * 5 + [_vp]),
     "attn_pages_trim": (_c_int, [_vp, _c_int] + [_vp] * 3 + [_c_int] * 3 + [_vp]),
+    "attn_packed_map_shift": (_c_ll, [ctypes.c_ulonglong, _c_ll, _c_ll]),
     "attn_fwd_split_plan": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
                                      _c_int, ctypes.POINTER(ctypes.c_int),
                                      ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]),
@@ -761,6 +762,15 @@ def attn_fwd_split_plan(B, Hq, Hkv, Nq, Nk, d, causal, num_sms):
     if rc != 0:
         raise ValueError("attn_fwd_split_plan rejected its arguments")
     return tuple(o.value for o in out)
+
+
+def attn_packed_map_shift(address: int, rows: int, row_bytes: int) -> int:
+    """Bytes below a packed array (rows of row_bytes bytes at address) at which its
+    tensor map begins: 0, or 256 KB."""
+    n = int(load().attn_packed_map_shift(address, rows, row_bytes))
+    if n < 0:
+        raise ValueError("attn_packed_map_shift rejected its arguments")
+    return n
 
 
 def attn_decode_kernel_launches(B, Hq, Hkv, Nmax, d, num_splits=0) -> int:

@@ -148,21 +148,28 @@ attn_status_t encode_tmap_f32_sw128_3d(CUtensorMap* map, void* base, int d, int 
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+// Bytes below a packed array at which its map begins.  Rows outside a sequence are filled
+// with zeros, but for these maps (not for dense ones) the hardware looks at memory that lies
+// 64 to 128 KB past the map's base: a shorter array that begins near the end of its 2 MB
+// block (the unit in which device memory is mapped) gets a map that begins 256 KB lower,
+// and its columns start that far on.  (A 9 KB array 25 KB before the end of what was mapped
+// gave an invalid access.  The reach is an observation, on pages of host memory that
+// became resident: the same for rows of 16 bytes to 512 KB, head dims 8 to 256, boxes of 64 and
+// 128 rows of bf16, sequences of 0 to 500 rows; never for the stores of gradients, bf16 or
+// fp32.  256 KB is twice what was seen.)
+static uintptr_t packed_map_shift(uintptr_t at, long long rows, size_t row_bytes) {
+    constexpr uintptr_t kReach = 256 << 10, kBlock = 2 << 20;
+    return (unsigned long long)rows * row_bytes < kReach && at % kBlock > kBlock - kReach ? kReach : 0;
+}
+
 attn_status_t encode_tmap_ragged(CUtensorMap* map, int* col, const void* base, int rows, bool f32, int d,
                                  int heads, int box_cols, int box_rows, bool swizzle128) {
     if (!load_encoder()) return ATTN_ERR_CUDA;
     const cuuint64_t es = f32 ? 4 : 2;
     const cuuint64_t rs = (cuuint64_t)heads * d * es;  // row stride (bytes)
     if (rs >= (1ull << 34)) return ATTN_ERR_UNSUPPORTED;
-    // Rows outside a sequence are filled with zeros, but for these maps (not for dense
-    // ones) the hardware looks at memory up to 128 KB past the map's base: a shorter array
-    // that begins near the end of its 2 MB block (the unit in which device memory is
-    // mapped) gets a map that begins 256 KB lower, and its columns start that far on.
-    // (Seen on pages of host memory becoming resident.  A 9 KB array 25 KB before the
-    // end of what was mapped gave an invalid access.)
-    constexpr uintptr_t kReach = 256 << 10, kBlock = 2 << 20;
     const uintptr_t at = reinterpret_cast<uintptr_t>(base);
-    const uintptr_t lower = (cuuint64_t)rows * rs < kReach && at % kBlock > kBlock - kReach ? kReach : 0;
+    const uintptr_t lower = packed_map_shift(at, rows, rs);
     *col = (int)(lower / es);
     cuuint64_t dims[5] = {(cuuint64_t)(d + *col), (cuuint64_t)heads, (cuuint64_t)kRaggedWindow,
                           (cuuint64_t)kRaggedOuterExtent, (cuuint64_t)kRaggedOuterExtent};
@@ -1138,6 +1145,11 @@ int attn_fwd_schedule(int B, int Hq, int Hkv, int Nq, int Nk, int d, int causal,
         if (cost_out) cost_out[i] = tile_kv_count(mb, 0, s) + tile_kv_count(mb, 1, s);
     }
     return 0;
+}
+
+long long attn_packed_map_shift(unsigned long long address, long long rows, long long row_bytes) {
+    if (rows < 1 || rows > kMaxPackedRows || row_bytes < 1 || row_bytes >= (1ll << 34)) return -1;
+    return (long long)packed_map_shift((uintptr_t)address, rows, (size_t)row_bytes);
 }
 
 int attn_fwd_split_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d, int causal, int num_sms,

@@ -857,6 +857,15 @@ int attn_fwd_split_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d, int causa
                         int* n_full, int* n_split, int* parts);
 
 /*
+ * How many bytes below a packed array (attn_fwd_varlen's Q, K, V and the like) of
+ * `rows` rows of `row_bytes` bytes at `address` its tensor map begins: 256 KB for an
+ * array shorter than that which begins in the last 256 KB of a 2 MB block of memory
+ * (the map's loads may look at up to 128 KB past its beginning, which would
+ * lie past the block), else 0.  -1 on a bad argument.
+ */
+long long attn_packed_map_shift(unsigned long long address, long long rows, long long row_bytes);
+
+/*
  * attn_selftest_bounded_wait -- diagnostic of the kernels' bounded waits (every
  * spin in the library's kernels gives up after 2 s, records ATTN_ERR_TIMEOUT in
  * the device error word, and lets the context carry on).  One CTA waits, with
