@@ -9,13 +9,14 @@
 // (P_b + need_b > count) gets none; every later one that needs a page does not
 // either, so the pages given are the first max(P_b + need_b) of the stack.
 //
-// Each block takes the prefix sums itself (at most 4096 requests, two loads each:
-// cheaper than a second launch), then a share of the tokens and pages; which
-// request a token or page belongs to is a binary search in shared memory.  The
-// lengths and the stack's count change only when every block has read them: the
-// last to arrive, counted in the pool's second word, writes them.  Bound by latency
-// (12 bytes a token leave): in a graph an extend and a trim take 8.9 us together for 16
-// requests of a token, 20.1 for 512 prompts of 17..4096 tokens, a million in all.
+// Each block takes the prefix sums itself (at most 4096 requests, two loads each for the
+// sums, and again where they go to shared memory: cheaper than a second launch), then a
+// share of the tokens and pages; which request a token or page belongs to is a binary
+// search in shared memory.  The lengths and the stack's count change only when every
+// block has read them: the last to arrive, counted in the pool's second word, writes
+// them.  Bound by latency (12 bytes a token leave): in a graph an extend and a trim take
+// 8.5 us together for 16 requests of a token, 21.9 for 512 prompts of 17..4105 tokens, a
+// million in all.
 #include <cstdint>
 
 #include "internal.h"
@@ -26,7 +27,7 @@ namespace {
 
 constexpr int kPagesThreads = 256;
 constexpr int kPagesMaxRequests = 4096;
-constexpr int kPoolHeader = 4;       // count, blocks arrived, whether one saw a bad page, one word unused
+constexpr int kPoolHeader = 4;       // count, blocks arrived, two words unused
 constexpr int kTokensPerThread = 4;  // two 16-byte stores of slots, one of positions
 
 __device__ __forceinline__ int sat_add(int a, int b) {   // of numbers >= 0
@@ -71,21 +72,23 @@ __device__ __forceinline__ int find(const int* prefix, int n, int i) {
     return lo;
 }
 
-// Whether this block is the launch's last to get here (uniform over its threads).
+// Whether this block is the launch's last to get here (uniform over its threads; at most
+// 65535 blocks).  `flag`, of all threads alike: set on return if a block came with it set.
 // What the block read before is not read after, so the last one may overwrite it.
-__device__ __forceinline__ bool last_block(int* pool) {
-    __shared__ bool last;
-    __syncthreads();
+__device__ __forceinline__ bool last_block(int* pool, bool& flag) {
+    __shared__ unsigned int seen;   // blocks before this one, and above them how many had it set
     if (threadIdx.x == 0) {
-        last = gridDim.x == 1;
-        if (!last) {
+        const unsigned int mine = flag ? 1u << 16 : 0u;
+        seen = mine;
+        if (gridDim.x > 1) {
             __threadfence();
-            last = atomicAdd(reinterpret_cast<unsigned int*>(pool) + 1, 1u) == gridDim.x - 1;
+            seen = atomicAdd(reinterpret_cast<unsigned int*>(pool) + 1, 1u + mine) + mine;
             __threadfence();
         }
     }
     __syncthreads();
-    return last;
+    flag = seen >> 16;
+    return (seen & 0xFFFFu) == gridDim.x - 1;
 }
 
 struct ExtendArgs {
@@ -136,6 +139,7 @@ attn_pages_extend_kernel(const ExtendArgs a, unsigned int* err) {
     }
     int all_rows, all_want;
     r = block_scan(r, warp_sums, all_rows);
+    w = block_scan(w, warp_sums, all_want);
     // packed rows for fewer tokens: from the first request whose tokens end past them on,
     // new tokens count as none (`at`: the sum with them, which says which requests these are)
     const int limit = a.width > 0 ? 0x7FFFFFFF : a.total;
@@ -153,8 +157,8 @@ attn_pages_extend_kernel(const ExtendArgs a, unsigned int* err) {
             w = sat_add(w, pages_of(len + add, a.page_size) - pages_of(len, a.page_size));
         }
         r = block_scan(r, warp_sums, all_rows);
+        w = block_scan(w, warp_sums, all_want);
     }
-    w = block_scan(w, warp_sums, all_want);
     for (int b = b0; b < b1; ++b) {
         int len, add;
         request(a, b, len, add);
@@ -241,7 +245,9 @@ attn_pages_extend_kernel(const ExtendArgs a, unsigned int* err) {
             for (int b = tid; b <= a.B; b += kPagesThreads) a.cu_seqlens[b] = rows[b];
     }
     if (bad) atomicOr(err, kErrBadSeqlen);
-    if (!last_block(a.pool)) return;
+    bool no_flag = false;
+    __syncthreads();
+    if (!last_block(a.pool, no_flag)) return;
     int taken = 0;
     for (int b = tid; b < a.B; b += kPagesThreads) {
         if (!given(b)) continue;
@@ -302,30 +308,26 @@ attn_pages_trim_kernel(int* pool, int num_blocks, const int* block_table, int* s
     // more pages than the cache has: some were given back twice; nothing is done
     const bool fits = count >= 0 && count <= num_blocks && all <= num_blocks - count;
     bad |= !fits;
+    bool no_page = false;
     if (fits) {
         int* stack = pool + kPoolHeader;
         for (int i = blockIdx.x * kPagesThreads + tid; i < all; i += gridDim.x * kPagesThreads) {
             const int b = find(freed, B, i);
             lens(b, now, keep);
             const int page = __ldg(block_table + (size_t)b * max_blocks + pages_of(keep, page_size) + (i - freed[b]));
-            if ((unsigned)page >= (unsigned)num_blocks) {
-                bad = true;
-                atomicExch(pool + 2, 1);
-                __threadfence();   // (seen by the last block, which this one's arrival follows)
-            }
+            no_page |= (unsigned)page >= (unsigned)num_blocks;
             stack[count + all - 1 - i] = page;
         }
     }
-    if (bad) atomicOr(err, kErrBadSeqlen);
-    if (!last_block(pool)) return;
-    const bool all_pages = *reinterpret_cast<volatile int*>(pool + 2) == 0;
-    __syncthreads();   // (before the word is cleared)
-    if (fits && all_pages) {
+    if (bad || no_page) atomicOr(err, kErrBadSeqlen);
+    no_page = __syncthreads_or(no_page);
+    if (!last_block(pool, no_page)) return;
+    if (fits && !no_page) {
         for (int b = tid; b < B; b += kPagesThreads)
             if (lens(b, now, keep) && keep < now) seqlens[b] = keep;
         if (tid == 0) pool[0] = count + all;
     }
-    if (tid == 0) pool[1] = pool[2] = 0;
+    if (tid == 0) pool[1] = 0;
 }
 
 __global__ void __launch_bounds__(kPagesThreads) attn_pages_init_kernel(int* pool, int num_blocks) {
