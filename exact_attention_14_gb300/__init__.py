@@ -1,8 +1,9 @@
 """GB300 (sm_103a) exact attention: fused forward (dense and packed
-variable-length), backward, and split-KV decode (contiguous or paged cache), each
-also with a learned relative position bias; and around it rotary positions, writing
-and reading the paged cache (bf16 or E4M3), its block tables and slots built from
-the requests' lengths, and attention of a tree of drafted tokens over that cache.
+variable-length), backward, and split-KV decode (contiguous or paged cache); the
+forward, its backward and decode over bf16 pages also with a learned relative position
+bias (head dims up to 128); and around it rotary positions, writing and reading the
+paged cache (bf16 or E4M3), its block tables and slots built from the requests'
+lengths, and attention of a tree of drafted tokens over that cache.
 
 Thin ctypes binding over the C ABI in ``include/attn.h`` (library
 ``libgb300_attn.so`` built in-tree by ``_build.build()``).  The functions here

@@ -27,7 +27,7 @@
 //               A warp reaches TMEM lanes 32*(warp % 4) .. +31, so each
 //               warpgroup covers the tile's 128 rows.
 //   warps 2-3   idle; with a relative position bias (BIAS), warp 2 + t looks up
-//               the biases of Q tile t, a K/V tile ahead of its softmax.
+//               the biases of Q tile t ahead of its softmax (run_bias).
 // Registers: launched at 168 per thread; the first warpgroup (producer, MMA
 // issuer) gives back to 104 and the softmax warpgroups take 200 each
 // (128*104 + 256*200 = 384*168, the launch allocation; no spills).
@@ -816,9 +816,10 @@ __device__ __noinline__ void split_piece_epilogue(unsigned int* merge_count, flo
 // ---------------------------------------------------------------------------
 // Of K/V tile j, the distances base0 + 128 j .. + 254 of the window, or the one bias
 // that they share.  Masked tiles get a window in either case (the softmax then has
-// an instantiation less).  Two slots: the warp runs a tile ahead of the softmax, so
-// that nobody waits for the two dependent loads of a look-up.  The windows lie in
-// the second store buffer of the tile's first softmax warp.  (8 x 16 heads x 4096
+// an instantiation less).  Two slots: while the softmax uses one tile's biases the next
+// tile's are there and those of the one after it are fetched to registers, so that
+// nobody waits for the two dependent loads of a look-up.  The windows lie in the
+// second store buffer of the tile's first softmax warp.  (8 x 16 heads x 4096
 // positions, not causal: 642 us without a bias, 672 with one for all distances, 690
 // with a map of 128 distances either way, 838 with every tile inside the map.)
 template <int D>

@@ -7,7 +7,8 @@
 //
 // A tile of 128 query rows and 128 keys meets 255 distances, base .. base + 254: a
 // window of 256 floats in shared memory, one per distance, that a warp of its own
-// fills up to two tiles ahead of those that use it.
+// fills: there are two, so the next tile's is full while one is in use, and the biases
+// of the tile after it are on their way to registers.
 // Forward: where all distances lie on one side of the map (or at its end) the whole
 // tile has one bias, which costs a term of the exponent that is there anyway; other
 // tiles take theirs from the window.  Lanes of a warp hold consecutive rows, so a
