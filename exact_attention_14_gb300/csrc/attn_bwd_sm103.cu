@@ -291,16 +291,20 @@ __device__ __forceinline__ BwdWork bwd_item(const BwdParams& p, unsigned idx, un
 // kernel).  (16 packed sequences of 256..4096 rows, 16 heads, whose items cost 1 to 32
 // tiles: 1770 us with every (grid size)-th item, so 1490.)  take_item: the role's k-th
 // item, every (grid size)-th one without a bias; false after the last or on abort.
+// `waits`: bounded waits for it, one after the other, for a role that may be a whole item
+// ahead of the others (the next one is fetched when this one's last tile has been).
 template <bool BIAS>
 __device__ __forceinline__ bool take_item(ItemRing& ring, unsigned k, unsigned n_items, unsigned& idx, bool& ok,
-                                          const volatile int* abort_flag) {
+                                          const volatile int* abort_flag, int waits = 1) {
     if constexpr (!BIAS) {
         idx = k == 0 ? blockIdx.x : idx + gridDim.x;
         return ok && idx < n_items;
     } else {
         if (!ok) return false;
         const unsigned i = k & 1;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ring.full[i]), (k >> 1) & 1, abort_flag));
+        do {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&ring.full[i]), (k >> 1) & 1, abort_flag));
+        } while (!ok && --waits > 0 && !__any_sync(0xFFFFFFFFu, *abort_flag != 0));
         if (!ok) return false;
         idx = *const_cast<volatile unsigned*>(&ring.item[i]);
         __syncwarp();
@@ -730,8 +734,12 @@ __device__ void bwd_bias_sums(int lane, uint8_t* smem, BwdBars* bars, const BwdP
     bool ok = true;
     uint32_t n = 0;   // tiles' sums read
     unsigned idx = 0;
-    for (unsigned item = 0; take_item<true>(bars->items, item, n_items, idx, ok, abort_flag); ++item) {
+    // An item with no tile near the map is done here at once, and the next one comes when the
+    // others are through its tiles, under 2 us each: a wait of 2 s for each 2^18 of them.
+    int waits = 1;
+    for (unsigned item = 0; take_item<true>(bars->items, item, n_items, idx, ok, abort_flag, waits); ++item) {
         const BwdWork w = bwd_item<VARLEN>(p, idx, err);
+        waits = 1 + (w.n_tiles >> 18);
         const int base0 = w.k0 - (w.qt_first * kBT + w.off) - (kBT - 1);
         for (int h = 0; h < p.group && ok; ++h) {
             float* out = bias_sums(p, w, w.g * p.group + h);

@@ -106,3 +106,23 @@ def test_packed(d, causal, kind):
             bound[:, at] += bounds.pop()
             check_gradients([dq[at, x], dk[at, y], dv[at, y]], grads, bounds)
     check_gradients([got[3]] * 4, [want] * 4, [bound] * 4)
+
+
+def test_one_item_of_two_million_tiles():
+    """A key tile whose 14 heads of 2^24 queries all lie past the map: the warp that adds up
+    distances has nothing to do and waits over 2 s, a wait's bound, for the next item.  Queries
+    of zeros, keys, values, O and dO of ones: P is 1/8, dS 0.  dV is a sum of 14 * 2^24 eighths
+    in fp32: exact below 2^21, where fp32's step is at most 1/8; from there on an addend may be
+    lost but none is added twice, so it ends between 2^21 and 14 * 2^21."""
+    H, n, m, d = 14, 1 << 24, 8, 8
+    ones = torch.ones(1, H, n, d, dtype=torch.bfloat16, device="cuda")
+    q, dq = torch.zeros_like(ones), torch.empty_like(ones)
+    k = torch.ones(1, 1, m, d, dtype=torch.bfloat16, device="cuda")
+    dk, dv = torch.empty_like(k), torch.empty_like(k)
+    lse = torch.full((1, H, n), 8.0, device="cuda").log_()
+    ids, table = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, H, device="cuda")
+    dtable = torch.empty_like(table)
+    ea.attn_bwd_bias(q, k, k, ones, ones, lse, table, ids, -1000, dq, dk, dv, dtable)
+    assert ea.attn_last_device_error() == 0
+    assert (dv >= 2 ** 21).all() and (dv <= H * 2 ** 21).all()
+    assert not dk.any() and not dtable.any() and not dq.any()
