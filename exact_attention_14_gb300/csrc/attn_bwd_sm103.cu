@@ -285,6 +285,9 @@ __device__ __forceinline__ BwdWork bwd_item(const BwdParams& p, unsigned idx, un
     else return bwd_work(p, idx);
 }
 
+// What a role's item index is before its first take_item.
+__device__ __forceinline__ unsigned before_first_item() { return blockIdx.x - gridDim.x; }
+
 // With a bias an item's cost depends on the sequence and on where the tiles lie on the
 // map, so a CTA takes its next item when it is ready for one: the first is its own
 // index, the others come off the pass's counter (in the workspace, zeroed by the prep
@@ -297,8 +300,8 @@ template <bool BIAS>
 __device__ __forceinline__ bool take_item(ItemRing& ring, unsigned k, unsigned n_items, unsigned& idx, bool& ok,
                                           const volatile int* abort_flag, int waits = 1) {
     if constexpr (!BIAS) {
-        idx = k == 0 ? blockIdx.x : idx + gridDim.x;
-        return ok && idx < n_items;
+        idx += gridDim.x;
+        return idx < n_items && ok;
     } else {
         if (!ok) return false;
         const unsigned i = k & 1;
@@ -365,7 +368,7 @@ __device__ void bwd_producer(const CUtensorMap* tq, const CUtensorMap* tk, const
     bool ok = true;
     int issued = 0;   // Q / dO tiles issued, over the CTA's items
     int kv_uses = 0;  // K / V loads issued (items with work)
-    unsigned idx = 0;
+    unsigned idx = before_first_item();
     for (unsigned item = 0; fetch_item<BIAS>(bars->items, item, n_items, idx, ok, p.queue, leader, abort_flag); ++item) {
         const BwdWork w = bwd_item<VARLEN>(p, idx, err);
         if (w.n_tiles == 0) continue;
@@ -495,7 +498,7 @@ __device__ void bwd_mma(uint8_t* smem, BwdBars* bars, uint32_t tmem, const BwdPa
     bool ok = true;
     int g = 0;  // Q / dO tiles consumed, over the CTA's items
     int u = 0;  // items with work
-    unsigned idx = 0;
+    unsigned idx = before_first_item();
     for (unsigned item = 0; take_item<BIAS>(bars->items, item, n_items, idx, ok, abort_flag); ++item) {
         const BwdWork w = bwd_item<VARLEN>(p, idx, err);
         const int n = w.n_tiles;
@@ -955,7 +958,7 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
             part[x] = smem_u32(smem + C::kDiag) + ((grp * 4 + wq) * kDiagFloats + (x & 1) * kDiagHalf +
                                                    ((lane + x) >> 3) * kDiagRow + 4 * ((lane + x) & 7) + (x >> 1)) * 4;
     }
-    unsigned idx = 0;
+    unsigned idx = before_first_item();
     for (unsigned item = 0; take_item<BIAS>(bars->items, item, n_items, idx, ok, abort_flag); ++item) {
         const BwdWork w = bwd_item<VARLEN>(p, idx, err);
         const int jg = w.k0 + j;
@@ -1031,7 +1034,7 @@ __device__ void bwd_pds(int wq, int grp, int lane, uint8_t* smem, BwdBars* bars,
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&bars->dp_full), gi & 1, abort_flag, 32));
             if (!ok) break;
             tc_fence_after();
-            auto phase2 = [&](int cc, float (&pf)[32]) {
+            auto phase2 = [&](int cc, const float (&pf)[32]) {
                 uint32_t dp[32], dd[16];
                 tmem_ld32(tdP + cc * 32, dp);
                 tmem_wait_ld();
@@ -1186,12 +1189,14 @@ attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         mbar_init(smem_u32(&bars->p_full), 8);
         mbar_init(smem_u32(&bars->ds_full), 8);
         mbar_init(smem_u32(&bars->acc_full), 1);
-        init_items(bars->items, 11);   // every role but the producer
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(&bars->win_full[s]), 1);
-            mbar_init(smem_u32(&bars->win_empty[s]), 8);
-            mbar_init(smem_u32(&bars->diag_full[s]), 8);
-            mbar_init(smem_u32(&bars->diag_empty[s]), 1);
+        if constexpr (BIAS) {
+            init_items(bars->items, 11);   // every role but the producer
+            for (int s = 0; s < 2; ++s) {
+                mbar_init(smem_u32(&bars->win_full[s]), 1);
+                mbar_init(smem_u32(&bars->win_empty[s]), 8);
+                mbar_init(smem_u32(&bars->diag_full[s]), 8);
+                mbar_init(smem_u32(&bars->diag_empty[s]), 1);
+            }
         }
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort = 0;
@@ -1367,7 +1372,7 @@ __device__ void dq_producer(const CUtensorMap* tq, const CUtensorMap* tk, const 
     bool ok = true;
     int q_uses = 0;      // Q / dO loads issued (items with work)
     int nk = 0, nv = 0;  // K and V loads issued, over the CTA's items
-    unsigned idx = 0;
+    unsigned idx = before_first_item();
     for (unsigned item = 0; fetch_item<BIAS>(bars->items, item, n_items, idx, ok, p.queue + 1, leader, abort_flag); ++item) {
         const DqWork w = dq_item<VARLEN>(p, idx, err);
         if (w.n_kv == 0) continue;
@@ -1502,7 +1507,7 @@ __device__ void dq_mma(uint8_t* smem, DqBars* bars, uint32_t tmem, const BwdPara
     bool ok = true;
     int t0 = 0;  // K/V tiles before this item
     int u = 0;   // items with work
-    unsigned idx = 0;
+    unsigned idx = before_first_item();
     for (unsigned item = 0; take_item<BIAS>(bars->items, item, n_items, idx, ok, abort_flag); ++item) {
         const DqWork w = dq_item<VARLEN>(p, idx, err);
         const int n = w.n_kv;
@@ -1674,7 +1679,7 @@ __device__ void dq_ds(int wq, int grp, int lane, uint8_t* smem, DqBars* bars, ui
     bool ok = true;
     int t0 = 0;  // K/V tiles before this item, over the CTA's items
     int u = 0;   // items with work
-    unsigned idx = 0;
+    unsigned idx = before_first_item();
     for (unsigned item = 0; take_item<BIAS>(bars->items, item, n_items, idx, ok, abort_flag); ++item) {
         const DqWork w = dq_item<VARLEN>(p, idx, err);
         const int row = w.q0 + wq * 32 + lane;
@@ -1825,10 +1830,12 @@ attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         mbar_init(smem_u32(&bars->dp_full), 1);
         mbar_init(smem_u32(&bars->ds_full), 8);
         mbar_init(smem_u32(&bars->dq_full), 1);
-        init_items(bars->items, 10);
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(&bars->win_full[s]), 1);
-            mbar_init(smem_u32(&bars->win_empty[s]), 8);
+        if constexpr (BIAS) {
+            init_items(bars->items, 10);
+            for (int s = 0; s < 2; ++s) {
+                mbar_init(smem_u32(&bars->win_full[s]), 1);
+                mbar_init(smem_u32(&bars->win_empty[s]), 8);
+            }
         }
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort = 0;

@@ -1026,9 +1026,11 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             mbar_init(smem_u32(&bars->s_full[t]), 1);
             mbar_init(smem_u32(&bars->p_full[t]), 4);
             mbar_init(smem_u32(&bars->o_full[t]), 1);
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(smem_u32(&bars->win_full[t][i]), 1);
-                mbar_init(smem_u32(&bars->win_empty[t][i]), 4);
+            if constexpr (BIAS) {
+                for (int i = 0; i < 2; ++i) {
+                    mbar_init(smem_u32(&bars->win_full[t][i]), 1);
+                    mbar_init(smem_u32(&bars->win_empty[t][i]), 4);
+                }
             }
         }
         for (int i = 0; i < C::kStages; ++i) {
