@@ -74,7 +74,8 @@ __device__ __forceinline__ int find(const int* prefix, int n, int i) {
 
 // Whether this block is the launch's last to get here (uniform over its threads; at most
 // 65535 blocks).  `flag`, of all threads alike: set on return if a block came with it set.
-// What the block read before is not read after, so the last one may overwrite it.
+// Called behind a barrier of the block: what it read before is not read after, so the
+// last one may overwrite it.
 __device__ __forceinline__ bool last_block(int* pool, bool& flag) {
     __shared__ unsigned int seen;   // blocks before this one, and above them how many had it set
     if (threadIdx.x == 0) {
